@@ -6,4 +6,5 @@ adds tensor-level helpers.  Importing the package loads the library and raises
 if it is not built: there is no CPU or eager fallback.
 """
 from . import msa  # noqa: F401  (loads libmsa.so, fails loudly if missing)
-from .api import MsaDecode, MsaPrefill, decode, prefill  # noqa: F401
+from .api import (Kv4Pool, MsaDecode, MsaDecodeKv4, MsaDensePrefill, MsaPrefill, PagedCache, decode,  # noqa: F401
+                  prefill)

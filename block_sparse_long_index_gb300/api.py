@@ -89,6 +89,193 @@ class MsaDecode:
         return _c.msa_check_device_error(self.workspace, stream)
 
 
+def _check_tensor(name, t, dtype, shape):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+class MsaDensePrefill:
+    """Dense causal attention over packed prompts of N rows in all, S sequences."""
+
+    def __init__(self, N, H_q, H_kv, d, S, device="cuda"):
+        self.N, self.H_q, self.H_kv, self.d, self.S = N, H_q, H_kv, d, S
+        self.workspace = torch.empty(_c.msa_dense_prefill_varlen_workspace(N, S, H_q, H_kv, d), dtype=torch.uint8,
+                                     device=device)
+        self.out = torch.empty((N, H_q, d), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((H_q, N), dtype=torch.float32, device=device)
+
+    def __call__(self, q, k, v, cu_seqlens, scale=None, stream=None):
+        _check_bf16("q", q, (self.N, self.H_q, self.d))
+        _check_bf16("k", k, (self.N, self.H_kv, self.d))
+        _check_bf16("v", v, (self.N, self.H_kv, self.d))
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (self.S + 1,))
+        scale = 1.0 / math.sqrt(self.d) if scale is None else scale
+        _c.msa_dense_prefill_varlen(q, k, v, cu_seqlens, self.S, self.N, self.H_q, self.H_kv, self.d, scale, self.out,
+                                    self.lse, self.workspace, stream=stream)
+        return self.out, self.lse
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
+class Kv4Pool:
+    """A 4-bit paged K/V cache: codes [n_pages, page_size, H_kv, d / 2] and scales [n_pages, page_size, H_kv, 4]
+    of K and of V (uint8).  ``Kv4Pool.empty`` makes one."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        self.n_pages, self.page_size, self.H_kv, half = k_codes.shape
+        self.d = 2 * half
+        for name, t, last in (("k_codes", k_codes, half), ("k_scales", k_scales, 4), ("v_codes", v_codes, half),
+                              ("v_scales", v_scales, 4)):
+            _check_tensor(name, t, torch.uint8, (self.n_pages, self.page_size, self.H_kv, last))
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.c = _c.kv4_pool(k_codes, k_scales, v_codes, v_scales, self.n_pages, self.page_size, self.H_kv, self.d)
+        self.workspace = torch.empty(_c.msa_kv4_workspace(), dtype=torch.uint8, device=k_codes.device)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, H_kv, d, device="cuda"):
+        return cls(*[torch.zeros((n_pages, page_size, H_kv, last), dtype=torch.uint8, device=device)
+                     for last in (d // 2, 4, d // 2, 4)])
+
+    def tensors(self):
+        return [self.k_codes, self.k_scales, self.v_codes, self.v_scales]
+
+    def _rows(self, cu_seqlens, pos0, page_table):
+        S = cu_seqlens.numel() - 1
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (S + 1,))
+        _check_tensor("pos0", pos0, torch.int32, (S,))
+        _check_tensor("page_table", page_table, torch.int32, (S, page_table.shape[-1]))
+        return S, page_table.shape[1]
+
+    def store(self, k, v, cu_seqlens, pos0, page_table, stream=None):
+        """Quantizes rows k, v [N, H_kv, d] into the pages of their sequences (see msa_kv4_store)."""
+        N = k.shape[0]
+        _check_bf16("k", k, (N, self.H_kv, self.d))
+        _check_bf16("v", v, (N, self.H_kv, self.d))
+        S, max_pages = self._rows(cu_seqlens, pos0, page_table)
+        _c.msa_kv4_store(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, self.c, self.workspace, stream=stream)
+
+    def load(self, N, cu_seqlens, pos0, page_table, k=None, v=None, stream=None):
+        """The rows' values as bf16 [N, H_kv, d] (see msa_kv4_load); rows of no sequence stay as k and v had them."""
+        S, max_pages = self._rows(cu_seqlens, pos0, page_table)
+        shape = (N, self.H_kv, self.d)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if v is None else v
+        _check_bf16("k", k, shape)
+        _check_bf16("v", v, shape)
+        _c.msa_kv4_load(self.c, N, cu_seqlens, S, pos0, page_table, max_pages, k, v, self.workspace, stream=stream)
+        return k, v
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
+class MsaDecodeKv4:
+    """One decode token for B sequences over a Kv4Pool: ``dense`` attends to the whole context, calling the
+    object runs the MSA step (select by the index branch, attend to the chosen blocks; needs d_I, Bk and k)."""
+
+    def __init__(self, pool: Kv4Pool, B, max_pages, H_q, d_I=None, Bk=128, k=16, device=None):
+        device = pool.k_codes.device if device is None else device
+        self.pool, self.B, self.max_pages, self.H_q, self.d_I = pool, B, max_pages, H_q, d_I
+        need = _c.msa_dense_decode_paged_kv4_workspace(B, H_q, pool.H_kv, pool.d)
+        if d_I is not None:
+            self.shape = _c.shape(max_pages * pool.page_size, H_q, pool.H_kv, pool.d, d_I, Bk, k)
+            need = max(need, _c.msa_decode_workspace(B, self.shape))
+            self.block_idx = torch.empty((B, pool.H_kv, k), dtype=torch.int32, device=device)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self.out = torch.empty((B, H_q, pool.d), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((B, H_q), dtype=torch.float32, device=device)
+
+    def _check(self, q_t, page_table, ctx_len):
+        _check_bf16("q_t", q_t, (self.B, self.H_q, self.pool.d))
+        _check_tensor("page_table", page_table, torch.int32, (self.B, self.max_pages))
+        _check_tensor("ctx_len", ctx_len, torch.int32, (self.B,))
+
+    def dense(self, q_t, page_table, ctx_len, scale=None, stream=None):
+        self._check(q_t, page_table, ctx_len)
+        scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
+        _c.msa_dense_decode_paged_kv4(q_t, self.pool.c, page_table, self.max_pages, ctx_len, self.B, self.H_q, scale,
+                                      self.out, self.lse, self.workspace, stream=stream)
+        return self.out, self.lse
+
+    def __call__(self, q_t, q_idx_t, k_idx_pool, page_table, ctx_len, scale=None, stream=None):
+        """q_idx_t [B, H_kv, d_I] and k_idx_pool [n_pages, page_size, d_I]: both bf16, or both uint8 (E4M3 codes)."""
+        if self.d_I is None:
+            raise ValueError("the MSA step needs d_I (and Bk, k) when the object is made")
+        self._check(q_t, page_table, ctx_len)
+        f8 = q_idx_t.dtype == torch.uint8
+        idx = torch.uint8 if f8 else torch.bfloat16
+        _check_tensor("q_idx_t", q_idx_t, idx, (self.B, self.pool.H_kv, self.d_I))
+        _check_tensor("k_idx_pool", k_idx_pool, idx, (self.pool.n_pages, self.pool.page_size, self.d_I))
+        scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
+        call = _c.msa_decode_paged_kv4_fp8 if f8 else _c.msa_decode_paged_kv4
+        call(q_t, q_idx_t, k_idx_pool, self.pool.c, page_table, self.max_pages, ctx_len, self.B, self.shape, scale,
+             self.out, self.lse, self.block_idx, self.workspace, stream=stream)
+        return self.out, self.lse, self.block_idx
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
+class PagedCache:
+    """Page tables, lengths and reference counts of a paged cache, and the pools that they address.
+
+    page_table [n_seqs, max_pages], ctx_len [n_seqs] and refs [n_pages] are int32 device tensors; every pool is a
+    contiguous tensor of n_pages pages, at most 8 of them.  ``PagedCache.empty`` makes the tables.  A call's
+    errors (MSA_ERR_NO_PAGES, MSA_ERR_BAD_INDEX) are what ``device_status`` returns after it."""
+
+    def __init__(self, page_table, ctx_len, refs, page_size, pools=()):
+        n_seqs, max_pages = page_table.shape
+        n_pages = refs.numel()
+        _check_tensor("page_table", page_table, torch.int32, (n_seqs, max_pages))
+        _check_tensor("ctx_len", ctx_len, torch.int32, (n_seqs,))
+        _check_tensor("refs", refs, torch.int32, (n_pages,))
+        for i, t in enumerate(pools):
+            _check_tensor("pools[%d]" % i, t, t.dtype, (n_pages, page_size) + tuple(t.shape[2:]))
+        self.page_table, self.ctx_len, self.refs, self.page_size = page_table, ctx_len, refs, page_size
+        self.pools, self.n_pages = list(pools), n_pages
+        self.c = _c.pages(page_table, ctx_len, refs, max_pages, n_pages, n_seqs, page_size)
+        self.c_pools = _c.page_pools((t, t.numel() // n_pages * t.element_size()) for t in self.pools)
+        self.page_map = torch.empty((n_pages,), dtype=torch.int32, device=refs.device)
+        self.n_live = torch.empty((1,), dtype=torch.int32, device=refs.device)
+        need = max(_c.msa_pages_workspace(self.c, 0), _c.msa_pages_workspace(self.c, min(n_seqs, 4096)))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=refs.device)
+
+    @classmethod
+    def empty(cls, n_seqs, max_pages, n_pages, page_size, pools=(), device="cuda"):
+        return cls(torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros((n_seqs,), dtype=torch.int32, device=device),
+                   torch.zeros((n_pages,), dtype=torch.int32, device=device), page_size, pools)
+
+    def reserve(self, seqs, new_len, stream=None):
+        n = seqs.numel()
+        _check_tensor("seqs", seqs, torch.int32, (n,))
+        _check_tensor("new_len", new_len, torch.int32, (n,))
+        _c.msa_pages_reserve(self.c, seqs, new_len, n, self.workspace, stream=stream)
+
+    def fork(self, src, dst, stream=None):
+        n = src.numel()
+        _check_tensor("src", src, torch.int32, (n,))
+        _check_tensor("dst", dst, torch.int32, (n,))
+        _c.msa_pages_fork(self.c, src, dst, n, self.c_pools, len(self.pools), self.workspace, stream=stream)
+
+    def free(self, seqs, stream=None):
+        n = seqs.numel()
+        _check_tensor("seqs", seqs, torch.int32, (n,))
+        _c.msa_pages_free(self.c, seqs, n, self.workspace, stream=stream)
+
+    def compact(self, stream=None):
+        """Returns (page_map [n_pages], n_live [1]): each page's new id (-1 where it was free), and the pages held."""
+        _c.msa_pages_compact(self.c, self.c_pools, len(self.pools), self.page_map, self.n_live, self.workspace,
+                             stream=stream)
+        return self.page_map, self.n_live
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
 def prefill(q, k, v, q_idx, k_idx, Bk=128, k_blocks=16, scale=None):
     """One-shot prefill: returns (out [N,H_q,d] bf16, lse [H_q,N] fp32, block_idx [G,N,k] int32)."""
     N, H_q, d = q.shape

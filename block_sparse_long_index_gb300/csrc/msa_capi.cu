@@ -485,6 +485,284 @@ msa_status_t msa_decode_paged_fp8(const void* q_t, const void* q_idx_t, const vo
                            ctx_len, B, shape, scale, out, lse, block_idx, workspace, workspace_bytes, stream, true);
 }
 
+// ---------------------------------------------------------------- dense prefill
+static msa_status_t check_heads(int H_q, int H_kv, int d) {
+  if (H_q < 1 || H_kv < 1 || d < 1 || H_q % H_kv != 0) return MSA_ERR_INVALID_ARGUMENT;
+  if (!pow2_upto8(H_q / H_kv) || (d != 64 && d != 128) || H_kv > 64) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
+static msa_status_t check_dense_prefill(int64_t N, int S, int H_q, int H_kv, int d) {
+  if (N < 1 || S < 1) return MSA_ERR_INVALID_ARGUMENT;
+  msa_status_t st = check_heads(H_q, H_kv, d);
+  if (st != MSA_OK) return st;
+  return N > ((int64_t)1 << 24) ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+
+size_t msa_dense_prefill_varlen_workspace(int64_t N, int S, int H_q, int H_kv, int d) {
+  if (check_dense_prefill(N, S, H_q, H_kv, d) != MSA_OK) return kHeader;
+  return kHeader + msa::dense_scratch_bytes(msa::dense_plan(N, S, H_q, H_kv, d));
+}
+
+msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int S,
+                                      int64_t N, int H_q, int H_kv, int d, float scale, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  if (!q || !k || !v || !cu_seqlens || !out || !lse) return MSA_ERR_INVALID_ARGUMENT;
+  msa_status_t st = check_dense_prefill(N, S, H_q, H_kv, d);
+  if (st != MSA_OK) return st;
+  if (!(scale > 0.f) || scale != scale) return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)lse & 3u) ||
+      ((uintptr_t)cu_seqlens & 3u))
+    return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  const msa::DensePlan p = msa::dense_plan(N, S, H_q, H_kv, d);
+  st = begin(workspace, workspace_bytes, kHeader + msa::dense_scratch_bytes(p), s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_dense_prefill(q, k, v, cu_seqlens, p, scale, out, lse, (char*)workspace + kHeader,
+                                          (msa::DeviceStatus*)workspace, s));
+}
+
+// ---------------------------------------------------------------- 4-bit cache
+static msa_status_t check_kv4(const msa_kv4_pool_t* p, const int32_t* page_table, int64_t max_pages) {
+  if (!p || !p->k_codes || !p->k_scales || !p->v_codes || !p->v_scales || !page_table) return MSA_ERR_INVALID_ARGUMENT;
+  if (p->n_pages < 1 || p->page_size < 16 || p->page_size % 16 != 0 || p->H_kv < 1 || p->d < 1 || max_pages < 1)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if ((p->d != 64 && p->d != 128) || p->H_kv > 64) return MSA_ERR_UNSUPPORTED;
+  // ids and positions are int32
+  if (p->n_pages >= (int64_t)1 << 31 || max_pages >= (int64_t)1 << 31 ||
+      max_pages * (int64_t)p->page_size >= (int64_t)1 << 31)
+    return MSA_ERR_UNSUPPORTED;
+  if (!aligned16(p->k_codes) || !aligned16(p->k_scales) || !aligned16(p->v_codes) || !aligned16(p->v_scales) ||
+      ((uintptr_t)page_table & 3u))
+    return MSA_ERR_INVALID_ARGUMENT;
+  return MSA_OK;
+}
+
+static msa::Kv4Pool kv4_pool(const msa_kv4_pool_t* p) {
+  msa::Kv4Pool r;
+  r.k_codes = (uint8_t*)p->k_codes;
+  r.k_scales = (uint8_t*)p->k_scales;
+  r.v_codes = (uint8_t*)p->v_codes;
+  r.v_scales = (uint8_t*)p->v_scales;
+  r.n_pages = p->n_pages;
+  r.page = p->page_size;
+  r.H_kv = p->H_kv;
+  r.d = p->d;
+  return r;
+}
+
+size_t msa_kv4_workspace(void) { return kHeader; }
+
+static msa_status_t check_kv4_rows(const void* k, const void* v, int64_t N, const int32_t* cu_seqlens, int S,
+                                   const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                                   const msa_kv4_pool_t* pool) {
+  msa_status_t st = check_kv4(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  if (!k || !v || !cu_seqlens || !pos0 || N < 1 || S < 1) return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(k) || !aligned16(v) || ((uintptr_t)cu_seqlens & 3u) || ((uintptr_t)pos0 & 3u))
+    return MSA_ERR_INVALID_ARGUMENT;
+  return N >= (int64_t)1 << 31 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+
+msa_status_t msa_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu_seqlens, int S,
+                           const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                           const msa_kv4_pool_t* pool, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv4_rows(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, pool);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, kHeader, s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_kv4_store(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, kv4_pool(pool),
+                                      (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_kv4_load(const msa_kv4_pool_t* pool, int64_t N, const int32_t* cu_seqlens, int S,
+                          const int32_t* pos0, const int32_t* page_table, int64_t max_pages, void* k, void* v,
+                          void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv4_rows(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, pool);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, kHeader, s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_kv4_load(kv4_pool(pool), N, cu_seqlens, S, pos0, page_table, max_pages, k, v,
+                                     (msa::DeviceStatus*)workspace, s));
+}
+
+size_t msa_dense_decode_paged_kv4_workspace(int B, int H_q, int H_kv, int d) {
+  if (B < 1 || check_heads(H_q, H_kv, d) != MSA_OK) return kHeader;
+  return kHeader + msa::dense_decode_scratch_bytes(H_kv, H_q / H_kv, d);
+}
+
+msa_status_t msa_dense_decode_paged_kv4(const void* q_t, const msa_kv4_pool_t* pool, const int32_t* page_table,
+                                        int64_t max_pages, const int32_t* ctx_len, int B, int H_q, float scale,
+                                        void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                        msa_stream_t stream) {
+  msa_status_t st = check_kv4(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  if (!q_t || !ctx_len || !out || B < 1) return MSA_ERR_INVALID_ARGUMENT;
+  st = check_heads(H_q, pool->H_kv, pool->d);
+  if (st != MSA_OK) return st;
+  if (B > 1 << 20) return MSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale != scale) return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q_t) || !aligned16(out) || ((uintptr_t)ctx_len & 3u) || ((uintptr_t)lse & 3u))
+    return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, msa_dense_decode_paged_kv4_workspace(B, H_q, pool->H_kv, pool->d), s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_dense_decode(q_t, kv4_pool(pool), page_table, max_pages, ctx_len, B, H_q, scale, out, lse,
+                                         (char*)workspace + kHeader, (msa::DeviceStatus*)workspace, s));
+}
+
+static msa_status_t decode_kv4_impl(const void* q_t, const void* q_idx_t, const void* k_idx_pool,
+                                    const msa_kv4_pool_t* pool, const int32_t* page_table, int64_t max_pages,
+                                    const int32_t* ctx_len, int B, const msa_shape_t* shape, float scale, void* out,
+                                    float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
+                                    msa_stream_t stream, bool f8) {
+  msa_status_t st = check_kv4(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  if (!q_t || !q_idx_t || !k_idx_pool || !ctx_len || !out || B < 1) return MSA_ERR_INVALID_ARGUMENT;
+  st = check_shape(shape);
+  if (st != MSA_OK) return st;
+  if (shape->N != max_pages * (int64_t)pool->page_size || shape->H_kv != pool->H_kv || shape->d != pool->d)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (f8 && shape->d_I == 32) return MSA_ERR_UNSUPPORTED;
+  if (shape->H_kv > 8) return MSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale != scale) return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q_t) || !aligned16(q_idx_t) || !aligned16(k_idx_pool) || ((uintptr_t)ctx_len & 3u) ||
+      ((uintptr_t)out & 1u) || ((uintptr_t)lse & 3u) || ((uintptr_t)block_idx & 3u))
+    return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  msa::DecodePlan p = msa::decode_plan(B, shape->N, shape->H_q, shape->H_kv, shape->d, shape->d_I, shape->Bk,
+                                       shape->k);
+  p.f8 = f8;
+  st = begin(workspace, workspace_bytes, msa_decode_workspace(B, shape), s, kHeader + msa::decode_clear_bytes(p));
+  if (st != MSA_OK) return st;
+  msa::CacheMap map;
+  map.table = page_table;
+  map.max_pages = max_pages;
+  map.n_pages = pool->n_pages;
+  map.page = pool->page_size;
+  const msa::Kv4Pool kv4 = kv4_pool(pool);
+  return finish(msa::launch_decode(q_t, q_idx_t, k_idx_pool, nullptr, nullptr, ctx_len, p, scale, out, lse, block_idx,
+                                   (char*)workspace + kHeader, (msa::DeviceStatus*)workspace, s, &map, &kv4));
+}
+
+msa_status_t msa_decode_paged_kv4(const void* q_t, const void* q_idx_t, const void* k_idx_pool,
+                                  const msa_kv4_pool_t* pool, const int32_t* page_table, int64_t max_pages,
+                                  const int32_t* ctx_len, int B, const msa_shape_t* shape, float scale, void* out,
+                                  float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
+                                  msa_stream_t stream) {
+  return decode_kv4_impl(q_t, q_idx_t, k_idx_pool, pool, page_table, max_pages, ctx_len, B, shape, scale, out, lse,
+                         block_idx, workspace, workspace_bytes, stream, false);
+}
+
+msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, const void* k_idx_pool,
+                                      const msa_kv4_pool_t* pool, const int32_t* page_table, int64_t max_pages,
+                                      const int32_t* ctx_len, int B, const msa_shape_t* shape, float scale, void* out,
+                                      float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
+                                      msa_stream_t stream) {
+  return decode_kv4_impl(q_t, q_idx_t, k_idx_pool, pool, page_table, max_pages, ctx_len, B, shape, scale, out, lse,
+                         block_idx, workspace, workspace_bytes, stream, true);
+}
+
+// ---------------------------------------------------------------- pages of a cache
+static msa_status_t check_pages(const msa_pages_t* p, int n) {
+  if (!p || !p->page_table || !p->ctx_len || !p->refs || n < 0) return MSA_ERR_INVALID_ARGUMENT;
+  if (p->max_pages < 1 || p->n_pages < 1 || p->n_seqs < 1 || p->page_size < 16 || p->page_size % 16 != 0)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)p->page_table | (uintptr_t)p->ctx_len | (uintptr_t)p->refs) & 3u) return MSA_ERR_INVALID_ARGUMENT;
+  if (p->n_pages >= (int64_t)1 << 27 || p->max_pages >= (int64_t)1 << 27 ||
+      p->max_pages * (int64_t)p->page_size >= (int64_t)1 << 31 || n > msa::kMaxPageSeqs)
+    return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
+static bool bad_list(const int32_t* p, int n) { return n > 0 && (!p || ((uintptr_t)p & 3u)); }
+
+static msa::Pages pages_view(const msa_pages_t* p) {
+  msa::Pages r;
+  r.table = p->page_table;
+  r.ctx = p->ctx_len;
+  r.refs = p->refs;
+  r.max_pages = p->max_pages;
+  r.n_pages = p->n_pages;
+  r.n_seqs = p->n_seqs;
+  r.page = p->page_size;
+  return r;
+}
+
+static msa_status_t pools_view(const msa_page_pool_t* pools, int n_pools, msa::PagePools* out) {
+  if (n_pools < 0 || (n_pools > 0 && !pools)) return MSA_ERR_INVALID_ARGUMENT;
+  if (n_pools > msa::kMaxPools) return MSA_ERR_UNSUPPORTED;
+  *out = msa::PagePools{};
+  out->n = n_pools;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i].base || !aligned16(pools[i].base) || pools[i].page_bytes == 0 || pools[i].page_bytes % 16 != 0)
+      return MSA_ERR_INVALID_ARGUMENT;
+    out->base[i] = (char*)pools[i].base;
+    out->page_bytes[i] = pools[i].page_bytes;
+  }
+  return MSA_OK;
+}
+
+size_t msa_pages_workspace(const msa_pages_t* pages, int n) {
+  if (check_pages(pages, n) != MSA_OK) return kHeader;
+  return kHeader + msa::pages_scratch_bytes(pages_view(pages), n);
+}
+
+msa_status_t msa_pages_reserve(const msa_pages_t* pages, const int32_t* seqs, const int32_t* new_len, int n,
+                               void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_pages(pages, n);
+  if (st != MSA_OK) return st;
+  if (bad_list(seqs, n) || bad_list(new_len, n)) return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, kHeader, s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_pages_reserve(pages_view(pages), seqs, new_len, n, (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_pages_fork(const msa_pages_t* pages, const int32_t* src, const int32_t* dst, int n,
+                            const msa_page_pool_t* pools, int n_pools, void* workspace, size_t workspace_bytes,
+                            msa_stream_t stream) {
+  msa_status_t st = check_pages(pages, n);
+  if (st != MSA_OK) return st;
+  msa::PagePools pp;
+  st = pools_view(pools, n_pools, &pp);
+  if (st != MSA_OK) return st;
+  if (bad_list(src, n) || bad_list(dst, n)) return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, n), s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_pages_fork(pages_view(pages), src, dst, n, pp, (char*)workspace + kHeader,
+                                       (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_pages_free(const msa_pages_t* pages, const int32_t* seqs, int n, void* workspace,
+                            size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_pages(pages, n);
+  if (st != MSA_OK) return st;
+  if (bad_list(seqs, n)) return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, kHeader, s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_pages_free(pages_view(pages), seqs, n, (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_pages_compact(const msa_pages_t* pages, const msa_page_pool_t* pools, int n_pools, int32_t* page_map,
+                               int32_t* n_live, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_pages(pages, 0);
+  if (st != MSA_OK) return st;
+  msa::PagePools pp;
+  st = pools_view(pools, n_pools, &pp);
+  if (st != MSA_OK) return st;
+  if (((uintptr_t)page_map | (uintptr_t)n_live) & 3u) return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, 0), s);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_pages_compact(pages_view(pages), pp, page_map, n_live, (char*)workspace + kHeader,
+                                          (msa::DeviceStatus*)workspace, s));
+}
+
 // The decode step without a caller workspace: its scratch is the library's
 // fixed device array (see msa_decode.cu), so this call allocates nothing.
 msa_status_t msa_decode_noalloc(const void* q_t, const void* q_idx_t, const void* k_idx_cache, const void* k_cache,
@@ -520,6 +798,7 @@ msa_status_t msa_check_device_error(void* workspace, msa_stream_t stream) {
   if (cudaMemcpy(&flags, workspace, sizeof(flags), cudaMemcpyDeviceToHost) != cudaSuccess) return MSA_ERR_CUDA;
   if (flags & msa::kErrBadIndex) return MSA_ERR_BAD_INDEX;
   if (flags & msa::kErrTimeout) return MSA_ERR_TIMEOUT;
+  if (flags & msa::kErrNoPages) return MSA_ERR_NO_PAGES;
   return MSA_OK;
 }
 
@@ -532,6 +811,7 @@ const char* msa_status_string(msa_status_t status) {
     case MSA_ERR_CUDA: return "CUDA launch or runtime error";
     case MSA_ERR_BAD_INDEX: return "bad index found on the device (entry skipped)";
     case MSA_ERR_TIMEOUT: return "a bounded device wait gave up";
+    case MSA_ERR_NO_PAGES: return "too few free pages (nothing was changed)";
     default: return "unknown status";
   }
 }

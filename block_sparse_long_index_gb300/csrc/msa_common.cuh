@@ -14,7 +14,7 @@ namespace msa {
 // The first bytes of every workspace hold a DeviceStatus; kernels raise bits
 // with atomicOr and never trap.
 struct DeviceStatus {
-  unsigned int flags;       // kErrBadIndex | kErrTimeout
+  unsigned int flags;       // kErrBadIndex | kErrTimeout | kErrNoPages
   unsigned int first_code;  // kernel-specific code of the first bad entry
   unsigned int pad[62];
 };
@@ -22,6 +22,7 @@ static_assert(sizeof(DeviceStatus) == 256, "status header is 256 bytes");
 
 constexpr unsigned int kErrBadIndex = 1u;
 constexpr unsigned int kErrTimeout = 2u;
+constexpr unsigned int kErrNoPages = 4u;
 
 __device__ __forceinline__ void raise_error(DeviceStatus* st, unsigned int flag, unsigned int code) {
   if (st == nullptr) return;

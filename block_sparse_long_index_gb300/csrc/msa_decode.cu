@@ -29,6 +29,7 @@
 #include <cudaTypedefs.h>
 #include <mutex>
 
+#include "msa_kv4.cuh"
 #include "msa_sm100.cuh"
 
 namespace msa {
@@ -340,7 +341,11 @@ __device__ __forceinline__ uint64_t merged_key(const uint64_t* sl, int splits, i
 // The last CTA of a (sequence, group) to finish merges the group's k partials
 // per head: M = max lse_s, w_s = e^(lse_s - M) / sum e^(lse_s - M),
 // out = sum w_s O_s, lse = M + ln sum e^(lse_s - M).
-template <int D, int BK, bool PAGED, int LPL>
+//
+// KV4: K and V rows come from 4-bit pools (paged) and are expanded to their
+// exact bf16 values, K's words in registers on their way into the B fragments
+// and V's on their way into shared memory; the rest is the same arithmetic.
+template <int D, int BK, bool PAGED, int LPL, bool KV4 = false>
 __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __restrict__ q_t,
                                                           const uint16_t* __restrict__ k_cache,
                                                           const uint16_t* __restrict__ v_cache,
@@ -351,7 +356,8 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
                                                           float* __restrict__ part_o, float* __restrict__ part_lse,
                                                           unsigned int* __restrict__ tickets,
                                                           uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                          DeviceStatus* st) {
+                                                          DeviceStatus* st, Kv4Pool pool) {
+  static_assert(PAGED || !KV4, "4-bit caches are paged");
   // the group's candidate lists first; then V rows [BK][D]; later the warps' partial O
   extern __shared__ __align__(16) uint16_t v_s[];
   __shared__ float red_m[4][8], red_l[4][8];
@@ -420,21 +426,52 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
     }
     auto row_off = [&](int j) -> int64_t { return (PAGED ? krow_s[PAGED ? j : 0] : (int64_t)j) * kv_row; };
     // V rows into shared memory (rows past nvis read as zero), every copy in flight at once
-    for (int i = tid; i < BK * C8; i += blockDim.x) {
-      const int j = i / C8, c8 = i % C8;
-      const bool in = j < nvis;
-      cp_async_16(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8, Vb + row_off(in ? j : 0) + c8 * 8, in ? 16 : 0);
+    if constexpr (KV4) {
+      constexpr int W4 = D / 32;  // 16-byte pieces of a row's codes: 32 channels
+#pragma unroll 4
+      for (int i = tid; i < BK * W4; i += blockDim.x) {
+        const int j = i / W4, w = i % W4;
+        const bool in = j < nvis;
+        const int64_t hr = krow_s[in ? j : 0] * G + g;
+        const uint4 x = ldg_stream_16(pool.v_codes + hr * (D / 2) + 16 * w);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(pool.v_scales + hr * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c8 = 4 * w + e;
+          const uint32_t s = kv4::scale_bf16((sc >> (8 * (c8 / (C8 / 4)))) & 255u), s2 = s | (s << 16);
+          const uint4 y = kv4::expand8(words[e], s2, kv4::scale_bias(s2));
+          *reinterpret_cast<uint4*>(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8) = in ? y : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else {
+      for (int i = tid; i < BK * C8; i += blockDim.x) {
+        const int j = i / C8, c8 = i % C8;
+        const bool in = j < nvis;
+        cp_async_16(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8, Vb + row_off(in ? j : 0) + c8 * 8, in ? 16 : 0);
+      }
+      cp_async_commit();
     }
-    cp_async_commit();
     // K rows of this warp's keys as B fragments (key = column gq of n-tile nt); rows past nvis repeat a
     // visible row and are masked below
     uint4 kf[NT][NP];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int j = min(warp * KPW + nt * 8 + gq, nvis - 1);
-      const uint16_t* kr = Kb + row_off(j) + 8 * tq;
+      if constexpr (KV4) {
+        const int64_t hr = krow_s[j] * G + g;
+        const uint32_t* kr = reinterpret_cast<const uint32_t*>(pool.k_codes + hr * (D / 2)) + tq;
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(pool.k_scales + hr * 4);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) kf[nt][p] = ldg_stream_16(kr + 32 * p);
+        for (int p = 0; p < NP; ++p) {  // word 4p + tq: channels 32p + 8tq .. + 7, in group (4p + tq) / (d / 32)
+          const uint32_t s = kv4::scale_bf16((sc >> (8 * ((4 * p + tq) / NP))) & 255u), s2 = s | (s << 16);
+          kf[nt][p] = kv4::expand8(__ldg(kr + 4 * p), s2, kv4::scale_bias(s2));
+        }
+      } else {
+        const uint16_t* kr = Kb + row_off(j) + 8 * tq;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) kf[nt][p] = ldg_stream_16(kr + 32 * p);
+      }
     }
     // S = q K^T for this warp's keys
     float sacc[NT][4];
@@ -648,13 +685,14 @@ cudaError_t launch_scan(const void* q_idx_t, const void* k_idx_cache, const int3
 
 // The attention grid as a programmatic dependent of the scan: its CTAs may be
 // scheduled while the scan drains and wait (griddepcontrol.wait) for its results.
-template <int D, int BK, bool PAGED, int LPL>
+template <int D, int BK, bool PAGED, int LPL, bool KV4>
 cudaError_t launch_attn_dep_t(const void* q_t, const void* k_cache, const void* v_cache, const int32_t* ctx_len,
                               int32_t* blk, const CacheMap& map, const DecodePlan& p, float scale,
-                              const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
+                              const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s,
+                              const Kv4Pool& pool) {
   const size_t vb = (size_t)BK * D * 2, lb = group_lists_bytes(p);
   const int smem = (int)(vb > lb ? vb : lb);  // V rows of one block, or first the group's candidate lists
-  auto kern = decode_attn_kernel<D, BK, PAGED, LPL>;
+  auto kern = decode_attn_kernel<D, BK, PAGED, LPL, KV4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -669,25 +707,33 @@ cudaError_t launch_attn_dep_t(const void* q_t, const void* k_cache, const void* 
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, (const uint16_t*)q_t, (const uint16_t*)k_cache, (const uint16_t*)v_cache,
                             ctx_len, (const uint64_t*)sc.cand, p.splits, blk, p.ctx_max, map, p.H_q, p.H_kv, p.k,
-                            scale, sc.part_o, sc.part_lse, sc.tickets, (uint16_t*)out, lse, st);
+                            scale, sc.part_o, sc.part_lse, sc.tickets, (uint16_t*)out, lse, st, pool);
 }
 
-template <int D, int BK, bool PAGED>
+template <int D, int BK, bool PAGED, bool KV4 = false>
 cudaError_t launch_attn_dep_p(const void* q_t, const void* k_cache, const void* v_cache, const int32_t* ctx_len,
                               int32_t* blk, const CacheMap& map, const DecodePlan& p, float scale,
-                              const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
+                              const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s,
+                              const Kv4Pool& pool = Kv4Pool{}) {
   // lists per lane of the merge: splits <= 64, 128, 256
   if (p.splits <= 64)
-    return launch_attn_dep_t<D, BK, PAGED, 2>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s);
+    return launch_attn_dep_t<D, BK, PAGED, 2, KV4>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s,
+                                                  pool);
   if (p.splits <= 128)
-    return launch_attn_dep_t<D, BK, PAGED, 4>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s);
-  return launch_attn_dep_t<D, BK, PAGED, 8>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s);
+    return launch_attn_dep_t<D, BK, PAGED, 4, KV4>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s,
+                                                  pool);
+  return launch_attn_dep_t<D, BK, PAGED, 8, KV4>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s,
+                                                  pool);
 }
 
 template <int D, int BK>
 cudaError_t launch_attn_dep(const void* q_t, const void* k_cache, const void* v_cache, const int32_t* ctx_len,
                             int32_t* blk, const CacheMap& map, const DecodePlan& p, float scale,
-                            const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
+                            const DecodeScratch& sc, void* out, float* lse, DeviceStatus* st, cudaStream_t s,
+                            const Kv4Pool* kv4) {
+  if (kv4)
+    return launch_attn_dep_p<D, BK, true, true>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s,
+                                                *kv4);
   return map.table ? launch_attn_dep_p<D, BK, true>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse,
                                                      st, s)
                    : launch_attn_dep_p<D, BK, false>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out,
@@ -728,7 +774,7 @@ size_t decode_clear_bytes(const DecodePlan& p) { return ticket_bytes(p); }
 cudaError_t launch_decode(const void* q_t, const void* q_idx_t, const void* k_idx_cache, const void* k_cache,
                           const void* v_cache, const int32_t* ctx_len, const DecodePlan& p, float scale, void* out,
                           float* lse, int32_t* block_idx, void* scratch, DeviceStatus* st, cudaStream_t s,
-                          const CacheMap* paged) {
+                          const CacheMap* paged, const Kv4Pool* kv4) {
   const CacheMap map = paged ? *paged : CacheMap{};
   DecodeScratch sc;
   carve(p, scratch, &sc);
@@ -745,11 +791,11 @@ cudaError_t launch_decode(const void* q_t, const void* q_idx_t, const void* k_id
                    : launch_scan<128, 128>(q_idx_t, k_idx_cache, ctx_len, map, p, sc, st, s);
   }
   if (e != cudaSuccess) return e;
-  if (p.d == 64)
-    return p.Bk == 64 ? launch_attn_dep<64, 64>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s)
-                      : launch_attn_dep<64, 128>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s);
-  return p.Bk == 64 ? launch_attn_dep<128, 64>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s)
-                    : launch_attn_dep<128, 128>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s);
+#define MSA_ATTN(D, BK) \
+  launch_attn_dep<D, BK>(q_t, k_cache, v_cache, ctx_len, blk, map, p, scale, sc, out, lse, st, s, kv4)
+  if (p.d == 64) return p.Bk == 64 ? MSA_ATTN(64, 64) : MSA_ATTN(64, 128);
+  return p.Bk == 64 ? MSA_ATTN(128, 64) : MSA_ATTN(128, 128);
+#undef MSA_ATTN
 }
 
 // ---------------------------------------------------------------- fixed scratch for msa_decode_noalloc

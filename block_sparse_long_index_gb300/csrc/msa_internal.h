@@ -133,6 +133,16 @@ cudaError_t launch_warmup_grad_tc(const void* q, const void* k, const void* q_id
                                   int H_q, int H_kv, float scale, float kl_weight, const float* lse, const float* lseI,
                                   float* dq_idx, float* dk_idx, float* kl, DeviceStatus* st, cudaStream_t s);
 
+// Pools of a 4-bit paged cache (the format: msa_kv4.cuh).
+struct Kv4Pool {
+  uint8_t* k_codes;   // [n_pages, page, H_kv, d / 2]
+  uint8_t* k_scales;  // [n_pages, page, H_kv, 4]
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int64_t n_pages;
+  int page, H_kv, d;
+};
+
 // ---- decode (msa_decode.cu)
 // Where token `key` of sequence `seq` sits in a decode cache: contiguous (no
 // table: row seq * ctx_max + key) or paged (row table[seq][key / page] * page +
@@ -163,7 +173,61 @@ size_t decode_clear_bytes(const DecodePlan& p);
 cudaError_t launch_decode(const void* q_t, const void* q_idx_t, const void* k_idx_cache, const void* k_cache,
                           const void* v_cache, const int32_t* ctx_len, const DecodePlan& p, float scale, void* out,
                           float* lse, int32_t* block_idx, void* scratch, DeviceStatus* st, cudaStream_t s,
-                          const CacheMap* paged = nullptr);
+                          const CacheMap* paged = nullptr, const Kv4Pool* kv4 = nullptr);
+
+// ---- dense prefill over packed sequences (msa_dense.cu)
+struct DensePlan {
+  int64_t N;
+  int S, H_q, H_kv, d;
+  int P;              // positions per work item
+  int64_t max_items;  // bound on the items of one group
+};
+#ifdef __CUDACC__
+struct DensePlanScratch {
+  int* n_items;
+  int* first;   // [S + 1] items before each sequence
+  int* depth;   // [ceil(N / P) + 1] counts, then the next free place of each depth
+  int4* items;  // (first position, sequence's first and end row, 0), those that see most keys first
+};
+#endif
+DensePlan dense_plan(int64_t N, int S, int H_q, int H_kv, int d);
+size_t dense_scratch_bytes(const DensePlan& p);
+cudaError_t launch_dense_prefill(const void* q, const void* k, const void* v, const int32_t* cu, const DensePlan& p,
+                                 float scale, void* out, float* lse, void* scratch, DeviceStatus* st, cudaStream_t s);
+
+// ---- 4-bit paged cache (msa_kv4.cu)
+cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
+                             const int32_t* table, int64_t max_pages, const Kv4Pool& pool, DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
+                            const int32_t* table, int64_t max_pages, void* k, void* v, DeviceStatus* st, cudaStream_t s);
+size_t dense_decode_scratch_bytes(int H_kv, int gs, int d);
+cudaError_t launch_dense_decode(const void* q, const Kv4Pool& pool, const int32_t* table, int64_t max_pages,
+                                const int32_t* ctx_len, int B, int H_q, float scale, void* out, float* lse, void* scratch,
+                                DeviceStatus* st, cudaStream_t s);
+
+// ---- page tables (msa_pages.cu)
+struct Pages {
+  int32_t* table;  // [n_seqs, max_pages]
+  int32_t* ctx;    // [n_seqs]
+  int32_t* refs;   // [n_pages]
+  int64_t max_pages, n_pages;
+  int n_seqs, page;
+};
+constexpr int kMaxPools = 8;
+constexpr int kMaxPageSeqs = 4096;  // sequences named in one call
+struct PagePools {
+  char* base[kMaxPools];
+  size_t page_bytes[kMaxPools];  // multiples of 16
+  int n;
+};
+size_t pages_scratch_bytes(const Pages& p, int n);
+cudaError_t launch_pages_reserve(const Pages& p, const int32_t* seqs, const int32_t* new_len, int n, DeviceStatus* st,
+                                 cudaStream_t s);
+cudaError_t launch_pages_fork(const Pages& p, const int32_t* src, const int32_t* dst, int n, const PagePools& pools,
+                              void* scratch, DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_pages_free(const Pages& p, const int32_t* seqs, int n, DeviceStatus* st, cudaStream_t s);
+cudaError_t launch_pages_compact(const Pages& p, const PagePools& pools, int32_t* page_map, int32_t* n_live, void* scratch,
+                                 DeviceStatus* st, cudaStream_t s);
 
 // Fixed device scratch of msa_decode_noalloc (8 MiB, shared by all calls on a
 // device).  Returns its device address for the current device (looked up on

@@ -1,0 +1,72 @@
+// The 4-bit cache format on the device: encoding one lane's 8 channels and
+// expanding codes to exact bf16 values.
+//
+// A head row of d values has 4 groups of d / 4.  A group's scale is a byte
+// e << 3 | m of value 2^(e - 20) (1 + m / 8) (255 = NaN), a value is
+// (code - 8) * scale.  code - 8 has at most 4 significant bits and the scale
+// has 4, so every value is exact in bf16 (8 significant bits).
+#pragma once
+
+#include "msa_common.cuh"
+
+namespace msa {
+namespace kv4 {
+
+constexpr int kGroups = 4;            // scales of a head row
+constexpr uint32_t kScaleNaN = 255u;  // a group that held a NaN or an infinity
+constexpr uint32_t kScaleMax = 254u;
+
+// bf16 bits of a scale: the byte is the top of a bf16 mantissa, its exponent moved by 127 - 20.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) {
+  return byte == kScaleNaN ? 0x7FFFu : (byte << 4) + (107u << 7);
+}
+__device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float((byte << 20) + (107u << 23)); }
+
+__device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// -136 * scale of both halves: exact (136 = 17 * 8 and the scale's mantissa is at most 15, 17 * 15 = 255).
+__device__ __forceinline__ uint32_t scale_bias(uint32_t s2) { return hmul2_bf16(s2, 0xC308C308u); }
+
+// Nibble n (0..3) of both 16-bit halves of w as two bf16 values: 0x4300 | code is the bf16 128 + code, and
+// (128 + code) s - 136 s is exact under one rounding because the result is.
+template <int N>
+__device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t b2) {
+  return hfma2_bf16(((w >> (4 * N)) & 0x000F000Fu) | 0x43004300u, s2, b2);
+}
+
+// A word's 8 channels in order, as 4 bf16 pairs: nibble n of the low half is channel 2n, of the high half 2n + 1.
+__device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t s2, uint32_t b2) {
+  return make_uint4(expand<0>(w, s2, b2), expand<1>(w, s2, b2), expand<2>(w, s2, b2), expand<3>(w, s2, b2));
+}
+
+// The scale of a group whose largest magnitude is the bf16 `amax` (bits, finite): the smallest one with
+// 7 scale >= amax.  The top mantissa bits of amax / 7 give it or the one below it, and 7 scale is exact.
+__device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits << 16);
+  int b = (int)(__float_as_uint(a * (1.0f / 7.0f)) >> 20) - (107 << 3);
+  b = min(max(b, 0), (int)kScaleMax);
+  if (7.0f * scale_f32((uint32_t)b) < a) ++b;
+  return (uint32_t)min(b, (int)kScaleMax);
+}
+
+// round-to-nearest-even(x / s) clamped to -7..7, plus 8.  x has 8 and s has 4 significant bits, so x / s is a
+// tie or at least 2^-11 away from one wherever it rounds to a code; x * (1 / s) in fp32 is off by less than
+// 2^-20, and adding and taking off 1.5 * 2^10 rounds it to a multiple of 2^-13, which makes a tie exact again.
+__device__ __forceinline__ uint32_t code_of(float x, float inv_s) {
+  float y = __fmul_rn(x, inv_s);
+  y = fminf(fmaxf(y, -8.0f), 8.0f);
+  y = __fadd_rn(__fadd_rn(y, 1536.0f), -1536.0f);
+  const int c = __float2int_rn(y);
+  return (uint32_t)(min(max(c, -7), 7) + 8);
+}
+
+}  // namespace kv4
+}  // namespace msa

@@ -26,6 +26,7 @@ MSA_ERR_WORKSPACE_TOO_SMALL = 3
 MSA_ERR_CUDA = 4
 MSA_ERR_BAD_INDEX = 5
 MSA_ERR_TIMEOUT = 6
+MSA_ERR_NO_PAGES = 7
 
 
 class msa_shape_t(ctypes.Structure):
@@ -33,8 +34,25 @@ class msa_shape_t(ctypes.Structure):
                 ("d_I", ctypes.c_int), ("Bk", ctypes.c_int), ("k", ctypes.c_int)]
 
 
+class msa_kv4_pool_t(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class msa_pages_t(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("n_seqs", ctypes.c_int),
+                ("page_size", ctypes.c_int)]
+
+
+class msa_page_pool_t(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
+
+
 _P, _I64, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SP = ctypes.POINTER(msa_shape_t)
+_KP, _GP, _LP = ctypes.POINTER(msa_kv4_pool_t), ctypes.POINTER(msa_pages_t), ctypes.POINTER(msa_page_pool_t)
 
 _SIGS = {
     "msa_select_blocks_workspace": (_SZ, [_I64, _I, _I, _I, _I]),
@@ -63,6 +81,20 @@ _SIGS = {
     "msa_prefill_fp8": (_I, [_P, _P, _P, _P, _P, _SP, _F, _P, _P, _P, _P, _SZ, _P]),
     "msa_decode_fp8": (_I, [_P, _P, _P, _P, _P, _P, _I, _SP, _F, _P, _P, _P, _P, _SZ, _P]),
     "msa_decode_paged_fp8": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I, _P, _I, _SP, _F, _P, _P, _P, _P, _SZ, _P]),
+    "msa_dense_prefill_varlen_workspace": (_SZ, [_I64, _I, _I, _I, _I]),
+    "msa_dense_prefill_varlen": (_I, [_P, _P, _P, _P, _I, _I64, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "msa_kv4_workspace": (_SZ, []),
+    "msa_kv4_store": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I64, _KP, _P, _SZ, _P]),
+    "msa_kv4_load": (_I, [_KP, _I64, _P, _I, _P, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "msa_dense_decode_paged_kv4_workspace": (_SZ, [_I, _I, _I, _I]),
+    "msa_dense_decode_paged_kv4": (_I, [_P, _KP, _P, _I64, _P, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "msa_decode_paged_kv4": (_I, [_P, _P, _P, _KP, _P, _I64, _P, _I, _SP, _F, _P, _P, _P, _P, _SZ, _P]),
+    "msa_decode_paged_kv4_fp8": (_I, [_P, _P, _P, _KP, _P, _I64, _P, _I, _SP, _F, _P, _P, _P, _P, _SZ, _P]),
+    "msa_pages_workspace": (_SZ, [_GP, _I]),
+    "msa_pages_reserve": (_I, [_GP, _P, _P, _I, _P, _SZ, _P]),
+    "msa_pages_fork": (_I, [_GP, _P, _P, _I, _LP, _I, _P, _SZ, _P]),
+    "msa_pages_free": (_I, [_GP, _P, _I, _P, _SZ, _P]),
+    "msa_pages_compact": (_I, [_GP, _LP, _I, _P, _P, _P, _SZ, _P]),
     "msa_check_device_error": (_I, [_P, _P]),
     "msa_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -269,6 +301,113 @@ def msa_warmup_index_grad(q, k, q_idx, k_idx, lse, lse_idx, shp, scale, kl_weigh
     return _check(_lib.msa_warmup_index_grad(_ptr(q), _ptr(k), _ptr(q_idx), _ptr(k_idx), _ptr(lse), _ptr(lse_idx),
                                              ctypes.byref(shp), float(scale), float(kl_weight), _ptr(dq_idx),
                                              _ptr(dk_idx), _ptr(kl), _stream(stream)), "msa_warmup_index_grad")
+
+
+def msa_dense_prefill_varlen_workspace(N, S, H_q, H_kv, d):
+    return int(_lib.msa_dense_prefill_varlen_workspace(int(N), int(S), H_q, H_kv, d))
+
+
+def msa_dense_prefill_varlen(q, k, v, cu_seqlens, S, N, H_q, H_kv, d, scale, out, lse, workspace,
+                             workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_dense_prefill_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), int(S), int(N), H_q, H_kv,
+                                                d, float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb,
+                                                _stream(stream)), "msa_dense_prefill_varlen")
+
+
+def kv4_pool(k_codes, k_scales, v_codes, v_scales, n_pages, page_size, H_kv, d):
+    return msa_kv4_pool_t(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), int(n_pages), int(page_size),
+                          int(H_kv), int(d))
+
+
+def msa_kv4_workspace():
+    return int(_lib.msa_kv4_workspace())
+
+
+def msa_kv4_store(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, pool, workspace, workspace_bytes=None,
+                  stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_kv4_store(_ptr(k), _ptr(v), int(N), _ptr(cu_seqlens), int(S), _ptr(pos0), _ptr(page_table),
+                                     int(max_pages), ctypes.byref(pool), _ptr(workspace), wb, _stream(stream)),
+                  "msa_kv4_store")
+
+
+def msa_kv4_load(pool, N, cu_seqlens, S, pos0, page_table, max_pages, k, v, workspace, workspace_bytes=None,
+                 stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_kv4_load(ctypes.byref(pool), int(N), _ptr(cu_seqlens), int(S), _ptr(pos0),
+                                    _ptr(page_table), int(max_pages), _ptr(k), _ptr(v), _ptr(workspace), wb,
+                                    _stream(stream)), "msa_kv4_load")
+
+
+def msa_dense_decode_paged_kv4_workspace(B, H_q, H_kv, d):
+    return int(_lib.msa_dense_decode_paged_kv4_workspace(int(B), H_q, H_kv, d))
+
+
+def msa_dense_decode_paged_kv4(q_t, pool, page_table, max_pages, ctx_len, B, H_q, scale, out, lse, workspace,
+                               workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_dense_decode_paged_kv4(_ptr(q_t), ctypes.byref(pool), _ptr(page_table), int(max_pages),
+                                                  _ptr(ctx_len), int(B), H_q, float(scale), _ptr(out), _ptr(lse),
+                                                  _ptr(workspace), wb, _stream(stream)), "msa_dense_decode_paged_kv4")
+
+
+def msa_decode_paged_kv4(q_t, q_idx_t, k_idx_pool, pool, page_table, max_pages, ctx_len, B, shp, scale, out, lse,
+                         block_idx, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_decode_paged_kv4(_ptr(q_t), _ptr(q_idx_t), _ptr(k_idx_pool), ctypes.byref(pool),
+                                            _ptr(page_table), int(max_pages), _ptr(ctx_len), int(B),
+                                            ctypes.byref(shp), float(scale), _ptr(out), _ptr(lse), _ptr(block_idx),
+                                            _ptr(workspace), wb, _stream(stream)), "msa_decode_paged_kv4")
+
+
+def msa_decode_paged_kv4_fp8(q_t, q_idx_t, k_idx_pool, pool, page_table, max_pages, ctx_len, B, shp, scale, out, lse,
+                             block_idx, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_decode_paged_kv4_fp8(_ptr(q_t), _ptr(q_idx_t), _ptr(k_idx_pool), ctypes.byref(pool),
+                                                _ptr(page_table), int(max_pages), _ptr(ctx_len), int(B),
+                                                ctypes.byref(shp), float(scale), _ptr(out), _ptr(lse),
+                                                _ptr(block_idx), _ptr(workspace), wb, _stream(stream)),
+                  "msa_decode_paged_kv4_fp8")
+
+
+def pages(page_table, ctx_len, refs, max_pages, n_pages, n_seqs, page_size):
+    return msa_pages_t(_ptr(page_table), _ptr(ctx_len), _ptr(refs), int(max_pages), int(n_pages), int(n_seqs),
+                       int(page_size))
+
+
+def page_pools(entries):
+    """A C array of (base, page_bytes) entries for the page calls."""
+    entries = list(entries)
+    return (msa_page_pool_t * max(1, len(entries)))(*[msa_page_pool_t(_ptr(b), int(n)) for b, n in entries])
+
+
+def msa_pages_workspace(pgs, n):
+    return int(_lib.msa_pages_workspace(ctypes.byref(pgs), int(n)))
+
+
+def msa_pages_reserve(pgs, seqs, new_len, n, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_pages_reserve(ctypes.byref(pgs), _ptr(seqs), _ptr(new_len), int(n), _ptr(workspace), wb,
+                                         _stream(stream)), "msa_pages_reserve")
+
+
+def msa_pages_fork(pgs, src, dst, n, pools, n_pools, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_pages_fork(ctypes.byref(pgs), _ptr(src), _ptr(dst), int(n), pools, int(n_pools),
+                                      _ptr(workspace), wb, _stream(stream)), "msa_pages_fork")
+
+
+def msa_pages_free(pgs, seqs, n, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_pages_free(ctypes.byref(pgs), _ptr(seqs), int(n), _ptr(workspace), wb, _stream(stream)),
+                  "msa_pages_free")
+
+
+def msa_pages_compact(pgs, pools, n_pools, page_map, n_live, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_pages_compact(ctypes.byref(pgs), pools, int(n_pools), _ptr(page_map), _ptr(n_live),
+                                         _ptr(workspace), wb, _stream(stream)), "msa_pages_compact")
 
 
 def msa_check_device_error(workspace, stream=None):

@@ -53,7 +53,8 @@ typedef enum {
   MSA_ERR_WORKSPACE_TOO_SMALL = 3,
   MSA_ERR_CUDA = 4,
   MSA_ERR_BAD_INDEX = 5,
-  MSA_ERR_TIMEOUT = 6
+  MSA_ERR_TIMEOUT = 6,
+  MSA_ERR_NO_PAGES = 7
 } msa_status_t;
 
 /* Problem shape.  G = H_kv GQA groups (one index-query head per group);
@@ -397,10 +398,197 @@ msa_status_t msa_decode_noalloc(const void* q_t, const void* q_idx_t, const void
                                 const void* v_cache, const int32_t* ctx_len, int B, const msa_shape_t* shape,
                                 float scale, void* out, float* lse, int32_t* block_idx, msa_stream_t stream);
 
+/* ---------------------------------------------------------------- dense prefill
+ * Dense causal GQA attention over a packed batch of whole prompts, without an
+ * index branch.  Pages: the "MSA" study note, 1-1 (dense causal GQA
+ * attention, the branch that the sparse one replaces), and the velog llama.cpp
+ * analysis, section 4 (the path that a serving engine falls back to when
+ * several sequences share a batch).
+ *
+ * Sequence s holds rows [cu_seqlens[s], cu_seqlens[s+1]) of the N-row tensors;
+ * cu_seqlens[0] = 0, the values do not decrease and cu_seqlens[S] <= N.  Any
+ * lengths are allowed, 0 among them, and starts need no alignment.  For row t
+ * of a sequence, over its rows j <= t:
+ *   out[t, h] = softmax_j(scale q[t, h].k[j, h / gs]) v[j, h / gs].
+ *
+ *   q          [N, H_q, d] bf16;  k, v [N, H_kv, d] bf16
+ *   cu_seqlens [S+1] int32 (device), S >= 1
+ *   out        [N, H_q, d] bf16 out
+ *   lse        [H_q, N] fp32 out: natural-log log-sum-exp of the scaled scores
+ * Rows of no sequence (past cu_seqlens[S]) are neither read into a result nor
+ * written: their out and lse stay as they were, whatever q, k and v hold there.
+ * A cu_seqlens that breaks the rules sets the device error word
+ * (MSA_ERR_BAD_INDEX) and nothing is written.  Supported: d in {64, 128},
+ * H_q / H_kv in {1, 2, 4, 8}, H_kv <= 64, N <= 2^24.
+ */
+size_t msa_dense_prefill_varlen_workspace(int64_t N, int S, int H_q, int H_kv, int d);
+msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int S,
+                                      int64_t N, int H_q, int H_kv, int d, float scale, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit cache
+ * A paged K/V cache in 4 bits.  Pages: velog llama.cpp analysis, section 2 (at
+ * 1M tokens the K/V cache is what fills the memory: 4096 bytes a token and
+ * layer in bf16; the pages name no 4-bit form, this one is the library's own).
+ *
+ * Format.  A head row of d values has 4 groups of d / 4 channels.  Each group
+ * has a scale byte e << 3 | m of value 2^(e - 20) (1 + m / 8), 255 = NaN, and
+ * each value a code 0..15 that stands for (code - 8) * scale, which bf16 holds
+ * exactly.  Codes fill 32-bit words of 8 channels: nibble n (bits 4n .. 4n + 3)
+ * is channel 2n for n < 4 and channel 2 (n - 4) + 1 for n >= 4.
+ * Quantization of a group: scale = the smallest one with 7 scale >= max |x|,
+ * code = 8 + x / scale rounded to nearest even and clamped to -7 .. 7.
+ * Magnitudes beyond 7 * 3584 saturate.  A group that holds a NaN or an infinity
+ * gets the NaN scale: all its values read as NaN.
+ *
+ *   k_codes, v_codes   [n_pages, page_size, H_kv, d / 2] bytes
+ *   k_scales, v_scales [n_pages, page_size, H_kv, 4] bytes
+ * All four 16-byte aligned; page_size a positive multiple of 16; d in {64, 128};
+ * 1 <= H_kv <= 64.  A token takes (d / 2 + 4) * 2 * H_kv bytes (1088 at d = 128,
+ * H_kv = 8, against 4096 in bf16).
+ *
+ * msa_kv4_store: quantizes packed rows into the pages of their sequences.
+ *   k, v       [N, H_kv, d] bf16
+ *   cu_seqlens [S+1] int32 (device): sequence s's rows are [cu[s], cu[s+1])
+ *   pos0       [S] int32 (device): token position of a sequence's first row
+ *   page_table [S, max_pages] int32 (device): row i of sequence s becomes token
+ *              t = pos0[s] + i - cu[s], in page page_table[s][t / page_size]
+ * A whole prompt is stored with pos0 = 0, the new tokens of a decode step with
+ * one row a sequence and pos0 = the lengths so far.  Rows of no sequence are
+ * passed over.  A row whose position lies outside the table, or whose page id
+ * lies outside [0, n_pages), is skipped and sets the device error word
+ * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.
+ * msa_kv4_load: the same rows back, k and v [N, H_kv, d] bf16 out (exact
+ *   values of the codes); a bad row reads as zeros (and sets the error word),
+ *   rows of no sequence stay as they were.
+ * workspace: msa_kv4_workspace() bytes (the error word).
+ */
+typedef struct {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int64_t n_pages;
+  int page_size;
+  int H_kv;
+  int d;
+} msa_kv4_pool_t;
+size_t msa_kv4_workspace(void);
+msa_status_t msa_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu_seqlens, int S,
+                           const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                           const msa_kv4_pool_t* pool, void* workspace, size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_kv4_load(const msa_kv4_pool_t* pool, int64_t N, const int32_t* cu_seqlens, int S,
+                          const int32_t* pos0, const int32_t* page_table, int64_t max_pages, void* k, void* v,
+                          void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* msa_dense_decode_paged_kv4: one decode token per sequence over its whole
+ * 4-bit cache (the single-token form of msa_dense_prefill_varlen).
+ *   q_t        [B, H_q, d] bf16
+ *   page_table [B, max_pages] int32 (device); entries past a sequence's length
+ *              are not read
+ *   ctx_len    [B] int32 (device): tokens of each sequence in the cache, its
+ *              newest included.  0 is an empty sequence: out 0, lse -inf.
+ *   out        [B, H_q, d] bf16 out;  lse [B, H_q] fp32 out (nullable)
+ * ctx_len outside [0, max_pages * page_size] counts as 0 and sets the device
+ * error word; so does a page id outside [0, n_pages), read as page 0.
+ * Scores, softmax and sums are fp32; probabilities are rounded to bf16 for the
+ * product with V.  Supported: H_q / H_kv in {1, 2, 4, 8}.
+ *
+ * msa_decode_paged_kv4, msa_decode_paged_kv4_fp8: msa_decode_paged and
+ * msa_decode_paged_fp8 with K and V in a 4-bit pool (index keys stay in their
+ * own pool [n_pages, page_size, d_I] of the same pages).  Same selection, the
+ * attention over the chosen blocks on the 4-bit values.  shape->H_kv and d are
+ * the pool's, shape->N = max_pages * page_size; workspace
+ * msa_decode_workspace(B, shape) bytes.
+ */
+size_t msa_dense_decode_paged_kv4_workspace(int B, int H_q, int H_kv, int d);
+msa_status_t msa_dense_decode_paged_kv4(const void* q_t, const msa_kv4_pool_t* pool, const int32_t* page_table,
+                                        int64_t max_pages, const int32_t* ctx_len, int B, int H_q, float scale,
+                                        void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                        msa_stream_t stream);
+msa_status_t msa_decode_paged_kv4(const void* q_t, const void* q_idx_t, const void* k_idx_pool,
+                                  const msa_kv4_pool_t* pool, const int32_t* page_table, int64_t max_pages,
+                                  const int32_t* ctx_len, int B, const msa_shape_t* shape, float scale, void* out,
+                                  float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
+                                  msa_stream_t stream);
+msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, const void* k_idx_pool,
+                                      const msa_kv4_pool_t* pool, const int32_t* page_table, int64_t max_pages,
+                                      const int32_t* ctx_len, int B, const msa_shape_t* shape, float scale, void* out,
+                                      float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
+                                      msa_stream_t stream);
+
+/* ---------------------------------------------------------------- pages of a cache
+ * Page tables with reference counts, for any paged cache of this library (the
+ * bf16 pools of msa_decode_paged, the 4-bit pools, the index-key pools).
+ * Pages: velog llama.cpp analysis, sections 4 and 5 (an explicit map from a
+ * sequence's positions to cache cells is what lets sequences share a cache).
+ *
+ * State (device, the caller's):
+ *   page_table [n_seqs, max_pages] int32: sequence s holds the pages
+ *              page_table[s][0 .. ceil(ctx_len[s] / page_size)); entries past
+ *              them are not read, and written only where a call says so
+ *   ctx_len    [n_seqs] int32
+ *   refs       [n_pages] int32: how many sequences hold each page, 0 = free.
+ * A new cache has ctx_len and refs 0.  Pages are shared whole: only a page
+ * that one sequence holds is ever partly filled.
+ *
+ * msa_pages_reserve: sequence seqs[i] grows to new_len[i] tokens.  The pages
+ *   it lacks are the lowest-numbered free ones, given out in the order of the
+ *   entries and of the positions within one.  An entry that names no sequence,
+ *   names one twice or would shrink it (or outgrow its table) sets the error
+ *   word (MSA_ERR_BAD_INDEX); too few free pages set MSA_ERR_NO_PAGES.  Either
+ *   way the call then changes nothing.
+ * msa_pages_fork: the empty sequence dst[i] becomes a copy of src[i].  Full
+ *   pages are shared; a partly filled last page is copied, in every pool, into
+ *   the lowest free page (in the order of the entries).  dst must be distinct
+ *   and empty (ctx_len 0) when the call begins; a source may occur often.
+ *   Errors as above: the call then changes nothing (an id outside the pools
+ *   among a source's full pages is copied as it is and sets the error word).
+ * msa_pages_free: sequence seqs[i] becomes empty; its table entries become -1
+ *   and its pages' counts fall.  A sequence named twice is freed once; an entry
+ *   with a bad sequence or a bad page id is skipped and sets the error word.
+ * msa_pages_compact: with L pages held, moves them to pages 0 .. L - 1: the r-th
+ *   free page below L takes in the r-th held page from L on.  Contents (every
+ *   pool), counts and tables follow.
+ *     page_map [n_pages] int32 out (nullable): each page's new id, -1 if free
+ *     n_live   [1] int32 out (nullable): L
+ *
+ * seqs, new_len, src, dst are int32 device arrays of n entries, n <= 4096 (0 is
+ * allowed).  pools: n_pools <= 8 host entries, each a device array of n_pages
+ * pages of page_bytes (a multiple of 16) at a 16-byte aligned address; pass every
+ * pool that the tables address.  workspace: msa_pages_workspace(pages, n)
+ * bytes, n as in the call (0 for compact).
+ * Limits: n_pages, max_pages < 2^27; max_pages * page_size < 2^31.
+ */
+typedef struct {
+  int32_t* page_table;
+  int32_t* ctx_len;
+  int32_t* refs;
+  int64_t max_pages;
+  int64_t n_pages;
+  int n_seqs;
+  int page_size;
+} msa_pages_t;
+typedef struct {
+  void* base;
+  size_t page_bytes;
+} msa_page_pool_t;
+size_t msa_pages_workspace(const msa_pages_t* pages, int n);
+msa_status_t msa_pages_reserve(const msa_pages_t* pages, const int32_t* seqs, const int32_t* new_len, int n,
+                               void* workspace, size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_pages_fork(const msa_pages_t* pages, const int32_t* src, const int32_t* dst, int n,
+                            const msa_page_pool_t* pools, int n_pools, void* workspace, size_t workspace_bytes,
+                            msa_stream_t stream);
+msa_status_t msa_pages_free(const msa_pages_t* pages, const int32_t* seqs, int n, void* workspace,
+                            size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_pages_compact(const msa_pages_t* pages, const msa_page_pool_t* pools, int n_pools, int32_t* page_map,
+                               int32_t* n_live, void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
 /* ---------------------------------------------------------------- status
  * msa_check_device_error: waits for `stream`, then returns MSA_ERR_BAD_INDEX
  * if the last call that used `workspace` met bad data on the device,
- * MSA_ERR_TIMEOUT if one of its kernels gave up a bounded wait, MSA_OK
+ * MSA_ERR_TIMEOUT if one of its kernels gave up a bounded wait,
+ * MSA_ERR_NO_PAGES if a page call found too few free pages, MSA_OK
  * otherwise (or MSA_ERR_CUDA if the wait itself failed).
  * msa_status_string: a static, readable description of a status.
  */
