@@ -7,14 +7,13 @@
 // end of the launch.
 #include <math.h>
 
-#include "msa_common.cuh"
-#include "msa_tiles.cuh"
+#include "msa_sm100.cuh"
 
 namespace msa {
 
 namespace {
 
-using namespace tiles;
+using namespace sm100;
 
 constexpr int kPlanThreads = 1024;
 
@@ -49,6 +48,7 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
                                                                   DensePlanScratch w, int depths, DeviceStatus* st) {
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
+  griddep_launch_dependents();  // the attention's CTAs may set up meanwhile; they wait for this grid's end
   int bad = 0;
   for (int s = tid; s <= S; s += kPlanThreads) {
     const int32_t c = cu[s];
@@ -105,124 +105,536 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
   }
 }
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+// ---------------------------------------------------------------- attention
+// One CTA per SM, persistent.  A work item is two query tiles of 128 rows (row
+// = position * gs + head: 128 / gs positions x gs heads of one group) over the
+// same keys; items are taken in the planned order, every other round backwards,
+// so that the CTAs' sums stay even.  Per 128-key tile and query tile:
+//   S = Q K^T -> TMEM;  P = 2^(S scale' - m) as bf16 over S's columns;  O += P V
+// with O in TMEM.  The two query tiles alternate: while one's softmax runs, the
+// tensor cores work on the other's P V and next S.  The running maximum is
+// lazy: O and the row sum are rescaled only when a row's maximum has grown by
+// more than 2^8, so P stays below 256 (its bf16 rounding is relative, so the
+// factor costs no precision) and the rescale of O in TMEM is rare.
+// Warpgroups: 0 and 1 the softmax of query tile 0 and 1 (a thread per row), 2
+// the output (O / l, lse), 3 one warp each for the TMA loads, the MMA issue,
+// and two guard warps.
+//
+// The guard warps make the masked places of V harmless, because a weight of 0
+// times a NaN or an infinity would not be 0 on the tensor cores: in the key
+// tiles that not every row of the item sees whole, they clear the rows past the
+// item's last position and any value that is not finite, and the epilogue then
+// adds the latter to the rows that do see them.
+constexpr int kRowsT = 128, kKeysT = 128;
+constexpr int kThreadsA = 512;
+constexpr uint32_t kRegsSoft = 184, kRegsEpi = 72, kRegsLoad = 72;
+static_assert(256 * kRegsSoft + 128 * kRegsEpi + 128 * kRegsLoad == kThreadsA * 128, "the registers of the launch");
+constexpr int kWarpEpi = 8, kWarpLoad = 12, kWarpMma = 13, kWarpGuard = 14;
+constexpr float kLazy = 8.0f;
+constexpr int kPoisonSlots = 8;
 
-// One CTA per (item, group): 64 rows = 64 / gs positions x gs heads, row = position * gs + head; keys in tiles
-// of 64 through shared memory, online softmax in registers.
 template <int D>
-__global__ void __launch_bounds__(kThreads) dense_prefill_kernel(const uint16_t* __restrict__ q,
-                                                                 const uint16_t* __restrict__ kc,
-                                                                 const uint16_t* __restrict__ vc, int64_t N, int H_q,
-                                                                 int H_kv, float scale, DensePlanScratch w,
-                                                                 uint16_t* __restrict__ out, float* __restrict__ lse) {
-  extern __shared__ __align__(16) uint16_t sm[];
-  const int item = blockIdx.x / H_kv, g = blockIdx.x % H_kv, gs = H_q / H_kv;
-  if (item >= *w.n_items) return;
-  const int4 it = w.items[item];
-  const int64_t t0 = it.x, seq0 = it.y, seq1 = it.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint16_t* qs = sm;
-  uint16_t* ks = sm + kRows * D;
-  uint16_t* vs = ks + kKeys * D;
-  const int64_t kv_row = (int64_t)H_kv * D;
-  load_rows(qs, kRows, D, q, [&](int r) -> const uint16_t* {
-    const int64_t t = t0 + r / gs;
-    return t < seq1 ? q + (t * H_q + (int64_t)g * gs + r % gs) * D : nullptr;
-  });
-  cp_async_commit();
-  const int64_t t_last = min(t0 + kRows / gs, seq1) - 1;
-  const float sl2 = scale * 1.4426950408889634f;
-  float o[D / 8][4], m[2], l[2];
+struct Layout {
+  static constexpr int NC = D / 64;                  // 64-column chunks
+  static constexpr int CHUNK = 128 * 128;            // bytes of one chunk of a 128-row tile
+  static constexpr int TILE = NC * CHUNK;
+  static constexpr int STAGES = D == 128 ? 4 : 8;    // K and V tiles in flight
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_ST = OFF_KV + STAGES * TILE;  // (m, l) of each row
+  static constexpr int OFF_BAR = OFF_ST + 2 * 128 * 8;
+  static constexpr int SMEM = 1024 + OFF_BAR + 512;
+  static constexpr uint32_t TMEM_O = 256;            // S / P of tile q at 128 q, O of tile q at 256 + 128 q
+};
+
+template <uint32_t R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R)); }
+template <uint32_t R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
+  return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+}
+
+// One item of the CTA's sequence of them, positions relative to the start of the sequence.
+struct Item {
+  int t0, len;   // first position, length of the sequence
+  int row0, g;   // row of the sequence's first position, group
+  int n[2];      // key tiles that query tile 0 and 1 see (0: no rows)
+  __device__ __forceinline__ int n_max() const { return max(n[0], n[1]); }
+};
+struct Items {
+  const int4* items;
+  int total, H_kv, PT;  // items x groups, groups, positions of a query tile
+  __device__ __forceinline__ bool get(int round, Item& it) const {
+    const int b = (int)blockIdx.x, n = (int)gridDim.x;
+    const int i = round * n + ((round & 1) ? n - 1 - b : b);
+    if (i >= total) return false;
+    const int4 x = items[i / H_kv];
+    it.g = i % H_kv;
+    it.row0 = x.y;
+    it.t0 = x.x - x.y;
+    it.len = x.z - x.y;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  m[0] = m[1] = __int_as_float(0xff800000);
-  l[0] = l[1] = 0.f;
-  int64_t row_t[2];
+    for (int q = 0; q < 2; ++q) {
+      const int a = it.t0 + q * PT;
+      it.n[q] = a < it.len ? (min(a + PT, it.len) - 1) / kKeysT + 1 : 0;
+    }
+    return true;
+  }
+};
+
+template <int D, int GS>
+__global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ v, int64_t N, int H_q, int H_kv,
+    float scale_log2, DensePlanScratch w, uint16_t* __restrict__ out, float* __restrict__ lse, DeviceStatus* st) {
+  using L = Layout<D>;
+  constexpr int PT = kRowsT / GS;
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(kRowsT, kKeysT);
+  constexpr uint32_t IDESC_PV = idesc_bf16_f32(kRowsT, D) | (1u << 16);  // V is MN-major
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(sm);
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int poison[kPoisonSlots];  // 1 + the round whose V tiles held values that are not finite
+  const uint32_t bar = sb + L::OFF_BAR;
+  auto kv_full = [&](int i) { return bar + 8u * i; };                    // TMA -> MMA, guard
+  auto kv_empty = [&](int i) { return bar + 8u * (L::STAGES + i); };     // MMA (commit) -> TMA
+  constexpr int B0 = 2 * L::STAGES;
+  auto q_full = [&](int q) { return bar + 8u * (B0 + q); };              // TMA -> MMA
+  auto q_empty = [&](int q) { return bar + 8u * (B0 + 2 + q); };         // MMA (commit) -> TMA
+  auto s_full = [&](int q) { return bar + 8u * (B0 + 4 + q); };          // MMA (commit) -> softmax
+  auto p_full = [&](int q) { return bar + 8u * (B0 + 6 + q); };          // softmax (4 warps) -> MMA
+  auto pv_done = [&](int q) { return bar + 8u * (B0 + 8 + q); };         // MMA (commit) -> softmax
+  auto o_full = [&](int q) { return bar + 8u * (B0 + 10 + q); };         // MMA (commit) -> output
+  auto o_empty = [&](int q) { return bar + 8u * (B0 + 12 + q); };        // output (4 warps) -> MMA, softmax
+  auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (4 warps) -> output
+  // V tiles alone, which sit in the odd stages; one a stage, so that the guard cannot be two phases ahead
+  auto v_ok = [&](int i) { return bar + 8u * (B0 + 16 + i / 2); };       // guard (2 warps) -> MMA
+  const uint32_t drain = bar + 8u * (B0 + 16 + L::STAGES / 2);
+  static_assert(L::STAGES % 2 == 0 && 8 * (B0 + 17 + L::STAGES / 2) <= 512, "K and V alternate; barriers fit");
+  float2* ml_s = reinterpret_cast<float2*>(sm + L::OFF_ST);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < L::STAGES; ++i) {
+      mbar_init(kv_full(i), 1);
+      mbar_init(kv_empty(i), 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(q_full(q), 1);
+      mbar_init(q_empty(q), 1);
+      mbar_init(s_full(q), 1);
+      mbar_init(p_full(q), 4);
+      mbar_init(pv_done(q), 1);
+      mbar_init(o_full(q), 1);
+      mbar_init(o_empty(q), 4);
+      mbar_init(ml_full(q), 4);
+    }
+    for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_ok(i), 2);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    abort_flag = 0;
+    for (int i = 0; i < kPoisonSlots; ++i) poison[i] = 0;
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // the plan
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort = &abort_flag;
+  Items items;
+  items.items = w.items;
+  items.total = *w.n_items * H_kv;
+  items.H_kv = H_kv;
+  items.PT = PT;
+  Item it;
+
+  if (warp >= kWarpLoad) {
+    regs_dec<kRegsLoad>();
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------------------ TMA
+      if (lane == 0) {
+        uint32_t kv = 0, qn[2] = {0, 0};
+        bool ok = true;
+        auto load_kv = [&](const CUtensorMap* map, int j) {
+          const int s = (int)(kv % L::STAGES);
+          if (!(ok = mbar_wait(kv_empty(s), ((kv / L::STAGES) & 1) ^ 1, abort, st, 0xD01))) return;
+          mbar_arrive_expect_tx(kv_full(s), (uint32_t)L::TILE);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) row_t[e] = t0 + (warp * 16 + (lane >> 2) + 8 * e) / gs;
-  for (int64_t j0 = seq0; j0 <= t_last; j0 += kKeys) {
-    __syncthreads();
-    auto src = [&](const uint16_t* base) {
-      return [=](int r) -> const uint16_t* { return j0 + r < seq1 ? base + (j0 + r) * kv_row + (int64_t)g * D : nullptr; };
-    };
-    load_rows(ks, kKeys, D, kc, src(kc));
-    load_rows(vs, kKeys, D, vc, src(vc));
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    float s[kKeys / 8][4];
+          for (int c = 0; c < L::NC; ++c)
+            tma_load_3d(sb + L::OFF_KV + s * L::TILE + c * L::CHUNK, map, c * 64, it.g, it.row0 + j * kKeysT, kv_full(s));
+          ++kv;
+        };
+        auto load_q = [&](int q) {
+          if (!(ok = mbar_wait(q_empty(q), (qn[q] & 1) ^ 1, abort, st, 0xD02))) return;
+          mbar_arrive_expect_tx(q_full(q), (uint32_t)L::TILE);
 #pragma unroll
-    for (int i = 0; i < kKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+          for (int c = 0; c < L::NC; ++c)
+            tma_load_3d(sb + L::OFF_Q + q * L::TILE + c * L::CHUNK, &tm_q, c * 64, it.g * GS, it.row0 + it.t0 + q * PT,
+                        q_full(q));
+          ++qn[q];
+        };
+        for (int r = 0; ok && items.get(r, it); ++r) {
+          const int n = it.n_max();
+          load_q(0);
+          if (ok) load_kv(&tm_k, 0);
+          if (ok && it.n[1]) load_q(1);
+          if (ok) load_kv(&tm_v, 0);
+          for (int j = 1; ok && j < n; ++j) {
+            load_kv(&tm_k, j);
+            if (ok) load_kv(&tm_v, j);
+          }
+        }
+        if (!ok) {  // let the copies in flight land before the CTA ends
+          for (uint32_t x = kv > (uint32_t)L::STAGES ? kv - L::STAGES : 0; x < kv; ++x)
+            mbar_wait(kv_full((int)(x % L::STAGES)), (x / L::STAGES) & 1, nullptr, st, 0xDF1);
+          for (int q = 0; q < 2; ++q)
+            if (qn[q]) mbar_wait(q_full(q), (qn[q] - 1) & 1, nullptr, st, 0xDF2);
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        uint32_t kv = 0, sn[2] = {0, 0}, in[2] = {0, 0};  // K and V tiles, S products, items
+        bool ok = true;
+        uint32_t k_at = 0, v_at = 0;
+        auto wait_kv = [&](uint32_t x, unsigned code) {
+          return mbar_wait(kv_full((int)(x % L::STAGES)), (x / L::STAGES) & 1, abort, st, code);
+        };
+        auto product_s = [&](int q) {
+          tc_fence_after();
+          const uint32_t qa = sb + L::OFF_Q + q * L::TILE, ka = sb + L::OFF_KV + (k_at % L::STAGES) * L::TILE;
 #pragma unroll
-    for (int kk = 0; kk < D; kk += 16) {
-      uint32_t a[4];
-      lds_a(a, smem_u32(qs), warp * 16, kk, D);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int c = ks >> 2, kk = ks & 3;
+            mma_bf16_ss(tmem + q * 128, umma_desc_kmajor(qa + c * L::CHUNK + kk * 32, 128),
+                        umma_desc_kmajor(ka + c * L::CHUNK + kk * 32, 128), IDESC_S, ks > 0);
+          }
+          umma_commit(s_full(q));
+        };
+        for (int r = 0; ok && items.get(r, it); ++r) {
+          const int n = it.n_max();
+          k_at = kv;
+          ok = mbar_wait(q_full(0), in[0] & 1, abort, st, 0xD10) && wait_kv(k_at, 0xD11);
+          if (!ok) break;
+          product_s(0);
+          if (it.n[0] == 1) umma_commit(q_empty(0));
+          if (it.n[1]) {
+            if (!(ok = mbar_wait(q_full(1), in[1] & 1, abort, st, 0xD12))) break;
+            product_s(1);
+            if (it.n[1] == 1) umma_commit(q_empty(1));
+          }
+          umma_commit(kv_empty((int)(k_at % L::STAGES)));
+          for (int j = 0; ok && j < n; ++j) {
+            v_at = kv + 1;
+            k_at = kv + 2;
+            if (!(ok = wait_kv(v_at, 0xD13) && mbar_wait(v_ok((int)(v_at % L::STAGES)), (v_at / L::STAGES) & 1, abort, st,
+                                                         0xD14)))
+              break;
 #pragma unroll
-      for (int n = 0; n < kKeys; n += 16) {
-        uint32_t b[4];
-        lds_b_nk(b, smem_u32(ks), n, kk, D);
-        mma2(s[n / 8], s[n / 8 + 1], a, b);
+            for (int q = 0; q < 2; ++q) {
+              if (j < it.n[q]) {
+                if (j == 0 && !(ok = mbar_wait(o_empty(q), (in[q] & 1) ^ 1, abort, st, 0xD15))) break;
+                if (!(ok = mbar_wait(p_full(q), sn[q] & 1, abort, st, 0xD16))) break;
+                ++sn[q];
+                tc_fence_after();
+                const uint32_t va = sb + L::OFF_KV + (v_at % L::STAGES) * L::TILE;
+#pragma unroll
+                for (int ks = 0; ks < kKeysT / 16; ++ks)
+                  mma_bf16_ts(tmem + L::TMEM_O + q * 128, tmem + q * 128 + ks * 8,
+                              umma_desc_mnmajor_sw128(va + ks * 16 * 128, L::CHUNK), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+                umma_commit(pv_done(q));
+                if (j + 1 == it.n[q]) {
+                  umma_commit(o_full(q));
+                  ++in[q];
+                }
+              }
+              if (j + 1 < it.n[q]) {
+                if (!(ok = wait_kv(k_at, 0xD17))) break;
+                product_s(q);
+                if (j + 2 == it.n[q]) umma_commit(q_empty(q));
+              }
+            }
+            if (!ok) break;
+            umma_commit(kv_empty((int)(v_at % L::STAGES)));
+            if (j + 1 < n) umma_commit(kv_empty((int)(k_at % L::STAGES)));
+            kv += 2;
+          }
+        }
+        if (!ok) {  // the products in flight end before TMEM is released
+          umma_commit(drain);
+          mbar_wait(drain, 0, nullptr, st, 0xDF3);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ guard: rows 64 (warp - kWarpGuard) .. + 63 of V
+      uint32_t kv = 0;
+      bool ok = true;
+      for (int r = 0; ok && items.get(r, it); ++r) {
+        const int n = it.n_max(), jd = it.t0 / kKeysT;
+        const int t_end = min(it.t0 + 2 * PT, it.len);  // past the item's last position
+        for (int j = 0; j < n; ++j) {
+          const uint32_t x = kv + 2 * j + 1;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(kv_full((int)(x % L::STAGES)), (x / L::STAGES) & 1, abort, st, 0xD20))))
+            break;
+          if (j < jd) {  // every row of the item sees the whole tile
+            if (lane == 0) mbar_arrive(v_ok((int)(x % L::STAGES)));
+            continue;
+          }
+          uint8_t* va = sm + L::OFF_KV + (x % L::STAGES) * L::TILE;
+          bool found = false;
+#pragma unroll 4
+          for (int i = lane; i < 64 * L::NC * 8; i += 32) {
+            const int c = i / 512, e = i % 512, row = (warp - kWarpGuard) * 64 + e / 8;  // 16-byte piece of a row
+            uint4* at = reinterpret_cast<uint4*>(va + c * L::CHUNK + row * 128 + (e & 7) * 16);
+            if (j * kKeysT + row >= t_end) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint4 y = *at;
+              if (!(finite_bf16x2(y.x) && finite_bf16x2(y.y) && finite_bf16x2(y.z) && finite_bf16x2(y.w))) {
+                uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((z[k] & 0x7F80u) == 0x7F80u) z[k] &= 0xFFFF0000u;
+                  if ((z[k] & 0x7F800000u) == 0x7F800000u) z[k] &= 0x0000FFFFu;
+                }
+                *at = make_uint4(z[0], z[1], z[2], z[3]);
+                found = true;
+              }
+            }
+          }
+          if (found) poison[r % kPoisonSlots] = r + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_ok((int)(x % L::STAGES)));
+        }
+        kv += 2 * n;
       }
     }
+  } else if (warp >= kWarpEpi) {
+    regs_dec<kRegsEpi>();
+    // ------------------------------------------------------------ output: a thread per row
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const int pos = row / GS, hh = row % GS;
+    uint32_t in[2] = {0, 0};
+    bool ok = true;
+    for (int r = 0; ok && items.get(r, it); ++r) {
+#pragma unroll 1
+      for (int q = 0; ok && q < 2; ++q) {
+        if (it.n[q] == 0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(ml_full(q), in[q] & 1, abort, st, 0xD30) &&
+                                         mbar_wait(o_full(q), in[q] & 1, abort, st, 0xD31));
+        if (!ok) break;
+        ++in[q];
+        tc_fence_after();
+        const float2 ml = ml_s[q * 128 + row];
+        const int t = it.t0 + q * PT + pos;
+        const bool live = t < it.len;
+        const bool bad = poison[r % kPoisonSlots] == r + 1;
+        const float inv = 1.f / ml.y;
+        const int64_t grow = (int64_t)it.row0 + t;
+        const int h = it.g * GS + hh;
+        uint4* orow = reinterpret_cast<uint4*>(out + (grow * H_q + h) * D);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld_x32(tmem + ((uint32_t)(quarter * 32) << 16) + L::TMEM_O + q * 128 + c * 32, x);
+          tmem_ld_wait();
+          reg_fence32(x);
+          if (bad && live)  // the values that the guard took out, for the rows that see them
+            for (int j = it.t0 / kKeysT * kKeysT; j <= t; ++j) {
+              const uint16_t* vr = v + (((int64_t)it.row0 + j) * H_kv + it.g) * D + c * 32;
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t b = vr[e];
+                if ((b & 0x7F80u) == 0x7F80u) {
+                  const float add = __uint_as_float(b << 16);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mx = m[e];
+                  for (int i = 0; i < 32; ++i)
+                    if (i == e) x[i] = __float_as_uint(__uint_as_float(x[i]) + add);
+                }
+              }
+            }
+          if (live)
 #pragma unroll
-      for (int n = 0; n < kKeys / 8; ++n)
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int64_t j = j0 + n * 8 + 2 * (lane & 3) + c;
-          float& x = s[n][2 * e + c];
-          x = j <= row_t[e] ? x * sl2 : __int_as_float(0xff800000);
-          mx = fmaxf(mx, x);
+              for (int i = 0; i < 4; ++i)
+                y[i] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * inv, __uint_as_float(x[8 * e + 2 * i + 1]) * inv);
+              orow[c * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float ms = mx == __int_as_float(0xff800000) ? 0.f : mx;
-      const float alpha = exp2f(m[e] - ms);
-      m[e] = mx;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float& x = s[n][2 * e + c];
-          x = exp2f(x - ms);
-          sum += x;
-        }
-      l[e] = l[e] * alpha + sum;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * e] *= alpha;
-        o[i][2 * e + 1] *= alpha;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty(q));
+        if (live) lse[(int64_t)h * N + grow] = (ml.x + lg2_approx(ml.y)) * 0.69314718055994530942f;
       }
     }
+  } else {
+    regs_inc<kRegsSoft>();
+    // ------------------------------------------------------------ softmax of query tile q: a thread per row
+    const int q = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t scol = tmem + lane_base + q * 128, ocol = tmem + lane_base + L::TMEM_O + q * 128;
+    const float kInf = __int_as_float(0x7f800000);
+    uint32_t sn = 0, in = 0;  // S products and items of this tile so far
+    bool ok = true;
+    for (int r = 0; ok && items.get(r, it); ++r) {
+      const int n = it.n[q];
+      if (n == 0) continue;
+      const int t = min(it.t0 + q * PT + row / GS, it.len - 1);  // rows past the sequence repeat its last one
+      float m = -kInf;
+      uint64_t l2[2] = {0, 0};
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(q), sn & 1, abort, st, 0xD40)))) break;
+        tc_fence_after();
+        uint32_t x[4][32];
 #pragma unroll
-    for (int kk = 0; kk < kKeys; kk += 16) {
-      uint32_t a[4];
-      c_to_a(a, s[kk / 8], s[kk / 8 + 1]);
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(scol + c * 32, x[c]);
+        tmem_ld_wait();
 #pragma unroll
-      for (int n = 0; n < D; n += 16) {
-        uint32_t b[4];
-        lds_b_kn(b, smem_u32(vs), kk, n, D);
-        mma2(o[n / 8], o[n / 8 + 1], a, b);
+        for (int c = 0; c < 4; ++c) reg_fence32(x[c]);
+        const int lim = t - j * kKeysT;  // last visible column
+        if (__any_sync(0xffffffffu, lim < kKeysT - 1)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e > lim) x[c][e] = 0xff800000u;
+        }
+        float mc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mc[c] = -kInf;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mc[c] = max3(mc[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+        }
+        const float mt = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * scale_log2;
+        const bool grow = mt > m + kLazy;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = !grow ? 1.f : ex2_approx(m - mt);  // 2^-inf = 0 at the first tile
+          if (grow) {
+            m = mt;
+            float a, b;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              f2_unpack(l2[i], a, b);
+              l2[i] = f2_pack(a * alpha, b * alpha);
+            }
+          }
+          if (j > 0) {  // O holds the products up to tile j - 1
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done(q), (sn - 1) & 1, abort, st, 0xD41)))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld_x32(ocol + c * 32, o);
+              tmem_ld_wait();
+              reg_fence32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_x32(ocol + c * 32, o);
+            }
+          }
+        }
+        const float mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
+        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-mz, -mz);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2), a0, a1);
+            a0 = ex2_approx(a0);
+            a1 = ex2_approx(a1);
+            l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(a0, a1));
+            pk[e >> 1] = pack_bf16x2(a0, a1);
+          }
+          tmem_st_x16(scol + c * 16, pk);  // keys 32 c .. -> packed columns 16 c ..
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(q));
+        ++sn;
       }
+      if (!ok) break;
+      // the output warps have read the item before's (m, l) once they gave O back
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_empty(q), (in & 1) ^ 1, abort, st, 0xD42)))) break;
+      ++in;
+      float a, b, c, d;
+      f2_unpack(l2[0], a, b);
+      f2_unpack(l2[1], c, d);
+      ml_s[q * 128 + row] = make_float2(m, (a + b) + (c + d));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ml_full(q));
     }
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float L = l[e];
-    L += __shfl_xor_sync(0xffffffffu, L, 1);
-    L += __shfl_xor_sync(0xffffffffu, L, 2);
-    const int h = g * gs + (warp * 16 + (lane >> 2) + 8 * e) % gs;
-    if (row_t[e] >= seq1) continue;
-    const float inv = 1.f / L;
-    uint32_t* orow = reinterpret_cast<uint32_t*>(out + (row_t[e] * H_q + h) * D);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      orow[i * 4 + (lane & 3)] = pack_bf16x2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
-    if ((lane & 3) == 0) lse[(int64_t)h * N + row_t[e]] = (m[e] + log2f(L)) * 0.69314718055994530942f;
+
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
+}
+
+template <int D, int GS>
+cudaError_t launch_t(const void* q, const void* k, const void* v, const DensePlan& p, const DensePlanScratch& w,
+                     float scale, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
+  using L = Layout<D>;
+  alignas(64) unsigned char tq[128], tk[128], tv[128];
+  const uint64_t row = (uint64_t)D * 2;
+  // q [N][H_q][d] as boxes {64 dims, gs heads, 128 / gs positions}; k, v [N][H_kv][d] as {64, 1, 128 rows}
+  if (!encode_tmap_3d(tq, q, D, (uint64_t)p.H_q, (uint64_t)p.N, row, (uint64_t)p.H_q * row, 64, GS, kRowsT / GS, 128) ||
+      !encode_tmap_3d(tk, k, D, (uint64_t)p.H_kv, (uint64_t)p.N, row, (uint64_t)p.H_kv * row, 64, 1, kKeysT, 128) ||
+      !encode_tmap_3d(tv, v, D, (uint64_t)p.H_kv, (uint64_t)p.N, row, (uint64_t)p.H_kv * row, 64, 1, kKeysT, 128))
+    return cudaErrorInvalidValue;
+  auto kern = dense_prefill_kernel<D, GS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t most = p.max_items * p.H_kv;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < num_sms() ? most : num_sms()));
+  cfg.blockDim = dim3(kThreadsA);
+  cfg.dynamicSmemBytes = L::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, *reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
+                            *reinterpret_cast<const CUtensorMap*>(tv), (const uint16_t*)v, p.N, p.H_q, p.H_kv,
+                            scale * 1.4426950408889634f, w, (uint16_t*)out, lse, st);
 }
 
 int64_t depths_of(int64_t N, int P) { return ceil_div(N, P); }
@@ -252,7 +664,7 @@ DensePlan dense_plan(int64_t N, int S, int H_q, int H_kv, int d) {
   p.H_q = H_q;
   p.H_kv = H_kv;
   p.d = d;
-  p.P = kRows / (H_q / H_kv);
+  p.P = 2 * kRowsT / (H_q / H_kv);
   // a sequence of n > 0 rows has ceil(n / P) <= n / P + 1 items
   p.max_items = N / p.P + (S < N ? S : N);
   return p;
@@ -267,13 +679,12 @@ cudaError_t launch_dense_prefill(const void* q, const void* k, const void* v, co
   dense_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, p.S, p.N, p.P, w, (int)depths_of(p.N, p.P), st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)(kRows + 2 * kKeys) * p.d * 2;
-  auto kern = p.d == 64 ? dense_prefill_kernel<64> : dense_prefill_kernel<128>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(p.max_items * p.H_kv), kThreads, smem, s>>>((const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v,
-                                                                p.N, p.H_q, p.H_kv, scale, w, (uint16_t*)out, lse);
-  return cudaGetLastError();
+  using Fn = cudaError_t (*)(const void*, const void*, const void*, const DensePlan&, const DensePlanScratch&, float,
+                             void*, float*, DeviceStatus*, cudaStream_t);
+  static const Fn table[2][4] = {{launch_t<64, 1>, launch_t<64, 2>, launch_t<64, 4>, launch_t<64, 8>},
+                                 {launch_t<128, 1>, launch_t<128, 2>, launch_t<128, 4>, launch_t<128, 8>}};
+  const int gs = p.H_q / p.H_kv;
+  return table[p.d == 128][gs == 1 ? 0 : gs == 2 ? 1 : gs == 4 ? 2 : 3](q, k, v, p, w, scale, out, lse, st, s);
 }
 
 }  // namespace msa

@@ -148,3 +148,29 @@ def test_two_calls_at_once():
         oa, ob = run(*a, 0.1, stream=s1)[1], run(*b, 0.1, stream=s2)[1]
         torch.cuda.synchronize()
         assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+@pytest.mark.parametrize("H_q,H_kv,d", [(8, 1, 128), (4, 1, 64), (2, 2, 128), (1, 1, 64)])
+@pytest.mark.parametrize("at", [0, 5, 130, 300])
+def test_values_that_are_not_finite(at, H_q, H_kv, d):
+    """A NaN or an infinity in V (and a NaN in K) reaches the rows that see it, and no row before it."""
+    lens = [310, 40]
+    q, k, v, cu = make(lens, H_q, H_kv, d)
+    want = run(q, k, v, cu, 0.1)[1].clone()
+    v[at, 0, 3] = math.nan
+    v[at, 0, 5] = math.inf
+    v[at + 4, 0, 5] = -math.inf
+    plan, out, _ = run(q, k, v, cu, 0.1)
+    assert plan.device_status() == 0
+    gs = H_q // H_kv
+    o, w = out[:, :gs], want[:, :gs]
+    clean = [c for c in range(d) if c not in (3, 5)]
+    assert torch.equal(o[:, :, clean], w[:, :, clean]) and torch.equal(out[:, gs:], want[:, gs:])
+    assert torch.equal(o[:at], w[:at]) and torch.equal(o[310:], w[310:])
+    assert bool(torch.isnan(o[at:310, :, 3]).all())
+    assert bool((o[at:at + 4, :, 5] == math.inf).all()) and bool(torch.isnan(o[at + 4:310, :, 5]).all())
+    q, k, v, cu = make(lens, H_q, H_kv, d)
+    k[at, 0, 7] = math.nan
+    _, out, lse = run(q, k, v, cu, 0.1)
+    assert torch.equal(out[:at], want[:at]) and torch.equal(out[310:], want[310:])
+    assert bool(torch.isnan(out[at:310, :gs]).all()) and bool(torch.isnan(lse[:gs, at:310]).all())
