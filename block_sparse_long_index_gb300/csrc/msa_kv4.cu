@@ -141,6 +141,11 @@ __device__ __forceinline__ int64_t units_of(int32_t len, int64_t cap) {
   return len <= 0 || (int64_t)len > cap ? 1 : ((int64_t)len + kUnit - 1) / kUnit;
 }
 
+// Units of a CTA's run: a multiple of the warps that share a head, so that none of them starts idle.
+__device__ __forceinline__ int64_t quota_of(int64_t total, int n_cta, int tw) {
+  return ((total + n_cta - 1) / n_cta + tw - 1) / tw * tw;
+}
+
 // The split of the flat unit list, worked out by every CTA from the lengths.
 struct FlatSplit {
   int64_t total;   // units over all sequences and head blocks
@@ -150,7 +155,7 @@ struct FlatSplit {
 };
 
 // Block-wide sums over the sequences; want(total, quota) names the unit to look for.
-template <typename F>
+template <int HC, typename F>
 __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, int64_t cap, int n_hb, int n_cta, F want) {
   __shared__ int64_t part[kDecWarps], found_before;
   __shared__ int found_seq;
@@ -167,7 +172,7 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) f.total += part[w];
   f.total *= n_hb;
-  f.quota = (f.total + n_cta - 1) / n_cta;
+  f.quota = quota_of(f.total, n_cta, kDecWarps / HC);
   const int64_t at = want(f.total, f.quota);
   int64_t base = 0;
   for (int s0 = 0; s0 < B; s0 += kDecThreads) {
@@ -200,8 +205,35 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
   return f;
 }
 
+// A warp's units pass through a ring of kStages in shared memory (cp.async), so that the bytes in flight do not
+// depend on registers: 2 CTAs x 8 warps x 5 units of 2176 bytes (d = 128) an SM.
+constexpr int kStages = 6;
+template <int D>
+struct Ring {
+  static constexpr int CODES = kUnit * D / 2;                 // bytes of a unit's codes of one head
+  static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + kUnit * kGroups;
+  static constexpr int STAGE = VS + kUnit * kGroups;
+  static constexpr int WARP = kStages * STAGE;
+  static constexpr int SMEM = kDecWarps * WARP;
+};
+static_assert(Ring<64>::SMEM >= kDecWarps * 8 * 64 * 4 && Ring<128>::SMEM >= kDecWarps * 8 * 128 * 4, "red_o fits over the ring");
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Where token t's V codes sit in a unit: a lane column c reads tokens 2c, 2c + 1, 2c + 8, 2c + 9, so the four
+// columns' tokens lie side by side, and (d = 128) every other pair has its 32-byte halves exchanged: 16 lanes'
+// 8-byte reads then fall in distinct banks.
+__device__ __forceinline__ int v_slot(int t) { return ((t >> 1) & 3) + 4 * (t & 1) + 8 * (t >> 3); }
+template <int D>
+__device__ __forceinline__ int v_flip(int slot) { return D == 128 ? 32 * ((slot >> 1) & 1) : 0; }
+
 template <int D, int HC>
-__global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uint16_t* __restrict__ q, Kv4Pool pool,
+__global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const uint16_t* __restrict__ q, Kv4Pool pool,
                                                                        CacheMap map, const int32_t* __restrict__ ctx_len,
                                                                        int B, int64_t cap, int gs, float scale,
                                                                        uint16_t* __restrict__ out, float* __restrict__ lse,
@@ -210,7 +242,9 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
   constexpr int TW = kDecWarps / HC;  // warps that share a head, every TW-th unit each
   constexpr int CB = D / 2;           // bytes of a head row's codes
   constexpr int CT = D / 8;           // channels of a lane's V column
-  __shared__ float red_o[TW > 1 ? kDecWarps : 1][TW > 1 ? 8 : 1][TW > 1 ? D : 1];
+  using R = Ring<D>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  float(*red_o)[8][D] = reinterpret_cast<float(*)[8][D]>(ring);  // over the ring, between segments
   __shared__ float red_m[kDecWarps][8], red_l[kDecWarps][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -218,7 +252,7 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
   const int H_kv = pool.H_kv, n_hb = H_kv / HC, H_q = H_kv * gs;
   const float kInf = __int_as_float(0x7f800000);
   const int64_t cta = blockIdx.x;
-  const FlatSplit fs = flat_split(ctx_len, B, cap, n_hb, gridDim.x, [&](int64_t, int64_t quota) { return cta * quota; });
+  const FlatSplit fs = flat_split<HC>(ctx_len, B, cap, n_hb, gridDim.x, [&](int64_t, int64_t quota) { return cta * quota; });
   int64_t f = cta * fs.quota;
   const int64_t f1 = min(fs.total, f + fs.quota);
   if (f >= f1) return;
@@ -250,11 +284,53 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
     float o[D / 16][4], m[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    if (len > 0)
-      for (int64_t u = u0 + tl; u < u1; u += TW) {
-        const int64_t tok = u * kUnit;
-        const int64_t row = map.row(seq, tok, lane == 0 ? st : nullptr);  // a page holds whole units
-        const int64_t hrow = row * H_kv + head;
+    if (len > 0) {
+      // this warp's units u0 + tl + i TW: n of them
+      const int n = u1 - u0 > tl ? (int)((u1 - u0 - tl + TW - 1) / TW) : 0;
+      const uint32_t my_ring = smem_u32(ring) + warp * R::WARP;
+      // the page of the next unit to fetch; 32 table entries at a time sit in the lanes
+      const int upp = map.page / kUnit;
+      int64_t lp = (u0 + tl) / upp, id_base = lp - 32;
+      int in_page = (int)((u0 + tl) - lp * upp), ids = 0;
+      uint32_t fetch_at = my_ring;
+      constexpr int PIECES = D / 32;  // 16-byte pieces of a head row
+      auto fetch = [&](int i) {
+        if (i < n) {
+          if (lp - id_base >= 32) {
+            id_base = lp;
+            ids = lp + lane < map.max_pages ? __ldg(map.table + (int64_t)seq * map.max_pages + lp + lane) : 0;
+          }
+          int32_t pp = __shfl_sync(0xffffffffu, ids, (int)(lp - id_base));
+          if (pp < 0 || (int64_t)pp >= map.n_pages) {
+            if (lane == 0) raise_error(st, kErrBadIndex, 3u);
+            pp = 0;
+          }
+          const int64_t hrow = ((int64_t)pp * map.page + in_page * kUnit) * H_kv + head;
+          const uint8_t* ks = pool.k_codes + hrow * CB;
+          const uint8_t* vs = pool.v_codes + hrow * CB;
+#pragma unroll
+          for (int x = 0; x < PIECES / 2; ++x) {
+            const int t = (lane + 32 * x) / PIECES, piece = lane % PIECES, slot = v_slot(t);
+            cp_async_16s(fetch_at + R::K + t * CB + piece * 16, ks + t * (H_kv * CB) + piece * 16);
+            cp_async_16s(fetch_at + R::V + slot * CB + ((piece * 16) ^ v_flip<D>(slot)), vs + t * (H_kv * CB) + piece * 16);
+          }
+          const int t = lane & 15;
+          cp_async_4(fetch_at + R::KS + lane * 4, (lane < 16 ? pool.k_scales : pool.v_scales) + (hrow + t * H_kv) * kGroups);
+          in_page += TW;
+          while (in_page >= upp) in_page -= upp, ++lp;
+        }
+        fetch_at = fetch_at + R::STAGE == my_ring + R::WARP ? my_ring : fetch_at + R::STAGE;
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) fetch(i);
+      const uint8_t* at = ring + warp * R::WARP;
+      for (int i = 0; i < n; ++i) {
+        __syncwarp();  // every lane has read the stage that is now filled again
+        fetch(i + kStages - 1);
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const int64_t tok = (u0 + tl + (int64_t)i * TW) * kUnit;
         const bool tail = tok + kUnit > len;
         // S^T = K q^T: token rows r and r + 8, the D / 4 channels (one group) 
         float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -262,11 +338,15 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
           uint32_t kw[2][D / 32], s2[2], b2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int64_t hr = hrow + (int64_t)(r + 8 * e) * H_kv;
-            const uint32_t* kp = reinterpret_cast<const uint32_t*>(pool.k_codes + hr * CB) + (D / 32) * c;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) kw[e][i] = __ldg(kp + i);
-            const uint32_t sb = scale_bf16(__ldg(pool.k_scales + hr * kGroups + c));
+            const uint8_t* kp = at + R::K + (r + 8 * e) * CB + (CB / 4) * c;
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(kp);
+              kw[e][0] = x.x, kw[e][1] = x.y, kw[e][2] = x.z, kw[e][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(kp);
+              kw[e][0] = x.x, kw[e][1] = x.y;
+            }
+            const uint32_t sb = scale_bf16(at[R::KS + (r + 8 * e) * kGroups + c]);
             s2[e] = sb | (sb << 16);
             b2[e] = scale_bias(s2[e]);
           }
@@ -317,12 +397,15 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
         uint32_t sc[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = 2 * c + (e & 1) + 8 * (e >> 1);
-          const int64_t hr = hrow + (int64_t)t * H_kv;
-          const uint32_t* vp = reinterpret_cast<const uint32_t*>(pool.v_codes + hr * CB) + (D / 64) * r;
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) vw[e][i] = __ldg(vp + i);
-          sc[e] = scale_bf16(__ldg(pool.v_scales + hr * kGroups + (r >> 1)));
+          const int t = 2 * c + (e & 1) + 8 * (e >> 1), slot = c + 4 * (e & 1) + 8 * (e >> 1);
+          const uint8_t* vp = at + R::V + slot * CB + (((CB / 8) * r) ^ v_flip<D>(c));
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vp);
+            vw[e][0] = x.x, vw[e][1] = x.y;
+          } else {
+            vw[e][0] = *reinterpret_cast<const uint32_t*>(vp);
+          }
+          sc[e] = scale_bf16(at[R::VS + t * kGroups + (r >> 1)]);
           if (tail && tok + t >= len) sc[e] = 0u;  // weight 0 times whatever lies there stays 0
         }
 #pragma unroll
@@ -348,14 +431,16 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
           mma_bf16_16816(o[4 * i + 2], a2, pb);
           mma_bf16_16816(o[4 * i + 3], a3, pb);
         }
+        at = at + R::STAGE == ring + warp * R::WARP + R::WARP ? ring + warp * R::WARP : at + R::STAGE;
       }
+      cp_async_wait<0>();
+    }
     // ---- the segment's result: l over the token rows, then over the head's TW warps
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
     if (TW > 1) {
-      __syncthreads();  // red_* of the segment before is no longer read
       if (r == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) red_m[warp][2 * c + e] = m[e], red_l[warp][2 * c + e] = l[e];
@@ -399,6 +484,7 @@ __global__ void __launch_bounds__(kDecThreads) kv4_dense_decode_kernel(const uin
           }
         }
       }
+      __syncthreads();  // the ring and red_* are free again
     }
     if (tl == 0) {
       const bool whole = u0 == 0 && u1 == T;
@@ -459,7 +545,7 @@ __global__ void __launch_bounds__(kDecThreads) kv4_combine_kernel(const int32_t*
   total = before = 0;
   for (int w = 0; w < kDecWarps; ++w) total += sums[0][w], before += sums[1][w];
   total *= n_hb;
-  const int64_t quota = (total + n_cta - 1) / n_cta;
+  const int64_t quota = quota_of(total, n_cta, kDecWarps / HC);
   const int64_t T = units_of(ctx_len[seq], cap);
   const int64_t r0 = before * n_hb + hb * T, r1 = r0 + T;
   const int c0 = (int)(r0 / quota), c1 = (int)((r1 - 1) / quota);
@@ -515,9 +601,12 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
                                   int64_t cap, int gs, float scale, void* out, float* lse, float* part_o, float2* part_ml,
                                   DeviceStatus* st, cudaStream_t s) {
   const int n_cta = decode_ctas();
-  kv4_dense_decode_kernel<D, HC><<<n_cta, kDecThreads, 0, s>>>((const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale,
-                                                               (uint16_t*)out, lse, part_o, part_ml, st);
-  cudaError_t e = cudaGetLastError();
+  auto kern = kv4_dense_decode_kernel<D, HC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<n_cta, kDecThreads, Ring<D>::SMEM, s>>>((const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale, (uint16_t*)out,
+                                                 lse, part_o, part_ml, st);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   kv4_combine_kernel<D><<<(unsigned)(B * (pool.H_kv / HC)), kDecThreads, 0, s>>>(ctx_len, B, cap, pool.H_kv, HC, gs, n_cta,
                                                                                  part_o, part_ml, (uint16_t*)out, lse);
