@@ -2,12 +2,14 @@
 #include <math.h>
 
 #include "msa_kv4.cuh"
+#include "msa_sm100.cuh"
 
 namespace msa {
 
 namespace {
 
 using namespace kv4;
+using namespace sm100;
 
 constexpr int kRowThreads = 256;
 
@@ -116,23 +118,77 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
 // ---------------------------------------------------------------- dense decode
 // One query token per sequence against its whole cache.  The caches are read
 // as one flat list of 16-token units, ordered by (sequence, head block, unit),
-// a head block being HC heads of the 8 warps' (HC = 8, 4, 2 or 1, whichever
-// divides H_kv); every CTA takes an equal run of it, whatever the lengths are.
+// a head block being HC heads (HC = 8, 4, 2 or 1, whichever divides H_kv);
+// every CTA takes an equal run of it, whatever the lengths are.  Its 8 warps
+// work on HC heads x TW = 8 / HC units at a time: a step.  Steps come by TMA
+// through a ring (K and V codes of HC heads x 16 tokens in one box each, the
+// tokens' scales as one bulk copy each); the warps take turns in looking up a
+// step's pages and issuing its copies, which leaves nearly all issue slots to
+// expanding codes and needs no registers for a warp of its own.
 // A run that covers a (sequence, head block) row whole writes its output; the
 // others leave (O, max, sum) partials, at most two a CTA, for the combine.
+//
+// Per unit and head, with mma.sync m16n8k16 (bf16, fp32 accumulation):
+//   S^T [16 tokens x 8 heads of the group] = K q^T: a lane holds one group (a
+//     quarter) of the channels of 2 tokens, so one scale each, and the query's
+//     fragments take the same channel order;
+//   O^T [d x 8 heads] += V^T P^T: a lane holds d / 8 channels of 4 tokens; the
+//     16-bit halves of two tokens' words are paired before their nibbles are
+//     expanded, which transposes V on the way; P^T comes from S^T by movmatrix.
+// S^T's row i is token perm(i) of the unit, chosen so that both the K and the V
+// reads of the swizzled tiles fall in distinct banks.
 constexpr int kUnit = 16;
-constexpr int kDecThreads = 256, kDecWarps = 8;
+constexpr int kDecWarps = 8;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kCombThreads = 256;
 constexpr float kLazy = 8.0f;  // log2 units a row maximum may grow before O is rescaled
+constexpr int kMaxStages = 8;
+constexpr int kDecSmem = 112 * 1024;  // two CTAs an SM
 
+template <int D>
+struct Tile {
+  static constexpr int CB = D / 2;           // bytes of a head row's codes, and the span of the TMA swizzle
+  static constexpr int BYTES = kUnit * CB;   // a unit's codes of one head
+  // token of row i of S^T (rows 8 .. 15: 8 more).  d = 128 (64-byte rows, 16-byte piece p at p ^ (token / 2 % 4)):
+  // even rows 0 1 4 5, odd rows 3 2 7 6; d = 64 (32-byte rows, piece p at p ^ (token / 4 % 2)): 0 1 2 3 and 6 7 4 5.
+  __device__ static __forceinline__ int perm(int i) {
+    const int c = (i >> 1) & 3;
+    const int even = D == 128 ? c + 2 * (c >> 1) : c;
+    return (i & 8) + ((i & 1) == 0 ? even : D == 128 ? (even ^ 3) : 4 + ((c + 2) & 3));
+  }
+  // where byte b of token t's codes sits in the tile
+  __device__ static __forceinline__ int at(int t, int b) {
+    return t * CB + (b ^ (16 * (D == 128 ? (t >> 1) & 3 : (t >> 2) & 1)));
+  }
+};
+
+// Bytes of a stage: K and V codes of the step's 8 (head, unit) tiles, then its TW units' scales of every head.
+__host__ __device__ constexpr int stage_bytes(int d, int tw, int H_kv) {
+  return (16 * kUnit * (d / 2) + 2 * tw * kUnit * H_kv * kGroups + 1023) / 1024 * 1024;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+__device__ __forceinline__ uint32_t hmax2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // Units of sequence s (at least one, so that an empty sequence's output is written); a length outside
@@ -151,12 +207,11 @@ struct FlatSplit {
   int64_t total;   // units over all sequences and head blocks
   int64_t quota;   // units a CTA takes
   int64_t before;  // units (times head blocks) before sequence `seq`
-  int seq;         // the sequence that holds unit `want` (B if none)
+  int seq;         // the sequence that holds this CTA's first unit (B if none)
 };
 
-// Block-wide sums over the sequences; want(total, quota) names the unit to look for.
-template <int HC, typename F>
-__device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, int64_t cap, int n_hb, int n_cta, F want) {
+template <int HC>
+__device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, int64_t cap, int n_hb) {
   __shared__ int64_t part[kDecWarps], found_before;
   __shared__ int found_seq;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -172,8 +227,8 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) f.total += part[w];
   f.total *= n_hb;
-  f.quota = quota_of(f.total, n_cta, kDecWarps / HC);
-  const int64_t at = want(f.total, f.quota);
+  f.quota = quota_of(f.total, gridDim.x, kDecWarps / HC);
+  const int64_t at = blockIdx.x * f.quota;
   int64_t base = 0;
   for (int s0 = 0; s0 < B; s0 += kDecThreads) {
     const int s = s0 + tid;
@@ -193,7 +248,7 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
       base += part[w];
     }
     const int64_t lo = (off + incl - n) * n_hb, hi = (off + incl) * n_hb;
-    if (s < B && lo <= at && at < hi) {
+    if (n > 0 && lo <= at && at < hi) {
       found_seq = s;
       found_before = lo;
     }
@@ -205,70 +260,133 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
   return f;
 }
 
-// A warp's units pass through a ring of kStages in shared memory (cp.async), so that the bytes in flight do not
-// depend on registers: 2 CTAs x 8 warps x 5 units of 2176 bytes (d = 128) an SM.
-constexpr int kStages = 6;
-template <int D>
-struct Ring {
-  static constexpr int CODES = kUnit * D / 2;                 // bytes of a unit's codes of one head
-  static constexpr int K = 0, V = CODES, KS = 2 * CODES, VS = KS + kUnit * kGroups;
-  static constexpr int STAGE = VS + kUnit * kGroups;
-  static constexpr int WARP = kStages * STAGE;
-  static constexpr int SMEM = kDecWarps * WARP;
+// A CTA's run, segment by segment: units [u0, u1) of the T units of (sequence, head block).
+struct Segments {
+  const int32_t* ctx_len;
+  int64_t cap, f, f1, before;
+  int seq, n_hb;
+  // the segment
+  int64_t len, T, u0, u1;
+  int hb;
+  bool bad;
+  __device__ __forceinline__ bool next() {
+    if (f >= f1) return false;
+    const int32_t raw = ctx_len[seq];
+    bad = raw < 0 || (int64_t)raw > cap;
+    len = bad ? 0 : raw;
+    T = units_of(raw, cap);
+    hb = (int)((f - before) / T);
+    const int64_t r0 = before + hb * T;
+    u0 = f - r0;
+    u1 = min(f1 - r0, T);
+    return true;
+  }
+  __device__ __forceinline__ void done() {
+    f += u1 - u0;
+    if (f >= before + n_hb * T) {
+      before += n_hb * T;
+      ++seq;
+    }
+  }
 };
-static_assert(Ring<64>::SMEM >= kDecWarps * 8 * 64 * 4 && Ring<128>::SMEM >= kDecWarps * 8 * 128 * 4, "red_o fits over the ring");
-
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-}
-
-// Where token t's V codes sit in a unit: a lane column c reads tokens 2c, 2c + 1, 2c + 8, 2c + 9, so the four
-// columns' tokens lie side by side, and (d = 128) every other pair has its 32-byte halves exchanged: 16 lanes'
-// 8-byte reads then fall in distinct banks.
-__device__ __forceinline__ int v_slot(int t) { return ((t >> 1) & 3) + 4 * (t & 1) + 8 * (t >> 3); }
-template <int D>
-__device__ __forceinline__ int v_flip(int slot) { return D == 128 ? 32 * ((slot >> 1) & 1) : 0; }
 
 template <int D, int HC>
-__global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const uint16_t* __restrict__ q, Kv4Pool pool,
-                                                                       CacheMap map, const int32_t* __restrict__ ctx_len,
-                                                                       int B, int64_t cap, int gs, float scale,
-                                                                       uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                                       float* __restrict__ part_o,
-                                                                       float2* __restrict__ part_ml, DeviceStatus* st) {
-  constexpr int TW = kDecWarps / HC;  // warps that share a head, every TW-th unit each
-  constexpr int CB = D / 2;           // bytes of a head row's codes
+__global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ q,
+    Kv4Pool pool, CacheMap map, const int32_t* __restrict__ ctx_len, int B, int64_t cap, int gs, float scale, int stages,
+    uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
+    DeviceStatus* st) {
+  constexpr int TW = kDecWarps / HC;  // units of a step
   constexpr int CT = D / 8;           // channels of a lane's V column
-  using R = Ring<D>;
-  extern __shared__ __align__(16) uint8_t ring[];
-  float(*red_o)[8][D] = reinterpret_cast<float(*)[8][D]>(ring);  // over the ring, between segments
+  using X = Tile<D>;
+  extern __shared__ uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
+  __shared__ int abort_flag;
   __shared__ float red_m[kDecWarps][8], red_l[kDecWarps][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H_kv = pool.H_kv, H_q = H_kv * gs;
+  const int stage = stage_bytes(D, TW, H_kv);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int i) { return bar0 + 8u * i; };                  // TMA -> consumers
+  auto empty = [&](int i) { return bar0 + 8u * (kMaxStages + i); };  // consumers (8 warps) -> TMA
+  float(*red_o)[8][D] = reinterpret_cast<float(*)[8][D]>(sm + stages * stage);  // TW > 1 alone
+  griddep_launch_dependents();  // the combine may be scheduled; it waits for this grid's end
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), kDecWarps);
+    }
+    fence_mbar_init();
+    abort_flag = 0;
+  }
+  volatile int* abort = &abort_flag;
+  Segments sg;
+  sg.ctx_len = ctx_len;
+  sg.cap = cap;
+  sg.n_hb = H_kv / HC;
+  {
+    const FlatSplit fs = flat_split<HC>(ctx_len, B, cap, sg.n_hb);
+    sg.f = blockIdx.x * fs.quota;
+    sg.f1 = min(fs.total, sg.f + fs.quota);
+    sg.before = fs.before;
+    sg.seq = fs.seq;
+  }
+  const float kInf = __int_as_float(0x7f800000);
+  constexpr int kScales = 16 * X::BYTES;  // offset of the scales in a stage
+  const int sc_unit = kUnit * H_kv * kGroups;
+
   const int r = lane >> 2, c = lane & 3;
   const int hl = warp % HC, tl = warp / HC;
-  const int H_kv = pool.H_kv, n_hb = H_kv / HC, H_q = H_kv * gs;
-  const float kInf = __int_as_float(0x7f800000);
-  const int64_t cta = blockIdx.x;
-  const FlatSplit fs = flat_split<HC>(ctx_len, B, cap, n_hb, gridDim.x, [&](int64_t, int64_t quota) { return cta * quota; });
-  int64_t f = cta * fs.quota;
-  const int64_t f1 = min(fs.total, f + fs.quota);
-  if (f >= f1) return;
-  int seq = fs.seq;
-  int64_t before = fs.before;
-  const float sl2 = scale * 1.4426950408889634f;
-  for (int part = 0; f < f1;) {
-    const int32_t len_raw = ctx_len[seq];
-    const bool bad = len_raw < 0 || (int64_t)len_raw > cap;
-    if (bad && threadIdx.x == 0) raise_error(st, kErrBadIndex, 8u);
-    const int64_t len = bad ? 0 : len_raw;
-    const int64_t T = units_of(len_raw, cap);
-    const int hb = (int)((f - before) / T);
-    const int64_t r0 = before + hb * T;
-    const int64_t u0 = f - r0, u1 = min(f1 - r0, T);  // this segment's units of the row
-    const int head = hb * HC + hl;
+  const float sl2 = scale * 1.4426950408889634f, lazy = kLazy / sl2;
+  // this lane's places in its tile: K rows perm(r) (and 8 more), V tokens perm(2c) and perm(2c + 1) (and 8 more)
+  const int tile = (tl * HC + hl) * X::BYTES;
+  const int k_at = tile + X::at(X::perm(r), (X::CB / 4) * c);
+  const int v_at0 = 8 * X::BYTES + tile + X::at(X::perm(2 * c), (X::CB / 8) * r);
+  const int v_at1 = 8 * X::BYTES + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
+  // the ring's next stage and the parity of its use
+  int slot = 0;
+  uint32_t phase = 0;
+  const int ahead = stages - 2;  // steps fetched ahead: the stage's last readers are two steps behind
+  bool ok = true;
+  uint32_t fetched = 0;  // stages that this warp has filled, and from bit 16 on the parity of the last time
+  for (int part = 0; sg.next(); sg.done()) {
+    if (sg.bad && threadIdx.x == 0) raise_error(st, kErrBadIndex, 8u);
+    const int steps = sg.len > 0 ? (int)((sg.u1 - sg.u0 + TW - 1) / TW) : 0;
+    // step i into the stage `off` past `slot`
+    auto fetch = [&](int i, int off) {
+      int fs = slot + off;
+      uint32_t fp = phase;
+      if (fs >= stages) fs -= stages, fp ^= 1u;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty(fs), fp ^ 1u, abort, st, 0xE01)))) return;
+      const int64_t u = sg.u0 + (int64_t)i * TW + lane;  // lanes 0 .. TW - 1: a unit each
+      const int n = (int)min((int64_t)TW, sg.u1 - u + lane);
+      if (lane == 0) mbar_arrive_expect_tx(full(fs), (uint32_t)(n * (2 * HC * X::BYTES + 2 * sc_unit)));
+      fetched = (fetched & ~(0x10000u << fs)) | 1u << fs | fp << (16 + fs);
+      __syncwarp();
+      if (lane < n) {
+        const uint32_t upp = (uint32_t)map.page / kUnit, lp = (uint32_t)u / upp;
+        const int in_page = (int)((uint32_t)u - lp * upp) * kUnit;
+        int32_t pp = __ldg(map.table + (int64_t)sg.seq * map.max_pages + lp);
+        if (pp < 0 || (int64_t)pp >= map.n_pages) {
+          raise_error(st, kErrBadIndex, 3u);
+          pp = 0;
+        }
+        const uint32_t at = smem_u32(sm) + fs * stage;
+        // tiles in (unit, head) order; a page holds whole units
+        tma_load_4d(at + lane * HC * X::BYTES, &tm_k, 0, in_page, sg.hb * HC, pp, full(fs));
+        tma_load_4d(at + 8 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, sg.hb * HC, pp, full(fs));
+        const int64_t row = ((int64_t)pp * map.page + in_page) * (H_kv * kGroups);
+        bulk_load(at + kScales + lane * sc_unit, pool.k_scales + row, (uint32_t)sc_unit, full(fs));
+        bulk_load(at + kScales + (TW + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
+      }
+      __syncwarp();
+    };
+    if (ok && warp < min(ahead, steps)) fetch(warp, warp);
+    const int head = sg.hb * HC + hl, seq = sg.seq;
+    const int ks_at = kScales + tl * sc_unit + (X::perm(r) * H_kv + head) * kGroups + c;
+    const int vs_at0 = kScales + (TW + tl) * sc_unit + (X::perm(2 * c) * H_kv + head) * kGroups + (r >> 1);
+    const int vs_at1 = kScales + (TW + tl) * sc_unit + (X::perm(2 * c + 1) * H_kv + head) * kGroups + (r >> 1);
     // the query as B fragments: lane (n = r, c) holds channels (D / 4) c .. of head r of the group
     uint32_t qf[D / 8];
 #pragma unroll
@@ -277,169 +395,144 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const 
       const uint4* qp = reinterpret_cast<const uint4*>(q + ((int64_t)seq * H_q + head * gs + r) * D + (D / 4) * c);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 x = qp[i];
-        qf[4 * i] = x.x, qf[4 * i + 1] = x.y, qf[4 * i + 2] = x.z, qf[4 * i + 3] = x.w;
+        const uint4 y = qp[i];
+        qf[4 * i] = y.x, qf[4 * i + 1] = y.y, qf[4 * i + 2] = y.z, qf[4 * i + 3] = y.w;
       }
     }
-    float o[D / 16][4], m[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
+    // running maximum (raw scores), what a score must exceed to move it, and the maximum in log2 units
+    float o[D / 16][4], m[2] = {-kInf, -kInf}, thr[2] = {-kInf, -kInf}, z[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    if (len > 0) {
-      // this warp's units u0 + tl + i TW: n of them
-      const int n = u1 - u0 > tl ? (int)((u1 - u0 - tl + TW - 1) / TW) : 0;
-      const uint32_t my_ring = smem_u32(ring) + warp * R::WARP;
-      // the page of the next unit to fetch; 32 table entries at a time sit in the lanes
-      const int upp = map.page / kUnit;
-      int64_t lp = (u0 + tl) / upp, id_base = lp - 32;
-      int in_page = (int)((u0 + tl) - lp * upp), ids = 0;
-      uint32_t fetch_at = my_ring;
-      constexpr int PIECES = D / 32;  // 16-byte pieces of a head row
-      auto fetch = [&](int i) {
-        if (i < n) {
-          if (lp - id_base >= 32) {
-            id_base = lp;
-            ids = lp + lane < map.max_pages ? __ldg(map.table + (int64_t)seq * map.max_pages + lp + lane) : 0;
-          }
-          int32_t pp = __shfl_sync(0xffffffffu, ids, (int)(lp - id_base));
-          if (pp < 0 || (int64_t)pp >= map.n_pages) {
-            if (lane == 0) raise_error(st, kErrBadIndex, 3u);
-            pp = 0;
-          }
-          const int64_t hrow = ((int64_t)pp * map.page + in_page * kUnit) * H_kv + head;
-          const uint8_t* ks = pool.k_codes + hrow * CB;
-          const uint8_t* vs = pool.v_codes + hrow * CB;
-#pragma unroll
-          for (int x = 0; x < PIECES / 2; ++x) {
-            const int t = (lane + 32 * x) / PIECES, piece = lane % PIECES, slot = v_slot(t);
-            cp_async_16s(fetch_at + R::K + t * CB + piece * 16, ks + t * (H_kv * CB) + piece * 16);
-            cp_async_16s(fetch_at + R::V + slot * CB + ((piece * 16) ^ v_flip<D>(slot)), vs + t * (H_kv * CB) + piece * 16);
-          }
-          const int t = lane & 15;
-          cp_async_4(fetch_at + R::KS + lane * 4, (lane < 16 ? pool.k_scales : pool.v_scales) + (hrow + t * H_kv) * kGroups);
-          in_page += TW;
-          while (in_page >= upp) in_page -= upp, ++lp;
-        }
-        fetch_at = fetch_at + R::STAGE == my_ring + R::WARP ? my_ring : fetch_at + R::STAGE;
-        cp_async_commit();
-      };
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fetch(i);
-      const uint8_t* at = ring + warp * R::WARP;
-      for (int i = 0; i < n; ++i) {
-        __syncwarp();  // every lane has read the stage that is now filled again
-        fetch(i + kStages - 1);
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        const int64_t tok = (u0 + tl + (int64_t)i * TW) * kUnit;
-        const bool tail = tok + kUnit > len;
-        // S^T = K q^T: token rows r and r + 8, the D / 4 channels (one group) 
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-          uint32_t kw[2][D / 32], s2[2], b2[2];
+    {
+      int units = (int)(sg.u1 - sg.u0) - tl;            // left for this warp's place in the steps
+      int left = (int)(sg.len - (sg.u0 + tl) * kUnit);  // tokens from this warp's unit on (lengths are int32)
+      for (int i = 0; i < steps; ++i, units -= TW, left -= TW * kUnit) {
+        if (ok && ((i + ahead) & (kDecWarps - 1)) == warp && i + ahead < steps) fetch(i + ahead, ahead);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(full(slot), phase, abort, st, 0xE10));
+        const uint8_t* at = sm + slot * stage;
+        if (ok && units > 0) {
+          uint32_t ks2[2], vs2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint8_t* kp = at + R::K + (r + 8 * e) * CB + (CB / 4) * c;
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(kp);
-              kw[e][0] = x.x, kw[e][1] = x.y, kw[e][2] = x.z, kw[e][3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(kp);
-              kw[e][0] = x.x, kw[e][1] = x.y;
+            ks2[e] = at[ks_at + e * 8 * H_kv * kGroups] * 0x00100010u + 0x35803580u;
+            vs2[e] = at[vs_at1 + e * 8 * H_kv * kGroups] * 0x00100000u +
+                     (at[vs_at0 + e * 8 * H_kv * kGroups] * 16u + 0x35803580u);
+          }
+          // a scale of 255 came out as 3840, more than any other: NaN instead
+          const uint32_t top = hmax2_bf16(hmax2_bf16(ks2[0], ks2[1]), hmax2_bf16(vs2[0], vs2[1]));
+          if (__any_sync(0xffffffffu, (top & 0xFFFFu) == 0x4570u || (top >> 16) == 0x4570u)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (ks2[e] == 0x45704570u) ks2[e] = 0x7FFF7FFFu;
+              if ((vs2[e] & 0xFFFFu) == 0x4570u) vs2[e] |= 0x7FFFu;
+              if ((vs2[e] >> 16) == 0x4570u) vs2[e] |= 0x7FFF0000u;
             }
-            const uint32_t sb = scale_bf16(at[R::KS + (r + 8 * e) * kGroups + c]);
-            s2[e] = sb | (sb << 16);
-            b2[e] = scale_bias(s2[e]);
           }
+          // S^T = K q^T
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          {
+            uint32_t kw[2][D / 32];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint4 x = expand8(kw[0][i], s2[0], b2[0]), y = expand8(kw[1][i], s2[1], b2[1]);
-            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-            const uint32_t q0[2] = {qf[4 * i], qf[4 * i + 1]}, q1[2] = {qf[4 * i + 2], qf[4 * i + 3]};
-            mma_bf16_16816(s, a0, q0);
-            mma_bf16_16816(s, a1, q1);
+            for (int e = 0; e < 2; ++e) {
+              const uint8_t* kp = at + k_at + e * 8 * X::CB;
+              if constexpr (D == 128) {
+                const uint4 y = *reinterpret_cast<const uint4*>(kp);
+                kw[e][0] = y.x, kw[e][1] = y.y, kw[e][2] = y.z, kw[e][3] = y.w;
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2*>(kp);
+                kw[e][0] = y.x, kw[e][1] = y.y;
+              }
+            }
+            const uint32_t b2[2] = {scale_bias(ks2[0]), scale_bias(ks2[1])};
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint4 a = expand8(kw[0][i], ks2[0], b2[0]), b = expand8(kw[1][i], ks2[1], b2[1]);
+              const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
+              const uint32_t q0[2] = {qf[4 * i], qf[4 * i + 1]}, q1[2] = {qf[4 * i + 2], qf[4 * i + 3]};
+              mma_bf16_16816(s, a0, q0);
+              mma_bf16_16816(s, a1, q1);
+            }
+          }
+          if (left < kUnit) {  // tokens past the length: no score, and whatever lies there stays out of V
+            if (X::perm(r) >= left) s[0] = s[1] = -kInf;
+            if (X::perm(r) + 8 >= left) s[2] = s[3] = -kInf;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (X::perm(2 * c) + 8 * e >= left) vs2[e] &= 0xFFFF0000u;
+              if (X::perm(2 * c + 1) + 8 * e >= left) vs2[e] &= 0x0000FFFFu;
+            }
+          }
+          const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+          if (__any_sync(0xffffffffu, t0 > thr[0] || t1 > thr[1])) {
+            float n[2] = {t0, t1}, a[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int y = 4; y < 32; y <<= 1) n[e] = fmaxf(n[e], __shfl_xor_sync(0xffffffffu, n[e], y));
+              n[e] = fmaxf(n[e], m[e]);
+              const float zn = n[e] == -kInf ? 0.f : n[e] * sl2;  // scores of -inf alone weigh 0
+              a[e] = m[e] == -kInf ? 1.f : ex2_approx(z[e] - zn);
+              m[e] = n[e];
+              z[e] = zn;
+              thr[e] = n[e] == -kInf ? -kInf : n[e] + lazy;
+              l[e] *= a[e];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][0] *= a[0], o[i][2] *= a[0];
+              o[i][1] *= a[1], o[i][3] *= a[1];
+            }
+          }
+          const float p0 = ex2_approx(fmaf(s[0], sl2, -z[0])), p1 = ex2_approx(fmaf(s[1], sl2, -z[1]));
+          const float p2 = ex2_approx(fmaf(s[2], sl2, -z[0])), p3 = ex2_approx(fmaf(s[3], sl2, -z[1]));
+          l[0] += p0 + p2;
+          l[1] += p1 + p3;
+          // P^T as a B operand (tokens x heads): the 8 x 8 halves transposed across the warp
+          const uint32_t pb[2] = {movmatrix_t(pack_bf16x2(p0, p1)), movmatrix_t(pack_bf16x2(p2, p3))};
+          // O^T += V^T P^T
+          uint32_t vw[4][D / 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint8_t* vp = at + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB;
+            if constexpr (D == 128) {
+              const uint2 y = *reinterpret_cast<const uint2*>(vp);
+              vw[e][0] = y.x, vw[e][1] = y.y;
+            } else {
+              vw[e][0] = *reinterpret_cast<const uint32_t*>(vp);
+            }
+          }
+          const uint32_t vb2[2] = {scale_bias(vs2[0]), scale_bias(vs2[1])};
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            // halves of the same nibbles of two tokens side by side: even channels from the low halves, odd from the high
+            uint32_t ev[2], od[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              ev[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x5410);
+              od[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x7632);
+            }
+            const uint4 e0 = expand8(ev[0], vs2[0], vb2[0]), e1 = expand8(ev[1], vs2[1], vb2[1]);
+            const uint4 d0 = expand8(od[0], vs2[0], vb2[0]), d1 = expand8(od[1], vs2[1], vb2[1]);
+            const uint32_t a0[4] = {e0.x, d0.x, e1.x, d1.x}, a1[4] = {e0.y, d0.y, e1.y, d1.y};
+            const uint32_t a2[4] = {e0.z, d0.z, e1.z, d1.z}, a3[4] = {e0.w, d0.w, e1.w, d1.w};
+            mma_bf16_16816(o[4 * i], a0, pb);
+            mma_bf16_16816(o[4 * i + 1], a1, pb);
+            mma_bf16_16816(o[4 * i + 2], a2, pb);
+            mma_bf16_16816(o[4 * i + 3], a3, pb);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] *= sl2;
-        if (tail) {
-          if (tok + r >= len) s[0] = s[1] = -kInf;
-          if (tok + r + 8 >= len) s[2] = s[3] = -kInf;
-        }
-        const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
-        if (__any_sync(0xffffffffu, t0 > m[0] + kLazy || t1 > m[1] + kLazy)) {
-          float n0 = t0, n1 = t1;
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-          }
-          n0 = fmaxf(n0, m[0]);
-          n1 = fmaxf(n1, m[1]);
-          const float a0 = m[0] == n0 ? 1.f : ex2(m[0] - n0), a1 = m[1] == n1 ? 1.f : ex2(m[1] - n1);
-          m[0] = n0;
-          m[1] = n1;
-          l[0] *= a0;
-          l[1] *= a1;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            o[i][0] *= a0, o[i][2] *= a0;
-            o[i][1] *= a1, o[i][3] *= a1;
-          }
-        }
-        const float z0 = m[0] == -kInf ? 0.f : m[0], z1 = m[1] == -kInf ? 0.f : m[1];
-        const float p0 = ex2(s[0] - z0), p1 = ex2(s[1] - z1), p2 = ex2(s[2] - z0), p3 = ex2(s[3] - z1);
-        l[0] += p0 + p2;
-        l[1] += p1 + p3;
-        // P^T as a B operand (tokens x heads): the 8 x 8 halves transposed across the warp
-        const uint32_t pb[2] = {movmatrix_t(pack_bf16x2(p0, p1)), movmatrix_t(pack_bf16x2(p2, p3))};
-        // O^T += V^T P^T: channels CT r .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9
-        uint32_t vw[4][D / 64], vs2[2], vb2[2];
-        uint32_t sc[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 2 * c + (e & 1) + 8 * (e >> 1), slot = c + 4 * (e & 1) + 8 * (e >> 1);
-          const uint8_t* vp = at + R::V + slot * CB + (((CB / 8) * r) ^ v_flip<D>(c));
-          if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vp);
-            vw[e][0] = x.x, vw[e][1] = x.y;
-          } else {
-            vw[e][0] = *reinterpret_cast<const uint32_t*>(vp);
-          }
-          sc[e] = scale_bf16(at[R::VS + t * kGroups + (r >> 1)]);
-          if (tail && tok + t >= len) sc[e] = 0u;  // weight 0 times whatever lies there stays 0
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          vs2[e] = sc[2 * e] | (sc[2 * e + 1] << 16);
-          vb2[e] = scale_bias(vs2[e]);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          // halves of the same nibbles of two tokens side by side: even channels from the low halves, odd from the high
-          uint32_t ev[2], od[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            ev[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x5410);
-            od[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x7632);
-          }
-          const uint4 e0 = expand8(ev[0], vs2[0], vb2[0]), e1 = expand8(ev[1], vs2[1], vb2[1]);
-          const uint4 d0 = expand8(od[0], vs2[0], vb2[0]), d1 = expand8(od[1], vs2[1], vb2[1]);
-          const uint32_t a0[4] = {e0.x, d0.x, e1.x, d1.x}, a1[4] = {e0.y, d0.y, e1.y, d1.y};
-          const uint32_t a2[4] = {e0.z, d0.z, e1.z, d1.z}, a3[4] = {e0.w, d0.w, e1.w, d1.w};
-          mma_bf16_16816(o[4 * i], a0, pb);
-          mma_bf16_16816(o[4 * i + 1], a1, pb);
-          mma_bf16_16816(o[4 * i + 2], a2, pb);
-          mma_bf16_16816(o[4 * i + 3], a3, pb);
-        }
-        at = at + R::STAGE == ring + warp * R::WARP + R::WARP ? ring + warp * R::WARP : at + R::STAGE;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(slot));
+        if (++slot == stages) slot = 0, phase ^= 1u;
       }
-      cp_async_wait<0>();
     }
-    // ---- the segment's result: l over the token rows, then over the head's TW warps
+    // ---- the segment's result: l over the token rows, then over the head's TW warps (z: the maximum in log2 units)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+      for (int y = 4; y < 32; y <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], y);
+      m[e] = m[e] == -kInf ? -kInf : z[e];
+    }
     if (TW > 1) {
       if (r == 0) {
 #pragma unroll
@@ -449,12 +542,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const 
       float M[2] = {-kInf, -kInf}, w[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        for (int x = 0; x < TW; ++x) M[e] = fmaxf(M[e], red_m[x * HC + hl][2 * c + e]);
-        w[e] = m[e] == M[e] ? 1.f : ex2(m[e] - M[e]);
+        for (int y = 0; y < TW; ++y) M[e] = fmaxf(M[e], red_m[y * HC + hl][2 * c + e]);
+        w[e] = m[e] == M[e] ? 1.f : ex2_approx(m[e] - M[e]);
         l[e] = 0.f;
-        for (int x = 0; x < TW; ++x) {
-          const float mx = red_m[x * HC + hl][2 * c + e];
-          l[e] += red_l[x * HC + hl][2 * c + e] * (mx == M[e] ? 1.f : ex2(mx - M[e]));
+        for (int y = 0; y < TW; ++y) {
+          const float my = red_m[y * HC + hl][2 * c + e];
+          l[e] += red_l[y * HC + hl][2 * c + e] * (my == M[e] ? 1.f : ex2_approx(my - M[e]));
         }
         m[e] = M[e];
       }
@@ -475,33 +568,33 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float x0 = 0.f, x1 = 0.f;
-            for (int x = 0; x < TW; ++x) {
-              x0 += red_o[x * HC + hl][2 * c + e][ch];
-              x1 += red_o[x * HC + hl][2 * c + e][ch + 1];
+            for (int y = 0; y < TW; ++y) {
+              x0 += red_o[y * HC + hl][2 * c + e][ch];
+              x1 += red_o[y * HC + hl][2 * c + e][ch + 1];
             }
             o[i][e] = x0;
             o[i][2 + e] = x1;
           }
         }
       }
-      __syncthreads();  // the ring and red_* are free again
+      __syncthreads();  // red_* are free again
     }
     if (tl == 0) {
-      const bool whole = u0 == 0 && u1 == T;
+      const bool whole = sg.u0 == 0 && sg.u1 == sg.T;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hh = 2 * c + e;  // head of the group
         if (hh >= gs) continue;
         if (whole) {
-          const float inv = l[e] > 0.f || l[e] != l[e] ? 1.f / l[e] : 0.f;
+          const bool any = l[e] > 0.f || l[e] != l[e];
+          const float inv = any ? 1.f / l[e] : 0.f;
           uint32_t* op = reinterpret_cast<uint32_t*>(out + ((int64_t)seq * H_q + head * gs + hh) * D + CT * r);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) op[i] = pack_bf16x2(o[i][e] * inv, o[i][2 + e] * inv);
           if (r == 0 && lse)
-            lse[(int64_t)seq * H_q + head * gs + hh] =
-                l[e] > 0.f || l[e] != l[e] ? (m[e] + log2f(l[e])) * 0.69314718055994530942f : -kInf;
+            lse[(int64_t)seq * H_q + head * gs + hh] = any ? (m[e] + log2f(l[e])) * 0.69314718055994530942f : -kInf;
         } else {
-          const int64_t slot = ((cta * 2 + part) * HC + hl) * gs + hh;
+          const int64_t slot = (((int64_t)blockIdx.x * 2 + part) * HC + hl) * gs + hh;
           float2* po = reinterpret_cast<float2*>(part_o + slot * D + CT * r);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) po[i] = make_float2(o[i][e], o[i][2 + e]);
@@ -509,28 +602,26 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(const 
         }
       }
     }
-    // ---- the next row of this CTA's run; a segment that began the CTA's run is partial 0, a later one partial 1
-    part = 1;
-    f = r0 + u1;
-    if (f >= before + n_hb * T) {
-      before += n_hb * T;
-      ++seq;
-    }
+    part = 1;  // the segment that began the CTA's run is its partial 0, a later one partial 1
   }
+  if (*abort && lane == 0)  // a wait gave up: let this warp's copies land before the CTA ends
+    for (int i = 0; i < stages; ++i)
+      if (fetched >> i & 1u) mbar_wait(full(i), fetched >> (16 + i) & 1u, nullptr, st, 0xEF1);
 }
 
 // One CTA per (sequence, head block) row: merges the partials of the CTAs that share it.
 template <int D>
-__global__ void __launch_bounds__(kDecThreads) kv4_combine_kernel(const int32_t* __restrict__ ctx_len, int B, int64_t cap,
+__global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t* __restrict__ ctx_len, int B, int64_t cap,
                                                                   int H_kv, int HC, int gs, int n_cta,
                                                                   const float* __restrict__ part_o,
                                                                   const float2* __restrict__ part_ml,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse) {
   const int n_hb = H_kv / HC, seq = blockIdx.x / n_hb, hb = blockIdx.x % n_hb;
   const int tid = threadIdx.x;
+  griddep_wait();  // the partials
   int64_t total = 0, before = 0;
   __shared__ int64_t sums[2][kDecWarps];
-  for (int s = tid; s < B; s += kDecThreads) {
+  for (int s = tid; s < B; s += kCombThreads) {
     const int64_t n = units_of(ctx_len[s], cap);
     total += n;
     if (s < seq) before += n;
@@ -554,7 +645,7 @@ __global__ void __launch_bounds__(kDecThreads) kv4_combine_kernel(const int32_t*
   auto slot_of = [&](int ct, int h) {  // a row that holds the CTA's first unit is its partial 0
     return ((int64_t)ct * 2 + (r0 <= ct * quota ? 0 : 1)) * heads + h;
   };
-  for (int e = tid; e < heads * (D / 4); e += kDecThreads) {
+  for (int e = tid; e < heads * (D / 4); e += kCombThreads) {
     const int h = e / (D / 4), ch = 4 * (e % (D / 4));
     float M = __int_as_float(0xff800000);
     for (int ct = c0; ct <= c1; ++ct) M = fmaxf(M, part_ml[slot_of(ct, h)].x);
@@ -563,7 +654,7 @@ __global__ void __launch_bounds__(kDecThreads) kv4_combine_kernel(const int32_t*
     for (int ct = c0; ct <= c1; ++ct) {
       const int64_t sl = slot_of(ct, h);
       const float2 ml = part_ml[sl];
-      const float w = ml.x == M ? 1.f : ex2(ml.x - M);
+      const float w = ml.x == M ? 1.f : ex2_approx(ml.x - M);
       const float4 x = *reinterpret_cast<const float4*>(part_o + sl * D + ch);
       L += ml.y * w;
       acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w;
@@ -600,17 +691,36 @@ template <int D, int HC>
 cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const CacheMap& map, const int32_t* ctx_len, int B,
                                   int64_t cap, int gs, float scale, void* out, float* lse, float* part_o, float2* part_ml,
                                   DeviceStatus* st, cudaStream_t s) {
+  constexpr int TW = kDecWarps / HC, CB = D / 2;
+  alignas(64) unsigned char tk[128], tv[128];
+  // codes [n_pages][page][H_kv][CB] bytes (as 16-bit words) in the order {row, token, head, page}
+  const uint64_t dims[4] = {CB / 2, (uint64_t)pool.page, (uint64_t)pool.H_kv, (uint64_t)pool.n_pages};
+  const uint64_t strides[3] = {(uint64_t)pool.H_kv * CB, CB, (uint64_t)pool.page * pool.H_kv * CB};
+  const uint32_t box[4] = {CB / 2, kUnit, HC, 1};
+  if (!encode_tmap_4d(tk, pool.k_codes, dims, strides, box, CB) || !encode_tmap_4d(tv, pool.v_codes, dims, strides, box, CB))
+    return cudaErrorInvalidValue;
+  const int stage = stage_bytes(D, TW, pool.H_kv), red = TW > 1 ? kDecWarps * 8 * D * 4 : 0;
+  const int fit = (kDecSmem - 1024 - red) / stage, stages = fit > kMaxStages ? kMaxStages : fit;
+  const int smem = 1024 + stages * stage + red;
   const int n_cta = decode_ctas();
   auto kern = kv4_dense_decode_kernel<D, HC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
   if (e != cudaSuccess) return e;
-  kern<<<n_cta, kDecThreads, Ring<D>::SMEM, s>>>((const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale, (uint16_t*)out,
-                                                 lse, part_o, part_ml, st);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  kv4_combine_kernel<D><<<(unsigned)(B * (pool.H_kv / HC)), kDecThreads, 0, s>>>(ctx_len, B, cap, pool.H_kv, HC, gs, n_cta,
-                                                                                 part_o, part_ml, (uint16_t*)out, lse);
-  return cudaGetLastError();
+  kern<<<n_cta, kDecThreads, smem, s>>>(*reinterpret_cast<const CUtensorMap*>(tk), *reinterpret_cast<const CUtensorMap*>(tv),
+                                        (const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale, stages, (uint16_t*)out,
+                                        lse, part_o, part_ml, st);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * (pool.H_kv / HC)));
+  cfg.blockDim = dim3(kCombThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D>, ctx_len, B, cap, pool.H_kv, HC, gs, n_cta, (const float*)part_o,
+                            (const float2*)part_ml, (uint16_t*)out, lse);
 }
 
 int heads_per_cta(int H_kv) { return H_kv % 8 == 0 ? 8 : H_kv % 4 == 0 ? 4 : H_kv % 2 == 0 ? 2 : 1; }
