@@ -185,6 +185,20 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// Reads of the ring by shared-memory address (a generic pointer would cost 64-bit arithmetic for each).
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(x) : "r"(a));
+  return x;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "a load's width");
+  if constexpr (N == 1) asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[0]) : "r"(a));
+  if constexpr (N == 2) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+}
 __device__ __forceinline__ uint32_t hmax2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
   }
   const float kInf = __int_as_float(0x7f800000);
   constexpr int kScales = 16 * X::BYTES;  // offset of the scales in a stage
-  const int sc_unit = kUnit * H_kv * kGroups;
+  const int sc_unit = kUnit * H_kv * kGroups, sc_half = sc_unit / 2;
 
   const int r = lane >> 2, c = lane & 3;
   const int hl = warp % HC, tl = warp / HC;
@@ -346,7 +360,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
   const int v_at1 = 8 * X::BYTES + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
   // the ring's next stage and the parity of its use
   int slot = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, at = smem_u32(sm);
   const int ahead = stages - 2;  // steps fetched ahead: the stage's last readers are two steps behind
   bool ok = true;
   uint32_t fetched = 0;  // stages that this warp has filled, and from bit 16 on the parity of the last time
@@ -372,13 +386,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
           raise_error(st, kErrBadIndex, 3u);
           pp = 0;
         }
-        const uint32_t at = smem_u32(sm) + fs * stage;
+        const uint32_t to = smem_u32(sm) + fs * stage;
         // tiles in (unit, head) order; a page holds whole units
-        tma_load_4d(at + lane * HC * X::BYTES, &tm_k, 0, in_page, sg.hb * HC, pp, full(fs));
-        tma_load_4d(at + 8 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, sg.hb * HC, pp, full(fs));
+        tma_load_4d(to + lane * HC * X::BYTES, &tm_k, 0, in_page, sg.hb * HC, pp, full(fs));
+        tma_load_4d(to + 8 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, sg.hb * HC, pp, full(fs));
         const int64_t row = ((int64_t)pp * map.page + in_page) * (H_kv * kGroups);
-        bulk_load(at + kScales + lane * sc_unit, pool.k_scales + row, (uint32_t)sc_unit, full(fs));
-        bulk_load(at + kScales + (TW + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
+        bulk_load(to + kScales + lane * sc_unit, pool.k_scales + row, (uint32_t)sc_unit, full(fs));
+        bulk_load(to + kScales + (TW + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
       }
       __syncwarp();
     };
@@ -409,14 +423,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
       for (int i = 0; i < steps; ++i, units -= TW, left -= TW * kUnit) {
         if (ok && ((i + ahead) & (kDecWarps - 1)) == warp && i + ahead < steps) fetch(i + ahead, ahead);
         ok = ok && __all_sync(0xffffffffu, mbar_wait(full(slot), phase, abort, st, 0xE10));
-        const uint8_t* at = sm + slot * stage;
         if (ok && units > 0) {
           uint32_t ks2[2], vs2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            ks2[e] = at[ks_at + e * 8 * H_kv * kGroups] * 0x00100010u + 0x35803580u;
-            vs2[e] = at[vs_at1 + e * 8 * H_kv * kGroups] * 0x00100000u +
-                     (at[vs_at0 + e * 8 * H_kv * kGroups] * 16u + 0x35803580u);
+            ks2[e] = lds_u8(at + ks_at + e * sc_half) * 0x00100010u + 0x35803580u;
+            vs2[e] = lds_u8(at + vs_at1 + e * sc_half) * 0x00100000u + (lds_u8(at + vs_at0 + e * sc_half) * 16u + 0x35803580u);
           }
           // a scale of 255 came out as 3840, more than any other: NaN instead
           const uint32_t top = hmax2_bf16(hmax2_bf16(ks2[0], ks2[1]), hmax2_bf16(vs2[0], vs2[1]));
@@ -433,16 +445,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
           {
             uint32_t kw[2][D / 32];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint8_t* kp = at + k_at + e * 8 * X::CB;
-              if constexpr (D == 128) {
-                const uint4 y = *reinterpret_cast<const uint4*>(kp);
-                kw[e][0] = y.x, kw[e][1] = y.y, kw[e][2] = y.z, kw[e][3] = y.w;
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(kp);
-                kw[e][0] = y.x, kw[e][1] = y.y;
-              }
-            }
+            for (int e = 0; e < 2; ++e) lds_words(at + k_at + e * 8 * X::CB, kw[e]);
             const uint32_t b2[2] = {scale_bias(ks2[0]), scale_bias(ks2[1])};
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -492,15 +495,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
           // O^T += V^T P^T
           uint32_t vw[4][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint8_t* vp = at + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB;
-            if constexpr (D == 128) {
-              const uint2 y = *reinterpret_cast<const uint2*>(vp);
-              vw[e][0] = y.x, vw[e][1] = y.y;
-            } else {
-              vw[e][0] = *reinterpret_cast<const uint32_t*>(vp);
-            }
-          }
+          for (int e = 0; e < 4; ++e) lds_words(at + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
           const uint32_t vb2[2] = {scale_bias(vs2[0]), scale_bias(vs2[1])};
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
@@ -523,7 +518,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(slot));
-        if (++slot == stages) slot = 0, phase ^= 1u;
+        at += stage;
+        if (++slot == stages) slot = 0, phase ^= 1u, at = smem_u32(sm);
       }
     }
     // ---- the segment's result: l over the token rows, then over the head's TW warps (z: the maximum in log2 units)

@@ -37,9 +37,14 @@ __device__ __forceinline__ uint32_t scale_bias(uint32_t s2) { return hmul2_bf16(
 
 // Nibble n (0..3) of both 16-bit halves of w as two bf16 values: 0x4300 | code is the bf16 128 + code, and
 // (128 + code) s - 136 s is exact under one rounding because the result is.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {  // (a & b) | c in one instruction
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t b2) {
-  return hfma2_bf16(((w >> (4 * N)) & 0x000F000Fu) | 0x43004300u, s2, b2);
+  return hfma2_bf16(and_or(w >> (4 * N), 0x000F000Fu, 0x43004300u), s2, b2);
 }
 
 // A word's 8 channels in order, as 4 bf16 pairs: nibble n of the low half is channel 2n, of the high half 2n + 1.
