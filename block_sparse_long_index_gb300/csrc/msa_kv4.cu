@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
 // ---------------------------------------------------------------- dense decode
 // One query token per sequence against its whole cache.  The caches are read
 // as one flat list of 16-token units, ordered by (sequence, head block, unit),
-// a head block being HC heads (HC = 8, 4, 2 or 1, whichever divides H_kv);
-// every CTA takes an equal run of it, whatever the lengths are.  Its 8 warps
-// work on HC heads x TW = 8 / HC units at a time: a step.  Steps come by TMA
+// a head block being HC heads (8, or the power of two that holds H_kv; heads
+// past H_kv leave their warps idle); every CTA takes an equal run of it,
+// whatever the lengths are.  Its 8 warps work on HC heads x TW = 8 / HC pairs of
+// units at a time: a step.  Steps come by TMA
 // through a ring (K and V codes of HC heads x 16 tokens in one box each, the
 // tokens' scales as one bulk copy each); the warps take turns in looking up a
 // step's pages and issuing its copies, which leaves nearly all issue slots to
@@ -162,9 +163,9 @@ struct Tile {
   }
 };
 
-// Bytes of a stage: K and V codes of the step's 8 (head, unit) tiles, then its TW units' scales of every head.
+// Bytes of a stage: K and V codes of the step's 16 (unit, head) tiles, then its 2 TW units' scales of every head.
 __host__ __device__ constexpr int stage_bytes(int d, int tw, int H_kv) {
-  return (16 * kUnit * (d / 2) + 2 * tw * kUnit * H_kv * kGroups + 1023) / 1024 * 1024;
+  return (32 * kUnit * (d / 2) + 4 * tw * kUnit * H_kv * kGroups + 1023) / 1024 * 1024;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
@@ -211,9 +212,9 @@ __device__ __forceinline__ int64_t units_of(int32_t len, int64_t cap) {
   return len <= 0 || (int64_t)len > cap ? 1 : ((int64_t)len + kUnit - 1) / kUnit;
 }
 
-// Units of a CTA's run: a multiple of the warps that share a head, so that none of them starts idle.
-__device__ __forceinline__ int64_t quota_of(int64_t total, int n_cta, int tw) {
-  return ((total + n_cta - 1) / n_cta + tw - 1) / tw * tw;
+// Units of a CTA's run: a multiple of a step's, so that none of its warps starts idle.
+__device__ __forceinline__ int64_t quota_of(int64_t total, int n_cta, int step) {
+  return ((total + n_cta - 1) / n_cta + step - 1) / step * step;
 }
 
 // The split of the flat unit list, worked out by every CTA from the lengths.
@@ -241,7 +242,7 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) f.total += part[w];
   f.total *= n_hb;
-  f.quota = quota_of(f.total, gridDim.x, kDecWarps / HC);
+  f.quota = quota_of(f.total, gridDim.x, 2 * kDecWarps / HC);
   const int64_t at = blockIdx.x * f.quota;
   int64_t base = 0;
   for (int s0 = 0; s0 < B; s0 += kDecThreads) {
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     Kv4Pool pool, CacheMap map, const int32_t* __restrict__ ctx_len, int B, int64_t cap, int gs, float scale, int stages,
     uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
     DeviceStatus* st) {
-  constexpr int TW = kDecWarps / HC;  // units of a step
+  constexpr int TW = kDecWarps / HC, SU = 2 * TW;  // warps that share a head, units of a step
   constexpr int CT = D / 8;           // channels of a lane's V column
   using X = Tile<D>;
   extern __shared__ uint8_t smraw[];
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
   Segments sg;
   sg.ctx_len = ctx_len;
   sg.cap = cap;
-  sg.n_hb = H_kv / HC;
+  sg.n_hb = (H_kv + HC - 1) / HC;
   {
     const FlatSplit fs = flat_split<HC>(ctx_len, B, cap, sg.n_hb);
     sg.f = blockIdx.x * fs.quota;
@@ -347,34 +348,34 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     sg.seq = fs.seq;
   }
   const float kInf = __int_as_float(0x7f800000);
-  constexpr int kScales = 16 * X::BYTES;  // offset of the scales in a stage
+  constexpr int kScales = 32 * X::BYTES;  // offset of the scales in a stage
   const int sc_unit = kUnit * H_kv * kGroups, sc_half = sc_unit / 2;
 
   const int r = lane >> 2, c = lane & 3;
   const int hl = warp % HC, tl = warp / HC;
   const float sl2 = scale * 1.4426950408889634f, lazy = kLazy / sl2;
   // this lane's places in its tile: K rows perm(r) (and 8 more), V tokens perm(2c) and perm(2c + 1) (and 8 more)
-  const int tile = (tl * HC + hl) * X::BYTES;
+  const int tile = (2 * tl * HC + hl) * X::BYTES;  // of the warp's first unit; the second one's is HC tiles on
   const int k_at = tile + X::at(X::perm(r), (X::CB / 4) * c);
-  const int v_at0 = 8 * X::BYTES + tile + X::at(X::perm(2 * c), (X::CB / 8) * r);
-  const int v_at1 = 8 * X::BYTES + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
+  const int v_at0 = 16 * X::BYTES + tile + X::at(X::perm(2 * c), (X::CB / 8) * r);
+  const int v_at1 = 16 * X::BYTES + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
   // the ring's next stage and the parity of its use
   int slot = 0;
   uint32_t phase = 0, at = smem_u32(sm);
-  const int ahead = stages - 2;  // steps fetched ahead: the stage's last readers are two steps behind
+  const int ahead = stages - 1;  // steps fetched ahead
   bool ok = true;
   uint32_t fetched = 0;  // stages that this warp has filled, and from bit 16 on the parity of the last time
   for (int part = 0; sg.next(); sg.done()) {
     if (sg.bad && threadIdx.x == 0) raise_error(st, kErrBadIndex, 8u);
-    const int steps = sg.len > 0 ? (int)((sg.u1 - sg.u0 + TW - 1) / TW) : 0;
+    const int steps = sg.len > 0 ? (int)((sg.u1 - sg.u0 + SU - 1) / SU) : 0;
     // step i into the stage `off` past `slot`
     auto fetch = [&](int i, int off) {
       int fs = slot + off;
       uint32_t fp = phase;
       if (fs >= stages) fs -= stages, fp ^= 1u;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty(fs), fp ^ 1u, abort, st, 0xE01)))) return;
-      const int64_t u = sg.u0 + (int64_t)i * TW + lane;  // lanes 0 .. TW - 1: a unit each
-      const int n = (int)min((int64_t)TW, sg.u1 - u + lane);
+      const int64_t u = sg.u0 + (int64_t)i * SU + lane;  // lanes 0 .. SU - 1: a unit each
+      const int n = (int)min((int64_t)SU, sg.u1 - u + lane);
       if (lane == 0) mbar_arrive_expect_tx(full(fs), (uint32_t)(n * (2 * HC * X::BYTES + 2 * sc_unit)));
       fetched = (fetched & ~(0x10000u << fs)) | 1u << fs | fp << (16 + fs);
       __syncwarp();
@@ -389,23 +390,24 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
         const uint32_t to = smem_u32(sm) + fs * stage;
         // tiles in (unit, head) order; a page holds whole units
         tma_load_4d(to + lane * HC * X::BYTES, &tm_k, 0, in_page, sg.hb * HC, pp, full(fs));
-        tma_load_4d(to + 8 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, sg.hb * HC, pp, full(fs));
+        tma_load_4d(to + 16 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, sg.hb * HC, pp, full(fs));
         const int64_t row = ((int64_t)pp * map.page + in_page) * (H_kv * kGroups);
         bulk_load(to + kScales + lane * sc_unit, pool.k_scales + row, (uint32_t)sc_unit, full(fs));
-        bulk_load(to + kScales + (TW + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
+        bulk_load(to + kScales + (SU + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
       }
       __syncwarp();
     };
     if (ok && warp < min(ahead, steps)) fetch(warp, warp);
     const int head = sg.hb * HC + hl, seq = sg.seq;
-    const int ks_at = kScales + tl * sc_unit + (X::perm(r) * H_kv + head) * kGroups + c;
-    const int vs_at0 = kScales + (TW + tl) * sc_unit + (X::perm(2 * c) * H_kv + head) * kGroups + (r >> 1);
-    const int vs_at1 = kScales + (TW + tl) * sc_unit + (X::perm(2 * c + 1) * H_kv + head) * kGroups + (r >> 1);
+    const int ks_at = kScales + 2 * tl * sc_unit + (X::perm(r) * H_kv + head) * kGroups + c;
+    const int vs_at0 = kScales + (SU + 2 * tl) * sc_unit + (X::perm(2 * c) * H_kv + head) * kGroups + (r >> 1);
+    const int vs_at1 = kScales + (SU + 2 * tl) * sc_unit + (X::perm(2 * c + 1) * H_kv + head) * kGroups + (r >> 1);
     // the query as B fragments: lane (n = r, c) holds channels (D / 4) c .. of head r of the group
     uint32_t qf[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) qf[i] = 0u;
-    if (r < gs) {
+    const bool on = head < H_kv;
+    if (on && r < gs) {
       const uint4* qp = reinterpret_cast<const uint4*>(q + ((int64_t)seq * H_q + head * gs + r) * D + (D / 4) * c);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -417,110 +419,131 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     float o[D / 16][4], m[2] = {-kInf, -kInf}, thr[2] = {-kInf, -kInf}, z[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    {
-      int units = (int)(sg.u1 - sg.u0) - tl;            // left for this warp's place in the steps
-      int left = (int)(sg.len - (sg.u0 + tl) * kUnit);  // tokens from this warp's unit on (lengths are int32)
-      for (int i = 0; i < steps; ++i, units -= TW, left -= TW * kUnit) {
-        if (ok && ((i + ahead) & (kDecWarps - 1)) == warp && i + ahead < steps) fetch(i + ahead, ahead);
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(full(slot), phase, abort, st, 0xE10));
-        if (ok && units > 0) {
-          uint32_t ks2[2], vs2[2];
+    int units = (int)(sg.u1 - sg.u0) - 2 * tl;            // left from this warp's place in the step on
+    int left = (int)(sg.len - (sg.u0 + 2 * tl) * kUnit);  // tokens likewise (lengths are int32)
+    for (int i = 0; i < steps; ++i, units -= SU, left -= SU * kUnit) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(full(slot), phase, abort, st, 0xE10));
+      if (ok && on && units > 0) {
+        // A second unit past the run's end holds whatever lay in the stage: its tokens count as past the length.
+        const int seen = units > 1 ? left : min(left, kUnit);
+        uint32_t ks2[2][2], vs2[2][2], top = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            ks2[e] = lds_u8(at + ks_at + e * sc_half) * 0x00100010u + 0x35803580u;
-            vs2[e] = lds_u8(at + vs_at1 + e * sc_half) * 0x00100000u + (lds_u8(at + vs_at0 + e * sc_half) * 16u + 0x35803580u);
+            const uint32_t a = at + h * sc_unit + e * sc_half;
+            ks2[h][e] = lds_u8(a + ks_at) * 0x00100010u + 0x35803580u;
+            vs2[h][e] = lds_u8(a + vs_at1) * 0x00100000u + (lds_u8(a + vs_at0) * 16u + 0x35803580u);
+            top = hmax2_bf16(top, hmax2_bf16(ks2[h][e], vs2[h][e]));
           }
-          // a scale of 255 came out as 3840, more than any other: NaN instead
-          const uint32_t top = hmax2_bf16(hmax2_bf16(ks2[0], ks2[1]), hmax2_bf16(vs2[0], vs2[1]));
-          if (__any_sync(0xffffffffu, (top & 0xFFFFu) == 0x4570u || (top >> 16) == 0x4570u)) {
+        // a scale of 255 came out as 3840, more than any other: NaN instead
+        if (__any_sync(0xffffffffu, (top & 0xFFFFu) == 0x4570u || (top >> 16) == 0x4570u)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (ks2[e] == 0x45704570u) ks2[e] = 0x7FFF7FFFu;
-              if ((vs2[e] & 0xFFFFu) == 0x4570u) vs2[e] |= 0x7FFFu;
-              if ((vs2[e] >> 16) == 0x4570u) vs2[e] |= 0x7FFF0000u;
+              if (ks2[h][e] == 0x45704570u) ks2[h][e] = 0x7FFF7FFFu;
+              if ((vs2[h][e] & 0xFFFFu) == 0x4570u) vs2[h][e] |= 0x7FFFu;
+              if ((vs2[h][e] >> 16) == 0x4570u) vs2[h][e] |= 0x7FFF0000u;
             }
-          }
-          // S^T = K q^T
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-          {
-            uint32_t kw[2][D / 32];
+        }
+        // S^T = K q^T
+        float s[2][4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) lds_words(at + k_at + e * 8 * X::CB, kw[e]);
-            const uint32_t b2[2] = {scale_bias(ks2[0]), scale_bias(ks2[1])};
+        for (int h = 0; h < 2; ++h) {
+          s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+          uint32_t kw[2][D / 32];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              const uint4 a = expand8(kw[0][i], ks2[0], b2[0]), b = expand8(kw[1][i], ks2[1], b2[1]);
-              const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
-              const uint32_t q0[2] = {qf[4 * i], qf[4 * i + 1]}, q1[2] = {qf[4 * i + 2], qf[4 * i + 3]};
-              mma_bf16_16816(s, a0, q0);
-              mma_bf16_16816(s, a1, q1);
-            }
+          for (int e = 0; e < 2; ++e) lds_words(at + k_at + h * HC * X::BYTES + e * 8 * X::CB, kw[e]);
+          const uint32_t b2[2] = {scale_bias(ks2[h][0]), scale_bias(ks2[h][1])};
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            const uint4 a = expand8(kw[0][w], ks2[h][0], b2[0]), b = expand8(kw[1][w], ks2[h][1], b2[1]);
+            const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
+            const uint32_t q0[2] = {qf[4 * w], qf[4 * w + 1]}, q1[2] = {qf[4 * w + 2], qf[4 * w + 3]};
+            mma_bf16_16816(s[h], a0, q0);
+            mma_bf16_16816(s[h], a1, q1);
           }
-          if (left < kUnit) {  // tokens past the length: no score, and whatever lies there stays out of V
-            if (X::perm(r) >= left) s[0] = s[1] = -kInf;
-            if (X::perm(r) + 8 >= left) s[2] = s[3] = -kInf;
+        }
+        if (seen < 2 * kUnit) {  // tokens past the length: no score, and whatever lies there stays out of V
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (X::perm(r) + 16 * h >= seen) s[h][0] = s[h][1] = -kInf;
+            if (X::perm(r) + 16 * h + 8 >= seen) s[h][2] = s[h][3] = -kInf;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (X::perm(2 * c) + 8 * e >= left) vs2[e] &= 0xFFFF0000u;
-              if (X::perm(2 * c + 1) + 8 * e >= left) vs2[e] &= 0x0000FFFFu;
+              if (X::perm(2 * c) + 16 * h + 8 * e >= seen) vs2[h][e] &= 0xFFFF0000u;
+              if (X::perm(2 * c + 1) + 16 * h + 8 * e >= seen) vs2[h][e] &= 0x0000FFFFu;
             }
           }
-          const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
-          if (__any_sync(0xffffffffu, t0 > thr[0] || t1 > thr[1])) {
-            float n[2] = {t0, t1}, a[2];
+        }
+        const float t0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+        const float t1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+        if (__any_sync(0xffffffffu, t0 > thr[0] || t1 > thr[1])) {
+          float n[2] = {t0, t1}, a[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < 2; ++e) {
 #pragma unroll
-              for (int y = 4; y < 32; y <<= 1) n[e] = fmaxf(n[e], __shfl_xor_sync(0xffffffffu, n[e], y));
-              n[e] = fmaxf(n[e], m[e]);
-              const float zn = n[e] == -kInf ? 0.f : n[e] * sl2;  // scores of -inf alone weigh 0
-              a[e] = m[e] == -kInf ? 1.f : ex2_approx(z[e] - zn);
-              m[e] = n[e];
-              z[e] = zn;
-              thr[e] = n[e] == -kInf ? -kInf : n[e] + lazy;
-              l[e] *= a[e];
-            }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[i][0] *= a[0], o[i][2] *= a[0];
-              o[i][1] *= a[1], o[i][3] *= a[1];
-            }
+            for (int y = 4; y < 32; y <<= 1) n[e] = fmaxf(n[e], __shfl_xor_sync(0xffffffffu, n[e], y));
+            n[e] = fmaxf(n[e], m[e]);
+            const float zn = n[e] == -kInf ? 0.f : n[e] * sl2;  // scores of -inf alone weigh 0
+            a[e] = m[e] == -kInf ? 1.f : ex2_approx(z[e] - zn);
+            m[e] = n[e];
+            z[e] = zn;
+            thr[e] = n[e] == -kInf ? -kInf : n[e] + lazy;
+            l[e] *= a[e];
           }
-          const float p0 = ex2_approx(fmaf(s[0], sl2, -z[0])), p1 = ex2_approx(fmaf(s[1], sl2, -z[1]));
-          const float p2 = ex2_approx(fmaf(s[2], sl2, -z[0])), p3 = ex2_approx(fmaf(s[3], sl2, -z[1]));
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            o[x][0] *= a[0], o[x][2] *= a[0];
+            o[x][1] *= a[1], o[x][3] *= a[1];
+          }
+        }
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = ex2_approx(fmaf(s[h][0], sl2, -z[0])), p1 = ex2_approx(fmaf(s[h][1], sl2, -z[1]));
+          const float p2 = ex2_approx(fmaf(s[h][2], sl2, -z[0])), p3 = ex2_approx(fmaf(s[h][3], sl2, -z[1]));
           l[0] += p0 + p2;
           l[1] += p1 + p3;
           // P^T as a B operand (tokens x heads): the 8 x 8 halves transposed across the warp
-          const uint32_t pb[2] = {movmatrix_t(pack_bf16x2(p0, p1)), movmatrix_t(pack_bf16x2(p2, p3))};
-          // O^T += V^T P^T
+          pb[h][0] = movmatrix_t(pack_bf16x2(p0, p1));
+          pb[h][1] = movmatrix_t(pack_bf16x2(p2, p3));
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t vw[4][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) lds_words(at + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
-          const uint32_t vb2[2] = {scale_bias(vs2[0]), scale_bias(vs2[1])};
+          for (int e = 0; e < 4; ++e)
+            lds_words(at + h * HC * X::BYTES + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
+          const uint32_t vb2[2] = {scale_bias(vs2[h][0]), scale_bias(vs2[h][1])};
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
+          for (int w = 0; w < D / 64; ++w) {
             // halves of the same nibbles of two tokens side by side: even channels from the low halves, odd from the high
             uint32_t ev[2], od[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              ev[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x5410);
-              od[e] = __byte_perm(vw[2 * e][i], vw[2 * e + 1][i], 0x7632);
+              ev[e] = __byte_perm(vw[2 * e][w], vw[2 * e + 1][w], 0x5410);
+              od[e] = __byte_perm(vw[2 * e][w], vw[2 * e + 1][w], 0x7632);
             }
-            const uint4 e0 = expand8(ev[0], vs2[0], vb2[0]), e1 = expand8(ev[1], vs2[1], vb2[1]);
-            const uint4 d0 = expand8(od[0], vs2[0], vb2[0]), d1 = expand8(od[1], vs2[1], vb2[1]);
+            const uint4 e0 = expand8(ev[0], vs2[h][0], vb2[0]), e1 = expand8(ev[1], vs2[h][1], vb2[1]);
+            const uint4 d0 = expand8(od[0], vs2[h][0], vb2[0]), d1 = expand8(od[1], vs2[h][1], vb2[1]);
             const uint32_t a0[4] = {e0.x, d0.x, e1.x, d1.x}, a1[4] = {e0.y, d0.y, e1.y, d1.y};
             const uint32_t a2[4] = {e0.z, d0.z, e1.z, d1.z}, a3[4] = {e0.w, d0.w, e1.w, d1.w};
-            mma_bf16_16816(o[4 * i], a0, pb);
-            mma_bf16_16816(o[4 * i + 1], a1, pb);
-            mma_bf16_16816(o[4 * i + 2], a2, pb);
-            mma_bf16_16816(o[4 * i + 3], a3, pb);
+            mma_bf16_16816(o[4 * w], a0, pb[h]);
+            mma_bf16_16816(o[4 * w + 1], a1, pb[h]);
+            mma_bf16_16816(o[4 * w + 2], a2, pb[h]);
+            mma_bf16_16816(o[4 * w + 3], a3, pb[h]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(slot));
-        at += stage;
-        if (++slot == stages) slot = 0, phase ^= 1u, at = smem_u32(sm);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
+      // the warps' turns: the stage before this one, once every warp is done with it, takes the step `ahead` on
+      if (ok && ((i + ahead) & (kDecWarps - 1)) == warp && i + ahead < steps) fetch(i + ahead, ahead);
+      at += stage;
+      if (++slot == stages) slot = 0, phase ^= 1u, at = smem_u32(sm);
     }
     // ---- the segment's result: l over the token rows, then over the head's TW warps (z: the maximum in log2 units)
 #pragma unroll
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
       }
       __syncthreads();  // red_* are free again
     }
-    if (tl == 0) {
+    if (tl == 0 && on) {
       const bool whole = sg.u0 == 0 && sg.u1 == sg.T;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -612,7 +635,7 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t
                                                                   const float* __restrict__ part_o,
                                                                   const float2* __restrict__ part_ml,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse) {
-  const int n_hb = H_kv / HC, seq = blockIdx.x / n_hb, hb = blockIdx.x % n_hb;
+  const int n_hb = (H_kv + HC - 1) / HC, seq = blockIdx.x / n_hb, hb = blockIdx.x % n_hb;
   const int tid = threadIdx.x;
   griddep_wait();  // the partials
   int64_t total = 0, before = 0;
@@ -632,7 +655,7 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t
   total = before = 0;
   for (int w = 0; w < kDecWarps; ++w) total += sums[0][w], before += sums[1][w];
   total *= n_hb;
-  const int64_t quota = quota_of(total, n_cta, kDecWarps / HC);
+  const int64_t quota = quota_of(total, n_cta, 2 * kDecWarps / HC);
   const int64_t T = units_of(ctx_len[seq], cap);
   const int64_t r0 = before * n_hb + hb * T, r1 = r0 + T;
   const int c0 = (int)(r0 / quota), c1 = (int)((r1 - 1) / quota);
@@ -641,7 +664,8 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t
   auto slot_of = [&](int ct, int h) {  // a row that holds the CTA's first unit is its partial 0
     return ((int64_t)ct * 2 + (r0 <= ct * quota ? 0 : 1)) * heads + h;
   };
-  for (int e = tid; e < heads * (D / 4); e += kCombThreads) {
+  const int mine = min(heads, (H_kv - hb * HC) * gs);  // the last block may be short of heads
+  for (int e = tid; e < mine * (D / 4); e += kCombThreads) {
     const int h = e / (D / 4), ch = 4 * (e % (D / 4));
     float M = __int_as_float(0xff800000);
     for (int ct = c0; ct <= c1; ++ct) M = fmaxf(M, part_ml[slot_of(ct, h)].x);
@@ -707,7 +731,7 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
                                         lse, part_o, part_ml, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(B * (pool.H_kv / HC)));
+  cfg.gridDim = dim3((unsigned)(B * ((pool.H_kv + HC - 1) / HC)));
   cfg.blockDim = dim3(kCombThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -719,7 +743,7 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
                             (const float2*)part_ml, (uint16_t*)out, lse);
 }
 
-int heads_per_cta(int H_kv) { return H_kv % 8 == 0 ? 8 : H_kv % 4 == 0 ? 4 : H_kv % 2 == 0 ? 2 : 1; }
+int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
 
 }  // namespace
 
