@@ -144,6 +144,7 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kCombThreads = 256;
 constexpr float kLazy = 8.0f;  // log2 units a row maximum may grow before O is rescaled
 constexpr int kMaxStages = 8;
+constexpr uint32_t kNaNRaw = (kScaleNaN << 4) + kSubScaleBias;  // M of the NaN scale before it is made NaN
 constexpr int kDecSmem = 112 * 1024;  // two CTAs an SM
 
 template <int D>
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
 
   const int r = lane >> 2, c = lane & 3;
   const int hl = warp % HC, tl = warp / HC;
-  const float sl2 = scale * 1.4426950408889634f, lazy = kLazy / sl2;
+  const float sl2 = scale * (1.4426950408889634f * kSubUnscale), lazy = kLazy / sl2;  // of scores as they come out
   // this lane's places in its tile: K rows perm(r) (and 8 more), V tokens perm(2c) and perm(2c + 1) (and 8 more)
   const int tile = (2 * tl * HC + hl) * X::BYTES;  // of the warp's first unit; the second one's is HC tiles on
   const int k_at = tile + X::at(X::perm(r), (X::CB / 4) * c);
@@ -432,19 +433,19 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t a = at + h * sc_unit + e * sc_half;
-            ks2[h][e] = lds_u8(a + ks_at) * 0x00100010u + 0x35803580u;
-            vs2[h][e] = lds_u8(a + vs_at1) * 0x00100000u + (lds_u8(a + vs_at0) * 16u + 0x35803580u);
+            ks2[h][e] = lds_u8(a + ks_at) * 0x00100010u + kSubScaleBias * 0x00010001u;
+            vs2[h][e] = lds_u8(a + vs_at1) * 0x00100000u + (lds_u8(a + vs_at0) * 16u + kSubScaleBias * 0x00010001u);
             top = hmax2_bf16(top, hmax2_bf16(ks2[h][e], vs2[h][e]));
           }
-        // a scale of 255 came out as 3840, more than any other: NaN instead
-        if (__any_sync(0xffffffffu, (top & 0xFFFFu) == 0x4570u || (top >> 16) == 0x4570u)) {
+        // a scale of 255 came out as a number, larger than any other: NaN instead
+        if (__any_sync(0xffffffffu, (top & 0xFFFFu) == kNaNRaw || (top >> 16) == kNaNRaw)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (ks2[h][e] == 0x45704570u) ks2[h][e] = 0x7FFF7FFFu;
-              if ((vs2[h][e] & 0xFFFFu) == 0x4570u) vs2[h][e] |= 0x7FFFu;
-              if ((vs2[h][e] >> 16) == 0x4570u) vs2[h][e] |= 0x7FFF0000u;
+              if ((ks2[h][e] & 0xFFFFu) == kNaNRaw) ks2[h][e] = 0x7FFF7FFFu;
+              if ((vs2[h][e] & 0xFFFFu) == kNaNRaw) vs2[h][e] |= 0x7FFFu;
+              if ((vs2[h][e] >> 16) == kNaNRaw) vs2[h][e] |= 0x7FFF0000u;
             }
         }
         // S^T = K q^T
@@ -455,10 +456,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
           uint32_t kw[2][D / 32];
 #pragma unroll
           for (int e = 0; e < 2; ++e) lds_words(at + k_at + h * HC * X::BYTES + e * 8 * X::CB, kw[e]);
-          const uint32_t b2[2] = {scale_bias(ks2[h][0]), scale_bias(ks2[h][1])};
+          const SubScale sc[2] = {sub_scale(ks2[h][0]), sub_scale(ks2[h][1])};
 #pragma unroll
           for (int w = 0; w < D / 32; ++w) {
-            const uint4 a = expand8(kw[0][w], ks2[h][0], b2[0]), b = expand8(kw[1][w], ks2[h][1], b2[1]);
+            const uint4 a = expand8_sub(kw[0][w], sc[0]), b = expand8_sub(kw[1][w], sc[1]);
             const uint32_t a0[4] = {a.x, b.x, a.y, b.y}, a1[4] = {a.z, b.z, a.w, b.w};
             const uint32_t q0[2] = {qf[4 * w], qf[4 * w + 1]}, q1[2] = {qf[4 * w + 2], qf[4 * w + 3]};
             mma_bf16_16816(s[h], a0, q0);
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             lds_words(at + h * HC * X::BYTES + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
-          const uint32_t vb2[2] = {scale_bias(vs2[h][0]), scale_bias(vs2[h][1])};
+          const SubScale sc[2] = {sub_scale(vs2[h][0]), sub_scale(vs2[h][1])};
 #pragma unroll
           for (int w = 0; w < D / 64; ++w) {
             // halves of the same nibbles of two tokens side by side: even channels from the low halves, odd from the high
@@ -527,8 +528,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
               ev[e] = __byte_perm(vw[2 * e][w], vw[2 * e + 1][w], 0x5410);
               od[e] = __byte_perm(vw[2 * e][w], vw[2 * e + 1][w], 0x7632);
             }
-            const uint4 e0 = expand8(ev[0], vs2[h][0], vb2[0]), e1 = expand8(ev[1], vs2[h][1], vb2[1]);
-            const uint4 d0 = expand8(od[0], vs2[h][0], vb2[0]), d1 = expand8(od[1], vs2[h][1], vb2[1]);
+            const uint4 e0 = expand8_sub(ev[0], sc[0]), e1 = expand8_sub(ev[1], sc[1]);
+            const uint4 d0 = expand8_sub(od[0], sc[0]), d1 = expand8_sub(od[1], sc[1]);
             const uint32_t a0[4] = {e0.x, d0.x, e1.x, d1.x}, a1[4] = {e0.y, d0.y, e1.y, d1.y};
             const uint32_t a2[4] = {e0.z, d0.z, e1.z, d1.z}, a3[4] = {e0.w, d0.w, e1.w, d1.w};
             mma_bf16_16816(o[4 * w], a0, pb[h]);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
         if (hh >= gs) continue;
         if (whole) {
           const bool any = l[e] > 0.f || l[e] != l[e];
-          const float inv = any ? 1.f / l[e] : 0.f;
+          const float inv = any ? kSubUnscale / l[e] : 0.f;
           uint32_t* op = reinterpret_cast<uint32_t*>(out + ((int64_t)seq * H_q + head * gs + hh) * D + CT * r);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) op[i] = pack_bf16x2(o[i][e] * inv, o[i][2 + e] * inv);
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t
       acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w;
     }
     const bool any = L > 0.f || L != L;  // scores of -inf alone weigh nothing: out 0, lse -inf
-    const float inv = any ? 1.f / L : 0.f;
+    const float inv = any ? kSubUnscale / L : 0.f;  // (partial O comes scaled like V's values)
     const int64_t hq = (int64_t)seq * H_q + hb * heads + h;
     *reinterpret_cast<uint2*>(out + hq * D + ch) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

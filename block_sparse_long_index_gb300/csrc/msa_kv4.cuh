@@ -52,6 +52,29 @@ __device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t s2, uint32_t b2) {
   return make_uint4(expand<0>(w, s2, b2), expand<1>(w, s2, b2), expand<2>(w, s2, b2), expand<3>(w, s2, b2));
 }
 
+// The same expansion for a kernel bound by its integer instructions.  The low byte of a half, masked to one of
+// its nibbles, is already a bf16 proportional to the code: as bits of a subnormal (or of the first binade, where
+// the spacing is the same) c << 0 is c 2^-133 and c << 4 is 16 c 2^-133.  So half the shifts and every OR go, and
+//   c 2^-133 * M - 8 s 2^-18 = (c - 8) s 2^-18,  M = s 2^115 (or M / 16),
+// is exact: all values come out scaled by 2^-18, which their user takes back in fp32.  M stays below 2^127.
+constexpr float kSubUnscale = 262144.0f;                 // 2^18
+constexpr uint32_t kSubScaleBias = (107u + 115u) << 7;   // M's bits are (byte << 4) + this
+struct SubScale {
+  uint32_t m, m16, b;
+};
+__device__ __forceinline__ SubScale sub_scale(uint32_t m) {
+  SubScale s;
+  s.m = m;
+  s.m16 = hmul2_bf16(m, 0x3D803D80u);  // 2^-4
+  s.b = hmul2_bf16(m, 0x80088008u);    // -8 * 2^-133
+  return s;
+}
+__device__ __forceinline__ uint4 expand8_sub(uint32_t w, const SubScale& s) {
+  const uint32_t h = w >> 8;
+  return make_uint4(hfma2_bf16(w & 0x000F000Fu, s.m, s.b), hfma2_bf16(w & 0x00F000F0u, s.m16, s.b),
+                    hfma2_bf16(h & 0x000F000Fu, s.m, s.b), hfma2_bf16(h & 0x00F000F0u, s.m16, s.b));
+}
+
 // The scale of a group whose largest magnitude is the bf16 `amax` (bits, finite): the smallest one with
 // 7 scale >= amax.  The top mantissa bits of amax / 7 give it or the one below it, and 7 scale is exact.
 __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {

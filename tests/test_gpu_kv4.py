@@ -339,3 +339,20 @@ def test_msa_step_every_block_is_dense():
     b = run.dense(q, table, i32(ctx), 0.1)
     assert float((a[0].float() - b[0].float()).norm() / b[0].float().norm()) < 2 * ref.BF16_HALF
     assert float((a[1] - b[1]).abs().max()) < 1e-5
+
+
+def test_dense_decode_every_code_and_scale():
+    """One token a sequence: its output is V itself, so each (code, scale) pair is seen to be exact, the largest
+    and the smallest ones, and NaN scales, among them."""
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    for d in (64, 128):
+        pool = random_pool(256, 16, 1, d)
+        codes = np.tile(np.arange(16), d // 16)
+        pool.v_codes[:, 0] = torch.from_numpy(ref.pack(codes[None])).cuda()
+        pool.v_scales[:, 0] = torch.arange(256, device="cuda", dtype=torch.uint8)[:, None, None]
+        q = torch.randn(256, 8, d, device="cuda").to(torch.bfloat16)
+        run = MsaDecodeKv4(pool, 256, 1, 8)
+        out, _ = run.dense(q, torch.arange(256, dtype=torch.int32, device="cuda")[:, None], i32([1] * 256), 0.1)
+        want = ref.values(np.broadcast_to(codes, (256, d)), np.repeat(np.arange(256), 4).reshape(256, 4))
+        got = out.double().cpu().numpy()
+        assert all(np.array_equal(got[:, h], want, equal_nan=True) for h in range(8))
