@@ -607,7 +607,8 @@ msa_status_t msa_dense_decode_paged_kv4(const void* q_t, const msa_kv4_pool_t* p
   if (!aligned16(q_t) || !aligned16(out) || ((uintptr_t)ctx_len & 3u) || ((uintptr_t)lse & 3u))
     return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, msa_dense_decode_paged_kv4_workspace(B, H_q, pool->H_kv, pool->d), s);
+  st = begin(workspace, workspace_bytes, msa_dense_decode_paged_kv4_workspace(B, H_q, pool->H_kv, pool->d), s,
+             kHeader + msa::kDenseDecodeClear);
   if (st != MSA_OK) return st;
   return finish(msa::launch_dense_decode(q_t, kv4_pool(pool), page_table, max_pages, ctx_len, B, H_q, scale, out, lse,
                                          (char*)workspace + kHeader, (msa::DeviceStatus*)workspace, s));

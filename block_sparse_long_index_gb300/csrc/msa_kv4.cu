@@ -276,6 +276,13 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
   return f;
 }
 
+// A row that several CTAs share, listed by the second of them.
+struct SplitRow {
+  int seq, hb;
+  int c0, c1;   // the CTAs that hold it
+  int part0;    // which partial of c0 it is (partial 0 of the others)
+};
+
 // A CTA's run, segment by segment: units [u0, u1) of the T units of (sequence, head block).
 struct Segments {
   const int32_t* ctx_len;
@@ -310,8 +317,8 @@ template <int D, int HC>
 __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ q,
     Kv4Pool pool, CacheMap map, const int32_t* __restrict__ ctx_len, int B, int64_t cap, int gs, float scale, int stages,
-    uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml,
-    DeviceStatus* st) {
+    uint16_t* __restrict__ out, float* __restrict__ lse, int* __restrict__ n_rows, SplitRow* __restrict__ rows,
+    float* __restrict__ part_o, float2* __restrict__ part_ml, DeviceStatus* st) {
   constexpr int TW = kDecWarps / HC, SU = 2 * TW;  // warps that share a head, units of a step
   constexpr int CT = D / 8;           // channels of a lane's V column
   using X = Tile<D>;
@@ -347,6 +354,19 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     sg.f1 = min(fs.total, sg.f + fs.quota);
     sg.before = fs.before;
     sg.seq = fs.seq;
+    if (threadIdx.x == 0 && sg.next() && sg.u0 > 0) {  // the run begins inside a row
+      const int64_t r0 = sg.f - sg.u0, c = blockIdx.x;
+      const int c0 = (int)(r0 / fs.quota);
+      if (c0 == c - 1) {
+        SplitRow row;
+        row.seq = sg.seq;
+        row.hb = sg.hb;
+        row.c0 = c0;
+        row.c1 = (int)((r0 + sg.T - 1) / fs.quota);
+        row.part0 = r0 == c0 * fs.quota ? 0 : 1;
+        rows[atomicAdd(n_rows, 1)] = row;  // the list's order is free: rows are merged independently
+      }
+    }
   }
   const float kInf = __int_as_float(0x7f800000);
   constexpr int kScales = 32 * X::BYTES;  // offset of the scales in a stage
@@ -629,64 +649,65 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
       if (fetched >> i & 1u) mbar_wait(full(i), fetched >> (16 + i) & 1u, nullptr, st, 0xEF1);
 }
 
-// One CTA per (sequence, head block) row: merges the partials of the CTAs that share it.
+// Merges the partials of the listed rows: a CTA per (row, two heads), 4 warps a head, each with every 4th partial.
 template <int D>
-__global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int32_t* __restrict__ ctx_len, int B, int64_t cap,
-                                                                  int H_kv, int HC, int gs, int n_cta,
+__global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int* __restrict__ n_rows,
+                                                                  const SplitRow* __restrict__ rows, int H_kv, int HC, int gs,
                                                                   const float* __restrict__ part_o,
                                                                   const float2* __restrict__ part_ml,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse) {
-  const int n_hb = (H_kv + HC - 1) / HC, seq = blockIdx.x / n_hb, hb = blockIdx.x % n_hb;
-  const int tid = threadIdx.x;
+  constexpr int V = D / 32;  // channels of a lane
+  __shared__ float acc_s[2][4][D], l_s[2][4];
   griddep_wait();  // the partials
-  int64_t total = 0, before = 0;
-  __shared__ int64_t sums[2][kDecWarps];
-  for (int s = tid; s < B; s += kCombThreads) {
-    const int64_t n = units_of(ctx_len[s], cap);
-    total += n;
-    if (s < seq) before += n;
-  }
+  if ((int)blockIdx.x >= *n_rows) return;
+  const SplitRow row = rows[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp & 3;
+  const int h = blockIdx.y * 2 + (warp >> 2);  // head of the block
+  const int heads = min(HC * gs, (H_kv - row.hb * HC) * gs);
+  const bool on = h < heads;
+  const float kInf = __int_as_float(0x7f800000);
+  auto slot_of = [&](int ct) { return ((int64_t)ct * 2 + (ct == row.c0 ? row.part0 : 0)) * (HC * gs) + h; };
+  float M = -kInf, L = 0.f, acc[V];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if ((tid & 31) == 0) sums[0][tid >> 5] = total, sums[1][tid >> 5] = before;
-  __syncthreads();
-  total = before = 0;
-  for (int w = 0; w < kDecWarps; ++w) total += sums[0][w], before += sums[1][w];
-  total *= n_hb;
-  const int64_t quota = quota_of(total, n_cta, 2 * kDecWarps / HC);
-  const int64_t T = units_of(ctx_len[seq], cap);
-  const int64_t r0 = before * n_hb + hb * T, r1 = r0 + T;
-  const int c0 = (int)(r0 / quota), c1 = (int)((r1 - 1) / quota);
-  if (c0 == c1) return;  // one CTA held the row whole
-  const int heads = HC * gs, H_q = H_kv * gs;
-  auto slot_of = [&](int ct, int h) {  // a row that holds the CTA's first unit is its partial 0
-    return ((int64_t)ct * 2 + (r0 <= ct * quota ? 0 : 1)) * heads + h;
-  };
-  const int mine = min(heads, (H_kv - hb * HC) * gs);  // the last block may be short of heads
-  for (int e = tid; e < mine * (D / 4); e += kCombThreads) {
-    const int h = e / (D / 4), ch = 4 * (e % (D / 4));
-    float M = __int_as_float(0xff800000);
-    for (int ct = c0; ct <= c1; ++ct) M = fmaxf(M, part_ml[slot_of(ct, h)].x);
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int ct = c0; ct <= c1; ++ct) {
-      const int64_t sl = slot_of(ct, h);
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  if (on) {
+    for (int ct = row.c0 + lane; ct <= row.c1; ct += 32) M = fmaxf(M, part_ml[slot_of(ct)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+    for (int ct = row.c0 + w; ct <= row.c1; ct += 4) {
+      const int64_t sl = slot_of(ct);
       const float2 ml = part_ml[sl];
-      const float w = ml.x == M ? 1.f : ex2_approx(ml.x - M);
-      const float4 x = *reinterpret_cast<const float4*>(part_o + sl * D + ch);
-      L += ml.y * w;
-      acc.x += x.x * w, acc.y += x.y * w, acc.z += x.z * w, acc.w += x.w * w;
+      const float wt = ml.x == M ? 1.f : ex2_approx(ml.x - M);
+      L += ml.y * wt;
+      const float* p = part_o + sl * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        acc[0] += x.x * wt, acc[1] += x.y * wt, acc[2] += x.z * wt, acc[3] += x.w * wt;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        acc[0] += x.x * wt, acc[1] += x.y * wt;
+      }
     }
-    const bool any = L > 0.f || L != L;  // scores of -inf alone weigh nothing: out 0, lse -inf
-    const float inv = any ? kSubUnscale / L : 0.f;  // (partial O comes scaled like V's values)
-    const int64_t hq = (int64_t)seq * H_q + hb * heads + h;
-    *reinterpret_cast<uint2*>(out + hq * D + ch) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (ch == 0 && lse) lse[hq] = any ? (M + log2f(L)) * 0.69314718055994530942f : __int_as_float(0xff800000);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc_s[warp >> 2][w][lane * V + i] = acc[i];
+    if (lane == 0) l_s[warp >> 2][w] = L;
   }
+  __syncthreads();
+  if (!on || w != 0) return;
+  L = l_s[warp >> 2][0] + l_s[warp >> 2][1] + l_s[warp >> 2][2] + l_s[warp >> 2][3];
+  const bool any = L > 0.f || L != L;  // scores of -inf alone weigh nothing: out 0, lse -inf
+  const float inv = any ? kSubUnscale / L : 0.f;  // (partial O comes scaled like V's values)
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int ch = lane * V + i;
+    acc[i] = (acc_s[warp >> 2][0][ch] + acc_s[warp >> 2][1][ch] + acc_s[warp >> 2][2][ch] + acc_s[warp >> 2][3][ch]) * inv;
+  }
+  const int64_t hq = (int64_t)row.seq * (H_kv * gs) + row.hb * HC * gs + h;
+  uint32_t* op = reinterpret_cast<uint32_t*>(out + hq * D + lane * V);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) op[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
+  if (lane == 0 && lse) lse[hq] = any ? (M + log2f(L)) * 0.69314718055994530942f : -kInf;
 }
 
 RowMap row_map(const Kv4Pool& pool, const int32_t* cu, int S, const int32_t* pos0, const int32_t* table, int64_t max_pages) {
@@ -710,8 +731,8 @@ int decode_ctas() { return 2 * num_sms(); }
 
 template <int D, int HC>
 cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const CacheMap& map, const int32_t* ctx_len, int B,
-                                  int64_t cap, int gs, float scale, void* out, float* lse, float* part_o, float2* part_ml,
-                                  DeviceStatus* st, cudaStream_t s) {
+                                  int64_t cap, int gs, float scale, void* out, float* lse, int* n_rows, SplitRow* rows,
+                                  float* part_o, float2* part_ml, DeviceStatus* st, cudaStream_t s) {
   constexpr int TW = kDecWarps / HC, CB = D / 2;
   alignas(64) unsigned char tk[128], tv[128];
   // codes [n_pages][page][H_kv][CB] bytes (as 16-bit words) in the order {row, token, head, page}
@@ -729,10 +750,11 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
   if (e != cudaSuccess) return e;
   kern<<<n_cta, kDecThreads, smem, s>>>(*reinterpret_cast<const CUtensorMap*>(tk), *reinterpret_cast<const CUtensorMap*>(tv),
                                         (const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale, stages, (uint16_t*)out,
-                                        lse, part_o, part_ml, st);
+                                        lse, n_rows, rows, part_o, part_ml, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(B * ((pool.H_kv + HC - 1) / HC)));
+  const int64_t most = (int64_t)B * ((pool.H_kv + HC - 1) / HC);  // rows; at most one split a CTA boundary
+  cfg.gridDim = dim3((unsigned)(most < n_cta ? most : n_cta), (unsigned)(HC * gs + 1) / 2);
   cfg.blockDim = dim3(kCombThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -740,8 +762,8 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D>, ctx_len, B, cap, pool.H_kv, HC, gs, n_cta, (const float*)part_o,
-                            (const float2*)part_ml, (uint16_t*)out, lse);
+  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D>, (const int*)n_rows, (const SplitRow*)rows, pool.H_kv, HC, gs,
+                            (const float*)part_o, (const float2*)part_ml, (uint16_t*)out, lse);
 }
 
 int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
@@ -768,25 +790,46 @@ cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, i
   return cudaGetLastError();
 }
 
-size_t dense_decode_scratch_bytes(int H_kv, int gs, int d) {
+// Scratch: the number of split rows (cleared before each call), their list, the partials.
+struct DecScratch {
+  int* n_rows;
+  SplitRow* rows;
+  float* part_o;
+  float2* part_ml;
+};
+static size_t carve_dense_decode(int H_kv, int gs, int d, char* base, DecScratch* out) {
   const size_t slots = (size_t)decode_ctas() * 2 * heads_per_cta(H_kv) * gs;
-  return align_up(slots * d * 4, 256) + align_up(slots * 8, 256);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* r = base ? base + off : nullptr;
+    off += align_up(bytes, 256);
+    return r;
+  };
+  DecScratch w;
+  w.n_rows = (int*)take(kDenseDecodeClear);
+  w.rows = (SplitRow*)take((size_t)decode_ctas() * sizeof(SplitRow));
+  w.part_o = (float*)take(slots * d * 4);
+  w.part_ml = (float2*)take(slots * 8);
+  if (out) *out = w;
+  return off;
 }
+
+size_t dense_decode_scratch_bytes(int H_kv, int gs, int d) { return carve_dense_decode(H_kv, gs, d, nullptr, nullptr); }
 
 cudaError_t launch_dense_decode(const void* q, const Kv4Pool& pool, const int32_t* table, int64_t max_pages,
                                 const int32_t* ctx_len, int B, int H_q, float scale, void* out, float* lse, void* scratch,
                                 DeviceStatus* st, cudaStream_t s) {
   const int gs = H_q / pool.H_kv, HC = heads_per_cta(pool.H_kv);
-  const size_t slots = (size_t)decode_ctas() * 2 * HC * gs;
-  float* po = (float*)scratch;
-  float2* ml = (float2*)((char*)scratch + align_up(slots * pool.d * 4, 256));
+  DecScratch w;
+  carve_dense_decode(pool.H_kv, gs, pool.d, (char*)scratch, &w);
   CacheMap map;
   map.table = table;
   map.max_pages = max_pages;
   map.n_pages = pool.n_pages;
   map.page = pool.page;
   const int64_t cap = max_pages * pool.page;
-#define MSA_DD(D, H) launch_dense_decode_t<D, H>(q, pool, map, ctx_len, B, cap, gs, scale, out, lse, po, ml, st, s)
+#define MSA_DD(D, H) \
+  launch_dense_decode_t<D, H>(q, pool, map, ctx_len, B, cap, gs, scale, out, lse, w.n_rows, w.rows, w.part_o, w.part_ml, st, s)
   if (pool.d == 64) return HC == 8 ? MSA_DD(64, 8) : HC == 4 ? MSA_DD(64, 4) : HC == 2 ? MSA_DD(64, 2) : MSA_DD(64, 1);
   return HC == 8 ? MSA_DD(128, 8) : HC == 4 ? MSA_DD(128, 4) : HC == 2 ? MSA_DD(128, 2) : MSA_DD(128, 1);
 #undef MSA_DD
