@@ -43,74 +43,121 @@ struct RowMap {
   }
 };
 
-// One warp per packed row (token): 8 channels of a head row a lane, K's head rows then V's.  A group is 4
-// (d = 128) or 2 (d = 64) lanes, whose shared maximum gives its scale.
-template <int D>
+// A CTA takes R x U x tpp packed rows (tokens), tpp = the tokens that 256 threads cover at 8 channels a thread (K's
+// head rows, then V's): it looks all of them up first, then has the reads of U x tpp of them in flight at a time.
+// U = 4 and R up to kRounds where the CTAs still fill the GPU, 1 and 1 otherwise (a decode step's few rows).
+constexpr int kRounds = 8;
+struct RowTile {
+  int per_tok, tpp;
+  __host__ __device__ RowTile(int H_kv, int lanes_per_row) {
+    per_tok = 2 * H_kv * lanes_per_row;
+    tpp = per_tok < kRowThreads ? kRowThreads / per_tok : 1;
+  }
+};
+
+template <int D, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* __restrict__ k,
-                                                                const uint16_t* __restrict__ v, int64_t N, RowMap map,
+                                                                const uint16_t* __restrict__ v, int64_t N, int R, RowMap map,
                                                                 Kv4Pool pool, DeviceStatus* st) {
-  constexpr int LPR = D / 8, LPG = LPR / kGroups;
-  const int lane = threadIdx.x & 31;
-  const int64_t stride = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < N; i += stride) {
-    const int64_t row = map.row(i, lane == 0 ? st : nullptr);
-    if (row < 0) continue;
-    const int tasks = pool.H_kv * LPR;
+  constexpr int LPR = D / 8, LPG = LPR / kGroups;  // threads of a head row, of a group
+  __shared__ int64_t rows[U == 1 ? 32 : U * kRounds * 16];
+  const RowTile rt(pool.H_kv, LPR);
+  const int half = rt.per_tok / 2;
+  const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
+  for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) rows[t] = i0 + t < N ? map.row(i0 + t, st) : -1;
+  __syncthreads();
+  const int sub = threadIdx.x / rt.per_tok;  // 0 where a token takes the whole CTA
+  for (int c = threadIdx.x - sub * rt.per_tok; c < rt.per_tok; c += kRowThreads) {
+    const bool on = sub < rt.tpp, is_v = c >= half;
+    const int e = is_v ? c - half : c;  // 8-channel piece of the token's K or V
+    const uint16_t* src = (is_v ? v : k) + e * 8;
+    uint8_t* codes = is_v ? pool.v_codes : pool.k_codes;
+    uint8_t* scales = is_v ? pool.v_scales : pool.k_scales;
+    const unsigned lanes = ((1u << LPG) - 1u) << (threadIdx.x & 31u & ~(LPG - 1u));  // the group (per_tok holds whole ones)
 #pragma unroll 1
-    for (int c0 = 0; c0 < 2 * tasks; c0 += 32) {
-      const int c = c0 + lane;
-      const bool in = c < 2 * tasks, is_v = c >= tasks;
-      const int e = is_v ? c - tasks : c;  // 8-channel piece of the token's K or V
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (in) x = ldg_stream_16((is_v ? v : k) + (i * tasks + e) * 8);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
+    for (int r = 0; r < R; ++r) {
+      int64_t row[U];
+      uint4 x[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = max(mx, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-#pragma unroll
-      for (int o = 1; o < LPG; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const bool bad = mx >= 0x7F80u;
-      const uint32_t sb = bad ? kScaleNaN : scale_of(mx);
-      const float inv = bad ? 0.f : 1.0f / scale_f32(sb);
-      uint32_t code = 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // channels 2j, 2j + 1 -> nibbles j, j + 4
-        code |= (bad ? 8u : code_of(bf16_lo(w[j]), inv)) << (4 * j);
-        code |= (bad ? 8u : code_of(bf16_hi(w[j]), inv)) << (4 * j + 16);
+      for (int u = 0; u < U; ++u) {
+        const int t = (r * U + u) * rt.tpp + sub;
+        row[u] = on ? rows[t] : -1;
+        x[u] = row[u] >= 0 ? ldg_stream_16(src + (i0 + t) * half * 8) : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (in) {
-        uint8_t* codes = is_v ? pool.v_codes : pool.k_codes;
-        uint8_t* scales = is_v ? pool.v_scales : pool.k_scales;
-        reinterpret_cast<uint32_t*>(codes)[row * tasks + e] = code;
-        if (lane % LPG == 0) scales[row * (pool.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = max(mx, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, o));
+        uint32_t sb = scale_of(mx), code;
+        const float s = scale_f32(sb), inv = __fdividef(1.0f, s);
+        float lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lo[j] = bf16_lo(w[j]), hi[j] = bf16_hi(w[j]);
+        if (mx >= 0x7F80u) {
+          sb = kScaleNaN;
+          code = 0x88888888u;
+        } else {
+          if (sb == kScaleMax) {  // the one scale whose group may reach past 7 s
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lo[j] = fminf(fmaxf(lo[j], -7.f * s), 7.f * s), hi[j] = fminf(fmaxf(hi[j], -7.f * s), 7.f * s);
+          }
+          code = codes4(lo, inv) | codes4(hi, inv) << 16;
+        }
+        if (row[u] >= 0) {
+          reinterpret_cast<uint32_t*>(codes)[row[u] * half + e] = code;
+          if (e % LPG == 0) scales[row[u] * (pool.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
+        }
       }
     }
   }
 }
 
 // The same rows back as exact bf16 values; zeros where the row map has no place.
-template <int D>
-__global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int64_t N, RowMap map,
+template <int D, int U>
+__global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int64_t N, int R, RowMap map,
                                                                uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                                DeviceStatus* st) {
   constexpr int LPR = D / 8, LPG = LPR / kGroups;
-  const int lane = threadIdx.x & 31;
-  const int64_t stride = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < N; i += stride) {
-    if (i >= map.cu[map.S] || i < map.cu[0]) continue;  // rows of no sequence stay as they were
-    const int64_t row = map.row(i, lane == 0 ? st : nullptr);
-    const int tasks = pool.H_kv * LPR;
-    for (int c = lane; c < 2 * tasks; c += 32) {
-      const bool is_v = c >= tasks;
-      const int e = is_v ? c - tasks : c;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= 0) {
-        const uint8_t* codes = is_v ? pool.v_codes : pool.k_codes;
-        const uint8_t* scales = is_v ? pool.v_scales : pool.k_scales;
-        const uint32_t s = scale_bf16(scales[row * (pool.H_kv * kGroups) + e / LPG]), s2 = s | (s << 16);
-        x = expand8(reinterpret_cast<const uint32_t*>(codes)[row * tasks + e], s2, scale_bias(s2));
+  __shared__ int64_t rows[U == 1 ? 32 : U * kRounds * 16];  // pool row, -1: zeros, -2: a row of no sequence
+  const RowTile rt(pool.H_kv, LPR);
+  const int half = rt.per_tok / 2;
+  const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
+  const int64_t in0 = map.cu[0], in1 = map.cu[map.S];
+  for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) {
+    const int64_t i = i0 + t;
+    rows[t] = i < N && i >= in0 && i < in1 ? map.row(i, st) : -2;
+  }
+  __syncthreads();
+  const int sub = threadIdx.x / rt.per_tok;
+  if (sub >= rt.tpp) return;
+  for (int c = threadIdx.x - sub * rt.per_tok; c < rt.per_tok; c += kRowThreads) {
+    const bool is_v = c >= half;
+    const int e = is_v ? c - half : c;
+    const uint8_t* codes = is_v ? pool.v_codes : pool.k_codes;
+    const uint8_t* scales = is_v ? pool.v_scales : pool.k_scales;
+    uint16_t* dst = (is_v ? v : k) + e * 8;
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+      uint32_t w[U], sb[U];
+      int64_t row[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        row[u] = rows[(r * U + u) * rt.tpp + sub];
+        const int64_t at = row[u] < 0 ? 0 : row[u];
+        w[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + at * half + e);
+        sb[u] = __ldg(scales + at * (pool.H_kv * kGroups) + e / LPG);
       }
-      *reinterpret_cast<uint4*>((is_v ? v : k) + (i * tasks + e) * 8) = x;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (row[u] == -2) continue;
+        const uint32_t s = scale_bf16(sb[u]), s2 = s | (s << 16);
+        const uint4 x = expand8(w[u], s2, scale_bias(s2));
+        *reinterpret_cast<uint4*>(dst + (i0 + (r * U + u) * rt.tpp + sub) * half * 8) = row[u] < 0 ? make_uint4(0u, 0u, 0u, 0u) : x;
+      }
     }
   }
 }
@@ -722,11 +769,6 @@ RowMap row_map(const Kv4Pool& pool, const int32_t* cu, int S, const int32_t* pos
   return m;
 }
 
-unsigned row_grid(int64_t N) {
-  const int64_t want = ceil_div(N, kRowThreads / 32), most = (int64_t)num_sms() * 8;
-  return (unsigned)(want < most ? want : most);
-}
-
 int decode_ctas() { return 2 * num_sms(); }
 
 template <int D, int HC>
@@ -770,23 +812,31 @@ int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
 
 }  // namespace
 
+// Rounds of a CTA: 0 stands for U = 1.  Four CTAs an SM at least before a CTA takes a second round.
+static int rows_rounds(int64_t N, int tpp) {
+  const int64_t fill = (int64_t)4 * num_sms() * 4 * tpp, r = N / fill;
+  return r > kRounds ? kRounds : (int)r;
+}
+
 cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                              const int32_t* table, int64_t max_pages, const Kv4Pool& pool, DeviceStatus* st, cudaStream_t s) {
   const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
-  if (pool.d == 64)
-    kv4_store_kernel<64><<<row_grid(N), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N, map, pool, st);
-  else
-    kv4_store_kernel<128><<<row_grid(N), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N, map, pool, st);
+  const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
+  auto kern = pool.d == 64 ? (R ? kv4_store_kernel<64, 4> : kv4_store_kernel<64, 1>)
+                           : (R ? kv4_store_kernel<128, 4> : kv4_store_kernel<128, 1>);
+  kern<<<(unsigned)ceil_div(N, (R ? 4 * R : 1) * tpp), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N,
+                                                                          R ? R : 1, map, pool, st);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                             const int32_t* table, int64_t max_pages, void* k, void* v, DeviceStatus* st, cudaStream_t s) {
   const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
-  if (pool.d == 64)
-    kv4_load_kernel<64><<<row_grid(N), kRowThreads, 0, s>>>(pool, N, map, (uint16_t*)k, (uint16_t*)v, st);
-  else
-    kv4_load_kernel<128><<<row_grid(N), kRowThreads, 0, s>>>(pool, N, map, (uint16_t*)k, (uint16_t*)v, st);
+  const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
+  auto kern = pool.d == 64 ? (R ? kv4_load_kernel<64, 4> : kv4_load_kernel<64, 1>)
+                           : (R ? kv4_load_kernel<128, 4> : kv4_load_kernel<128, 1>);
+  kern<<<(unsigned)ceil_div(N, (R ? 4 * R : 1) * tpp), kRowThreads, 0, s>>>(pool, N, R ? R : 1, map, (uint16_t*)k,
+                                                                          (uint16_t*)v, st);
   return cudaGetLastError();
 }
 

@@ -85,15 +85,19 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
   return (uint32_t)min(b, (int)kScaleMax);
 }
 
-// round-to-nearest-even(x / s) clamped to -7..7, plus 8.  x has 8 and s has 4 significant bits, so x / s is a
-// tie or at least 2^-11 away from one wherever it rounds to a code; x * (1 / s) in fp32 is off by less than
-// 2^-20, and adding and taking off 1.5 * 2^10 rounds it to a multiple of 2^-13, which makes a tie exact again.
-__device__ __forceinline__ uint32_t code_of(float x, float inv_s) {
-  float y = __fmul_rn(x, inv_s);
-  y = fminf(fmaxf(y, -8.0f), 8.0f);
-  y = __fadd_rn(__fadd_rn(y, 1536.0f), -1536.0f);
-  const int c = __float2int_rn(y);
-  return (uint32_t)(min(max(c, -7), 7) + 8);
+// Four codes, nibbles 0 .. 3: round-to-nearest-even(x / s) + 8 for |x / s| <= 7.
+// x has 8 and s has 4 significant bits, so x / s is a tie or at least 2^-11 away from one wherever it rounds to a
+// code that is not 0.  fma(x, 1/s, 1.5 * 2^10) rounds x / s to a multiple of 2^-13 (1/s may be 2^-20 off): a tie is
+// exact again, the others keep their side.  Adding 1.5 * 2^23 - 1.5 * 2^10 rounds that to an integer, which the
+// mantissa then holds; its bits are summed with weights 16^i and the constant part taken off at the end.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv_s) {
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const float t = __fadd_rn(__fmaf_rn(x[i], inv_s, 1536.0f), 12582912.0f - 1536.0f);
+    sum = sum * 16u + __float_as_uint(t);
+  }
+  return sum - (0x4B400000u * 0x1111u - 0x8888u);
 }
 
 }  // namespace kv4
