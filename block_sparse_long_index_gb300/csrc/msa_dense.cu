@@ -116,9 +116,11 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // lazy: O and the row sum are rescaled only when a row's maximum has grown by
 // more than 2^8, so P stays below 256 (its bf16 rounding is relative, so the
 // factor costs no precision) and the rescale of O in TMEM is rare.
-// Warpgroups: 0 and 1 the softmax of query tile 0 and 1 (a thread per row), 2
-// the output (O / l, lse), 3 one warp each for the TMA loads, the MMA issue,
-// and two guard warps.
+// Warpgroups: 0 and 1 the softmax of query tile 0, 2 and 3 of query tile 1 (a
+// row is two threads', 64 keys each, which exchange their maxima through shared
+// memory: a tile's softmax has to end before the tensor cores run out of the
+// other tile's products), 4 the output (O / l, lse), 5 one warp each for the TMA
+// loads, the MMA issue, and two guard warps.
 //
 // The guard warps make the masked places of V harmless, because a weight of 0
 // times a NaN or an infinity would not be 0 on the tensor cores: in the key
@@ -126,10 +128,10 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // item's last position and any value that is not finite, and the epilogue then
 // adds the latter to the rows that do see them.
 constexpr int kRowsT = 128, kKeysT = 128;
-constexpr int kThreadsA = 512;
-constexpr uint32_t kRegsSoft = 184, kRegsEpi = 72, kRegsLoad = 72;
-static_assert(256 * kRegsSoft + 128 * kRegsEpi + 128 * kRegsLoad == kThreadsA * 128, "the registers of the launch");
-constexpr int kWarpEpi = 8, kWarpLoad = 12, kWarpMma = 13, kWarpGuard = 14;
+constexpr int kThreadsA = 768;
+constexpr uint32_t kRegsSoft = 96, kRegsEpi = 48, kRegsLoad = 48;
+static_assert(512 * kRegsSoft + 128 * kRegsEpi + 128 * kRegsLoad <= kThreadsA * 80, "the registers of the launch");
+constexpr int kWarpEpi = 16, kWarpLoad = 20, kWarpMma = 21, kWarpGuard = 22;
 constexpr float kLazy = 8.0f;
 constexpr int kPoisonSlots = 8;
 
@@ -141,8 +143,9 @@ struct Layout {
   static constexpr int STAGES = D == 128 ? 4 : 8;    // K and V tiles in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_ST = OFF_KV + STAGES * TILE;  // (m, l) of each row
-  static constexpr int OFF_BAR = OFF_ST + 2 * 128 * 8;
+  static constexpr int OFF_ST = OFF_KV + STAGES * TILE;  // each row's (m, l), two halves' l: [2 tiles][128] x 16 bytes
+  static constexpr int OFF_MX = OFF_ST + 2 * 128 * 16;   // exchange of row maxima: [key tile parity][2 tiles][2 halves][128]
+  static constexpr int OFF_BAR = OFF_MX + 2 * 2 * 2 * 128 * 4;
   static constexpr int SMEM = 1024 + OFF_BAR + 512;
   static constexpr uint32_t TMEM_O = 256;            // S / P of tile q at 128 q, O of tile q at 256 + 128 q
 };
@@ -160,16 +163,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+// The two warps that hold a row quarter's halves meet (64 threads, one of 8 named barriers).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
 }
@@ -224,16 +231,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   auto q_full = [&](int q) { return bar + 8u * (B0 + q); };              // TMA -> MMA
   auto q_empty = [&](int q) { return bar + 8u * (B0 + 2 + q); };         // MMA (commit) -> TMA
   auto s_full = [&](int q) { return bar + 8u * (B0 + 4 + q); };          // MMA (commit) -> softmax
-  auto p_full = [&](int q) { return bar + 8u * (B0 + 6 + q); };          // softmax (4 warps) -> MMA
+  auto p_full = [&](int q) { return bar + 8u * (B0 + 6 + q); };          // softmax (8 warps) -> MMA
   auto pv_done = [&](int q) { return bar + 8u * (B0 + 8 + q); };         // MMA (commit) -> softmax
   auto o_full = [&](int q) { return bar + 8u * (B0 + 10 + q); };         // MMA (commit) -> output
   auto o_empty = [&](int q) { return bar + 8u * (B0 + 12 + q); };        // output (4 warps) -> MMA, softmax
-  auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (4 warps) -> output
+  auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (8 warps) -> output
   // V tiles alone, which sit in the odd stages; one a stage, so that the guard cannot be two phases ahead
   auto v_ok = [&](int i) { return bar + 8u * (B0 + 16 + i / 2); };       // guard (2 warps) -> MMA
   const uint32_t drain = bar + 8u * (B0 + 16 + L::STAGES / 2);
   static_assert(L::STAGES % 2 == 0 && 8 * (B0 + 17 + L::STAGES / 2) <= 512, "K and V alternate; barriers fit");
-  float2* ml_s = reinterpret_cast<float2*>(sm + L::OFF_ST);
+  float4* ml_s = reinterpret_cast<float4*>(sm + L::OFF_ST);
+  float* mx_s = reinterpret_cast<float*>(sm + L::OFF_MX);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < L::STAGES; ++i) {
@@ -244,11 +252,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
       mbar_init(q_full(q), 1);
       mbar_init(q_empty(q), 1);
       mbar_init(s_full(q), 1);
-      mbar_init(p_full(q), 4);
+      mbar_init(p_full(q), 8);
       mbar_init(pv_done(q), 1);
       mbar_init(o_full(q), 1);
       mbar_init(o_empty(q), 4);
-      mbar_init(ml_full(q), 4);
+      mbar_init(ml_full(q), 8);
     }
     for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_ok(i), 2);
     mbar_init(drain, 1);
@@ -331,12 +339,13 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         };
         auto product_s = [&](int q) {
           tc_fence_after();
-          const uint32_t qa = sb + L::OFF_Q + q * L::TILE, ka = sb + L::OFF_KV + (k_at % L::STAGES) * L::TILE;
+          // a descriptor's low bits are the address / 16: the steps along d are added to it
+          const uint64_t qd = umma_desc_kmajor(sb + L::OFF_Q + q * L::TILE, 128);
+          const uint64_t kd = umma_desc_kmajor(sb + L::OFF_KV + (k_at % L::STAGES) * L::TILE, 128);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const int c = ks >> 2, kk = ks & 3;
-            mma_bf16_ss(tmem + q * 128, umma_desc_kmajor(qa + c * L::CHUNK + kk * 32, 128),
-                        umma_desc_kmajor(ka + c * L::CHUNK + kk * 32, 128), IDESC_S, ks > 0);
+            const uint32_t off = ((ks >> 2) * L::CHUNK + (ks & 3) * 32) / 16;
+            mma_bf16_ss(tmem + q * 128, qd + off, kd + off, IDESC_S, ks > 0);
           }
           umma_commit(s_full(q));
         };
@@ -366,11 +375,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
                 if (!(ok = mbar_wait(p_full(q), sn[q] & 1, abort, st, 0xD16))) break;
                 ++sn[q];
                 tc_fence_after();
-                const uint32_t va = sb + L::OFF_KV + (v_at % L::STAGES) * L::TILE;
+                const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + (v_at % L::STAGES) * L::TILE, L::CHUNK);
 #pragma unroll
-                for (int ks = 0; ks < kKeysT / 16; ++ks)
-                  mma_bf16_ts(tmem + L::TMEM_O + q * 128, tmem + q * 128 + ks * 8,
-                              umma_desc_mnmajor_sw128(va + ks * 16 * 128, L::CHUNK), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+                for (int ks = 0; ks < kKeysT / 16; ++ks)  // keys 16 ks ..: half ks / 4, packed from column 64 half on
+                  mma_bf16_ts(tmem + L::TMEM_O + q * 128, tmem + q * 128 + 64 * (ks >> 2) + 8 * (ks & 3),
+                              vd + ks * (16 * 128 / 16), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
                 umma_commit(pv_done(q));
                 if (j + 1 == it.n[q]) {
                   umma_commit(o_full(q));
@@ -455,90 +464,107 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         if (!ok) break;
         ++in[q];
         tc_fence_after();
-        const float2 ml = ml_s[q * 128 + row];
+        const float4 ml = ml_s[q * 128 + row];  // m, the halves' sums
+        const float sum = ml.y + ml.z;
         const int t = it.t0 + q * PT + pos;
         const bool live = t < it.len;
         const bool bad = poison[r % kPoisonSlots] == r + 1;
-        const float inv = 1.f / ml.y;
+        const float inv = 1.f / sum;
         const int64_t grow = (int64_t)it.row0 + t;
         const int h = it.g * GS + hh;
         uint4* orow = reinterpret_cast<uint4*>(out + (grow * H_q + h) * D);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld_x32(tmem + ((uint32_t)(quarter * 32) << 16) + L::TMEM_O + q * 128 + c * 32, x);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t x[16];
+          tmem_ld_x16(tmem + ((uint32_t)(quarter * 32) << 16) + L::TMEM_O + q * 128 + c * 16, x);
           tmem_ld_wait();
-          reg_fence32(x);
+          reg_fence16(x);
           if (bad && live)  // the values that the guard took out, for the rows that see them
             for (int j = it.t0 / kKeysT * kKeysT; j <= t; ++j) {
-              const uint16_t* vr = v + (((int64_t)it.row0 + j) * H_kv + it.g) * D + c * 32;
-              for (int e = 0; e < 32; ++e) {
+              const uint16_t* vr = v + (((int64_t)it.row0 + j) * H_kv + it.g) * D + c * 16;
+              for (int e = 0; e < 16; ++e) {
                 const uint32_t b = vr[e];
                 if ((b & 0x7F80u) == 0x7F80u) {
                   const float add = __uint_as_float(b << 16);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
+                  for (int i = 0; i < 16; ++i)
                     if (i == e) x[i] = __float_as_uint(__uint_as_float(x[i]) + add);
                 }
               }
             }
           if (live)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t y[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 y[i] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * inv, __uint_as_float(x[8 * e + 2 * i + 1]) * inv);
-              orow[c * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
+              orow[c * 2 + e] = make_uint4(y[0], y[1], y[2], y[3]);
             }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty(q));
-        if (live) lse[(int64_t)h * N + grow] = (ml.x + lg2_approx(ml.y)) * 0.69314718055994530942f;
+        if (live) lse[(int64_t)h * N + grow] = (ml.x + lg2_approx(sum)) * 0.69314718055994530942f;
       }
     }
   } else {
     regs_inc<kRegsSoft>();
-    // ------------------------------------------------------------ softmax of query tile q: a thread per row
-    const int q = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    // ------------------------------------------------------------ softmax of query tile q, keys 64 half .. + 63
+    constexpr int HK = kKeysT / 2;
+    const int q = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t scol = tmem + lane_base + q * 128, ocol = tmem + lane_base + L::TMEM_O + q * 128;
+    const uint32_t scol = tmem + lane_base + q * 128 + half * HK;
+    const uint32_t ocol = tmem + lane_base + L::TMEM_O + q * 128 + half * (D / 2);
+    const int pair = 1 + q * 4 + quarter;
+    float* mx_own = mx_s + (q * 2 + half) * 128 + row;
+    const float* mx_other = mx_s + (q * 2 + (half ^ 1)) * 128 + row;
     const float kInf = __int_as_float(0x7f800000);
     uint32_t sn = 0, in = 0;  // S products and items of this tile so far
     bool ok = true;
-    for (int r = 0; ok && items.get(r, it); ++r) {
+    for (int r = 0; items.get(r, it); ++r) {
       const int n = it.n[q];
       if (n == 0) continue;
       const int t = min(it.t0 + q * PT + row / GS, it.len - 1);  // rows past the sequence repeat its last one
       float m = -kInf;
       uint64_t l2[2] = {0, 0};
+      // After a wait that gave up the warps of a pair go on to meet, without waiting or computing, until the end.
       for (int j = 0; j < n; ++j) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(q), sn & 1, abort, st, 0xD40)))) break;
-        tc_fence_after();
-        uint32_t x[4][32];
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(s_full(q), sn & 1, abort, st, 0xD40));
+        uint32_t x[2][32];
+        float mc = -kInf;
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_x32(scol, x[0]);
+          tmem_ld_x32(scol + 32, x[1]);
+          tmem_ld_wait();
+          reg_fence32(x[0]);
+          reg_fence32(x[1]);
+          const int lim = t - j * kKeysT - half * HK;  // last visible column
+          if (__any_sync(0xffffffffu, lim < HK - 1)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(scol + c * 32, x[c]);
-        tmem_ld_wait();
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(x[c]);
-        const int lim = t - j * kKeysT;  // last visible column
-        if (__any_sync(0xffffffffu, lim < kKeysT - 1)) {
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e > lim) x[c][e] = 0xff800000u;
+          }
+          float m4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int e = 0; e < 32; e += 4) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e > lim) x[c][e] = 0xff800000u;
+            for (int c = 0; c < 2; ++c) {
+              m4[2 * c] = max3(m4[2 * c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+              m4[2 * c + 1] = max3(m4[2 * c + 1], __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
+            }
+          }
+          mc = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         }
-        float mc[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mc[c] = -kInf;
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mc[c] = max3(mc[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-        }
-        const float mt = fmaxf(max3(mc[0], mc[1], mc[2]), mc[3]) * scale_log2;
-        const bool grow = mt > m + kLazy;
+        // two buffers: who writes one again has met the other warp since it was read
+        mx_own[(sn & 1) * 512] = mc;
+        pair_sync(pair);
+        const float mt = fmaxf(mc, mx_other[(sn & 1) * 512]) * scale_log2;
+        if (!ok) continue;
+        const bool grow = mt > m + kLazy;  // both halves of a row decide alike
         if (__any_sync(0xffffffffu, grow)) {
           const float alpha = !grow ? 1.f : ex2_approx(m - mt);  // 2^-inf = 0 at the first tile
           if (grow) {
@@ -550,25 +576,25 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
               l2[i] = f2_pack(a * alpha, b * alpha);
             }
           }
-          if (j > 0) {  // O holds the products up to tile j - 1
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done(q), (sn - 1) & 1, abort, st, 0xD41)))) break;
+          if (j > 0) {  // O holds the products up to tile j - 1; this half's columns of it
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done(q), (sn - 1) & 1, abort, st, 0xD41)))) continue;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_x32(ocol + c * 32, o);
+              uint32_t o[16];
+              tmem_ld_x16(ocol + c * 16, o);
               tmem_ld_wait();
-              reg_fence32(o);
+              reg_fence16(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st_x32(ocol + c * 32, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_x16(ocol + c * 16, o);
             }
           }
         }
         const float mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
         const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-mz, -mz);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -579,7 +605,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
             l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(a0, a1));
             pk[e >> 1] = pack_bf16x2(a0, a1);
           }
-          tmem_st_x16(scol + c * 16, pk);  // keys 32 c .. -> packed columns 16 c ..
+          tmem_st_x16(scol + c * 16, pk);  // this half's keys 32 c .. -> its packed columns 16 c ..
         }
         tmem_st_wait();
         tc_fence_before();
@@ -587,14 +613,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         if (lane == 0) mbar_arrive(p_full(q));
         ++sn;
       }
-      if (!ok) break;
+      if (!ok) continue;
       // the output warps have read the item before's (m, l) once they gave O back
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_empty(q), (in & 1) ^ 1, abort, st, 0xD42)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_empty(q), (in & 1) ^ 1, abort, st, 0xD42)))) continue;
       ++in;
       float a, b, c, d;
       f2_unpack(l2[0], a, b);
       f2_unpack(l2[1], c, d);
-      ml_s[q * 128 + row] = make_float2(m, (a + b) + (c + d));
+      float* ml = reinterpret_cast<float*>(ml_s + q * 128 + row);
+      if (half == 0) ml[0] = m;
+      ml[1 + half] = (a + b) + (c + d);
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_full(q));
     }
