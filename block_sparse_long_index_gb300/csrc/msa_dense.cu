@@ -181,6 +181,14 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
 }
 
+// The value that every lane of the warp has, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // One item of the CTA's sequence of them, positions relative to the start of the sequence.
 struct Item {
   int t0, len;   // first position, length of the sequence
@@ -191,10 +199,17 @@ struct Item {
 struct Items {
   const int4* items;
   int total, H_kv, PT;  // items x groups, groups, positions of a query tile
-  __device__ __forceinline__ bool get(int round, Item& it) const {
+  __device__ __forceinline__ int index(int round) const {
     const int b = (int)blockIdx.x, n = (int)gridDim.x;
-    const int i = round * n + ((round & 1) ? n - 1 - b : b);
+    return round * n + ((round & 1) ? n - 1 - b : b);
+  }
+  __device__ __forceinline__ bool get(int round, Item& it) const {
+    const int i = index(round);
     if (i >= total) return false;
+    load(i, it);
+    return true;
+  }
+  __device__ __forceinline__ void load(int i, Item& it) const {
     const int4 x = items[i / H_kv];
     it.g = i % H_kv;
     it.row0 = x.y;
@@ -205,7 +220,6 @@ struct Items {
       const int a = it.t0 + q * PT;
       it.n[q] = a < it.len ? (min(a + PT, it.len) - 1) / kKeysT + 1 : 0;
     }
-    return true;
   }
 };
 
@@ -330,78 +344,83 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issue
-      if (lane == 0) {
-        uint32_t kv = 0, sn[2] = {0, 0}, in[2] = {0, 0};  // K and V tiles, S products, items
-        bool ok = true;
-        uint32_t k_at = 0, v_at = 0;
-        auto wait_kv = [&](uint32_t x, unsigned code) {
-          return mbar_wait(kv_full((int)(x % L::STAGES)), (x / L::STAGES) & 1, abort, st, code);
-        };
-        auto product_s = [&](int q) {
-          tc_fence_after();
-          // a descriptor's low bits are the address / 16: the steps along d are added to it
-          const uint64_t qd = umma_desc_kmajor(sb + L::OFF_Q + q * L::TILE, 128);
-          const uint64_t kd = umma_desc_kmajor(sb + L::OFF_KV + (k_at % L::STAGES) * L::TILE, 128);
+      // The whole warp runs the loops on warp-uniform values and one elected lane issues: descriptors then live in
+      // uniform registers.  (Run by one lane alone, the register moves of each product cost more than the product.)
+      // A wait that gives up is not looked at: the later ones return at once, and every address stays in bounds.
+      const uint32_t tm = uniform(tmem);
+      const int total = (int)uniform((uint32_t)items.total);
+      uint32_t ks = 0, kph = 0;         // stage of the next K tile (its V tile is the one after) and the parity of its use
+      uint32_t sp[2] = {0, 0}, ip[2] = {0, 0};  // parities: softmax results, items of each query tile
+      auto next_stage = [&]() {
+        ks += 2;
+        if (ks == (uint32_t)L::STAGES) ks = 0, kph ^= 1u;
+      };
+      auto product_s = [&](int q, uint32_t stage, bool q_last) {
+        // a descriptor's low bits are the address / 16: the steps along d are added to it
+        const uint64_t qd = umma_desc_kmajor(sb + L::OFF_Q + q * L::TILE, 128);
+        const uint64_t kd = umma_desc_kmajor(sb + L::OFF_KV + stage * L::TILE, 128);
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * L::CHUNK + (ks & 3) * 32) / 16;
-            mma_bf16_ss(tmem + q * 128, qd + off, kd + off, IDESC_S, ks > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * L::CHUNK + (k & 3) * 32) / 16;
+            mma_bf16_ss(tm + q * 128, qd + off, kd + off, IDESC_S, k > 0);
           }
           umma_commit(s_full(q));
-        };
-        for (int r = 0; ok && items.get(r, it); ++r) {
-          const int n = it.n_max();
-          k_at = kv;
-          ok = mbar_wait(q_full(0), in[0] & 1, abort, st, 0xD10) && wait_kv(k_at, 0xD11);
-          if (!ok) break;
-          product_s(0);
-          if (it.n[0] == 1) umma_commit(q_empty(0));
-          if (it.n[1]) {
-            if (!(ok = mbar_wait(q_full(1), in[1] & 1, abort, st, 0xD12))) break;
-            product_s(1);
-            if (it.n[1] == 1) umma_commit(q_empty(1));
-          }
-          umma_commit(kv_empty((int)(k_at % L::STAGES)));
-          for (int j = 0; ok && j < n; ++j) {
-            v_at = kv + 1;
-            k_at = kv + 2;
-            if (!(ok = wait_kv(v_at, 0xD13) && mbar_wait(v_ok((int)(v_at % L::STAGES)), (v_at / L::STAGES) & 1, abort, st,
-                                                         0xD14)))
-              break;
+          if (q_last) umma_commit(q_empty(q));
+        }
+      };
+      for (int r = 0; items.index(r) < total; ++r) {
+        items.load(items.index(r), it);
+        const int n0 = (int)uniform((uint32_t)it.n[0]), n1 = (int)uniform((uint32_t)it.n[1]), n = max(n0, n1);
+        mbar_wait(q_full(0), ip[0], abort, st, 0xD10);
+        mbar_wait(kv_full(ks), kph, abort, st, 0xD11);
+        tc_fence_after();
+        product_s(0, ks, n0 == 1);
+        if (n1) {
+          mbar_wait(q_full(1), ip[1], abort, st, 0xD12);
+          tc_fence_after();
+          product_s(1, ks, n1 == 1);
+        }
+        if (elect_one()) umma_commit(kv_empty(ks));
+        for (int j = 0; j < n; ++j) {
+          const uint32_t vs = ks + 1, vph = kph;
+          next_stage();  // the K tile of j + 1
+          mbar_wait(kv_full(vs), vph, abort, st, 0xD13);
+          mbar_wait(v_ok(vs), vph, abort, st, 0xD14);
+          const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + vs * L::TILE, L::CHUNK);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              if (j < it.n[q]) {
-                if (j == 0 && !(ok = mbar_wait(o_empty(q), (in[q] & 1) ^ 1, abort, st, 0xD15))) break;
-                if (!(ok = mbar_wait(p_full(q), sn[q] & 1, abort, st, 0xD16))) break;
-                ++sn[q];
-                tc_fence_after();
-                const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + (v_at % L::STAGES) * L::TILE, L::CHUNK);
+          for (int q = 0; q < 2; ++q) {
+            const int nq = q ? n1 : n0;
+            if (j < nq) {
+              if (j == 0) mbar_wait(o_empty(q), ip[q] ^ 1u, abort, st, 0xD15);
+              mbar_wait(p_full(q), sp[q], abort, st, 0xD16);
+              sp[q] ^= 1u;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kKeysT / 16; ++ks)  // keys 16 ks ..: half ks / 4, packed from column 64 half on
-                  mma_bf16_ts(tmem + L::TMEM_O + q * 128, tmem + q * 128 + 64 * (ks >> 2) + 8 * (ks & 3),
-                              vd + ks * (16 * 128 / 16), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+                for (int k = 0; k < kKeysT / 16; ++k)  // keys 16 k ..: half k / 4, packed from column 64 half on
+                  mma_bf16_ts(tm + L::TMEM_O + q * 128, tm + q * 128 + 64 * (k >> 2) + 8 * (k & 3),
+                              vd + k * (16 * 128 / 16), IDESC_PV, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(pv_done(q));
-                if (j + 1 == it.n[q]) {
-                  umma_commit(o_full(q));
-                  ++in[q];
-                }
+                if (j + 1 == nq) umma_commit(o_full(q));
               }
-              if (j + 1 < it.n[q]) {
-                if (!(ok = wait_kv(k_at, 0xD17))) break;
-                product_s(q);
-                if (j + 2 == it.n[q]) umma_commit(q_empty(q));
-              }
+              if (j + 1 == nq) ip[q] ^= 1u;
             }
-            if (!ok) break;
-            umma_commit(kv_empty((int)(v_at % L::STAGES)));
-            if (j + 1 < n) umma_commit(kv_empty((int)(k_at % L::STAGES)));
-            kv += 2;
+            if (j + 1 < nq) {
+              mbar_wait(kv_full(ks), kph, abort, st, 0xD17);
+              tc_fence_after();
+              product_s(q, ks, j + 2 == nq);
+            }
+          }
+          if (elect_one()) {
+            umma_commit(kv_empty(vs));
+            if (j + 1 < n) umma_commit(kv_empty(ks));
           }
         }
-        if (!ok) {  // the products in flight end before TMEM is released
-          umma_commit(drain);
-          mbar_wait(drain, 0, nullptr, st, 0xDF3);
-        }
+      }
+      if (*abort) {  // the products in flight end before TMEM is released
+        if (elect_one()) umma_commit(drain);
+        mbar_wait(drain, 0, nullptr, st, 0xDF3);
       }
     } else {
       // ------------------------------------------------------------ guard: rows 64 (warp - kWarpGuard) .. + 63 of V
