@@ -116,11 +116,13 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // lazy: O and the row sum are rescaled only when a row's maximum has grown by
 // more than 2^8, so P stays below 256 (its bf16 rounding is relative, so the
 // factor costs no precision) and the rescale of O in TMEM is rare.
-// Warpgroups: 0 and 1 the softmax of query tile 0, 2 and 3 of query tile 1 (a
-// row is two threads', 64 keys each, which exchange their maxima through shared
-// memory: a tile's softmax has to end before the tensor cores run out of the
-// other tile's products), 4 the output (O / l, lse), 5 one warp each for the TMA
-// loads, the MMA issue, and two guard warps.
+// Warpgroups: 0 to 3 the softmax, of query tile 0 and 1 in turn: warpgroup h has
+// keys 32 h .. + 31 of every row, and the four threads of a row exchange their
+// maxima through shared memory.  (A tile's softmax lies between its S and its
+// P V, so what counts is how long one takes: with two warpgroups for each tile
+// it took 1670 cycles of 64 exponentials a thread against 1024 cycles of
+// products.)  4 the output (O / l, lse), 5 one warp each for the TMA loads, the
+// MMA issue, and two guard warps.
 //
 // The guard warps make the masked places of V harmless, because a weight of 0
 // times a NaN or an infinity would not be 0 on the tensor cores: in the key
@@ -129,8 +131,6 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // adds the latter to the rows that do see them.
 constexpr int kRowsT = 128, kKeysT = 128;
 constexpr int kThreadsA = 768;
-constexpr uint32_t kRegsSoft = 96, kRegsEpi = 48, kRegsLoad = 48;
-static_assert(512 * kRegsSoft + 128 * kRegsEpi + 128 * kRegsLoad <= kThreadsA * 80, "the registers of the launch");
 constexpr int kWarpEpi = 16, kWarpLoad = 20, kWarpMma = 21, kWarpGuard = 22;
 constexpr float kLazy = 8.0f;
 constexpr int kPoisonSlots = 8;
@@ -143,17 +143,13 @@ struct Layout {
   static constexpr int STAGES = D == 128 ? 4 : 8;    // K and V tiles in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_ST = OFF_KV + STAGES * TILE;  // each row's (m, l), two halves' l: [2 tiles][128] x 16 bytes
-  static constexpr int OFF_MX = OFF_ST + 2 * 128 * 16;   // exchange of row maxima: [key tile parity][2 tiles][2 halves][128]
-  static constexpr int OFF_BAR = OFF_MX + 2 * 2 * 2 * 128 * 4;
+  static constexpr int OFF_ST = OFF_KV + STAGES * TILE;  // each row's sums (four parts): [2 tiles][128] x 16 bytes
+  static constexpr int OFF_MM = OFF_ST + 2 * 128 * 16;   // each row's maximum: [2 tiles][128]
+  static constexpr int OFF_MX = OFF_MM + 2 * 128 * 4;    // exchange of row maxima, two buffers: [2][128] x 16 bytes
+  static constexpr int OFF_BAR = OFF_MX + 2 * 128 * 16;
   static constexpr int SMEM = 1024 + OFF_BAR + 512;
   static constexpr uint32_t TMEM_O = 256;            // S / P of tile q at 128 q, O of tile q at 256 + 128 q
 };
-
-template <uint32_t R>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R)); }
-template <uint32_t R>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                             uint32_t bar) {
@@ -175,8 +171,8 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
-// The two warps that hold a row quarter's halves meet (64 threads, one of 8 named barriers).
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
+// The four warps that hold a quarter of the rows meet (a named barrier each).
+__device__ __forceinline__ void quarter_sync(int quarter) { asm volatile("bar.sync %0, 128;\n" ::"r"(1 + quarter) : "memory"); }
 __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
 }
@@ -245,16 +241,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   auto q_full = [&](int q) { return bar + 8u * (B0 + q); };              // TMA -> MMA
   auto q_empty = [&](int q) { return bar + 8u * (B0 + 2 + q); };         // MMA (commit) -> TMA
   auto s_full = [&](int q) { return bar + 8u * (B0 + 4 + q); };          // MMA (commit) -> softmax
-  auto p_full = [&](int q) { return bar + 8u * (B0 + 6 + q); };          // softmax (8 warps) -> MMA
+  auto p_full = [&](int q) { return bar + 8u * (B0 + 6 + q); };          // softmax (16 warps) -> MMA
   auto pv_done = [&](int q) { return bar + 8u * (B0 + 8 + q); };         // MMA (commit) -> softmax
   auto o_full = [&](int q) { return bar + 8u * (B0 + 10 + q); };         // MMA (commit) -> output
   auto o_empty = [&](int q) { return bar + 8u * (B0 + 12 + q); };        // output (4 warps) -> MMA, softmax
-  auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (8 warps) -> output
+  auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (16 warps) -> output
   // V tiles alone, which sit in the odd stages; one a stage, so that the guard cannot be two phases ahead
   auto v_ok = [&](int i) { return bar + 8u * (B0 + 16 + i / 2); };       // guard (2 warps) -> MMA
   const uint32_t drain = bar + 8u * (B0 + 16 + L::STAGES / 2);
   static_assert(L::STAGES % 2 == 0 && 8 * (B0 + 17 + L::STAGES / 2) <= 512, "K and V alternate; barriers fit");
   float4* ml_s = reinterpret_cast<float4*>(sm + L::OFF_ST);
+  float* mm_s = reinterpret_cast<float*>(sm + L::OFF_MM);
   float* mx_s = reinterpret_cast<float*>(sm + L::OFF_MX);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -266,11 +263,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
       mbar_init(q_full(q), 1);
       mbar_init(q_empty(q), 1);
       mbar_init(s_full(q), 1);
-      mbar_init(p_full(q), 8);
+      mbar_init(p_full(q), 16);
       mbar_init(pv_done(q), 1);
       mbar_init(o_full(q), 1);
       mbar_init(o_empty(q), 4);
-      mbar_init(ml_full(q), 8);
+      mbar_init(ml_full(q), 16);
     }
     for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_ok(i), 2);
     mbar_init(drain, 1);
@@ -300,7 +297,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   Item it;
 
   if (warp >= kWarpLoad) {
-    regs_dec<kRegsLoad>();
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA
       if (lane == 0) {
@@ -398,8 +394,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kKeysT / 16; ++k)  // keys 16 k ..: half k / 4, packed from column 64 half on
-                  mma_bf16_ts(tm + L::TMEM_O + q * 128, tm + q * 128 + 64 * (k >> 2) + 8 * (k & 3),
+                for (int k = 0; k < kKeysT / 16; ++k)  // keys 16 k ..: part k / 2, packed from column 32 part on
+                  mma_bf16_ts(tm + L::TMEM_O + q * 128, tm + q * 128 + 32 * (k >> 1) + 8 * (k & 1),
                               vd + k * (16 * 128 / 16), IDESC_PV, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(pv_done(q));
                 if (j + 1 == nq) umma_commit(o_full(q));
@@ -468,7 +464,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
       }
     }
   } else if (warp >= kWarpEpi) {
-    regs_dec<kRegsEpi>();
     // ------------------------------------------------------------ output: a thread per row
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const int pos = row / GS, hh = row % GS;
@@ -483,8 +478,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         if (!ok) break;
         ++in[q];
         tc_fence_after();
-        const float4 ml = ml_s[q * 128 + row];  // m, the halves' sums
-        const float sum = ml.y + ml.z;
+        const float4 ml = ml_s[q * 128 + row];
+        const float m = mm_s[q * 128 + row], sum = (ml.x + ml.y) + (ml.z + ml.w);
         const int t = it.t0 + q * PT + pos;
         const bool live = t < it.len;
         const bool bad = poison[r % kPoisonSlots] == r + 1;
@@ -524,126 +519,110 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty(q));
-        if (live) lse[(int64_t)h * N + grow] = (ml.x + lg2_approx(sum)) * 0.69314718055994530942f;
+        if (live) lse[(int64_t)h * N + grow] = (m + lg2_approx(sum)) * 0.69314718055994530942f;
       }
     }
   } else {
-    regs_inc<kRegsSoft>();
-    // ------------------------------------------------------------ softmax of query tile q, keys 64 half .. + 63
-    constexpr int HK = kKeysT / 2;
-    const int q = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t scol = tmem + lane_base + q * 128 + half * HK;
-    const uint32_t ocol = tmem + lane_base + L::TMEM_O + q * 128 + half * (D / 2);
-    const int pair = 1 + q * 4 + quarter;
-    float* mx_own = mx_s + (q * 2 + half) * 128 + row;
-    const float* mx_other = mx_s + (q * 2 + (half ^ 1)) * 128 + row;
+    // ------------------------------------------------------------ softmax: keys 32 part .. + 31 of both query tiles
+    constexpr int PK = kKeysT / 4;
+    const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t scol0 = tmem + ((uint32_t)(quarter * 32) << 16) + part * PK;
+    const uint32_t ocol0 = tmem + ((uint32_t)(quarter * 32) << 16) + L::TMEM_O + part * (D / 4);
     const float kInf = __int_as_float(0x7f800000);
-    uint32_t sn = 0, in = 0;  // S products and items of this tile so far
-    bool ok = true;
+    const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
+    uint32_t sn[2] = {0, 0}, in[2] = {0, 0}, ex = 0;  // S products and items of each tile so far; exchanges
+    // (A wait that gave up is not looked at: the later ones return at once, and the warps of a quarter stay in step.)
     for (int r = 0; items.get(r, it); ++r) {
-      const int n = it.n[q];
-      if (n == 0) continue;
-      const int t = min(it.t0 + q * PT + row / GS, it.len - 1);  // rows past the sequence repeat its last one
-      float m = -kInf;
+      const int n = it.n_max();
+      const int t0 = min(it.t0 + row / GS, it.len - 1), t1 = min(it.t0 + PT + row / GS, it.len - 1);  // past it: the last row
+      float m[2] = {-kInf, -kInf};
       uint64_t l2[2] = {0, 0};
-      // After a wait that gave up the warps of a pair go on to meet, without waiting or computing, until the end.
       for (int j = 0; j < n; ++j) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(s_full(q), sn & 1, abort, st, 0xD40));
-        uint32_t x[2][32];
-        float mc = -kInf;
-        if (ok) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (j >= it.n[q]) continue;
+          mbar_wait(s_full(q), sn[q] & 1, abort, st, 0xD40);
+          __syncwarp();
           tc_fence_after();
-          tmem_ld_x32(scol, x[0]);
-          tmem_ld_x32(scol + 32, x[1]);
+          uint32_t x[32];
+          tmem_ld_x32(scol0 + q * 128, x);
           tmem_ld_wait();
-          reg_fence32(x[0]);
-          reg_fence32(x[1]);
-          const int lim = t - j * kKeysT - half * HK;  // last visible column
-          if (__any_sync(0xffffffffu, lim < HK - 1)) {
+          reg_fence32(x);
+          const int lim = (q ? t1 : t0) - j * kKeysT - part * PK;  // last visible column
+          if (__any_sync(0xffffffffu, lim < PK - 1)) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c * 32 + e > lim) x[c][e] = 0xff800000u;
+            for (int e = 0; e < 32; ++e)
+              if (e > lim) x[e] = 0xff800000u;
           }
           float m4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              m4[2 * c] = max3(m4[2 * c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-              m4[2 * c + 1] = max3(m4[2 * c + 1], __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
-            }
-          }
-          mc = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-        }
-        // two buffers: who writes one again has met the other warp since it was read
-        mx_own[(sn & 1) * 512] = mc;
-        pair_sync(pair);
-        const float mt = fmaxf(mc, mx_other[(sn & 1) * 512]) * scale_log2;
-        if (!ok) continue;
-        const bool grow = mt > m + kLazy;  // both halves of a row decide alike
-        if (__any_sync(0xffffffffu, grow)) {
-          const float alpha = !grow ? 1.f : ex2_approx(m - mt);  // 2^-inf = 0 at the first tile
-          if (grow) {
-            m = mt;
+          for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          // two buffers: who writes one again has met the other warps since they read it
+          float* mx = mx_s + ((ex & 1) * 128 + row) * 4;
+          ++ex;
+          mx[part] = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+          quarter_sync(quarter);
+          const float4 mo = *reinterpret_cast<const float4*>(mx);
+          const float mt = fmaxf(max3(mo.x, mo.y, mo.z), mo.w) * scale_log2;
+          const bool grow = mt > m[q] + kLazy;  // the threads of a row decide alike
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = !grow ? 1.f : ex2_approx(m[q] - mt);  // 2^-inf = 0 at the first tile
+            if (grow) m[q] = mt;
             float a, b;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              f2_unpack(l2[i], a, b);
-              l2[i] = f2_pack(a * alpha, b * alpha);
-            }
-          }
-          if (j > 0) {  // O holds the products up to tile j - 1; this half's columns of it
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done(q), (sn - 1) & 1, abort, st, 0xD41)))) continue;
-            tc_fence_after();
+            f2_unpack(l2[q], a, b);
+            l2[q] = f2_pack(a * alpha, b * alpha);
+            if (j > 0) {  // O holds the products up to tile j - 1; this part's columns of it
+              mbar_wait(pv_done(q), (sn[q] - 1) & 1, abort, st, 0xD41);
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[16];
-              tmem_ld_x16(ocol + c * 16, o);
-              tmem_ld_wait();
-              reg_fence16(o);
+              for (int c = 0; c < D / 64; ++c) {
+                uint32_t o[16];
+                tmem_ld_x16(ocol0 + q * 128 + c * 16, o);
+                tmem_ld_wait();
+                reg_fence16(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st_x16(ocol + c * 16, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st_x16(ocol0 + q * 128 + c * 16, o);
+              }
             }
           }
-        }
-        const float mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
-        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-mz, -mz);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+          const float mz = m[q] == -kInf ? 0.f : m[q];  // scores of -inf alone weigh 0
+          const uint64_t nm2 = f2_pack(-mz, -mz);
           uint32_t pk[16];
+          uint64_t ls[2] = {l2[q], 0};
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float a0, a1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2), a0, a1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nm2), a0, a1);
             a0 = ex2_approx(a0);
             a1 = ex2_approx(a1);
-            l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(a0, a1));
+            ls[(e >> 1) & 1] = f2_add(ls[(e >> 1) & 1], f2_pack(a0, a1));
             pk[e >> 1] = pack_bf16x2(a0, a1);
           }
-          tmem_st_x16(scol + c * 16, pk);  // this half's keys 32 c .. -> its packed columns 16 c ..
+          l2[q] = f2_add(ls[0], ls[1]);
+          tmem_st_x16(scol0 + q * 128, pk);  // keys of this part -> its first 16 columns, packed
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(q));
+          ++sn[q];
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(q));
-        ++sn;
       }
-      if (!ok) continue;
-      // the output warps have read the item before's (m, l) once they gave O back
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_empty(q), (in & 1) ^ 1, abort, st, 0xD42)))) continue;
-      ++in;
-      float a, b, c, d;
-      f2_unpack(l2[0], a, b);
-      f2_unpack(l2[1], c, d);
-      float* ml = reinterpret_cast<float*>(ml_s + q * 128 + row);
-      if (half == 0) ml[0] = m;
-      ml[1 + half] = (a + b) + (c + d);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ml_full(q));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (it.n[q] == 0) continue;
+        // the output warps have read the item before's (m, l) once they gave O back
+        mbar_wait(o_empty(q), (in[q] & 1) ^ 1, abort, st, 0xD42);
+        __syncwarp();
+        ++in[q];
+        float a, b;
+        f2_unpack(l2[q], a, b);
+        reinterpret_cast<float*>(ml_s + q * 128 + row)[part] = a + b;
+        if (part == 0) mm_s[q * 128 + row] = m[q];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full(q));
+      }
     }
   }
 
