@@ -14,6 +14,8 @@ from . import msa as _c
 
 
 def _check_bf16(name, t, shape):
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA bfloat16 tensor" % name)
     if tuple(t.shape) != tuple(shape):
@@ -90,6 +92,8 @@ class MsaDecode:
 
 
 def _check_tensor(name, t, dtype, shape):
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
     if tuple(t.shape) != tuple(shape):

@@ -122,12 +122,13 @@ msa_status_t check_shape(const msa_shape_t* s) {
 }
 
 // Validates the workspace and clears its first `clear` bytes (the status header
-// and, for calls that keep completion counters there, those counters).
+// and, for calls that keep completion counters there, those counters; 0 for
+// calls whose first kernel is a single CTA, which clears the status itself).
 msa_status_t begin(void* ws, size_t ws_bytes, size_t need, cudaStream_t s, size_t clear = kHeader) {
   if (!ws) return MSA_ERR_INVALID_ARGUMENT;
   if (((uintptr_t)ws & 255u) != 0) return MSA_ERR_INVALID_ARGUMENT;
   if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
-  if (cudaMemsetAsync(ws, 0, clear, s) != cudaSuccess) return MSA_ERR_CUDA;
+  if (clear && cudaMemsetAsync(ws, 0, clear, s) != cudaSuccess) return MSA_ERR_CUDA;
   return MSA_OK;
 }
 
@@ -516,7 +517,7 @@ msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* 
     return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
   const msa::DensePlan p = msa::dense_plan(N, S, H_q, H_kv, d);
-  st = begin(workspace, workspace_bytes, kHeader + msa::dense_scratch_bytes(p), s);
+  st = begin(workspace, workspace_bytes, kHeader + msa::dense_scratch_bytes(p), s, p.own ? kHeader : 0);
   if (st != MSA_OK) return st;
   return finish(msa::launch_dense_prefill(q, k, v, cu_seqlens, p, scale, out, lse, (char*)workspace + kHeader,
                                           (msa::DeviceStatus*)workspace, s));
@@ -717,9 +718,10 @@ msa_status_t msa_pages_reserve(const msa_pages_t* pages, const int32_t* seqs, co
   if (st != MSA_OK) return st;
   if (bad_list(seqs, n) || bad_list(new_len, n)) return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, kHeader, s);
+  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, n), s, n > 0 ? 0 : kHeader);
   if (st != MSA_OK) return st;
-  return finish(msa::launch_pages_reserve(pages_view(pages), seqs, new_len, n, (msa::DeviceStatus*)workspace, s));
+  return finish(msa::launch_pages_reserve(pages_view(pages), seqs, new_len, n, (char*)workspace + kHeader,
+                                          (msa::DeviceStatus*)workspace, s));
 }
 
 msa_status_t msa_pages_fork(const msa_pages_t* pages, const int32_t* src, const int32_t* dst, int n,
@@ -732,7 +734,7 @@ msa_status_t msa_pages_fork(const msa_pages_t* pages, const int32_t* src, const 
   if (st != MSA_OK) return st;
   if (bad_list(src, n) || bad_list(dst, n)) return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, n), s);
+  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, n), s, n > 0 ? 0 : kHeader);
   if (st != MSA_OK) return st;
   return finish(msa::launch_pages_fork(pages_view(pages), src, dst, n, pp, (char*)workspace + kHeader,
                                        (msa::DeviceStatus*)workspace, s));
@@ -758,7 +760,7 @@ msa_status_t msa_pages_compact(const msa_pages_t* pages, const msa_page_pool_t* 
   if (st != MSA_OK) return st;
   if (((uintptr_t)page_map | (uintptr_t)n_live) & 3u) return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, 0), s);
+  st = begin(workspace, workspace_bytes, msa_pages_workspace(pages, 0), s, 0);
   if (st != MSA_OK) return st;
   return finish(msa::launch_pages_compact(pages_view(pages), pp, page_map, n_live, (char*)workspace + kHeader,
                                           (msa::DeviceStatus*)workspace, s));

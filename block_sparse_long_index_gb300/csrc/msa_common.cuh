@@ -30,6 +30,15 @@ __device__ __forceinline__ void raise_error(DeviceStatus* st, unsigned int flag,
   if (old == 0) atomicExch(&st->first_code, code);
 }
 
+// For the single CTA that begins a call: no error yet (every thread of it calls this).
+__device__ __forceinline__ void clear_errors(DeviceStatus* st) {
+  if (threadIdx.x == 0) {
+    st->flags = 0u;
+    st->first_code = 0u;
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ int64_t CacheMap::row(int64_t seq, int64_t key, DeviceStatus* st) const {
   const int64_t lp = key / page;
   int32_t pp = __ldg(table + seq * max_pages + lp);

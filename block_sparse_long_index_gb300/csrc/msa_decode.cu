@@ -425,49 +425,59 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
       __syncthreads();
     }
     auto row_off = [&](int j) -> int64_t { return (PAGED ? krow_s[PAGED ? j : 0] : (int64_t)j) * kv_row; };
-    // V rows into shared memory (rows past nvis read as zero), every copy in flight at once
+    // K rows of this warp's keys as B fragments (key = column gq of n-tile nt); rows past nvis repeat a
+    // visible row and are masked below
+    uint4 kf[NT][NP];
     if constexpr (KV4) {
-      constexpr int W4 = D / 32;  // 16-byte pieces of a row's codes: 32 channels
-#pragma unroll 4
-      for (int i = tid; i < BK * W4; i += blockDim.x) {
-        const int j = i / W4, w = i % W4;
-        const bool in = j < nvis;
-        const int64_t hr = krow_s[in ? j : 0] * G + g;
-        const uint4 x = ldg_stream_16(pool.v_codes + hr * (D / 2) + 16 * w);
-        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(pool.v_scales + hr * 4);
+      // every read in flight before the first code is expanded: K's words, then V's 16-byte pieces (32 channels)
+      constexpr int W4 = D / 32, VT = BK * W4 / 128;  // pieces of a row; pieces of a thread
+      uint32_t kw[NT][NP], ksc[NT], vsc[VT];
+      uint4 vw[VT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int64_t hr = krow_s[min(warp * KPW + nt * 8 + gq, nvis - 1)] * G + g;
+        const uint32_t* kr = reinterpret_cast<const uint32_t*>(pool.k_codes + hr * (D / 2)) + tq;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) kw[nt][p] = __ldg(kr + 4 * p);
+        ksc[nt] = __ldg(reinterpret_cast<const uint32_t*>(pool.k_scales + hr * 4));
+      }
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        const int e = tid + 128 * i, j = e / W4, w = e % W4;
+        const int64_t hr = krow_s[j < nvis ? j : 0] * G + g;
+        vw[i] = ldg_stream_16(pool.v_codes + hr * (D / 2) + 16 * w);
+        vsc[i] = __ldg(reinterpret_cast<const uint32_t*>(pool.v_scales + hr * 4));
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {  // word 4p + tq: channels 32p + 8tq .. + 7, in group (4p + tq) / (d / 32)
+          const uint32_t s = kv4::scale_bf16((ksc[nt] >> (8 * ((4 * p + tq) / NP))) & 255u), s2 = s | (s << 16);
+          kf[nt][p] = kv4::expand8(kw[nt][p], s2, kv4::scale_bias(s2));
+        }
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {  // rows past nvis as zeros
+        const int e0 = tid + 128 * i, j = e0 / W4, w = e0 % W4;
+        const uint32_t words[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c8 = 4 * w + e;
-          const uint32_t s = kv4::scale_bf16((sc >> (8 * (c8 / (C8 / 4)))) & 255u), s2 = s | (s << 16);
+          const uint32_t s = kv4::scale_bf16((vsc[i] >> (8 * (c8 / (C8 / 4)))) & 255u), s2 = s | (s << 16);
           const uint4 y = kv4::expand8(words[e], s2, kv4::scale_bias(s2));
-          *reinterpret_cast<uint4*>(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8) = in ? y : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8) = j < nvis ? y : make_uint4(0u, 0u, 0u, 0u);
         }
       }
     } else {
+      // V rows into shared memory (rows past nvis read as zero), every copy in flight at once
       for (int i = tid; i < BK * C8; i += blockDim.x) {
         const int j = i / C8, c8 = i % C8;
         const bool in = j < nvis;
         cp_async_16(v_s + j * D + (c8 ^ (j & (C8 - 1))) * 8, Vb + row_off(in ? j : 0) + c8 * 8, in ? 16 : 0);
       }
       cp_async_commit();
-    }
-    // K rows of this warp's keys as B fragments (key = column gq of n-tile nt); rows past nvis repeat a
-    // visible row and are masked below
-    uint4 kf[NT][NP];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int j = min(warp * KPW + nt * 8 + gq, nvis - 1);
-      if constexpr (KV4) {
-        const int64_t hr = krow_s[j] * G + g;
-        const uint32_t* kr = reinterpret_cast<const uint32_t*>(pool.k_codes + hr * (D / 2)) + tq;
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(pool.k_scales + hr * 4);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {  // word 4p + tq: channels 32p + 8tq .. + 7, in group (4p + tq) / (d / 32)
-          const uint32_t s = kv4::scale_bf16((sc >> (8 * ((4 * p + tq) / NP))) & 255u), s2 = s | (s << 16);
-          kf[nt][p] = kv4::expand8(__ldg(kr + 4 * p), s2, kv4::scale_bias(s2));
-        }
-      } else {
+      for (int nt = 0; nt < NT; ++nt) {
+        const int j = min(warp * KPW + nt * 8 + gq, nvis - 1);
         const uint16_t* kr = Kb + row_off(j) + 8 * tq;
 #pragma unroll
         for (int p = 0; p < NP; ++p) kf[nt][p] = ldg_stream_16(kr + 32 * p);

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
   griddep_launch_dependents();  // the attention's CTAs may set up meanwhile; they wait for this grid's end
+  clear_errors(st);
   int bad = 0;
   for (int s = tid; s <= S; s += kPlanThreads) {
     const int32_t c = cu[s];
@@ -134,6 +135,7 @@ constexpr int kThreadsA = 768;
 constexpr int kWarpEpi = 16, kWarpLoad = 20, kWarpMma = 21, kWarpGuard = 22;
 constexpr float kLazy = 8.0f;
 constexpr int kPoisonSlots = 8;
+constexpr int kOwnRounds = 4;  // rounds that a CTA may plan for itself
 
 template <int D>
 struct Layout {
@@ -193,7 +195,8 @@ struct Item {
   __device__ __forceinline__ int n_max() const { return max(n[0], n[1]); }
 };
 struct Items {
-  const int4* items;
+  const int4* items;    // the planned list, or (own) this CTA's items by round
+  bool own;
   int total, H_kv, PT;  // items x groups, groups, positions of a query tile
   __device__ __forceinline__ int index(int round) const {
     const int b = (int)blockIdx.x, n = (int)gridDim.x;
@@ -202,11 +205,12 @@ struct Items {
   __device__ __forceinline__ bool get(int round, Item& it) const {
     const int i = index(round);
     if (i >= total) return false;
-    load(i, it);
+    load(round, it);
     return true;
   }
-  __device__ __forceinline__ void load(int i, Item& it) const {
-    const int4 x = items[i / H_kv];
+  __device__ __forceinline__ void load(int round, Item& it) const {
+    const int i = index(round);
+    const int4 x = items[own ? round : i / H_kv];
     it.g = i % H_kv;
     it.row0 = x.y;
     it.t0 = x.x - x.y;
@@ -219,11 +223,43 @@ struct Items {
   }
 };
 
+// The plan's list worked out by one warp for its CTA's few rounds, where S <= 32 (a lane a sequence): item i is of the
+// largest depth d with more than i items at depth d or deeper.  Sequences of one depth go by their number.
+__device__ __forceinline__ void plan_own(const int32_t* cu, int S, int64_t N, int P, int H_kv, int4* own, int* total,
+                                         DeviceStatus* st) {
+  const int lane = threadIdx.x & 31;
+  const int32_t c0 = lane < S ? cu[lane] : 0, c1 = lane < S ? cu[lane + 1] : 0;
+  const bool bad = lane < S && (c0 < 0 || c1 < c0 || (int64_t)c1 > N || (lane == 0 && c0 != 0));
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) {
+      if (blockIdx.x == 0) raise_error(st, kErrBadIndex, 5u);
+      *total = 0;
+    }
+    return;
+  }
+  const int n = (c1 - c0 + P - 1) / P, deepest = __reduce_max_sync(0xffffffffu, n);
+  const int items = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) *total = items * H_kv;
+  for (int r = 0; r < kOwnRounds; ++r) {
+    const int at = r * (int)gridDim.x + ((r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (at >= items * H_kv) break;
+    const int i = at / H_kv;
+    int lo = 0, hi = deepest;  // the number of items at depth lo or deeper exceeds i, at hi it does not
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__reduce_add_sync(0xffffffffu, max(n - mid, 0)) > i) lo = mid; else hi = mid;
+    }
+    const int rank = i - __reduce_add_sync(0xffffffffu, max(n - lo - 1, 0));
+    const unsigned who = __ballot_sync(0xffffffffu, n > lo);
+    if (n > lo && __popc(who & ((1u << lane) - 1u)) == rank) own[r] = make_int4(c0 + lo * P, c0, c1, 0);
+  }
+}
+
 template <int D, int GS>
 __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ v, int64_t N, int H_q, int H_kv,
-    float scale_log2, DensePlanScratch w, uint16_t* __restrict__ out, float* __restrict__ lse, DeviceStatus* st) {
+    const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ v, const int32_t* __restrict__ cu, int own_S,
+    int64_t N, int H_q, int H_kv, float scale_log2, DensePlanScratch w, uint16_t* __restrict__ out, float* __restrict__ lse, DeviceStatus* st) {
   using L = Layout<D>;
   constexpr int PT = kRowsT / GS;
   constexpr uint32_t IDESC_S = idesc_bf16_f32(kRowsT, kKeysT);
@@ -233,6 +269,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   const uint32_t sb = smem_u32(sm);
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int4 own_items[kOwnRounds];
+  __shared__ int own_total;
   __shared__ int poison[kPoisonSlots];  // 1 + the round whose V tiles held values that are not finite
   const uint32_t bar = sb + L::OFF_BAR;
   auto kv_full = [&](int i) { return bar + 8u * i; };                    // TMA -> MMA, guard
@@ -284,14 +322,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  if (own_S && warp == kWarpGuard) plan_own(cu, own_S, N, 2 * PT, H_kv, own_items, &own_total, st);
   __syncthreads();
   tc_fence_after();
-  griddep_wait();  // the plan
+  griddep_wait();  // the plan, where there is one
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &abort_flag;
   Items items;
-  items.items = w.items;
-  items.total = *w.n_items * H_kv;
+  items.own = own_S != 0;
+  items.items = own_S ? own_items : w.items;
+  items.total = own_S ? own_total : *w.n_items * H_kv;
   items.H_kv = H_kv;
   items.PT = PT;
   Item it;
@@ -366,7 +406,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         }
       };
       for (int r = 0; items.index(r) < total; ++r) {
-        items.load(items.index(r), it);
+        items.load(r, it);
         const int n0 = (int)uniform((uint32_t)it.n[0]), n1 = (int)uniform((uint32_t)it.n[1]), n = max(n0, n1);
         mbar_wait(q_full(0), ip[0], abort, st, 0xD10);
         mbar_wait(kv_full(ks), kph, abort, st, 0xD11);
@@ -634,8 +674,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
 }
 
 template <int D, int GS>
-cudaError_t launch_t(const void* q, const void* k, const void* v, const DensePlan& p, const DensePlanScratch& w,
-                     float scale, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
+cudaError_t launch_t(const void* q, const void* k, const void* v, const int32_t* cu, const DensePlan& p,
+                     const DensePlanScratch& w, float scale, void* out, float* lse, DeviceStatus* st, cudaStream_t s) {
   using L = Layout<D>;
   alignas(64) unsigned char tq[128], tk[128], tv[128];
   const uint64_t row = (uint64_t)D * 2;
@@ -659,8 +699,8 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const DensePla
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, *reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
-                            *reinterpret_cast<const CUtensorMap*>(tv), (const uint16_t*)v, p.N, p.H_q, p.H_kv,
-                            scale * 1.4426950408889634f, w, (uint16_t*)out, lse, st);
+                            *reinterpret_cast<const CUtensorMap*>(tv), (const uint16_t*)v, cu, p.own ? p.S : 0, p.N, p.H_q,
+                            p.H_kv, scale * 1.4426950408889634f, w, (uint16_t*)out, lse, st);
 }
 
 int64_t depths_of(int64_t N, int P) { return ceil_div(N, P); }
@@ -693,6 +733,7 @@ DensePlan dense_plan(int64_t N, int S, int H_q, int H_kv, int d) {
   p.P = 2 * kRowsT / (H_q / H_kv);
   // a sequence of n > 0 rows has ceil(n / P) <= n / P + 1 items
   p.max_items = N / p.P + (S < N ? S : N);
+  p.own = S <= 32 && p.max_items * H_kv <= (int64_t)kOwnRounds * num_sms();
   return p;
 }
 
@@ -702,15 +743,17 @@ cudaError_t launch_dense_prefill(const void* q, const void* k, const void* v, co
                                  float scale, void* out, float* lse, void* scratch, DeviceStatus* st, cudaStream_t s) {
   DensePlanScratch w;
   carve(p, (char*)scratch, &w);
-  dense_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, p.S, p.N, p.P, w, (int)depths_of(p.N, p.P), st);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  using Fn = cudaError_t (*)(const void*, const void*, const void*, const DensePlan&, const DensePlanScratch&, float,
+  if (!p.own) {
+    dense_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, p.S, p.N, p.P, w, (int)depths_of(p.N, p.P), st);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  using Fn = cudaError_t (*)(const void*, const void*, const void*, const int32_t*, const DensePlan&, const DensePlanScratch&, float,
                              void*, float*, DeviceStatus*, cudaStream_t);
   static const Fn table[2][4] = {{launch_t<64, 1>, launch_t<64, 2>, launch_t<64, 4>, launch_t<64, 8>},
                                  {launch_t<128, 1>, launch_t<128, 2>, launch_t<128, 4>, launch_t<128, 8>}};
   const int gs = p.H_q / p.H_kv;
-  return table[p.d == 128][gs == 1 ? 0 : gs == 2 ? 1 : gs == 4 ? 2 : 3](q, k, v, p, w, scale, out, lse, st, s);
+  return table[p.d == 128][gs == 1 ? 0 : gs == 2 ? 1 : gs == 4 ? 2 : 3](q, k, v, cu, p, w, scale, out, lse, st, s);
 }
 
 }  // namespace msa

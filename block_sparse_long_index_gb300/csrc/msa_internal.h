@@ -181,6 +181,7 @@ struct DensePlan {
   int S, H_q, H_kv, d;
   int P;              // positions per work item
   int64_t max_items;  // bound on the items of one group
+  bool own;           // few: every CTA plans its own items (the status is then cleared before)
 };
 #ifdef __CUDACC__
 struct DensePlanScratch {
@@ -222,8 +223,8 @@ struct PagePools {
   int n;
 };
 size_t pages_scratch_bytes(const Pages& p, int n);
-cudaError_t launch_pages_reserve(const Pages& p, const int32_t* seqs, const int32_t* new_len, int n, DeviceStatus* st,
-                                 cudaStream_t s);
+cudaError_t launch_pages_reserve(const Pages& p, const int32_t* seqs, const int32_t* new_len, int n, void* scratch,
+                                 DeviceStatus* st, cudaStream_t s);
 cudaError_t launch_pages_fork(const Pages& p, const int32_t* src, const int32_t* dst, int n, const PagePools& pools,
                               void* scratch, DeviceStatus* st, cudaStream_t s);
 cudaError_t launch_pages_free(const Pages& p, const int32_t* seqs, int n, DeviceStatus* st, cudaStream_t s);

@@ -278,44 +278,49 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
   __shared__ int64_t part[kDecWarps], found_before;
   __shared__ int found_seq;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t sum = 0;
-  for (int s = tid; s < B; s += kDecThreads) sum += units_of(ctx_len[s], cap);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) part[warp] = sum;
-  if (tid == 0) found_seq = B;
-  __syncthreads();
-  FlatSplit f;
-  f.total = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) f.total += part[w];
-  f.total *= n_hb;
-  f.quota = quota_of(f.total, gridDim.x, 2 * kDecWarps / HC);
-  const int64_t at = blockIdx.x * f.quota;
-  int64_t base = 0;
-  for (int s0 = 0; s0 < B; s0 += kDecThreads) {
-    const int s = s0 + tid;
-    const int64_t n = s < B ? units_of(ctx_len[s], cap) : 0;
+  // inclusive sums of n over the CTA, the CTA's sum added to `base`
+  auto scan = [&](int64_t n, int64_t& base) {
     int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    __syncthreads();  // part of the step before is no longer read
     if (lane == 31) part[warp] = incl;
     __syncthreads();
     int64_t off = base;
+#pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
-      if (w < warp) off += part[w];
-      base += part[w];
+      const int64_t x = part[w];
+      if (w < warp) off += x;
+      base += x;
     }
-    const int64_t lo = (off + incl - n) * n_hb, hi = (off + incl) * n_hb;
-    if (n > 0 && lo <= at && at < hi) {
+    return off + incl;
+  };
+  if (tid == 0) found_seq = B;
+  FlatSplit f;
+  f.total = 0;
+  int64_t n = tid < B ? units_of(ctx_len[tid], cap) : 0, incl = scan(n, f.total);
+  for (int s = kDecThreads + tid; s - tid < B; s += kDecThreads) {  // more sequences than threads: the sum first
+    __syncthreads();  // part is read
+    scan(s < B ? units_of(ctx_len[s], cap) : 0, f.total);
+  }
+  f.total *= n_hb;
+  f.quota = quota_of(f.total, gridDim.x, 2 * kDecWarps / HC);
+  const int64_t at = blockIdx.x * f.quota;
+  int64_t base = 0;
+  for (int s = tid;; s += kDecThreads) {
+    if (B > kDecThreads) {
+      n = s < B ? units_of(ctx_len[s], cap) : 0;
+      __syncthreads();  // part is read
+      incl = scan(n, base);
+    }
+    const int64_t lo = (incl - n) * n_hb;
+    if (n > 0 && lo <= at && at < incl * n_hb) {
       found_seq = s;
       found_before = lo;
     }
-    if (base * n_hb > at) break;  // uniform
+    if (B <= kDecThreads || s - tid + kDecThreads >= B || base * n_hb > at) break;  // uniform
   }
   __syncthreads();
   f.seq = found_seq;

@@ -22,8 +22,10 @@ struct PageScratch {
   int32_t* len;      // [n] fork: the source's length when the call began
   int32_t* last;     // [n] fork: the new last page (-1: none)
   int32_t* map;      // [n_pages] compact: new id of each page
+  int32_t* list;     // [n_pages] reserve: the free pages taken
 };
 
+// n > 0: reserve and fork with n entries; n = 0: compact.
 size_t carve(const Pages& p, int n, char* base, PageScratch* w) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -38,7 +40,7 @@ size_t carve(const Pages& p, int n, char* base, PageScratch* w) {
   s.to = (int32_t*)take(moves * 4);
   s.len = (int32_t*)take((size_t)n * 4);
   s.last = (int32_t*)take((size_t)n * 4);
-  s.map = (int32_t*)take(n > 0 ? 0 : (size_t)p.n_pages * 4);
+  s.map = s.list = (int32_t*)take((size_t)p.n_pages * 4);  // one or the other
   if (w) *w = s;
   return off;
 }
@@ -71,42 +73,38 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
 
 __device__ __forceinline__ int64_t pages_of(int64_t len, int page) { return (len + page - 1) / page; }
 
-// Whether an earlier entry of the call names the same sequence.
-__device__ __forceinline__ bool named_before(const int32_t* seqs, int i) {
-  for (int j = 0; j < i; ++j)
-    if (seqs[j] == seqs[i]) return true;
-  return false;
+// Whether an earlier entry of the call names the same sequence (`names`: the entries in shared memory).
+__device__ __forceinline__ bool named_before(const int* names, int i) {
+  bool hit = false;
+#pragma unroll 4
+  for (int j = 0; j < i; ++j) hit |= names[j] == names[i];
+  return hit;
 }
 
-// The lowest free pages: place(r, page) is called for the r-th one, r < need.  Every thread takes part;
-// returns how many of the `need` were found.
-template <typename F>
-__device__ __forceinline__ int take_free(const Pages& p, int need, int* warp_sums, F place) {
+// Lists the `need` lowest free pages in the scratch `list` (nothing else is changed, so a call that finds too few
+// can give up).  Every thread takes part; returns how many were found.
+__device__ __forceinline__ int list_free(const Pages& p, int need, int* warp_sums, int32_t* list) {
   int have = 0;
   for (int64_t b = 0; b < p.n_pages && have < need; b += kThreads * 4) {
     const int64_t i0 = b + threadIdx.x * 4;
     int32_t f[4];
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = i0 + j < p.n_pages ? p.refs[i0 + j] : 1;
-      n += f[j] == 0 ? 1 : 0;
-    }
+    for (int j = 0; j < 4; ++j) f[j] = i0 + j < p.n_pages ? p.refs[i0 + j] : 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) n += f[j] == 0 ? 1 : 0;
     int total;
     int r = have + block_scan(n, warp_sums, total) - n;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (f[j] == 0) {
-        if (r < need) place(r, (int32_t)(i0 + j));
+        if (r < need) list[r] = (int32_t)(i0 + j);
         ++r;
       }
     have += total;
   }
+  __syncthreads();  // the list is whole
   return min(have, need);
-}
-// The free pages without taking any, up to `need`.
-__device__ __forceinline__ int count_free(const Pages& p, int need, int* warp_sums) {
-  return take_free(p, need, warp_sums, [](int, int32_t) {});
 }
 
 // The entry whose run [pre[i], pre[i + 1]) holds r; pre has n + 1 values.
@@ -120,20 +118,25 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int r) {
 }
 
 __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(Pages p, const int32_t* __restrict__ seqs,
-                                                                 const int32_t* __restrict__ new_len, int n,
+                                                                 const int32_t* __restrict__ new_len, int n, PageScratch w,
                                                                  DeviceStatus* st) {
   __shared__ int warp_sums[32];
   __shared__ int64_t need_sums[32];
-  extern __shared__ int pre[];  // [n + 1] pages needed before each entry (where they are as many as there are pages)
+  extern __shared__ int dyn[];
+  int* names = dyn;          // [n]
+  int* pre = dyn + n;        // [n + 1] pages needed before each entry (where they are as many as there are pages)
   const int tid = threadIdx.x;
+  clear_errors(st);
+  for (int i = tid; i < n; i += kThreads) names[i] = seqs[i];
+  __syncthreads();
   int64_t carry = 0;
   int bad = 0;
   for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + tid;
     int64_t need = 0;
     if (i < n) {
-      const int32_t s = seqs[i], want = new_len[i];
-      bool ok = s >= 0 && s < p.n_seqs && !named_before(seqs, i);
+      const int32_t s = names[i], want = new_len[i];
+      bool ok = s >= 0 && s < p.n_seqs && !named_before(names, i);
       if (ok) {
         const int32_t len = p.ctx[s];
         ok = len >= 0 && want >= len && (int64_t)want <= p.max_pages * p.page;
@@ -151,19 +154,18 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(Pages p, const 
     if (tid == 0) raise_error(st, kErrBadIndex, 9u);
     return;
   }
-  if (carry > p.n_pages || count_free(p, (int)carry, warp_sums) < (int)carry) {  // uniform
+  if (carry > p.n_pages || list_free(p, (int)carry, warp_sums, w.list) < (int)carry) {  // uniform
     if (tid == 0) raise_error(st, kErrNoPages, 10u);
     return;
   }
-  __syncthreads();
-  take_free(p, (int)carry, warp_sums, [&](int r, int32_t page) {
+  for (int r = tid; r < (int)carry; r += kThreads) {
     const int i = owner_of(pre, n, r);
-    const int32_t s = seqs[i];
+    const int32_t s = names[i], page = w.list[r];
     p.table[(int64_t)s * p.max_pages + pages_of(p.ctx[s], p.page) + (r - pre[i])] = page;
     p.refs[page] = 1;
-  });
+  }
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads) p.ctx[seqs[i]] = new_len[i];
+  for (int i = tid; i < n; i += kThreads) p.ctx[names[i]] = new_len[i];
 }
 
 // Checks the entries and gives each one whose source ends inside a page a new last page.
@@ -171,28 +173,35 @@ __global__ void __launch_bounds__(kThreads) pages_fork_plan_kernel(Pages p, cons
                                                                    const int32_t* __restrict__ dst, int n, PageScratch w,
                                                                    DeviceStatus* st) {
   __shared__ int warp_sums[32];
-  extern __shared__ int pre[];
+  extern __shared__ int dyn[];
+  int* names = dyn;    // [n] dst
+  int* pre = dyn + n;  // [n + 1]
   const int tid = threadIdx.x;
+  griddep_launch_dependents();  // the copying grid waits for this one's end
+  clear_errors(st);
+  for (int i = tid; i < n; i += kThreads) names[i] = dst[i];
+  __syncthreads();
   int carry = 0, bad = 0;
   for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + tid;
     int need = 0;
     if (i < n) {
-      const int32_t s = src[i], d = dst[i];
-      bool ok = s >= 0 && s < p.n_seqs && d >= 0 && d < p.n_seqs && !named_before(dst, i) && p.ctx[d] == 0;
+      const int32_t s = src[i], d = names[i];
+      bool ok = s >= 0 && s < p.n_seqs && d >= 0 && d < p.n_seqs && !named_before(names, i);
+      int32_t len = 0;
       if (ok) {
-        const int32_t len = p.ctx[s];
-        ok = len >= 0 && (int64_t)len <= p.max_pages * p.page;
+        len = p.ctx[s];
+        ok = p.ctx[d] == 0 && len >= 0 && (int64_t)len <= p.max_pages * p.page;
         if (ok && len % p.page) {
           need = 1;
           const int32_t last = p.table[(int64_t)s * p.max_pages + len / p.page];
           ok = last >= 0 && (int64_t)last < p.n_pages;
-          w.from[i] = last;  // until the moves are listed
+          w.from[i] = last;
         }
       }
       if (!ok) bad = 1;
       w.last[i] = -1;
-      w.len[i] = ok ? p.ctx[s] : 0;
+      w.len[i] = ok ? len : 0;
     }
     int total;
     const int incl = block_scan(need, warp_sums, total);
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_plan_kernel(Pages p, cons
   }
   if (tid == 0) pre[n] = carry;
   bad = __syncthreads_or(bad);
-  const bool room = !bad && count_free(p, carry, warp_sums) == carry;
+  const bool room = !bad && list_free(p, carry, warp_sums, w.to) == carry;
   if (!room) {
     if (tid == 0) {
       raise_error(st, bad ? kErrBadIndex : kErrNoPages, 11u);
@@ -209,13 +218,11 @@ __global__ void __launch_bounds__(kThreads) pages_fork_plan_kernel(Pages p, cons
     }
     return;
   }
-  __syncthreads();
-  take_free(p, carry, warp_sums, [&](int r, int32_t page) {
-    const int i = owner_of(pre, n, r);
-    w.last[i] = page;
-    w.to[i] = page;
+  for (int r = tid; r < carry; r += kThreads) {
+    const int32_t page = w.to[r];
+    w.last[owner_of(pre, n, r)] = page;
     p.refs[page] = 1;
-  });
+  }
   if (tid == 0) *w.n_moves = n;  // entries without a new page are passed over by the copy (last < 0)
 }
 
@@ -251,6 +258,7 @@ __device__ __forceinline__ void copy_moves(const PagePools& pools, int64_t moves
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(Pages p, const int32_t* __restrict__ src,
                                                                   const int32_t* __restrict__ dst, int n, PageScratch w,
                                                                   PagePools pools, DeviceStatus* st) {
+  griddep_wait();  // the plan
   if (*w.n_moves < 0) return;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int32_t s = src[i], d = dst[i];
@@ -271,8 +279,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(Pages p, const
   }
   copy_moves(pools, n, [&](int64_t i, int32_t& a, int32_t& b) {
     a = w.from[i];
-    b = w.to[i];
-    return w.last[i] >= 0;
+    b = w.last[i];
+    return b >= 0;
   });
 }
 
@@ -306,10 +314,12 @@ __global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(Pages p, const
 
 // The r-th free page below n_live takes in the r-th held page at or above it.
 __global__ void __launch_bounds__(kThreads) pages_compact_plan_kernel(Pages p, PageScratch w, int32_t* __restrict__ map,
-                                                                      int32_t* __restrict__ n_live_out) {
+                                                                      int32_t* __restrict__ n_live_out, DeviceStatus* st) {
   __shared__ int warp_sums[32];
   __shared__ int n_live_s;
   const int tid = threadIdx.x;
+  griddep_launch_dependents();  // the copying grid waits for this one's end
+  clear_errors(st);
   int live = 0;
   for (int64_t i = tid; i < p.n_pages; i += kThreads) live += p.refs[i] > 0 ? 1 : 0;
   int total;
@@ -362,6 +372,7 @@ __global__ void __launch_bounds__(kThreads) pages_compact_plan_kernel(Pages p, P
 
 __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(Pages p, PageScratch w, const int32_t* __restrict__ map,
                                                                      PagePools pools, DeviceStatus* st) {
+  griddep_wait();  // the plan
   for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
     const int32_t len = p.ctx[s];
     if (len < 0 || (int64_t)len > p.max_pages * p.page) {
@@ -386,13 +397,31 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(Pages p, Pa
 
 unsigned copy_grid() { return (unsigned)(num_sms() * 8); }
 
+// The copying grid as a programmatic dependent of the single CTA before it.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, (P)args...);
+}
+
 }  // namespace
 
 size_t pages_scratch_bytes(const Pages& p, int n) { return carve(p, n, nullptr, nullptr); }
 
-cudaError_t launch_pages_reserve(const Pages& p, const int32_t* seqs, const int32_t* new_len, int n, DeviceStatus* st,
-                                 cudaStream_t s) {
-  if (n > 0) pages_reserve_kernel<<<1, kThreads, (size_t)(n + 1) * 4, s>>>(p, seqs, new_len, n, st);
+cudaError_t launch_pages_reserve(const Pages& p, const int32_t* seqs, const int32_t* new_len, int n, void* scratch,
+                                 DeviceStatus* st, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  PageScratch w;
+  carve(p, n, (char*)scratch, &w);
+  pages_reserve_kernel<<<1, kThreads, (size_t)(2 * n + 1) * 4, s>>>(p, seqs, new_len, n, w, st);
   return cudaGetLastError();
 }
 
@@ -401,11 +430,10 @@ cudaError_t launch_pages_fork(const Pages& p, const int32_t* src, const int32_t*
   if (n == 0) return cudaSuccess;
   PageScratch w;
   carve(p, n, (char*)scratch, &w);
-  pages_fork_plan_kernel<<<1, kThreads, (size_t)(n + 1) * 4, s>>>(p, src, dst, n, w, st);
+  pages_fork_plan_kernel<<<1, kThreads, (size_t)(2 * n + 1) * 4, s>>>(p, src, dst, n, w, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  pages_fork_kernel<<<copy_grid(), kCopyThreads, 0, s>>>(p, src, dst, n, w, pools, st);
-  return cudaGetLastError();
+  return launch_dependent(pages_fork_kernel, copy_grid(), s, p, src, dst, n, w, pools, st);
 }
 
 cudaError_t launch_pages_free(const Pages& p, const int32_t* seqs, int n, DeviceStatus* st, cudaStream_t s) {
@@ -418,11 +446,10 @@ cudaError_t launch_pages_compact(const Pages& p, const PagePools& pools, int32_t
   PageScratch w;
   carve(p, 0, (char*)scratch, &w);
   int32_t* map = page_map ? page_map : w.map;
-  pages_compact_plan_kernel<<<1, kThreads, 0, s>>>(p, w, map, n_live);
+  pages_compact_plan_kernel<<<1, kThreads, 0, s>>>(p, w, map, n_live, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  pages_compact_kernel<<<copy_grid(), kCopyThreads, 0, s>>>(p, w, map, pools, st);
-  return cudaGetLastError();
+  return launch_dependent(pages_compact_kernel, copy_grid(), s, p, w, (const int32_t*)map, pools, st);
 }
 
 }  // namespace msa

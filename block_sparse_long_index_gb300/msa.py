@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
 
@@ -115,16 +117,18 @@ class MsaError(RuntimeError):
 def _ptr(t):
     if t is None:
         return None
-    return ctypes.c_void_p(t.data_ptr() if hasattr(t, "data_ptr") else int(t))
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return int(t)
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch.cuda.current_stream().cuda_stream
     if hasattr(stream, "cuda_stream"):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _check(status, where):
