@@ -179,6 +179,11 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
 }
 
+__device__ __forceinline__ uint32_t drop_not_finite(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
 // The value that every lane of the warp has, in a uniform register.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 __device__ __forceinline__ bool elect_one() {
@@ -421,8 +426,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         for (int j = 0; j < n; ++j) {
           const uint32_t vs = ks + 1, vph = kph;
           next_stage();  // the K tile of j + 1
-          mbar_wait(kv_full(vs), vph, abort, st, 0xD13);
-          mbar_wait(v_ok(vs), vph, abort, st, 0xD14);
+          mbar_wait(v_ok(vs), vph, abort, st, 0xD14);  // (V is there, and guarded)
           const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + vs * L::TILE, L::CHUNK);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
               if (j + 1 == nq) ip[q] ^= 1u;
             }
             if (j + 1 < nq) {
-              mbar_wait(kv_full(ks), kph, abort, st, 0xD17);
+              if (q == 0 || j + 1 >= n0) mbar_wait(kv_full(ks), kph, abort, st, 0xD17);
               tc_fence_after();
               product_s(q, ks, j + 2 == nq);
             }
@@ -473,26 +477,23 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
             if (lane == 0) mbar_arrive(v_ok((int)(x % L::STAGES)));
             continue;
           }
-          uint8_t* va = sm + L::OFF_KV + (x % L::STAGES) * L::TILE;
+          // 16-byte piece lane % 8 of a chunk's row lane / 8; rows before the item's first position are seen by all
+          const uint32_t va = sb + L::OFF_KV + (x % L::STAGES) * L::TILE + (lane & 7) * 16;
           bool found = false;
-#pragma unroll 4
-          for (int i = lane; i < 64 * L::NC * 8; i += 32) {
-            const int c = i / 512, e = i % 512, row = (warp - kWarpGuard) * 64 + e / 8;  // 16-byte piece of a row
-            uint4* at = reinterpret_cast<uint4*>(va + c * L::CHUNK + row * 128 + (e & 7) * 16);
-            if (j * kKeysT + row >= t_end) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint4 y = *at;
-              if (!(finite_bf16x2(y.x) && finite_bf16x2(y.y) && finite_bf16x2(y.z) && finite_bf16x2(y.w))) {
-                uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll 2
+          for (int row = (max(it.t0 - j * kKeysT, 0) & ~7) + (warp - kWarpGuard) * 4 + (lane >> 3); row < 128; row += 8) {
+            const bool past = j * kKeysT + row >= t_end;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((z[k] & 0x7F80u) == 0x7F80u) z[k] &= 0xFFFF0000u;
-                  if ((z[k] & 0x7F800000u) == 0x7F800000u) z[k] &= 0x0000FFFFu;
-                }
-                *at = make_uint4(z[0], z[1], z[2], z[3]);
+            for (int c = 0; c < L::NC; ++c) {
+              const uint32_t at = va + c * L::CHUNK + row * 128;
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (!past) {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at));
+                if (finite_bf16x2(y.x) && finite_bf16x2(y.y) && finite_bf16x2(y.z) && finite_bf16x2(y.w)) continue;
                 found = true;
+                y = make_uint4(drop_not_finite(y.x), drop_not_finite(y.y), drop_not_finite(y.z), drop_not_finite(y.w));
               }
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
             }
           }
           if (found) poison[r % kPoisonSlots] = r + 1;
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
           tmem_ld_wait();
           reg_fence16(x);
           if (bad && live)  // the values that the guard took out, for the rows that see them
-            for (int j = it.t0 / kKeysT * kKeysT; j <= t; ++j) {
+            for (int j = it.t0 & ~7; j <= t; ++j) {
               const uint16_t* vr = v + (((int64_t)it.row0 + j) * H_kv + it.g) * D + c * 16;
               for (int e = 0; e < 16; ++e) {
                 const uint32_t b = vr[e];
