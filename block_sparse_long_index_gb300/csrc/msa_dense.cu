@@ -123,16 +123,18 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // P V, so what counts is how long one takes: with two warpgroups for each tile
 // it took 1670 cycles of 64 exponentials a thread against 1024 cycles of
 // products.)  4 the output (O / l, lse), 5 one warp each for the TMA loads, the
-// MMA issue, and two guard warps.
+// MMA issue of query tile 0 and 1, and the guard.  (With both tiles' products
+// on one warp, each wait of it, some 150 cycles for a phase long complete, left
+// the tensor cores idle: 11.9 ms at 32K and 64 heads against 11.7.)
 //
-// The guard warps make the masked places of V harmless, because a weight of 0
-// times a NaN or an infinity would not be 0 on the tensor cores: in the key
-// tiles that not every row of the item sees whole, they clear the rows past the
-// item's last position and any value that is not finite, and the epilogue then
-// adds the latter to the rows that do see them.
+// The guard makes the masked places of V harmless, because a weight of 0 times
+// a NaN or an infinity would not be 0 on the tensor cores: in the key tiles
+// that not every row of the item sees whole, it clears the rows past the item's
+// last position and, from its first position on, any value that is not finite;
+// the epilogue then adds the latter to the rows that do see them.
 constexpr int kRowsT = 128, kKeysT = 128;
 constexpr int kThreadsA = 768;
-constexpr int kWarpEpi = 16, kWarpLoad = 20, kWarpMma = 21, kWarpGuard = 22;
+constexpr int kWarpEpi = 16, kWarpLoad = 20, kWarpMma = 21, kWarpGuard = 23;
 constexpr float kLazy = 8.0f;
 constexpr int kPoisonSlots = 8;
 constexpr int kOwnRounds = 4;  // rounds that a CTA may plan for itself
@@ -179,6 +181,14 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
   return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
 }
 
+__device__ __forceinline__ uint4 lds_16(uint32_t at) {
+  uint4 y;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at));
+  return y;
+}
+__device__ __forceinline__ void sts_16(uint32_t at, uint4 y) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+}
 __device__ __forceinline__ uint32_t drop_not_finite(uint32_t w) {
   if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   __shared__ int poison[kPoisonSlots];  // 1 + the round whose V tiles held values that are not finite
   const uint32_t bar = sb + L::OFF_BAR;
   auto kv_full = [&](int i) { return bar + 8u * i; };                    // TMA -> MMA, guard
-  auto kv_empty = [&](int i) { return bar + 8u * (L::STAGES + i); };     // MMA (commit) -> TMA
+  auto kv_empty = [&](int i) { return bar + 8u * (L::STAGES + i); };     // MMA (each tile's commit) -> TMA
   constexpr int B0 = 2 * L::STAGES;
   auto q_full = [&](int q) { return bar + 8u * (B0 + q); };              // TMA -> MMA
   auto q_empty = [&](int q) { return bar + 8u * (B0 + 2 + q); };         // MMA (commit) -> TMA
@@ -310,9 +320,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   auto o_empty = [&](int q) { return bar + 8u * (B0 + 12 + q); };        // output (4 warps) -> MMA, softmax
   auto ml_full = [&](int q) { return bar + 8u * (B0 + 14 + q); };        // softmax (16 warps) -> output
   // V tiles alone, which sit in the odd stages; one a stage, so that the guard cannot be two phases ahead
-  auto v_ok = [&](int i) { return bar + 8u * (B0 + 16 + i / 2); };       // guard (2 warps) -> MMA
-  const uint32_t drain = bar + 8u * (B0 + 16 + L::STAGES / 2);
-  static_assert(L::STAGES % 2 == 0 && 8 * (B0 + 17 + L::STAGES / 2) <= 512, "K and V alternate; barriers fit");
+  auto v_ok = [&](int i) { return bar + 8u * (B0 + 16 + i / 2); };       // guard -> MMA
+  auto drain = [&](int q) { return bar + 8u * (B0 + 16 + L::STAGES / 2 + q); };
+  static_assert(L::STAGES % 2 == 0 && 8 * (B0 + 18 + L::STAGES / 2) <= 512, "K and V alternate; barriers fit");
   float4* ml_s = reinterpret_cast<float4*>(sm + L::OFF_ST);
   float* mm_s = reinterpret_cast<float*>(sm + L::OFF_MM);
   float* mx_s = reinterpret_cast<float*>(sm + L::OFF_MX);
@@ -320,9 +330,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
   if (tid == 0) {
     for (int i = 0; i < L::STAGES; ++i) {
       mbar_init(kv_full(i), 1);
-      mbar_init(kv_empty(i), 1);
+      mbar_init(kv_empty(i), 2);
     }
     for (int q = 0; q < 2; ++q) {
+      mbar_init(drain(q), 1);
       mbar_init(q_full(q), 1);
       mbar_init(q_empty(q), 1);
       mbar_init(s_full(q), 1);
@@ -332,8 +343,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
       mbar_init(o_empty(q), 4);
       mbar_init(ml_full(q), 16);
     }
-    for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_ok(i), 2);
-    mbar_init(drain, 1);
+    for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_ok(i), 1);
     fence_mbar_init();
     abort_flag = 0;
     for (int i = 0; i < kPoisonSlots; ++i) poison[i] = 0;
@@ -403,81 +413,67 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
             if (qn[q]) mbar_wait(q_full(q), (qn[q] - 1) & 1, nullptr, st, 0xDF2);
         }
       }
-    } else if (warp == kWarpMma) {
-      // ------------------------------------------------------------ MMA issue
+    } else if (warp < kWarpGuard) {
+      // ------------------------------------------------------------ MMA issue: warp kWarpMma + q for query tile q
       // The whole warp runs the loops on warp-uniform values and one elected lane issues: descriptors then live in
       // uniform registers.  (Run by one lane alone, the register moves of each product cost more than the product.)
       // A wait that gives up is not looked at: the later ones return at once, and every address stays in bounds.
-      const uint32_t tm = uniform(tmem), lead = elect_one();
+      const int q = (int)uniform((uint32_t)(warp - kWarpMma));
+      const uint32_t ts = uniform(tmem) + q * 128, to = ts + L::TMEM_O, lead = elect_one();
       const int total = (int)uniform((uint32_t)items.total);
-      uint32_t ks = 0, kph = 0;         // stage of the next K tile (its V tile is the one after) and the parity of its use
-      uint32_t sp[2] = {0, 0}, ip[2] = {0, 0};  // parities: softmax results, items of each query tile
-      auto next_stage = [&]() {
-        ks += 2;
-        if (ks == (uint32_t)L::STAGES) ks = 0, kph ^= 1u;
-      };
-      auto product_s = [&](int q, uint32_t stage, bool q_last) {
-        // a descriptor's low bits are the address / 16: the steps along d are added to it
-        const uint64_t qd = umma_desc_kmajor(sb + L::OFF_Q + q * L::TILE, 128);
-        const uint64_t kd = umma_desc_kmajor(sb + L::OFF_KV + stage * L::TILE, 128);
+      uint32_t ks = 0, kph = 0;  // stage of the next K tile (its V tile is the one after) and the parity of its use
+      uint32_t sp = 0, ip = 0;   // parities: softmax results, items of the query tile
+      const uint64_t qd = umma_desc_kmajor(sb + L::OFF_Q + q * L::TILE, 128);
+      auto product_s = [&](bool on, bool q_last) {
+        mbar_wait(kv_full(ks), kph, abort, st, 0xD11);  // (a tile that is passed over too: the ring is walked in step)
+        if (on) {
+          tc_fence_after();
+          // a descriptor's low bits are the address / 16: the steps along d are added to it
+          const uint64_t kd = umma_desc_kmajor(sb + L::OFF_KV + ks * L::TILE, 128);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * L::CHUNK + (k & 3) * 32) / 16;
-          mma_ss_if(lead, tm + q * 128, qd + off, kd + off, IDESC_S, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * L::CHUNK + (k & 3) * 32) / 16;
+            mma_ss_if(lead, ts, qd + off, kd + off, IDESC_S, k > 0);
+          }
+          commit_if(lead, s_full(q));
+          commit_if(lead & (uint32_t)q_last, q_empty(q));
         }
-        commit_if(lead, s_full(q));
-        commit_if(lead & (uint32_t)q_last, q_empty(q));
+        commit_if(lead, kv_empty(ks));
       };
       for (int r = 0; items.index(r) < total; ++r) {
         items.load(r, it);
-        const int n0 = (int)uniform((uint32_t)it.n[0]), n1 = (int)uniform((uint32_t)it.n[1]), n = max(n0, n1);
-        mbar_wait(q_full(0), ip[0], abort, st, 0xD10);
-        mbar_wait(kv_full(ks), kph, abort, st, 0xD11);
-        tc_fence_after();
-        product_s(0, ks, n0 == 1);
-        if (n1) {
-          mbar_wait(q_full(1), ip[1], abort, st, 0xD12);
-          tc_fence_after();
-          product_s(1, ks, n1 == 1);
-        }
-        commit_if(lead, kv_empty(ks));
+        const int n = (int)uniform((uint32_t)it.n_max()), nq = (int)uniform((uint32_t)it.n[q]);
+        if (nq) mbar_wait(q_full(q), ip, abort, st, 0xD10);
+        product_s(nq > 0, nq == 1);
         for (int j = 0; j < n; ++j) {
           const uint32_t vs = ks + 1, vph = kph;
-          next_stage();  // the K tile of j + 1
+          ks += 2;  // the K tile of j + 1
+          if (ks == (uint32_t)L::STAGES) ks = 0, kph ^= 1u;
           mbar_wait(v_ok(vs), vph, abort, st, 0xD14);  // (V is there, and guarded)
-          const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + vs * L::TILE, L::CHUNK);
+          if (j < nq) {
+            const uint64_t vd = umma_desc_mnmajor_sw128(sb + L::OFF_KV + vs * L::TILE, L::CHUNK);
+            if (j == 0) mbar_wait(o_empty(q), ip ^ 1u, abort, st, 0xD15);
+            mbar_wait(p_full(q), sp, abort, st, 0xD16);
+            sp ^= 1u;
+            tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int nq = q ? n1 : n0;
-            if (j < nq) {
-              if (j == 0) mbar_wait(o_empty(q), ip[q] ^ 1u, abort, st, 0xD15);
-              mbar_wait(p_full(q), sp[q], abort, st, 0xD16);
-              sp[q] ^= 1u;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kKeysT / 16; ++k)  // keys 16 k ..: part k / 2, packed from column 32 part on
-                mma_ts_if(lead, tm + L::TMEM_O + q * 128, tm + q * 128 + 32 * (k >> 1) + 8 * (k & 1),
-                          vd + k * (16 * 128 / 16), IDESC_PV, (j > 0 || k > 0) ? 1u : 0u);
-              commit_if(lead, pv_done(q));
-              commit_if(lead & (uint32_t)(j + 1 == nq), o_full(q));
-              if (j + 1 == nq) ip[q] ^= 1u;
-            }
-            if (j + 1 < nq) {
-              if (q == 0 || j + 1 >= n0) mbar_wait(kv_full(ks), kph, abort, st, 0xD17);
-              tc_fence_after();
-              product_s(q, ks, j + 2 == nq);
-            }
+            for (int k = 0; k < kKeysT / 16; ++k)  // keys 16 k ..: part k / 2, packed from column 32 part on
+              mma_ts_if(lead, to, ts + 32 * (k >> 1) + 8 * (k & 1), vd + k * (16 * 128 / 16), IDESC_PV,
+                        (j > 0 || k > 0) ? 1u : 0u);
+            commit_if(lead, pv_done(q));
+            commit_if(lead & (uint32_t)(j + 1 == nq), o_full(q));
           }
           commit_if(lead, kv_empty(vs));
-          commit_if(lead & (uint32_t)(j + 1 < n), kv_empty(ks));
+          if (j + 1 < n) product_s(j + 1 < nq, j + 2 == nq);
         }
+        ip ^= (uint32_t)(nq > 0);
       }
       if (*abort) {  // the products in flight end before TMEM is released
-        commit_if(lead, drain);
-        mbar_wait(drain, 0, nullptr, st, 0xDF3);
+        commit_if(lead, drain(q));
+        mbar_wait(drain(q), 0, nullptr, st, 0xDF3);
       }
     } else {
-      // ------------------------------------------------------------ guard: rows 64 (warp - kWarpGuard) .. + 63 of V
+      // ------------------------------------------------------------ guard
       uint32_t kv = 0;
       bool ok = true;
       for (int r = 0; ok && items.get(r, it); ++r) {
@@ -491,25 +487,37 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
             if (lane == 0) mbar_arrive(v_ok((int)(x % L::STAGES)));
             continue;
           }
-          // 16-byte piece lane % 8 of a chunk's row lane / 8; rows before the item's first position are seen by all
+          // lane: 16-byte piece lane % 8 of a chunk's row lane / 8; rows before the item's first position are seen by all
           const uint32_t va = sb + L::OFF_KV + (x % L::STAGES) * L::TILE + (lane & 7) * 16;
+          const int rows = min(128, t_end - j * kKeysT);  // of the tile, up to the item's last position
           bool found = false;
-#pragma unroll 2
-          for (int row = (max(it.t0 - j * kKeysT, 0) & ~7) + (warp - kWarpGuard) * 4 + (lane >> 3); row < 128; row += 8) {
-            const bool past = j * kKeysT + row >= t_end;
+          for (int r0 = (max(it.t0 - j * kKeysT, 0) & ~7) + (lane >> 3); r0 - (lane >> 3) < rows; r0 += 16) {
+            uint4 y[4][L::NC];
+            uint32_t most = 0u;
 #pragma unroll
-            for (int c = 0; c < L::NC; ++c) {
-              const uint32_t at = va + c * L::CHUNK + row * 128;
-              uint4 y = make_uint4(0u, 0u, 0u, 0u);
-              if (!past) {
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at));
-                if (finite_bf16x2(y.x) && finite_bf16x2(y.y) && finite_bf16x2(y.z) && finite_bf16x2(y.w)) continue;
-                found = true;
-                y = make_uint4(drop_not_finite(y.x), drop_not_finite(y.y), drop_not_finite(y.z), drop_not_finite(y.w));
-              }
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
-            }
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int c = 0; c < L::NC; ++c) y[u][c] = r0 + 4 * u < rows ? lds_16(va + c * L::CHUNK + (r0 + 4 * u) * 128) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int c = 0; c < L::NC; ++c)
+                most = __vmaxu2(most, __vmaxu2(__vmaxu2(y[u][c].x & 0x7FFF7FFFu, y[u][c].y & 0x7FFF7FFFu),
+                                               __vmaxu2(y[u][c].z & 0x7FFF7FFFu, y[u][c].w & 0x7FFF7FFFu)));
+            if (finite_bf16x2(most)) continue;
+            found = true;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int c = 0; c < L::NC; ++c)
+                if (r0 + 4 * u < rows)
+                  sts_16(va + c * L::CHUNK + (r0 + 4 * u) * 128, make_uint4(drop_not_finite(y[u][c].x), drop_not_finite(y[u][c].y),
+                                                                        drop_not_finite(y[u][c].z), drop_not_finite(y[u][c].w)));
           }
+#pragma unroll 4
+          for (int row = max(rows, 0) + (lane >> 3); row < 128; row += 4)
+#pragma unroll
+            for (int c = 0; c < L::NC; ++c) sts_16(va + c * L::CHUNK + row * 128, make_uint4(0u, 0u, 0u, 0u));
           if (found) poison[r % kPoisonSlots] = r + 1;
           fence_proxy_async_smem();
           __syncwarp();
