@@ -571,7 +571,7 @@ msa_status_t msa_kv4_store(const void* k, const void* v, int64_t N, const int32_
   msa_status_t st = check_kv4_rows(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, pool);
   if (st != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, kHeader, s);
+  st = begin(workspace, workspace_bytes, kHeader, s, msa::kv4_rows_report(N) ? 0 : kHeader);
   if (st != MSA_OK) return st;
   return finish(msa::launch_kv4_store(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, kv4_pool(pool),
                                       (msa::DeviceStatus*)workspace, s));
@@ -583,7 +583,7 @@ msa_status_t msa_kv4_load(const msa_kv4_pool_t* pool, int64_t N, const int32_t* 
   msa_status_t st = check_kv4_rows(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, pool);
   if (st != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  st = begin(workspace, workspace_bytes, kHeader, s);
+  st = begin(workspace, workspace_bytes, kHeader, s, msa::kv4_rows_report(N) ? 0 : kHeader);
   if (st != MSA_OK) return st;
   return finish(msa::launch_kv4_load(kv4_pool(pool), N, cu_seqlens, S, pos0, page_table, max_pages, k, v,
                                      (msa::DeviceStatus*)workspace, s));
@@ -609,7 +609,7 @@ msa_status_t msa_dense_decode_paged_kv4(const void* q_t, const msa_kv4_pool_t* p
     return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
   st = begin(workspace, workspace_bytes, msa_dense_decode_paged_kv4_workspace(B, H_q, pool->H_kv, pool->d), s,
-             kHeader + msa::kDenseDecodeClear);
+             0);  // the combine writes the status
   if (st != MSA_OK) return st;
   return finish(msa::launch_dense_decode(q_t, kv4_pool(pool), page_table, max_pages, ctx_len, B, H_q, scale, out, lse,
                                          (char*)workspace + kHeader, (msa::DeviceStatus*)workspace, s));

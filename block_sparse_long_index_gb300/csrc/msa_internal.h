@@ -197,11 +197,12 @@ cudaError_t launch_dense_prefill(const void* q, const void* k, const void* v, co
                                  float scale, void* out, float* lse, void* scratch, DeviceStatus* st, cudaStream_t s);
 
 // ---- 4-bit paged cache (msa_kv4.cu)
+// Calls whose status one CTA writes (the header is then not cleared before them).
+constexpr bool kv4_rows_report(int64_t N) { return N <= 256; }
 cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                              const int32_t* table, int64_t max_pages, const Kv4Pool& pool, DeviceStatus* st, cudaStream_t s);
 cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                             const int32_t* table, int64_t max_pages, void* k, void* v, DeviceStatus* st, cudaStream_t s);
-constexpr size_t kDenseDecodeClear = 256;  // bytes at the start of its scratch that are 0 when a call starts
 size_t dense_decode_scratch_bytes(int H_kv, int gs, int d);
 cudaError_t launch_dense_decode(const void* q, const Kv4Pool& pool, const int32_t* table, int64_t max_pages,
                                 const int32_t* ctx_len, int B, int H_q, float scale, void* out, float* lse, void* scratch,

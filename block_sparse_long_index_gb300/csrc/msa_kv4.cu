@@ -55,6 +55,22 @@ struct RowTile {
   }
 };
 
+// A call of at most kRowThreads rows has its status written by CTA 0 alone, which looks at all of them (the other
+// CTAs report nothing): it needs no clearing before the kernel, a launch of its own (a decode step's store and load
+// 12.4 -> 10.4 us on the GPU).
+__device__ __forceinline__ void report_rows(const RowMap& map, int64_t N, DeviceStatus* st) {
+  __shared__ unsigned int est[2];
+  DeviceStatus* own = reinterpret_cast<DeviceStatus*>(est);  // (its first two words are all that an error touches)
+  if (threadIdx.x == 0) est[0] = est[1] = 0u;
+  __syncthreads();
+  if (threadIdx.x < N) map.row(threadIdx.x, own);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    st->flags = own->flags;
+    st->first_code = own->first_code;
+  }
+}
+
 template <int D, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* __restrict__ k,
                                                                 const uint16_t* __restrict__ v, int64_t N, int R, RowMap map,
@@ -64,6 +80,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* 
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
+  if (U == 1 && kv4_rows_report(N)) {
+    if (blockIdx.x == 0) report_rows(map, N, st);
+    st = nullptr;
+  }
   for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) rows[t] = i0 + t < N ? map.row(i0 + t, st) : -1;
   __syncthreads();
   const int sub = threadIdx.x / rt.per_tok;  // 0 where a token takes the whole CTA
@@ -126,6 +146,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
+  if (U == 1 && kv4_rows_report(N)) {
+    if (blockIdx.x == 0) report_rows(map, N, st);
+    st = nullptr;
+  }
   const int64_t in0 = map.cu[0], in1 = map.cu[map.S];
   for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) {
     const int64_t i = i0 + t;
@@ -328,11 +352,14 @@ __device__ __forceinline__ FlatSplit flat_split(const int32_t* ctx_len, int B, i
   return f;
 }
 
-// A row that several CTAs share, listed by the second of them.
-struct SplitRow {
-  int seq, hb;
+// What a CTA leaves beside its partials: the row that it is the second CTA of, if any, and the errors it met.  Every
+// CTA writes its own record, so nothing has to be cleared before a call.
+struct __align__(16) SplitRow {
+  int seq, hb;  // seq -1: no such row
   int c0, c1;   // the CTAs that hold it
   int part0;    // which partial of c0 it is (partial 0 of the others)
+  unsigned int flags, first_code;
+  int pad;
 };
 
 // A CTA's run, segment by segment: units [u0, u1) of the T units of (sequence, head block).
@@ -369,8 +396,8 @@ template <int D, int HC>
 __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ q,
     Kv4Pool pool, CacheMap map, const int32_t* __restrict__ ctx_len, int B, int64_t cap, int gs, float scale, int stages,
-    uint16_t* __restrict__ out, float* __restrict__ lse, int* __restrict__ n_rows, SplitRow* __restrict__ rows,
-    float* __restrict__ part_o, float2* __restrict__ part_ml, DeviceStatus* st) {
+    uint16_t* __restrict__ out, float* __restrict__ lse, SplitRow* __restrict__ rows, float* __restrict__ part_o,
+    float2* __restrict__ part_ml) {
   constexpr int TW = kDecWarps / HC, SU = 2 * TW;  // warps that share a head, units of a step
   constexpr int CT = D / 8;           // channels of a lane's V column
   using X = Tile<D>;
@@ -378,6 +405,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
   __shared__ int abort_flag;
+  __shared__ unsigned int est[2];
+  DeviceStatus* st = reinterpret_cast<DeviceStatus*>(est);  // the CTA's own (an error touches its first two words)
   __shared__ float red_m[kDecWarps][8], red_l[kDecWarps][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H_kv = pool.H_kv, H_q = H_kv * gs;
@@ -394,6 +423,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     }
     fence_mbar_init();
     abort_flag = 0;
+    est[0] = est[1] = 0u;
   }
   volatile int* abort = &abort_flag;
   Segments sg;
@@ -406,18 +436,20 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
     sg.f1 = min(fs.total, sg.f + fs.quota);
     sg.before = fs.before;
     sg.seq = fs.seq;
-    if (threadIdx.x == 0 && sg.next() && sg.u0 > 0) {  // the run begins inside a row
-      const int64_t r0 = sg.f - sg.u0, c = blockIdx.x;
-      const int c0 = (int)(r0 / fs.quota);
-      if (c0 == c - 1) {
-        SplitRow row;
-        row.seq = sg.seq;
-        row.hb = sg.hb;
-        row.c0 = c0;
-        row.c1 = (int)((r0 + sg.T - 1) / fs.quota);
-        row.part0 = r0 == c0 * fs.quota ? 0 : 1;
-        rows[atomicAdd(n_rows, 1)] = row;  // the list's order is free: rows are merged independently
+    if (threadIdx.x == 0) {
+      SplitRow row = {-1, 0, 0, 0, 0, 0u, 0u, 0};
+      if (sg.next() && sg.u0 > 0) {  // the run begins inside a row
+        const int64_t r0 = sg.f - sg.u0, c = blockIdx.x;
+        const int c0 = (int)(r0 / fs.quota);
+        if (c0 == c - 1) {
+          row.seq = sg.seq;
+          row.hb = sg.hb;
+          row.c0 = c0;
+          row.c1 = (int)((r0 + sg.T - 1) / fs.quota);
+          row.part0 = r0 == c0 * fs.quota ? 0 : 1;
+        }
       }
+      rows[blockIdx.x] = row;
     }
   }
   const float kInf = __int_as_float(0x7f800000);
@@ -699,20 +731,60 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
   if (*abort && lane == 0)  // a wait gave up: let this warp's copies land before the CTA ends
     for (int i = 0; i < stages; ++i)
       if (fetched >> i & 1u) mbar_wait(full(i), fetched >> (16 + i) & 1u, nullptr, st, 0xEF1);
+  __syncthreads();
+  if (threadIdx.x == 0 && st->flags) {
+    rows[blockIdx.x].flags = st->flags;
+    rows[blockIdx.x].first_code = st->first_code;
+  }
 }
 
-// Merges the partials of the listed rows: a CTA per (row, two heads), 4 warps a head, each with every 4th partial.
+// Merges the partials of the rows that CTAs share: a CTA per (row, two heads), 4 warps a head, each with every 4th
+// partial.  Row blockIdx.x is that of the blockIdx.x-th record that names one; CTA 0 also sums up the errors.
 template <int D>
-__global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const int* __restrict__ n_rows,
-                                                                  const SplitRow* __restrict__ rows, int H_kv, int HC, int gs,
-                                                                  const float* __restrict__ part_o,
+__global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRow* __restrict__ rows, int n_cta, int H_kv,
+                                                                  int HC, int gs, const float* __restrict__ part_o,
                                                                   const float2* __restrict__ part_ml,
-                                                                  uint16_t* __restrict__ out, float* __restrict__ lse) {
+                                                                  uint16_t* __restrict__ out, float* __restrict__ lse,
+                                                                  DeviceStatus* st) {
   constexpr int V = D / 32;  // channels of a lane
   __shared__ float acc_s[2][4][D], l_s[2][4];
-  griddep_wait();  // the partials
-  if ((int)blockIdx.x >= *n_rows) return;
-  const SplitRow row = rows[blockIdx.x];
+  __shared__ SplitRow row_s;
+  __shared__ int named[kCombThreads / 32];
+  __shared__ unsigned int est[2];
+  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+  if (threadIdx.x == 0) row_s.seq = -1, est[0] = est[1] = 0u;
+  griddep_wait();  // the records and the partials
+  for (int c0 = 0, before = 0; c0 < n_cta; c0 += kCombThreads) {
+    const int ct = c0 + threadIdx.x;
+    SplitRow row;
+    row.seq = -1, row.flags = 0u;
+    if (ct < n_cta) {
+      const int4* p = reinterpret_cast<const int4*>(rows + ct);
+      *reinterpret_cast<int4*>(&row) = p[0];
+      *(reinterpret_cast<int4*>(&row) + 1) = p[1];
+    }
+    const unsigned int has = __ballot_sync(0xffffffffu, row.seq >= 0);
+    __syncthreads();  // named is read (and row_s, est begun)
+    if ((threadIdx.x & 31) == 0) named[threadIdx.x >> 5] = __popc(has);
+    if (first && row.flags) {
+      atomicOr(&est[0], row.flags);
+      est[1] = row.first_code;  // any of them
+    }
+    __syncthreads();
+    int rank = before + __popc(has & ((1u << (threadIdx.x & 31)) - 1u));
+    for (int x = 0; x < kCombThreads / 32; ++x) {
+      before += named[x];
+      if (x < (int)threadIdx.x >> 5) rank += named[x];
+    }
+    if (row.seq >= 0 && rank == (int)blockIdx.x) row_s = row;
+  }
+  __syncthreads();
+  if (first && threadIdx.x == 0) {
+    st->flags = est[0];
+    st->first_code = est[1];
+  }
+  const SplitRow row = row_s;
+  if (row.seq < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp & 3;
   const int h = blockIdx.y * 2 + (warp >> 2);  // head of the block
   const int heads = min(HC * gs, (H_kv - row.hb * HC) * gs);
@@ -778,7 +850,7 @@ int decode_ctas() { return 2 * num_sms(); }
 
 template <int D, int HC>
 cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const CacheMap& map, const int32_t* ctx_len, int B,
-                                  int64_t cap, int gs, float scale, void* out, float* lse, int* n_rows, SplitRow* rows,
+                                  int64_t cap, int gs, float scale, void* out, float* lse, SplitRow* rows,
                                   float* part_o, float2* part_ml, DeviceStatus* st, cudaStream_t s) {
   constexpr int TW = kDecWarps / HC, CB = D / 2;
   alignas(64) unsigned char tk[128], tv[128];
@@ -797,7 +869,7 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
   if (e != cudaSuccess) return e;
   kern<<<n_cta, kDecThreads, smem, s>>>(*reinterpret_cast<const CUtensorMap*>(tk), *reinterpret_cast<const CUtensorMap*>(tv),
                                         (const uint16_t*)q, pool, map, ctx_len, B, cap, gs, scale, stages, (uint16_t*)out,
-                                        lse, n_rows, rows, part_o, part_ml, st);
+                                        lse, rows, part_o, part_ml);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int64_t most = (int64_t)B * ((pool.H_kv + HC - 1) / HC);  // rows; at most one split a CTA boundary
@@ -809,8 +881,8 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D>, (const int*)n_rows, (const SplitRow*)rows, pool.H_kv, HC, gs,
-                            (const float*)part_o, (const float2*)part_ml, (uint16_t*)out, lse);
+  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D>, (const SplitRow*)rows, n_cta, pool.H_kv, HC, gs,
+                            (const float*)part_o, (const float2*)part_ml, (uint16_t*)out, lse, st);
 }
 
 int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
@@ -845,9 +917,8 @@ cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, i
   return cudaGetLastError();
 }
 
-// Scratch: the number of split rows (cleared before each call), their list, the partials.
+// Scratch: a record of each CTA, the partials.
 struct DecScratch {
-  int* n_rows;
   SplitRow* rows;
   float* part_o;
   float2* part_ml;
@@ -861,7 +932,6 @@ static size_t carve_dense_decode(int H_kv, int gs, int d, char* base, DecScratch
     return r;
   };
   DecScratch w;
-  w.n_rows = (int*)take(kDenseDecodeClear);
   w.rows = (SplitRow*)take((size_t)decode_ctas() * sizeof(SplitRow));
   w.part_o = (float*)take(slots * d * 4);
   w.part_ml = (float2*)take(slots * 8);
@@ -884,7 +954,7 @@ cudaError_t launch_dense_decode(const void* q, const Kv4Pool& pool, const int32_
   map.page = pool.page;
   const int64_t cap = max_pages * pool.page;
 #define MSA_DD(D, H) \
-  launch_dense_decode_t<D, H>(q, pool, map, ctx_len, B, cap, gs, scale, out, lse, w.n_rows, w.rows, w.part_o, w.part_ml, st, s)
+  launch_dense_decode_t<D, H>(q, pool, map, ctx_len, B, cap, gs, scale, out, lse, w.rows, w.part_o, w.part_ml, st, s)
   if (pool.d == 64) return HC == 8 ? MSA_DD(64, 8) : HC == 4 ? MSA_DD(64, 4) : HC == 2 ? MSA_DD(64, 2) : MSA_DD(64, 1);
   return HC == 8 ? MSA_DD(128, 8) : HC == 4 ? MSA_DD(128, 4) : HC == 2 ? MSA_DD(128, 2) : MSA_DD(128, 1);
 #undef MSA_DD
