@@ -109,23 +109,28 @@ __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* 
         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         uint32_t mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx = max(mx, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
 #pragma unroll
-        for (int o = 1; o < LPG; o <<= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, o));
+        for (int o = 1; o < LPG; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(lanes, mx, o));
+        mx = max(mx & 0xFFFFu, mx >> 16);
         uint32_t sb = scale_of(mx), code;
         const float s = scale_f32(sb), inv = __fdividef(1.0f, s);
-        float lo[4], hi[4];
+        uint64_t x2[4];  // channels 2 j and 2 j + 1
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lo[j] = bf16_lo(w[j]), hi[j] = bf16_hi(w[j]);
+        for (int j = 0; j < 4; ++j) x2[j] = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
         if (mx >= 0x7F80u) {
           sb = kScaleNaN;
           code = 0x88888888u;
         } else {
           if (sb == kScaleMax) {  // the one scale whose group may reach past 7 s
 #pragma unroll
-            for (int j = 0; j < 4; ++j) lo[j] = fminf(fmaxf(lo[j], -7.f * s), 7.f * s), hi[j] = fminf(fmaxf(hi[j], -7.f * s), 7.f * s);
+            for (int j = 0; j < 4; ++j) {
+              float a, b;
+              f2_unpack(x2[j], a, b);
+              x2[j] = f2_pack(fminf(fmaxf(a, -7.f * s), 7.f * s), fminf(fmaxf(b, -7.f * s), 7.f * s));
+            }
           }
-          code = codes4(lo, inv) | codes4(hi, inv) << 16;
+          code = codes8(x2, inv);
         }
         if (row[u] >= 0) {
           reinterpret_cast<uint32_t*>(codes)[row[u] * half + e] = code;

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "msa_common.cuh"
+#include "msa_sm100.cuh"
 
 namespace msa {
 namespace kv4 {
@@ -85,19 +86,24 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
   return (uint32_t)min(b, (int)kScaleMax);
 }
 
-// Four codes, nibbles 0 .. 3: round-to-nearest-even(x / s) + 8 for |x / s| <= 7.
+// The 8 codes of 4 channel pairs, round-to-nearest-even(x / s) + 8 for |x / s| <= 7: pair j's in nibble j of the halves.
 // x has 8 and s has 4 significant bits, so x / s is a tie or at least 2^-11 away from one wherever it rounds to a
 // code that is not 0.  fma(x, 1/s, 1.5 * 2^10) rounds x / s to a multiple of 2^-13 (1/s may be 2^-20 off): a tie is
 // exact again, the others keep their side.  Adding 1.5 * 2^23 - 1.5 * 2^10 rounds that to an integer, which the
 // mantissa then holds; its bits are summed with weights 16^i and the constant part taken off at the end.
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv_s) {
-  uint32_t sum = 0;
+__device__ __forceinline__ uint32_t codes8(const uint64_t (&x2)[4], float inv_s) {
+  const uint64_t inv2 = f2_pack(inv_s, inv_s), half = f2_pack(1536.0f, 1536.0f);
+  const uint64_t rest = f2_pack(12582912.0f - 1536.0f, 12582912.0f - 1536.0f);
+  uint32_t lo = 0, hi = 0;
 #pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    const float t = __fadd_rn(__fmaf_rn(x[i], inv_s, 1536.0f), 12582912.0f - 1536.0f);
-    sum = sum * 16u + __float_as_uint(t);
+  for (int j = 3; j >= 0; --j) {
+    float a, b;
+    f2_unpack(f2_add(f2_fma(x2[j], inv2, half), rest), a, b);
+    lo = lo * 16u + __float_as_uint(a);
+    hi = hi * 16u + __float_as_uint(b);
   }
-  return sum - (0x4B400000u * 0x1111u - 0x8888u);
+  const uint32_t off = 0x4B400000u * 0x1111u - 0x8888u;
+  return (lo - off) | (hi - off) << 16;
 }
 
 }  // namespace kv4
