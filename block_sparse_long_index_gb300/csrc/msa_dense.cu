@@ -5,6 +5,16 @@
 // A work item is a run of positions of one sequence; the planning kernel lists
 // them with the ones that see most keys first, so that the short ones fill the
 // end of the launch.
+//
+// Bound: the tensor cores, 4 d FLOP for every visible (row, key, head) pair;
+// operands are read once from HBM and again from L2.  Measured, against a
+// library bf16 product's 1913.8 TFLOP/s on the same GPU (1709 when it runs for
+// seconds):
+//   one prompt of 32768, 64 heads on 8, d = 128: 11.7 ms, 1500 TFLOP/s (0.78);
+//   10.7 ms, 1640 TFLOP/s (0.86) for a call by itself - calls in a row reach the
+//   board's 1400 W, and the clock falls from 2.07 to 1.88 GHz;
+//   8 prompts of 167 to 16000 rows, 32 heads on 8: 1.97 ms, 1430 TFLOP/s (0.75);
+//   5 prompts of 1 to 640 rows, 32 heads on 8: 19.6 us, where start and end count.
 #include <math.h>
 
 #include "msa_sm100.cuh"
@@ -116,7 +126,16 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // tensor cores work on the other's P V and next S.  The running maximum is
 // lazy: O and the row sum are rescaled only when a row's maximum has grown by
 // more than 2^8, so P stays below 256 (its bf16 rounding is relative, so the
-// factor costs no precision) and the rescale of O in TMEM is rare.
+// factor costs no precision) and the rescale of O in TMEM is rare.  P's bf16 is
+// what the product takes; sums, maxima and O are fp32.
+//
+// What bounds a step: the softmax.  A query tile's softmax takes some 1500
+// cycles of the SM (512 of them exponentials, the rest the latencies of S's
+// read, the maxima's exchange and P's write), the two tiles' products 2048 in
+// 3000.  Measured and slower at 32K: 8 softmax warps a tile on both at once
+// 12.4 ms; a tile's S read while the other's P is written 12.6 ms; P handed over
+// in two parts 14.5 ms; 64-key steps 12.9 ms; exponentials before the maxima's
+// exchange 13.3 ms.
 // Warpgroups: 0 to 3 the softmax, of query tile 0 and 1 in turn: warpgroup h has
 // keys 32 h .. + 31 of every row, and the four threads of a row exchange their
 // maxima through shared memory.  (A tile's softmax lies between its S and its
@@ -258,8 +277,10 @@ struct Items {
   }
 };
 
-// The plan's list worked out by one warp for its CTA's few rounds, where S <= 32 (a lane a sequence): item i is of the
-// largest depth d with more than i items at depth d or deeper.  Sequences of one depth go by their number.
+// The plan's list worked out by one warp for its CTA's few rounds, where S <= 32 (a lane a sequence) and the items give
+// a CTA at most kOwnRounds: 5 prompts of 1 to 640 rows took 25.3 us with the planning kernel before it and 22.6 us so.
+// (With more rounds it stops to matter: 8 prompts of 167 to 16000 rows, 28 rounds, 1961 us with the kernel, 1968 so.)
+// Item i is of the largest depth d with more than i items at depth d or deeper.  Sequences of one depth go by their number.
 __device__ __forceinline__ void plan_own(const int32_t* cu, int S, int64_t N, int P, int H_kv, int4* own, int* total,
                                          DeviceStatus* st) {
   const int lane = threadIdx.x & 31;
@@ -720,7 +741,7 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const int32_t*
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.own ? 0 : 1;  // (a CTA that plans for itself reads cu before it waits)
   return cudaLaunchKernelEx(&cfg, kern, *reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
                             *reinterpret_cast<const CUtensorMap*>(tv), (const uint16_t*)v, cu, p.own ? p.S : 0, p.N, p.H_q,
                             p.H_kv, scale * 1.4426950408889634f, w, (uint16_t*)out, lse, st);

@@ -43,10 +43,14 @@ struct RowMap {
   }
 };
 
+// Rows in (store) and out (load): bound by HBM, 2 d bytes of bf16 and d / 2 + 4 of codes and scales a head row, each
+// touched once; the store comes near its instructions too (74 % of issue slots: maxima, scale, 8 roundings a thread).
 // A CTA takes R x U x tpp packed rows (tokens), tpp = the tokens that 256 threads cover at 8 channels a thread (K's
 // head rows, then V's): it looks all of them up first, then has the reads of U x tpp of them in flight at a time.
-// U = 4 and R up to kRounds where the CTAs still fill the GPU, 1 and 1 otherwise (a decode step's few rows).
-constexpr int kRounds = 8;
+// R grows up to kRounds where the CTAs still fill the GPU.
+// 131072 tokens of 8 heads, d = 128, in and out: 258 us, 5.26 TB/s (0.78 of the measured copy rate); 604 us with U = 1,
+// which is no faster for few rows either (48 tokens in and out 10.3 us, 10.2 with U = 4: two launches' latency).
+constexpr int kUnroll = 4, kRounds = 8;
 struct RowTile {
   int per_tok, tpp;
   __host__ __device__ RowTile(int H_kv, int lanes_per_row) {
@@ -71,16 +75,16 @@ __device__ __forceinline__ void report_rows(const RowMap& map, int64_t N, Device
   }
 }
 
-template <int D, int U>
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* __restrict__ k,
                                                                 const uint16_t* __restrict__ v, int64_t N, int R, RowMap map,
                                                                 Kv4Pool pool, DeviceStatus* st) {
-  constexpr int LPR = D / 8, LPG = LPR / kGroups;  // threads of a head row, of a group
-  __shared__ int64_t rows[U == 1 ? 32 : U * kRounds * 16];
+  constexpr int U = kUnroll, LPR = D / 8, LPG = LPR / kGroups;  // threads of a head row, of a group
+  __shared__ int64_t rows[U * kRounds * 16];
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
-  if (U == 1 && kv4_rows_report(N)) {
+  if (kv4_rows_report(N)) {
     if (blockIdx.x == 0) report_rows(map, N, st);
     st = nullptr;
   }
@@ -142,16 +146,16 @@ __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* 
 }
 
 // The same rows back as exact bf16 values; zeros where the row map has no place.
-template <int D, int U>
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int64_t N, int R, RowMap map,
                                                                uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                                DeviceStatus* st) {
-  constexpr int LPR = D / 8, LPG = LPR / kGroups;
-  __shared__ int64_t rows[U == 1 ? 32 : U * kRounds * 16];  // pool row, -1: zeros, -2: a row of no sequence
+  constexpr int U = kUnroll, LPR = D / 8, LPG = LPR / kGroups;
+  __shared__ int64_t rows[U * kRounds * 16];  // pool row, -1: zeros, -2: a row of no sequence
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
-  if (U == 1 && kv4_rows_report(N)) {
+  if (kv4_rows_report(N)) {
     if (blockIdx.x == 0) report_rows(map, N, st);
     st = nullptr;
   }
@@ -214,6 +218,16 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
 //     expanded, which transposes V on the way; P^T comes from S^T by movmatrix.
 // S^T's row i is token perm(i) of the unit, chosen so that both the K and the V
 // reads of the swizzled tiles fall in distinct banks.
+//
+// Bound: HBM, (d / 2 + 4) 2 H_kv bytes a token, and close to it the integer
+// instructions that expand the codes (ALU 53 %, issue 61 % of the slots).
+// mma.sync, not tcgen05: a group's 8 query heads fill an n = 8 tile, where
+// tcgen05's 128-row tiles would be 15/16 empty, and codes would have to be
+// expanded into shared memory instead of registers.  Measured, 64 heads on 8,
+// d = 128: 4 sequences of 2^20 tokens 830 us, 5.5 TB/s (0.81 of the measured
+// copy rate); 48 sequences of some 12000, 32 heads on 8: 84 us, 4.15 TB/s (0.61,
+// of which some 12 us are the start and the combine); one of 1500 tokens:
+// 12.3 us, a chain of round trips.
 constexpr int kUnit = 16;
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
@@ -744,7 +758,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
 }
 
 // Merges the partials of the rows that CTAs share: a CTA per (row, two heads), 4 warps a head, each with every 4th
-// partial.  Row blockIdx.x is that of the blockIdx.x-th record that names one; CTA 0 also sums up the errors.
+// partial.  Row blockIdx.x is that of the blockIdx.x-th record that names one; CTA 0 also sums up the errors.  (Rows
+// found by searching the lengths and a CTA a row took 107 us instead of 84 at 48 sequences of some 12000 tokens.)
 template <int D>
 __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRow* __restrict__ rows, int n_cta, int H_kv,
                                                                   int HC, int gs, const float* __restrict__ part_o,
@@ -890,24 +905,26 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
                             (const float*)part_o, (const float2*)part_ml, (uint16_t*)out, lse, st);
 }
 
+// Heads of a CTA: all of up to 8, so that a token's scales come as one run; for H_kv > 4 always 8 (8 heads,
+// 4 sequences of 2^20 tokens: 1303 us with 4 a CTA, 829 with 8; 48 of some 12000: 128 and 84), for fewer the next power
+// of two, the warps left over sharing a head's tokens.
 int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
 
 }  // namespace
 
-// Rounds of a CTA: 0 stands for U = 1.  Four CTAs an SM at least before a CTA takes a second round.
+// Rounds of a CTA: four CTAs an SM at least before a CTA takes a second round.
 static int rows_rounds(int64_t N, int tpp) {
-  const int64_t fill = (int64_t)4 * num_sms() * 4 * tpp, r = N / fill;
-  return r > kRounds ? kRounds : (int)r;
+  const int64_t r = N / ((int64_t)4 * num_sms() * kUnroll * tpp);
+  return r > kRounds ? kRounds : r < 1 ? 1 : (int)r;
 }
 
 cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                              const int32_t* table, int64_t max_pages, const Kv4Pool& pool, DeviceStatus* st, cudaStream_t s) {
   const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
   const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
-  auto kern = pool.d == 64 ? (R ? kv4_store_kernel<64, 4> : kv4_store_kernel<64, 1>)
-                           : (R ? kv4_store_kernel<128, 4> : kv4_store_kernel<128, 1>);
-  kern<<<(unsigned)ceil_div(N, (R ? 4 * R : 1) * tpp), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N,
-                                                                          R ? R : 1, map, pool, st);
+  auto kern = pool.d == 64 ? kv4_store_kernel<64> : kv4_store_kernel<128>;
+  kern<<<(unsigned)ceil_div(N, R * kUnroll * tpp), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N, R, map,
+                                                                       pool, st);
   return cudaGetLastError();
 }
 
@@ -915,10 +932,8 @@ cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, i
                             const int32_t* table, int64_t max_pages, void* k, void* v, DeviceStatus* st, cudaStream_t s) {
   const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
   const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
-  auto kern = pool.d == 64 ? (R ? kv4_load_kernel<64, 4> : kv4_load_kernel<64, 1>)
-                           : (R ? kv4_load_kernel<128, 4> : kv4_load_kernel<128, 1>);
-  kern<<<(unsigned)ceil_div(N, (R ? 4 * R : 1) * tpp), kRowThreads, 0, s>>>(pool, N, R ? R : 1, map, (uint16_t*)k,
-                                                                          (uint16_t*)v, st);
+  auto kern = pool.d == 64 ? kv4_load_kernel<64> : kv4_load_kernel<128>;
+  kern<<<(unsigned)ceil_div(N, R * kUnroll * tpp), kRowThreads, 0, s>>>(pool, N, R, map, (uint16_t*)k, (uint16_t*)v, st);
   return cudaGetLastError();
 }
 

@@ -4,7 +4,14 @@
 // A page is free when its count is 0; the call that needs pages takes the
 // lowest free ones, in the order of its entries, so that a call's result does
 // not depend on timing.  One CTA does what is ordered (checks, prefix sums, the
-// search for free pages); tables and page contents are then written by a grid.
+// search for free pages); tables and page contents are then written by a grid,
+// its programmatic dependent, 16 KB of a page's pool a CTA at a time.
+//
+// Bound: the copies by HBM (a page read and written once), small calls by the
+// two launches.  Measured: 8 sequences grown by a token and 56 forked from them
+// (62 MB read and written, 1024 pages searched) 20 us for the two calls; 32
+// sequences released and 2560 pages compacted, 643 MB read and written: 127 us,
+// of which the copies take 93 (6.9 TB/s).
 #include "msa_common.cuh"
 
 namespace msa {
