@@ -13,7 +13,7 @@ using namespace sm100;
 
 constexpr int kRowThreads = 256;
 
-// Where packed row i goes: the pool row of its sequence's token, or -1 (past the last sequence, or bad: flagged).
+// Where packed row i, of one of the sequences, goes: the pool row of its token, or -1 (bad: flagged).
 struct RowMap {
   const int32_t* cu;    // [S + 1]
   const int32_t* pos0;  // [S] token position of each sequence's first row
@@ -22,7 +22,6 @@ struct RowMap {
   int S, page;
 
   __device__ __forceinline__ int64_t row(int64_t i, DeviceStatus* st) const {
-    if (i < cu[0] || i >= cu[S]) return -1;
     int lo = 0, hi = S;  // a sequence with cu[lo] <= i < cu[lo + 1] (a search by halves ends whatever cu holds)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -49,7 +48,7 @@ struct RowMap {
 // head rows, then V's): it looks all of them up first, then has the reads of U x tpp of them in flight at a time.
 // R grows up to kRounds where the CTAs still fill the GPU.
 // 131072 tokens of 8 heads, d = 128, in and out: 258 us, 5.26 TB/s (0.78 of the measured copy rate); 604 us with U = 1,
-// which is no faster for few rows either (48 tokens in and out 10.3 us, 10.2 with U = 4: two launches' latency).
+// which is no faster for few rows either (48 tokens in and out: 10.3 and 10.2 us, two launches' latency).
 constexpr int kUnroll = 4, kRounds = 8;
 struct RowTile {
   int per_tok, tpp;
@@ -59,15 +58,25 @@ struct RowTile {
   }
 };
 
-// A call of at most kRowThreads rows has its status written by CTA 0 alone, which looks at all of them (the other
-// CTAs report nothing): it needs no clearing before the kernel, a launch of its own (a decode step's store and load
-// 12.4 -> 10.4 us on the GPU).
-__device__ __forceinline__ void report_rows(const RowMap& map, int64_t N, DeviceStatus* st) {
+// The pool rows of the CTA's `n` packed rows from i0 on; `none` for those of no sequence.
+// A call of at most kRowThreads rows has its status written by CTA 0 alone, which looks up all of them (the other CTAs
+// report nothing): the error word then needs no clearing before the kernel, a launch of its own (48 tokens in and out
+// 12.4 -> 10.2 us on the GPU).
+__device__ __forceinline__ void look_up(const RowMap& map, int64_t N, int64_t i0, int n, int64_t none, int64_t* rows,
+                                        DeviceStatus* st) {
   __shared__ unsigned int est[2];
-  DeviceStatus* own = reinterpret_cast<DeviceStatus*>(est);  // (its first two words are all that an error touches)
+  const int64_t in0 = map.cu[0], in1 = min((int64_t)map.cu[map.S], N);
+  auto row = [&](int64_t i, DeviceStatus* s) { return i >= in0 && i < in1 ? map.row(i, s) : none; };
+  if (!kv4_rows_report(N) || blockIdx.x) {
+    for (int t = threadIdx.x; t < n; t += kRowThreads) rows[t] = row(i0 + t, kv4_rows_report(N) ? nullptr : st);
+    __syncthreads();
+    return;
+  }
+  DeviceStatus* own = reinterpret_cast<DeviceStatus*>(est);  // (an error touches its first two words)
   if (threadIdx.x == 0) est[0] = est[1] = 0u;
   __syncthreads();
-  if (threadIdx.x < N) map.row(threadIdx.x, own);
+  const int64_t r = row(threadIdx.x, own);
+  if ((int)threadIdx.x < n) rows[threadIdx.x] = r;
   __syncthreads();
   if (threadIdx.x == 0) {
     st->flags = own->flags;
@@ -84,12 +93,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* 
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
-  if (kv4_rows_report(N)) {
-    if (blockIdx.x == 0) report_rows(map, N, st);
-    st = nullptr;
-  }
-  for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) rows[t] = i0 + t < N ? map.row(i0 + t, st) : -1;
-  __syncthreads();
+  look_up(map, N, i0, R * U * rt.tpp, -1, rows, st);
   const int sub = threadIdx.x / rt.per_tok;  // 0 where a token takes the whole CTA
   for (int c = threadIdx.x - sub * rt.per_tok; c < rt.per_tok; c += kRowThreads) {
     const bool on = sub < rt.tpp, is_v = c >= half;
@@ -155,16 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
   const RowTile rt(pool.H_kv, LPR);
   const int half = rt.per_tok / 2;
   const int64_t i0 = (int64_t)blockIdx.x * R * U * rt.tpp;
-  if (kv4_rows_report(N)) {
-    if (blockIdx.x == 0) report_rows(map, N, st);
-    st = nullptr;
-  }
-  const int64_t in0 = map.cu[0], in1 = map.cu[map.S];
-  for (int t = threadIdx.x; t < R * U * rt.tpp; t += kRowThreads) {
-    const int64_t i = i0 + t;
-    rows[t] = i < N && i >= in0 && i < in1 ? map.row(i, st) : -2;
-  }
-  __syncthreads();
+  look_up(map, N, i0, R * U * rt.tpp, -2, rows, st);
   const int sub = threadIdx.x / rt.per_tok;
   if (sub >= rt.tpp) return;
   for (int c = threadIdx.x - sub * rt.per_tok; c < rt.per_tok; c += kRowThreads) {
