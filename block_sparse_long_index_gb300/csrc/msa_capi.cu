@@ -493,11 +493,13 @@ static msa_status_t check_heads(int H_q, int H_kv, int d) {
   return MSA_OK;
 }
 
+constexpr int kMaxPacked = 1 << 24;  // sequences of a packed call (sums of two stay in an int)
+
 static msa_status_t check_dense_prefill(int64_t N, int S, int H_q, int H_kv, int d) {
   if (N < 1 || S < 1) return MSA_ERR_INVALID_ARGUMENT;
   msa_status_t st = check_heads(H_q, H_kv, d);
   if (st != MSA_OK) return st;
-  return N > ((int64_t)1 << 24) ? MSA_ERR_UNSUPPORTED : MSA_OK;
+  return N > ((int64_t)1 << 24) || S > kMaxPacked ? MSA_ERR_UNSUPPORTED : MSA_OK;
 }
 
 size_t msa_dense_prefill_varlen_workspace(int64_t N, int S, int H_q, int H_kv, int d) {
@@ -562,7 +564,7 @@ static msa_status_t check_kv4_rows(const void* k, const void* v, int64_t N, cons
   if (!k || !v || !cu_seqlens || !pos0 || N < 1 || S < 1) return MSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)cu_seqlens & 3u) || ((uintptr_t)pos0 & 3u))
     return MSA_ERR_INVALID_ARGUMENT;
-  return N >= (int64_t)1 << 31 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+  return N >= (int64_t)1 << 31 || S > kMaxPacked ? MSA_ERR_UNSUPPORTED : MSA_OK;
 }
 
 msa_status_t msa_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu_seqlens, int S,

@@ -419,7 +419,7 @@ msa_status_t msa_decode_noalloc(const void* q_t, const void* q_idx_t, const void
  * written: their out and lse stay as they were, whatever q, k and v hold there.
  * A cu_seqlens that breaks the rules sets the device error word
  * (MSA_ERR_BAD_INDEX) and nothing is written.  Supported: d in {64, 128},
- * H_q / H_kv in {1, 2, 4, 8}, H_kv <= 64, N <= 2^24.
+ * H_q / H_kv in {1, 2, 4, 8}, H_kv <= 64, N and S <= 2^24.
  */
 size_t msa_dense_prefill_varlen_workspace(int64_t N, int S, int H_q, int H_kv, int d);
 msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int S,
@@ -457,7 +457,8 @@ msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* 
  * one row a sequence and pos0 = the lengths so far.  Rows of no sequence are
  * passed over.  A row whose position lies outside the table, or whose page id
  * lies outside [0, n_pages), is skipped and sets the device error word
- * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.
+ * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.  N < 2^31,
+ * S <= 2^24.
  * msa_kv4_load: the same rows back, k and v [N, H_kv, d] bf16 out (exact
  *   values of the codes); a bad row reads as zeros (and sets the error word),
  *   rows of no sequence stay as they were.

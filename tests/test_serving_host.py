@@ -180,3 +180,17 @@ def test_pages_pins():
     assert p.refs == [1, 0, 0, 1, 0, 0]
     assert p.compact() == ([0, -1, -1, 1, -1, -1], 2) and p.table[2] == [0, 1] and p.data[1] == 1
     assert not p.reserve([0], [16 * 5])
+
+
+def test_limits_of_packed_calls(lib):  # noqa: F811
+    """The number of sequences stays where sums of two of them fit an int."""
+    raw, S = lib.raw(), 1 << 24
+    p = pool_of(lib)
+    for n, want in ((S, lib.MSA_ERR_WORKSPACE_TOO_SMALL), (S + 1, lib.MSA_ERR_UNSUPPORTED),
+                    ((1 << 31) - 1, lib.MSA_ERR_UNSUPPORTED)):
+        assert raw.msa_dense_prefill_varlen(FAKE, FAKE, FAKE, FAKE, n, 1000, 8, 2, 128, 0.1, FAKE, FAKE, FAKE, 0, None) == want
+        assert raw.msa_kv4_store(FAKE, FAKE, 3, FAKE, n, FAKE, FAKE, 2, ctypes.byref(p), FAKE, 0, None) == want
+        assert raw.msa_kv4_load(ctypes.byref(p), 3, FAKE, n, FAKE, FAKE, 2, FAKE, FAKE, FAKE, 0, None) == want
+    assert lib.msa_dense_prefill_varlen_workspace(1000, S, 8, 2, 128) > 4 * S
+    assert lib.msa_dense_prefill_varlen_workspace(1000, S + 1, 8, 2, 128) == 256
+    assert raw.msa_kv4_store(FAKE, FAKE, 1 << 31, FAKE, 1, FAKE, FAKE, 2, ctypes.byref(p), FAKE, 0, None) == lib.MSA_ERR_UNSUPPORTED
