@@ -91,13 +91,25 @@ class MsaDecode:
         return _c.msa_check_device_error(self.workspace, stream)
 
 
-def _check_tensor(name, t, dtype, shape):
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _check_tensor(name, t, dtype, shape, dev=None):
+    """t: contiguous, of the type and shape, on device number dev (any CUDA device where dev is None)."""
+    at = t.get_device()  # -1 on the CPU
+    if t.dtype is dtype and t.shape == shape and at >= 0 and (dev is None or at == dev) and t.is_contiguous():
         return
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype != dtype or at < 0 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if at != dev and dev is not None:
+        raise ValueError("%s is on cuda:%d, the object on cuda:%d" % (name, at, dev))
+
+
+def _device(t):
+    """The number of t's device, which has to be the current one: launches go there."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("the object is on cuda:%d, the current device is cuda:%d" % (dev, torch.cuda.current_device()))
+    return dev
 
 
 class MsaDensePrefill:
@@ -111,10 +123,11 @@ class MsaDensePrefill:
         self.lse = torch.empty((H_q, N), dtype=torch.float32, device=device)
 
     def __call__(self, q, k, v, cu_seqlens, scale=None, stream=None):
-        _check_bf16("q", q, (self.N, self.H_q, self.d))
-        _check_bf16("k", k, (self.N, self.H_kv, self.d))
-        _check_bf16("v", v, (self.N, self.H_kv, self.d))
-        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (self.S + 1,))
+        dev = _device(self.workspace)
+        _check_tensor("q", q, torch.bfloat16, (self.N, self.H_q, self.d), dev)
+        _check_tensor("k", k, torch.bfloat16, (self.N, self.H_kv, self.d), dev)
+        _check_tensor("v", v, torch.bfloat16, (self.N, self.H_kv, self.d), dev)
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (self.S + 1,), dev)
         scale = 1.0 / math.sqrt(self.d) if scale is None else scale
         _c.msa_dense_prefill_varlen(q, k, v, cu_seqlens, self.S, self.N, self.H_q, self.H_kv, self.d, scale, self.out,
                                     self.lse, self.workspace, stream=stream)
@@ -133,7 +146,7 @@ class Kv4Pool:
         self.d = 2 * half
         for name, t, last in (("k_codes", k_codes, half), ("k_scales", k_scales, 4), ("v_codes", v_codes, half),
                               ("v_scales", v_scales, 4)):
-            _check_tensor(name, t, torch.uint8, (self.n_pages, self.page_size, self.H_kv, last))
+            _check_tensor(name, t, torch.uint8, (self.n_pages, self.page_size, self.H_kv, last), k_codes.get_device())
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.c = _c.kv4_pool(k_codes, k_scales, v_codes, v_scales, self.n_pages, self.page_size, self.H_kv, self.d)
         self.workspace = torch.empty(_c.msa_kv4_workspace(), dtype=torch.uint8, device=k_codes.device)
@@ -146,29 +159,27 @@ class Kv4Pool:
     def tensors(self):
         return [self.k_codes, self.k_scales, self.v_codes, self.v_scales]
 
-    def _rows(self, cu_seqlens, pos0, page_table):
-        S = cu_seqlens.numel() - 1
-        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (S + 1,))
-        _check_tensor("pos0", pos0, torch.int32, (S,))
-        _check_tensor("page_table", page_table, torch.int32, (S, page_table.shape[-1]))
+    def _rows(self, k, v, shape, cu_seqlens, pos0, page_table):
+        S, dev = cu_seqlens.numel() - 1, _device(self.workspace)
+        _check_tensor("k", k, torch.bfloat16, shape, dev)
+        _check_tensor("v", v, torch.bfloat16, shape, dev)
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
+        _check_tensor("pos0", pos0, torch.int32, (S,), dev)
+        _check_tensor("page_table", page_table, torch.int32, (S, page_table.shape[-1]), dev)
         return S, page_table.shape[1]
 
     def store(self, k, v, cu_seqlens, pos0, page_table, stream=None):
         """Quantizes rows k, v [N, H_kv, d] into the pages of their sequences (see msa_kv4_store)."""
         N = k.shape[0]
-        _check_bf16("k", k, (N, self.H_kv, self.d))
-        _check_bf16("v", v, (N, self.H_kv, self.d))
-        S, max_pages = self._rows(cu_seqlens, pos0, page_table)
+        S, max_pages = self._rows(k, v, (N, self.H_kv, self.d), cu_seqlens, pos0, page_table)
         _c.msa_kv4_store(k, v, N, cu_seqlens, S, pos0, page_table, max_pages, self.c, self.workspace, stream=stream)
 
     def load(self, N, cu_seqlens, pos0, page_table, k=None, v=None, stream=None):
         """The rows' values as bf16 [N, H_kv, d] (see msa_kv4_load); rows of no sequence stay as k and v had them."""
-        S, max_pages = self._rows(cu_seqlens, pos0, page_table)
         shape = (N, self.H_kv, self.d)
         k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if k is None else k
         v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if v is None else v
-        _check_bf16("k", k, shape)
-        _check_bf16("v", v, shape)
+        S, max_pages = self._rows(k, v, shape, cu_seqlens, pos0, page_table)
         _c.msa_kv4_load(self.c, N, cu_seqlens, S, pos0, page_table, max_pages, k, v, self.workspace, stream=stream)
         return k, v
 
@@ -182,6 +193,8 @@ class MsaDecodeKv4:
 
     def __init__(self, pool: Kv4Pool, B, max_pages, H_q, d_I=None, Bk=128, k=16, device=None):
         device = pool.k_codes.device if device is None else device
+        if torch.device(device).index not in (None, pool.k_codes.get_device()):
+            raise ValueError("the pool is on cuda:%d" % pool.k_codes.get_device())
         self.pool, self.B, self.max_pages, self.H_q, self.d_I = pool, B, max_pages, H_q, d_I
         need = _c.msa_dense_decode_paged_kv4_workspace(B, H_q, pool.H_kv, pool.d)
         if d_I is not None:
@@ -193,9 +206,11 @@ class MsaDecodeKv4:
         self.lse = torch.empty((B, H_q), dtype=torch.float32, device=device)
 
     def _check(self, q_t, page_table, ctx_len):
-        _check_bf16("q_t", q_t, (self.B, self.H_q, self.pool.d))
-        _check_tensor("page_table", page_table, torch.int32, (self.B, self.max_pages))
-        _check_tensor("ctx_len", ctx_len, torch.int32, (self.B,))
+        dev = _device(self.workspace)
+        _check_tensor("q_t", q_t, torch.bfloat16, (self.B, self.H_q, self.pool.d), dev)
+        _check_tensor("page_table", page_table, torch.int32, (self.B, self.max_pages), dev)
+        _check_tensor("ctx_len", ctx_len, torch.int32, (self.B,), dev)
+        return dev
 
     def dense(self, q_t, page_table, ctx_len, scale=None, stream=None):
         self._check(q_t, page_table, ctx_len)
@@ -208,11 +223,11 @@ class MsaDecodeKv4:
         """q_idx_t [B, H_kv, d_I] and k_idx_pool [n_pages, page_size, d_I]: both bf16, or both uint8 (E4M3 codes)."""
         if self.d_I is None:
             raise ValueError("the MSA step needs d_I (and Bk, k) when the object is made")
-        self._check(q_t, page_table, ctx_len)
+        dev = self._check(q_t, page_table, ctx_len)
         f8 = q_idx_t.dtype == torch.uint8
         idx = torch.uint8 if f8 else torch.bfloat16
-        _check_tensor("q_idx_t", q_idx_t, idx, (self.B, self.pool.H_kv, self.d_I))
-        _check_tensor("k_idx_pool", k_idx_pool, idx, (self.pool.n_pages, self.pool.page_size, self.d_I))
+        _check_tensor("q_idx_t", q_idx_t, idx, (self.B, self.pool.H_kv, self.d_I), dev)
+        _check_tensor("k_idx_pool", k_idx_pool, idx, (self.pool.n_pages, self.pool.page_size, self.d_I), dev)
         scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
         call = _c.msa_decode_paged_kv4_fp8 if f8 else _c.msa_decode_paged_kv4
         call(q_t, q_idx_t, k_idx_pool, self.pool.c, page_table, self.max_pages, ctx_len, self.B, self.shape, scale,
@@ -233,11 +248,12 @@ class PagedCache:
     def __init__(self, page_table, ctx_len, refs, page_size, pools=()):
         n_seqs, max_pages = page_table.shape
         n_pages = refs.numel()
-        _check_tensor("page_table", page_table, torch.int32, (n_seqs, max_pages))
-        _check_tensor("ctx_len", ctx_len, torch.int32, (n_seqs,))
-        _check_tensor("refs", refs, torch.int32, (n_pages,))
+        dev = page_table.get_device()
+        _check_tensor("page_table", page_table, torch.int32, (n_seqs, max_pages), dev)
+        _check_tensor("ctx_len", ctx_len, torch.int32, (n_seqs,), dev)
+        _check_tensor("refs", refs, torch.int32, (n_pages,), dev)
         for i, t in enumerate(pools):
-            _check_tensor("pools[%d]" % i, t, t.dtype, (n_pages, page_size) + tuple(t.shape[2:]))
+            _check_tensor("pools[%d]" % i, t, t.dtype, (n_pages, page_size) + tuple(t.shape[2:]), dev)
         self.page_table, self.ctx_len, self.refs, self.page_size = page_table, ctx_len, refs, page_size
         self.pools, self.n_pages = list(pools), n_pages
         self.c = _c.pages(page_table, ctx_len, refs, max_pages, n_pages, n_seqs, page_size)
@@ -254,24 +270,25 @@ class PagedCache:
                    torch.zeros((n_pages,), dtype=torch.int32, device=device), page_size, pools)
 
     def reserve(self, seqs, new_len, stream=None):
-        n = seqs.numel()
-        _check_tensor("seqs", seqs, torch.int32, (n,))
-        _check_tensor("new_len", new_len, torch.int32, (n,))
+        n, dev = seqs.numel(), _device(self.workspace)
+        _check_tensor("seqs", seqs, torch.int32, (n,), dev)
+        _check_tensor("new_len", new_len, torch.int32, (n,), dev)
         _c.msa_pages_reserve(self.c, seqs, new_len, n, self.workspace, stream=stream)
 
     def fork(self, src, dst, stream=None):
-        n = src.numel()
-        _check_tensor("src", src, torch.int32, (n,))
-        _check_tensor("dst", dst, torch.int32, (n,))
+        n, dev = src.numel(), _device(self.workspace)
+        _check_tensor("src", src, torch.int32, (n,), dev)
+        _check_tensor("dst", dst, torch.int32, (n,), dev)
         _c.msa_pages_fork(self.c, src, dst, n, self.c_pools, len(self.pools), self.workspace, stream=stream)
 
     def free(self, seqs, stream=None):
-        n = seqs.numel()
-        _check_tensor("seqs", seqs, torch.int32, (n,))
+        n, dev = seqs.numel(), _device(self.workspace)
+        _check_tensor("seqs", seqs, torch.int32, (n,), dev)
         _c.msa_pages_free(self.c, seqs, n, self.workspace, stream=stream)
 
     def compact(self, stream=None):
         """Returns (page_map [n_pages], n_live [1]): each page's new id (-1 where it was free), and the pages held."""
+        _device(self.workspace)
         _c.msa_pages_compact(self.c, self.c_pools, len(self.pools), self.page_map, self.n_live, self.workspace,
                              stream=stream)
         return self.page_map, self.n_live

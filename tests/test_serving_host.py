@@ -194,3 +194,34 @@ def test_limits_of_packed_calls(lib):  # noqa: F811
     assert lib.msa_dense_prefill_varlen_workspace(1000, S, 8, 2, 128) > 4 * S
     assert lib.msa_dense_prefill_varlen_workspace(1000, S + 1, 8, 2, 128) == 256
     assert raw.msa_kv4_store(FAKE, FAKE, 1 << 31, FAKE, 1, FAKE, FAKE, 2, ctypes.byref(p), FAKE, 0, None) == lib.MSA_ERR_UNSUPPORTED
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The serving classes refuse tensors and calls of another device than their own (stand-ins for CUDA tensors)."""
+    from block_sparse_long_index_gb300 import Kv4Pool, PagedCache, api
+
+    class On:
+        def __init__(self, dev, shape=(3,), dtype=torch.int32, contiguous=True):
+            self.dev, self.shape, self.dtype, self.contiguous = dev, torch.Size(shape), dtype, contiguous
+
+        def get_device(self):
+            return self.dev
+
+        def is_contiguous(self):
+            return self.contiguous
+
+    api._check_tensor("x", On(1), torch.int32, (3,), 1)
+    api._check_tensor("x", On(1), torch.int32, (3,))
+    for t, dev, words in ((On(1), 0, "cuda:1"), (On(-1), -1, "contiguous CUDA"), (On(-1), None, "contiguous CUDA"),
+                          (On(0, dtype=torch.int64), 0, "contiguous CUDA int32"), (On(0, (4,)), 0, "shape"),
+                          (On(0, contiguous=False), 0, "contiguous")):
+        with pytest.raises(ValueError, match=words):
+            api._check_tensor("x", t, torch.int32, (3,), dev)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert api._device(On(1)) == 1
+    with pytest.raises(ValueError, match="cuda:0"):
+        api._device(On(0))
+    with pytest.raises(ValueError, match="CUDA"):
+        PagedCache(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        Kv4Pool(*[torch.zeros(2, 16, 1, n, dtype=torch.uint8) for n in (32, 4, 32, 4)])
