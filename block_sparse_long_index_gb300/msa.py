@@ -125,7 +125,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # (no Stream object: 1 us less)
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
