@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRo
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse,
                                                                   DeviceStatus* st) {
   constexpr int V = D / 32;  // channels of a lane
-  __shared__ float acc_s[2][4][D], l_s[2][4];
+  __shared__ float acc_s[2][4][D];
+  __shared__ float2 l_s[2][4];  // each warp's maximum and sum
   __shared__ SplitRow row_s;
   __shared__ int named[kCombThreads / 32];
   __shared__ unsigned int est[2];
@@ -810,38 +811,66 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRo
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
   if (on) {
-    for (int ct = row.c0 + lane; ct <= row.c1; ct += 32) M = fmaxf(M, part_ml[slot_of(ct)].x);
+    for (int c0 = row.c0 + w; c0 <= row.c1; c0 += 16) {  // four partials of the warp in flight
+      float2 ml[4];
+      float x[4][V];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 4
-    for (int ct = row.c0 + w; ct <= row.c1; ct += 4) {
-      const int64_t sl = slot_of(ct);
-      const float2 ml = part_ml[sl];
-      const float wt = ml.x == M ? 1.f : ex2_approx(ml.x - M);
-      L += ml.y * wt;
-      const float* p = part_o + sl * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        acc[0] += x.x * wt, acc[1] += x.y * wt, acc[2] += x.z * wt, acc[3] += x.w * wt;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        acc[0] += x.x * wt, acc[1] += x.y * wt;
+      for (int u = 0; u < 4; ++u) {
+        const int ct = c0 + 4 * u;
+        ml[u] = make_float2(-kInf, 0.f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[u][i] = 0.f;
+        if (ct <= row.c1) {
+          const int64_t sl = slot_of(ct);
+          const float* p = part_o + sl * D + lane * V;
+          ml[u] = part_ml[sl];
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            x[u][0] = y.x, x[u][1] = y.y, x[u][2] = y.z, x[u][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            x[u][0] = y.x, x[u][1] = y.y;
+          }
+        }
+      }
+      const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+      const float old = M == m ? 1.f : ex2_approx(M - m);
+      L *= old;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] *= old;
+      M = m;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float wt = ml[u].x == m ? 1.f : ex2_approx(ml[u].x - m);
+        L += ml[u].y * wt;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += x[u][i] * wt;
       }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) acc_s[warp >> 2][w][lane * V + i] = acc[i];
-    if (lane == 0) l_s[warp >> 2][w] = L;
+    if (lane == 0) l_s[warp >> 2][w] = make_float2(M, L);
   }
   __syncthreads();
   if (!on || w != 0) return;
-  L = l_s[warp >> 2][0] + l_s[warp >> 2][1] + l_s[warp >> 2][2] + l_s[warp >> 2][3];
+  float2 ml[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) ml[u] = l_s[warp >> 2][u];
+  M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float wt = ml[u].x == M ? 1.f : ex2_approx(ml[u].x - M);
+    L += ml[u].y * wt;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += acc_s[warp >> 2][u][lane * V + i] * wt;
+  }
   const bool any = L > 0.f || L != L;  // scores of -inf alone weigh nothing: out 0, lse -inf
   const float inv = any ? kSubUnscale / L : 0.f;  // (partial O comes scaled like V's values)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int ch = lane * V + i;
-    acc[i] = (acc_s[warp >> 2][0][ch] + acc_s[warp >> 2][1][ch] + acc_s[warp >> 2][2][ch] + acc_s[warp >> 2][3][ch]) * inv;
-  }
+  for (int i = 0; i < V; ++i) acc[i] *= inv;
   const int64_t hq = (int64_t)row.seq * (H_kv * gs) + row.hb * HC * gs + h;
   uint32_t* op = reinterpret_cast<uint32_t*>(out + hq * D + lane * V);
 #pragma unroll
