@@ -6,6 +6,7 @@ compute is in libmsa.so.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -112,6 +113,14 @@ def _device(t):
     return dev
 
 
+def _allocating_for(stream):
+    """Within it tensors come from the memory of `stream` (None: the current one), so that work of the current stream
+    that still uses a freed block is not overtaken by the stream's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
 class MsaDensePrefill:
     """Dense causal attention over packed prompts of N rows in all, S sequences."""
 
@@ -177,8 +186,10 @@ class Kv4Pool:
     def load(self, N, cu_seqlens, pos0, page_table, k=None, v=None, stream=None):
         """The rows' values as bf16 [N, H_kv, d] (see msa_kv4_load); rows of no sequence stay as k and v had them."""
         shape = (N, self.H_kv, self.d)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if v is None else v
+        if k is None or v is None:
+            with _allocating_for(stream):
+                k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if k is None else k
+                v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_codes.device) if v is None else v
         S, max_pages = self._rows(k, v, shape, cu_seqlens, pos0, page_table)
         _c.msa_kv4_load(self.c, N, cu_seqlens, S, pos0, page_table, max_pages, k, v, self.workspace, stream=stream)
         return k, v

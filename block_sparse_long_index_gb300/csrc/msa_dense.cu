@@ -10,10 +10,10 @@
 // operands are read once from HBM and again from L2.  Measured, against a
 // library bf16 product's 1913.8 TFLOP/s on the same GPU (1709 when it runs for
 // seconds):
-//   one prompt of 32768, 64 heads on 8, d = 128: 11.7 ms, 1500 TFLOP/s (0.78);
+//   one prompt of 32768, 64 heads on 8, d = 128: 11.6 ms, 1510 TFLOP/s (0.79);
 //   10.7 ms, 1640 TFLOP/s (0.86) for a call by itself - calls in a row reach the
 //   board's 1400 W, and the clock falls from 2.07 to 1.88 GHz;
-//   8 prompts of 167 to 16000 rows, 32 heads on 8: 1.97 ms, 1430 TFLOP/s (0.75);
+//   8 prompts of 167 to 16000 rows, 32 heads on 8: 1.95 ms, 1450 TFLOP/s (0.76);
 //   5 prompts of 1 to 640 rows, 32 heads on 8: 19.6 us, where start and end count.
 #include <math.h>
 
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // read, the maxima's exchange and P's write), the two tiles' products 2048 in
 // 3000.  Measured and slower at 32K: 8 softmax warps a tile on both at once
 // 12.4 ms; a tile's S read while the other's P is written 12.6 ms; P handed over
-// in two parts 14.5 ms; 64-key steps 12.9 ms; exponentials before the maxima's
-// exchange 13.3 ms.
+// in two parts 14.5 ms; 64-key steps 12.9 ms; exponentials under the old maximum
+// before the exchange, done again where it proves too low, 11.7 ms.
 // Warpgroups: 0 to 3 the softmax, of query tile 0 and 1 in turn: warpgroup h has
 // keys 32 h .. + 31 of every row, and the four threads of a row exchange their
 // maxima through shared memory.  (A tile's softmax lies between its S and its

@@ -47,7 +47,7 @@ struct RowMap {
 // A CTA takes R x U x tpp packed rows (tokens), tpp = the tokens that 256 threads cover at 8 channels a thread (K's
 // head rows, then V's): it looks all of them up first, then has the reads of U x tpp of them in flight at a time.
 // R grows up to kRounds where the CTAs still fill the GPU.
-// 131072 tokens of 8 heads, d = 128, in and out: 258 us, 5.26 TB/s (0.78 of the measured copy rate); 604 us with U = 1,
+// 131072 tokens of 8 heads, d = 128, in and out: 260 us, 5.23 TB/s (0.77 of the measured copy rate); 604 us with U = 1,
 // which is no faster for few rows either (48 tokens in and out: 10.3 and 10.2 us, two launches' latency).
 constexpr int kUnroll = 4, kRounds = 8;
 struct RowTile {
@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
 // mma.sync, not tcgen05: a group's 8 query heads fill an n = 8 tile, where
 // tcgen05's 128-row tiles would be 15/16 empty, and codes would have to be
 // expanded into shared memory instead of registers.  Measured, 64 heads on 8,
-// d = 128: 4 sequences of 2^20 tokens 830 us, 5.5 TB/s (0.81 of the measured
-// copy rate); 48 sequences of some 12000, 32 heads on 8: 84 us, 4.15 TB/s (0.61,
-// of which some 12 us are the start and the combine); one of 1500 tokens:
-// 12.3 us, a chain of round trips.
+// d = 128: 4 sequences of 2^20 tokens 823 us, 5.5 TB/s (0.82 of the measured
+// copy rate); 48 sequences of 1200 to 12000, 32 heads on 8: 84 us, 4.2 TB/s
+// (0.62, of which some 10 us are the start and the combine); one of 1500 tokens:
+// 10.4 us, a chain of round trips.
 constexpr int kUnit = 16;
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv4_dense_decode_kernel(
 
 // Merges the partials of the rows that CTAs share: a CTA per (row, two heads), 4 warps a head, each with every 4th
 // partial.  Row blockIdx.x is that of the blockIdx.x-th record that names one; CTA 0 also sums up the errors.  (Rows
-// found by searching the lengths and a CTA a row took 107 us instead of 84 at 48 sequences of some 12000 tokens.)
+// found by searching the lengths and a CTA a row took 107 us instead of 84 at 48 sequences of 1200 to 12000 tokens.)
 template <int D>
 __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRow* __restrict__ rows, int n_cta, int H_kv,
                                                                   int HC, int gs, const float* __restrict__ part_o,
@@ -930,7 +930,7 @@ cudaError_t launch_dense_decode_t(const void* q, const Kv4Pool& pool, const Cach
 }
 
 // Heads of a CTA: all of up to 8, so that a token's scales come as one run; for H_kv > 4 always 8 (8 heads,
-// 4 sequences of 2^20 tokens: 1303 us with 4 a CTA, 829 with 8; 48 of some 12000: 128 and 84), for fewer the next power
+// 4 sequences of 2^20 tokens: 1303 us with 4 a CTA, 829 with 8; 48 of 1200 to 12000: 128 and 84), for fewer the next power
 // of two, the warps left over sharing a head's tokens.
 int heads_per_cta(int H_kv) { return H_kv > 4 ? 8 : H_kv > 2 ? 4 : H_kv; }
 

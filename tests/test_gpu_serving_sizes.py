@@ -260,3 +260,25 @@ def test_captured_step():
     assert a.cache.ctx_len.tolist() == [n + 20 for n in lens]
     n = [x + 20 for x in lens]
     ref.check_attention(*a.dense, *dense_ref(a.pool, q, a.cache.page_table, n, 0.125), d, max(n))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_load_allocates_for_its_stream(handle):
+    """Rows that a call on another stream makes do not take memory that the current stream still reads."""
+    from block_sparse_long_index_gb300 import Kv4Pool
+    N, H, d, page = 4096, 2, 128, 64
+    pool = Kv4Pool.empty(N // page, page, H, d)
+    table = i32([list(range(N // page))])
+    x = torch.randn(N, H, d, device="cuda").to(torch.bfloat16)
+    pool.store(x, x, cu_of([N]), i32([0]), table)
+    want = pool.load(N, cu_of([N]), i32([0]), table)[0].clone()
+    cu, pos, s = cu_of([N]), i32([0]), torch.cuda.Stream()
+    old = torch.full((N, H, d), 3.0, device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some 10 ms on the current stream
+    seen = old.clone()
+    del old  # its block is free for the current stream, which still has to read it
+    k, v = pool.load(N, cu, pos, table, stream=s.cuda_stream if handle else s)
+    torch.cuda.synchronize()
+    assert torch.equal(k, want) and torch.equal(v, want)
+    assert bool((seen == 3.0).all())
