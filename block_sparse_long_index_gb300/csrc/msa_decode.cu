@@ -345,8 +345,13 @@ __device__ __forceinline__ uint64_t merged_key(const uint64_t* sl, int splits, i
 // KV4: K and V rows come from 4-bit pools (paged) and are expanded to their
 // exact bf16 values, K's words in registers on their way into the B fragments
 // and V's on their way into shared memory; the rest is the same arithmetic.
+// Blocks of 64 keys leave a CTA little to read, so what counts is that all CTAs
+// run at once: held to 72 registers, seven of an SM do instead of five (16
+// sequences, 8 groups, k = 8: 28.6 -> 24.3 us a step).  With blocks of 128 the
+// reads in flight count more: 4 sequences of 2^20 tokens, k = 16, take 188 us
+// with all the registers that they need and 192 with seven CTAs an SM.
 template <int D, int BK, bool PAGED, int LPL, bool KV4 = false>
-__global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __restrict__ q_t,
+__global__ void __launch_bounds__(128, !KV4 ? 0 : BK == 64 ? 7 : 1) decode_attn_kernel(const uint16_t* __restrict__ q_t,
                                                           const uint16_t* __restrict__ k_cache,
                                                           const uint16_t* __restrict__ v_cache,
                                                           const int32_t* __restrict__ ctx_len,
@@ -528,9 +533,12 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
     cp_async_wait<0>();
     __syncthreads();
     // O = P V over this warp's keys
-    float oacc[D / 8][4];
+    // (KV4: O^T = V^T P^T, whose fragments are the same registers: 16 channels x 8 heads fill an accumulator that the
+    // other form leaves half empty)
+    constexpr int NO = KV4 ? D / 16 : D / 8;
+    float oacc[NO][4];
 #pragma unroll
-    for (int nd = 0; nd < D / 8; ++nd) oacc[nd][0] = oacc[nd][1] = oacc[nd][2] = oacc[nd][3] = 0.f;
+    for (int nd = 0; nd < NO; ++nd) oacc[nd][0] = oacc[nd][1] = oacc[nd][2] = oacc[nd][3] = 0.f;
 #pragma unroll
     for (int ks2 = 0; ks2 < NT / 2; ++ks2) {
       const uint32_t a[4] = {pa[ks2][0], 0u, pa[ks2][1], 0u};
@@ -541,25 +549,37 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
         const int chunk = nd + (lane >> 4);
         uint32_t r0, r1, r2, r3;
         ldmatrix_x4_trans(r0, r1, r2, r3, v_s + key * D + ((chunk ^ (key & (C8 - 1))) * 8));
-        const uint32_t b0[2] = {r0, r1}, b1[2] = {r2, r3};
-        mma_bf16_16816(oacc[nd], a, b0);
-        mma_bf16_16816(oacc[nd + 1], a, b1);
+        if constexpr (KV4) {
+          const uint32_t vt[4] = {r0, r2, r1, r3}, pt[2] = {pa[ks2][0], pa[ks2][1]};
+          mma_bf16_16816(oacc[nd / 2], vt, pt);
+        } else {
+          const uint32_t b0[2] = {r0, r1}, b1[2] = {r2, r3};
+          mma_bf16_16816(oacc[nd], a, b0);
+          mma_bf16_16816(oacc[nd + 1], a, b1);
+        }
       }
     }
     // sum the warps' partial O in shared memory (over the V rows, which are no longer read)
     __syncthreads();
     float* red_o = reinterpret_cast<float*>(v_s);  // [4 warps][8 rows][D]
+    // KV4: channel dc of head hh sits at dc ^ 8 (hh / 2): the lanes of a store then hit distinct banks
+    auto o_at = [&](int hh, int dc) { return hh * D + (KV4 ? dc ^ (hh >> 1) << 3 : dc); };
 #pragma unroll
-    for (int nd = 0; nd < D / 8; ++nd) {
-      red_o[(warp * 8 + gq) * D + nd * 8 + 2 * tq] = oacc[nd][0];
-      red_o[(warp * 8 + gq) * D + nd * 8 + 2 * tq + 1] = oacc[nd][1];
+    for (int nd = 0; nd < NO; ++nd) {
+      if constexpr (KV4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red_o[warp * 8 * D + o_at(2 * tq + (e & 1), nd * 16 + gq + 8 * (e >> 1))] = oacc[nd][e];
+      } else {
+        red_o[(warp * 8 + gq) * D + nd * 8 + 2 * tq] = oacc[nd][0];
+        red_o[(warp * 8 + gq) * D + nd * 8 + 2 * tq + 1] = oacc[nd][1];
+      }
     }
     __syncthreads();
     for (int i = tid; i < gs * D; i += blockDim.x) {
       const int hh = i / D, dc = i % D;
       const float L = red_l[0][hh] + red_l[1][hh] + red_l[2][hh] + red_l[3][hh];
-      const float o = red_o[(0 * 8 + hh) * D + dc] + red_o[(1 * 8 + hh) * D + dc] + red_o[(2 * 8 + hh) * D + dc] +
-                      red_o[(3 * 8 + hh) * D + dc];
+      const int at = o_at(hh, dc);
+      const float o = red_o[at] + red_o[8 * D + at] + red_o[16 * D + at] + red_o[24 * D + at];
       po[(int64_t)hh * k * D + dc] = o / L;
     }
     if (tid < gs) {
@@ -591,22 +611,23 @@ __global__ void __launch_bounds__(128) decode_attn_kernel(const uint16_t* __rest
       lse[(int64_t)seq * H_q + g * gs + hh] = L > 0.f ? M + logf(L) : __int_as_float(0xff800000);
   }
   __syncthreads();
-  // thread -> (head, 4 columns); the partial loads of 16 slots are all in flight before the sums
+  // thread -> (head, 4 columns); the partial loads of NB slots are all in flight before the sums
+  constexpr int NB = KV4 && BK == 64 ? 8 : 16;
   const float* go = part_o + ((int64_t)seq * H_q + g * gs) * k * D;  // [gs][k][D]
   for (int i = tid; i < gs * (D / 4); i += blockDim.x) {
     const int hh = i / (D / 4), dc = 4 * (i % (D / 4));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < k; s0 += 16) {
-      float4 o[16];
+    for (int s0 = 0; s0 < k; s0 += NB) {
+      float4 o[NB];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < NB; ++j) {
         const int s = s0 + j;
         const bool use = s < k && w_s[hh][s < k ? s : 0] != 0.f;
         o[j] = use ? __ldcg(reinterpret_cast<const float4*>(go + ((int64_t)hh * k + s) * D + dc))
                    : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < NB; ++j) {
         const int s = s0 + j;
         const float w = s < k ? w_s[hh][s] : 0.f;
         acc.x += w * o[j].x;
