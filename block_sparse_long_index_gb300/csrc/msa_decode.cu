@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(128, !KV4 ? 0 : BK == 64 ? 7 : 1) decode_attn_
   // the group's candidate lists first; then V rows [BK][D]; later the warps' partial O
   extern __shared__ __align__(16) uint16_t v_s[];
   __shared__ float red_m[4][8], red_l[4][8];
-  __shared__ float w_s[8][32];  // combine weights [head][slot]
+  __shared__ float w_s[8][32];  // combine weights [head][slot], -1 for a slot without a partial (which adds zeros)
   __shared__ int s_last;
   __shared__ int32_t s_blk;
   __shared__ int64_t krow_s[PAGED ? BK : 1];  // cache row of each key of the block (paged caches)
@@ -601,14 +601,17 @@ __global__ void __launch_bounds__(128, !KV4 ? 0 : BK == 64 ? 7 : 1) decode_attn_
     float M = v;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float w = M == __int_as_float(0xff800000) || v == __int_as_float(0xff800000) ? 0.f : __expf(v - M);
+    // the maximum drops a NaN, its weight does not: e^(NaN - M) is NaN whatever M is, and L with it
+    const bool none = v == __int_as_float(0xff800000);  // an empty slot: no partial was written
+    const float w = none ? 0.f : __expf(v - M);
     float L = w;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    w_s[hh][lane] = w * inv;
+    const bool any = L > 0.f || L != L;
+    const float inv = any ? 1.f / L : 0.f;
+    w_s[hh][lane] = none ? -1.f : w * inv;
     if (lane == 0 && lse)
-      lse[(int64_t)seq * H_q + g * gs + hh] = L > 0.f ? M + logf(L) : __int_as_float(0xff800000);
+      lse[(int64_t)seq * H_q + g * gs + hh] = any ? M + logf(L) : __int_as_float(0xff800000);
   }
   __syncthreads();
   // thread -> (head, 4 columns); the partial loads of NB slots are all in flight before the sums
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(128, !KV4 ? 0 : BK == 64 ? 7 : 1) decode_attn_
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int s = s0 + j;
-        const bool use = s < k && w_s[hh][s < k ? s : 0] != 0.f;
+        const bool use = s < k && !(w_s[hh][s < k ? s : 0] < 0.f);  // (a weight that underflowed still meets its NaNs)
         o[j] = use ? __ldcg(reinterpret_cast<const float4*>(go + ((int64_t)hh * k + s) * D + dc))
                    : make_float4(0.f, 0.f, 0.f, 0.f);
       }

@@ -1,0 +1,146 @@
+"""Keys and values that are not finite in the decode steps: a NaN that is attended reaches the outputs of its heads,
+one that is not attended reaches none."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_kv4 import i32, random_pool, table_of
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [
+    # ctx, k, token with the NaN, H_q, H_kv, d, Bk, page; sequence 1 stays clean
+    ([50, 40], 4, 20, 8, 2, 64, 64, 16),       # one valid slot of several
+    ([200, 190], 1, 199, 16, 2, 128, 128, 64),  # one slot
+    ([300, 500], 8, 299, 16, 2, 128, 64, 32),   # the local block of several
+    ([300, 500], 8, 70, 8, 8, 64, 64, 16),      # another chosen block
+    ([700, 900], 8, 3, 4, 4, 128, 128, 48),
+]
+
+
+def step_inputs(ctx, H_q, H_kv, d, page, index):
+    from block_sparse_long_index_gb300 import msa
+    counts = [-(-c // page) for c in ctx]
+    n_pages, B = sum(counts) + 2, len(ctx)
+    pool, table = random_pool(n_pages, page, H_kv, d), table_of(counts, max(counts), n_pages)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, qi, ki = rnd(B, H_q, d), rnd(B, H_kv, 64), rnd(n_pages, page, 64)
+    if index == "fp8":
+        codes = [torch.empty(t.shape, dtype=torch.uint8, device="cuda") for t in (qi, ki)]
+        for t, c in zip((qi, ki), codes):
+            msa.msa_quantize_e4m3(t, t.numel(), 16.0, c)
+        qi, ki = codes
+    return pool, table, q, qi, ki
+
+
+def step(pool, table, q, qi, ki, ctx, Bk, k):
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    run = MsaDecodeKv4(pool, len(ctx), table.shape[1], q.shape[1], d_I=64, Bk=Bk, k=k)
+    run.out.fill_(7.0)
+    run.lse.fill_(7.0)
+    got = [t.clone() for t in run(q, qi, ki, table, i32(ctx), 0.1)]
+    assert run.device_status() == 0
+    return got
+
+
+def place(table, b, token, page):
+    return int(table[b, token // page]), token % page
+
+
+@pytest.mark.parametrize("index", ["bf16", "fp8"])
+@pytest.mark.parametrize("ctx,k,token,H_q,H_kv,d,Bk,page", SHAPES)
+def test_step_over_nan_groups(ctx, k, token, H_q, H_kv, d, Bk, page, index):
+    pool, table, q, qi, ki = step_inputs(ctx, H_q, H_kv, d, page, index)
+    out, lse, blk = step(pool, table, q, qi, ki, ctx, Bk, k)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    gs, g = H_q // H_kv, H_kv - 1
+    hit = slice(g * gs, g * gs + gs)
+    at = place(table, 0, token, page)
+    # a group of K: every score of the token is NaN, so everything of its heads is
+    keep = pool.k_scales[at[0], at[1], g, 2].clone()
+    pool.k_scales[at[0], at[1], g, 2] = 255
+    o, l, b = step(pool, table, q, qi, ki, ctx, Bk, k)
+    assert token // Bk in blk[0, g].tolist() and torch.equal(b, blk)
+    assert bool(torch.isnan(o[0, hit]).all()) and bool(torch.isnan(l[0, hit]).all())
+    o[0, hit], l[0, hit] = out[0, hit], lse[0, hit]
+    assert torch.equal(o, out) and torch.equal(l, lse)
+    pool.k_scales[at[0], at[1], g, 2] = keep
+    # a group of V: its channels alone
+    pool.v_scales[at[0], at[1], g, 1] = 255
+    o, l, _ = step(pool, table, q, qi, ki, ctx, Bk, k)
+    c = slice(d // 4, d // 2)
+    assert bool(torch.isnan(o[0, hit, c]).all()) and torch.equal(l, lse)
+    o[0, hit, c] = out[0, hit, c]
+    assert torch.equal(o, out)
+
+
+def test_step_leaves_out_nan_groups_that_it_does_not_attend():
+    """Blocks that were not chosen, and tokens past the length."""
+    ctx, Bk, k, page = [1000, 130], 64, 3, 16
+    pool, table, q, qi, ki = step_inputs(ctx, 8, 2, 64, page, "bf16")
+    out, lse, blk = step(pool, table, q, qi, ki, ctx, Bk, k)
+    for b, n in enumerate(ctx):
+        for t in range(table.shape[1] * page):
+            if table[b, t // page] < 0:
+                continue
+            for g in range(2):
+                if t >= n or t // Bk not in blk[b, g].tolist():
+                    p, r = place(table, b, t, page)
+                    pool.k_scales[p, r, g] = 255
+                    pool.v_scales[p, r, g] = 255
+    o, l, b = step(pool, table, q, qi, ki, ctx, Bk, k)
+    assert torch.equal(o, out) and torch.equal(l, lse) and torch.equal(b, blk)
+
+
+def test_step_from_stored_infinities():
+    """What store makes of an infinity in K is a NaN of the step, whole context or chosen blocks."""
+    from block_sparse_long_index_gb300 import Kv4Pool, MsaDecodeKv4
+    N, H_kv, d, page = 90, 2, 128, 16
+    pool = Kv4Pool.empty(6, page, H_kv, d)
+    k, v = (torch.randn(N, H_kv, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k[33, 1, 5] = math.inf
+    table, cu, pos = i32([[3, 0, 5, 1, 4, 2]]), i32([0, N]), i32([0])
+    pool.store(k, v, cu, pos, table)
+    q, qi = torch.randn(1, 4, d, device="cuda").to(torch.bfloat16), torch.randn(1, H_kv, 64, device="cuda").to(torch.bfloat16)
+    ki = torch.randn(6, page, 64, device="cuda").to(torch.bfloat16)
+    run = MsaDecodeKv4(pool, 1, 6, 4, d_I=64, Bk=64, k=2)
+    for o, l in (run.dense(q, table, i32([N]), 0.1), run(q, qi, ki, table, i32([N]), 0.1)[:2]):
+        assert bool(torch.isnan(o[0, 2:]).all()) and bool(torch.isnan(l[0, 2:]).all())
+        assert bool(torch.isfinite(o[0, :2]).all()) and bool(torch.isfinite(l[0, :2]).all())
+
+
+@pytest.mark.parametrize("ctx", [[40, 30], [200, 90]])
+def test_bf16_steps_over_nan(ctx):
+    """The same of the steps over bf16 caches, contiguous and paged."""
+    from block_sparse_long_index_gb300 import msa
+    B, H_q, H_kv, d, N = 2, 8, 2, 64, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, qi, ki, k, v = rnd(B, H_q, d), rnd(B, H_kv, 64), rnd(B, N, 64), rnd(B, N, H_kv, d), rnd(B, N, H_kv, d)
+    shape = msa.shape(N, H_q, H_kv, d, 64, 64, 4)
+    ws = torch.empty(msa.msa_decode_workspace(B, shape), dtype=torch.uint8, device="cuda")
+    table = i32([list(range(16)), list(range(16, 32))])
+
+    def both():
+        got = []
+        for paged in (False, True):
+            o, l = torch.empty_like(q), torch.empty(B, H_q, device="cuda")
+            if paged:
+                msa.msa_decode_paged(q, qi, ki, k, v, table, 16, 32, 16, i32(ctx), B, shape, 0.1, o, l, None, ws)
+            else:
+                msa.msa_decode(q, qi, ki, k, v, i32(ctx), B, shape, 0.1, o, l, None, ws)
+            assert msa.msa_check_device_error(ws) == 0
+            got.append((o, l))
+        assert torch.equal(got[0][0].isnan(), got[1][0].isnan())
+        return got
+
+    clean = both()
+    k[0, 11, 1, 7] = math.nan
+    for (o, l), (co, cl) in zip(both(), clean):
+        assert bool(torch.isnan(o[0, 4:]).all()) and bool(torch.isnan(l[0, 4:]).all())
+        o[0, 4:], l[0, 4:] = co[0, 4:], cl[0, 4:]
+        assert torch.equal(o, co) and torch.equal(l, cl)
