@@ -342,6 +342,12 @@ __device__ __forceinline__ uint64_t merged_key(const uint64_t* sl, int splits, i
 // per head: M = max lse_s, w_s = e^(lse_s - M) / sum e^(lse_s - M),
 // out = sum w_s O_s, lse = M + ln sum e^(lse_s - M).
 //
+// Contiguous bf16 caches with d = 64 are held to 96 registers, five CTAs an SM:
+// left to itself the compiler takes 99, and with four CTAs an SM 48 sequences
+// of 6000 tokens (32 heads on 8, k = 16) take 72.2 us instead of 64.2 and 10 of
+// 9000 (64 on 8, k = 8) 20.7 instead of 19.5 (8 of them, which fit either way,
+// 17.4 and 18.6).  The other bf16 forms stay below 97 by themselves.
+//
 // KV4: K and V rows come from 4-bit pools (paged) and are expanded to their
 // exact bf16 values, K's words in registers on their way into the B fragments
 // and V's on their way into shared memory; the rest is the same arithmetic.
@@ -351,7 +357,8 @@ __device__ __forceinline__ uint64_t merged_key(const uint64_t* sl, int splits, i
 // reads in flight count more: 4 sequences of 2^20 tokens, k = 16, take 188 us
 // with all the registers that they need and 192 with seven CTAs an SM.
 template <int D, int BK, bool PAGED, int LPL, bool KV4 = false>
-__global__ void __launch_bounds__(128, !KV4 ? 0 : BK == 64 ? 7 : 1) decode_attn_kernel(const uint16_t* __restrict__ q_t,
+__global__ void __launch_bounds__(128, KV4 ? (BK == 64 ? 7 : 1) : D == 64 && !PAGED ? 5 : 0)
+    decode_attn_kernel(const uint16_t* __restrict__ q_t,
                                                           const uint16_t* __restrict__ k_cache,
                                                           const uint16_t* __restrict__ v_cache,
                                                           const int32_t* __restrict__ ctx_len,
