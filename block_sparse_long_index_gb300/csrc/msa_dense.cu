@@ -567,7 +567,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) dense_prefill_kernel(
         const int t = it.t0 + q * PT + pos;
         const bool live = t < it.len;
         const bool bad = poison[r % kPoisonSlots] == r + 1;
-        const float inv = 1.f / sum;
+        // scores of -inf alone leave a sum of 0: out 0 (0 / 0 otherwise), lse -inf
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int64_t grow = (int64_t)it.row0 + t;
         const int h = it.g * GS + hh;
         uint4* orow = reinterpret_cast<uint4*>(out + (grow * H_q + h) * D);

@@ -415,6 +415,8 @@ msa_status_t msa_decode_noalloc(const void* q_t, const void* q_idx_t, const void
  *   cu_seqlens [S+1] int32 (device), S >= 1
  *   out        [N, H_q, d] bf16 out
  *   lse        [H_q, N] fp32 out: natural-log log-sum-exp of the scaled scores
+ * A key whose score is -inf weighs 0; a row that sees no other key has out 0 and
+ * lse -inf.  A NaN score makes the row's out and lse of that head NaN.
  * Rows of no sequence (past cu_seqlens[S]) are neither read into a result nor
  * written: their out and lse stay as they were, whatever q, k and v hold there.
  * A cu_seqlens that breaks the rules sets the device error word
@@ -493,7 +495,8 @@ msa_status_t msa_kv4_load(const msa_kv4_pool_t* pool, int64_t N, const int32_t* 
  * ctx_len outside [0, max_pages * page_size] counts as 0 and sets the device
  * error word; so does a page id outside [0, n_pages), read as page 0.
  * Scores, softmax and sums are fp32; probabilities are rounded to bf16 for the
- * product with V.  Supported: H_q / H_kv in {1, 2, 4, 8}.
+ * product with V.  Scores of -inf and NaN count as in msa_dense_prefill_varlen.
+ * Supported: H_q / H_kv in {1, 2, 4, 8}.
  *
  * msa_decode_paged_kv4, msa_decode_paged_kv4_fp8: msa_decode_paged and
  * msa_decode_paged_fp8 with K and V in a 4-bit pool (index keys stay in their

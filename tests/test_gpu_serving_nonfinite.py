@@ -1,11 +1,13 @@
-"""Keys and values that are not finite in the decode steps: a NaN that is attended reaches the outputs of its heads,
-one that is not attended reaches none."""
+"""Keys and values that are not finite: a NaN that is attended reaches the outputs of its heads, one that is not
+attended reaches none; a key whose score is -inf weighs nothing, and a row without another is like an empty one."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_kv4 import i32, random_pool, table_of
+import serving_ref as ref
+from test_gpu_dense_prefill import make, run
+from test_gpu_kv4 import dense_ref, i32, random_pool, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +146,75 @@ def test_bf16_steps_over_nan(ctx):
         assert bool(torch.isnan(o[0, 4:]).all()) and bool(torch.isnan(l[0, 4:]).all())
         o[0, 4:], l[0, 4:] = co[0, 4:], cl[0, 4:]
         assert torch.equal(o, co) and torch.equal(l, cl)
+
+
+# ---------------------------------------------------------------- scores of -inf
+def seen_attention(q, k, v, lens, dead, scale):
+    """ref.dense_prefill with the tokens marked in `dead` [N] taken out of every row's keys."""
+    N, H_q, d = q.shape
+    gs = H_q // k.shape[1]
+    k = torch.where(dead[:, None, None], 0, k.double())
+    out, A = (torch.zeros(N, H_q, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, S = torch.full((N, H_q), -math.inf, dtype=torch.float64, device="cuda"), torch.zeros(N, H_q, dtype=torch.float64, device="cuda")
+    a = 0
+    for n in lens:
+        r = slice(a, a + n)
+        mask = torch.ones(n, n, dtype=torch.bool, device="cuda").tril() & ~dead[None, r]
+        some = mask.any(1)
+        for h in range(H_q if bool(some.any()) else 0):
+            kk, vv, qq = k[r, h // gs], v[r, h // gs].double(), q[r, h].double()
+            x = (qq @ kk.T * scale).masked_fill(~mask, -math.inf)[some]
+            ls = torch.logsumexp(x, 1)
+            p = torch.exp(x - ls[:, None])
+            rows = torch.arange(a, a + n, device="cuda")[some]
+            out[rows, h], lse[rows, h], A[rows, h] = p @ vv, ls, p @ vv.abs()
+            S[rows, h] = (qq.abs() @ kk.abs().T).masked_fill(~mask, 0).amax(1)[some] * scale
+        a += n
+    return out, lse, A, S
+
+
+@pytest.mark.parametrize("H_q,H_kv,d", [(8, 1, 128), (2, 2, 64), (4, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("lens,dead", [
+    ([1], [(0, 1)]),                       # one row
+    ([1, 40, 1], [(0, 1), (1, 6), (41, 42)]),
+    ([400], [(0, 256)]),                   # the first key tiles, and whole items where a tile holds few positions
+    ([300], [(128, 256)]),                 # a tile in the middle
+    ([140, 270], [(0, 140), (140, 145), (270, 410)]),
+])
+def test_prefill_scores_of_minus_infinity(lens, dead, H_q, H_kv, d):
+    q, k, v, cu = make(lens, H_q, H_kv, d)
+    q[:, :, 3] = 1.0
+    marked = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+    for a, b in dead:
+        marked[a:b] = True
+    k[marked, :, 3] = -math.inf
+    plan, out, lse = run(q, k, v, cu, 0.1)
+    assert plan.device_status() == 0
+    o, l, A, S = seen_attention(q, k, v, lens, marked, 0.1)
+    none = l[:, 0] == -math.inf
+    assert bool(none.any()) == (dead[0][0] == 0)
+    assert bool((out[none] == 0).all()) and bool((lse.T[none] == -math.inf).all())
+    ref.check_attention(out, lse.T, o, l, A, S, d, max(lens))
+
+
+@pytest.mark.parametrize("d,H_kv", [(64, 1), (128, 2), (64, 8)])
+@pytest.mark.parametrize("ctx", [[1, 5, 0], [16, 300, 31], [9000, 40, 7000]])
+def test_dense_decode_scores_of_minus_infinity(ctx, H_kv, d):
+    """Rows that one CTA holds and rows that several share.  (The query's infinity meets codes of one sign.)"""
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    page = 16
+    counts = [-(-c // page) for c in ctx]
+    pool, table = random_pool(sum(counts) + 1, page, H_kv, d), table_of(counts, max(counts), sum(counts) + 1)
+    pool.k_codes[..., 0] |= 0xF  # channel 0: the largest code
+    q = torch.randn(3, 4 * H_kv, d, device="cuda").to(torch.bfloat16)
+    plan = MsaDecodeKv4(pool, 3, table.shape[1], 4 * H_kv)
+    want = [t[:, ::2] for t in dense_ref(pool, q, table, ctx, 0.1)]
+    q[:, 1::2, 0] = -math.inf
+    plan.out.fill_(7.0)
+    plan.lse.fill_(7.0)
+    out, lse = plan.dense(q, table, i32(ctx), 0.1)
+    assert plan.device_status() == 0
+    assert bool((out[:, 1::2] == 0).all()) and bool((lse[:, 1::2] == -math.inf).all())
+    # (not the bits of a call without them: a warp moves the maxima that its 8 heads' sums refer to together, and any
+    # reference within 2^8 gives the same sums up to the roundings that the tolerance counts)
+    ref.check_attention(out[:, ::2], lse[:, ::2], *want, d, max(ctx))
