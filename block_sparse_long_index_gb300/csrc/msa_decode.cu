@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(128, KV4 ? (BK == 64 ? 7 : 1) : D == 64 && !PA
   // the group's candidate lists first; then V rows [BK][D]; later the warps' partial O
   extern __shared__ __align__(16) uint16_t v_s[];
   __shared__ float red_m[4][8], red_l[4][8];
-  __shared__ float w_s[8][32];  // combine weights [head][slot], -1 for a slot without a partial (which adds zeros)
+  __shared__ float w_s[8][32];  // combine weights [head][slot], -1 for an empty slot (which adds zeros)
   __shared__ int s_last;
   __shared__ int32_t s_blk;
   __shared__ int64_t krow_s[PAGED ? BK : 1];  // cache row of each key of the block (paged caches)
@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(128, KV4 ? (BK == 64 ? 7 : 1) : D == 64 && !PA
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (tq == 0) red_m[warp][gq] = mx;
     __syncthreads();
-    const float m = fmaxf(fmaxf(red_m[0][gq], red_m[1][gq]), fmaxf(red_m[2][gq], red_m[3][gq]));
+    const float mb = fmaxf(fmaxf(red_m[0][gq], red_m[1][gq]), fmaxf(red_m[2][gq], red_m[3][gq]));
+    // scores of -inf alone weigh 0: the block's sum is 0, its lse -inf, and the merge takes the slot as empty
+    const float m = mb == __int_as_float(0xff800000) ? 0.f : mb;
     float ls = 0.f;
     uint32_t pa[NT / 2][2];  // P as A fragments of the P V k-steps (16 keys each)
 #pragma unroll
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(128, KV4 ? (BK == 64 ? 7 : 1) : D == 64 && !PA
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     // the maximum drops a NaN, its weight does not: e^(NaN - M) is NaN whatever M is, and L with it
-    const bool none = v == __int_as_float(0xff800000);  // an empty slot: no partial was written
+    const bool none = v == __int_as_float(0xff800000);  // an empty slot (whose partial O is not read)
     const float w = none ? 0.f : __expf(v - M);
     float L = w;
 #pragma unroll

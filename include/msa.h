@@ -283,7 +283,8 @@ msa_status_t msa_prefill_varlen(const void* q, const void* k, const void* v, con
  *   lse          [B, H_q] fp32 out (nullable)
  *   block_idx    [B, G, k] int32 out (nullable): the sets chosen
  * ctx_len values outside [1, N] set the device error word; that sequence's
- * outputs are zero.
+ * outputs are zero.  A key whose score is -inf weighs 0; a head that attends to
+ * no other key has out 0 and lse -inf.  A NaN score makes out and lse NaN.
  */
 size_t msa_decode_workspace(int B, const msa_shape_t* shape);
 msa_status_t msa_decode(const void* q_t, const void* q_idx_t, const void* k_idx_cache, const void* k_cache,

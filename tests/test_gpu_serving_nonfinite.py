@@ -218,3 +218,48 @@ def test_dense_decode_scores_of_minus_infinity(ctx, H_kv, d):
     # (not the bits of a call without them: a warp moves the maxima that its 8 heads' sums refer to together, and any
     # reference within 2^8 gives the same sums up to the roundings that the tolerance counts)
     ref.check_attention(out[:, ::2], lse[:, ::2], *want, d, max(ctx))
+
+
+@pytest.mark.parametrize("index", ["bf16", "fp8"])
+@pytest.mark.parametrize("ctx,k,H_q,H_kv,d,Bk,page", [([1, 50], 3, 8, 2, 64, 64, 16), ([200, 700], 1, 16, 2, 128, 128, 64),
+                                                      ([300, 900], 8, 8, 8, 128, 64, 32)])
+def test_step_scores_of_minus_infinity(ctx, k, H_q, H_kv, d, Bk, page, index):
+    pool, table, q, qi, ki = step_inputs(ctx, H_q, H_kv, d, page, index)
+    pool.k_codes[..., 0] |= 0xF  # channel 0: the largest code
+    want, want_lse, blk = step(pool, table, q, qi, ki, ctx, Bk, k)
+    q[1, ::2, 0] = -math.inf
+    out, lse, b = step(pool, table, q, qi, ki, ctx, Bk, k)
+    assert bool((out[1, ::2] == 0).all()) and bool((lse[1, ::2] == -math.inf).all())
+    want[1, ::2], want_lse[1, ::2] = 0, -math.inf
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(b, blk)  # (a head has its own maximum here)
+
+
+def test_bf16_step_blocks_of_minus_infinity():
+    """A chosen block whose scores are all -inf adds nothing to the others."""
+    from block_sparse_long_index_gb300 import msa
+    B, H_q, H_kv, d, N = 2, 8, 2, 128, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, qi, ki, k, v = rnd(B, H_q, d), rnd(B, H_kv, 64), rnd(B, N, 64), rnd(B, N, H_kv, d), rnd(B, N, H_kv, d)
+    q[:, :, 3] = 1.0
+    k[0, 64:128, :, 3] = -math.inf
+    k[0, 200:, :, 3] = -math.inf  # a part of a block
+    k[1, :, 1, 3] = -math.inf     # every key of a head
+    shape = msa.shape(N, H_q, H_kv, d, 64, 64, 4)
+    ws = torch.empty(msa.msa_decode_workspace(B, shape), dtype=torch.uint8, device="cuda")
+    table = i32([list(range(16)), list(range(16, 32))])
+    ctx = i32([256, 130])
+    for paged in (False, True):
+        o, l = torch.full_like(q, 7.0), torch.full((B, H_q), 7.0, device="cuda")
+        if paged:
+            msa.msa_decode_paged(q, qi, ki, k, v, table, 16, 32, 16, ctx, B, shape, 0.1, o, l, None, ws)
+        else:
+            msa.msa_decode(q, qi, ki, k, v, ctx, B, shape, 0.1, o, l, None, ws)
+        assert msa.msa_check_device_error(ws) == 0
+        assert bool((o[1, 4:] == 0).all()) and bool((l[1, 4:] == -math.inf).all())
+        rows = torch.cat([torch.arange(64), torch.arange(128, 200)]).cuda()
+        for b, h, at in ((0, 0, rows), (0, 1, rows), (1, 0, torch.arange(130).cuda())):
+            hs = slice(4 * h, 4 * h + 4)
+            r = ref.attend(q[b, hs].double(), k[b, at, h].double(), v[b, at, h].double(), 0.1)
+            ref.check_attention(o[b, hs], l[b, hs], *r, d, 256)
