@@ -203,9 +203,10 @@ class MsaDecodeKv4:
     object runs the MSA step (select by the index branch, attend to the chosen blocks; needs d_I, Bk and k)."""
 
     def __init__(self, pool: Kv4Pool, B, max_pages, H_q, d_I=None, Bk=128, k=16, device=None):
-        device = pool.k_codes.device if device is None else device
-        if torch.device(device).index not in (None, pool.k_codes.get_device()):
-            raise ValueError("the pool is on cuda:%d" % pool.k_codes.get_device())
+        at = pool.k_codes.get_device()
+        if device is not None and (torch.device(device).type != "cuda" or torch.device(device).index not in (None, at)):
+            raise ValueError("the pool is on cuda:%d" % at)
+        device = pool.k_codes.device  # ("cuda" alone would be the current one)
         self.pool, self.B, self.max_pages, self.H_q, self.d_I = pool, B, max_pages, H_q, d_I
         need = _c.msa_dense_decode_paged_kv4_workspace(B, H_q, pool.H_kv, pool.d)
         if d_I is not None:

@@ -225,3 +225,38 @@ def test_tensors_of_another_device(monkeypatch):
         PagedCache(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), 16)
     with pytest.raises(ValueError, match="CUDA"):
         Kv4Pool(*[torch.zeros(2, 16, 1, n, dtype=torch.uint8) for n in (32, 4, 32, 4)])
+
+
+def stand_in_pool(dev, monkeypatch):
+    """A pool of device `dev` for MsaDecodeKv4, and the devices of what is allocated from here on (on `meta`)."""
+    class Codes:
+        device = torch.device("cuda", dev)
+
+        def get_device(self):
+            return dev
+
+    class Pool:
+        k_codes, n_pages, page_size, H_kv, d = Codes(), 4, 16, 2, 64
+
+    made, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: made.append(torch.device(device)) or empty(*a, device="meta", **k))
+    return Pool(), made
+
+
+@pytest.mark.parametrize("device", [None, "cuda", "cuda:0", torch.device("cuda", 0)])
+def test_decode_kv4_allocates_beside_its_pool(monkeypatch, lib, device):  # noqa: F811
+    """The workspace and the outputs lie on the pool's device, whatever device is current."""
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    pool, made = stand_in_pool(0, monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    MsaDecodeKv4(pool, 2, 3, 8, d_I=64, Bk=64, k=2, device=device)
+    assert len(made) >= 4 and set(made) == {torch.device("cuda", 0)}
+
+
+@pytest.mark.parametrize("device", ["cuda:1", "cpu", torch.device("cuda", 7)])
+def test_decode_kv4_refuses_another_device(monkeypatch, lib, device):  # noqa: F811
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    pool, made = stand_in_pool(0, monkeypatch)
+    with pytest.raises(ValueError, match="cuda:0"):
+        MsaDecodeKv4(pool, 2, 3, 8, device=device)
+    assert not made
