@@ -200,7 +200,11 @@ class Kv4Pool:
 
 class MsaDecodeKv4:
     """One decode token for B sequences over a Kv4Pool: ``dense`` attends to the whole context, calling the
-    object runs the MSA step (select by the index branch, attend to the chosen blocks; needs d_I, Bk and k)."""
+    object runs the MSA step (select by the index branch, attend to the chosen blocks; needs d_I, Bk and k).
+
+    The tensors that a call returns are the object's own: the next call of the same operator overwrites them, one
+    of the other operator does not.  ``out`` and ``lse`` are those of the last call.  Both use one workspace, so two
+    calls in flight at once need two objects."""
 
     def __init__(self, pool: Kv4Pool, B, max_pages, H_q, d_I=None, Bk=128, k=16, device=None):
         at = pool.k_codes.get_device()
@@ -214,8 +218,10 @@ class MsaDecodeKv4:
             need = max(need, _c.msa_decode_workspace(B, self.shape))
             self.block_idx = torch.empty((B, pool.H_kv, k), dtype=torch.int32, device=device)
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        self.out = torch.empty((B, H_q, pool.d), dtype=torch.bfloat16, device=device)
-        self.lse = torch.empty((B, H_q), dtype=torch.float32, device=device)
+        self._dense, self._step = [(torch.empty((B, H_q, pool.d), dtype=torch.bfloat16, device=device),
+                                    torch.empty((B, H_q), dtype=torch.float32, device=device))
+                                   if wanted else None for wanted in (True, d_I is not None)]
+        self.out, self.lse = self._step or self._dense
 
     def _check(self, q_t, page_table, ctx_len):
         dev = _device(self.workspace)
@@ -227,9 +233,11 @@ class MsaDecodeKv4:
     def dense(self, q_t, page_table, ctx_len, scale=None, stream=None):
         self._check(q_t, page_table, ctx_len)
         scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
+        out, lse = self._dense
         _c.msa_dense_decode_paged_kv4(q_t, self.pool.c, page_table, self.max_pages, ctx_len, self.B, self.H_q, scale,
-                                      self.out, self.lse, self.workspace, stream=stream)
-        return self.out, self.lse
+                                      out, lse, self.workspace, stream=stream)
+        self.out, self.lse = out, lse
+        return out, lse
 
     def __call__(self, q_t, q_idx_t, k_idx_pool, page_table, ctx_len, scale=None, stream=None):
         """q_idx_t [B, H_kv, d_I] and k_idx_pool [n_pages, page_size, d_I]: both bf16, or both uint8 (E4M3 codes)."""
@@ -242,9 +250,11 @@ class MsaDecodeKv4:
         _check_tensor("k_idx_pool", k_idx_pool, idx, (self.pool.n_pages, self.pool.page_size, self.d_I), dev)
         scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
         call = _c.msa_decode_paged_kv4_fp8 if f8 else _c.msa_decode_paged_kv4
+        out, lse = self._step
         call(q_t, q_idx_t, k_idx_pool, self.pool.c, page_table, self.max_pages, ctx_len, self.B, self.shape, scale,
-             self.out, self.lse, self.block_idx, self.workspace, stream=stream)
-        return self.out, self.lse, self.block_idx
+             out, lse, self.block_idx, self.workspace, stream=stream)
+        self.out, self.lse = out, lse
+        return out, lse, self.block_idx
 
     def device_status(self, stream=None):
         return _c.msa_check_device_error(self.workspace, stream)
