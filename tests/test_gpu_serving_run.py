@@ -35,3 +35,44 @@ def test_dense_and_step_keep_their_outputs():
         assert all(torch.equal(x, y) for x, y in zip(got, want)) and all(torch.equal(x, y) for x, y in zip(got2, step))
         a.dense(q, table, i32(ctx), 0.1)
     assert a.device_status() == 0 and b.device_status() == 0
+
+
+def test_step_of_a_cache_that_was_forked_freed_and_compacted():
+    """With every block chosen the MSA step is the dense step: compared with it, and with 64 bits, after the page calls
+    have moved the sequences about."""
+    from block_sparse_long_index_gb300 import Kv4Pool, MsaDecodeKv4, PagedCache
+    H_q, H_kv, d, d_I, page, n_pages, n_seqs, Bk, k = 8, 2, 64, 32, 16, 60, 6, 64, 3
+    lens = [37, 150, 64]
+    N = sum(lens)
+    pool = Kv4Pool.empty(n_pages, page, H_kv, d)
+    ki = torch.zeros(n_pages, page, d_I, dtype=torch.bfloat16, device="cuda")
+    cache = PagedCache.empty(n_seqs, 12, n_pages, page, pool.tensors() + [ki])
+    cache.reserve(i32([0, 1, 2]), i32(lens))
+    pool.store(rnd(N, H_kv, d), rnd(N, H_kv, d), i32([0, 37, 187, 251]), i32([0, 0, 0]), cache.page_table[:3])
+    ki.copy_(rnd(*ki.shape))
+    cache.fork(i32([1, 0, 1]), i32([3, 4, 5]))
+    before = cache.ctx_len.clone()
+    cache.reserve(i32(range(n_seqs)), before + 1)
+    pool.store(rnd(n_seqs, H_kv, d), rnd(n_seqs, H_kv, d), i32(range(n_seqs + 1)), before, cache.page_table)
+    cache.free(i32([1, 4]))
+    cache.compact()
+    live = [0, 2, 3, 5]
+    table, ctx = cache.page_table[live].contiguous(), cache.ctx_len[live].contiguous()
+    n = ctx.tolist()
+    assert cache.device_status() == 0 and pool.device_status() == 0 and n == [38, 65, 151, 151]
+    q, qi = rnd(4, H_q, d), rnd(4, H_kv, d_I)
+    run = MsaDecodeKv4(pool, 4, 12, H_q, d_I=d_I, Bk=Bk, k=k)
+    o, l = run.dense(q, table, ctx, 0.125)
+    assert run.device_status() == 0
+    run._step[0].fill_(7.0)
+    run._step[1].fill_(7.0)
+    run.block_idx.fill_(99)
+    o2, l2, blk = run(q, qi, ki, table, ctx, 0.125)
+    assert run.device_status() == 0 and o2.data_ptr() != o.data_ptr()
+    for b in range(4):
+        nb = -(-n[b] // Bk)
+        for g in range(H_kv):
+            assert sorted(blk[b, g].tolist()) == [-1] * (k - nb) + list(range(nb))
+    want = dense_ref(pool, q, table, n, 0.125)
+    ref.check_attention(o, l, *want, d, max(n))
+    ref.check_attention(o2, l2, *want, d, max(n))  # (the merge of k partials is an fp32 sum of k terms more)
