@@ -282,7 +282,7 @@ class PagedCache:
         self.c_pools = _c.page_pools((t, t.numel() // n_pages * t.element_size()) for t in self.pools)
         self.page_map = torch.empty((n_pages,), dtype=torch.int32, device=refs.device)
         self.n_live = torch.empty((1,), dtype=torch.int32, device=refs.device)
-        need = max(_c.msa_pages_workspace(self.c, 0), _c.msa_pages_workspace(self.c, min(n_seqs, 4096)))
+        need = max(_c.msa_pages_workspace(self.c, 0), _c.msa_pages_workspace(self.c, 4096))  # compact, the most entries
         self.workspace = torch.empty(need, dtype=torch.uint8, device=refs.device)
 
     @classmethod

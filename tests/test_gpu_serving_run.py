@@ -76,3 +76,24 @@ def test_step_of_a_cache_that_was_forked_freed_and_compacted():
     want = dense_ref(pool, q, table, n, 0.125)
     ref.check_attention(o, l, *want, d, max(n))
     ref.check_attention(o2, l2, *want, d, max(n))  # (the merge of k partials is an fp32 sum of k terms more)
+
+
+# ---------------------------------------------------------------- pages
+def tables(cache):
+    return [t.clone() for t in [cache.page_table, cache.ctx_len, cache.refs] + cache.pools]
+
+
+def test_more_entries_than_sequences():
+    """Such a call names a sequence twice or one that is not there: the device says so, and nothing changes."""
+    from block_sparse_long_index_gb300 import PagedCache, msa
+    cache = PagedCache.empty(2, 4, 8, 16)
+    cache.reserve(i32([0]), i32([20]))
+    was = tables(cache)
+    many = i32([1] * 100)
+    cache.reserve(many, many)
+    assert cache.device_status() == msa.MSA_ERR_BAD_INDEX
+    cache.fork(i32([0] * 100), many)
+    assert cache.device_status() == msa.MSA_ERR_BAD_INDEX
+    assert all(torch.equal(a, b) for a, b in zip(tables(cache), was))
+    cache.free(many)
+    assert cache.device_status() == 0
