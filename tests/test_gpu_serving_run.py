@@ -97,3 +97,83 @@ def test_more_entries_than_sequences():
     assert all(torch.equal(a, b) for a, b in zip(tables(cache), was))
     cache.free(many)
     assert cache.device_status() == 0
+
+
+def test_fork_without_pages_changes_nothing():
+    """More partly filled last pages than free pages."""
+    from block_sparse_long_index_gb300 import PagedCache, msa
+    n_pages, page = 8, 16
+    pools = [torch.arange(n_pages * page * 4, dtype=torch.int32, device="cuda").view(n_pages, page, 4)]
+    cache = PagedCache.empty(6, 4, n_pages, page, pools)
+    cache.reserve(i32([0, 1]), i32([40, 33]))  # 3 + 3 pages, both last ones partly filled: 2 free
+    was = tables(cache)
+    for src, dst in (([0, 1, 0], [2, 3, 4]), ([1, 1, 1, 1], [5, 4, 3, 2])):
+        cache.fork(i32(src), i32(dst))
+        assert cache.device_status() == msa.MSA_ERR_NO_PAGES
+        assert all(torch.equal(a, b) for a, b in zip(tables(cache), was))
+    cache.fork(i32([0, 1]), i32([2, 3]))  # as many as there are
+    assert cache.device_status() == 0 and cache.ctx_len.tolist() == [40, 33, 40, 33, 0, 0]
+    assert torch.equal(pools[0][cache.page_table[2, 2]], was[3][was[0][0, 2]])
+    was = tables(cache)
+    cache.fork(i32([1]), i32([4]))
+    assert cache.device_status() == msa.MSA_ERR_NO_PAGES
+    assert all(torch.equal(a, b) for a, b in zip(tables(cache), was))
+
+
+def test_free_clears_the_entries():
+    """What a freed sequence held reads -1; entries past it and other sequences stay as they were."""
+    from block_sparse_long_index_gb300 import PagedCache
+    cache = PagedCache.empty(4, 6, 16, 16)
+    cache.reserve(i32([0, 1, 2]), i32([70, 16, 48]))
+    cache.page_table[0, 5] = 77  # past the length: neither read nor written
+    keep = cache.page_table[1:2].clone()
+    cache.free(i32([0, 3, 2]))  # (3 is empty)
+    assert cache.device_status() == 0 and cache.ctx_len.tolist() == [0, 16, 0, 0]
+    assert cache.page_table[0].tolist() == [-1] * 5 + [77] and cache.page_table[2].tolist() == [-1] * 6
+    assert torch.equal(cache.page_table[1:2], keep) and int(cache.refs.sum()) == 1
+
+
+# ---------------------------------------------------------------- two calls at once
+def test_two_prefills_at_once():
+    """Two plans, made before, on two streams: out and lse of both, rows of no sequence, and both statuses."""
+    from block_sparse_long_index_gb300 import MsaDensePrefill
+    cases = [([900, 50], 8, 1, 128), ([20, 700], 8, 8, 64)]
+    ins = [make(*c, pad=5, seed=i) for i, c in enumerate(cases)]
+    plans = [MsaDensePrefill(q.shape[0], q.shape[1], k.shape[1], q.shape[2], 2) for q, k, _, _ in ins]
+    want = [[t.clone() for t in p(*x, 0.1)] for p, x in zip(plans, ins)]
+    streams = [torch.cuda.Stream() for _ in plans]
+    for _ in range(4):
+        for p in plans:
+            p.out.fill_(7.0)
+            p.lse.fill_(7.0)
+        torch.cuda.synchronize()
+        for p, x, s in zip(plans, ins, streams):
+            p(*x, 0.1, stream=s)
+        torch.cuda.synchronize()
+        for p, (o, l), (lens, _, _, _) in zip(plans, want, cases):
+            n = sum(lens)
+            assert p.device_status() == 0
+            assert torch.equal(p.out[:n], o[:n]) and torch.equal(p.lse[:, :n], l[:, :n])
+            assert bool((p.out[n:] == 7.0).all()) and bool((p.lse[:, n:] == 7.0).all())
+
+
+def test_stores_and_loads_at_once():
+    """Other sequences of one pool on two streams (the pool's error word is the only thing that they share)."""
+    from block_sparse_long_index_gb300 import Kv4Pool
+    page, H, d = 16, 2, 128
+    for n in (5, 900):  # calls whose status one CTA writes, and calls that clear it before
+        pages = -(-n // page)
+        pool = Kv4Pool.empty(2 * pages, page, H, d)
+        ids = torch.randperm(2 * pages, device="cuda").to(torch.int32).view(2, 1, pages).contiguous()
+        cu, pos = i32([0, n]), i32([0])
+        x, streams = [rnd(n, H, d) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+        got = [[torch.empty(n, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            pool.store(x[i], x[1 - i], cu, pos, ids[i], stream=s)
+            pool.load(n, cu, pos, ids[i], *got[i], stream=s)
+        torch.cuda.synchronize()
+        assert pool.device_status() == 0
+        assert torch.equal(got[0][0], got[1][1]) and torch.equal(got[0][1], got[1][0])
+        k, v = pool.load(n, cu, pos, ids[0])
+        assert torch.equal(k, got[0][0]) and torch.equal(v, got[0][1]) and bool((k != 0).any())
