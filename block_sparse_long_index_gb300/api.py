@@ -122,7 +122,10 @@ def _allocating_for(stream):
 
 
 class MsaDensePrefill:
-    """Dense causal attention over packed prompts of N rows in all, S sequences."""
+    """Dense causal attention over packed prompts of N rows in all, S sequences.
+
+    A call returns the object's own ``out`` and ``lse``, which the next call overwrites; two calls in flight at once
+    need two objects."""
 
     def __init__(self, N, H_q, H_kv, d, S, device="cuda"):
         self.N, self.H_q, self.H_kv, self.d, self.S = N, H_q, H_kv, d, S
@@ -148,7 +151,10 @@ class MsaDensePrefill:
 
 class Kv4Pool:
     """A 4-bit paged K/V cache: codes [n_pages, page_size, H_kv, d / 2] and scales [n_pages, page_size, H_kv, 4]
-    of K and of V (uint8).  ``Kv4Pool.empty`` makes one."""
+    of K and of V (uint8).  ``Kv4Pool.empty`` makes one.
+
+    Calls on other streams may touch other rows at the same time; the error word that ``device_status`` reads is one
+    for all of them, that of the call that ran last."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         self.n_pages, self.page_size, self.H_kv, half = k_codes.shape
@@ -265,7 +271,8 @@ class PagedCache:
 
     page_table [n_seqs, max_pages], ctx_len [n_seqs] and refs [n_pages] are int32 device tensors; every pool is a
     contiguous tensor of n_pages pages, at most 8 of them.  ``PagedCache.empty`` makes the tables.  A call's
-    errors (MSA_ERR_NO_PAGES, MSA_ERR_BAD_INDEX) are what ``device_status`` returns after it."""
+    errors (MSA_ERR_NO_PAGES, MSA_ERR_BAD_INDEX) are what ``device_status`` returns after it.  Calls follow one
+    another on the device: calls on other streams have to be ordered by the caller."""
 
     def __init__(self, page_table, ctx_len, refs, page_size, pools=()):
         n_seqs, max_pages = page_table.shape
@@ -309,7 +316,8 @@ class PagedCache:
         _c.msa_pages_free(self.c, seqs, n, self.workspace, stream=stream)
 
     def compact(self, stream=None):
-        """Returns (page_map [n_pages], n_live [1]): each page's new id (-1 where it was free), and the pages held."""
+        """Returns (page_map [n_pages], n_live [1]): each page's new id (-1 where it was free), and the pages held.
+        Both are the object's own; the next compact overwrites them."""
         _device(self.workspace)
         _c.msa_pages_compact(self.c, self.c_pools, len(self.pools), self.page_map, self.n_live, self.workspace,
                              stream=stream)

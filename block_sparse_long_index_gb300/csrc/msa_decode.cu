@@ -352,10 +352,15 @@ __device__ __forceinline__ uint64_t merged_key(const uint64_t* sl, int splits, i
 // exact bf16 values, K's words in registers on their way into the B fragments
 // and V's on their way into shared memory; the rest is the same arithmetic.
 // Blocks of 64 keys leave a CTA little to read, so what counts is that all CTAs
-// run at once: held to 72 registers, seven of an SM do instead of five (16
-// sequences, 8 groups, k = 8: 28.6 -> 24.3 us a step).  With blocks of 128 the
-// reads in flight count more: 4 sequences of 2^20 tokens, k = 16, take 188 us
-// with all the registers that they need and 192 with seven CTAs an SM.
+// run at once: held to 72 registers, seven of an SM do instead of five.  d = 128,
+// d_I = 64: 16 sequences of 9000 tokens, 32 heads on 8, k = 8, 26.9 -> 23.1 us
+// (FP8 index 26.0 -> 22.8); 48 of them, 64 heads, k = 16, 100.8 -> 89.8 us; 4 of
+// 2^20, k = 32, 133.9 -> 129.7 us.  A grid of at most 512 CTAs runs at once
+// either way and loses reads in flight: 4 of 2^18 tokens, k = 16, 45.1 -> 47.4
+// us, 4 of 2^20 110.1 -> 112.4 us.  (d = 64 needs no more registers.)  With
+// blocks of 128 those reads count more: 4 sequences of 2^20 tokens, d_I = 128,
+// k = 16, take 188 us with all the registers that they need and 192 with seven
+// CTAs an SM.
 template <int D, int BK, bool PAGED, int LPL, bool KV4 = false>
 __global__ void __launch_bounds__(128, KV4 ? (BK == 64 ? 7 : 1) : D == 64 && !PAGED ? 5 : 0)
     decode_attn_kernel(const uint16_t* __restrict__ q_t,

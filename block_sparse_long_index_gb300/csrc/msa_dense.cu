@@ -10,11 +10,14 @@
 // operands are read once from HBM and again from L2.  Measured, against a
 // library bf16 product's 1913.8 TFLOP/s on the same GPU (1709 when it runs for
 // seconds):
-//   one prompt of 32768, 64 heads on 8, d = 128: 11.6 ms, 1510 TFLOP/s (0.79);
-//   10.7 ms, 1640 TFLOP/s (0.86) for a call by itself - calls in a row reach the
-//   board's 1400 W, and the clock falls from 2.07 to 1.88 GHz;
-//   8 prompts of 167 to 16000 rows, 32 heads on 8: 1.95 ms, 1450 TFLOP/s (0.76);
-//   5 prompts of 1 to 640 rows, 32 heads on 8: 19.6 us, where start and end count.
+//   one prompt of 32768, 64 heads on 8, d = 128: 11.6 to 11.8 ms, 1490 to 1510
+//   TFLOP/s (0.78 to 0.79); 10.7 ms, 1640 TFLOP/s (0.86) for a call after a pause -
+//   calls in a row reach the board's 1400 W, and the clock falls from 2.07 to 1.88 GHz;
+//   8 prompts of 167 to 16000 rows, 32 heads on 8: 1.95 to 1.98 ms, 1450 TFLOP/s
+//   (0.75 to 0.76);
+//   5 prompts of 1 to 640 rows, 32 heads on 8: 20 us, where start and end count;
+//   d = 64, whose products take half as long while the softmax does not: 32768
+//   rows, 64 heads on 8, 10.0 ms, 877 TFLOP/s (0.46), 16 on 16, 2.56 ms (0.45).
 #include <math.h>
 
 #include "msa_sm100.cuh"
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) dense_plan_kernel(const int32_t*
 // What bounds a step: the softmax.  A query tile's softmax takes some 1500
 // cycles of the SM (512 of them exponentials, the rest the latencies of S's
 // read, the maxima's exchange and P's write), the two tiles' products 2048 in
-// 3000.  Measured and slower at 32K: 8 softmax warps a tile on both at once
+// 3000 (1024 at d = 64: tensor pipe 36 % active).  Measured and slower at 32K: 8 softmax warps a tile on both at once
 // 12.4 ms; a tile's S read while the other's P is written 12.6 ms; P handed over
 // in two parts 14.5 ms; 64-key steps 12.9 ms; exponentials under the old maximum
 // before the exchange, done again where it proves too low, 11.7 ms.
@@ -171,7 +174,7 @@ struct Layout {
   static constexpr int OFF_MX = OFF_MM + 2 * 128 * 4;    // exchange of row maxima, two buffers: [2][128] x 16 bytes
   static constexpr int OFF_BAR = OFF_MX + 2 * 128 * 16;
   static constexpr int SMEM = 1024 + OFF_BAR + 512;
-  static constexpr uint32_t TMEM_O = 256;            // S / P of tile q at 128 q, O of tile q at 256 + 128 q
+  static constexpr uint32_t TMEM_O = 256;            // S / P of tile q at 128 q, O of tile q (d columns) at 256 + 128 q
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,

@@ -47,8 +47,9 @@ struct RowMap {
 // A CTA takes R x U x tpp packed rows (tokens), tpp = the tokens that 256 threads cover at 8 channels a thread (K's
 // head rows, then V's): it looks all of them up first, then has the reads of U x tpp of them in flight at a time.
 // R grows up to kRounds where the CTAs still fill the GPU.
-// 131072 tokens of 8 heads, d = 128, in and out: 260 us, 5.23 TB/s (0.77 of the measured copy rate); 604 us with U = 1,
-// which is no faster for few rows either (48 tokens in and out: 10.3 and 10.2 us, two launches' latency).
+// 131072 tokens of 8 heads, d = 128, in and out: 260 us, 5.23 TB/s (0.77 of the measured copy rate); the store alone 144
+// us, 4.72 TB/s (0.70), the load 115 us, 5.89 TB/s (0.87); at d = 64 87 us (0.58) and 66 us (0.77).  604 us in and out
+// with U = 1, which is no faster for few rows either (48 tokens: 10.3 and 10.2 us, two launches' latency).
 constexpr int kUnroll = 4, kRounds = 8;
 struct RowTile {
   int per_tok, tpp;
@@ -222,7 +223,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_load_kernel(Kv4Pool pool, int
 // d = 128: 4 sequences of 2^20 tokens 823 us, 5.5 TB/s (0.82 of the measured
 // copy rate); 48 sequences of 1200 to 12000, 32 heads on 8: 84 us, 4.2 TB/s
 // (0.62, of which some 10 us are the start and the combine); one of 1500 tokens:
-// 10.4 us, a chain of round trips.
+// 10.4 us, a chain of round trips.  More than 8 K/V heads cost more, because each
+// head block fetches the scales of all heads and its stages get larger: 4 of
+// 65536 tokens with 16, 32, 64 heads 130, 353, 711 us at d = 128 (0.65, 0.48,
+// 0.47), 93, 160, 332 us at d = 64 (0.48, 0.56, 0.54); with 8 85 us (0.50).
 constexpr int kUnit = 16;
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;

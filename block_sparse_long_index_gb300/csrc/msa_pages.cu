@@ -12,6 +12,12 @@
 // (62 MB read and written, 1024 pages searched) 20 us for the two calls; 32
 // sequences released and 2560 pages compacted, 643 MB read and written: 127 us,
 // of which the copies take 93 (6.9 TB/s).
+// What grows with the limits: the search for free pages goes through refs from
+// page 0, 4096 at a time (64 entries of 8 pages: 9 us with 1024 pages, 13 us where
+// the first 16384 of 32768 are held, 31 us where 100000 of 200000 are), compact's
+// plan goes through all of them twice (25 us at 32768 pages, 119 us at 200000),
+// and each entry is compared with those before it (1024 entries: 38 us, 4096:
+// 271 us).
 #include "msa_common.cuh"
 
 namespace msa {

@@ -416,13 +416,15 @@ msa_status_t msa_decode_noalloc(const void* q_t, const void* q_idx_t, const void
  *   cu_seqlens [S+1] int32 (device), S >= 1
  *   out        [N, H_q, d] bf16 out
  *   lse        [H_q, N] fp32 out: natural-log log-sum-exp of the scaled scores
- * A key whose score is -inf weighs 0; a row that sees no other key has out 0 and
- * lse -inf.  A NaN score makes the row's out and lse of that head NaN.
+ * Scores, softmax and sums are fp32; probabilities are rounded to bf16 for the
+ * product with V.  A key whose score is -inf weighs 0; a row that sees no other
+ * key has out 0 and lse -inf.  A NaN score makes the row's out and lse of that
+ * head NaN.
  * Rows of no sequence (past cu_seqlens[S]) are neither read into a result nor
  * written: their out and lse stay as they were, whatever q, k and v hold there.
  * A cu_seqlens that breaks the rules sets the device error word
  * (MSA_ERR_BAD_INDEX) and nothing is written.  Supported: d in {64, 128},
- * H_q / H_kv in {1, 2, 4, 8}, H_kv <= 64, N and S <= 2^24.
+ * H_q / H_kv in {1, 2, 4, 8}, H_kv <= 64, 1 <= N <= 2^24, S <= 2^24.
  */
 size_t msa_dense_prefill_varlen_workspace(int64_t N, int S, int H_q, int H_kv, int d);
 msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int S,
@@ -460,8 +462,8 @@ msa_status_t msa_dense_prefill_varlen(const void* q, const void* k, const void* 
  * one row a sequence and pos0 = the lengths so far.  Rows of no sequence are
  * passed over.  A row whose position lies outside the table, or whose page id
  * lies outside [0, n_pages), is skipped and sets the device error word
- * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.  N < 2^31,
- * S <= 2^24.
+ * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.
+ * 1 <= N < 2^31, 1 <= S <= 2^24.
  * msa_kv4_load: the same rows back, k and v [N, H_kv, d] bf16 out (exact
  *   values of the codes); a bad row reads as zeros (and sets the error word),
  *   rows of no sequence stay as they were.
@@ -561,8 +563,10 @@ msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, cons
  * seqs, new_len, src, dst are int32 device arrays of n entries, n <= 4096 (0 is
  * allowed).  pools: n_pools <= 8 host entries, each a device array of n_pages
  * pages of page_bytes (a multiple of 16) at a 16-byte aligned address; pass every
- * pool that the tables address.  workspace: msa_pages_workspace(pages, n)
- * bytes, n as in the call (0 for compact).
+ * pool that the tables address.  (reserve and free touch no pool, and compact's
+ * page_map tells where the pages of further pools go; fork has no such list, so
+ * tables that are forked serve at most 8 pools.)  workspace:
+ * msa_pages_workspace(pages, n) bytes, n as in the call (0 for compact).
  * Limits: n_pages, max_pages < 2^27; max_pages * page_size < 2^31.
  */
 typedef struct {
