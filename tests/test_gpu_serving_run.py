@@ -1,5 +1,5 @@
 """The serving classes together: what their calls return stays until its own buffer is written again, the MSA step after
-a cache was forked, freed and compacted, page calls that refuse, and two prefills at once."""
+a cache was forked, freed and compacted, page calls that refuse, calls at once, captured calls, and statuses."""
 import math
 
 import pytest
@@ -177,3 +177,107 @@ def test_stores_and_loads_at_once():
         assert torch.equal(got[0][0], got[1][1]) and torch.equal(got[0][1], got[1][0])
         k, v = pool.load(n, cu, pos, ids[0])
         assert torch.equal(k, got[0][0]) and torch.equal(v, got[0][1]) and bool((k != 0).any())
+
+
+# ---------------------------------------------------------------- captured calls
+def test_captured_prefill_with_a_plan_of_its_own():
+    """More sequences than a warp has lanes: the planning kernel and its dependent in one graph, other offsets a replay."""
+    from block_sparse_long_index_gb300 import MsaDensePrefill
+    S, d = 40, 64
+    lens = [(11 * i) % 37 for i in range(S)]
+    q, k, v, cu = make(lens, 4, 2, d, pad=50)
+    N = q.shape[0]
+    plan = MsaDensePrefill(N, 4, 2, d, S)
+    plan(q, k, v, cu, 0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan(q, k, v, cu, 0.1)
+    for step in (5, 17, 0):
+        lens = [(step * i) % 23 for i in range(S)] if step else [0] * (S - 1) + [N]
+        n = sum(lens)
+        cu.copy_(torch.tensor([sum(lens[:i]) for i in range(S + 1)], dtype=torch.int32))
+        plan.out.fill_(7.0)
+        plan.lse.fill_(7.0)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert plan.device_status() == 0
+        ref.check_attention(plan.out[:n], plan.lse[:, :n].T, *ref.dense_prefill(q[:n], k[:n], v[:n], lens, 0.1), d, max(lens))
+        assert bool((plan.out[n:] == 7.0).all()) and bool((plan.lse[:, n:] == 7.0).all())
+
+
+def test_captured_page_cycle():
+    """Reserve, fork, free and compact in one graph, replayed on the state that the replay before left."""
+    from test_gpu_pages import Both
+    b = Both(6, 8, 60, 16)
+    grow, to, src, dst, gone = i32([0, 1]), i32([70, 40]), i32([0, 1, 0]), i32([2, 3, 4]), i32([0, 3])
+    b.gpu.reserve(grow, to)
+    b.gpu.free(grow)
+    b.gpu.fork(i32([5]), i32([4]))  # (an empty one: kernels loaded before the capture)
+    b.gpu.compact()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.gpu.reserve(grow, to)
+        b.gpu.fork(src, dst)
+        b.gpu.free(gone)
+        page_map, n_live = b.gpu.compact()
+    for rest in ([1, 2, 4], [4, 2, 1], [2, 1, 4]):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert b.gpu.device_status() == 0
+        b.ref.reserve([0, 1], [70, 40])
+        b.ref.fork([0, 1, 0], [2, 3, 4])
+        b.ref.free([0, 3])
+        want, n = b.ref.compact()
+        assert page_map.tolist() == want and n_live.tolist() == [n]
+        b.check()
+        b.gpu.free(i32(rest))
+        b.ref.free(rest)
+        b.check()
+
+
+# ---------------------------------------------------------------- status
+def test_status_is_that_of_the_last_call():
+    """A call with bad data sets it, the next call without clears it, whichever kernel of a call writes it."""
+    from block_sparse_long_index_gb300 import Kv4Pool, MsaDecodeKv4, MsaDensePrefill, PagedCache, msa
+    bad, no_pages = msa.MSA_ERR_BAD_INDEX, msa.MSA_ERR_NO_PAGES
+    for S in (1, 40):  # planned by the CTAs, by a kernel
+        plan, x = MsaDensePrefill(80, 2, 1, 64, S), [rnd(80, h, 64) for h in (2, 1, 1)]
+        good, wrong = i32([2 * i for i in range(S + 1)]), i32([1] * (S + 1))
+        for cu, want in ((wrong, bad), (good, 0), (wrong, bad)):
+            plan(*x, cu)
+            assert plan.device_status() == want
+    for n in (5, 300):
+        pool, x = Kv4Pool.empty(30, 16, 1, 64), rnd(n, 1, 64)
+        good, wrong = i32([list(range(20))]), i32([[99] * 20])
+        for table, want in ((wrong, bad), (good, 0), (wrong, bad), (good, 0)):
+            pool.store(x, x, i32([0, n]), i32([0]), table)
+            assert pool.device_status() == want
+            pool.load(n, i32([0, n]), i32([0]), table)
+            assert pool.device_status() == want
+    run = MsaDecodeKv4(pool, 2, 20, 2, d_I=64, Bk=64, k=2)
+    q, qi, ki, table = rnd(2, 2, 64), rnd(2, 1, 64), rnd(30, 16, 64), i32([list(range(20)), list(range(10, 30))])
+    for ctx, want in (([-1, 5], bad), ([30, 300], 0), ([20, 321], bad), ([1, 320], 0)):
+        run.dense(q, table, i32(ctx))
+        assert run.device_status() == want
+        run(q, qi, ki, table, i32(ctx))
+        assert run.device_status() == want
+        run.dense(q, table, i32([7, 7]))
+        assert run.device_status() == 0
+    cache = PagedCache.empty(3, 4, 4, 16)
+    for seqs, lens, want in (([3], [1], bad), ([0], [20], 0), ([1, 2], [33, 1], no_pages), ([1], [10], 0)):
+        cache.reserve(i32(seqs), i32(lens))
+        assert cache.device_status() == want
+    for src, dst, want in (([0], [1], bad), ([0], [2], 0)):
+        cache.fork(i32(src), i32(dst))
+        assert cache.device_status() == want
+    for seqs, want in (([7], bad), ([2], 0)):
+        cache.free(i32(seqs))
+        assert cache.device_status() == want
+    cache.page_table[0, 0] = 77
+    cache.compact()
+    assert cache.device_status() == bad
+    cache.free(i32([]))
+    assert cache.device_status() == 0
