@@ -263,3 +263,31 @@ def test_bf16_step_blocks_of_minus_infinity():
             hs = slice(4 * h, 4 * h + 4)
             r = ref.attend(q[b, hs].double(), k[b, at, h].double(), v[b, at, h].double(), 0.1)
             ref.check_attention(o[b, hs], l[b, hs], *r, d, 256)
+
+
+@pytest.mark.parametrize("token", [0, 5000, 8999])
+@pytest.mark.parametrize("H_kv,d", [(1, 128), (2, 64), (8, 128), (9, 64)])
+def test_dense_decode_over_nan_groups(token, H_kv, d):
+    """In a row that many CTAs share: everything of its heads for a group of K, its channels for a group of V."""
+    from block_sparse_long_index_gb300 import MsaDecodeKv4
+    ctx, page = [9000, 40], 16
+    counts = [-(-c // page) for c in ctx]
+    pool, table = random_pool(sum(counts), page, H_kv, d), table_of(counts, max(counts), sum(counts))
+    q = torch.randn(2, 4 * H_kv, d, device="cuda").to(torch.bfloat16)
+    plan = MsaDecodeKv4(pool, 2, table.shape[1], 4 * H_kv)
+    want = dense_ref(pool, q, table, ctx, 0.1)
+    p, r = place(table, 0, token, page)
+    hit, c = slice(4 * H_kv - 4, 4 * H_kv), slice(d // 4, d // 2)
+    for scales in (pool.k_scales, pool.v_scales):
+        keep = scales[p, r, H_kv - 1, 1].clone()
+        scales[p, r, H_kv - 1, 1] = 255
+        out, lse = [t.clone() for t in plan.dense(q, table, i32(ctx), 0.1)]
+        assert plan.device_status() == 0
+        scales[p, r, H_kv - 1, 1] = keep
+        at = (0, hit) if scales is pool.k_scales else (0, hit, c)
+        assert bool(torch.isnan(out[at]).all())
+        out[at] = want[0][at].to(torch.bfloat16)
+        if scales is pool.k_scales:
+            assert bool(torch.isnan(lse[0, hit]).all())
+            lse[0, hit] = want[1][0, hit].float()
+        ref.check_attention(out, lse, *want, d, max(ctx))
