@@ -149,12 +149,225 @@ class MsaDensePrefill:
         return _c.msa_check_device_error(self.workspace, stream)
 
 
-class Kv4Pool:
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0, beta_slow=1.0):
+    """Radians a position of the rot / 2 pairs, a list of floats: base^(-2 i / rot), scaled for contexts `factor` times
+    as long as those of training where `scaling` says so:
+
+    "linear"   every frequency over factor;
+    "base"     the base grown so that the lowest frequency falls by factor and the highest stays: base factor^(rot / (rot - 2));
+    "parts"    a pair that turns over beta_fast times within original_len positions stays, one that turns less than
+               beta_slow times is divided by factor, those between are mixed linearly in their index.
+               (Attention over such rows is often sharpened by Rope's `factor` 1 + 0.1 ln factor.)"""
+    rot, base, factor = int(rot), float(base), float(factor)
+    if rot < 2 or rot % 2:
+        raise ValueError("rot has to be even")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base has to be above 1 and factor at least 1")
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError("scaling by the base needs two pairs at least")
+        base *= factor ** (rot / (rot - 2.0))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling in (None, "base"):
+        return f
+    if scaling == "linear":
+        return [x / factor for x in f]
+    if scaling != "parts":
+        raise ValueError("scaling is None, 'linear', 'base' or 'parts'")
+    if not original_len or original_len < 1:
+        raise ValueError("scaling by parts needs original_len")
+    # the (real) index of the pair that turns n times within original_len
+    index = lambda n: rot * math.log(original_len / (2.0 * math.pi * n)) / (2.0 * math.log(base))  # noqa: E731
+    lo, hi = max(0.0, math.floor(index(beta_fast))), min(rot - 1.0, math.ceil(index(beta_slow)))
+    mix = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(rot // 2)]
+    return [x * (1.0 - m) + x / factor * m for x, m in zip(f, mix)]
+
+
+class Rope:
+    """Rotary positions: a table of frequencies on the device.  Calling it turns rows (or turns them back).
+
+    ``Rope(rot, base, ...)`` takes rope_frequencies' arguments, ``Rope.from_frequencies`` any frequencies in radians a
+    position.  `amplitude` multiplies the turned channels."""
+
+    def __init__(self, rot, base=10000.0, interleaved=False, amplitude=1.0, device="cuda", **scaling):
+        self._set(rope_frequencies(rot, base, **scaling), interleaved, amplitude, device)
+
+    @classmethod
+    def from_frequencies(cls, freqs, interleaved=False, amplitude=1.0, device=None):
+        """freqs: a float64 tensor, or numbers; the table goes to its device, or to `device`."""
+        self = cls.__new__(cls)
+        if isinstance(freqs, torch.Tensor):
+            device = freqs.device if device is None else device
+            freqs = freqs.tolist()
+        self._set(freqs, interleaved, amplitude, "cuda" if device is None else device)
+        return self
+
+    def _set(self, freqs, interleaved, amplitude, device):
+        self.rot, self.interleaved, self.amplitude = 2 * len(freqs), bool(interleaved), float(amplitude)
+        self.turns = torch.tensor([_turns(float(f)) for f in freqs], dtype=torch.int64, device=device)
+        self.c = _c.rope(self.turns, self.rot, self.interleaved, self.amplitude)
+
+    def __call__(self, x, positions, out=None, inverse=False, stream=None):
+        """x [N, H, d] bf16 or fp32 turned by positions [N] int32 into `out` (x itself is allowed; a new tensor where it
+        is None).  Heads are contiguous, rows may lie apart, as slices of a wider projection.  With `inverse` turned
+        back: the gradient of x from that of the result."""
+        dev = _device(self.turns)
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("x has to be bfloat16 or float32")
+        if x.dim() != 3:
+            raise ValueError("x has shape %s, expected [N, H, d]" % (tuple(x.shape),))
+        N, H, d = x.shape
+        _check_rows("x", x, x.dtype, (N, H, d), dev)
+        _check_tensor("positions", positions, torch.int32, (N,), dev)
+        if out is None:
+            with _allocating_for(stream):
+                out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
+        _check_rows("out", out, x.dtype, (N, H, d), dev)
+        if N:
+            _c.msa_rope(x, x.stride(0) if N > 1 else H * d, out, out.stride(0) if N > 1 else H * d, N, H, d,
+                        x.dtype == torch.float32, positions, self.c, inverse, stream=stream)
+        return out
+
+
+def _turns(f):
+    """f radians a position as 2^-64 turns: f / (2 pi) 2^64 rounded, modulo 2^64, as a signed integer."""
+    if not math.isfinite(f):
+        raise ValueError("a frequency is not finite")
+    n, d = f.as_integer_ratio()
+    # pi 2^132 as an integer: f / (2 pi) 2^64 = n 2^(63 + 132) / (d pi 2^132)
+    pi = 0x3243F6A8885A308D313198A2E03707344A
+    num, den = n << (63 + 132), d * pi
+    t = (2 * num + den) // (2 * den) % (1 << 64)
+    return t - (1 << 64) if t >= 1 << 63 else t
+
+
+def _check_rows(name, t, dtype, shape, dev):
+    """t [N, ...] of the type and shape, on device number dev; each row contiguous, rows apart by any stride that holds one."""
+    if t.dtype != dtype or t.get_device() < 0:
+        raise ValueError("%s must be a CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, the object on cuda:%d" % (name, t.get_device(), dev))
+    row = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != row:
+            raise ValueError("%s: the rows themselves must be contiguous" % name)
+        row *= n
+    if t.shape[0] > 1 and t.stride(0) < row:
+        raise ValueError("%s: rows must not overlap" % name)
+
+
+def _row_stride(t):
+    """Elements from row to row of a checked tensor (one row: its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.numel()
+
+
+class _Append:
+    """What KvPool and Kv4Pool share: new rows on their way into the pool."""
+
+    def append(self, k, v, cu_seqlens, pos0, page_table, rope=None, positions=None, q=None, k_idx=None, k_idx_pool=None,
+               q_idx=None, idx_rope=None, idx_scale=1.0, q_out=None, q_idx_out=None, stream=None):
+        """Stores packed rows k (turned by `rope`) and v [N, H_kv, d] at the places of their tokens (cu_seqlens, pos0 and
+        page_table as in Kv4Pool.store), index keys k_idx [N, d_I] in k_idx_pool [n_pages, page_size, d_I] (bf16, or
+        uint8: E4M3 codes of idx_scale times the rows), and returns (q, q_idx) turned, None for what was not given.
+
+        The index rows are turned by idx_rope (`rope` where it is None).  positions [N] int32: what rows are turned by
+        where it is not their place in the cache.  Rows of the inputs may lie apart, as slices of a wider projection.
+        See msa_append_paged."""
+        N, S, dev = k.shape[0], cu_seqlens.numel() - 1, _device(self.workspace)
+        _check_rows("k", k, torch.bfloat16, (N, self.H_kv, self.d), dev)
+        _check_rows("v", v, torch.bfloat16, (N, self.H_kv, self.d), dev)
+        _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
+        _check_tensor("pos0", pos0, torch.int32, (S,), dev)
+        _check_tensor("page_table", page_table, torch.int32, (S, page_table.shape[-1]), dev)
+        if positions is not None:
+            _check_tensor("positions", positions, torch.int32, (N,), dev)
+        for name, r in (("rope", rope), ("idx_rope", idx_rope)):
+            if r is not None and r.turns.get_device() != dev:
+                raise ValueError("%s is on cuda:%d, the object on cuda:%d" % (name, r.turns.get_device(), dev))
+        rows = _c.msa_append_t()
+        rows.k, rows.v, rows.k_stride, rows.v_stride = k.data_ptr(), v.data_ptr(), _row_stride(k), _row_stride(v)
+        if positions is not None:
+            rows.positions = positions.data_ptr()
+        f8 = False
+        if k_idx is not None:
+            if k_idx_pool is None:
+                raise ValueError("k_idx needs k_idx_pool")
+            f8 = k_idx_pool.dtype == torch.uint8
+        elif k_idx_pool is not None:
+            raise ValueError("k_idx_pool needs k_idx")
+        elif q_idx_out is not None:
+            f8 = q_idx_out.dtype == torch.uint8
+        if q is not None:
+            _check_rows("q", q, torch.bfloat16, (N,) + tuple(q.shape[1:]), dev)
+            if q.dim() != 3 or q.shape[2] != self.d:
+                raise ValueError("q has shape %s, expected [N, H_q, %d]" % (tuple(q.shape), self.d))
+            q_out = self._fresh(q.shape, torch.bfloat16, q_out, "q_out", dev, stream)
+            rows.q, rows.q_stride, rows.q_out, rows.H_q = q.data_ptr(), _row_stride(q), q_out.data_ptr(), q.shape[1]
+        if k_idx is not None:
+            d_I = k_idx.shape[-1]
+            _check_rows("k_idx", k_idx, torch.bfloat16, (N, d_I), dev)
+            _check_tensor("k_idx_pool", k_idx_pool, torch.uint8 if f8 else torch.bfloat16, (self.n_pages, self.page_size, d_I), dev)
+            rows.k_idx, rows.k_idx_stride, rows.k_idx_pool, rows.d_I = k_idx.data_ptr(), _row_stride(k_idx), k_idx_pool.data_ptr(), d_I
+        if q_idx is not None:
+            d_I = q_idx.shape[-1]
+            if k_idx is not None and d_I != k_idx.shape[-1]:
+                raise ValueError("q_idx and k_idx differ in d_I")
+            _check_rows("q_idx", q_idx, torch.bfloat16, (N, self.H_kv, d_I), dev)
+            q_idx_out = self._fresh(q_idx.shape, torch.uint8 if f8 else torch.bfloat16, q_idx_out, "q_idx_out", dev, stream)
+            rows.q_idx, rows.q_idx_stride, rows.q_idx_out, rows.d_I = q_idx.data_ptr(), _row_stride(q_idx), q_idx_out.data_ptr(), d_I
+        rows.idx_f8, rows.idx_scale = int(f8), float(idx_scale)
+        idx_rope = None if k_idx is None and q_idx is None else rope if idx_rope is None else idx_rope
+        if N:
+            self._append(rows, N, cu_seqlens, S, pos0, page_table, page_table.shape[1], self.c, None if rope is None else rope.c,
+                         None if idx_rope is None else idx_rope.c, self.workspace, stream=stream)
+        return q_out if q is not None else None, q_idx_out if q_idx is not None else None
+
+    @staticmethod
+    def _fresh(shape, dtype, out, name, dev, stream):
+        if out is None:
+            with _allocating_for(stream):
+                return torch.empty(tuple(shape), dtype=dtype, device="cuda:%d" % dev)
+        _check_tensor(name, out, dtype, tuple(shape), dev)
+        return out
+
+
+class KvPool(_Append):
+    """A bf16 paged K/V cache: k and v [n_pages, page_size, H_kv, d].  ``KvPool.empty`` makes one.
+
+    What msa_decode_paged reads and MsaTreeDecode attends to.  Calls on other streams may touch other rows at the same
+    time; the error word that ``device_status`` reads is one for all of them, that of the call that ran last."""
+
+    _append = staticmethod(_c.msa_append_paged)
+
+    def __init__(self, k, v):
+        self.n_pages, self.page_size, self.H_kv, self.d = k.shape
+        for name, t in (("k", k), ("v", v)):
+            _check_tensor(name, t, torch.bfloat16, tuple(k.shape), k.get_device())
+        self.k, self.v = k, v
+        self.c = _c.kv_pool(k, v, self.n_pages, self.page_size, self.H_kv, self.d)
+        self.workspace = torch.empty(_c.msa_append_workspace(), dtype=torch.uint8, device=k.device)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, H_kv, d, device="cuda"):
+        return cls(*[torch.zeros((n_pages, page_size, H_kv, d), dtype=torch.bfloat16, device=device) for _ in range(2)])
+
+    def tensors(self):
+        return [self.k, self.v]
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
+class Kv4Pool(_Append):
     """A 4-bit paged K/V cache: codes [n_pages, page_size, H_kv, d / 2] and scales [n_pages, page_size, H_kv, 4]
-    of K and of V (uint8).  ``Kv4Pool.empty`` makes one.
+    of K and of V (uint8).  ``Kv4Pool.empty`` makes one.  ``append`` is ``store`` with the rotation on the way.
 
     Calls on other streams may touch other rows at the same time; the error word that ``device_status`` reads is one
     for all of them, that of the call that ran last."""
+
+    _append = staticmethod(_c.msa_append_paged_kv4)
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         self.n_pages, self.page_size, self.H_kv, half = k_codes.shape
@@ -266,6 +479,73 @@ class MsaDecodeKv4:
         return _c.msa_check_device_error(self.workspace, stream)
 
 
+class MsaTreeDecode:
+    """Dense attention of trees of up to T drafted tokens, one for each of B sequences, over a KvPool or a Kv4Pool.
+
+    (T = 1 is a dense decode step.)  A call returns the object's own ``out`` [B, T, H_q, d] and ``lse`` [B, T, H_q], which
+    the next call overwrites, nodes past a tree's length left as they were; two calls in flight at once need two objects."""
+
+    def __init__(self, pool, B, T, max_pages, H_q):
+        device = pool.tensors()[0].device
+        self.pool, self.B, self.T, self.max_pages, self.H_q = pool, B, T, max_pages, H_q
+        self.workspace = torch.empty(_c.msa_tree_decode_workspace(B, T, H_q, pool.H_kv, pool.d), dtype=torch.uint8, device=device)
+        self.out = torch.zeros((B, T, H_q, pool.d), dtype=torch.bfloat16, device=device)
+        self.lse = torch.zeros((B, T, H_q), dtype=torch.float32, device=device)
+        self._call = _c.msa_tree_decode_paged_kv4 if isinstance(pool, Kv4Pool) else _c.msa_tree_decode_paged
+
+    def __call__(self, q, page_table, ctx_len, parents, tree_len=None, scale=None, stream=None):
+        """q [B, T, H_q, d]; parents [B, T] int32 (-1: a root); ctx_len [B]: tokens before the tree, whose node j is token
+        ctx_len + j of the cache; tree_len [B]: nodes of each tree (T each where None)."""
+        dev = _device(self.workspace)
+        _check_tensor("q", q, torch.bfloat16, (self.B, self.T, self.H_q, self.pool.d), dev)
+        _check_tensor("page_table", page_table, torch.int32, (self.B, self.max_pages), dev)
+        _check_tensor("ctx_len", ctx_len, torch.int32, (self.B,), dev)
+        _check_tensor("parents", parents, torch.int32, (self.B, self.T), dev)
+        if tree_len is not None:
+            _check_tensor("tree_len", tree_len, torch.int32, (self.B,), dev)
+        scale = 1.0 / math.sqrt(self.pool.d) if scale is None else scale
+        self._call(q, self.pool.c, page_table, self.max_pages, ctx_len, tree_len, parents, self.B, self.T, self.H_q, scale,
+                   self.out, self.lse, self.workspace, stream=stream)
+        return self.out, self.lse
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
+class DraftVerifier:
+    """Verification of trees of up to T nodes, one for each of B sequences, over a vocabulary of V tokens.
+
+    A call returns the object's own ``path`` [B, T] (accepted nodes, node 0 first, then -1), ``n_path`` [B] and
+    ``next_token`` [B], int32, which the next call overwrites; PagedCache.accept takes them as they are."""
+
+    def __init__(self, B, T, V, device="cuda"):
+        self.B, self.T, self.V = B, T, V
+        self.workspace = torch.empty(_c.msa_verify_workspace(), dtype=torch.uint8, device=device)
+        self.path = torch.empty((B, T), dtype=torch.int32, device=device)
+        self.n_path = torch.empty((B,), dtype=torch.int32, device=device)
+        self.next_token = torch.empty((B,), dtype=torch.int32, device=device)
+
+    def __call__(self, probs, tokens, parents, u, u_last, draft_probs=None, tree_len=None, stream=None):
+        """probs, draft_probs [B, T, V] fp32: the target's distribution after each node, and that which its children were
+        drawn from (None: the drafts were certain); u [B, T] and u_last [B] fp32 random numbers in [0, 1)."""
+        dev = _device(self.workspace)
+        _check_tensor("probs", probs, torch.float32, (self.B, self.T, self.V), dev)
+        _check_tensor("tokens", tokens, torch.int32, (self.B, self.T), dev)
+        _check_tensor("parents", parents, torch.int32, (self.B, self.T), dev)
+        _check_tensor("u", u, torch.float32, (self.B, self.T), dev)
+        _check_tensor("u_last", u_last, torch.float32, (self.B,), dev)
+        if draft_probs is not None:
+            _check_tensor("draft_probs", draft_probs, torch.float32, (self.B, self.T, self.V), dev)
+        if tree_len is not None:
+            _check_tensor("tree_len", tree_len, torch.int32, (self.B,), dev)
+        _c.msa_verify_tree(probs, draft_probs, tokens, parents, tree_len, u, u_last, self.B, self.T, self.V, self.path,
+                           self.n_path, self.next_token, self.workspace, stream=stream)
+        return self.path, self.n_path, self.next_token
+
+    def device_status(self, stream=None):
+        return _c.msa_check_device_error(self.workspace, stream)
+
+
 class PagedCache:
     """Page tables, lengths and reference counts of a paged cache, and the pools that they address.
 
@@ -289,7 +569,8 @@ class PagedCache:
         self.c_pools = _c.page_pools((t, t.numel() // n_pages * t.element_size()) for t in self.pools)
         self.page_map = torch.empty((n_pages,), dtype=torch.int32, device=refs.device)
         self.n_live = torch.empty((1,), dtype=torch.int32, device=refs.device)
-        need = max(_c.msa_pages_workspace(self.c, 0), _c.msa_pages_workspace(self.c, 4096))  # compact, the most entries
+        need = max(_c.msa_pages_workspace(self.c, 0), _c.msa_pages_workspace(self.c, 4096),  # compact, the most entries
+                   _c.msa_pages_accept_workspace(self.c, 4096, 64))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=refs.device)
 
     @classmethod
@@ -314,6 +595,18 @@ class PagedCache:
         n, dev = seqs.numel(), _device(self.workspace)
         _check_tensor("seqs", seqs, torch.int32, (n,), dev)
         _c.msa_pages_free(self.c, seqs, n, self.workspace, stream=stream)
+
+    def accept(self, seqs, base_len, path, n_path, stream=None):
+        """Of sequence seqs[i]'s tokens from base_len[i] on, those at base_len[i] + path[i][: n_path[i]] stay, in their
+        order, and the sequence ends after them (path [n, T] and n_path [n] as DraftVerifier returns them; n_path 0 cuts
+        the sequence off at base_len)."""
+        n, dev = seqs.numel(), _device(self.workspace)
+        _check_tensor("seqs", seqs, torch.int32, (n,), dev)
+        _check_tensor("base_len", base_len, torch.int32, (n,), dev)
+        _check_tensor("path", path, torch.int32, (n, path.shape[-1]), dev)
+        _check_tensor("n_path", n_path, torch.int32, (n,), dev)
+        _c.msa_pages_accept(self.c, seqs, base_len, path, n_path, n, path.shape[1], self.c_pools, len(self.pools),
+                            self.workspace, stream=stream)
 
     def compact(self, stream=None):
         """Returns (page_map [n_pages], n_live [1]): each page's new id (-1 where it was free), and the pages held.

@@ -669,6 +669,221 @@ msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, cons
                          block_idx, workspace, workspace_bytes, stream, true);
 }
 
+// ---------------------------------------------------------------- rotary positions, rows into a cache
+static bool misaligned4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
+
+static msa_status_t check_rope(const msa_rope_t* r, int d, int most) {
+  if (!r || !r->turns || ((uintptr_t)r->turns & 7u) || r->rot < 1 || r->rot > d) return MSA_ERR_INVALID_ARGUMENT;
+  if (!(r->factor - r->factor == 0.f)) return MSA_ERR_INVALID_ARGUMENT;  // infinite or NaN
+  return r->rot % 16 != 0 || r->rot > most ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+
+static msa::Rope rope_view(const msa_rope_t* r) {
+  msa::Rope v = {};
+  if (!r) return v;
+  v.turns = r->turns;
+  v.rot = r->rot;
+  v.interleaved = r->interleaved != 0;
+  v.factor = r->factor;
+  return v;
+}
+
+msa_status_t msa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, int64_t N, int H, int d, int f32,
+                      const int32_t* positions, const msa_rope_t* rope, int inverse, msa_stream_t stream) {
+  if (!x || !y || !positions || N < 1 || H < 1 || d < 1) return MSA_ERR_INVALID_ARGUMENT;
+  if (d != 32 && d != 64 && d != 128 && d != 256) return MSA_ERR_UNSUPPORTED;
+  msa_status_t st = check_rope(rope, d, 256);
+  if (st != MSA_OK) return st;
+  const int64_t row = (int64_t)H * d;
+  if (H > 65536 || N >= (int64_t)1 << 31) return MSA_ERR_UNSUPPORTED;
+  if (x_stride < row || y_stride < row || x_stride % (f32 ? 4 : 8) != 0 || y_stride % (f32 ? 4 : 8) != 0)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(y) || misaligned4(positions)) return MSA_ERR_INVALID_ARGUMENT;
+  if (x == y && x_stride != y_stride) return MSA_ERR_INVALID_ARGUMENT;
+  return finish(msa::launch_rope(x, x_stride, y, y_stride, N, H, d, f32 != 0, positions, rope_view(rope), inverse != 0,
+                                 (cudaStream_t)stream));
+}
+
+size_t msa_append_workspace(void) { return kHeader; }
+
+static msa_status_t check_kv(const msa_kv_pool_t* p, const int32_t* page_table, int64_t max_pages) {
+  if (!p || !p->k || !p->v || !page_table) return MSA_ERR_INVALID_ARGUMENT;
+  if (p->n_pages < 1 || p->page_size < 16 || p->page_size % 16 != 0 || p->H_kv < 1 || p->d < 1 || max_pages < 1)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if ((p->d != 64 && p->d != 128) || p->H_kv > 64) return MSA_ERR_UNSUPPORTED;
+  if (p->n_pages >= (int64_t)1 << 31 || max_pages >= (int64_t)1 << 31 ||
+      max_pages * (int64_t)p->page_size >= (int64_t)1 << 31)
+    return MSA_ERR_UNSUPPORTED;
+  if (!aligned16(p->k) || !aligned16(p->v) || misaligned4(page_table)) return MSA_ERR_INVALID_ARGUMENT;
+  return MSA_OK;
+}
+
+// A kind of rows: present, aligned, a stride that holds a token's.
+static bool bad_rows(const void* p, int64_t stride, int64_t row) {
+  return !p || !aligned16(p) || stride < row || stride % 8 != 0;
+}
+
+static msa_status_t append_impl(const msa_append_t* r, int64_t N, const int32_t* cu_seqlens, int S, const int32_t* pos0,
+                                const int32_t* page_table, int64_t max_pages, int H_kv, int d, int64_t n_pages, int page,
+                                void* k_pool, void* v_pool, const msa::Kv4Pool* kv4, const msa_rope_t* rope,
+                                const msa_rope_t* rope_idx, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  if (!r || !cu_seqlens || !pos0 || N < 1 || S < 1) return MSA_ERR_INVALID_ARGUMENT;
+  if (misaligned4(cu_seqlens) || misaligned4(pos0) || misaligned4(r->positions)) return MSA_ERR_INVALID_ARGUMENT;
+  if (N >= (int64_t)1 << 31 || S > kMaxPacked) return MSA_ERR_UNSUPPORTED;
+  if (bad_rows(r->k, r->k_stride, (int64_t)H_kv * d) || bad_rows(r->v, r->v_stride, (int64_t)H_kv * d))
+    return MSA_ERR_INVALID_ARGUMENT;
+  const bool idx = r->k_idx || r->q_idx;
+  if (r->q) {
+    if (r->H_q < 1 || bad_rows(r->q, r->q_stride, (int64_t)r->H_q * d) || !r->q_out || !aligned16(r->q_out))
+      return MSA_ERR_INVALID_ARGUMENT;
+    if (r->H_q > 512) return MSA_ERR_UNSUPPORTED;
+    if (r->q_out == r->q && r->q_stride != (int64_t)r->H_q * d) return MSA_ERR_INVALID_ARGUMENT;
+  }
+  if (idx) {
+    if (r->d_I < 1) return MSA_ERR_INVALID_ARGUMENT;
+    if (r->d_I != 32 && r->d_I != 64 && r->d_I != 128) return MSA_ERR_UNSUPPORTED;
+    if (r->idx_f8 && !(r->idx_scale > 0.f && r->idx_scale - r->idx_scale == 0.f)) return MSA_ERR_INVALID_ARGUMENT;
+    if (r->k_idx && (bad_rows(r->k_idx, r->k_idx_stride, r->d_I) || !r->k_idx_pool || !aligned16(r->k_idx_pool)))
+      return MSA_ERR_INVALID_ARGUMENT;
+    if (r->q_idx && (bad_rows(r->q_idx, r->q_idx_stride, (int64_t)H_kv * r->d_I) || !r->q_idx_out || !aligned16(r->q_idx_out)))
+      return MSA_ERR_INVALID_ARGUMENT;
+    if (r->q_idx && r->q_idx_out == r->q_idx && (r->idx_f8 || r->q_idx_stride != (int64_t)H_kv * r->d_I))
+      return MSA_ERR_INVALID_ARGUMENT;
+  } else if (rope_idx) {
+    return MSA_ERR_INVALID_ARGUMENT;
+  }
+  msa_status_t st = rope ? check_rope(rope, d, 128) : MSA_OK;
+  if (st == MSA_OK && rope_idx) st = check_rope(rope_idx, r->d_I, 128);
+  if (st != MSA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, kHeader, s, msa::kv4_rows_report(N) ? 0 : kHeader);
+  if (st != MSA_OK) return st;
+  msa::AppendRows a = {};
+  a.q = (const uint16_t*)r->q;
+  a.k = (const uint16_t*)r->k;
+  a.v = (const uint16_t*)r->v;
+  a.q_idx = (const uint16_t*)r->q_idx;
+  a.k_idx = (const uint16_t*)r->k_idx;
+  a.q_stride = r->q_stride;
+  a.k_stride = r->k_stride;
+  a.v_stride = r->v_stride;
+  a.q_idx_stride = r->q_idx_stride;
+  a.k_idx_stride = r->k_idx_stride;
+  a.q_out = (uint16_t*)r->q_out;
+  a.q_idx_out = r->q_idx_out;
+  a.k_idx_pool = r->k_idx_pool;
+  a.positions = r->positions;
+  a.H_q = r->q ? r->H_q : 0;
+  a.H_kv = H_kv;
+  a.d_I = idx ? r->d_I : 32;  // (no index rows: any width)
+  a.idx_f8 = r->idx_f8 != 0;
+  a.idx_scale = r->idx_scale;
+  a.rope = rope_view(rope);
+  a.rope_idx = rope_view(rope_idx);
+  return finish(msa::launch_append(a, N, cu_seqlens, S, pos0, page_table, max_pages, k_pool, v_pool, kv4, n_pages, page, d,
+                                   (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_append_paged(const msa_append_t* rows, int64_t N, const int32_t* cu_seqlens, int S,
+                              const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                              const msa_kv_pool_t* pool, const msa_rope_t* rope, const msa_rope_t* rope_idx,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  return append_impl(rows, N, cu_seqlens, S, pos0, page_table, max_pages, pool->H_kv, pool->d, pool->n_pages, pool->page_size,
+                     pool->k, pool->v, nullptr, rope, rope_idx, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_append_paged_kv4(const msa_append_t* rows, int64_t N, const int32_t* cu_seqlens, int S,
+                                  const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                                  const msa_kv4_pool_t* pool, const msa_rope_t* rope, const msa_rope_t* rope_idx,
+                                  void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv4(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  const msa::Kv4Pool kv4 = kv4_pool(pool);
+  return append_impl(rows, N, cu_seqlens, S, pos0, page_table, max_pages, pool->H_kv, pool->d, pool->n_pages, pool->page_size,
+                     nullptr, nullptr, &kv4, rope, rope_idx, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- drafted trees
+constexpr int kMaxTree = 64;
+
+static msa_status_t check_tree(int B, int T, int H_q, int H_kv, int d) {
+  if (B < 1 || T < 1) return MSA_ERR_INVALID_ARGUMENT;
+  msa_status_t st = check_heads(H_q, H_kv, d);
+  if (st != MSA_OK) return st;
+  return T > kMaxTree || B > 1 << 20 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+
+size_t msa_tree_decode_workspace(int B, int T, int H_q, int H_kv, int d) {
+  if (check_tree(B, T, H_q, H_kv, d) != MSA_OK) return kHeader;
+  return kHeader + msa::tree_scratch_bytes(msa::tree_plan(B, T, H_q, H_kv, d));
+}
+
+static msa_status_t tree_impl(const void* q, const void* k_pool, const void* v_pool, const msa::Kv4Pool* kv4, int H_kv, int d,
+                              int64_t n_pages, int page, const int32_t* page_table, int64_t max_pages, const int32_t* ctx_len,
+                              const int32_t* tree_len, const int32_t* parents, int B, int T, int H_q, float scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  if (!q || !ctx_len || !parents || !out) return MSA_ERR_INVALID_ARGUMENT;
+  msa_status_t st = check_tree(B, T, H_q, H_kv, d);
+  if (st != MSA_OK) return st;
+  if (!kv4 && n_pages * (int64_t)page >= (int64_t)1 << 31) return MSA_ERR_UNSUPPORTED;  // TMA coordinates are int32
+  if (!(scale > 0.f) || scale != scale) return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(out) || misaligned4(ctx_len) || misaligned4(tree_len) || misaligned4(parents) || misaligned4(lse))
+    return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  const msa::TreePlan p = msa::tree_plan(B, T, H_q, H_kv, d);
+  st = begin(workspace, workspace_bytes, kHeader + msa::tree_scratch_bytes(p), s, 0);  // the first kernel clears the status
+  if (st != MSA_OK) return st;
+  msa::CacheMap map;
+  map.table = page_table;
+  map.max_pages = max_pages;
+  map.n_pages = n_pages;
+  map.page = page;
+  return finish(msa::launch_tree(q, p, k_pool, v_pool, kv4, map, ctx_len, tree_len, parents, scale, out, lse,
+                                 (char*)workspace + kHeader, (msa::DeviceStatus*)workspace, s));
+}
+
+msa_status_t msa_tree_decode_paged(const void* q, const msa_kv_pool_t* pool, const int32_t* page_table,
+                                   int64_t max_pages, const int32_t* ctx_len, const int32_t* tree_len,
+                                   const int32_t* parents, int B, int T, int H_q, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  return tree_impl(q, pool->k, pool->v, nullptr, pool->H_kv, pool->d, pool->n_pages, pool->page_size, page_table, max_pages,
+                   ctx_len, tree_len, parents, B, T, H_q, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_tree_decode_paged_kv4(const void* q, const msa_kv4_pool_t* pool, const int32_t* page_table,
+                                       int64_t max_pages, const int32_t* ctx_len, const int32_t* tree_len,
+                                       const int32_t* parents, int B, int T, int H_q, float scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_kv4(pool, page_table, max_pages);
+  if (st != MSA_OK) return st;
+  const msa::Kv4Pool kv4 = kv4_pool(pool);
+  return tree_impl(q, nullptr, nullptr, &kv4, pool->H_kv, pool->d, pool->n_pages, pool->page_size, page_table, max_pages, ctx_len,
+                   tree_len, parents, B, T, H_q, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t msa_verify_workspace(void) { return kHeader; }
+
+msa_status_t msa_verify_tree(const float* probs, const float* draft_probs, const int32_t* tokens,
+                             const int32_t* parents, const int32_t* tree_len, const float* u, const float* u_last,
+                             int B, int T, int64_t V, int32_t* path, int32_t* n_path, int32_t* next, void* workspace,
+                             size_t workspace_bytes, msa_stream_t stream) {
+  if (!probs || !tokens || !parents || !u || !u_last || !path || !n_path || !next || B < 1 || T < 1 || V < 1)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (T > kMaxTree || B > 1 << 20 || V >= (int64_t)1 << 31) return MSA_ERR_UNSUPPORTED;
+  if (!aligned16(probs) || !aligned16(draft_probs) || misaligned4(tokens) || misaligned4(parents) || misaligned4(tree_len) ||
+      misaligned4(u) || misaligned4(u_last) || misaligned4(path) || misaligned4(n_path) || misaligned4(next))
+    return MSA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = (cudaStream_t)stream;
+  msa_status_t st = begin(workspace, workspace_bytes, kHeader, s, msa::verify_reports(B, T) ? 0 : kHeader);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_verify(probs, draft_probs, tokens, parents, tree_len, u, u_last, B, T, V, path, n_path, next,
+                                   (msa::DeviceStatus*)workspace, s));
+}
+
 // ---------------------------------------------------------------- pages of a cache
 static msa_status_t check_pages(const msa_pages_t* p, int n) {
   if (!p || !p->page_table || !p->ctx_len || !p->refs || n < 0) return MSA_ERR_INVALID_ARGUMENT;
@@ -751,6 +966,30 @@ msa_status_t msa_pages_free(const msa_pages_t* pages, const int32_t* seqs, int n
   st = begin(workspace, workspace_bytes, kHeader, s);
   if (st != MSA_OK) return st;
   return finish(msa::launch_pages_free(pages_view(pages), seqs, n, (msa::DeviceStatus*)workspace, s));
+}
+
+size_t msa_pages_accept_workspace(const msa_pages_t* pages, int n, int T) {
+  if (check_pages(pages, n) != MSA_OK || T < 1 || T > kMaxTree) return kHeader;
+  return kHeader + msa::accept_scratch_bytes(pages_view(pages), n, T);
+}
+
+msa_status_t msa_pages_accept(const msa_pages_t* pages, const int32_t* seqs, const int32_t* base, const int32_t* path,
+                              const int32_t* n_path, int n, int T, const msa_page_pool_t* pools, int n_pools,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t st = check_pages(pages, n);
+  if (st != MSA_OK) return st;
+  msa::PagePools pp;
+  st = pools_view(pools, n_pools, &pp);
+  if (st != MSA_OK) return st;
+  for (int i = 0; i < pp.n; ++i)
+    if (pp.page_bytes[i] % (size_t)pages->page_size != 0) return MSA_ERR_INVALID_ARGUMENT;
+  if (bad_list(seqs, n) || bad_list(base, n) || bad_list(path, n) || bad_list(n_path, n) || T < 1) return MSA_ERR_INVALID_ARGUMENT;
+  if (T > kMaxTree) return MSA_ERR_UNSUPPORTED;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = begin(workspace, workspace_bytes, msa_pages_accept_workspace(pages, n, T), s, n > 0 ? 0 : kHeader);
+  if (st != MSA_OK) return st;
+  return finish(msa::launch_pages_accept(pages_view(pages), seqs, base, path, n_path, n, T, pp, (char*)workspace + kHeader,
+                                         (msa::DeviceStatus*)workspace, s));
 }
 
 msa_status_t msa_pages_compact(const msa_pages_t* pages, const msa_page_pool_t* pools, int n_pools, int32_t* page_map,

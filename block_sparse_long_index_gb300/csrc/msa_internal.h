@@ -208,6 +208,42 @@ cudaError_t launch_dense_decode(const void* q, const Kv4Pool& pool, const int32_
                                 const int32_t* ctx_len, int B, int H_q, float scale, void* out, float* lse, void* scratch,
                                 DeviceStatus* st, cudaStream_t s);
 
+// ---- rotary positions and rows into a paged cache (msa_rope.cu)
+struct Rope {
+  const uint64_t* turns;  // [rot / 2] 2^-64 turns a position
+  int rot;                // leading channels that turn, in pairs (a multiple of 16; 0: none)
+  int interleaved;        // pairs (2 i, 2 i + 1) instead of (i, i + rot / 2)
+  float factor;           // of the turned channels
+};
+struct AppendRows {
+  const uint16_t *q, *k, *v, *q_idx, *k_idx;  // q, q_idx, k_idx: null where there are none
+  int64_t q_stride, k_stride, v_stride, q_idx_stride, k_idx_stride;  // elements from token to token
+  uint16_t* q_out;
+  void *q_idx_out, *k_idx_pool;  // bf16 or (idx_f8) E4M3 codes
+  const int32_t* positions;      // null: token positions
+  int H_q, H_kv, d_I, idx_f8;
+  float idx_scale;
+  Rope rope, rope_idx;
+};
+cudaError_t launch_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, int64_t N, int H, int d, bool f32,
+                        const int32_t* positions, const Rope& rope, bool inverse, cudaStream_t s);
+// kv4 null: bf16 pools
+cudaError_t launch_append(const AppendRows& rows, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
+                          const int32_t* table, int64_t max_pages, void* k_pool, void* v_pool, const Kv4Pool* kv4,
+                          int64_t n_pages, int page, int d, DeviceStatus* st, cudaStream_t s);
+
+// ---- attention of drafted trees over a paged cache (msa_tree.cu)
+struct TreePlan {
+  int B, T, H_q, H_kv, d;
+  int RG, RU;  // row groups of a (sequence, K/V head), rows (node, head) of one
+};
+TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d);
+size_t tree_scratch_bytes(const TreePlan& p);
+// kv4 null: bf16 pools
+cudaError_t launch_tree(const void* q, const TreePlan& p, const void* k_pool, const void* v_pool, const Kv4Pool* kv4,
+                        const CacheMap& map, const int32_t* ctx, const int32_t* tree_len, const int32_t* parents, float scale, void* out,
+                        float* lse, void* scratch, DeviceStatus* st, cudaStream_t s);
+
 // ---- page tables (msa_pages.cu)
 struct Pages {
   int32_t* table;  // [n_seqs, max_pages]
@@ -231,6 +267,15 @@ cudaError_t launch_pages_fork(const Pages& p, const int32_t* src, const int32_t*
 cudaError_t launch_pages_free(const Pages& p, const int32_t* seqs, int n, DeviceStatus* st, cudaStream_t s);
 cudaError_t launch_pages_compact(const Pages& p, const PagePools& pools, int32_t* page_map, int32_t* n_live, void* scratch,
                                  DeviceStatus* st, cudaStream_t s);
+size_t accept_scratch_bytes(const Pages& p, int n, int T);
+cudaError_t launch_pages_accept(const Pages& p, const int32_t* seqs, const int32_t* base, const int32_t* path, const int32_t* n_path,
+                                int n, int T, const PagePools& pools, void* scratch, DeviceStatus* st, cudaStream_t s);
+
+// ---- verification of drafted trees (msa_draft.cu)
+bool verify_reports(int B, int T);  // the kernel writes the status itself (it is then not cleared before)
+cudaError_t launch_verify(const float* probs, const float* draft_probs, const int32_t* tokens, const int32_t* parents,
+                          const int32_t* tree_len, const float* u, const float* u_last, int B, int T, int64_t V, int32_t* path,
+                          int32_t* n_path, int32_t* next, DeviceStatus* st, cudaStream_t s);
 
 // Fixed device scratch of msa_decode_noalloc (8 MiB, shared by all calls on a
 // device).  Returns its device address for the current device (looked up on

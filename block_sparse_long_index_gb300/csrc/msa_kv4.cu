@@ -2,6 +2,7 @@
 #include <math.h>
 
 #include "msa_kv4.cuh"
+#include "msa_rows.cuh"
 #include "msa_sm100.cuh"
 
 namespace msa {
@@ -10,37 +11,6 @@ namespace {
 
 using namespace kv4;
 using namespace sm100;
-
-constexpr int kRowThreads = 256;
-
-// Where packed row i, of one of the sequences, goes: the pool row of its token, or -1 (bad: flagged).
-struct RowMap {
-  const int32_t* cu;    // [S + 1]
-  const int32_t* pos0;  // [S] token position of each sequence's first row
-  const int32_t* table;
-  int64_t max_pages, n_pages;
-  int S, page;
-
-  __device__ __forceinline__ int64_t row(int64_t i, DeviceStatus* st) const {
-    int lo = 0, hi = S;  // a sequence with cu[lo] <= i < cu[lo + 1] (a search by halves ends whatever cu holds)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cu[mid] <= i) lo = mid; else hi = mid;
-    }
-    const int64_t t = (int64_t)pos0[lo] + (i - cu[lo]);
-    if (i < cu[lo] || i >= cu[lo + 1] || pos0[lo] < 0 || t >= max_pages * page) {
-      raise_error(st, kErrBadIndex, 6u);
-      return -1;
-    }
-    const int64_t lp = t / page;
-    const int32_t pp = table[(int64_t)lo * max_pages + lp];
-    if (pp < 0 || (int64_t)pp >= n_pages) {
-      raise_error(st, kErrBadIndex, 7u);
-      return -1;
-    }
-    return (int64_t)pp * page + (t - lp * page);
-  }
-};
 
 // Rows in (store) and out (load): bound by HBM, 2 d bytes of bf16 and d / 2 + 4 of codes and scales a head row, each
 // touched once; the store comes near its instructions too (74 % of issue slots: maxima, scale, 8 roundings a thread).
@@ -58,32 +28,6 @@ struct RowTile {
     tpp = per_tok < kRowThreads ? kRowThreads / per_tok : 1;
   }
 };
-
-// The pool rows of the CTA's `n` packed rows from i0 on; `none` for those of no sequence.
-// A call of at most kRowThreads rows has its status written by CTA 0 alone, which looks up all of them (the other CTAs
-// report nothing): the error word then needs no clearing before the kernel, a launch of its own (48 tokens in and out
-// 12.4 -> 10.2 us on the GPU).
-__device__ __forceinline__ void look_up(const RowMap& map, int64_t N, int64_t i0, int n, int64_t none, int64_t* rows,
-                                        DeviceStatus* st) {
-  __shared__ unsigned int est[2];
-  const int64_t in0 = map.cu[0], in1 = min((int64_t)map.cu[map.S], N);
-  auto row = [&](int64_t i, DeviceStatus* s) { return i >= in0 && i < in1 ? map.row(i, s) : none; };
-  if (!kv4_rows_report(N) || blockIdx.x) {
-    for (int t = threadIdx.x; t < n; t += kRowThreads) rows[t] = row(i0 + t, kv4_rows_report(N) ? nullptr : st);
-    __syncthreads();
-    return;
-  }
-  DeviceStatus* own = reinterpret_cast<DeviceStatus*>(est);  // (an error touches its first two words)
-  if (threadIdx.x == 0) est[0] = est[1] = 0u;
-  __syncthreads();
-  const int64_t r = row(threadIdx.x, own);
-  if ((int)threadIdx.x < n) rows[threadIdx.x] = r;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    st->flags = own->flags;
-    st->first_code = own->first_code;
-  }
-}
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* __restrict__ k,
@@ -115,32 +59,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_store_kernel(const uint16_t* 
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
-#pragma unroll
-        for (int o = 1; o < LPG; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(lanes, mx, o));
-        mx = max(mx & 0xFFFFu, mx >> 16);
-        uint32_t sb = scale_of(mx), code;
-        const float s = scale_f32(sb), inv = __fdividef(1.0f, s);
-        uint64_t x2[4];  // channels 2 j and 2 j + 1
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x2[j] = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
-        if (mx >= 0x7F80u) {
-          sb = kScaleNaN;
-          code = 0x88888888u;
-        } else {
-          if (sb == kScaleMax) {  // the one scale whose group may reach past 7 s
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float a, b;
-              f2_unpack(x2[j], a, b);
-              x2[j] = f2_pack(fminf(fmaxf(a, -7.f * s), 7.f * s), fminf(fmaxf(b, -7.f * s), 7.f * s));
-            }
-          }
-          code = codes8(x2, inv);
-        }
+        uint32_t sb, code;
+        encode8<LPG>(x[u], lanes, code, sb);
         if (row[u] >= 0) {
           reinterpret_cast<uint32_t*>(codes)[row[u] * half + e] = code;
           if (e % LPG == 0) scales[row[u] * (pool.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
@@ -882,18 +802,6 @@ __global__ void __launch_bounds__(kCombThreads) kv4_combine_kernel(const SplitRo
   if (lane == 0 && lse) lse[hq] = any ? (M + log2f(L)) * 0.69314718055994530942f : -kInf;
 }
 
-RowMap row_map(const Kv4Pool& pool, const int32_t* cu, int S, const int32_t* pos0, const int32_t* table, int64_t max_pages) {
-  RowMap m;
-  m.cu = cu;
-  m.pos0 = pos0;
-  m.table = table;
-  m.max_pages = max_pages;
-  m.n_pages = pool.n_pages;
-  m.S = S;
-  m.page = pool.page;
-  return m;
-}
-
 int decode_ctas() { return 2 * num_sms(); }
 
 template <int D, int HC>
@@ -948,7 +856,7 @@ static int rows_rounds(int64_t N, int tpp) {
 
 cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                              const int32_t* table, int64_t max_pages, const Kv4Pool& pool, DeviceStatus* st, cudaStream_t s) {
-  const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
+  const RowMap map = row_map(cu, S, pos0, table, max_pages, pool.n_pages, pool.page);
   const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
   auto kern = pool.d == 64 ? kv4_store_kernel<64> : kv4_store_kernel<128>;
   kern<<<(unsigned)ceil_div(N, R * kUnroll * tpp), kRowThreads, 0, s>>>((const uint16_t*)k, (const uint16_t*)v, N, R, map,
@@ -958,7 +866,7 @@ cudaError_t launch_kv4_store(const void* k, const void* v, int64_t N, const int3
 
 cudaError_t launch_kv4_load(const Kv4Pool& pool, int64_t N, const int32_t* cu, int S, const int32_t* pos0,
                             const int32_t* table, int64_t max_pages, void* k, void* v, DeviceStatus* st, cudaStream_t s) {
-  const RowMap map = row_map(pool, cu, S, pos0, table, max_pages);
+  const RowMap map = row_map(cu, S, pos0, table, max_pages, pool.n_pages, pool.page);
   const int tpp = RowTile(pool.H_kv, pool.d / 8).tpp, R = rows_rounds(N, tpp);
   auto kern = pool.d == 64 ? kv4_load_kernel<64> : kv4_load_kernel<128>;
   kern<<<(unsigned)ceil_div(N, R * kUnroll * tpp), kRowThreads, 0, s>>>(pool, N, R, map, (uint16_t*)k, (uint16_t*)v, st);

@@ -408,6 +408,129 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(Pages p, Pa
   });
 }
 
+// ---------------------------------------------------------------- the accepted branch of a tree of drafts
+// Entry i keeps, of the tokens from base[i] on, those at base[i] + path[i][0 .. n_path[i]); they move together, in order,
+// and the sequence ends after them.
+struct AcceptArgs {
+  const int32_t *seqs, *base, *path, *n_path;
+  int n, T;
+};
+struct AcceptScratch {
+  int32_t* ok;   // 1: the call is carried out
+  int64_t* src;  // [n, T] pool rows, from and to
+  int64_t* dst;
+};
+
+// One CTA, a warp an entry.  What an entry moves or gives up has to be its own alone (count 1): then no other sequence
+// sees it change, and no two entries meet.
+__global__ void __launch_bounds__(kThreads) pages_accept_plan_kernel(Pages p, AcceptArgs a, AcceptScratch w, DeviceStatus* st) {
+  extern __shared__ int dyn[];
+  int* names = dyn;  // [n]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();  // the moving grid waits for this one's end
+  clear_errors(st);
+  for (int i = tid; i < a.n; i += kThreads) names[i] = a.seqs[i];
+  __syncthreads();
+  int bad = 0;
+  for (int i = warp; i < a.n; i += kThreads / 32) {
+    const int32_t s = names[i], b0 = a.base[i], k = a.n_path[i];
+    for (int j = lane; j < i; j += 32) bad |= names[j] == s;
+    if (s < 0 || s >= p.n_seqs) {
+      bad = 1;
+      continue;
+    }
+    const int32_t len = p.ctx[s];
+    if (len < 0 || (int64_t)len > p.max_pages * p.page || b0 < 0 || b0 > len || k < 0 || k > a.T) {
+      bad = 1;
+      continue;
+    }
+    const int32_t* path = a.path + (int64_t)i * a.T;
+    for (int j = lane; j < k; j += 32) bad |= path[j] < 0 || path[j] >= len - b0 || (j > 0 && path[j] <= path[j - 1]);
+    const int32_t* row = p.table + (int64_t)s * p.max_pages;
+    for (int64_t j = b0 / p.page + lane; j < pages_of(len, p.page); j += 32)
+      bad |= row[j] < 0 || (int64_t)row[j] >= p.n_pages || p.refs[row[j]] != 1;
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) *w.ok = !bad;
+  if (bad) {
+    if (tid == 0) raise_error(st, kErrBadIndex, 17u);
+    return;
+  }
+  for (int i = warp; i < a.n; i += kThreads / 32) {
+    const int32_t s = names[i], b0 = a.base[i], k = a.n_path[i], len = p.ctx[s];
+    int32_t* row = p.table + (int64_t)s * p.max_pages;
+    for (int j = lane; j < k; j += 32) {
+      const int32_t f = b0 + a.path[(int64_t)i * a.T + j], t = b0 + j;
+      w.src[(int64_t)i * a.T + j] = (int64_t)row[f / p.page] * p.page + f % p.page;
+      w.dst[(int64_t)i * a.T + j] = (int64_t)row[t / p.page] * p.page + t % p.page;
+    }
+    __syncwarp();
+    for (int64_t j = pages_of(b0 + k, p.page) + lane; j < pages_of(len, p.page); j += 32) {
+      p.refs[row[j]] = 0;
+      row[j] = -1;
+    }
+    if (lane == 0) p.ctx[s] = b0 + k;
+  }
+}
+
+// A thread has one column (of type V) of an entry's rows in one pool and takes its moves in order, eight reads before
+// their eight writes: a row is written only after it was read, because dst[j] <= path[j] < path[j + 1].
+template <typename V>
+__device__ __forceinline__ void move_rows(char* base, size_t row_bytes, size_t col, const int64_t* src, const int64_t* dst, int k) {
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    V x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j0 + u < k) x[u] = *reinterpret_cast<const V*>(base + src[j0 + u] * row_bytes + col);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j0 + u < k) *reinterpret_cast<V*>(base + dst[j0 + u] * row_bytes + col) = x[u];
+  }
+}
+__host__ __device__ inline int column_bytes(size_t row_bytes) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : 1; }
+
+__global__ void __launch_bounds__(kCopyThreads) pages_accept_kernel(AcceptArgs a, AcceptScratch w, PagePools pools, int page,
+                                                                    int64_t blocks) {
+  griddep_wait();  // the plan
+  if (!*w.ok) return;
+  for (int64_t x = blockIdx.x; x < (int64_t)a.n * blocks; x += gridDim.x) {
+    const int i = (int)(x / blocks);
+    const int64_t* src = w.src + (int64_t)i * a.T;
+    const int64_t* dst = w.dst + (int64_t)i * a.T;
+    int k = a.n_path[i], j = 0;
+    while (j < k && src[j] == dst[j]) ++j;  // what stays where it is
+    size_t c = (size_t)(x % blocks) * kCopyThreads + threadIdx.x;
+    for (int pool = 0; pool < pools.n; ++pool) {
+      const size_t rb = pools.page_bytes[pool] / page;
+      const int cb = column_bytes(rb);
+      const size_t cols = rb / cb;
+      if (c >= cols) {
+        c -= cols;
+        continue;
+      }
+      if (cb == 16) move_rows<uint4>(pools.base[pool], rb, c * 16, src + j, dst + j, k - j);
+      else if (cb == 4) move_rows<uint32_t>(pools.base[pool], rb, c * 4, src + j, dst + j, k - j);
+      else move_rows<uint8_t>(pools.base[pool], rb, c, src + j, dst + j, k - j);
+      break;
+    }
+  }
+}
+
+size_t carve_accept(int n, int T, char* base, AcceptScratch* out) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* r = base ? base + off : nullptr;
+    off += align_up(bytes, 256);
+    return r;
+  };
+  AcceptScratch w;
+  w.ok = (int32_t*)take(4);
+  w.src = (int64_t*)take((size_t)n * T * 8);
+  w.dst = (int64_t*)take((size_t)n * T * 8);
+  if (out) *out = w;
+  return off;
+}
+
 unsigned copy_grid() { return (unsigned)(num_sms() * 8); }
 
 // The copying grid as a programmatic dependent of the single CTA before it.
@@ -452,6 +575,34 @@ cudaError_t launch_pages_fork(const Pages& p, const int32_t* src, const int32_t*
 cudaError_t launch_pages_free(const Pages& p, const int32_t* seqs, int n, DeviceStatus* st, cudaStream_t s) {
   if (n > 0) pages_free_kernel<<<(unsigned)n, kCopyThreads, 0, s>>>(p, seqs, n, st);
   return cudaGetLastError();
+}
+
+// A call with more entries than sequences names one twice: nothing is written for it, so the scratch needs no more room.
+size_t accept_scratch_bytes(const Pages& p, int n, int T) { return carve_accept(n < p.n_seqs ? n : p.n_seqs, T, nullptr, nullptr); }
+
+cudaError_t launch_pages_accept(const Pages& p, const int32_t* seqs, const int32_t* base, const int32_t* path, const int32_t* n_path,
+                                int n, int T, const PagePools& pools, void* scratch, DeviceStatus* st, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  AcceptScratch w;
+  carve_accept(n < p.n_seqs ? n : p.n_seqs, T, (char*)scratch, &w);
+  AcceptArgs a;
+  a.seqs = seqs;
+  a.base = base;
+  a.path = path;
+  a.n_path = n_path;
+  a.n = n;
+  a.T = T;
+  pages_accept_plan_kernel<<<1, kThreads, (size_t)n * 4, s>>>(p, a, w, st);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || pools.n == 0) return e;
+  size_t cols = 0;
+  for (int i = 0; i < pools.n; ++i) {
+    const size_t rb = pools.page_bytes[i] / p.page;
+    cols += rb / column_bytes(rb);
+  }
+  const int64_t blocks = (int64_t)((cols + kCopyThreads - 1) / kCopyThreads), work = n * blocks;
+  const unsigned grid = (unsigned)(work < copy_grid() ? work : copy_grid());
+  return launch_dependent(pages_accept_kernel, grid, s, a, w, pools, p.page, blocks);
 }
 
 cudaError_t launch_pages_compact(const Pages& p, const PagePools& pools, int32_t* page_map, int32_t* n_live, void* scratch,

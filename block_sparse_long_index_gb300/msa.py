@@ -52,9 +52,27 @@ class msa_page_pool_t(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
 
 
+class msa_rope_t(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("factor", ctypes.c_float)]
+
+
+class msa_kv_pool_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class msa_append_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_idx", "k_idx")] +
+                [(n + "_stride", ctypes.c_int64) for n in ("q", "k", "v", "q_idx", "k_idx")] +
+                [(n, ctypes.c_void_p) for n in ("q_out", "q_idx_out", "k_idx_pool", "positions")] +
+                [("H_q", ctypes.c_int), ("d_I", ctypes.c_int), ("idx_f8", ctypes.c_int), ("idx_scale", ctypes.c_float)])
+
+
 _P, _I64, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SP = ctypes.POINTER(msa_shape_t)
 _KP, _GP, _LP = ctypes.POINTER(msa_kv4_pool_t), ctypes.POINTER(msa_pages_t), ctypes.POINTER(msa_page_pool_t)
+_RP, _VP, _AP = ctypes.POINTER(msa_rope_t), ctypes.POINTER(msa_kv_pool_t), ctypes.POINTER(msa_append_t)
 
 _SIGS = {
     "msa_select_blocks_workspace": (_SZ, [_I64, _I, _I, _I, _I]),
@@ -97,6 +115,17 @@ _SIGS = {
     "msa_pages_fork": (_I, [_GP, _P, _P, _I, _LP, _I, _P, _SZ, _P]),
     "msa_pages_free": (_I, [_GP, _P, _I, _P, _SZ, _P]),
     "msa_pages_compact": (_I, [_GP, _LP, _I, _P, _P, _P, _SZ, _P]),
+    "msa_pages_accept_workspace": (_SZ, [_GP, _I, _I]),
+    "msa_pages_accept": (_I, [_GP, _P, _P, _P, _P, _I, _I, _LP, _I, _P, _SZ, _P]),
+    "msa_rope": (_I, [_P, _I64, _P, _I64, _I64, _I, _I, _I, _P, _RP, _I, _P]),
+    "msa_append_workspace": (_SZ, []),
+    "msa_append_paged": (_I, [_AP, _I64, _P, _I, _P, _P, _I64, _VP, _RP, _RP, _P, _SZ, _P]),
+    "msa_append_paged_kv4": (_I, [_AP, _I64, _P, _I, _P, _P, _I64, _KP, _RP, _RP, _P, _SZ, _P]),
+    "msa_tree_decode_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "msa_tree_decode_paged": (_I, [_P, _VP, _P, _I64, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "msa_tree_decode_paged_kv4": (_I, [_P, _KP, _P, _I64, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "msa_verify_workspace": (_SZ, []),
+    "msa_verify_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I64, _P, _P, _P, _P, _SZ, _P]),
     "msa_check_device_error": (_I, [_P, _P]),
     "msa_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -412,6 +441,101 @@ def msa_pages_compact(pgs, pools, n_pools, page_map, n_live, workspace, workspac
     wb = workspace.numel() if workspace_bytes is None else workspace_bytes
     return _check(_lib.msa_pages_compact(ctypes.byref(pgs), pools, int(n_pools), _ptr(page_map), _ptr(n_live),
                                          _ptr(workspace), wb, _stream(stream)), "msa_pages_compact")
+
+
+def msa_pages_accept_workspace(pgs, n, T):
+    return int(_lib.msa_pages_accept_workspace(ctypes.byref(pgs), int(n), int(T)))
+
+
+def msa_pages_accept(pgs, seqs, base, path, n_path, n, T, pools, n_pools, workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_pages_accept(ctypes.byref(pgs), _ptr(seqs), _ptr(base), _ptr(path), _ptr(n_path), int(n),
+                                        int(T), pools, int(n_pools), _ptr(workspace), wb, _stream(stream)),
+                  "msa_pages_accept")
+
+
+def rope(turns, rot, interleaved, factor):
+    return msa_rope_t(_ptr(turns), int(rot), int(bool(interleaved)), float(factor))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def msa_rope(x, x_stride, y, y_stride, N, H, d, f32, positions, rope, inverse, stream=None):
+    return _check(_lib.msa_rope(_ptr(x), int(x_stride), _ptr(y), int(y_stride), int(N), int(H), int(d), int(bool(f32)),
+                                _ptr(positions), _ref(rope), int(bool(inverse)), _stream(stream)), "msa_rope")
+
+
+def kv_pool(k, v, n_pages, page_size, H_kv, d):
+    return msa_kv_pool_t(_ptr(k), _ptr(v), int(n_pages), int(page_size), int(H_kv), int(d))
+
+
+def append_rows(k, v, q=None, q_out=None, q_idx=None, q_idx_out=None, k_idx=None, k_idx_pool=None, positions=None, H_q=0,
+                d_I=0, idx_f8=False, idx_scale=1.0, strides=None):
+    """The rows of an append call; strides: elements from token to token by name, those of contiguous rows otherwise."""
+    r = msa_append_t(_ptr(q), _ptr(k), _ptr(v), _ptr(q_idx), _ptr(k_idx))
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_idx", q_idx), ("k_idx", k_idx)):
+        if t is not None:
+            setattr(r, name + "_stride", int(strides[name]) if strides else t.stride(0))
+    r.q_out, r.q_idx_out, r.k_idx_pool, r.positions = _ptr(q_out), _ptr(q_idx_out), _ptr(k_idx_pool), _ptr(positions)
+    r.H_q, r.d_I, r.idx_f8, r.idx_scale = int(H_q), int(d_I), int(bool(idx_f8)), float(idx_scale)
+    return r
+
+
+def msa_append_workspace():
+    return int(_lib.msa_append_workspace())
+
+
+def msa_append_paged(rows, N, cu_seqlens, S, pos0, page_table, max_pages, pool, rope, rope_idx, workspace,
+                     workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_append_paged(ctypes.byref(rows), int(N), _ptr(cu_seqlens), int(S), _ptr(pos0),
+                                        _ptr(page_table), int(max_pages), ctypes.byref(pool), _ref(rope),
+                                        _ref(rope_idx), _ptr(workspace), wb, _stream(stream)), "msa_append_paged")
+
+
+def msa_append_paged_kv4(rows, N, cu_seqlens, S, pos0, page_table, max_pages, pool, rope, rope_idx, workspace,
+                         workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_append_paged_kv4(ctypes.byref(rows), int(N), _ptr(cu_seqlens), int(S), _ptr(pos0),
+                                            _ptr(page_table), int(max_pages), ctypes.byref(pool), _ref(rope),
+                                            _ref(rope_idx), _ptr(workspace), wb, _stream(stream)),
+                  "msa_append_paged_kv4")
+
+
+def msa_tree_decode_workspace(B, T, H_q, H_kv, d):
+    return int(_lib.msa_tree_decode_workspace(int(B), int(T), int(H_q), int(H_kv), int(d)))
+
+
+def msa_tree_decode_paged(q, pool, page_table, max_pages, ctx_len, tree_len, parents, B, T, H_q, scale, out, lse,
+                          workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_tree_decode_paged(_ptr(q), ctypes.byref(pool), _ptr(page_table), int(max_pages),
+                                             _ptr(ctx_len), _ptr(tree_len), _ptr(parents), int(B), int(T), int(H_q),
+                                             float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream(stream)),
+                  "msa_tree_decode_paged")
+
+
+def msa_tree_decode_paged_kv4(q, pool, page_table, max_pages, ctx_len, tree_len, parents, B, T, H_q, scale, out, lse,
+                              workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_tree_decode_paged_kv4(_ptr(q), ctypes.byref(pool), _ptr(page_table), int(max_pages),
+                                                 _ptr(ctx_len), _ptr(tree_len), _ptr(parents), int(B), int(T),
+                                                 int(H_q), float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb,
+                                                 _stream(stream)), "msa_tree_decode_paged_kv4")
+
+
+def msa_verify_workspace():
+    return int(_lib.msa_verify_workspace())
+
+
+def msa_verify_tree(probs, draft_probs, tokens, parents, tree_len, u, u_last, B, T, V, path, n_path, next_token,
+                    workspace, workspace_bytes=None, stream=None):
+    wb = workspace.numel() if workspace_bytes is None else workspace_bytes
+    return _check(_lib.msa_verify_tree(_ptr(probs), _ptr(draft_probs), _ptr(tokens), _ptr(parents), _ptr(tree_len),
+                                       _ptr(u), _ptr(u_last), int(B), int(T), int(V), _ptr(path), _ptr(n_path),
+                                       _ptr(next_token), _ptr(workspace), wb, _stream(stream)), "msa_verify_tree")
 
 
 def msa_check_device_error(workspace, stream=None):

@@ -524,6 +524,179 @@ msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, cons
                                       float* lse, int32_t* block_idx, void* workspace, size_t workspace_bytes,
                                       msa_stream_t stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * Pages: the "MSA" study note, the model's configuration (d = 128, RoPE
+ * dimension 64).  Every other call takes rows that are turned already.
+ *
+ * A pair (a, b) of a head row's channels at position p turns by p f:
+ *   a' = factor (a cos p f - b sin p f),  b' = factor (b cos p f + a sin p f).
+ * The first `rot` channels turn, in pairs (i, i + rot / 2) or, interleaved,
+ * (2 i, 2 i + 1); the others stay.
+ *   turns [rot / 2] uint64 (device): f / (2 pi) in units of 2^-64 turns (the
+ *         integer nearest to it, modulo 2^64).  The angle modulo a turn is then
+ *         p turns modulo 2^64, with no rounding at any position: scalings for
+ *         long contexts are other tables (and, for some, a factor)
+ *   rot   a multiple of 16, 16 <= rot <= the row's length, rot <= 128 for the
+ *         calls that append
+ * cos and sin are fp32 (within 2^-24), a product of each is rounded to fp32, and
+ * so is their sum.
+ *
+ * msa_rope: rows turned (inverse 0) or turned back (inverse 1, the transpose:
+ *   the gradient of rows from that of the turned ones).
+ *   x, y      [N, H, d], bf16 (f32 = 0) or fp32 (f32 = 1), 16-byte aligned;
+ *             d in {32, 64, 128, 256}.  y is x itself or does not overlap it
+ *   x_stride, y_stride: elements from row n to row n + 1, at least H d (rows may
+ *             lie apart, as slices of a wider projection), multiples of 8 (fp32: 4)
+ *   positions [N] int32 (device), any value
+ */
+typedef struct {
+  const uint64_t* turns;
+  int rot;
+  int interleaved;
+  float factor;
+} msa_rope_t;
+msa_status_t msa_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, int64_t N, int H, int d, int f32,
+                      const int32_t* positions, const msa_rope_t* rope, int inverse, msa_stream_t stream);
+
+/* ---------------------------------------------------------------- rows into a paged cache
+ * New tokens on their way into a paged cache, turned as they go: what a step
+ * does between its projections and its attention, in one kernel.  Pages: velog
+ * llama.cpp analysis, sections 2 and 4 (K, V and index keys in caches of their
+ * own; an explicit map from positions to cells).
+ *
+ * N packed rows as for msa_kv4_store (cu_seqlens, pos0, page_table).  Of each:
+ *   k [H_kv, d] is turned, rounded to bf16 and stored; v [H_kv, d] is stored;
+ *   k_idx [d_I] (nullable) is turned and stored in k_idx_pool [n_pages,
+ *     page_size, d_I];
+ *   q [H_q, d] and q_idx [H_kv, d_I] (nullable) are turned into q_out [N, H_q, d]
+ *     and q_idx_out [N, H_kv, d_I] (contiguous; q_out may be a contiguous q).
+ * All inputs are bf16, 16-byte aligned, with a stride of elements from token to
+ * token (multiples of 8).  With idx_f8, k_idx_pool and q_idx_out hold E4M3
+ * codes: the turned rows, rounded to bf16, through msa_quantize_e4m3 with
+ * idx_scale.
+ *   positions [N] int32 (device, nullable): the positions that rows are turned
+ *     by, where they are not their tokens' places in the cache (the nodes of a
+ *     tree of drafts: ctx_len + depth)
+ *   rope (nullable: K and q stay as they are), rope_idx (nullable: the index rows
+ *     stay as they are; needs k_idx or q_idx)
+ * msa_append_paged stores K and V in bf16 pools [n_pages, page_size, H_kv, d],
+ * msa_append_paged_kv4 in a 4-bit pool, with the codes that msa_kv4_store
+ * makes of the turned bf16 rows.  Rows of no sequence are passed over, q_out
+ * and q_idx_out included; so are rows without a place (position outside the
+ * table, page id outside [0, n_pages)), which set the device error word
+ * (MSA_ERR_BAD_INDEX).  Two rows of a call must not name one place.
+ * Supported: d in {64, 128}, d_I in {32, 64, 128}, 1 <= H_kv <= 64, H_q <= 512,
+ * 1 <= N < 2^31, S <= 2^24.  workspace: msa_append_workspace() bytes.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int page_size;
+  int H_kv;
+  int d;
+} msa_kv_pool_t;
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_idx;
+  const void* k_idx;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_idx_stride;
+  int64_t k_idx_stride;
+  void* q_out;
+  void* q_idx_out;
+  void* k_idx_pool;
+  const int32_t* positions;
+  int H_q;
+  int d_I;
+  int idx_f8;
+  float idx_scale;
+} msa_append_t;
+size_t msa_append_workspace(void);
+msa_status_t msa_append_paged(const msa_append_t* rows, int64_t N, const int32_t* cu_seqlens, int S,
+                              const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                              const msa_kv_pool_t* pool, const msa_rope_t* rope, const msa_rope_t* rope_idx,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_append_paged_kv4(const msa_append_t* rows, int64_t N, const int32_t* cu_seqlens, int S,
+                                  const int32_t* pos0, const int32_t* page_table, int64_t max_pages,
+                                  const msa_kv4_pool_t* pool, const msa_rope_t* rope, const msa_rope_t* rope_idx,
+                                  void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* ---------------------------------------------------------------- drafted trees
+ * Speculative decoding on paged caches: a step proposes a tree of tokens a
+ * sequence, attends for all of them at once, keeps the branch that the target
+ * model accepts.  Pages: velog llama.cpp analysis, sections 2 and 4 (a decode
+ * step reads the whole cache for one token; caches of several sequences).
+ *
+ * A tree has up to T <= 64 nodes.  parents [B, T] int32 (device): the node above
+ * node j, below j itself, or -1 (a root).  Node j of sequence b is token
+ * ctx_len[b] + j of its cache (msa_append_paged puts it there).  tree_len [B]
+ * int32 (device, nullable: T each): nodes of each sequence's tree.
+ *
+ * msa_tree_decode_paged, msa_tree_decode_paged_kv4: dense attention of the
+ * trees' nodes over a bf16 or a 4-bit cache.  Node i sees tokens 0 .. ctx_len - 1,
+ * itself and the nodes above it.  (T = 1, parents -1, is a dense decode step; a
+ * chain, parents[j] = j - 1, a short prefill after a context.)
+ *   q          [B, T, H_q, d] bf16
+ *   page_table [B, max_pages] int32 (device); entries past a sequence's last node
+ *              are not read
+ *   ctx_len    [B] int32 (device): tokens before the tree, 0 allowed
+ *   out        [B, T, H_q, d] bf16 out;  lse [B, T, H_q] fp32 out (nullable):
+ *              natural-log log-sum-exp of the scaled scores.  Nodes past tree_len
+ *              stay as they were.
+ * Scores, softmax and sums are fp32; the probabilities of the context are
+ * rounded to bf16 for the product with V.  Scores of -inf and NaN count as in
+ * msa_dense_prefill_varlen; drafts that a node does not see count for nothing,
+ * whatever they hold.  The device error word (MSA_ERR_BAD_INDEX) is set by a
+ * page id outside [0, n_pages) (page 0 is read), a parent outside [-1, j) (it
+ * counts as -1), and lengths below 0, tree_len above T or ctx_len + tree_len
+ * above max_pages * page_size (nothing is written for that sequence).
+ * Supported: H_q / H_kv in {1, 2, 4, 8}, d in {64, 128}, H_kv <= 64, B <= 2^20,
+ * B T < 2^31, bf16 pools of fewer than 2^31 tokens.
+ *
+ * msa_verify_tree: which branch is accepted, and the token after it, from given
+ * random numbers.  Node 0 is the token that the step began with (its parent is
+ * not looked at); the drafts are tokens[j], j > 0.  The walk begins at node 0.
+ * The children x of its node n are tested in their order with
+ *   r = max(0, p - c q),  p = probs[n], q = draft_probs[n], c = 0, W = 1 at first:
+ *   accepted where u[j] q(x) W < r(x), and the walk goes on from it;
+ *   otherwise c grows by W and W becomes the sum of r.
+ * (So a child drawn from q is accepted with probability min(1, p / q), and a
+ * rejection leaves max(0, p - q), normalised, for the next one.)  Without
+ * draft_probs the drafts were certain: accepted where u[j] W < r(x) with r = p,
+ * otherwise r(x) becomes 0 and W falls by it.  Where no child is accepted, the
+ * next token is the lowest one whose cumulative sum of r exceeds u_last[b] times
+ * the sum of r (of p, where nothing is left of r).
+ *   probs, draft_probs (nullable) [B, T, V] fp32, 16-byte aligned, each row a
+ *              distribution; a value that is not a positive finite number counts as 0
+ *   tokens [B, T] int32 (tokens[b][0] is not looked at);  u [B, T], u_last [B] fp32
+ *              in [0, 1) (u_last: below it counts as 0, above as the largest number below 1)
+ *   path   [B, T] int32 out: the accepted nodes in order, node 0 first, then -1
+ *   n_path [B] int32 out: their number (0 where tree_len is 0)
+ *   next   [B] int32 out: the next token (-1 where tree_len is 0 or p holds nothing)
+ * Sums are held to 2^-48.  A parent outside [-1, j) or a child's token outside
+ * [0, V) takes the node out, a tree_len outside [0, T] counts as 0; both set the
+ * device error word.  Supported: 1 <= V < 2^31, B <= 2^20.  workspace: msa_verify_workspace() bytes.
+ */
+size_t msa_tree_decode_workspace(int B, int T, int H_q, int H_kv, int d);
+msa_status_t msa_tree_decode_paged(const void* q, const msa_kv_pool_t* pool, const int32_t* page_table,
+                                   int64_t max_pages, const int32_t* ctx_len, const int32_t* tree_len,
+                                   const int32_t* parents, int B, int T, int H_q, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_tree_decode_paged_kv4(const void* q, const msa_kv4_pool_t* pool, const int32_t* page_table,
+                                       int64_t max_pages, const int32_t* ctx_len, const int32_t* tree_len,
+                                       const int32_t* parents, int B, int T, int H_q, float scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes, msa_stream_t stream);
+size_t msa_verify_workspace(void);
+msa_status_t msa_verify_tree(const float* probs, const float* draft_probs, const int32_t* tokens,
+                             const int32_t* parents, const int32_t* tree_len, const float* u, const float* u_last,
+                             int B, int T, int64_t V, int32_t* path, int32_t* n_path, int32_t* next, void* workspace,
+                             size_t workspace_bytes, msa_stream_t stream);
+
 /* ---------------------------------------------------------------- pages of a cache
  * Page tables with reference counts, for any paged cache of this library (the
  * bf16 pools of msa_decode_paged, the 4-bit pools, the index-key pools).
@@ -560,6 +733,17 @@ msa_status_t msa_decode_paged_kv4_fp8(const void* q_t, const void* q_idx_t, cons
  *     page_map [n_pages] int32 out (nullable): each page's new id, -1 if free
  *     n_live   [1] int32 out (nullable): L
  *
+ * msa_pages_accept: of the tokens of sequence seqs[i] from base[i] on, those at
+ *   base[i] + path[i][j], j < n_path[i], stay, as tokens base[i] + j, in every
+ *   pool; the sequence then has base[i] + n_path[i] tokens, and the pages past
+ *   them are free (their table entries -1).  path [n, T] int32 rises within an
+ *   entry and stays below ctx_len - base (what msa_verify_tree returns, for
+ *   drafts from base on); n_path 0 cuts the sequence off at base.  Every page
+ *   from base on has to be the sequence's own (count 1).  An entry that breaks a
+ *   rule, or names a sequence twice, sets the error word and the call changes
+ *   nothing.  1 <= T <= 64; the pools' page_bytes are multiples of page_size.
+ *   workspace: msa_pages_accept_workspace(pages, n, T) bytes.
+ *
  * seqs, new_len, src, dst are int32 device arrays of n entries, n <= 4096 (0 is
  * allowed).  pools: n_pools <= 8 host entries, each a device array of n_pages
  * pages of page_bytes (a multiple of 16) at a 16-byte aligned address; pass every
@@ -590,6 +774,10 @@ msa_status_t msa_pages_fork(const msa_pages_t* pages, const int32_t* src, const 
                             msa_stream_t stream);
 msa_status_t msa_pages_free(const msa_pages_t* pages, const int32_t* seqs, int n, void* workspace,
                             size_t workspace_bytes, msa_stream_t stream);
+size_t msa_pages_accept_workspace(const msa_pages_t* pages, int n, int T);
+msa_status_t msa_pages_accept(const msa_pages_t* pages, const int32_t* seqs, const int32_t* base, const int32_t* path,
+                              const int32_t* n_path, int n, int T, const msa_page_pool_t* pools, int n_pools,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream);
 msa_status_t msa_pages_compact(const msa_pages_t* pages, const msa_page_pool_t* pools, int n_pools, int32_t* page_map,
                                int32_t* n_live, void* workspace, size_t workspace_bytes, msa_stream_t stream);
 
