@@ -817,7 +817,9 @@ static msa_status_t check_tree(int B, int T, int H_q, int H_kv, int d) {
 
 size_t msa_tree_decode_workspace(int B, int T, int H_q, int H_kv, int d) {
   if (check_tree(B, T, H_q, H_kv, d) != MSA_OK) return kHeader;
-  return kHeader + msa::tree_scratch_bytes(msa::tree_plan(B, T, H_q, H_kv, d));
+  const size_t a = msa::tree_scratch_bytes(msa::tree_plan(B, T, H_q, H_kv, d, false));
+  const size_t b = msa::tree_scratch_bytes(msa::tree_plan(B, T, H_q, H_kv, d, true));
+  return kHeader + (a > b ? a : b);
 }
 
 static msa_status_t tree_impl(const void* q, const void* k_pool, const void* v_pool, const msa::Kv4Pool* kv4, int H_kv, int d,
@@ -827,12 +829,14 @@ static msa_status_t tree_impl(const void* q, const void* k_pool, const void* v_p
   if (!q || !ctx_len || !parents || !out) return MSA_ERR_INVALID_ARGUMENT;
   msa_status_t st = check_tree(B, T, H_q, H_kv, d);
   if (st != MSA_OK) return st;
-  if (!kv4 && n_pages * (int64_t)page >= (int64_t)1 << 31) return MSA_ERR_UNSUPPORTED;  // TMA coordinates are int32
+  // TMA coordinates are int32: tokens of a bf16 pool, runs of 16 or more tokens of a 4-bit one
+  if (n_pages * (int64_t)page >= (int64_t)1 << (kv4 ? 35 : 31)) return MSA_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || scale != scale) return MSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(out) || misaligned4(ctx_len) || misaligned4(tree_len) || misaligned4(parents) || misaligned4(lse))
     return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
-  const msa::TreePlan p = msa::tree_plan(B, T, H_q, H_kv, d);
+  const msa::TreePlan p = msa::tree_plan(B, T, H_q, H_kv, d, kv4 != nullptr);
+  if ((max_pages * page + 127) / 128 > ((int64_t)1 << 31) / B) return MSA_ERR_UNSUPPORTED;  // a CTA's tiles are counted in an int
   st = begin(workspace, workspace_bytes, kHeader + msa::tree_scratch_bytes(p), s, 0);  // the first kernel clears the status
   if (st != MSA_OK) return st;
   msa::CacheMap map;

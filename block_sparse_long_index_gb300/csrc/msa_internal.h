@@ -235,9 +235,10 @@ cudaError_t launch_append(const AppendRows& rows, int64_t N, const int32_t* cu, 
 // ---- attention of drafted trees over a paged cache (msa_tree.cu)
 struct TreePlan {
   int B, T, H_q, H_kv, d;
-  int RG, RU;  // row groups of a (sequence, K/V head), rows (node, head) of one
+  int RG, RU;          // row groups of a (sequence, K/V head), rows (node, head) of one
+  int groups, rounds;  // runs of the tile list, items of a CTA
 };
-TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d);
+TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d, bool kv4);
 size_t tree_scratch_bytes(const TreePlan& p);
 // kv4 null: bf16 pools
 cudaError_t launch_tree(const void* q, const TreePlan& p, const void* k_pool, const void* v_pool, const Kv4Pool* kv4,

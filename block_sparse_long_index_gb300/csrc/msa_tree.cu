@@ -8,12 +8,16 @@
 // handful of keys that differ from row to row; the kernel that joins the partials adds it key by key in fp32, and keys
 // that a node does not see are never touched, whatever they hold.
 //
-// The context: the cache is one flat list of 128-token tiles, ordered by (sequence, K/V head, row group, tile); every CTA
-// takes an equal run of it, whatever the lengths are.  tree_context_kernel does a tile by tcgen05, S = Q K^T and O += P V
+// The context: all sequences' 128-token tiles are one list, whatever the lengths are; a CTA has one unit (K/V head, and
+// group of rows where they are many) and an equal run of the list.  The CTAs of all units take the same runs at the same
+// time: the heads of a token lie side by side in memory, and 64 bytes here and there (a 4-bit head row) would keep HBM to
+// a fifth of its rate.  tree_context_kernel does a tile by tcgen05, S = Q K^T and O += P V
 // with 128 query rows, Q and K, V in shared memory, S / P and O in TMEM.  Two streams of it alternate, so that one's
 // softmax runs under the other's products:
-//   up to 128 rows: one query tile, whose even and odd key tiles are the streams (their O are merged at the run's end);
-//   more: two query tiles over the same keys.
+//   up to 128 rows, and over a 4-bit cache always: one query tile, whose even and odd key tiles are the streams (their O
+//   are merged at the run's end);
+//   more rows over bf16 pages: two query tiles over the same keys.  (4-bit pages are expanded again for each 128 rows: a
+//   tile's softmax takes as long, and the room of the second query tile holds the codes in flight.)
 // Rows of a tile past the last one are computed on by the tensor cores alone; warps without a row rest.
 #include <math.h>
 
@@ -29,12 +33,12 @@ using namespace kv4;
 
 constexpr int kRowsT = 128, kKeysT = 128;
 constexpr int kMaxT = 64;  // nodes of a tree: a 64-bit mask
-constexpr int kCtxThreads = 768;
-constexpr int kWarpMma = 16, kWarpLoad = 18, kWarpGuard = 19;  // 4-bit pages: warps 19 .. 23 expand codes
-constexpr int kExpand = 5;                                     // warps that expand codes
-constexpr int kUnitRows = 16;                                  // tokens that one of them takes at a time
-constexpr int kUnits = kKeysT / kUnitRows;
+constexpr int kWarpMma = 16, kWarpLoad = 18, kWarpGuard = 19, kWarpExpand = 20;
+constexpr int kUnitRows = 16;                   // tokens of a tile that an expanding warp takes
+constexpr int kUnits = kKeysT / kUnitRows;      // warps that expand 4-bit codes
+__host__ __device__ constexpr int ctx_threads(bool kv4) { return 32 * (kv4 ? kWarpExpand + kUnits : kWarpExpand); }
 constexpr int kJoinThreads = 256;
+constexpr int kMaxRounds = 4;
 constexpr float kLazy = 8.0f;  // log2 units a row maximum may grow before O is rescaled
 
 struct TreeShape {
@@ -43,6 +47,7 @@ struct TreeShape {
   int64_t cap;
   int B, T, gs, H_kv;
   int RG, RU;  // row groups of a (sequence, K/V head), rows of one
+  int groups, rounds;  // see tree_plan
   // Nodes and context of sequence b; bad lengths count as none of either.
   __device__ __forceinline__ bool lengths(int b, int& n, int& t) const {
     n = ctx[b];
@@ -60,33 +65,39 @@ struct TreeShape {
   }
 };
 
-// A CTA's run [f, f1) of the flat list, segment by segment: tiles [t0, t1) of one unit (sequence, head, row group).
+// What a CTA begins a round with: its unit and its group's run of the tile list.
+struct Round {
+  int seq, off, left;  // tile `off` of sequence `seq`, so many tiles
+  int unit, group;
+};
+// The tiles of a CTA, round by round and segment by segment: tiles [t0, t1) of one sequence for the round's unit.
 struct Run {
-  int64_t f, f1, before;  // `before`: tiles before sequence `seq`
-  int seq;
-  int len, unit, t0, t1;  // of the segment: context length, unit within the sequence
-  __device__ __forceinline__ bool next(const TreeShape& sh) {
-    if (f >= f1) return false;
-    const int units = sh.H_kv * sh.RG;
-    for (;;) {  // (ends: f1 is no more than the sum over all sequences)
-      const int n = sh.tiles(seq);
-      if (f < before + (int64_t)n * units) {
-        unit = (int)((f - before) / n);
-        const int64_t r0 = before + (int64_t)unit * n;
-        t0 = (int)(f - r0);
-        t1 = (int)min(f1 - r0, (int64_t)n);
-        int t;
-        sh.lengths(seq, len, t);
-        f += t1 - t0;
-        return true;
-      }
-      before += (int64_t)n * units;
+  int round, rounds;
+  int left, off;  // tiles not given out yet; the next one's index in sequence `seq`
+  int seq, unit, group;
+  int len, t0, t1;  // of the segment: context length, tiles
+  __device__ __forceinline__ bool next(const TreeShape& sh, const Round* start) {
+    while (left <= 0) {
+      if (++round >= rounds) return false;
+      const Round r = start[round];
+      seq = r.seq, off = r.off, left = r.left, unit = r.unit, group = r.group;
+    }
+    int n;
+    while (off >= (n = sh.tiles(seq))) {  // (ends: the runs add up to the sum over all sequences)
+      off = 0;
       ++seq;
     }
+    t0 = off;
+    t1 = min(t0 + left, n);
+    int t;
+    sh.lengths(seq, len, t);
+    left -= t1 - t0;
+    off = t1;
+    return true;
   }
 };
 
-__device__ __forceinline__ int64_t run_quota(int64_t total, int n_cta) { return total ? (total + n_cta - 1) / n_cta : 1; }
+__device__ __forceinline__ int64_t run_quota(int64_t total, int groups) { return total ? (total + groups - 1) / groups : 1; }
 
 template <int D>
 struct Layout {
@@ -94,19 +105,16 @@ struct Layout {
   static constexpr int CHUNK = 128 * 128;          // bytes of a chunk of 128 rows
   static constexpr int TILE = NC * CHUNK;
   static constexpr int STAGES = D == 128 ? 4 : 8;  // K and V tiles in flight
-  static constexpr int RAW = kUnitRows * D + 2 * kUnitRows * kGroups;  // a unit's codes and scales of K and V
   static constexpr uint32_t TMEM_O = 256;          // S / P of stream q at 128 q, O of stream q at 256 + 128 q
   // places in shared memory, with one or two query tiles
   __host__ __device__ static constexpr int kv_at(bool two) { return (two ? 2 : 1) * TILE; }
   __host__ __device__ static constexpr int misc_at(bool two) { return kv_at(two) + STAGES * TILE; }
   static constexpr int SUMS = 0, MAXIMA = 2 * 128 * 16, BARS = MAXIMA + 2 * 128 * 16, MISC = BARS + 512;
-  // units that an expanding warp has in flight: what fits, 8 at most
-  __host__ __device__ static constexpr int depth(bool two) {
-    const int n = (227 * 1024 - 1024 - 1024 - misc_at(two) - MISC) / (kExpand * RAW);
-    return n > 8 ? 8 : n;
-  }
+  // 4-bit pages: a tile's codes of K and of V, then their scales; and the tiles of them in flight
+  static constexpr int CODES = kKeysT * D / 2, SCALES = kKeysT * kGroups, RAW = 2 * (CODES + SCALES), DEPTH = D == 128 ? 3 : 4;
+  __host__ __device__ static constexpr int raw_at(bool two) { return (misc_at(two) + MISC + 1023) / 1024 * 1024; }
   __host__ __device__ static constexpr int smem(bool two, bool kv4) {
-    return 1024 + misc_at(two) + MISC + (kv4 ? kExpand * depth(two) * RAW : 0);
+    return 1024 + (kv4 ? raw_at(two) + DEPTH * RAW : misc_at(two) + MISC);
   }
 };
 
@@ -116,6 +124,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
       "[%5];\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -137,19 +153,20 @@ __device__ __forceinline__ uint4 lds_16(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at));
   return y;
 }
-__device__ __forceinline__ uint32_t lds_4(uint32_t at) {
-  uint32_t y;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(y) : "r"(at));
-  return y;
-}
 __device__ __forceinline__ void sts_16(uint32_t at, uint4 y) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint32_t lds_2(uint32_t at) {
+  uint16_t y;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(y) : "r"(at));
+  return y;
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` once this thread's cp.async so far have landed (one of the arrivals that the barrier expects).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // Products and their completion by the one lane with `lead` set, predicated.
 __device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -170,6 +187,11 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
       : "memory");
 }
+// Registers a thread, for all four warps of a warpgroup.
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 // The value that every lane of the warp has, in a uniform register.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 __device__ __forceinline__ bool elect_one() {
@@ -178,20 +200,41 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Half a row's codes as bf16 times 2^-18, word w at `to` ^ 16 w; zeros where it is not context.
+template <int HW>
+__device__ __forceinline__ void expand_half(const uint4 (&c)[HW], uint32_t scales, bool on, uint32_t to) {
+  if (!on) {
+#pragma unroll
+    for (int w = 0; w < 4 * HW; ++w) sts_16(to ^ (w << 4), make_uint4(0u, 0u, 0u, 0u));
+    return;
+  }
+  SubScale sc[2];  // its two groups
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t b = scales >> (8 * x) & 0xFFu;
+    sc[x] = sub_scale(b == kScaleNaN ? 0x7FFF7FFFu : b * 0x00100010u + kSubScaleBias * 0x00010001u);
+  }
+#pragma unroll
+  for (int y = 0; y < HW; ++y) {
+    const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) sts_16(to ^ ((4 * y + x) << 4), expand8_sub(cw[x], sc[(4 * y + x) / (2 * HW)]));
+  }
+}
+
 // Scratch of a call: what the context kernel leaves for the joining one.
 struct TreeScratch {
-  int64_t* starts;      // [B + 1] tiles (times units) before each sequence
-  unsigned int* errors; // [CTAs] flags each met
-  float* part_o;        // [slots][RU][D]; slot = unit + CTA, which no two segments of the flat list share
-  float2* part_ml;      // [slots][RU] maximum (log2 units) and sum
+  int64_t* starts;       // [B + 1] tiles before each sequence
+  unsigned int* errors;  // [CTAs] flags each met
+  float* part_o;         // [slots][RU][D]; slot = (sequence + group) units + unit, which no two segments share
+  float2* part_ml;       // [slots][RU] maximum (log2 units) and sum
 };
 
-// `own`: places in the flat list of the CTA's run.  Every thread takes part.  CTA 0 writes starts.
-__device__ __forceinline__ void find_run(const TreeShape& sh, int n_cta, int64_t* starts, int64_t* warp_sums, int64_t* found,
-                                         Run& run) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = kCtxThreads / 32;
-  const int per = (sh.B + kCtxThreads - 1) / kCtxThreads, b0 = min(tid * per, sh.B), b1 = min(b0 + per, sh.B);
-  const int64_t units = (int64_t)sh.H_kv * sh.RG;
+// The CTA's rounds.  Every thread takes part.  CTA 0 writes starts.
+template <int THREADS>
+__device__ __forceinline__ void find_rounds(const TreeShape& sh, int64_t* starts, int64_t* warp_sums, Round* start) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = THREADS / 32;
+  const int per = (sh.B + THREADS - 1) / THREADS, b0 = min(tid * per, sh.B), b1 = min(b0 + per, sh.B);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += sh.tiles(b);
   int64_t incl = mine;
@@ -201,7 +244,6 @@ __device__ __forceinline__ void find_run(const TreeShape& sh, int n_cta, int64_t
     if (lane >= o) incl += u;
   }
   if (lane == 31) warp_sums[warp] = incl;
-  if (tid == 0) found[1] = sh.B;
   __syncthreads();
   int64_t total = 0, off = 0;
   for (int w = 0; w < nw; ++w) {
@@ -209,28 +251,46 @@ __device__ __forceinline__ void find_run(const TreeShape& sh, int n_cta, int64_t
     if (w < warp) off += x;
     total += x;
   }
-  total *= units;
-  const int64_t quota = run_quota(total, n_cta), at = blockIdx.x * quota;
-  int64_t x = (off + incl - mine) * units;
-  for (int b = b0; b < b1; ++b) {
-    const int64_t n = sh.tiles(b) * units;
-    if (x <= at && at < x + n) {
-      found[0] = x;
-      found[1] = b;
-    }
-    if (blockIdx.x == 0) starts[b] = x;
-    x += n;
+  const int64_t quota = run_quota(total, sh.groups);
+  const int units = sh.H_kv * sh.RG;
+  if (tid < sh.rounds) {
+    const int item = blockIdx.x + tid * gridDim.x;
+    Round r;
+    r.group = item / units;
+    r.unit = item % units;
+    r.seq = r.off = 0;
+    r.left = r.group < sh.groups ? (int)max(min(total - r.group * quota, quota), (int64_t)0) : 0;
+    start[tid] = r;
   }
-  if (blockIdx.x == 0 && tid == 0) starts[sh.B] = total;
   __syncthreads();
-  run.before = found[0];
-  run.seq = (int)found[1];
-  run.f = at;
-  run.f1 = min(total, at + quota);
+  const int64_t first = off + incl - mine;
+  for (int i = 0; i < sh.rounds; ++i) {
+    const int64_t at = (blockIdx.x + i * gridDim.x) / units * quota;
+    if (start[i].left <= 0 || at < first || at >= first + mine) continue;
+    int64_t x = first;
+    for (int b = b0; b < b1; ++b) {
+      const int n = sh.tiles(b);
+      if (at < x + n) {
+        start[i].seq = b;
+        start[i].off = (int)(at - x);
+        break;
+      }
+      x += n;
+    }
+  }
+  if (blockIdx.x == 0) {
+    int64_t x = first;
+    for (int b = b0; b < b1; ++b) {
+      starts[b] = x;
+      x += sh.tiles(b);
+    }
+    if (tid == 0) starts[sh.B] = total;
+  }
+  __syncthreads();
 }
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
+__global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     TreeShape sh, CacheMap map, Kv4Pool pool, int box_rows, float scale_log2, TreeScratch w, DeviceStatus* status) {
   using L = Layout<D>;
@@ -241,10 +301,12 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ unsigned int est[2];
-  __shared__ int64_t warp_sums[kCtxThreads / 32], found[2];
+  __shared__ int64_t warp_sums[ctx_threads(KV4) / 32];
+  __shared__ Round start[kMaxRounds];
+  __shared__ Run runs_s[kWarpMma];
   DeviceStatus* st = reinterpret_cast<DeviceStatus*>(est);  // the CTA's own (an error touches its first two words)
   const int R = sh.T * sh.gs;
-  const bool two = R > kRowsT;  // two query tiles a unit
+  const bool two = !KV4 && R > kRowsT;  // two query tiles a unit
   const uint32_t sm_kv = sb + L::kv_at(two), sm_misc = sb + L::misc_at(two), bar = sm_misc + L::BARS;
   auto kv_full = [&](int i) { return bar + 8u * i; };
   auto kv_empty = [&](int i) { return bar + 8u * (L::STAGES + i); };  // both MMA warps
@@ -259,11 +321,14 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
   // TMA -> guard, for V tiles (odd stages) that end inside the tile: the guard then fills kv_full.  A barrier of their
   // own, so that the guard, who passes over all other tiles, sees every phase of it.
   auto v_part = [&](int i) { return bar + 8u * (B0 + 14 + i / 2); };
-  static_assert(8 * (B0 + 14 + L::STAGES / 2) <= 512, "barriers fit");
+  constexpr int B1 = B0 + 14 + L::STAGES / 2;
+  auto raw_full = [&](int i) { return bar + 8u * (B1 + i); };               // 4-bit codes: TMA and cp.async -> expanding warps
+  auto raw_empty = [&](int i) { return bar + 8u * (B1 + L::DEPTH + i); };   // expanding warps -> loads
+  static_assert(8 * (B1 + 2 * L::DEPTH) <= 512, "barriers fit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
   // quarters (32 rows) that some tile of a stream uses
-  const int most[2] = {min(two ? kRowsT : R, kRowsT), two ? min(sh.RG > 1 ? kRowsT : R - kRowsT, kRowsT) : R};
+  const int most[2] = {min(R, kRowsT), two ? min(sh.RG > 1 ? kRowsT : R - kRowsT, kRowsT) : min(R, kRowsT)};
   const int live_q[2] = {(most[0] + 31) / 32, (most[1] + 31) / 32};
   if (tid == 0) {
     for (int i = 0; i < L::STAGES; ++i) {
@@ -271,8 +336,13 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
       mbar_init(kv_empty(i), 2);
     }
     for (int i = 1; i < L::STAGES; i += 2) mbar_init(v_part(i), 1);
+    for (int i = 0; i < L::DEPTH; ++i) {
+      mbar_init(raw_full(i), 33);  // TMA's bytes, every lane's scales
+      mbar_init(raw_empty(i), kUnits);
+    }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
+#pragma unroll
     for (int q = 0; q < 2; ++q) {
       mbar_init(s_full(q), 1);
       mbar_init(p_full(q), 4 * live_q[q]);
@@ -295,27 +365,30 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
   }
   if (warp == kWarpLoad && lane == 0) {
     prefetch_tmap(&tm_q);
-    if (!KV4) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
+  find_rounds<ctx_threads(KV4)>(sh, w.starts, warp_sums, start);
   Run run;
-  find_run(sh, gridDim.x, w.starts, warp_sums, found, run);
+  run.round = -1;
+  run.rounds = sh.rounds;
+  run.left = 0;
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int* abort = &abort_flag;
   // rows of query tile q of a unit, and whether stream q takes tile j of the segment
-  auto rows_of = [&](int unit, int q) { return min(kRowsT, max(0, R - (unit % sh.RG) * (2 * kRowsT) - (two ? q * kRowsT : 0))); };
+  auto rows_of = [&](int unit, int q) { return min(kRowsT, max(0, R - (unit % sh.RG) * (KV4 ? kRowsT : 2 * kRowsT) - (two ? q * kRowsT : 0))); };
 
+  // 896 threads start with 72 registers each, 64512 in all; 512 x 80 + 384 x 56 = 62464
+  if (KV4 && warp >= kWarpMma) regs_dec<56>();
   if (warp >= kWarpLoad) {
     if (warp == kWarpLoad) {
-      // ------------------------------------------------------------ loads: Q, and bf16 K and V
+      // ------------------------------------------------------------ loads: Q, then K and V
       uint32_t kv = 0, qn = 0;
       uint32_t last_part = 0, parts = 0;  // by stage: whether its last tile went by v_part, and the parity of the next such
       bool ok = true;
       const int per_tile = kRowsT / sh.gs;  // positions of a query tile
-      while (ok && run.next(sh)) {
+      while (ok && run.next(sh, start)) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (qn & 1) ^ 1, abort, st, 0xF01)))) break;
         const int g = run.unit / sh.RG, rg = run.unit % sh.RG;
         if (lane == 0) {
@@ -323,12 +396,48 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
           for (int q = 0; q < (two ? 2 : 1); ++q)
 #pragma unroll
             for (int c = 0; c < L::NC; ++c)
-              tma_load_3d(sb + q * L::TILE + c * L::CHUNK, &tm_q, c * 64, g * sh.gs, run.seq * sh.T + (2 * rg + q) * per_tile,
+              tma_load_3d(sb + q * L::TILE + c * L::CHUNK, &tm_q, c * 64, g * sh.gs, run.seq * sh.T + ((KV4 ? 1 : 2) * rg + q) * per_tile,
                           q_full);
         }
         ++qn;
         __syncwarp();
-        if (KV4) continue;
+        if constexpr (KV4) {
+          // codes by TMA, a lane a box of the tile; scales, 4 bytes a token, by cp.async, 4 tokens a lane
+          const int64_t row0 = (int64_t)run.seq * map.max_pages;
+          for (int j = run.t0; ok && j < run.t1; ++j, ++kv) {
+            const int rows = min(kKeysT, run.len - j * kKeysT), boxes = (rows + box_rows - 1) / box_rows;
+            int32_t row = 0;
+            if (lane < boxes) {
+              const int t = j * kKeysT + lane * box_rows, lp = t / map.page;
+              int32_t pp = __ldg(map.table + row0 + lp);
+              if (pp < 0 || (int64_t)pp >= map.n_pages) {
+                raise_error(st, kErrBadIndex, 3u);
+                pp = 0;
+              }
+              row = pp * (map.page / box_rows) + (t - lp * map.page) / box_rows;  // in boxes
+            }
+            const int s = (int)(kv % L::DEPTH);
+            const uint32_t to = sb + L::raw_at(two) + s * L::RAW, at = raw_full(s);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(raw_empty(s), ((kv / L::DEPTH) & 1) ^ 1, abort, st, 0xF02)))) break;
+            if (lane == 0) mbar_arrive_expect_tx(at, (uint32_t)(2 * boxes * box_rows * (D / 2)));
+            __syncwarp();
+            if (lane < boxes) {
+              tma_load_4d(to + lane * box_rows * (D / 2), &tm_k, 0, 0, g, row, at);
+              tma_load_4d(to + L::CODES + lane * box_rows * (D / 2), &tm_v, 0, 0, g, row, at);
+            }
+#pragma unroll
+            for (int i = 0; i < kKeysT / 32; ++i) {
+              const int tt = 32 * i + lane;
+              const int64_t token = (int64_t)__shfl_sync(0xffffffffu, row, tt / box_rows) * box_rows + (tt & (box_rows - 1));
+              if (tt < rows) {
+                cp_async4(to + 2 * L::CODES + tt * kGroups, pool.k_scales + (token * pool.H_kv + g) * kGroups);
+                cp_async4(to + 2 * L::CODES + L::SCALES + tt * kGroups, pool.v_scales + (token * pool.H_kv + g) * kGroups);
+              }
+            }
+            cp_async_arrive(at);
+          }
+          continue;
+        }
         const int piece = lane / L::NC, chunk = lane % L::NC;  // a lane's box of a tile
         for (int j = run.t0; ok && j < run.t1; ++j) {
           const int rows = min(kKeysT, run.len - j * kKeysT), boxes = (rows + box_rows - 1) / box_rows;
@@ -360,7 +469,10 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
         }
       }
       if (*abort && lane == 0) {  // let the copies in flight land before the CTA ends
-        if (!KV4)
+        if (KV4)
+          for (uint32_t x = kv > (uint32_t)L::DEPTH ? kv - L::DEPTH : 0; x < kv; ++x)
+            mbar_wait(raw_full((int)(x % L::DEPTH)), (x / L::DEPTH) & 1, nullptr, st, 0xFF1);
+        else
           for (uint32_t x = kv > (uint32_t)L::STAGES ? kv - L::STAGES : 0; x < kv; ++x) {
             const int s = (int)(x % L::STAGES);
             const bool part = last_part >> s & 1u;
@@ -368,121 +480,55 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
           }
         if (qn) mbar_wait(q_full, (qn - 1) & 1, nullptr, st, 0xFF2);
       }
-    } else if (KV4) {
+    } else if (KV4 && warp >= kWarpExpand) {
       // ------------------------------------------------------------ 4-bit codes into bf16 tiles
-      // A warp takes every kExpand-th unit of 16 tokens: their codes and scales of K and V come by cp.async into its own
-      // ring, `depth` units ahead, and leave as 16-byte pieces of the swizzled tiles; tokens past the context as zeros.
-      constexpr int CB = D / 2;  // bytes of a head row's codes
-      const int wx = warp - kWarpGuard, depth = L::depth(two);
-      const uint32_t ring = sm_misc + L::MISC + wx * depth * L::RAW;
-      const int row_bytes = pool.H_kv * CB;
-      Run ahead = run;
-      bool more = ahead.next(sh), have = run.next(sh);
-      int au = wx, cu = wx;  // units into the segments
-      // the next unit to fetch: false past the last one
-      auto settle = [&](Run& r, int& u, bool& on) {
-        while (on && u >= (r.t1 - r.t0) * kUnits) {
-          u -= (r.t1 - r.t0) * kUnits;
-          on = r.next(sh);
-        }
-      };
-      settle(ahead, au, more);
-      settle(run, cu, have);
-      auto page_of = [&]() {  // page id of the unit that `ahead` stands at (read a unit before it is used)
-        const int t = ahead.t0 * kKeysT + au * kUnitRows;
-        return more && t < ahead.len ? __ldg(map.table + (int64_t)ahead.seq * map.max_pages + t / map.page) : 0;
-      };
-      int32_t pp = page_of();
-      auto fetch = [&](uint32_t slot) {
-        const int t = ahead.t0 * kKeysT + au * kUnitRows;
-        if (more && t < ahead.len) {
-          if (pp < 0 || (int64_t)pp >= map.n_pages) {
-            raise_error(st, kErrBadIndex, 3u);
-            pp = 0;
-          }
-          const int g = ahead.unit / sh.RG;
-          const int64_t row = (int64_t)pp * map.page + t % map.page;
-          const uint32_t to = ring + slot * L::RAW;
-          constexpr int PR = CB / 16;  // 16-byte pieces of a row's codes
-#pragma unroll
-          for (int i = lane; i < kUnitRows * PR; i += 32) {
-            const int r = i / PR, p = i % PR;
-            // piece p of row r at p ^ (r / 2 % 4) (64-byte rows; 32-byte rows: p ^ (r / 4 % 2)): conflict-free reads
-            const int at = r * CB + ((p ^ (PR == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4);
-            const int64_t src = (row + r) * row_bytes + g * CB + p * 16;
-            cp_async16(to + at, pool.k_codes + src);
-            cp_async16(to + kUnitRows * CB + at, pool.v_codes + src);
-          }
-          const int r = lane & 15;
-          cp_async4(to + 2 * kUnitRows * CB + lane * 4,
-                    (lane < 16 ? pool.k_scales : pool.v_scales) + ((row + r) * pool.H_kv + g) * kGroups);
-        }
-        cp_async_commit();
-        au += kExpand;
-        settle(ahead, au, more);
-        pp = page_of();
-      };
-      for (int i = 0; i < depth - 1; ++i) fetch(i);
-      uint32_t slot = 0, kv0 = 0;  // ring slot; stage index of the segment's first K tile
+      // A warp has the same 16 tokens of every tile, a lane half a row of K and of V: codes leave as 16-byte pieces of
+      // the swizzled tiles (times 2^-18, see expand8_sub); tokens past the context as zeros.
+      constexpr int CB = D / 2, HW = D / 64;  // bytes of a row's codes, 16-byte pieces of half of them
+      const int r = (warp - kWarpExpand) * kUnitRows + (lane & 15), half = lane >> 4;
+      // piece p of a row is at p ^ (row / 2 % 4) of it (32-byte rows: p ^ (row / 4 % 2)), by TMA's swizzle
+      const uint32_t codes_at = sb + L::raw_at(two) + r * CB + (((half * HW) ^ (CB == 64 ? (r >> 1) & 2 : (r >> 2) & 1)) << 4);
+      const uint32_t odd = CB == 64 ? (r >> 1) & 1 : 0;  // which of the half row's two pieces comes first
+      const uint32_t scales_at = sb + L::raw_at(two) + 2 * L::CODES + r * kGroups + 2 * half;
+      // word w of the half row goes to piece w of its 64-channel chunk (d = 128), or 4 half + w (d = 64)
+      const uint32_t lane_to = sm_kv + (D == 128 ? half * L::CHUNK : 0) + r * 128 + (((D == 128 ? 0 : 4 * half) ^ (r & 7)) << 4);
+      int slot = 0;
+      uint32_t raw_ph = 0, ks = 0, kph = 1;  // parities of the ring's next use, of the last use of the next K tile's stage
       bool ok = true;
-      while (ok && have) {
-        fetch((slot + depth - 1) % depth);
-        switch (depth) {
-          case 8: cp_async_wait<7>(); break;
-          case 7: cp_async_wait<6>(); break;
-          case 6: cp_async_wait<5>(); break;
-          case 5: cp_async_wait<4>(); break;
-          case 4: cp_async_wait<3>(); break;
-          case 3: cp_async_wait<2>(); break;
-          default: cp_async_wait<1>(); break;
-        }
-        __syncwarp();
-        const int j = cu / kUnits, r0 = (cu % kUnits) * kUnitRows;
-        const int left = run.len - (run.t0 + j) * kKeysT - r0;  // tokens of the unit that are context
-        const uint32_t from = ring + slot * L::RAW;
-        const int r = lane & 15, half = lane >> 4;  // a lane has half a row of K and of V
-        const uint32_t kv = kv0 + 2 * j;
+      while (ok && run.next(sh, start)) {
+#pragma unroll 1
+        for (int j = run.t0; j < run.t1; ++j) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(raw_full(slot), raw_ph, abort, st, 0xF05)))) break;
+          uint4 kc[HW], vc[HW];
+          const uint32_t at = codes_at + slot * L::RAW;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int s = (int)((kv + i) % L::STAGES);
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(kv_empty(s), (((kv + i) / L::STAGES) & 1) ^ 1, abort, st, 0xF03));
-          if (!ok) break;
-          const uint32_t codes = from + i * kUnitRows * CB;
-          const uint32_t sc = lds_4(from + 2 * kUnitRows * CB + (i * 16 + r) * 4);
-          constexpr int NW = D / 16;  // words of half a row
-          const uint32_t row_at = sm_kv + s * L::TILE + (r0 + r) * 128;
-#pragma unroll
-          for (int y = 0; y < NW / 4; ++y) {
-            const int p = half * (NW / 4) + y;  // 16-byte piece of the codes
-            const uint4 c = lds_16(codes + r * CB + ((p ^ (CB == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4));
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int word = 4 * p + x;  // 8 channels; group word / (D / 32)
-              const uint32_t b = sc >> (8 * (word / (D / 32))) & 0xFFu, s1 = scale_bf16(b), s2 = s1 | (s1 << 16);
-              uint4 v = expand8(cw[x], s2, scale_bias(s2));
-              if (r >= left) v = make_uint4(0u, 0u, 0u, 0u);
-              sts_16(row_at + (word >> 3) * L::CHUNK + (((word & 7) ^ (r & 7)) << 4), v);
-            }
+          for (int y = 0; y < HW; ++y) {
+            kc[y] = lds_16(at + ((y ^ odd) << 4) * (HW - 1));
+            vc[y] = lds_16(at + L::CODES + ((y ^ odd) << 4) * (HW - 1));
           }
+          const uint32_t k_sc = lds_2(scales_at + slot * L::RAW), v_sc = lds_2(scales_at + slot * L::RAW + L::SCALES);
+          const bool on = j * kKeysT + r < run.len;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(ks), kph, abort, st, 0xF03)))) break;
+          expand_half<HW>(kc, k_sc, on, lane_to + ks * L::TILE);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(ks + 1), kph, abort, st, 0xF04)))) break;
+          expand_half<HW>(vc, v_sc, on, lane_to + (ks + 1) * L::TILE);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(kv_full(s));
-        }
-        slot = slot + 1 == (uint32_t)depth ? 0 : slot + 1;
-        cu += kExpand;
-        while (have && cu >= (run.t1 - run.t0) * kUnits) {
-          cu -= (run.t1 - run.t0) * kUnits;
-          kv0 += 2 * (run.t1 - run.t0);
-          have = run.next(sh);
+          if (lane == 0) {
+            mbar_arrive(raw_empty(slot));
+            mbar_arrive(kv_full(ks));
+            mbar_arrive(kv_full(ks + 1));
+          }
+          ks += 2;
+          if (ks == (uint32_t)L::STAGES) ks = 0, kph ^= 1u;
+          if (++slot == L::DEPTH) slot = 0, raw_ph ^= 1u;
         }
       }
-      cp_async_wait<0>();
-    } else if (warp == kWarpGuard) {
+    } else if (!KV4 && warp == kWarpGuard) {
       // ------------------------------------------------------------ guard: rows of V past the context become zeros
       uint32_t kv = 0, parts = 0;
       bool ok = true;
-      while (ok && run.next(sh)) {
+      while (ok && run.next(sh, start)) {
         const int n = run.t1 - run.t0, rows = run.len - (run.t1 - 1) * kKeysT;  // of the last tile
         kv += 2 * n;
         if (rows >= kKeysT) continue;
@@ -507,7 +553,7 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
     uint32_t ks = 0, kph = 0;          // stage of the next K tile and the parity of its use
     uint32_t sp = 0, ip = 0, qp = 0;   // parities: softmax results, segments with products, query tiles
     const uint64_t qd = umma_desc_kmajor(sb + (two ? q : 0) * L::TILE, 128);
-    while (run.next(sh)) {
+    while (run.next(sh, start)) {
       const int n = (int)uniform((uint32_t)(run.t1 - run.t0));
       const bool any = uniform((uint32_t)(rows_of(run.unit, q) > 0));
       auto on = [&](int j) { return two ? any : (j & 1) == q; };
@@ -560,31 +606,46 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
     }
   } else {
     // -------------------------------------------------------------- softmax: keys 32 part .. + 31 of a tile
+    if (KV4) regs_inc<80>();
     constexpr int PK = kKeysT / 4, PD = D / 4;
     const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t scol0 = tmem + ((uint32_t)(quarter * 32) << 16) + part * PK;
     const uint32_t ocol0 = tmem + ((uint32_t)(quarter * 32) << 16) + L::TMEM_O + part * PD;
     const float kInf = __int_as_float(0x7f800000);
     const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
-    uint32_t sn[2] = {0, 0}, in[2] = {0, 0}, ex = 0;  // S products and segments of each stream so far; exchanges
+    // What a segment's tiles do not need waits in shared memory (a register spilled here costs a trip to L2 each tile:
+    // next to 227 KB of shared memory the L1 keeps nothing).
+    runs_s[warp] = run;
+    // bits q: parity of stream q's next S; 2 + q: of its next finished segment; 4: buffer of the next exchange
+    uint32_t ph = 0;
     auto mx_at = [&](uint32_t i) { return sm_misc + L::MAXIMA + (i * 128 + row) * 16; };
     auto sum_at = [&](int q) { return sm_misc + L::SUMS + (q * 128 + row) * 16; };
     // (A wait that gave up is not looked at: the later ones return at once, and the warps of a quarter stay in step.)
-    while (run.next(sh)) {
-      const int n = run.t1 - run.t0, seg_seq = run.seq, seg_unit = run.unit;
+    for (;;) {
+      int n, seen, rows[2];  // tiles of the segment, tokens of it, rows of the streams
+      {
+        Run r = runs_s[warp];
+        if (!r.next(sh, start)) break;
+        n = r.t1 - r.t0;
+        seen = r.len - r.t0 * kKeysT;
+        rows[0] = rows_of(r.unit, 0);
+        rows[1] = rows_of(r.unit, 1);
+        __syncwarp();
+        if (lane == 0) runs_s[warp] = r;
+        __syncwarp();
+      }
       float m[2] = {-kInf, -kInf};
       uint64_t l2[2] = {0, 0};
-      const int rows[2] = {rows_of(run.unit, 0), rows_of(run.unit, 1)};
       for (int j = 0; j < n; ++j) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (two ? rows[q] == 0 : (j & 1) != q) continue;
           if (quarter >= live_q[q]) continue;
-          mbar_wait(s_full(q), sn[q] & 1, abort, st, 0xF40);
+          mbar_wait(s_full(q), ph >> q & 1u, abort, st, 0xF40);
+          ph ^= 1u << q;
           __syncwarp();
           if (quarter * 32 >= rows[q]) {  // no rows in this unit
             if (lane == 0) mbar_arrive(p_full(q));
-            ++sn[q];
             continue;
           }
           tc_fence_after();
@@ -592,7 +653,7 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
           tmem_ld_x32(scol0 + q * 128, x);
           tmem_ld_wait();
           reg_fence32(x);
-          const int lim = run.len - (run.t0 + j) * kKeysT - part * PK;  // columns that are context
+          const int lim = seen - j * kKeysT - part * PK;  // columns that are context
           if (lim < PK) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -602,8 +663,8 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
 #pragma unroll
           for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           // two buffers: who writes one again has met the other warps since they read it
-          const uint32_t mx = mx_at(ex & 1);
-          ++ex;
+          const uint32_t mx = mx_at(ph >> 4 & 1u);
+          ph ^= 16u;
           asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(mx + 4 * part), "f"(fmaxf(max3(m4[0], m4[1], m4[2]), m4[3])) : "memory");
           quarter_sync(quarter);
           const uint4 mo = lds_16(mx);
@@ -616,7 +677,7 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
             f2_unpack(l2[q], a, b);
             l2[q] = f2_pack(a * alpha, b * alpha);
             if (two ? j > 0 : j > 1) {  // O holds the stream's products so far; this part's columns of it
-              mbar_wait(pv_done(q), (sn[q] - 1) & 1, abort, st, 0xF41);
+              mbar_wait(pv_done(q), ph >> q & 1u, abort, st, 0xF41);  // (ph has this S's parity flipped)
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -650,18 +711,16 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(q));
-          ++sn[q];
         }
       }
       // ---- the segment's partial result: with one query tile the two streams' merged
-      const int64_t slot = (int64_t)seg_seq * (sh.H_kv * sh.RG) + seg_unit + blockIdx.x;
       const int nq[2] = {two ? (rows[0] ? n : 0) : (n + 1) / 2, two ? (rows[1] ? n : 0) : n / 2};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (nq[q] == 0 || quarter >= live_q[q]) continue;
-        mbar_wait(o_full(q), in[q] & 1, abort, st, 0xF50);
+        mbar_wait(o_full(q), ph >> (2 + q) & 1u, abort, st, 0xF50);
         __syncwarp();
-        ++in[q];
+        ph ^= 4u << q;
         if (quarter * 32 >= rows[q]) continue;
         float a, b;
         f2_unpack(l2[q], a, b);
@@ -674,11 +733,10 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
       for (int q = 0; q < 2; ++q) {
         if (!two && q == 1) break;
         if (nq[q] == 0 || quarter * 32 >= rows[q]) continue;
-        const int other = two ? q : 1;
         const bool both = !two && nq[1] > 0;
         const uint4 s0 = lds_16(sum_at(q));
         float M = m[q], sum = (__uint_as_float(s0.x) + __uint_as_float(s0.y)) + (__uint_as_float(s0.z) + __uint_as_float(s0.w));
-        float w0 = 1.f, w1 = 0.f;
+        float w0 = 1.f, w1 = 0.f;  // (4-bit values came in times 2^-18)
         if (both) {
           const uint4 s1 = lds_16(sum_at(1));
           M = fmaxf(m[0], m[1]);
@@ -686,21 +744,22 @@ __global__ void __launch_bounds__(kCtxThreads, 1) tree_context_kernel(
           w1 = m[1] == M ? 1.f : ex2_approx(m[1] - M);
           sum = sum * w0 + ((__uint_as_float(s1.x) + __uint_as_float(s1.y)) + (__uint_as_float(s1.z) + __uint_as_float(s1.w))) * w1;
         }
+        if (KV4) w0 *= kSubUnscale, w1 *= kSubUnscale;
         const bool live = row < rows[q];
-        const int64_t at = slot * sh.RU + (two ? q * kRowsT : 0) + row;
+        const Run& r = runs_s[warp];
+        const int64_t at = (((int64_t)r.seq + r.group) * (sh.H_kv * sh.RG) + r.unit) * sh.RU + (two ? q * kRowsT : 0) + row;
         float4* po = reinterpret_cast<float4*>(w.part_o + at * D + part * PD);
 #pragma unroll 1
         for (int c = 0; c < PD / 16; ++c) {
           uint32_t o[16], p[16];
           tmem_ld_x16(ocol0 + q * 128 + c * 16, o);
-          if (both) tmem_ld_x16(ocol0 + other * 128 + c * 16, p);
+          tmem_ld_x16(ocol0 + (two ? q : 1) * 128 + c * 16, p);
           tmem_ld_wait();
           reg_fence16(o);
-          if (both) {
-            reg_fence16(p);
+          reg_fence16(p);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(p[e]) * w1);
-          }
+          for (int e = 0; e < 16; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), w0, both ? __uint_as_float(p[e]) * w1 : 0.f));
           if (live)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -811,7 +870,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int c = tid; c < n_cta; c += kJoinThreads)
       if (w.errors[c]) raise_error(st, w.errors[c], 3u);
-  const int64_t total = w.starts[sh.B], quota = run_quota(total, n_cta);
+  const int64_t quota = run_quota(w.starts[sh.B], sh.groups);
   const int tiles = sh.tiles(b);
   const int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * rows_per_warp;
   for (int r = r0; r < r0 + rows_per_warp; ++r) {
@@ -829,9 +888,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
     const float kInf = __int_as_float(0x7f800000);
     if (tiles) {
       const int rg = r / sh.RU, unit = g * sh.RG + rg;
-      const int64_t f0 = w.starts[b] + (int64_t)unit * tiles, f1 = f0 + tiles;
-      const int c0 = (int)(f0 / quota), c1 = (int)((f1 - 1) / quota);
-      const int64_t s0 = ((int64_t)b * (sh.H_kv * sh.RG) + unit) * sh.RU + (r - rg * sh.RU);
+      const int64_t f0 = w.starts[b];
+      const int c0 = (int)(f0 / quota), c1 = (int)((f0 + tiles - 1) / quota);
+      const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // from group to group
+      const int64_t s0 = b * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
       for (int c = c0; c <= c1; c += 4) {  // four partials in flight
         float2 ml[4];
         float x[4][V];
@@ -841,7 +901,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
 #pragma unroll
           for (int e = 0; e < V; ++e) x[u][e] = 0.f;
           if (c + u <= c1) {
-            const int64_t s = s0 + (int64_t)(c + u) * sh.RU;
+            const int64_t s = s0 + (c + u) * per;
             ml[u] = w.part_ml[s];
             const float* p = w.part_o + s * D + lane * V;
             if constexpr (V == 4) {
@@ -905,7 +965,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
 }
 
 size_t carve(const TreePlan& p, char* base, TreeScratch* out) {
-  const size_t units = (size_t)p.B * p.H_kv * p.RG, slots = units + num_sms();
+  const size_t slots = ((size_t)p.B + p.groups) * p.H_kv * p.RG;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* r = base ? base + off : nullptr;
@@ -927,7 +987,7 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
                      float* lse, const TreeScratch& w, DeviceStatus* st, cudaStream_t s) {
   using L = Layout<D>;
   const int gs = p.H_q / p.H_kv;
-  const bool two = p.T * gs > kRowsT;
+  const bool two = !KV4 && p.T * gs > kRowsT;
   alignas(64) unsigned char tq[128] = {}, tk[128] = {}, tv[128] = {};
   const uint64_t row = (uint64_t)D * 2;
   // q [B T][H_q][d] as boxes {64 channels, gs heads, 128 / gs positions}; pools [rows][H_kv][d] as {64, 1, box_rows}
@@ -935,7 +995,15 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   while (box_rows < kKeysT && map.page % (2 * box_rows) == 0) box_rows *= 2;
   if (!encode_tmap_3d(tq, q, D, (uint64_t)p.H_q, (uint64_t)p.B * p.T, row, (uint64_t)p.H_q * row, 64, gs, kRowsT / gs, 128))
     return cudaErrorInvalidValue;
-  if (!KV4) {
+  if (KV4) {
+    // codes [rows][H_kv][d / 2] bytes (as 16-bit words) in the order {word, row of a box, head, box}
+    const uint64_t cb = D / 2, boxes = (uint64_t)map.n_pages * (map.page / box_rows);
+    const uint64_t dims[4] = {cb / 2, (uint64_t)box_rows, (uint64_t)p.H_kv, boxes};
+    const uint64_t strides[3] = {(uint64_t)p.H_kv * cb, cb, (uint64_t)box_rows * p.H_kv * cb};
+    const uint32_t box[4] = {(uint32_t)cb / 2, (uint32_t)box_rows, 1, 1};
+    if (!encode_tmap_4d(tk, pool.k_codes, dims, strides, box, D / 2) || !encode_tmap_4d(tv, pool.v_codes, dims, strides, box, D / 2))
+      return cudaErrorInvalidValue;
+  } else {
     const uint64_t rows = (uint64_t)map.n_pages * map.page;
     if (!encode_tmap_3d(tk, k_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128) ||
         !encode_tmap_3d(tv, v_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128))
@@ -951,13 +1019,16 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   sh.H_kv = p.H_kv;
   sh.RG = p.RG;
   sh.RU = p.RU;
+  sh.groups = p.groups;
+  sh.rounds = p.rounds;
   auto kern = tree_context_kernel<D, KV4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(two, KV4));
   if (e != cudaSuccess) return e;
   const float sl2 = scale * 1.4426950408889634f;
   const int n_cta = num_sms();
-  kern<<<n_cta, kCtxThreads, L::smem(two, KV4), s>>>(*reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
-                                                     *reinterpret_cast<const CUtensorMap*>(tv), sh, map, pool, box_rows, sl2, w, st);
+  kern<<<n_cta, ctx_threads(KV4), L::smem(two, KV4), s>>>(*reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
+                                                     *reinterpret_cast<const CUtensorMap*>(tv), sh, map, pool, box_rows,
+                                                     KV4 ? sl2 * kSubUnscale : sl2, w, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int R = p.T * gs;
   // a row a warp while that leaves the GPU room
@@ -978,7 +1049,7 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
 
 }  // namespace
 
-TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d) {
+TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d, bool kv4) {
   TreePlan p;
   p.B = B;
   p.T = T;
@@ -986,8 +1057,18 @@ TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d) {
   p.H_kv = H_kv;
   p.d = d;
   const int R = T * (H_q / H_kv);
-  p.RG = (R + 2 * kRowsT - 1) / (2 * kRowsT);
-  p.RU = R < 2 * kRowsT ? R : 2 * kRowsT;
+  const int most = kv4 ? kRowsT : 2 * kRowsT;
+  p.RG = (R + most - 1) / most;
+  p.RU = R < most ? R : most;
+  // A CTA has one unit (K/V head and row group) and, with the CTAs of the other units of its group, one run of the list
+  // of all sequences' tiles.  As many groups as fill the GPU in `rounds` items a CTA; more than one round where one
+  // leaves over 7 % of the CTAs without an item.
+  const int units = H_kv * p.RG, n_cta = num_sms();
+  p.groups = 0;
+  for (int k = 1, best = -1; k <= kMaxRounds && best < 93; ++k) {
+    const int m = k * n_cta / units, full = 100 * m * units / (k * n_cta);
+    if (m >= 1 && full > best) p.groups = m, p.rounds = k, best = full;
+  }
   return p;
 }
 
