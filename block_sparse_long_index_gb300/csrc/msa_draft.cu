@@ -7,13 +7,14 @@
 // otherwise r(x) becomes 0 and W falls by it.  The next token is drawn from the r of the node where the walk ends.
 //
 // Bound: HBM, one row of p and of q a sequence (a node whose drafts are accepted is left after reading one element of
-// each); a few sequences by latency.  A cluster of 8 CTAs a sequence: each of its 128 warps has one run of the
-// vocabulary, a pass over a row leaves every run's sum in shared memory, and the last pass's sums find the run, then the
-// token, without another pass over the row.
+// each), and more passes over it, from L2, for each further rejection at the node; a few sequences by latency.  A cluster of
+// 8 CTAs a sequence: each of its warps has one run of the vocabulary, a pass over a row leaves every run's sum in shared
+// memory, and the last pass's sums find the run, then the token, without another pass over the row.
 //
-// Which token is drawn hangs on comparisons of sums, so these are held to some 48 bits: each difference p - c q is an fp32
-// and its error, summed as such by a lane, and from there in 64 bits.  (64-bit sums throughout would be bound by the few
-// 64-bit units; fp32 sums draw another token in one of a thousand cases at 128000 tokens.)
+// Which token is drawn hangs on comparisons of sums, so these are held to some 43 bits: each difference p - c q is an fp32
+// and its error, a lane's sum likewise, and all sums above a lane's are integers of 2^-48, which add up the same in any
+// order.  (64-bit floating point throughout would be bound by the few units for it; fp32 sums draw another token in one of
+// a thousand cases at 128000 tokens.)
 #include <math.h>
 
 #include "msa_common.cuh"
@@ -23,22 +24,17 @@ namespace msa {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxNodes = 64;
+constexpr int kFly = 2;  // vectors of each row that a lane has in flight
+constexpr double kUnit = 281474976710656.0;  // 2^48
 
 // A probability: what is not a positive finite number counts as 0.
 __device__ __forceinline__ float prob(float x) { return x > 0.f && x <= 3.402823466e38f ? x : 0.f; }
 
-// A sum as an fp32 and its error.
-struct Sum2 {
-  float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float x, float err) {
-    const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)), err));
-    hi = s;
-  }
-};
+// (x + err) 2^48 as an integer, for sums of lanes (2 at most: 8192 lanes' fit, and a distribution's lane holds no more).
+__device__ __forceinline__ long long fixed(float x, float err) {
+  return __float2ll_rn(fminf(x, 2.f) * (float)kUnit) + __float2ll_rn(fminf(err, 1.f) * (float)kUnit);
+}
 
 struct VerifyArgs {
   const float *probs, *draft_probs;
@@ -77,24 +73,38 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ double remote_double(const double* p, uint32_t rank) {
-  double x;
+__device__ __forceinline__ long long remote_sum(const long long* p, uint32_t rank) {
+  long long x;
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
   return x;
 }
 
-// r of one element: an fp32 and its error, (0, 0) where it is not positive.  c = ch + cl.
-__device__ __forceinline__ void rest_of(float p, float q, float ch, float cl, float& x, float& err) {
-  p = prob(p);
-  q = prob(q);
+// How the difference of a row's elements is taken.
+enum Form {
+  kPlain,  // p
+  kOnce,   // p - q: the first rejection, c = 1
+  kTimes,  // p - c q, c = ch + cl
+};
+// p - c q of clean p and q as an fp32 and its error (exact but for the last bits of cl q); false where it is not positive.
+// Where it is, p is at least c q, so that the error of p - t is (p - s) - t.
+template <Form F>
+__device__ __forceinline__ bool rest_of(float p, float q, float ch, float cl, float& x, float& err) {
+  if (F == kPlain) {
+    x = p;
+    err = 0.f;
+    return p > 0.f;
+  }
+  if (F == kOnce) {
+    x = __fsub_rn(p, q);
+    err = __fsub_rn(__fsub_rn(p, x), q);
+    return x > 0.f;
+  }
   const float t = __fmul_rn(ch, q), te = __fmaf_rn(cl, q, __fmaf_rn(ch, q, -t));
-  const float s = __fsub_rn(p, t), b = __fsub_rn(s, p);
-  const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(s, b)), __fadd_rn(t, b)), te);
-  const bool on = __fadd_rn(s, e) > 0.f;
-  x = on ? s : 0.f;
-  err = on ? e : 0.f;
+  x = __fsub_rn(p, t);
+  err = __fsub_rn(__fsub_rn(__fsub_rn(p, x), t), te);
+  return __fadd_rn(x, err) > 0.f;
 }
 
 // The run [v0, v1) of 4-element vectors that warp `w` of the cluster has; element e of the row is number e + skew of them
@@ -103,10 +113,10 @@ struct RowRun {
   int64_t v0, v1;
   int skew;
 };
-__device__ __forceinline__ RowRun run_of(int64_t row_at, int64_t V, int w) {
+__device__ __forceinline__ RowRun run_of(int64_t row_at, int64_t V, int w, int runs) {
   RowRun r;
   r.skew = (int)(row_at & 3);
-  const int64_t vecs = (V + r.skew + 3) / 4, each = (vecs + kCluster * kWarps - 1) / (kCluster * kWarps);
+  const int64_t vecs = (V + r.skew + 3) / 4, each = (vecs + runs - 1) / runs;
   r.v0 = min(w * each, vecs);
   r.v1 = min(r.v0 + each, vecs);
   return r;
@@ -123,55 +133,120 @@ __device__ __forceinline__ float4 load_vec(const float* row, int64_t v, int skew
   return x;
 }
 
-// The state of a node's residual: c (with q), or the tokens taken out (without).
+// A node's rows and what its rejections left: c (with q), or the tokens that count as 0 (without).
 struct Residual {
   const float *p, *q;  // q null: p alone
   float ch, cl;
-  const int* out;  // tokens that count as 0
+  const int* out;
   int n_out;
   int64_t V;
   int skew;
-  __device__ __forceinline__ void at(int64_t v, float (&x)[4], float (&err)[4]) const {
-    const float4 a = load_vec(p, v, skew, V);
-    const float pv[4] = {a.x, a.y, a.z, a.w};
-    if (q) {
-      const float4 b = load_vec(q, v, skew, V);
-      const float qv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) rest_of(pv[j], qv[j], ch, cl, x[j], err[j]);
-      return;
+  template <Form F>
+  __device__ __forceinline__ void load(int64_t v, int64_t v1, float4& a, float4& b) const {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (v < v1) {
+      a = load_vec(p, v, skew, V);
+      if (F != kPlain) b = load_vec(q, v, skew, V);
     }
+  }
+  template <typename S>
+  __device__ __forceinline__ void set(const VerifyArgs& args, const S& step, int64_t at, const int* out_tokens) {
+    p = args.probs + at;
+    q = step.form == kPlain ? nullptr : args.draft_probs + at;
+    ch = step.ch;
+    cl = step.cl;
+    out = out_tokens;
+    n_out = step.n_out;
+    V = args.V;
+    skew = (int)(at & 3);
+  }
+  // The vector's r, one by one and clean, as integers.
+  __device__ __forceinline__ void each(int64_t v, const float4& a, const float4& b, long long (&d)[4]) const {
+    const float pv[4] = {a.x, a.y, a.z, a.w}, qv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = prob(pv[j]), err[j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      float x, err;
+      const bool on = q ? rest_of<kTimes>(prob(pv[j]), prob(qv[j]), ch, cl, x, err) : rest_of<kPlain>(prob(pv[j]), 0.f, 0.f, 0.f, x, err);
+      d[j] = on ? fixed(x, err) : 0;
+    }
     for (int i = 0; i < n_out; ++i) {
-      const int64_t d = (int64_t)out[i] + skew - v * 4;
+      const int64_t at = (int64_t)out[i] + skew - v * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (d == j) x[j] = 0.f;
+        if (at == j) d[j] = 0;
     }
   }
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) verify_kernel(VerifyArgs a, DeviceStatus* st) {
+// A lane's sum over the vectors v0 + lane, + 32, .. below v1.  The running sum begins at 2, above every probability, so that
+// the error of adding x to it is x - (sum - before); a value above 1 sends the lane through its vectors again, one by one.
+template <Form F>
+__device__ __forceinline__ long long lane_sum(const Residual& r, int64_t v0, int64_t v1) {
+  const int lane = threadIdx.x & 31;
+  float hi = 2.f, lo = 0.f, most = 0.f;
+  for (int64_t v = v0 + lane; v < v1; v += 32 * kFly) {
+    float4 a[kFly], b[kFly];
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) r.load<F>(v + 32 * u, v1, a[u], b[u]);
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      float pv[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+      const float qv[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+      if (F == kPlain)
+        for (int i = 0; i < r.n_out; ++i) {
+          const int64_t at = (int64_t)r.out[i] + r.skew - (v + 32 * u) * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (at == j) pv[j] = 0.f;
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x, err;
+        const float p = fmaxf(pv[j], 0.f), q = fmaxf(qv[j], 0.f);  // (a NaN as 0)
+        most = fmaxf(most, F == kPlain ? p : fmaxf(p, q));
+        if (rest_of<F>(p, q, r.ch, r.cl, x, err)) {
+          const float s = __fadd_rn(hi, x);
+          lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(x, __fsub_rn(s, hi)), err));
+          hi = s;
+        }
+      }
+    }
+  }
+  if (!(most <= 1.f)) {  // no distribution, or an infinity
+    long long sum = 0;
+    for (int64_t v = v0 + lane; v < v1; v += 32) {
+      float4 a, b;
+      r.load<F>(v, v1, a, b);
+      long long d[4];
+      r.each(v, a, b, d);
+      sum = min(sum + (d[0] + d[1]) + (d[2] + d[3]), (long long)(2 * kUnit));
+    }
+    return sum;
+  }
+  return fixed(hi - 2.f, lo);
+}
+
+// What a CTA does next: one thread's decision, in 64 bits (all threads of a CTA would queue for the few units there are
+// for that: with them the smallest call took 25 us).
+struct Step {
+  int node, n_out, pass;  // pass: sum the residual of `node`; otherwise the walk is over
+  int form;
+  float ch, cl;
+};
+
+// THREADS: 1024 where that leaves a CTA an SM, fewer where several CTAs have to share one.
+template <int THREADS>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(VerifyArgs a, DeviceStatus* st) {
+  constexpr int kWarps = THREADS / 32, kRuns = kCluster * kWarps;
   __shared__ int token_s[kMaxNodes], path_s[kMaxNodes], out_s[kMaxNodes];
   __shared__ float p_s[kMaxNodes], q_s[kMaxNodes], u_s[kMaxNodes];
   __shared__ unsigned long long kids_s[kMaxNodes];
-  __shared__ double seg_s[2][kWarps], cta_s[2];  // sums of the warps' runs, and of the CTA's, by pass
+  __shared__ long long seg_s[2][kWarps], cta_s[2];  // sums of the warps' runs, and of the CTA's, by pass
+  __shared__ Step step_s;
+  __shared__ int n_path_s;
+  __shared__ long long target_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / kCluster, rank = (int)cluster_rank();
-  if (a.report && blockIdx.x == 0) {
-    bool bad = false;
-    for (int i = tid; i < a.B * a.T; i += kThreads) {
-      const int s = i / a.T, j = i - s * a.T;
-      int x, y;
-      if (j < nodes_of(a, s, bad) && j > 0) offered(a, s, j, x, y, bad);
-    }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) {
-      st->flags = bad ? kErrBadIndex : 0u;
-      st->first_code = bad ? 14u : 0u;
-    }
-  }
   bool bad = false;
   const int T = nodes_of(a, b, bad);
   if (tid < kMaxNodes) kids_s[tid] = 0ull;
@@ -193,175 +268,190 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
   if (bad && !a.report && rank == 0) raise_error(st, kErrBadIndex, 14u);
   __syncthreads();
 
-  int node = 0, n_path = 0, n_out = 0, pass = 0;
-  double c = 0.0, W = 1.0, total = 0.0;
+  // ---- the walk: thread 0's state, from pass to pass (the CTAs of the cluster decide alike)
+  int n_path = 0, node = 0, n_out = 0, passes = 0;
+  unsigned long long kids = kids_s[0];
+  double c = 0.0, W = 1.0;
   bool summed = false;  // whether the last pass's sums are those of the present residual
-  // Sums the present residual (c: with q only where c > 0); every thread has the cluster's sum afterwards.
-  auto residual = [&]() {
-    Residual r;
-    const int64_t at = ((int64_t)b * a.T + node) * a.V;
-    r.p = a.probs + at;
-    r.q = a.draft_probs && c > 0.0 ? a.draft_probs + at : nullptr;
-    r.ch = (float)c;
-    r.cl = (float)(c - (double)r.ch);
-    r.out = out_s;
-    r.n_out = n_out;
-    r.V = a.V;
-    r.skew = (int)(at & 3);
-    return r;
-  };
-  auto sum_pass = [&]() {
-    const Residual r = residual();
-    const RowRun run = run_of(((int64_t)b * a.T + node) * a.V, a.V, rank * kWarps + warp);
-    Sum2 s;
-#pragma unroll 4
-    for (int64_t v = run.v0 + lane; v < run.v1; v += 32) {
-      float x[4], e[4];
-      r.at(v, x, e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s.add(x[j], e[j]);
-    }
-    double d = (double)s.hi + (double)s.lo;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) seg_s[pass & 1][warp] = d;
-    __syncthreads();
+  long long total = 0;  // of the last pass; every thread's
+  if (tid == 0 && T > 0) path_s[n_path++] = 0;
+  while (T > 0) {
     if (tid == 0) {
-      double t = 0.0;
-      for (int w = 0; w < kWarps; ++w) t += seg_s[pass & 1][w];
-      cta_s[pass & 1] = t;
-    }
-    cluster_sync();  // (and whoever read the buffer two passes ago is done)
-    double t = 0.0;
-    for (int k = 0; k < kCluster; ++k) t += remote_double(&cta_s[pass & 1], k);
-    ++pass;
-    summed = true;
-    return t;
-  };
-  if (T > 0) {
-    if (tid == 0) path_s[0] = 0;
-    n_path = 1;
-    unsigned long long kids = kids_s[0];
-    while (kids) {
-      const int j = __ffsll((long long)kids) - 1;
-      kids &= kids - 1;
-      double rx;
-      bool yes;
-      if (a.draft_probs) {
-        rx = (double)p_s[j] - c * (double)q_s[j];
-        if (!(rx > 0.0)) rx = 0.0;
-        yes = (double)q_s[j] * (double)u_s[j] * W < rx;
-      } else {
-        rx = (double)p_s[j];
-        for (int i = 0; i < n_out; ++i)
-          if (out_s[i] == token_s[j]) rx = 0.0;
-        yes = (double)u_s[j] * W < rx;
+      Step step;
+      step.pass = 0;
+      if (passes && summed) W = (double)total / kUnit;  // (a pass after a rejection; not read after another one)
+      while (kids) {
+        const int j = __ffsll((long long)kids) - 1;
+        kids &= kids - 1;
+        double rx;
+        bool yes;
+        if (a.draft_probs) {
+          rx = fmax((double)p_s[j] - c * (double)q_s[j], 0.0);
+          yes = (double)q_s[j] * (double)u_s[j] * W < rx;
+        } else {
+          rx = (double)p_s[j];
+          for (int i = 0; i < n_out; ++i)
+            if (out_s[i] == token_s[j]) rx = 0.0;
+          yes = (double)u_s[j] * W < rx;
+        }
+        if (yes) {
+          node = j;
+          kids = kids_s[j];
+          c = 0.0;
+          W = 1.0;
+          n_out = 0;
+          summed = false;
+          path_s[n_path++] = j;
+        } else if (a.draft_probs) {
+          c += W;
+          step.pass = 1;
+          break;
+        } else {
+          out_s[n_out++] = token_s[j];
+          W -= rx;
+          summed = false;
+        }
       }
-      if (yes) {
-        node = j;
-        kids = kids_s[j];
+      if (!step.pass && !summed) step.pass = 1;  // the walk is over: what the next token is drawn from
+      else if (!step.pass && total <= 0 && (c > 0.0 || n_out)) {  // nothing is left (p = q to the last bit): the target's own
         c = 0.0;
-        W = 1.0;
-        __syncthreads();  // out_s is read
         n_out = 0;
-        summed = false;
-        if (tid == 0) path_s[n_path] = j;
-        ++n_path;
-      } else if (a.draft_probs) {
-        c += W;
-        W = total = sum_pass();
-      } else {
-        __syncthreads();  // out_s is read
-        if (tid == 0) out_s[n_out] = token_s[j];
-        __syncthreads();
-        ++n_out;
-        W -= rx;
-        summed = false;
+        step.pass = 1;
       }
+      if (step.pass) summed = true;
+      step.node = node;
+      step.n_out = n_out;
+      step.form = !a.draft_probs || !(c > 0.0) ? kPlain : c == 1.0 ? kOnce : kTimes;
+      step.ch = (float)c;
+      step.cl = (float)(c - (double)step.ch);
+      step_s = step;
+      n_path_s = n_path;
     }
-    if (!summed) total = sum_pass();
-    if (!(total > 0.0) && (c > 0.0 || n_out)) {  // nothing is left (p = q to the last bit): the target's own distribution
-      c = 0.0;
-      n_out = 0;
-      total = sum_pass();
+    __syncthreads();
+    if (!step_s.pass) break;
+    // ---- a pass: the residual's sum over the cluster
+    {
+      Residual r;
+      const int64_t at = ((int64_t)b * a.T + step_s.node) * a.V;
+      r.set(a, step_s, at, out_s);
+      const RowRun run = run_of(at, a.V, rank * kWarps + warp, kRuns);
+      long long d = step_s.form == kPlain ? lane_sum<kPlain>(r, run.v0, run.v1)
+                    : step_s.form == kOnce ? lane_sum<kOnce>(r, run.v0, run.v1)
+                                           : lane_sum<kTimes>(r, run.v0, run.v1);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) seg_s[passes & 1][warp] = d;
+      __syncthreads();
+      if (warp == 0) {
+        d = lane < kWarps ? seg_s[passes & 1][lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) cta_s[passes & 1] = d;
+      }
+      cluster_sync();  // (and whoever read the buffer two passes ago is done)
+      long long x[kCluster];
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) x[k] = remote_sum(&cta_s[passes & 1], k);
+      total = 0;
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) total += x[k];
+      ++passes;
     }
   }
   if (rank == 0) {
-    __syncthreads();  // path_s is written
-    for (int i = tid; i < a.T; i += kThreads) a.path[(int64_t)b * a.T + i] = i < n_path ? path_s[i] : -1;
-    if (tid == 0) a.n_path[b] = n_path;
+    const int n = T > 0 ? n_path_s : 0;
+    for (int i = tid; i < a.T; i += THREADS) a.path[(int64_t)b * a.T + i] = i < n ? path_s[i] : -1;
+    if (tid == 0) a.n_path[b] = n;
   }
   // ---- the token: the CTA, the warp's run, the vector and the element at which the running sum first exceeds the target
-  if (T == 0 || !(total > 0.0)) {
+  if (T == 0 || total <= 0) {
     if (rank == 0 && tid == 0) a.next[b] = -1;
   } else {
-    float ul = a.u_last[b];
-    ul = ul > 0.f ? fminf(ul, 0.99999994f) : 0.f;  // (a NaN counts as 0)
-    const double target = (double)ul * total;
-    const int buf = (pass - 1) & 1;
-    double before = 0.0;
-    int k = 0;  // the last CTA with a share takes what rounding leaves over
-    {
-      double run = 0.0;
-      bool done = false;
-      for (int i = 0; i < kCluster; ++i) {
-        const double x = remote_double(&cta_s[buf], i);
-        if (!done && x > 0.0) {
-          k = i;
-          before = run;
-          done = run + x > target;
-        }
-        run += x;
-      }
+    if (tid == 0) {
+      float ul = a.u_last[b];
+      ul = ul > 0.f ? fminf(ul, 0.99999994f) : 0.f;  // (a NaN counts as 0)
+      target_s = (long long)((double)ul * (double)total);  // a whole sum exceeds u total where it exceeds its whole part
     }
-    if (k == rank) {
-      int w = 0;
-      double run = before;
-      bool done = false;
-      for (int i = 0; i < kWarps; ++i) {
-        const double x = seg_s[buf][i];
-        if (!done && x > 0.0) {
-          w = i;
-          before = run;
-          done = run + x > target;
-        }
-        run += x;
+    __syncthreads();
+    const long long target = target_s;
+    const int buf = (passes - 1) & 1;
+    long long before = 0;
+    int k = 0;
+    bool done = false;
+#pragma unroll
+    for (int i = 0; i < kCluster; ++i) {
+      const long long x = remote_sum(&cta_s[buf], i);
+      if (!done && before + x > target) k = i, done = true;
+      if (!done) before += x;
+    }
+    if (done && k == rank) {  // (it is: the sums add up to the total)
+      // the warps' runs likewise, a lane each
+      const long long mine = lane < kWarps ? seg_s[buf][lane] : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
       }
+      const int w = __ffs(__ballot_sync(0xffffffffu, before + incl > target)) - 1;
       if (warp == w) {
-        const Residual r = residual();
-        const RowRun rr = run_of(((int64_t)b * a.T + node) * a.V, a.V, rank * kWarps + warp);
-        int64_t last = -1, hit = -1;  // the last element with a share so far; the one
-        double sum = before;
-        for (int64_t v0 = rr.v0; v0 < rr.v1 && hit < 0; v0 += 32) {
-          const int64_t v = v0 + lane;
-          float x[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-          if (v < rr.v1) r.at(v, x, e);
-          double d[4], mine = 0.0;
+        const Step step = step_s;
+        Residual r;
+        const int64_t at = ((int64_t)b * a.T + step.node) * a.V;
+        r.set(a, step, at, out_s);
+        const RowRun run = run_of(at, a.V, rank * kWarps + warp, kRuns);
+        int64_t last = -1, hit = -1;  // the last element with a share so far (an element's sum may round below its lane's); the one
+        long long sum = before + __shfl_sync(0xffffffffu, incl - mine, w);
+        for (int64_t v0 = run.v0; v0 < run.v1 && hit < 0; v0 += 32 * kFly) {
+          float4 pa[kFly], qa[kFly];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) d[j] = (double)x[j] + (double)e[j], mine += d[j];
-          double incl = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
+          for (int u = 0; u < kFly; ++u) {
+            if (r.q) r.load<kTimes>(v0 + 32 * u + lane, run.v1, pa[u], qa[u]);
+            else r.load<kPlain>(v0 + 32 * u + lane, run.v1, pa[u], qa[u]);
           }
-          double s = sum + (incl - mine);
-          int64_t first = -1, end = -1;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s += d[j];
-            if (d[j] > 0.0) {
-              end = v * 4 - r.skew + j;
-              if (first < 0 && s > target) first = end;
+          for (int u = 0; u < kFly; ++u) {
+            const int64_t v = v0 + 32 * u + lane;
+            long long d[4];
+            r.each(v, pa[u], qa[u], d);
+            const long long of_lane = (d[0] + d[1]) + (d[2] + d[3]);
+            long long up = of_lane;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long t = __shfl_up_sync(0xffffffffu, up, o);
+              if (lane >= o) up += t;
             }
+            long long s = sum + (up - of_lane);
+            int64_t first = -1, end = -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s += d[j];
+              if (d[j] > 0) {
+                end = v * 4 - r.skew + j;
+                if (first < 0 && s > target) first = end;
+              }
+            }
+            const unsigned found = __ballot_sync(0xffffffffu, first >= 0), share = __ballot_sync(0xffffffffu, end >= 0);
+            if (found && hit < 0) hit = __shfl_sync(0xffffffffu, first, __ffs(found) - 1);
+            if (share) last = __shfl_sync(0xffffffffu, end, 31 - __clz(share));
+            sum += __shfl_sync(0xffffffffu, up, 31);
           }
-          const unsigned has = __ballot_sync(0xffffffffu, first >= 0), any = __ballot_sync(0xffffffffu, end >= 0);
-          if (has) hit = __shfl_sync(0xffffffffu, first, __ffs(has) - 1);
-          if (any) last = __shfl_sync(0xffffffffu, end, 31 - __clz(any));
-          sum += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) a.next[b] = (int32_t)(hit >= 0 ? hit : last);
       }
+    }
+  }
+  if (a.report && blockIdx.x == kCluster - 1) {
+    bad = false;
+    for (int i = tid; i < a.B * a.T; i += THREADS) {
+      const int s = i / a.T, j = i - s * a.T;
+      int x, y;
+      if (j < nodes_of(a, s, bad) && j > 0) offered(a, s, j, x, y, bad);
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+      st->flags = bad ? kErrBadIndex : 0u;
+      st->first_code = bad ? 14u : 0u;
     }
   }
   cluster_sync();  // no CTA leaves while another reads its sums
@@ -390,7 +480,11 @@ cudaError_t launch_verify(const float* probs, const float* draft_probs, const in
   a.T = T;
   a.V = V;
   a.report = verify_reports(B, T);
-  verify_kernel<<<(unsigned)(B * kCluster), kThreads, 0, s>>>(a, st);
+  // CTAs of all sequences together on the GPU, where that is possible
+  const int64_t ctas = (int64_t)B * kCluster, sms = num_sms();
+  if (ctas <= sms) verify_kernel<1024><<<(unsigned)ctas, 1024, 0, s>>>(a, st);
+  else if (ctas <= 2 * sms) verify_kernel<512><<<(unsigned)ctas, 512, 0, s>>>(a, st);
+  else verify_kernel<256><<<(unsigned)ctas, 256, 0, s>>>(a, st);
   return cudaGetLastError();
 }
 

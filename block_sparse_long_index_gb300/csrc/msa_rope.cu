@@ -107,13 +107,56 @@ __device__ __forceinline__ void turn8(float (&x)[8], int p, int lanes, const Rop
 }
 
 __device__ __forceinline__ uint4 ld_once(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(v[j]), x[2 * j + 1] = bf16_hi(v[j]);
+// Pairs of fp32 with every result rounded as by itself, subnormal ones included.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return f2_pack(bf16_lo(w), bf16_hi(w)); }
+
+// turn8 of bf16 rows: the words of a piece, turned and rounded.  (A product with -s is the product with s negated, so
+// a c - b s is a c + (-b) s to the last bit.)
+__device__ __forceinline__ uint4 turn8_bf16(uint4 w, int p, int lanes, const Rope& rope, const float* c, int span) {
+  uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  if (rope.interleaved) {
+    if (8 * p >= rope.rot) return w;
+    const float4 cv = *reinterpret_cast<const float4*>(c + 4 * p), sv = *reinterpret_cast<const float4*>(c + span + 4 * p);
+    const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t o = __byte_perm(v[j], v[j] ^ 0x80000000u, 0x1076);  // (-b, a)
+      v[j] = narrow2(add2(mul2(widen2(v[j]), f2_pack(cc[j], cc[j])), mul2(widen2(o), f2_pack(ss[j], ss[j]))));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  const int hp = rope.rot / 16;  // pieces of a half
+  const bool first = p < hp, in = p < 2 * hp;
+  const int q = !in ? p : first ? p + hp : p - hp, src = ((int)(threadIdx.x & 31u) & ~(lanes - 1)) | q;
+  const uint32_t sign = first ? 0x80008000u : 0u;
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = __shfl_sync(0xffffffffu, v[j], src) ^ sign;
+  if (!in) return w;
+  const ulonglong2* cp = reinterpret_cast<const ulonglong2*>(c + 8 * (first ? p : q));
+  const ulonglong2* sp = reinterpret_cast<const ulonglong2*>(c + span + 8 * (first ? p : q));
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const ulonglong2 cj = cp[j], sj = sp[j];
+    v[2 * j] = narrow2(add2(mul2(widen2(v[2 * j]), cj.x), mul2(widen2(o[2 * j]), sj.x)));
+    v[2 * j + 1] = narrow2(add2(mul2(widen2(v[2 * j + 1]), cj.y), mul2(widen2(o[2 * j + 1]), sj.y)));
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
   unsigned short r;
@@ -161,22 +204,18 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const T* __restrict__
     for (int u = 0; u < kFly; ++u) {
       const int task = base + u * kWarps, t = task / chunks, e = (task - t * chunks) * 32 + lane;
       if (task >= tasks) break;  // (uniform in the warp)
-      float v[8];
-      if constexpr (F32) {
-        v[0] = __uint_as_float(w[u][0].x), v[1] = __uint_as_float(w[u][0].y), v[2] = __uint_as_float(w[u][0].z);
-        v[3] = __uint_as_float(w[u][0].w), v[4] = __uint_as_float(w[u][1].x), v[5] = __uint_as_float(w[u][1].y);
-        v[6] = __uint_as_float(w[u][1].z), v[7] = __uint_as_float(w[u][1].w);
-      } else {
-        widen8(w[u][0], v);
-      }
-      turn8(v, e & (lanes - 1), lanes, rope, cs + 2 * t * 128, 128);
-      if (e >= pieces) continue;
+      const int p = e & (lanes - 1);
       T* to = y + (i0 + t) * y_stride + e * 8;
       if constexpr (F32) {
+        float v[8] = {__uint_as_float(w[u][0].x), __uint_as_float(w[u][0].y), __uint_as_float(w[u][0].z), __uint_as_float(w[u][0].w),
+                      __uint_as_float(w[u][1].x), __uint_as_float(w[u][1].y), __uint_as_float(w[u][1].z), __uint_as_float(w[u][1].w)};
+        turn8(v, p, lanes, rope, cs + 2 * t * 128, 128);
+        if (e >= pieces) continue;
         *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
       } else {
-        *reinterpret_cast<uint4*>(to) = narrow8(v);
+        const uint4 v = turn8_bf16(w[u][0], p, lanes, rope, cs + 2 * t * 128, 128);
+        if (e < pieces) *reinterpret_cast<uint4*>(to) = v;
       }
     }
   }
@@ -213,51 +252,42 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64
   first[0] = 0;
 #pragma unroll
   for (int x = 0; x < kKinds; ++x) first[x + 1] = first[x] + (pieces[x] + 31) / 32;
-  const int chunks = first[kKinds], tasks = n * chunks;
-  // token, kind and piece of a task; the piece -1 where this lane has none
-  auto split = [&](int task, int& t, int& kind, int& e) {
-    t = task / chunks;
-    const int c = task - t * chunks;
-    kind = (c >= first[1]) + (c >= first[2]) + (c >= first[3]) + (c >= first[4]);
-    int f = 0, m = pieces[0];
-#pragma unroll
-    for (int x = 1; x < kKinds; ++x)
-      if (kind == x) f = first[x], m = pieces[x];
-    e = (c - f) * 32 + lane;
-    if (e >= m || rows[t] < 0) e = -1 - e;
-  };
-  for (int base = warp; base < tasks; base += kWarps * kFly) {
+  // Tasks: a chunk of one kind of one token, the tokens of a chunk one after the other; a warp has kFly in a row at a time.
+  const int tasks = n * first[kKinds];
+  for (int base = warp * kFly; base < tasks; base += kWarps * kFly) {
     uint4 w[kFly];
+    int tok[kFly], piece[kFly];  // of each task; the piece -1 - e where this lane has none
+    int kinds = 0;               // 4 bits each
+    int c = base / n, t = base - c * n;
 #pragma unroll
     for (int u = 0; u < kFly; ++u) {
       w[u] = make_uint4(0u, 0u, 0u, 0u);
-      const int task = base + u * kWarps;
-      if (task >= tasks) continue;
-      int t, kind, e;
-      split(task, t, kind, e);
-      const uint16_t* src = kind == kQ ? a.q : kind == kK ? a.k : kind == kV ? a.v : kind == kQI ? a.q_idx : a.k_idx;
-      const int64_t stride = kind == kQ   ? a.q_stride
-                             : kind == kK ? a.k_stride
-                             : kind == kV ? a.v_stride
-                             : kind == kQI ? a.q_idx_stride
-                                           : a.k_idx_stride;
-      if (e >= 0) w[u] = ld_once(src + (i0 + t) * stride + e * 8);
+      if (base + u >= tasks) break;  // (uniform in the warp)
+      const int kind = (c >= first[1]) + (c >= first[2]) + (c >= first[3]) + (c >= first[4]);
+      int f = 0, m = pieces[0];
+      const uint16_t* src = a.q;
+      int64_t stride = a.q_stride;
+      if (kind == kK) f = first[kK], m = pieces[kK], src = a.k, stride = a.k_stride;
+      if (kind == kV) f = first[kV], m = pieces[kV], src = a.v, stride = a.v_stride;
+      if (kind == kQI) f = first[kQI], m = pieces[kQI], src = a.q_idx, stride = a.q_idx_stride;
+      if (kind == kKI) f = first[kKI], m = pieces[kKI], src = a.k_idx, stride = a.k_idx_stride;
+      const int e = (c - f) * 32 + lane;
+      const bool on = e < m && rows[t] >= 0;
+      if (on) w[u] = ld_once(src + (i0 + t) * stride + e * 8);
+      tok[u] = t;
+      piece[u] = on ? e : -1 - e;
+      kinds |= kind << (4 * u);
+      if (++t == n) t = 0, ++c;
     }
 #pragma unroll
     for (int u = 0; u < kFly; ++u) {
-      const int task = base + u * kWarps;
-      if (task >= tasks) break;
-      int t, kind, e;
-      split(task, t, kind, e);
-      const bool on = e >= 0;
-      if (!on) e = -1 - e;
+      if (base + u >= tasks) break;
+      const int kind = kinds >> (4 * u) & 15, t = tok[u];
+      const bool on = piece[u] >= 0, idx = kind >= kQI;
+      const int e = on ? piece[u] : -1 - piece[u];
       if (kind != kV) {
-        const bool idx = kind >= kQI;
         const int lanes = idx ? li : LPR;
-        float v[8];
-        widen8(w[u], v);
-        turn8(v, e & (lanes - 1), lanes, idx ? a.rope_idx : a.rope, cs[idx] + 2 * t * kSpan, kSpan);
-        w[u] = narrow8(v);
+        w[u] = turn8_bf16(w[u], e & (lanes - 1), lanes, idx ? a.rope_idx : a.rope, cs[idx] + 2 * t * kSpan, kSpan);
       }
       const int64_t row = rows[t];
       if (kind == kK || kind == kV) {
@@ -275,7 +305,6 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64
           *reinterpret_cast<uint4*>((kind == kV ? v_pool : k_pool) + row * (a.H_kv * D) + e * 8) = w[u];
         }
       } else if (on) {
-        const bool idx = kind != kQ;
         const int64_t at = kind == kQ    ? (i0 + t) * (a.H_q * D) + e * 8
                            : kind == kQI ? (i0 + t) * (a.H_kv * a.d_I) + e * 8
                                          : row * a.d_I + e * 8;

@@ -813,7 +813,8 @@ struct Row {
   }
 };
 
-// A warp a row (node, head): its partials of the context merged, then the drafts that it sees one after the other.
+// A warp a row (node, head) at a time: the drafts that it sees, then (once the context kernel has ended) the partials of
+// its context.
 template <int D, bool KV4>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, const int32_t* __restrict__ parents,
                                                                  const uint16_t* __restrict__ qp, const uint16_t* __restrict__ k_pool,
@@ -844,8 +845,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
       at[tid] = (int64_t)pp * map.page + (t - lp * map.page);
     }
   }
-  __syncthreads();
-  if (bad) bad_s = 1;
+  if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && tid == 0) bad_s = 1;
   // who is above whom, in doubling steps
   for (int i = 0, far = 1; far < T; far <<= 1, i ^= 1) {
     uint64_t s = 0;
@@ -864,33 +864,82 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
     }
     __syncthreads();
   }
-  griddep_wait();  // the partials
-  __syncthreads();
-  if (bad_s && g == 0 && blockIdx.y == 0 && tid == 0) raise_error(st, kErrBadIndex, 13u);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int c = tid; c < n_cta; c += kJoinThreads)
-      if (w.errors[c]) raise_error(st, w.errors[c], 3u);
-  const int64_t quota = run_quota(w.starts[sh.B], sh.groups);
+  const float kInf = __int_as_float(0x7f800000);
   const int tiles = sh.tiles(b);
-  const int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * rows_per_warp;
-  for (int r = r0; r < r0 + rows_per_warp; ++r) {
-    const int i = r / sh.gs, hh = r % sh.gs;
-    if (i >= T) break;
+  const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // rows of partials from group to group
+  int c0 = 0, c1 = -1;                                   // the groups that had a part of the sequence
+  bool waited = false;
+  const int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * rows_per_warp, r1 = min(r0 + rows_per_warp, T * sh.gs);
+  for (int r = r0; r < max(r1, r0 + 1); ++r) {
+    const int i = min(r, r1 - 1) / sh.gs, hh = r % sh.gs;
+    const bool on = r < r1;  // (a warp without a row waits for the partials' grid all the same)
     const int64_t row = ((int64_t)b * sh.T + i) * (sh.H_kv * sh.gs) + g * sh.gs + hh;
-    float M = -__int_as_float(0x7f800000), Lsum = 0.f, acc[V], q[V];
+    float M = -kInf, Lsum = 0.f, acc[V], q[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    {
+    if (on) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + row * D) + lane * (V / 2);
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) q[2 * e] = bf16_lo(p[e]) * scale_log2, q[2 * e + 1] = bf16_hi(p[e]) * scale_log2;
     }
-    const float kInf = __int_as_float(0x7f800000);
-    if (tiles) {
+    for (uint64_t left = on ? sees[i] : 0ull; left;) {  // four drafts at a time
+      float k[4][V], v[4][V], s[4];
+      int n = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        s[u] = 0.f;
+        const int j = left ? __ffsll((long long)left) - 1 : 0;
+        if (left) {
+          left &= left - 1;
+          ++n;
+          Row<D, KV4>::load(k_pool, pool.k_codes, pool.k_scales, at[j], sh.H_kv, g, k[u]);
+          Row<D, KV4>::load(v_pool, pool.v_codes, pool.v_scales, at[j], sh.H_kv, g, v[u]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) k[u][e] = v[u][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[u] = fmaf(q[e], k[u][e], s[u]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u >= n) s[u] = -kInf;
+      const float m = fmaxf(M, fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]))), mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
+      const float old = M == m ? 1.f : ex2_approx(M - mz);
+      Lsum *= old;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= old;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float pr = ex2_approx(s[u] - mz);
+        Lsum += pr;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(pr, v[u][e], acc[e]);
+      }
+      M = m;
+    }
+    if (!waited) {
+      waited = true;
+      griddep_wait();  // the partials
+      if (tid == 0 && bad_s) raise_error(st, kErrBadIndex, 13u);
+      if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int c = tid; c < n_cta; c += kJoinThreads)
+          if (w.errors[c]) raise_error(st, w.errors[c], 3u);
+      if (tiles) {
+        const int64_t quota = run_quota(w.starts[sh.B], sh.groups), f0 = w.starts[b];
+        c0 = (int)(f0 / quota);
+        c1 = (int)((f0 + tiles - 1) / quota);
+      }
+    }
+    if (!on) break;
+    {
       const int rg = r / sh.RU, unit = g * sh.RG + rg;
-      const int64_t f0 = w.starts[b];
-      const int c0 = (int)(f0 / quota), c1 = (int)((f0 + tiles - 1) / quota);
-      const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // from group to group
       const int64_t s0 = b * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
       for (int c = c0; c <= c1; c += 4) {  // four partials in flight
         float2 ml[4];
@@ -927,33 +976,6 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
           for (int e = 0; e < V; ++e) acc[e] += x[u][e] * wt;
         }
       }
-    }
-    for (uint64_t left = sees[i]; left; ) {  // two drafts at a time
-      const int j0 = __ffsll((long long)left) - 1;
-      left &= left - 1;
-      const bool pair = left != 0;
-      const int j1 = pair ? __ffsll((long long)left) - 1 : j0;
-      left &= left - 1;
-      float k0[V], k1[V], v0[V], v1[V];
-      Row<D, KV4>::load(k_pool, pool.k_codes, pool.k_scales, at[j0], sh.H_kv, g, k0);
-      Row<D, KV4>::load(k_pool, pool.k_codes, pool.k_scales, at[j1], sh.H_kv, g, k1);
-      Row<D, KV4>::load(v_pool, pool.v_codes, pool.v_scales, at[j0], sh.H_kv, g, v0);
-      Row<D, KV4>::load(v_pool, pool.v_codes, pool.v_scales, at[j1], sh.H_kv, g, v1);
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) s0 = fmaf(q[e], k0[e], s0), s1 = fmaf(q[e], k1[e], s1);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o), s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-      if (!pair) s1 = -kInf;
-      const float m = fmaxf(M, fmaxf(s0, s1)), mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
-      const float old = M == m ? 1.f : ex2_approx(M - mz), p0 = ex2_approx(s0 - mz), p1 = ex2_approx(s1 - mz);
-      Lsum = Lsum * old + (p0 + p1);
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(p0, v0[e], acc[e] * old);
-      if (pair)
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(p1, v1[e], acc[e]);
-      M = m;
     }
     const bool any = Lsum > 0.f || Lsum != Lsum;  // scores of -inf alone weigh nothing: out 0, lse -inf
     const float inv = any ? 1.f / Lsum : 0.f;
@@ -1031,9 +1053,10 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
                                                      KV4 ? sl2 * kSubUnscale : sl2, w, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int R = p.T * gs;
-  // a row a warp while that leaves the GPU room
+  // a warp has as many rows as it takes for four CTAs an SM (a CTA's beginning, pages and branches, costs as much as some rows)
   const int64_t rows = (int64_t)p.B * p.H_kv * R;
-  const int rows_per_warp = rows >= (int64_t)n_cta * 8 * 32 ? 4 : 1, per_cta = kJoinThreads / 32 * rows_per_warp;
+  const int64_t most = rows / ((int64_t)4 * n_cta * (kJoinThreads / 32));
+  const int rows_per_warp = most < 1 ? 1 : most > 32 ? 32 : (int)most, per_cta = kJoinThreads / 32 * rows_per_warp;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.H_kv), (unsigned)((R + per_cta - 1) / per_cta));
   cfg.blockDim = dim3(kJoinThreads);
