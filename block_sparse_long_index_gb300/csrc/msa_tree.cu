@@ -5,8 +5,7 @@
 //
 // The two parts are worked out apart, as partial softmaxes (O, maximum, sum).  The context needs no mask: all rows of a
 // (sequence, K/V head) see all of it, T gs rows that share every key, a matrix product.  A node's own branch is a
-// handful of keys that differ from row to row; the kernel that joins the partials adds it key by key in fp32, and keys
-// that a node does not see are never touched, whatever they hold.
+// handful of keys that differ from row to row, at most 64 in all: the kernel that joins the partials does it.
 //
 // The context: all sequences' 128-token tiles are one list, whatever the lengths are; a CTA has one unit (K/V head, and
 // group of rows where they are many) and an equal run of the list.  The CTAs of all units take the same runs at the same
@@ -785,52 +784,41 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
 }
 
 // ---------------------------------------------------------------- the drafts' own part, and joining the partials
-// 4 (d = 128) or 2 channels of a cached head row, as a lane of a warp holds them.
-template <int D, bool KV4>
-struct Row {
-  static constexpr int V = D / 32;
-  __device__ static __forceinline__ void load(const uint16_t* bf, const uint8_t* codes, const uint8_t* scales, int64_t row, int H_kv,
-                                              int g, float (&x)[V]) {
-    const int lane = threadIdx.x & 31;
-    const int64_t hr = row * H_kv + g;
-    if constexpr (!KV4) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(bf + hr * D) + lane * (V / 2);
-      if constexpr (V == 4) {
-        const uint2 y = *reinterpret_cast<const uint2*>(p);
-        x[0] = bf16_lo(y.x), x[1] = bf16_hi(y.x), x[2] = bf16_lo(y.y), x[3] = bf16_hi(y.y);
-      } else {
-        const uint32_t y = *p;
-        x[0] = bf16_lo(y), x[1] = bf16_hi(y);
-      }
-    } else {
-      // channel c of a word sits in nibble c / 2 + 4 (c % 2)
-      const uint32_t y = reinterpret_cast<const uint32_t*>(codes + hr * (D / 2))[lane * V / 8] >> (V == 4 ? 8 * (lane & 1) : 4 * (lane & 3));
-      const uint32_t b = scales[hr * kGroups + lane / 8];
-      const float s = b == kScaleNaN ? __uint_as_float(0x7FFFFFFFu) : scale_f32(b);
-      x[0] = (float)((int)(y & 15u) - 8) * s, x[1] = (float)((int)(y >> 16 & 15u) - 8) * s;
-      if constexpr (V == 4) x[2] = (float)((int)(y >> 4 & 15u) - 8) * s, x[3] = (float)((int)(y >> 20 & 15u) - 8) * s;
-    }
-  }
+// A CTA has 16 to 64 rows (node, head) of a (sequence, K/V head).  The drafts' K and V go to shared memory as bf16; a warp
+// for each 16 rows works out their softmax over the drafts that they see with mma.sync (m16n8k16; rows of T gs and at most 64
+// keys do not fill a tcgen05 tile).  Then, once the context kernel has ended, a warp a row joins that with the row's partials,
+// four of which are in flight at a time.  (With a warp a row for the drafts too, key by key in fp32, 16 trees of 64 nodes
+// took 70 us here instead of 43, with a cold L2.)
+// V's values that are not finite are taken out of shared memory, so that a weight of 0 leaves them out, and added for the rows
+// that see them.
+template <int D>
+struct JoinLayout {
+  static constexpr int ROW = D * 2, KV = kMaxT * ROW;  // bytes of a head row, of the drafts' K or V
+  __host__ __device__ static constexpr int smem(int tiles) { return 2 * KV + tiles * 16 * (D * 4 + 8); }
 };
 
-// A warp a row (node, head) at a time: the drafts that it sees, then (once the context kernel has ended) the partials of
-// its context.
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, const int32_t* __restrict__ parents,
-                                                                 const uint16_t* __restrict__ qp, const uint16_t* __restrict__ k_pool,
-                                                                 const uint16_t* __restrict__ v_pool, Kv4Pool pool, CacheMap map,
-                                                                 int n_cta, int rows_per_warp, float scale_log2, TreeScratch w,
-                                                                 uint16_t* __restrict__ out, float* __restrict__ lse, DeviceStatus* st) {
-  constexpr int V = D / 32;
+__global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh, const int32_t* __restrict__ parents,
+                                                                    const uint16_t* __restrict__ qp, const uint16_t* __restrict__ k_pool,
+                                                                    const uint16_t* __restrict__ v_pool, Kv4Pool pool, CacheMap map,
+                                                                    int n_cta, int m_tiles, float scale_log2, TreeScratch w,
+                                                                    uint16_t* __restrict__ out, float* __restrict__ lse, DeviceStatus* st) {
+  using J = JoinLayout<D>;
+  constexpr int V = D / 32, CH = D / 8;  // channels of a lane when a row is joined, 16-byte pieces of a row
+  extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int64_t at[kMaxT];  // cache rows of the drafts
   __shared__ uint64_t sees[kMaxT];
   __shared__ int up[2][kMaxT];
   __shared__ int bad_s;
+  __shared__ unsigned long long wild_s;  // drafts whose V holds values that are not finite
+  float* o_s = reinterpret_cast<float*>(sm + 2 * J::KV);                  // [16 m_tiles][D]
+  float2* ml_s = reinterpret_cast<float2*>(sm + 2 * J::KV + m_tiles * 16 * D * 4);  // [16 m_tiles]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / sh.H_kv, g = blockIdx.x % sh.H_kv;
+  const int r_cta = blockIdx.y * 16 * m_tiles;  // the CTA's first row
   int n, T;
   bool bad = !sh.lengths(b, n, T);
-  if (tid == 0) bad_s = 0;
+  if (tid == 0) bad_s = 0, wild_s = 0ull;
   if (tid < kMaxT) {
     sees[tid] = 0;
     up[0][tid] = -1;
@@ -846,6 +834,35 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
     }
   }
   if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && tid == 0) bad_s = 1;
+  // ---- K and V of the drafts, 16-byte pieces: K's piece x of row r at x ^ 4 (r & 1), V's at x ^ (r & 7); rows past T are zeros
+  const int Tp = (T + 15) & ~15;
+  for (int x = tid; x < 2 * Tp * CH; x += kJoinThreads) {
+    const bool is_v = x >= Tp * CH;
+    const int y = is_v ? x - Tp * CH : x, r = y / CH, ch = y % CH;
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+    if (r < T) {
+      const int64_t hr = at[r] * sh.H_kv + g;
+      if constexpr (!KV4) {
+        c = *reinterpret_cast<const uint4*>((is_v ? v_pool : k_pool) + hr * D + ch * 8);
+      } else {
+        const uint32_t code = reinterpret_cast<const uint32_t*>((is_v ? pool.v_codes : pool.k_codes) + hr * (D / 2))[ch];
+        const uint32_t s1 = scale_bf16((is_v ? pool.v_scales : pool.k_scales)[hr * kGroups + ch / (CH / kGroups)]), s2 = s1 | (s1 << 16);
+        c = expand8(code, s2, scale_bias(s2));
+      }
+      if (is_v) {
+        uint32_t v[4] = {c.x, c.y, c.z, c.w};
+        bool wild = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((v[j] & 0x7F80u) == 0x7F80u) v[j] &= 0xFFFF0000u, wild = true;
+          if ((v[j] & 0x7F800000u) == 0x7F800000u) v[j] &= 0x0000FFFFu, wild = true;
+        }
+        if (wild) atomicOr(&wild_s, 1ull << r);
+        c = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(sm + (is_v ? J::KV : 0) + r * J::ROW + ((ch ^ (is_v ? r & 7 : (r & 1) << 2)) << 4)) = c;
+  }
   // who is above whom, in doubling steps
   for (int i = 0, far = 1; far < T; far <<= 1, i ^= 1) {
     uint64_t s = 0;
@@ -864,124 +881,176 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeShape sh, c
     }
     __syncthreads();
   }
+  __syncthreads();
   const float kInf = __int_as_float(0x7f800000);
+  const int rows = T * sh.gs;
+  const int64_t first_row = (int64_t)b * sh.T * (sh.H_kv * sh.gs) + g * sh.gs;  // row r is first_row + (r / gs) H_q + r % gs
+  const int H_q = sh.H_kv * sh.gs;
+  if (warp < m_tiles && r_cta + warp * 16 < rows) {
+    // ---- 16 rows over the drafts: a lane has rows lane / 4 and 8 more, channels and keys by lane % 4
+    const int r = lane >> 2, c = lane & 3;
+    uint32_t qf[2][D / 8];  // channels 8 (4 t + c) .. + 7 of both rows: two steps of 16 each
+    uint64_t mask[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = r_cta + warp * 16 + r + 8 * e;
+      mask[e] = rr < rows ? sees[rr / sh.gs] : 0ull;
+      const uint16_t* p = qp + (first_row + (int64_t)(rr / sh.gs) * H_q + rr % sh.gs) * D;
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t) {
+        const uint4 y = rr < rows ? *reinterpret_cast<const uint4*>(p + (4 * t + c) * 8) : make_uint4(0u, 0u, 0u, 0u);
+        qf[e][4 * t] = y.x, qf[e][4 * t + 1] = y.y, qf[e][4 * t + 2] = y.z, qf[e][4 * t + 3] = y.w;
+      }
+    }
+    float s[kMaxT / 8][4], M[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kMaxT / 8; ++j) {
+      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if (8 * j < Tp) {
+        const uint8_t* kr = sm + (8 * j + r) * J::ROW;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) {
+          const uint4 y = *reinterpret_cast<const uint4*>(kr + (((4 * t + c) ^ ((r & 1) << 2)) << 4));
+          const uint32_t a0[4] = {qf[0][4 * t], qf[1][4 * t], qf[0][4 * t + 1], qf[1][4 * t + 1]}, b0[2] = {y.x, y.y};
+          const uint32_t a1[4] = {qf[0][4 * t + 2], qf[1][4 * t + 2], qf[0][4 * t + 3], qf[1][4 * t + 3]}, b1[2] = {y.z, y.w};
+          mma_bf16_16816(s[j], a0, b0);
+          mma_bf16_16816(s[j], a1, b1);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bool on = mask[x >> 1] >> (8 * j + 2 * c + (x & 1)) & 1ull;
+          s[j][x] = on ? s[j][x] * scale_log2 : -kInf;
+          M[x >> 1] = fmaxf(M[x >> 1], s[j][x]);
+        }
+      }
+    }
+    float mz[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      M[e] = fmaxf(M[e], __shfl_xor_sync(0xffffffffu, M[e], 1));
+      M[e] = fmaxf(M[e], __shfl_xor_sync(0xffffffffu, M[e], 2));
+      mz[e] = M[e] == -kInf ? 0.f : M[e];  // scores of -inf alone weigh 0
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < kMaxT / 16; ++kk) {
+      if (16 * kk >= Tp) break;
+      uint32_t pa[4];  // weights of 16 keys: row r, row r + 8, each keys 2 c and 8 more
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p0 = ex2_approx(s[2 * kk + y][2 * e] - mz[e]), p1 = ex2_approx(s[2 * kk + y][2 * e + 1] - mz[e]);
+          l[e] += p0 + p1;
+          pa[2 * y + e] = pack_bf16x2(p0, p1);
+        }
+      const int vr = 16 * kk + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t v[4];
+        ldmatrix_x4_trans(v[0], v[1], v[2], v[3], sm + J::KV + vr * J::ROW + (((2 * j + (lane >> 4)) ^ (vr & 7)) << 4));
+        const uint32_t b0[2] = {v[0], v[1]}, b1[2] = {v[2], v[3]};
+        mma_bf16_16816(acc[2 * j], pa, b0);
+        mma_bf16_16816(acc[2 * j + 1], pa, b1);
+      }
+    }
+    if (wild_s) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        for (uint64_t left = mask[e] & wild_s; left; left &= left - 1) {
+          const int64_t hr = at[__ffsll((long long)left) - 1] * sh.H_kv + g;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int ch = 8 * j + 2 * c + x;
+              float v;
+              if constexpr (KV4) v = pool.v_scales[hr * kGroups + ch / (D / kGroups)] == kScaleNaN ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+              else v = __uint_as_float((uint32_t)v_pool[hr * D + ch] << 16);
+              if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) acc[j][2 * e + x] += v;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      const int lr = warp * 16 + r + 8 * e;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) *reinterpret_cast<float2*>(o_s + lr * D + 8 * j + 2 * c) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+      if (c == 0) ml_s[lr] = make_float2(M[e], l[e]);
+    }
+  }
+  __syncthreads();
+  griddep_wait();  // the partials
+  if (tid == 0 && bad_s) raise_error(st, kErrBadIndex, 13u);
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int c = tid; c < n_cta; c += kJoinThreads)
+      if (w.errors[c]) raise_error(st, w.errors[c], 3u);
   const int tiles = sh.tiles(b);
   const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // rows of partials from group to group
   int c0 = 0, c1 = -1;                                   // the groups that had a part of the sequence
-  bool waited = false;
-  const int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * rows_per_warp, r1 = min(r0 + rows_per_warp, T * sh.gs);
-  for (int r = r0; r < max(r1, r0 + 1); ++r) {
-    const int i = min(r, r1 - 1) / sh.gs, hh = r % sh.gs;
-    const bool on = r < r1;  // (a warp without a row waits for the partials' grid all the same)
-    const int64_t row = ((int64_t)b * sh.T + i) * (sh.H_kv * sh.gs) + g * sh.gs + hh;
-    float M = -kInf, Lsum = 0.f, acc[V], q[V];
+  if (tiles) {
+    const int64_t quota = run_quota(w.starts[sh.B], sh.groups), f0 = w.starts[b];
+    c0 = (int)(f0 / quota);
+    c1 = (int)((f0 + tiles - 1) / quota);
+  }
+  for (int lr = warp; lr < 16 * m_tiles; lr += kJoinThreads / 32) {
+    const int r = r_cta + lr;
+    if (r >= rows) break;
+    float acc[V];
+    float2 own = ml_s[lr];
+    float M = own.x, Lsum = own.y;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (on) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + row * D) + lane * (V / 2);
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) q[2 * e] = bf16_lo(p[e]) * scale_log2, q[2 * e + 1] = bf16_hi(p[e]) * scale_log2;
-    }
-    for (uint64_t left = on ? sees[i] : 0ull; left;) {  // four drafts at a time
-      float k[4][V], v[4][V], s[4];
-      int n = 0;
+    for (int e = 0; e < V; ++e) acc[e] = o_s[lr * D + lane * V + e];
+    const int rg = r / sh.RU, unit = g * sh.RG + rg;
+    const int64_t s0 = b * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
+    for (int c = c0; c <= c1; c += 4) {  // four partials in flight
+      float2 ml[4];
+      float x[4][V];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        s[u] = 0.f;
-        const int j = left ? __ffsll((long long)left) - 1 : 0;
-        if (left) {
-          left &= left - 1;
-          ++n;
-          Row<D, KV4>::load(k_pool, pool.k_codes, pool.k_scales, at[j], sh.H_kv, g, k[u]);
-          Row<D, KV4>::load(v_pool, pool.v_codes, pool.v_scales, at[j], sh.H_kv, g, v[u]);
-        } else {
+        ml[u] = make_float2(-kInf, 0.f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) k[u][e] = v[u][e] = 0.f;
+        for (int e = 0; e < V; ++e) x[u][e] = 0.f;
+        if (c + u <= c1) {
+          const int64_t s = s0 + (c + u) * per;
+          ml[u] = w.part_ml[s];
+          const float* p = w.part_o + s * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            x[u][0] = y.x, x[u][1] = y.y, x[u][2] = y.z, x[u][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            x[u][0] = y.x, x[u][1] = y.y;
+          }
         }
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[u] = fmaf(q[e], k[u][e], s[u]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u >= n) s[u] = -kInf;
-      const float m = fmaxf(M, fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]))), mz = m == -kInf ? 0.f : m;  // scores of -inf alone weigh 0
-      const float old = M == m ? 1.f : ex2_approx(M - mz);
+      const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+      const float old = M == m ? 1.f : ex2_approx(M - m);
       Lsum *= old;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] *= old;
+      M = m;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float pr = ex2_approx(s[u] - mz);
-        Lsum += pr;
+        const float wt = ml[u].x == m ? 1.f : ex2_approx(ml[u].x - m);
+        Lsum += ml[u].y * wt;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(pr, v[u][e], acc[e]);
-      }
-      M = m;
-    }
-    if (!waited) {
-      waited = true;
-      griddep_wait();  // the partials
-      if (tid == 0 && bad_s) raise_error(st, kErrBadIndex, 13u);
-      if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int c = tid; c < n_cta; c += kJoinThreads)
-          if (w.errors[c]) raise_error(st, w.errors[c], 3u);
-      if (tiles) {
-        const int64_t quota = run_quota(w.starts[sh.B], sh.groups), f0 = w.starts[b];
-        c0 = (int)(f0 / quota);
-        c1 = (int)((f0 + tiles - 1) / quota);
-      }
-    }
-    if (!on) break;
-    {
-      const int rg = r / sh.RU, unit = g * sh.RG + rg;
-      const int64_t s0 = b * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
-      for (int c = c0; c <= c1; c += 4) {  // four partials in flight
-        float2 ml[4];
-        float x[4][V];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          ml[u] = make_float2(-kInf, 0.f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[u][e] = 0.f;
-          if (c + u <= c1) {
-            const int64_t s = s0 + (c + u) * per;
-            ml[u] = w.part_ml[s];
-            const float* p = w.part_o + s * D + lane * V;
-            if constexpr (V == 4) {
-              const float4 y = *reinterpret_cast<const float4*>(p);
-              x[u][0] = y.x, x[u][1] = y.y, x[u][2] = y.z, x[u][3] = y.w;
-            } else {
-              const float2 y = *reinterpret_cast<const float2*>(p);
-              x[u][0] = y.x, x[u][1] = y.y;
-            }
-          }
-        }
-        const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-        const float old = M == m ? 1.f : ex2_approx(M - m);
-        Lsum *= old;
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] *= old;
-        M = m;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float wt = ml[u].x == m ? 1.f : ex2_approx(ml[u].x - m);
-          Lsum += ml[u].y * wt;
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] += x[u][e] * wt;
-        }
+        for (int e = 0; e < V; ++e) acc[e] += x[u][e] * wt;
       }
     }
     const bool any = Lsum > 0.f || Lsum != Lsum;  // scores of -inf alone weigh nothing: out 0, lse -inf
     const float inv = any ? 1.f / Lsum : 0.f;
-    uint32_t* op = reinterpret_cast<uint32_t*>(out + row * D) + lane * (V / 2);
+    const int64_t row = first_row + (int64_t)(r / sh.gs) * H_q + r % sh.gs;
+    uint32_t y[V / 2];
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) op[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int e = 0; e < V / 2; ++e) y[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    uint32_t* op = reinterpret_cast<uint32_t*>(out + row * D) + lane * (V / 2);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(op) = make_uint2(y[0], y[1]);
+    else *op = y[0];
     if (lane == 0 && lse) lse[row] = any ? (M + log2f(Lsum)) * 0.69314718055994530942f : -kInf;
   }
 }
@@ -1053,12 +1122,15 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
                                                      KV4 ? sl2 * kSubUnscale : sl2, w, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int R = p.T * gs;
-  // a warp has as many rows as it takes for four CTAs an SM (a CTA's beginning, pages and branches, costs as much as some rows)
-  const int64_t rows = (int64_t)p.B * p.H_kv * R;
-  const int64_t most = rows / ((int64_t)4 * n_cta * (kJoinThreads / 32));
-  const int rows_per_warp = most < 1 ? 1 : most > 32 ? 32 : (int)most, per_cta = kJoinThreads / 32 * rows_per_warp;
+  // tiles of 16 rows a CTA: more than one where that leaves two CTAs an SM
+  const int64_t tiles16 = (int64_t)p.B * p.H_kv * ((R + 15) / 16);
+  const int m_tiles = tiles16 >= (int64_t)8 * n_cta ? 4 : tiles16 >= (int64_t)4 * n_cta ? 2 : 1;
+  auto join = tree_join_kernel<D, KV4>;
+  e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, JoinLayout<D>::smem(4));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv), (unsigned)((R + per_cta - 1) / per_cta));
+  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv), (unsigned)((R + 16 * m_tiles - 1) / (16 * m_tiles)));
+  cfg.dynamicSmemBytes = JoinLayout<D>::smem(m_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1066,8 +1138,8 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, KV4>, sh, parents, (const uint16_t*)q, (const uint16_t*)k_pool,
-                            (const uint16_t*)v_pool, pool, map, n_cta, rows_per_warp, sl2, w, (uint16_t*)out, lse, st);
+  return cudaLaunchKernelEx(&cfg, join, sh, parents, (const uint16_t*)q, (const uint16_t*)k_pool,
+                            (const uint16_t*)v_pool, pool, map, n_cta, m_tiles, sl2, w, (uint16_t*)out, lse, st);
 }
 
 }  // namespace

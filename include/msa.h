@@ -648,8 +648,8 @@ msa_status_t msa_append_paged_kv4(const msa_append_t* rows, int64_t N, const int
  *   out        [B, T, H_q, d] bf16 out;  lse [B, T, H_q] fp32 out (nullable):
  *              natural-log log-sum-exp of the scaled scores.  Nodes past tree_len
  *              stay as they were.
- * Scores, softmax and sums are fp32; the probabilities of the context are
- * rounded to bf16 for the product with V.  Scores of -inf and NaN count as in
+ * Scores, softmax and sums are fp32; probabilities are rounded to bf16 for the
+ * product with V.  Scores of -inf and NaN count as in
  * msa_dense_prefill_varlen; drafts that a node does not see count for nothing,
  * whatever they hold.  The device error word (MSA_ERR_BAD_INDEX) is set by a
  * page id outside [0, n_pages) (page 0 is read), a parent outside [-1, j) (it
