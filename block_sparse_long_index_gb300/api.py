@@ -205,27 +205,27 @@ class Rope:
     def _set(self, freqs, interleaved, amplitude, device):
         self.rot, self.interleaved, self.amplitude = 2 * len(freqs), bool(interleaved), float(amplitude)
         self.turns = torch.tensor([_turns(float(f)) for f in freqs], dtype=torch.int64, device=device)
+        self.dev = self.turns.get_device()  # -1 on the CPU
         self.c = _c.rope(self.turns, self.rot, self.interleaved, self.amplitude)
 
     def __call__(self, x, positions, out=None, inverse=False, stream=None):
         """x [N, H, d] bf16 or fp32 turned by positions [N] int32 into `out` (x itself is allowed; a new tensor where it
         is None).  Heads are contiguous, rows may lie apart, as slices of a wider projection.  With `inverse` turned
         back: the gradient of x from that of the result."""
-        dev = _device(self.turns)
-        if x.dtype not in (torch.bfloat16, torch.float32):
+        dev, dtype, shape = _device(self.turns), x.dtype, x.shape
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
             raise ValueError("x has to be bfloat16 or float32")
-        if x.dim() != 3:
-            raise ValueError("x has shape %s, expected [N, H, d]" % (tuple(x.shape),))
-        N, H, d = x.shape
-        _check_rows("x", x, x.dtype, (N, H, d), dev)
+        if len(shape) != 3:
+            raise ValueError("x has shape %s, expected [N, H, d]" % (tuple(shape),))
+        N, H, d = shape
+        x_stride = _check_rows("x", x, dtype, shape, dev)
         _check_tensor("positions", positions, torch.int32, (N,), dev)
         if out is None:
-            with _allocating_for(stream):
-                out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
-        _check_rows("out", out, x.dtype, (N, H, d), dev)
+            out, stride = _new(x, shape, dtype, stream), H * d
+        else:
+            stride = _check_rows("out", out, dtype, shape, dev)
         if N:
-            _c.msa_rope(x, x.stride(0) if N > 1 else H * d, out, out.stride(0) if N > 1 else H * d, N, H, d,
-                        x.dtype == torch.float32, positions, self.c, inverse, stream=stream)
+            _c.msa_rope(x, x_stride, out, stride, N, H, d, dtype is torch.float32, positions, self.c, inverse, stream=stream)
         return out
 
 
@@ -242,25 +242,35 @@ def _turns(f):
 
 
 def _check_rows(name, t, dtype, shape, dev):
-    """t [N, ...] of the type and shape, on device number dev; each row contiguous, rows apart by any stride that holds one."""
+    """t [N, ...] of the type and shape, on device number dev; each row contiguous, rows apart by any stride that holds one.
+    Returns the elements from row to row."""
+    row = math.prod(shape[1:])
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return row
     if t.dtype != dtype or t.get_device() < 0:
         raise ValueError("%s must be a CUDA %s tensor" % (name, str(dtype).replace("torch.", "")))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.get_device() != dev:
         raise ValueError("%s is on cuda:%d, the object on cuda:%d" % (name, t.get_device(), dev))
-    row = 1
+    step = 1
     for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and s != row:
+        if n > 1 and s != step:
             raise ValueError("%s: the rows themselves must be contiguous" % name)
-        row *= n
-    if t.shape[0] > 1 and t.stride(0) < row:
+        step *= n
+    if t.shape[0] < 2:
+        return row
+    if t.stride(0) < row:
         raise ValueError("%s: rows must not overlap" % name)
+    return t.stride(0)
 
 
-def _row_stride(t):
-    """Elements from row to row of a checked tensor (one row: its own length)."""
-    return t.stride(0) if t.shape[0] > 1 else t.numel()
+def _new(like, shape, dtype, stream):
+    """An uninitialized contiguous tensor on like's device, from the memory of `stream` (see _allocating_for)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _allocating_for(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 class _Append:
@@ -275,62 +285,57 @@ class _Append:
         The index rows are turned by idx_rope (`rope` where it is None).  positions [N] int32: what rows are turned by
         where it is not their place in the cache.  Rows of the inputs may lie apart, as slices of a wider projection.
         See msa_append_paged."""
-        N, S, dev = k.shape[0], cu_seqlens.numel() - 1, _device(self.workspace)
-        _check_rows("k", k, torch.bfloat16, (N, self.H_kv, self.d), dev)
-        _check_rows("v", v, torch.bfloat16, (N, self.H_kv, self.d), dev)
+        N, S, dev = k.shape[0], cu_seqlens.shape[0] - 1, _device(self.workspace)
+        shape, bf16 = (N, self.H_kv, self.d), torch.bfloat16
+        k_stride, v_stride = _check_rows("k", k, bf16, shape, dev), _check_rows("v", v, bf16, shape, dev)
+        max_pages = page_table.shape[-1]
         _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
         _check_tensor("pos0", pos0, torch.int32, (S,), dev)
-        _check_tensor("page_table", page_table, torch.int32, (S, page_table.shape[-1]), dev)
+        _check_tensor("page_table", page_table, torch.int32, (S, max_pages), dev)
         if positions is not None:
             _check_tensor("positions", positions, torch.int32, (N,), dev)
         for name, r in (("rope", rope), ("idx_rope", idx_rope)):
-            if r is not None and r.turns.get_device() != dev:
-                raise ValueError("%s is on cuda:%d, the object on cuda:%d" % (name, r.turns.get_device(), dev))
-        rows = _c.msa_append_t()
-        rows.k, rows.v, rows.k_stride, rows.v_stride = k.data_ptr(), v.data_ptr(), _row_stride(k), _row_stride(v)
-        if positions is not None:
-            rows.positions = positions.data_ptr()
-        f8 = False
+            if r is not None and r.dev != dev:
+                raise ValueError("%s is on device %d, the object on cuda:%d" % (name, r.dev, dev))
+        f8, q_stride, H_q, d_I, q_idx_stride, k_idx_stride = False, 0, 0, 0, 0, 0
+        if q is not None:
+            if q.dim() != 3 or q.shape[2] != self.d:
+                raise ValueError("q has shape %s, expected [N, H_q, %d]" % (tuple(q.shape), self.d))
+            H_q = q.shape[1]
+            q_stride = _check_rows("q", q, bf16, (N, H_q, self.d), dev)
+            if q_out is None:
+                q_out = _new(q, q.shape, bf16, stream)
+            else:
+                _check_tensor("q_out", q_out, bf16, q.shape, dev)
         if k_idx is not None:
             if k_idx_pool is None:
                 raise ValueError("k_idx needs k_idx_pool")
-            f8 = k_idx_pool.dtype == torch.uint8
+            f8, d_I = k_idx_pool.dtype is torch.uint8, k_idx.shape[-1]
+            k_idx_stride = _check_rows("k_idx", k_idx, bf16, (N, d_I), dev)
+            _check_tensor("k_idx_pool", k_idx_pool, torch.uint8 if f8 else bf16, (self.n_pages, self.page_size, d_I), dev)
         elif k_idx_pool is not None:
             raise ValueError("k_idx_pool needs k_idx")
         elif q_idx_out is not None:
-            f8 = q_idx_out.dtype == torch.uint8
-        if q is not None:
-            _check_rows("q", q, torch.bfloat16, (N,) + tuple(q.shape[1:]), dev)
-            if q.dim() != 3 or q.shape[2] != self.d:
-                raise ValueError("q has shape %s, expected [N, H_q, %d]" % (tuple(q.shape), self.d))
-            q_out = self._fresh(q.shape, torch.bfloat16, q_out, "q_out", dev, stream)
-            rows.q, rows.q_stride, rows.q_out, rows.H_q = q.data_ptr(), _row_stride(q), q_out.data_ptr(), q.shape[1]
-        if k_idx is not None:
-            d_I = k_idx.shape[-1]
-            _check_rows("k_idx", k_idx, torch.bfloat16, (N, d_I), dev)
-            _check_tensor("k_idx_pool", k_idx_pool, torch.uint8 if f8 else torch.bfloat16, (self.n_pages, self.page_size, d_I), dev)
-            rows.k_idx, rows.k_idx_stride, rows.k_idx_pool, rows.d_I = k_idx.data_ptr(), _row_stride(k_idx), k_idx_pool.data_ptr(), d_I
+            f8 = q_idx_out.dtype is torch.uint8
         if q_idx is not None:
-            d_I = q_idx.shape[-1]
-            if k_idx is not None and d_I != k_idx.shape[-1]:
+            if k_idx is not None and d_I != q_idx.shape[-1]:
                 raise ValueError("q_idx and k_idx differ in d_I")
-            _check_rows("q_idx", q_idx, torch.bfloat16, (N, self.H_kv, d_I), dev)
-            q_idx_out = self._fresh(q_idx.shape, torch.uint8 if f8 else torch.bfloat16, q_idx_out, "q_idx_out", dev, stream)
-            rows.q_idx, rows.q_idx_stride, rows.q_idx_out, rows.d_I = q_idx.data_ptr(), _row_stride(q_idx), q_idx_out.data_ptr(), d_I
-        rows.idx_f8, rows.idx_scale = int(f8), float(idx_scale)
-        idx_rope = None if k_idx is None and q_idx is None else rope if idx_rope is None else idx_rope
+            d_I, held = q_idx.shape[-1], torch.uint8 if f8 else bf16
+            q_idx_stride = _check_rows("q_idx", q_idx, bf16, (N, self.H_kv, d_I), dev)
+            if q_idx_out is None:
+                q_idx_out = _new(q_idx, q_idx.shape, held, stream)
+            else:
+                _check_tensor("q_idx_out", q_idx_out, held, q_idx.shape, dev)
         if N:
-            self._append(rows, N, cu_seqlens, S, pos0, page_table, page_table.shape[1], self.c, None if rope is None else rope.c,
+            at = _c._ptr
+            has_q, has_qi = q is not None, q_idx is not None
+            rows = _c.msa_append_t(at(q), at(k), at(v), at(q_idx), at(k_idx), q_stride, k_stride, v_stride, q_idx_stride, k_idx_stride,
+                                   at(q_out) if has_q else None, at(q_idx_out) if has_qi else None, at(k_idx_pool), at(positions), H_q,
+                                   d_I, f8, idx_scale)
+            idx_rope = None if k_idx is None and q_idx is None else rope if idx_rope is None else idx_rope
+            self._append(rows, N, cu_seqlens, S, pos0, page_table, max_pages, self.c, None if rope is None else rope.c,
                          None if idx_rope is None else idx_rope.c, self.workspace, stream=stream)
         return q_out if q is not None else None, q_idx_out if q_idx is not None else None
-
-    @staticmethod
-    def _fresh(shape, dtype, out, name, dev, stream):
-        if out is None:
-            with _allocating_for(stream):
-                return torch.empty(tuple(shape), dtype=dtype, device="cuda:%d" % dev)
-        _check_tensor(name, out, dtype, tuple(shape), dev)
-        return out
 
 
 class KvPool(_Append):

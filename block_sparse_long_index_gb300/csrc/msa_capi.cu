@@ -780,6 +780,7 @@ static msa_status_t append_impl(const msa_append_t* r, int64_t N, const int32_t*
   a.idx_scale = r->idx_scale;
   a.rope = rope_view(rope);
   a.rope_idx = rope_view(rope_idx);
+  a.rope_idx_own = rope_idx && !(rope && rope_idx->turns == rope->turns && rope_idx->rot == rope->rot && rope_idx->factor == rope->factor);
   return finish(msa::launch_append(a, N, cu_seqlens, S, pos0, page_table, max_pages, k_pool, v_pool, kv4, n_pages, page, d,
                                    (msa::DeviceStatus*)workspace, s));
 }

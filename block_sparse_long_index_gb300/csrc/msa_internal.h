@@ -224,6 +224,7 @@ struct AppendRows {
   int H_q, H_kv, d_I, idx_f8;
   float idx_scale;
   Rope rope, rope_idx;
+  bool rope_idx_own;  // rope_idx turns, and by another table than rope
 };
 cudaError_t launch_rope(const void* x, int64_t x_stride, void* y, int64_t y_stride, int64_t N, int H, int d, bool f32,
                         const int32_t* positions, const Rope& rope, bool inverse, cudaStream_t s);

@@ -222,9 +222,70 @@ __global__ void __launch_bounds__(kRowThreads) rope_kernel(const T* __restrict__
 }
 
 // ---------------------------------------------------------------- rows into a paged cache
-// What a token's rows are made of, in pieces of 8 channels: a warp takes 32 pieces of one kind at a time, so that the
-// kinds' branches are uniform.
-enum Kind { kQ, kK, kV, kQI, kKI, kKinds };
+// What a token's rows are made of, in pieces of 8 channels: a warp takes 32 pieces of one kind of a token at a time (a
+// chunk), with kFly tokens' in flight.  The kinds have code of their own: with one loop for all of them the choices among
+// them were half of the instructions (131072 tokens into 4 bits 324 us, 0.79 of the issue slots).
+enum Kind { kQ, kK, kV, kQI, kKI };
+constexpr int kSpan = 64;
+struct Rows {
+  int H_kv;
+  uint16_t *k_pool, *v_pool;
+  Kv4Pool pool;
+};
+template <int D, bool KV4, Kind K>
+__device__ __forceinline__ void append_kind(const AppendRows& a, const Rows& io, int pieces, int64_t i0, int n,
+                                            const int64_t* rows, const float* cs, int& turn) {
+  constexpr int LPR = D / 8, LPG = LPR / kGroups;
+  constexpr bool idx = K == kQI || K == kKI, pooled = K == kK || K == kV;
+  const int lane = threadIdx.x & 31, chunks = (pieces + 31) / 32, tasks = n * chunks;
+  const int batches = (tasks + kFly - 1) / kFly;
+  const uint16_t* const src = K == kQ ? a.q : K == kK ? a.k : K == kV ? a.v : K == kQI ? a.q_idx : a.k_idx;
+  const int64_t stride = K == kQ ? a.q_stride : K == kK ? a.k_stride : K == kV ? a.v_stride : K == kQI ? a.q_idx_stride : a.k_idx_stride;
+  for (int batch = turn; batch < batches; batch += kWarps) {
+    int c = batch * kFly / n, t = batch * kFly - c * n;  // the tokens of a chunk one after the other
+    uint4 w[kFly];
+    int tok[kFly], piece[kFly];  // piece -1 - e where this lane has none
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      const int e = c * 32 + lane;
+      const bool on = c < chunks && e < pieces && rows[t] >= 0;
+      w[u] = on ? ld_once(src + (i0 + t) * stride + e * 8) : make_uint4(0u, 0u, 0u, 0u);
+      tok[u] = t;
+      piece[u] = on ? e : -1 - e;
+      if (++t == n) t = 0, ++c;
+    }
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      if (batch * kFly + u >= tasks) break;  // (uniform in the warp)
+      const bool on = piece[u] >= 0;
+      const int e = on ? piece[u] : -1 - piece[u];
+      if (K != kV) {
+        const int lanes = idx ? a.d_I / 8 : LPR;
+        w[u] = turn8_bf16(w[u], e & (lanes - 1), lanes, idx ? a.rope_idx : a.rope, cs + 2 * tok[u] * kSpan, kSpan);
+      }
+      if (pooled && KV4) {
+        const unsigned lanes = ((1u << LPG) - 1u) << (lane & ~(LPG - 1));
+        uint32_t code, sb;
+        encode8<LPG>(w[u], lanes, code, sb);
+        if (on) {
+          const int64_t row = rows[tok[u]];
+          uint8_t* codes = K == kV ? io.pool.v_codes : io.pool.k_codes;
+          uint8_t* scales = K == kV ? io.pool.v_scales : io.pool.k_scales;
+          reinterpret_cast<uint32_t*>(codes)[row * (io.H_kv * LPR) + e] = code;
+          if (e % LPG == 0) scales[row * (io.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
+        }
+      } else if (on) {
+        const int64_t row = pooled || K == kKI ? rows[tok[u]] : i0 + tok[u];
+        const int width = K == kQ ? a.H_q * D : pooled ? io.H_kv * D : K == kQI ? io.H_kv * a.d_I : a.d_I;
+        void* to = K == kQ ? a.q_out : K == kK ? io.k_pool : K == kV ? io.v_pool : K == kQI ? a.q_idx_out : a.k_idx_pool;
+        const int64_t at = row * width + e * 8;
+        if (idx && a.idx_f8) *reinterpret_cast<uint2*>((uint8_t*)to + at) = e4m3_8(w[u], a.idx_scale);
+        else *reinterpret_cast<uint4*>((uint16_t*)to + at) = w[u];
+      }
+    }
+  }
+  turn = (turn - batches % kWarps + kWarps) % kWarps;  // the next kind begins where this one ended
+}
 
 // A CTA takes `toks` packed tokens: it looks up their places, works out their cos and sin, and its warps then go
 // through the tokens' chunks with four reads in flight.  K is rounded to bf16 once turned, then stored or quantized, so
@@ -233,8 +294,7 @@ enum Kind { kQ, kK, kV, kQI, kKI, kKinds };
 template <int D, bool KV4>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64_t N, int toks, RowMap map, uint16_t* k_pool,
                                                              uint16_t* v_pool, Kv4Pool pool, DeviceStatus* st) {
-  constexpr int LPR = D / 8, LPG = LPR / kGroups;
-  constexpr int kSpan = 64;
+  constexpr int LPR = D / 8;
   __shared__ __align__(16) float cs[2][kMaxToks * 2 * kSpan];  // of the attention's rows, of the index rows
   __shared__ int64_t rows[kRowThreads];
   __shared__ int32_t pos[kRowThreads];
@@ -244,76 +304,16 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64
   if (a.positions && (int)threadIdx.x < n) pos[threadIdx.x] = a.positions[i0 + threadIdx.x];
   __syncthreads();
   fill_turns(a.rope, pos, n, kSpan, 1.f, cs[0]);
-  if (a.rope_idx.rot) fill_turns(a.rope_idx, pos, n, kSpan, 1.f, cs[1]);
+  if (a.rope_idx_own) fill_turns(a.rope_idx, pos, n, kSpan, 1.f, cs[1]);
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = a.d_I / 8;
-  const int pieces[kKinds] = {a.q ? a.H_q * LPR : 0, a.H_kv * LPR, a.H_kv * LPR, a.q_idx ? a.H_kv * li : 0, a.k_idx ? li : 0};
-  int first[kKinds + 1];
-  first[0] = 0;
-#pragma unroll
-  for (int x = 0; x < kKinds; ++x) first[x + 1] = first[x] + (pieces[x] + 31) / 32;
-  // Tasks: a chunk of one kind of one token, the tokens of a chunk one after the other; a warp has kFly in a row at a time.
-  const int tasks = n * first[kKinds];
-  for (int base = warp * kFly; base < tasks; base += kWarps * kFly) {
-    uint4 w[kFly];
-    int tok[kFly], piece[kFly];  // of each task; the piece -1 - e where this lane has none
-    int kinds = 0;               // 4 bits each
-    int c = base / n, t = base - c * n;
-#pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      w[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (base + u >= tasks) break;  // (uniform in the warp)
-      const int kind = (c >= first[1]) + (c >= first[2]) + (c >= first[3]) + (c >= first[4]);
-      int f = 0, m = pieces[0];
-      const uint16_t* src = a.q;
-      int64_t stride = a.q_stride;
-      if (kind == kK) f = first[kK], m = pieces[kK], src = a.k, stride = a.k_stride;
-      if (kind == kV) f = first[kV], m = pieces[kV], src = a.v, stride = a.v_stride;
-      if (kind == kQI) f = first[kQI], m = pieces[kQI], src = a.q_idx, stride = a.q_idx_stride;
-      if (kind == kKI) f = first[kKI], m = pieces[kKI], src = a.k_idx, stride = a.k_idx_stride;
-      const int e = (c - f) * 32 + lane;
-      const bool on = e < m && rows[t] >= 0;
-      if (on) w[u] = ld_once(src + (i0 + t) * stride + e * 8);
-      tok[u] = t;
-      piece[u] = on ? e : -1 - e;
-      kinds |= kind << (4 * u);
-      if (++t == n) t = 0, ++c;
-    }
-#pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      if (base + u >= tasks) break;
-      const int kind = kinds >> (4 * u) & 15, t = tok[u];
-      const bool on = piece[u] >= 0, idx = kind >= kQI;
-      const int e = on ? piece[u] : -1 - piece[u];
-      if (kind != kV) {
-        const int lanes = idx ? li : LPR;
-        w[u] = turn8_bf16(w[u], e & (lanes - 1), lanes, idx ? a.rope_idx : a.rope, cs[idx] + 2 * t * kSpan, kSpan);
-      }
-      const int64_t row = rows[t];
-      if (kind == kK || kind == kV) {
-        if constexpr (KV4) {
-          const unsigned lanes = ((1u << LPG) - 1u) << (lane & ~(LPG - 1));
-          uint32_t code, sb;
-          encode8<LPG>(w[u], lanes, code, sb);
-          if (on) {
-            uint8_t* codes = kind == kV ? pool.v_codes : pool.k_codes;
-            uint8_t* scales = kind == kV ? pool.v_scales : pool.k_scales;
-            reinterpret_cast<uint32_t*>(codes)[row * (a.H_kv * LPR) + e] = code;
-            if (e % LPG == 0) scales[row * (a.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
-          }
-        } else if (on) {
-          *reinterpret_cast<uint4*>((kind == kV ? v_pool : k_pool) + row * (a.H_kv * D) + e * 8) = w[u];
-        }
-      } else if (on) {
-        const int64_t at = kind == kQ    ? (i0 + t) * (a.H_q * D) + e * 8
-                           : kind == kQI ? (i0 + t) * (a.H_kv * a.d_I) + e * 8
-                                         : row * a.d_I + e * 8;
-        void* to = kind == kQ ? a.q_out : kind == kQI ? a.q_idx_out : a.k_idx_pool;
-        if (idx && a.idx_f8) *reinterpret_cast<uint2*>((uint8_t*)to + at) = e4m3_8(w[u], a.idx_scale);
-        else *reinterpret_cast<uint4*>((uint16_t*)to + at) = w[u];
-      }
-    }
-  }
+  const Rows io = {a.H_kv, k_pool, v_pool, pool};
+  int turn = threadIdx.x >> 5;  // a batch of one kind after the other goes to the warps in turn
+  if (a.q) append_kind<D, KV4, kQ>(a, io, a.H_q * LPR, i0, n, rows, cs[0], turn);
+  append_kind<D, KV4, kK>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
+  append_kind<D, KV4, kV>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
+  const float* cs_idx = cs[a.rope_idx_own ? 1 : 0];
+  if (a.q_idx) append_kind<D, KV4, kQI>(a, io, a.H_kv * (a.d_I / 8), i0, n, rows, cs_idx, turn);
+  if (a.k_idx) append_kind<D, KV4, kKI>(a, io, a.d_I / 8, i0, n, rows, cs_idx, turn);
 }
 
 // Tokens of a CTA: more than one only where the CTAs still fill the GPU four times.

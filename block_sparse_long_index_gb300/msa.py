@@ -471,18 +471,6 @@ def kv_pool(k, v, n_pages, page_size, H_kv, d):
     return msa_kv_pool_t(_ptr(k), _ptr(v), int(n_pages), int(page_size), int(H_kv), int(d))
 
 
-def append_rows(k, v, q=None, q_out=None, q_idx=None, q_idx_out=None, k_idx=None, k_idx_pool=None, positions=None, H_q=0,
-                d_I=0, idx_f8=False, idx_scale=1.0, strides=None):
-    """The rows of an append call; strides: elements from token to token by name, those of contiguous rows otherwise."""
-    r = msa_append_t(_ptr(q), _ptr(k), _ptr(v), _ptr(q_idx), _ptr(k_idx))
-    for name, t in (("q", q), ("k", k), ("v", v), ("q_idx", q_idx), ("k_idx", k_idx)):
-        if t is not None:
-            setattr(r, name + "_stride", int(strides[name]) if strides else t.stride(0))
-    r.q_out, r.q_idx_out, r.k_idx_pool, r.positions = _ptr(q_out), _ptr(q_idx_out), _ptr(k_idx_pool), _ptr(positions)
-    r.H_q, r.d_I, r.idx_f8, r.idx_scale = int(H_q), int(d_I), int(bool(idx_f8)), float(idx_scale)
-    return r
-
-
 def msa_append_workspace():
     return int(_lib.msa_append_workspace())
 
