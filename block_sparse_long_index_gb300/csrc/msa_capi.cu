@@ -837,7 +837,7 @@ static msa_status_t tree_impl(const void* q, const void* k_pool, const void* v_p
     return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t s = (cudaStream_t)stream;
   const msa::TreePlan p = msa::tree_plan(B, T, H_q, H_kv, d, kv4 != nullptr);
-  if ((max_pages * page + 127) / 128 > ((int64_t)1 << 31) / B) return MSA_ERR_UNSUPPORTED;  // a CTA's tiles are counted in an int
+  if ((max_pages * page + 127) / 128 >= ((int64_t)1 << 31) / B) return MSA_ERR_UNSUPPORTED;  // a CTA's tiles are counted in an int
   st = begin(workspace, workspace_bytes, kHeader + msa::tree_scratch_bytes(p), s, 0);  // the first kernel clears the status
   if (st != MSA_OK) return st;
   msa::CacheMap map;

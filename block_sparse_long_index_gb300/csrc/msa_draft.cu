@@ -242,6 +242,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
   __shared__ float p_s[kMaxNodes], q_s[kMaxNodes], u_s[kMaxNodes];
   __shared__ unsigned long long kids_s[kMaxNodes];
   __shared__ long long seg_s[2][kWarps], cta_s[2];  // sums of the warps' runs, and of the CTA's, by pass
+  __shared__ long long all_s[kCluster];              // of all the cluster's CTAs, of the last pass
   __shared__ Step step_s;
   __shared__ int n_path_s;
   __shared__ long long target_s;
@@ -349,12 +350,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
         if (lane == 0) cta_s[passes & 1] = d;
       }
       cluster_sync();  // (and whoever read the buffer two passes ago is done)
-      long long x[kCluster];
-#pragma unroll
-      for (int k = 0; k < kCluster; ++k) x[k] = remote_sum(&cta_s[passes & 1], k);
+      if (tid < kCluster) all_s[tid] = remote_sum(&cta_s[passes & 1], tid);
+      __syncthreads();
       total = 0;
 #pragma unroll
-      for (int k = 0; k < kCluster; ++k) total += x[k];
+      for (int k = 0; k < kCluster; ++k) total += all_s[k];
       ++passes;
     }
   }
@@ -380,7 +380,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
     bool done = false;
 #pragma unroll
     for (int i = 0; i < kCluster; ++i) {
-      const long long x = remote_sum(&cta_s[buf], i);
+      const long long x = all_s[i];
       if (!done && before + x > target) k = i, done = true;
       if (!done) before += x;
     }

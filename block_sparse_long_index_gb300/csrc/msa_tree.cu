@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
             vc[y] = lds_16(at + L::CODES + ((y ^ odd) << 4) * (HW - 1));
           }
           const uint32_t k_sc = lds_2(scales_at + slot * L::RAW), v_sc = lds_2(scales_at + slot * L::RAW + L::SCALES);
-          const bool on = j * kKeysT + r < run.len;
+          const bool on = r < run.len - j * kKeysT;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(ks), kph, abort, st, 0xF03)))) break;
           expand_half<HW>(kc, k_sc, on, lane_to + ks * L::TILE);
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(ks + 1), kph, abort, st, 0xF04)))) break;
