@@ -107,6 +107,24 @@ __device__ __forceinline__ void mma_e4m3_16832(float* d, const uint32_t* a, cons
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// Thread-block clusters: the CTA's number in its cluster, a barrier of all its threads (which orders memory), a word of the
+// same variable in another CTA of it.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ int remote_int(const int* p, uint32_t rank) {
+  int x;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
 // Programmatic dependent launch: a primary grid lets its dependent grid be
 // scheduled; the dependent waits for the primary's completion and memory.
 __device__ __forceinline__ void griddep_launch_dependents() {

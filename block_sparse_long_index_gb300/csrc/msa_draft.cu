@@ -65,14 +65,6 @@ __device__ __forceinline__ bool offered(const VerifyArgs& a, int b, int j, int& 
   return parent >= 0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
 __device__ __forceinline__ long long remote_sum(const long long* p, uint32_t rank) {
   long long x;
   uint32_t at;

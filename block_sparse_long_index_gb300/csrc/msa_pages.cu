@@ -421,51 +421,57 @@ struct AcceptScratch {
   int64_t* dst;
 };
 
-// One CTA.  What an entry moves or gives up has to be its own alone (count 1): then no other sequence sees it change, and
-// no two entries meet.  A thread an entry, then an entry and a node, then eight threads an entry for its pages: with a warp
-// an entry the chains of reads of 256 entries, one after the other, took 30 us instead of 24 (with a cold L2).
+// What an entry moves or gives up has to be its own alone (count 1): then no other sequence sees it change, and no two
+// entries meet.  A cluster of kPlanCtas CTAs where there is work for more than one, which agree on whether the call is
+// carried out; entry i is CTA i % CTAs's.  A thread an entry, then an entry and a node, then eight threads an entry for
+// its pages.  (256 entries of 64 nodes, with a cold L2: 30 us with one CTA and a warp an entry, 24 us with one CTA, 12 us so.)
+constexpr int kPlanCtas = 8;
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads) pages_accept_plan_kernel(Pages p, AcceptArgs a, AcceptScratch w, DeviceStatus* st) {
   struct Entry {
     int s, base, k, len;  // sequence, first token that may go, tokens kept from there on, length
   };
   extern __shared__ int dyn[];
-  Entry* e_s = reinterpret_cast<Entry*>(dyn);  // [n]
-  const int tid = threadIdx.x;
+  int* names = dyn;  // [n]
+  Entry* e_s = reinterpret_cast<Entry*>(dyn + (a.n + 3) / 4 * 4);  // the CTA's entries
+  __shared__ int bad_s;
+  const int tid = threadIdx.x, rank = CTAS > 1 ? (int)blockIdx.x : 0;
+  const int mine = (a.n - rank + CTAS - 1) / CTAS;  // entries of the CTA
   griddep_launch_dependents();  // the moving grid waits for this one's end
-  clear_errors(st);
   int bad = a.n > p.n_seqs;  // (one is named twice, and the scratch has no room for them)
-  for (int i = tid; i < a.n; i += kThreads) {
+  for (int i = tid; i < a.n; i += kThreads) names[i] = a.seqs[i];
+  for (int y = tid; y < mine; y += kThreads) {
+    const int i = y * CTAS + rank;
     Entry e = {a.seqs[i], a.base[i], a.n_path[i], -1};
     if (e.s >= 0 && e.s < p.n_seqs) e.len = p.ctx[e.s];
     if (e.len < 0 || (int64_t)e.len > p.max_pages * p.page || e.base < 0 || e.base > e.len || e.k < 0 || e.k > a.T) {
       bad = 1;
       e.k = e.len = e.base = 0;
     }
-    e_s[i] = e;
+    e_s[y] = e;
   }
   bad = __syncthreads_or(bad);
   if (!bad) {
-    for (int i = tid; i < a.n; i += kThreads)
-#pragma unroll 8
-      for (int j = 0; j < i; ++j) bad |= e_s[j].s == e_s[i].s;
-    const int total = a.n * a.T;
+    for (int y = tid; y < mine; y += kThreads) bad |= named_before(names, y * CTAS + rank);
+    const int total = mine * a.T;
 #pragma unroll 4
     for (int x = tid; x < total; x += kThreads) {
-      const int i = x / a.T, j = x - i * a.T;
-      const Entry e = e_s[i];
+      const int y = x / a.T, j = x - y * a.T;
+      const Entry e = e_s[y];
       if (j >= e.k) continue;
-      const int f = a.path[x], before = j > 0 ? a.path[x - 1] : -1;
+      const int64_t at = (int64_t)(y * CTAS + rank) * a.T + j;
+      const int f = a.path[at], before = j > 0 ? a.path[at - 1] : -1;
       if (f <= before || f >= e.len - e.base) {
         bad = 1;
         continue;
       }
       const int32_t* row = p.table + (int64_t)e.s * p.max_pages;
       const int from = e.base + f, to = e.base + j;
-      w.src[x] = (int64_t)row[from / p.page] * p.page + from % p.page;
-      w.dst[x] = (int64_t)row[to / p.page] * p.page + to % p.page;
+      w.src[at] = (int64_t)row[from / p.page] * p.page + from % p.page;
+      w.dst[at] = (int64_t)row[to / p.page] * p.page + to % p.page;
     }
-    for (int i = tid / 8; i < a.n; i += kThreads / 8) {
-      const Entry e = e_s[i];
+    for (int y = tid / 8; y < mine; y += kThreads / 8) {
+      const Entry e = e_s[y];
       const int32_t* row = p.table + (int64_t)e.s * p.max_pages;
       for (int64_t j = e.base / p.page + tid % 8; j < pages_of(e.len, p.page); j += 8) {
         const int32_t id = row[j];
@@ -474,20 +480,27 @@ __global__ void __launch_bounds__(kThreads) pages_accept_plan_kernel(Pages p, Ac
     }
     bad = __syncthreads_or(bad);
   }
-  if (tid == 0) *w.ok = !bad;
-  if (bad) {
-    if (tid == 0) raise_error(st, kErrBadIndex, 17u);
-    return;
+  if (CTAS > 1) {  // all of the cluster's CTAs
+    if (tid == 0) bad_s = bad;
+    cluster_sync();
+    bad = __syncthreads_or(tid < CTAS ? remote_int(&bad_s, tid) : 0);
   }
-  for (int i = tid / 8; i < a.n; i += kThreads / 8) {
-    const Entry e = e_s[i];
-    int32_t* row = p.table + (int64_t)e.s * p.max_pages;
-    for (int64_t j = pages_of(e.base + e.k, p.page) + tid % 8; j < pages_of(e.len, p.page); j += 8) {
-      p.refs[row[j]] = 0;
-      row[j] = -1;
+  if (rank == 0 && tid == 0) {
+    *w.ok = !bad;
+    st->flags = bad ? kErrBadIndex : 0u;
+    st->first_code = bad ? 17u : 0u;
+  }
+  if (!bad)
+    for (int y = tid / 8; y < mine; y += kThreads / 8) {
+      const Entry e = e_s[y];
+      int32_t* row = p.table + (int64_t)e.s * p.max_pages;
+      for (int64_t j = pages_of(e.base + e.k, p.page) + tid % 8; j < pages_of(e.len, p.page); j += 8) {
+        p.refs[row[j]] = 0;
+        row[j] = -1;
+      }
+      if (tid % 8 == 0) p.ctx[e.s] = e.base + e.k;
     }
-    if (tid % 8 == 0) p.ctx[e.s] = e.base + e.k;
-  }
+  if (CTAS > 1) cluster_sync();  // no CTA leaves while another reads its word
 }
 
 // A thread has one column (of type V) of an entry's rows in one pool and takes its moves in order, eight reads before
@@ -616,10 +629,24 @@ cudaError_t launch_pages_accept(const Pages& p, const int32_t* seqs, const int32
   a.n_path = n_path;
   a.n = n;
   a.T = T;
-  const int smem = n * 16;
-  cudaError_t e = cudaFuncSetAttribute(pages_accept_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPageSeqs * 16);
+  // one CTA up to two moves a thread
+  const bool one = (int64_t)n * T <= 2 * kThreads;
+  const int ctas = one ? 1 : kPlanCtas, smem = ((n + 3) / 4 * 4 + (n + ctas - 1) / ctas * 4) * 4;
+  auto plan = one ? pages_accept_plan_kernel<1> : pages_accept_plan_kernel<kPlanCtas>;
+  cudaError_t e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPageSeqs * (4 + 16));
   if (e != cudaSuccess) return e;
-  pages_accept_plan_kernel<<<1, kThreads, smem, s>>>(p, a, w, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, plan, p, a, w, st)) != cudaSuccess) return e;
   e = cudaGetLastError();
   if (e != cudaSuccess || pools.n == 0) return e;
   size_t cols = 0;
