@@ -15,6 +15,9 @@
 // and its error, a lane's sum likewise, and all sums above a lane's are integers of 2^-48, which add up the same in any
 // order.  (64-bit floating point throughout would be bound by the few units for it; fp32 sums draw another token in one of
 // a thousand cases at 128000 tokens.)
+//
+// Measured: 64 trees of 24 nodes over 128000 tokens 53 us (0.18 of HBM, a few passes in a row of 4 us each); one tree of 6
+// over 50001 tokens 12 us.
 #include <math.h>
 
 #include "msa_common.cuh"

@@ -6,6 +6,10 @@
 // The frequency is given as F = f / 2 pi in 2^-64 turns, so that p F modulo 2^64 is the angle modulo a turn, exactly,
 // whatever p is: two integer multiplications instead of a reduction in 64-bit floating point (at p = 2^20 an fp32
 // angle would be off by 0.03).  cos and sin are worked out once a (token, pair) and shared by all heads.
+//
+// Bound: HBM, rows in and out once.  Measured: 32768 rows of 64 heads, d = 128, fp32, half of the channels turned: 328 us,
+// 6.55 TB/s (0.98 of the measured copy rate), bf16 and all of them 200 us, 5.4 TB/s (0.80); 48 rows of 32 heads: 5 us, a
+// launch's latency and one round trip.
 #include <math.h>
 
 #include "msa_kv4.cuh"
@@ -290,7 +294,9 @@ __device__ __forceinline__ void append_kind(const AppendRows& a, const Rows& io,
 // A CTA takes `toks` packed tokens: it looks up their places, works out their cos and sin, and its warps then go
 // through the tokens' chunks with four reads in flight.  K is rounded to bf16 once turned, then stored or quantized, so
 // that the cache holds what turning and storing in two calls would leave.  Bound: HBM, rows in and out once; few
-// tokens by the launch and the chain look-up, angles, rows.
+// tokens by the launch and the chain look-up, angles, rows.  Measured, 131072 tokens of 8 heads, d = 128, with index keys:
+// into bf16 pages 179 us (0.89 of the copy rate), into 4-bit pages 250 us, where the issue slots are 71 % busy with the
+// angles, the turns and the codes; 48 tokens with 32 query heads: 7 us.
 template <int D, bool KV4>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64_t N, int toks, RowMap map, uint16_t* k_pool,
                                                              uint16_t* v_pool, Kv4Pool pool, DeviceStatus* st) {
