@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmsa.so")
 SOURCES = ["msa_capi.cu", "msa_select.cu", "msa_invert.cu", "msa_attn.cu", "msa_attn_tile.cu", "msa_decode.cu",
            "msa_bwd.cu", "msa_warmup.cu", "msa_warmup_tc.cu", "msa_dense.cu", "msa_kv4.cu", "msa_pages.cu",
-           "msa_rope.cu", "msa_tree.cu", "msa_draft.cu"]
+           "msa_rope.cu", "msa_tree.cu", "msa_tree_few.cu", "msa_draft.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"] + ARCH
 

@@ -238,6 +238,8 @@ struct TreePlan {
   int B, T, H_q, H_kv, d;
   int RG, RU;          // row groups of a (sequence, K/V head), rows (node, head) of one
   int groups, rounds;  // runs of the tile list, items of a CTA
+  int ctas, ways;      // of the context's kernel; partials of a segment's K/V head
+  bool few;            // few rows over 4-bit pages: the form of msa_tree_few.cu
 };
 TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d, bool kv4);
 size_t tree_scratch_bytes(const TreePlan& p);

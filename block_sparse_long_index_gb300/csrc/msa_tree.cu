@@ -30,6 +30,7 @@
 
 #include "msa_kv4.cuh"
 #include "msa_sm100.cuh"
+#include "msa_tree.cuh"
 
 namespace msa {
 
@@ -38,39 +39,15 @@ namespace {
 using namespace sm100;
 using namespace kv4;
 
-constexpr int kRowsT = 128, kKeysT = 128;
+constexpr int kRowsT = 128;
 constexpr int kMaxT = 64;  // nodes of a tree: a 64-bit mask
 constexpr int kWarpMma = 16, kWarpLoad = 18, kWarpGuard = 19, kWarpExpand = 20;
 constexpr int kUnitRows = 16;                   // tokens of a tile that an expanding warp takes
 constexpr int kUnits = kKeysT / kUnitRows;      // warps that expand 4-bit codes
 __host__ __device__ constexpr int ctx_threads(bool kv4) { return 32 * (kv4 ? kWarpExpand + kUnits : kWarpExpand); }
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxRounds = 4;
 constexpr float kLazy = 8.0f;  // log2 units a row maximum may grow before O is rescaled
-
-struct TreeShape {
-  const int32_t* ctx;       // [B]
-  const int32_t* tree_len;  // [B], null: T each
-  int64_t cap;
-  int B, T, gs, H_kv;
-  int RG, RU;  // row groups of a (sequence, K/V head), rows of one
-  int groups, rounds;  // see tree_plan
-  // Nodes and context of sequence b; bad lengths count as none of either.
-  __device__ __forceinline__ bool lengths(int b, int& n, int& t) const {
-    n = ctx[b];
-    t = tree_len ? tree_len[b] : T;
-    if (n < 0 || t < 0 || t > T || (int64_t)n + t > cap) {
-      n = t = 0;
-      return false;
-    }
-    return true;
-  }
-  __device__ __forceinline__ int tiles(int b) const {
-    int n, t;
-    lengths(b, n, t);
-    return t ? (int)(((int64_t)n + kKeysT - 1) / kKeysT) : 0;
-  }
-};
 
 // What a CTA begins a round with: its unit and its group's run of the tile list.
 struct Round {
@@ -229,14 +206,6 @@ __device__ __forceinline__ void expand_half(const uint4 (&c)[HW], uint32_t scale
   }
 }
 
-// Scratch of a call: what the context kernel leaves for the joining one.
-struct TreeScratch {
-  int64_t* starts;       // [B + 1] tiles before each sequence
-  unsigned int* errors;  // [CTAs] flags each met
-  float* part_o;         // [slots][RU][D]; slot = (sequence + group) units + unit, which no two segments share
-  float2* part_ml;       // [slots][RU] maximum (log2 units) and sum
-};
-
 // The CTA's rounds.  Every thread takes part.  CTA 0 writes starts.
 template <int THREADS>
 __device__ __forceinline__ void find_rounds(const TreeShape& sh, int64_t* starts, int64_t* warp_sums, Round* start) {
@@ -291,7 +260,7 @@ __device__ __forceinline__ void find_rounds(const TreeShape& sh, int64_t* starts
       starts[b] = x;
       x += sh.tiles(b);
     }
-    if (tid == 0) starts[sh.B] = total;
+    if (tid == 0) starts[sh.B] = quota;
   }
   __syncthreads();
 }
@@ -817,6 +786,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   __shared__ int64_t at[kMaxT];  // cache rows of the drafts
   __shared__ uint64_t sees[kMaxT];
   __shared__ int up[2][kMaxT];
+  __shared__ __align__(16) float more_o[kJoinWarps][D];  // of rows that several warps share
+  __shared__ float2 more_ml[kJoinWarps];
   __shared__ int bad_s;
   __shared__ unsigned long long wild_s;  // drafts whose V holds values that are not finite
   float* o_s = reinterpret_cast<float*>(sm + 2 * J::KV);                  // [16 m_tiles][D]
@@ -841,7 +812,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       at[tid] = (int64_t)pp * map.page + (t - lp * map.page);
     }
   }
-  if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && tid == 0) bad_s = 1;
+  if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) bad_s = 1;
   // ---- K and V of the drafts, 16-byte pieces: K's piece x of row r at x ^ 4 (r & 1), V's at x ^ (r & 7); rows past T are zeros
   const int Tp = (T + 15) & ~15;
   for (int x = tid; x < 2 * Tp * CH; x += kJoinThreads) {
@@ -994,28 +965,34 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   __syncthreads();
   griddep_wait();  // the partials
   if (tid == 0 && bad_s) raise_error(st, kErrBadIndex, 13u);
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
     for (int c = tid; c < n_cta; c += kJoinThreads)
       if (w.errors[c]) raise_error(st, w.errors[c], 3u);
-  const int tiles = sh.tiles(b);
-  const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // rows of partials from group to group
-  int c0 = 0, c1 = -1;                                   // the groups that had a part of the sequence
-  if (tiles) {
-    const int64_t quota = run_quota(w.starts[sh.B], sh.groups), f0 = w.starts[b];
-    c0 = (int)(f0 / quota);
-    c1 = (int)((f0 + tiles - 1) / quota);
+  const int64_t per = (int64_t)sh.H_kv * sh.RG * sh.RU;  // rows of partials from one to the next of a row
+  int c0 = 0, c1 = -1;                                   // the first and the last partial of the sequence
+  if (T > 0 && n > 0) {
+    const int64_t quota = w.starts[sh.B], f0 = w.starts[b];
+    c0 = (int)(f0 / quota) * sh.ways;
+    c1 = (int)((f0 + (n - 1) / kKeysT) / quota) * sh.ways + sh.ways - 1;
   }
-  for (int lr = warp; lr < 16 * m_tiles; lr += kJoinThreads / 32) {
-    const int r = r_cta + lr;
-    if (r >= rows) break;
-    float acc[V];
-    float2 own = ml_s[lr];
-    float M = own.x, Lsum = own.y;
+  // this CTA's slice of the rows; with fewer rows than warps, several warps a row, each with every `share`-th four partials
+  const int slice = 16 * m_tiles / gridDim.z, share = slice < kJoinWarps ? kJoinWarps / slice : 1, sub = warp % share;
+  for (int i = warp / share; i < slice; i += kJoinWarps / share) {  // (once, where a row has several warps)
+    const int lr = blockIdx.z * slice + i, r = r_cta + lr;
+    const bool live = r < rows;
+    if (!live && share == 1) break;
+    float acc[V], M = -kInf, Lsum = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = o_s[lr * D + lane * V + e];
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    if (live && sub == 0) {
+      const float2 own = ml_s[lr];
+      M = own.x, Lsum = own.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = o_s[lr * D + lane * V + e];
+    }
     const int rg = r / sh.RU, unit = g * sh.RG + rg;
-    const int64_t s0 = b * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
-    for (int c = c0; c <= c1; c += 4) {  // four partials in flight
+    const int64_t s0 = b * sh.ways * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
+    for (int c = c0 + 4 * sub; live && c <= c1; c += 4 * share) {  // four partials in flight
       float2 ml[4];
       float x[4][V];
 #pragma unroll
@@ -1050,6 +1027,23 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
         for (int e = 0; e < V; ++e) acc[e] += x[u][e] * wt;
       }
     }
+    if (share > 1) {  // the row's warps
+      if (sub) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) more_o[warp][lane * V + e] = acc[e];
+        if (lane == 0) more_ml[warp] = make_float2(M, Lsum);
+      }
+      __syncthreads();
+      if (sub || !live) break;
+      for (int x = 1; x < share; ++x) {
+        const float2 ml = more_ml[warp + x];
+        const float m = fmaxf(M, ml.x), a = M == m ? 1.f : ex2_approx(M - m), wt = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+        M = m;
+        Lsum = Lsum * a + ml.y * wt;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = acc[e] * a + more_o[warp + x][lane * V + e] * wt;
+      }
+    }
     const bool any = Lsum > 0.f || Lsum != Lsum;  // scores of -inf alone weigh nothing: out 0, lse -inf
     const float inv = any ? 1.f / Lsum : 0.f;
     const int64_t row = first_row + (int64_t)(r / sh.gs) * H_q + r % sh.gs;
@@ -1064,7 +1058,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
 }
 
 size_t carve(const TreePlan& p, char* base, TreeScratch* out) {
-  const size_t slots = ((size_t)p.B + p.groups) * p.H_kv * p.RG;
+  const size_t slots = ((size_t)p.B + p.groups) * p.ways * p.H_kv * p.RG;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* r = base ? base + off : nullptr;
@@ -1073,7 +1067,7 @@ size_t carve(const TreePlan& p, char* base, TreeScratch* out) {
   };
   TreeScratch w;
   w.starts = (int64_t*)take(((size_t)p.B + 1) * 8);
-  w.errors = (unsigned int*)take((size_t)num_sms() * 4);
+  w.errors = (unsigned int*)take((size_t)p.ctas * 4);
   w.part_o = (float*)take(slots * p.RU * p.d * 4);
   w.part_ml = (float2*)take(slots * p.RU * 8);
   if (out) *out = w;
@@ -1084,30 +1078,9 @@ template <int D, bool KV4>
 cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const void* v_pool, const Kv4Pool& pool,
                      const CacheMap& map, const int32_t* ctx, const int32_t* tree_len, const int32_t* parents, float scale, void* out,
                      float* lse, const TreeScratch& w, DeviceStatus* st, cudaStream_t s) {
-  using L = Layout<D>;
-  const int gs = p.H_q / p.H_kv;
-  const bool two = !KV4 && p.T * gs > kRowsT;
-  alignas(64) unsigned char tq[128] = {}, tk[128] = {}, tv[128] = {};
-  const uint64_t row = (uint64_t)D * 2;
-  // q [B T][H_q][d] as boxes {64 channels, gs heads, 128 / gs positions}; pools [rows][H_kv][d] as {64, 1, box_rows}
-  int box_rows = 16;
-  while (box_rows < kKeysT && map.page % (2 * box_rows) == 0) box_rows *= 2;
-  if (!encode_tmap_3d(tq, q, D, (uint64_t)p.H_q, (uint64_t)p.B * p.T, row, (uint64_t)p.H_q * row, 64, gs, kRowsT / gs, 128))
-    return cudaErrorInvalidValue;
-  if (KV4) {
-    // codes [rows][H_kv][d / 2] bytes (as 16-bit words) in the order {word, row of a box, head, box}
-    const uint64_t cb = D / 2, boxes = (uint64_t)map.n_pages * (map.page / box_rows);
-    const uint64_t dims[4] = {cb / 2, (uint64_t)box_rows, (uint64_t)p.H_kv, boxes};
-    const uint64_t strides[3] = {(uint64_t)p.H_kv * cb, cb, (uint64_t)box_rows * p.H_kv * cb};
-    const uint32_t box[4] = {(uint32_t)cb / 2, (uint32_t)box_rows, 1, 1};
-    if (!encode_tmap_4d(tk, pool.k_codes, dims, strides, box, D / 2) || !encode_tmap_4d(tv, pool.v_codes, dims, strides, box, D / 2))
-      return cudaErrorInvalidValue;
-  } else {
-    const uint64_t rows = (uint64_t)map.n_pages * map.page;
-    if (!encode_tmap_3d(tk, k_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128) ||
-        !encode_tmap_3d(tv, v_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128))
-      return cudaErrorInvalidValue;
-  }
+  const int gs = p.H_q / p.H_kv, n_cta = p.ctas;
+  const float sl2 = scale * 1.4426950408889634f;
+  cudaError_t e = cudaSuccess;
   TreeShape sh;
   sh.ctx = ctx;
   sh.tree_len = tree_len;
@@ -1120,24 +1093,52 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   sh.RU = p.RU;
   sh.groups = p.groups;
   sh.rounds = p.rounds;
-  auto kern = tree_context_kernel<D, KV4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(two, KV4));
-  if (e != cudaSuccess) return e;
-  const float sl2 = scale * 1.4426950408889634f;
-  const int n_cta = num_sms();
-  kern<<<n_cta, ctx_threads(KV4), L::smem(two, KV4), s>>>(*reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
-                                                     *reinterpret_cast<const CUtensorMap*>(tv), sh, map, pool, box_rows,
-                                                     KV4 ? sl2 * kSubUnscale : sl2, w, st);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  sh.ways = p.ways;
+  if (p.few) {
+    if ((e = launch_tree_few(q, sh, map, pool, D, sl2, w, st, s)) != cudaSuccess) return e;
+  } else {
+    using L = Layout<D>;
+    const bool two = !KV4 && p.T * gs > kRowsT;
+    alignas(64) unsigned char tq[128] = {}, tk[128] = {}, tv[128] = {};
+    const uint64_t row = (uint64_t)D * 2;
+    // q [B T][H_q][d] as boxes {64 channels, gs heads, 128 / gs positions}; pools [rows][H_kv][d] as {64, 1, box_rows}
+    int box_rows = 16;
+    while (box_rows < kKeysT && map.page % (2 * box_rows) == 0) box_rows *= 2;
+    if (!encode_tmap_3d(tq, q, D, (uint64_t)p.H_q, (uint64_t)p.B * p.T, row, (uint64_t)p.H_q * row, 64, gs, kRowsT / gs, 128))
+      return cudaErrorInvalidValue;
+    if (KV4) {
+      // codes [rows][H_kv][d / 2] bytes (as 16-bit words) in the order {word, row of a box, head, box}
+      const uint64_t cb = D / 2, boxes = (uint64_t)map.n_pages * (map.page / box_rows);
+      const uint64_t dims[4] = {cb / 2, (uint64_t)box_rows, (uint64_t)p.H_kv, boxes};
+      const uint64_t strides[3] = {(uint64_t)p.H_kv * cb, cb, (uint64_t)box_rows * p.H_kv * cb};
+      const uint32_t box[4] = {(uint32_t)cb / 2, (uint32_t)box_rows, 1, 1};
+      if (!encode_tmap_4d(tk, pool.k_codes, dims, strides, box, D / 2) || !encode_tmap_4d(tv, pool.v_codes, dims, strides, box, D / 2))
+        return cudaErrorInvalidValue;
+    } else {
+      const uint64_t rows = (uint64_t)map.n_pages * map.page;
+      if (!encode_tmap_3d(tk, k_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128) ||
+          !encode_tmap_3d(tv, v_pool, D, (uint64_t)p.H_kv, rows, row, (uint64_t)p.H_kv * row, 64, 1, box_rows, 128))
+        return cudaErrorInvalidValue;
+    }
+    auto kern = tree_context_kernel<D, KV4>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(two, KV4));
+    if (e != cudaSuccess) return e;
+    kern<<<p.ctas, ctx_threads(KV4), L::smem(two, KV4), s>>>(*reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
+                                                       *reinterpret_cast<const CUtensorMap*>(tv), sh, map, pool, box_rows,
+                                                       KV4 ? sl2 * kSubUnscale : sl2, w, st);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   const int R = p.T * gs;
   // tiles of 16 rows a CTA: more than one where that leaves two CTAs an SM
   const int64_t tiles16 = (int64_t)p.B * p.H_kv * ((R + 15) / 16);
-  const int m_tiles = tiles16 >= (int64_t)8 * n_cta ? 4 : tiles16 >= (int64_t)4 * n_cta ? 2 : 1;
+  const int sms = num_sms(), m_tiles = tiles16 >= (int64_t)8 * sms ? 4 : tiles16 >= (int64_t)4 * sms ? 2 : 1;
+  int slices = 1;  // CTAs that share the joining of 16 rows, where there are few
+  while (m_tiles == 1 && slices < 16 && 2 * slices * tiles16 <= 2 * sms) slices *= 2;
   auto join = tree_join_kernel<D, KV4>;
   e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, JoinLayout<D>::smem(4));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv), (unsigned)((R + 16 * m_tiles - 1) / (16 * m_tiles)));
+  cfg.gridDim = dim3((unsigned)(p.B * p.H_kv), (unsigned)((R + 16 * m_tiles - 1) / (16 * m_tiles)), (unsigned)slices);
   cfg.dynamicSmemBytes = JoinLayout<D>::smem(m_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
@@ -1160,6 +1161,16 @@ TreePlan tree_plan(int B, int T, int H_q, int H_kv, int d, bool kv4) {
   p.H_kv = H_kv;
   p.d = d;
   const int R = T * (H_q / H_kv);
+  p.few = kv4 && R <= kFewRows && H_kv <= kFewHeads;
+  if (p.few) {
+    p.RG = p.rounds = 1;
+    p.RU = R;
+    p.ctas = p.groups = few_ctas(R);
+    p.ways = few_ways(H_kv);
+    return p;
+  }
+  p.ctas = num_sms();
+  p.ways = 1;
   const int most = kv4 ? kRowsT : 2 * kRowsT;
   p.RG = (R + most - 1) / most;
   p.RU = R < most ? R : most;

@@ -279,3 +279,84 @@ def test_tree_refusals():
                 dict(parents=par[:, :2]), dict(parents=par.cpu()), dict(tree_len=i32([1]))):
         with pytest.raises(ValueError):
             d(**{**dict(q=c.q, page_table=c.table, ctx_len=ctx, parents=par), **bad})
+
+
+FORMS = [  # rows a K/V head about 8, 16 and 32, where the 4-bit cache's kernel changes its form, by K/V heads
+    ([500, 0, 31, 16, 15, 700], 8, 8, 8, 128, 16, "random"),
+    ([300, 17], 9, 5, 5, 128, 48, "wide"),
+    ([777, 1, 2000], 4, 28, 7, 64, 32, "random"),
+    ([250, 33], 17, 3, 3, 128, 16, "chain"),
+    ([1200, 5], 8, 16, 4, 64, 80, "random"),
+    ([90, 4000], 2, 16, 2, 128, 64, "chain"),
+    ([2500], 31, 2, 2, 64, 16, "random"),
+    ([1, 47, 48, 49], 8, 1, 1, 64, 16, "random"),
+    ([3000, 100], 3, 4, 1, 128, 32, "wide"),
+    ([640], 32, 8, 8, 128, 128, "random"),
+    ([640, 9], 33, 8, 8, 128, 128, "random"),
+    ([200, 321], 2, 18, 9, 64, 16, "chain"),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+@pytest.mark.parametrize("ctx,T,H_q,H_kv,d,page,tree", FORMS)
+def test_forms(kind, ctx, T, H_q, H_kv, d, page, tree):
+    c = Case(kind, ctx, T, H_q, H_kv, d, page, tree, seed=20 + T)
+    out, lse = c.run()
+    assert c.dec.device_status() == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("T,gs", [(3, 2), (7, 2), (5, 4), (12, 8)])
+def test_groups_that_hold_nan_in_the_4_bit_context(T, gs):
+    """A NaN group of K makes its head's rows NaN, one of V its channels; past the context neither counts."""
+    c = Case("kv4", [300, 75], T, 2 * gs, 2, 128, 16, "chain", seed=21)
+    c.pool.k_scales[c.table[0, 9].long(), 3, 1, 2] = 255  # token 147, head 1
+    c.pool.v_scales[c.table[0, 4].long(), 15, 0, 1] = 255  # token 79, head 0, channels 32 .. 63
+    for p, at in ((c.table[1, 4], 11 + T), (c.table[0, 18], 12 + T)):  # behind the last node, in its page
+        if at < 16:
+            c.pool.k_scales[p.long(), at:] = 255
+            c.pool.v_scales[p.long(), at:] = 255
+    out, lse = c.run()
+    assert bool(lse[0, :, gs:].isnan().all()) and bool(out[0, :, gs:].isnan().all())
+    assert bool(lse[0, :, :gs].isfinite().all()) and bool(out[0, :, :gs, 32:64].isnan().all())
+    assert bool(out[0, :, :gs, :32].isfinite().all()) and bool(out[0, :, :gs, 64:].isfinite().all())
+    c.check(out, lse, only=[1])
+
+
+def test_many_rows_over_a_4_bit_pool_past_32_bit_offsets():
+    from block_sparse_long_index_gb300 import Kv4Pool
+    c = Case("kv4", [200], 24, 16, 8, 128, 128, seed=22)
+    n_pages = (1 << 32) // (128 * 8 * 64) + 16
+    big = []
+    for t in c.pool.tensors():
+        x = torch.zeros((n_pages,) + tuple(t.shape[1:]), dtype=t.dtype, device="cuda")
+        x[-c.n_pages:] = t
+        big.append(x)
+    c.table = torch.where(c.table >= 0, c.table + (n_pages - c.n_pages), c.table)
+    c.n_pages, c.pool = n_pages, Kv4Pool(*big)
+    out, lse = c.run()
+    assert c.dec.device_status() == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("T,H_q", [(2, 4), (24, 8)])
+def test_a_long_4_bit_context(T, H_q):
+    """Every CTA has a part of one sequence; keys much larger than the ones before move the maxima late."""
+    c = Case("kv4", [50000], T, H_q, 2, 128, 64, "random", seed=23)
+    pages = c.table[0].long()
+    for i, t in enumerate(range(3000, 50000, 6007)):
+        c.pool.k_scales[pages[t // 64], t % 64] = 160 + 2 * i
+    out, lse = c.run()
+    assert c.dec.device_status() == 0
+    c.check(out, lse)
+
+
+def test_many_sequences_in_4_bits():
+    """More sequences than a CTA has threads, some empty."""
+    r = np.random.default_rng(24)
+    ctx = [int(x) for x in r.integers(0, 40, 900)]
+    for T, H_q in ((2, 2), (10, 8)):
+        c = Case("kv4", ctx, T, H_q, 2, 64, 16, "chain", seed=24)
+        out, lse = c.run()
+        assert c.dec.device_status() == 0
+        c.check(out, lse, only=[0, 1, 2, 255, 256, 257, 511, 898, 899] + [int(i) for i in r.integers(0, 900, 12)])
