@@ -13,14 +13,14 @@
 // a fifth of its rate.  tree_context_kernel does a tile by tcgen05, S = Q K^T and O += P V
 // with 128 query rows, Q and K, V in shared memory, S / P and O in TMEM.  Two streams of it alternate, so that one's
 // softmax runs under the other's products:
-//   up to 128 rows, and over a 4-bit cache always: one query tile, whose even and odd key tiles are the streams (their O
+//   up to 128 rows, and over a 4-bit cache always (up to 32 rows there mostly take another form, msa_tree_few.cu): one query tile, whose even and odd key tiles are the streams (their O
 //   are merged at the run's end);
 //   more rows over bf16 pages: two query tiles over the same keys.  (4-bit pages are expanded again for each 128 rows: a
 //   tile's softmax takes as long, and the room of the second query tile holds the codes in flight.)
 // Rows of a tile past the last one are computed on by the tensor cores alone; warps without a row rest.
 //
 // Measured, with the join: bf16 pages, 128 rows, 4 sequences of 262144 tokens: 636 us, HBM's rate (a tile takes 1955
-// cycles where the caches stay in L2, 2825 from HBM); 256 rows, 16 sequences of 1200 to 12000 tokens: 141 us, 0.46 of HBM
+// cycles where the caches stay in L2, 2825 from HBM); 256 rows, 16 sequences of 1200 to 12000 tokens: 138 us, 0.47 of HBM
 // (107 us the context, whose two query tiles' softmax takes 3150 cycles a tile).  4-bit pages, 128 rows, 4 of 2^20 tokens:
 // 2534 us, 0.45 of the tensor cores' and 0.27 of HBM's rate: a tile is 6900 warp instructions, issue slots 58 % and ALU
 // 45 % busy (2950 cycles).  Tried there and no faster: expanding warps moved away from the schedulers of live rows, K's
@@ -763,9 +763,10 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
 // ---------------------------------------------------------------- the drafts' own part, and joining the partials
 // A CTA has 16 to 64 rows (node, head) of a (sequence, K/V head).  The drafts' K and V go to shared memory as bf16; a warp
 // for each 16 rows works out their softmax over the drafts that they see with mma.sync (m16n8k16; rows of T gs and at most 64
-// keys do not fill a tcgen05 tile).  Then, once the context kernel has ended, a warp a row joins that with the row's partials,
-// four of which are in flight at a time.  (With a warp a row for the drafts too, key by key in fp32, 16 trees of 64 nodes
-// took 70 us here instead of 43, with a cold L2.)
+// keys do not fill a tcgen05 tile).  Then, once the context kernel has ended, a warp for two rows joins that with the rows'
+// partials, four of each in flight.  Where there are few rows, up to 16 CTAs share those of a tile, and the warps of a CTA a
+// row.  Measured, 16 trees of 64 nodes, 32768 rows, with a cold L2: 37 us (46 with one row in hand and a piece of K or V in
+// flight; 70 with a warp a row for the drafts too, key by key in fp32).
 // V's values that are not finite are taken out of shared memory, so that a weight of 0 leaves them out, and added for the rows
 // that see them.
 template <int D>
@@ -815,18 +816,35 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) bad_s = 1;
   // ---- K and V of the drafts, 16-byte pieces: K's piece x of row r at x ^ 4 (r & 1), V's at x ^ (r & 7); rows past T are zeros
   const int Tp = (T + 15) & ~15;
-  for (int x = tid; x < 2 * Tp * CH; x += kJoinThreads) {
-    const bool is_v = x >= Tp * CH;
-    const int y = is_v ? x - Tp * CH : x, r = y / CH, ch = y % CH;
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    if (r < T) {
-      const int64_t hr = at[r] * sh.H_kv + g;
-      if constexpr (!KV4) {
-        c = *reinterpret_cast<const uint4*>((is_v ? v_pool : k_pool) + hr * D + ch * 8);
-      } else {
-        const uint32_t code = reinterpret_cast<const uint32_t*>((is_v ? pool.v_codes : pool.k_codes) + hr * (D / 2))[ch];
-        const uint32_t s1 = scale_bf16((is_v ? pool.v_scales : pool.k_scales)[hr * kGroups + ch / (CH / kGroups)]), s2 = s1 | (s1 << 16);
-        c = expand8(code, s2, scale_bias(s2));
+  constexpr int FLY = 4;  // pieces of a thread in flight
+  for (int x0 = tid; x0 < 2 * Tp * CH; x0 += FLY * kJoinThreads) {
+    uint4 raw[FLY];
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      const int x = x0 + f * kJoinThreads;
+      const bool is_v = x >= Tp * CH;
+      const int y = is_v ? x - Tp * CH : x, r = y / CH, ch = y % CH;
+      raw[f] = make_uint4(0u, 0u, 0u, 0u);
+      if (x < 2 * Tp * CH && r < T) {
+        const int64_t hr = at[r] * sh.H_kv + g;
+        if constexpr (!KV4) {
+          raw[f] = *reinterpret_cast<const uint4*>((is_v ? v_pool : k_pool) + hr * D + ch * 8);
+        } else {
+          raw[f].x = reinterpret_cast<const uint32_t*>((is_v ? pool.v_codes : pool.k_codes) + hr * (D / 2))[ch];
+          raw[f].y = (is_v ? pool.v_scales : pool.k_scales)[hr * kGroups + ch / (CH / kGroups)];
+        }
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      const int x = x0 + f * kJoinThreads;
+      if (x >= 2 * Tp * CH) break;
+      const bool is_v = x >= Tp * CH;
+      const int y = is_v ? x - Tp * CH : x, r = y / CH, ch = y % CH;
+      uint4 c = raw[f];
+      if (KV4 && r < T) {
+        const uint32_t s1 = scale_bf16(c.y), s2 = s1 | (s1 << 16);
+        c = expand8(c.x, s2, scale_bias(s2));
       }
       if (is_v) {
         uint32_t v[4] = {c.x, c.y, c.z, c.w};
@@ -839,8 +857,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
         if (wild) atomicOr(&wild_s, 1ull << r);
         c = make_uint4(v[0], v[1], v[2], v[3]);
       }
+      *reinterpret_cast<uint4*>(sm + (is_v ? J::KV : 0) + r * J::ROW + ((ch ^ (is_v ? r & 7 : (r & 1) << 2)) << 4)) = c;
     }
-    *reinterpret_cast<uint4*>(sm + (is_v ? J::KV : 0) + r * J::ROW + ((ch ^ (is_v ? r & 7 : (r & 1) << 2)) << 4)) = c;
   }
   // who is above whom, in doubling steps
   for (int i = 0, far = 1; far < T; far <<= 1, i ^= 1) {
@@ -977,83 +995,101 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   }
   // this CTA's slice of the rows; with fewer rows than warps, several warps a row, each with every `share`-th four partials
   const int slice = 16 * m_tiles / gridDim.z, share = slice < kJoinWarps ? kJoinWarps / slice : 1, sub = warp % share;
-  for (int i = warp / share; i < slice; i += kJoinWarps / share) {  // (once, where a row has several warps)
-    const int lr = blockIdx.z * slice + i, r = r_cta + lr;
-    const bool live = r < rows;
-    if (!live && share == 1) break;
-    float acc[V], M = -kInf, Lsum = 0.f;
+  constexpr int NR = 2;  // rows that a warp has in hand
+  const int apart = kJoinWarps / share;
+  for (int i = warp / share; i < slice; i += NR * apart) {  // (once, where a row has several warps)
+    float acc[NR][V], M[NR], sum[NR];
+    int64_t s0[NR];
+    bool live[NR];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (live && sub == 0) {
-      const float2 own = ml_s[lr];
-      M = own.x, Lsum = own.y;
+    for (int k = 0; k < NR; ++k) {
+      const int lr = blockIdx.z * slice + i + k * apart, r = r_cta + lr;
+      live[k] = i + k * apart < slice && r < rows;
+      M[k] = -kInf, sum[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = o_s[lr * D + lane * V + e];
+      for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
+      if (live[k] && sub == 0) {
+        const float2 own = ml_s[lr];
+        M[k] = own.x, sum[k] = own.y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[k][e] = o_s[lr * D + lane * V + e];
+      }
+      const int rg = r / sh.RU, unit = g * sh.RG + rg;
+      s0[k] = b * sh.ways * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
     }
-    const int rg = r / sh.RU, unit = g * sh.RG + rg;
-    const int64_t s0 = b * sh.ways * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
-    for (int c = c0 + 4 * sub; live && c <= c1; c += 4 * share) {  // four partials in flight
-      float2 ml[4];
-      float x[4][V];
+    if (!live[0] && share == 1) break;
+    for (int c = c0 + 4 * sub; c <= c1; c += 4 * share) {  // four partials of each in flight
+      float2 ml[NR][4];
+      float x[NR][4][V];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        ml[u] = make_float2(-kInf, 0.f);
+      for (int k = 0; k < NR; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[u][e] = 0.f;
-        if (c + u <= c1) {
-          const int64_t s = s0 + (c + u) * per;
-          ml[u] = w.part_ml[s];
-          const float* p = w.part_o + s * D + lane * V;
-          if constexpr (V == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(p);
-            x[u][0] = y.x, x[u][1] = y.y, x[u][2] = y.z, x[u][3] = y.w;
-          } else {
-            const float2 y = *reinterpret_cast<const float2*>(p);
-            x[u][0] = y.x, x[u][1] = y.y;
+        for (int u = 0; u < 4; ++u) {
+          ml[k][u] = make_float2(-kInf, 0.f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[k][u][e] = 0.f;
+          if (live[k] && c + u <= c1) {
+            const int64_t s = s0[k] + (c + u) * per;
+            ml[k][u] = w.part_ml[s];
+            const float* p = w.part_o + s * D + lane * V;
+            if constexpr (V == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(p);
+              x[k][u][0] = y.x, x[k][u][1] = y.y, x[k][u][2] = y.z, x[k][u][3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(p);
+              x[k][u][0] = y.x, x[k][u][1] = y.y;
+            }
           }
         }
-      }
-      const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-      const float old = M == m ? 1.f : ex2_approx(M - m);
-      Lsum *= old;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] *= old;
-      M = m;
+      for (int k = 0; k < NR; ++k) {
+        const float m = fmaxf(fmaxf(fmaxf(ml[k][0].x, ml[k][1].x), fmaxf(ml[k][2].x, ml[k][3].x)), M[k]);
+        const float old = M[k] == m ? 1.f : ex2_approx(M[k] - m);
+        sum[k] *= old;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float wt = ml[u].x == m ? 1.f : ex2_approx(ml[u].x - m);
-        Lsum += ml[u].y * wt;
+        for (int e = 0; e < V; ++e) acc[k][e] *= old;
+        M[k] = m;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += x[u][e] * wt;
+        for (int u = 0; u < 4; ++u) {
+          const float wt = ml[k][u].x == m ? 1.f : ex2_approx(ml[k][u].x - m);
+          sum[k] += ml[k][u].y * wt;
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[k][e] += x[k][u][e] * wt;
+        }
       }
     }
     if (share > 1) {  // the row's warps
       if (sub) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) more_o[warp][lane * V + e] = acc[e];
-        if (lane == 0) more_ml[warp] = make_float2(M, Lsum);
+        for (int e = 0; e < V; ++e) more_o[warp][lane * V + e] = acc[0][e];
+        if (lane == 0) more_ml[warp] = make_float2(M[0], sum[0]);
       }
       __syncthreads();
-      if (sub || !live) break;
+      if (sub) break;
       for (int x = 1; x < share; ++x) {
         const float2 ml = more_ml[warp + x];
-        const float m = fmaxf(M, ml.x), a = M == m ? 1.f : ex2_approx(M - m), wt = ml.x == m ? 1.f : ex2_approx(ml.x - m);
-        M = m;
-        Lsum = Lsum * a + ml.y * wt;
+        const float m = fmaxf(M[0], ml.x), a = M[0] == m ? 1.f : ex2_approx(M[0] - m), wt = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+        M[0] = m;
+        sum[0] = sum[0] * a + ml.y * wt;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = acc[e] * a + more_o[warp + x][lane * V + e] * wt;
+        for (int e = 0; e < V; ++e) acc[0][e] = acc[0][e] * a + more_o[warp + x][lane * V + e] * wt;
       }
     }
-    const bool any = Lsum > 0.f || Lsum != Lsum;  // scores of -inf alone weigh nothing: out 0, lse -inf
-    const float inv = any ? 1.f / Lsum : 0.f;
-    const int64_t row = first_row + (int64_t)(r / sh.gs) * H_q + r % sh.gs;
-    uint32_t y[V / 2];
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) y[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    uint32_t* op = reinterpret_cast<uint32_t*>(out + row * D) + lane * (V / 2);
-    if constexpr (V == 4) *reinterpret_cast<uint2*>(op) = make_uint2(y[0], y[1]);
-    else *op = y[0];
-    if (lane == 0 && lse) lse[row] = any ? (M + log2f(Lsum)) * 0.69314718055994530942f : -kInf;
+    for (int k = 0; k < NR; ++k) {
+      if (!live[k]) continue;
+      const int r = r_cta + blockIdx.z * slice + i + k * apart;
+      const bool any = sum[k] > 0.f || sum[k] != sum[k];  // scores of -inf alone weigh nothing: out 0, lse -inf
+      const float inv = any ? 1.f / sum[k] : 0.f;
+      const int64_t row = first_row + (int64_t)(r / sh.gs) * H_q + r % sh.gs;
+      uint32_t y[V / 2];
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) y[e] = pack_bf16x2(acc[k][2 * e] * inv, acc[k][2 * e + 1] * inv);
+      uint32_t* op = reinterpret_cast<uint32_t*>(out + row * D) + lane * (V / 2);
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(op) = make_uint2(y[0], y[1]);
+      else *op = y[0];
+      if (lane == 0 && lse) lse[row] = any ? (M[k] + log2f(sum[k])) * 0.69314718055994530942f : -kInf;
+    }
   }
 }
 

@@ -9,9 +9,9 @@
 // for one another, takes as long for any number of rows up to 32 (2630 cycles a tile of 128 tokens of a head).
 //
 // Measured with the join, 8 heads, d = 128, tcgen05's form in brackets: 4 sequences of 2^20 tokens, 8 rows a head 817 us
-// (2400; 0.84 of HBM's rate, which bounds it), 16 rows 1099 us, 32 rows 1731 us (0.40 of HBM: the products, their latency
-// with two warps a scheduler, and registers for no more); 16 sequences of 15000 to 30000 tokens, 32 rows 174 us (226),
-// 16 rows 116 us, 8 rows 93 us.
+// (2400; 0.84 of HBM's rate, which bounds it), 16 rows 1094 us, 32 rows 1640 us (0.42 of HBM: 1806 cycles a tile and head, of
+// which the products need 1024; with registers for two warps a scheduler, what is left is latency); 16 sequences of
+// 15000 to 30000 tokens, 32 rows 169 us (226), 16 rows 116 us, 8 rows 93 us.
 #include <math.h>
 
 #include "msa_kv4_units.cuh"
@@ -25,12 +25,18 @@ namespace {
 using namespace kv4;
 using namespace sm100;
 
-// CTAs an SM, its shared memory
+constexpr int kWarpUnits = 2;  // units of a warp's step: with one at a time 32 rows take 1870 us instead of 1640, 16 rows 1420 instead of 1094
+// CTAs an SM, its shared memory (16 rows in two CTAs of 128 registers and two stages: 1560 us)
 template <int NT>
 struct Few {
   static constexpr int CTAS = NT == 1 ? 2 : 1;
   static constexpr int SMEM = (CTAS == 2 ? 112 : 224) * 1024;
 };
+constexpr float kNone = -3e38f;  // a maximum of no score yet: finite, so that scores of -inf alone weigh 0
+// Bytes of a stage: K and V codes of a step's units, then their scales of every head.
+__host__ __device__ constexpr int stage_of(int d, int units, int heads, int H_kv) {
+  return (2 * units * heads * kUnit * (d / 2) + 2 * units * kUnit * H_kv * kGroups + 1023) / 1024 * 1024;
+}
 // q's operands: 16 bytes a lane for each 32 channels of 8 rows, by warp
 __host__ __device__ constexpr int q_bytes(int d, int nt) { return nt == 1 ? 0 : kDecWarps * nt * (d / 32) * 512; }
 
@@ -46,17 +52,16 @@ __device__ __forceinline__ void sts_16(uint32_t at, uint4 y) {
 // A CTA's run of the list of tiles (128 tokens), and segment by segment units [u0, u1) of one sequence.
 constexpr int kTileUnits = kKeysT / kUnit;
 struct Run {
-  int64_t f, f1, before;  // next tile, end, tiles before sequence `seq`
-  int seq, len;
-  int64_t u0, u1;
+  int f, f1, before;  // next tile, end, tiles before sequence `seq` (all tiles fit an int)
+  int seq, len, u0, u1;
   __device__ __forceinline__ bool next(const TreeShape& sh) {
     if (f >= f1) return false;
     int n, t;
     while (f >= before + (n = sh.tiles(seq))) before += n, ++seq;  // (ends: the runs add up to all tiles)
     sh.lengths(seq, len, t);
-    const int64_t t0 = f - before, t1 = min(f1 - before, (int64_t)n);
+    const int t0 = f - before, t1 = min(f1 - before, n);
     u0 = t0 * kTileUnits;
-    u1 = min(t1 * kTileUnits, ((int64_t)len + kUnit - 1) / kUnit);
+    u1 = min(t1 * kTileUnits, (len - 1) / kUnit + 1);  // (a sequence with tiles is not empty)
     f += t1 - t0;
     return true;
   }
@@ -64,8 +69,8 @@ struct Run {
 
 // The run of the CTA, a multiple of `step` tiles.  Every thread takes part.  CTA 0 writes starts.
 __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* starts) {
-  __shared__ int64_t sums[kDecWarps], before_s;
-  __shared__ int seq_s;
+  __shared__ int64_t sums[kDecWarps];
+  __shared__ int seq_s, before_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sh.B + kDecThreads - 1) / kDecThreads, b0 = min(tid * per, sh.B), b1 = min(b0 + per, sh.B);
   int64_t mine = 0;
@@ -92,7 +97,7 @@ __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* 
     int b = b0, n;
     while (at >= x + (n = sh.tiles(b))) x += n, ++b;
     seq_s = b;
-    before_s = x;
+    before_s = (int)x;
   }
   if (blockIdx.x == 0) {
     int64_t x = first;
@@ -104,8 +109,8 @@ __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* 
   }
   __syncthreads();
   Run r;
-  r.f = at;
-  r.f1 = min(total, at + quota);
+  r.f = (int)min(at, total);
+  r.f1 = (int)min(total, at + quota);
   r.seq = at < total ? seq_s : 0;
   r.before = at < total ? before_s : 0;
   return r;
@@ -115,8 +120,7 @@ template <int D, int HC, int NT>
 __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const uint16_t* __restrict__ q, Kv4Pool pool,
     CacheMap map, TreeShape sh, float sl2, int stages, TreeScratch w, DeviceStatus* status) {
-  constexpr int TW = kDecWarps / HC, SU = 2 * TW;  // warps that share a head, units of a step
-  constexpr int G = NT == 4 ? 1 : 2;               // units worked on at a time (registers)
+  constexpr int G = kWarpUnits, TW = kDecWarps / HC, SU = G * TW;  // units of a warp's step; warps that share a head, units of a step
   constexpr int CT = D / 8;                        // channels of a lane's V column
   using X = Tile<D>;
   extern __shared__ uint8_t smraw[];
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
   DeviceStatus* st = reinterpret_cast<DeviceStatus*>(est);  // the CTA's own (an error touches its first two words)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H_kv = sh.H_kv, H_q = H_kv * sh.gs, R = sh.RU;
-  const int stage = stage_bytes(D, TW, H_kv);
+  const int stage = stage_of(D, SU, HC, H_kv);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int i) { return bar0 + 8u * i; };                  // TMA -> consumers
   auto empty = [&](int i) { return bar0 + 8u * (kMaxStages + i); };  // consumers (8 warps) -> TMA
@@ -148,21 +152,20 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
   volatile int* abort = &abort_flag;
   Run run = find_run(sh, SU > kTileUnits ? SU / kTileUnits : 1, w.starts);
   const float kInf = __int_as_float(0x7f800000);
-  constexpr int kScales = 32 * X::BYTES;  // offset of the scales in a stage
+  constexpr int kV = SU * HC * X::BYTES, kScales = 2 * kV;  // offsets of V's codes and of the scales in a stage
   const int sc_unit = kUnit * H_kv * kGroups, sc_half = sc_unit / 2;
 
   const int r = lane >> 2, c = lane & 3;
   const int head = warp % HC, tl = warp / HC;
   const bool on = head < H_kv;
-  const float lazy = fminf(kLazy / sl2, 1e38f);  // of scores as they come out
   // this lane's places in its tile: K rows perm(r) (and 8 more), V tokens perm(2c) and perm(2c + 1) (and 8 more)
-  const int tile = (2 * tl * HC + head) * X::BYTES;  // of the warp's first unit; the second one's is HC tiles on
+  const int tile = (G * tl * HC + head) * X::BYTES;  // of the warp's first unit; the second one's is HC tiles on
   const int k_at = tile + X::at(X::perm(r), (X::CB / 4) * c);
-  const int v_at0 = 16 * X::BYTES + tile + X::at(X::perm(2 * c), (X::CB / 8) * r);
-  const int v_at1 = 16 * X::BYTES + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
-  const int ks_at = kScales + 2 * tl * sc_unit + (X::perm(r) * H_kv + head) * kGroups + c;
-  const int vs_at0 = kScales + (SU + 2 * tl) * sc_unit + (X::perm(2 * c) * H_kv + head) * kGroups + (r >> 1);
-  const int vs_at1 = kScales + (SU + 2 * tl) * sc_unit + (X::perm(2 * c + 1) * H_kv + head) * kGroups + (r >> 1);
+  const int v_at0 = kV + tile + X::at(X::perm(2 * c), (X::CB / 8) * r);
+  const int v_at1 = kV + tile + X::at(X::perm(2 * c + 1), (X::CB / 8) * r);
+  const int ks_at = kScales + G * tl * sc_unit + (X::perm(r) * H_kv + head) * kGroups + c;
+  const int vs_at0 = kScales + (SU + G * tl) * sc_unit + (X::perm(2 * c) * H_kv + head) * kGroups + (r >> 1);
+  const int vs_at1 = kScales + (SU + G * tl) * sc_unit + (X::perm(2 * c + 1) * H_kv + head) * kGroups + (r >> 1);
   const uint32_t q_at = smem_u32(sm) + stages * stage + warp * (NT * (D / 32) * 512) + lane * 16;
   // the ring's next stage and the parity of its use
   int slot = 0;
@@ -171,21 +174,21 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
   bool ok = true;
   uint32_t fetched = 0;  // stages that this warp has filled, and from bit 16 on the parity of the last time
   while (run.next(sh)) {
-    const int steps = (int)((run.u1 - run.u0 + SU - 1) / SU);
+    const int steps = (run.u1 - run.u0 + SU - 1) / SU;
     // step i into the stage `off` past `slot`
     auto fetch = [&](int i, int off) {
       int fs = slot + off;
       uint32_t fp = phase;
       if (fs >= stages) fs -= stages, fp ^= 1u;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty(fs), fp ^ 1u, abort, st, 0xE21)))) return;
-      const int64_t u = run.u0 + (int64_t)i * SU + lane;  // lanes 0 .. SU - 1: a unit each
-      const int n = (int)min((int64_t)SU, run.u1 - u + lane);
+      const int u = run.u0 + i * SU + lane;  // lanes 0 .. SU - 1: a unit each
+      const int n = min(SU, run.u1 - u + lane);
       if (lane == 0) mbar_arrive_expect_tx(full(fs), (uint32_t)(n * (2 * HC * X::BYTES + 2 * sc_unit)));
       fetched = (fetched & ~(0x10000u << fs)) | 1u << fs | fp << (16 + fs);
       __syncwarp();
       if (lane < n) {
         const uint32_t upp = (uint32_t)map.page / kUnit, lp = (uint32_t)u / upp;
-        const int in_page = (int)((uint32_t)u - lp * upp) * kUnit;
+        const int in_page = ((uint32_t)u - lp * upp) * kUnit;
         int32_t pp = __ldg(map.table + (int64_t)run.seq * map.max_pages + lp);
         if (pp < 0 || (int64_t)pp >= map.n_pages) {
           raise_error(st, kErrBadIndex, 3u);
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
         const uint32_t to = smem_u32(sm) + fs * stage;
         // tiles in (unit, head) order; a page holds whole units
         tma_load_4d(to + lane * HC * X::BYTES, &tm_k, 0, in_page, 0, pp, full(fs));
-        tma_load_4d(to + 16 * X::BYTES + lane * HC * X::BYTES, &tm_v, 0, in_page, 0, pp, full(fs));
+        tma_load_4d(to + kV + lane * HC * X::BYTES, &tm_v, 0, in_page, 0, pp, full(fs));
         const int64_t row = ((int64_t)pp * map.page + in_page) * (H_kv * kGroups);
         bulk_load(to + kScales + lane * sc_unit, pool.k_scales + row, (uint32_t)sc_unit, full(fs));
         bulk_load(to + kScales + (SU + lane) * sc_unit, pool.v_scales + row, (uint32_t)sc_unit, full(fs));
@@ -215,32 +218,28 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
         else sts_16(q_at + (t * (D / 32) + i) * 512, y);  // (this lane alone reads it)
       }
     }
-    // running maximum (raw scores), the same in log2 units, and the sum
-    float o[D / 16][NT][4], m[NT][2], z[NT][2], l[NT][2];
+    // running maximum in log2 units, and the sum
+    float o[D / 16][NT][4], z[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -kInf;
-      z[t][0] = z[t][1] = l[t][0] = l[t][1] = 0.f;
+      z[t][0] = z[t][1] = kNone;
+      l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
     }
-    int units = (int)(run.u1 - run.u0) - 2 * tl;                     // left from this warp's place in the step on
-    int left = (int)(run.len - (run.u0 + 2 * tl) * kUnit);           // tokens likewise
+    int units = run.u1 - run.u0 - G * tl;  // left from this warp's place in the step on
+    int left = (int)(run.len - (int64_t)(run.u0 + G * tl) * kUnit);  // tokens likewise
     for (int i = 0; i < steps; ++i, units -= SU, left -= SU * kUnit) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(full(slot), phase, abort, st, 0xE20));
-      // A second unit past the run's end holds whatever lay in the stage: its tokens count as past the length.
-      const int some = units > 1 ? left : min(left, kUnit);
-#pragma unroll 1
-      for (int h0 = 0; h0 < 2; h0 += G) {
-        if (!ok || !on || units <= h0) break;
-        const int seen = some - h0 * kUnit;
-        const uint32_t here = at + h0 * HC * X::BYTES, sc_here = at + h0 * sc_unit;
+      if (ok && on && units > 0) {
+        // A second unit past the run's end holds whatever lay in the stage: its tokens count as past the length.
+        const int seen = units > 1 ? left : min(left, kUnit);
         uint32_t ks2[G][2], vs2[G][2], top = 0;
 #pragma unroll
         for (int h = 0; h < G; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t a = sc_here + h * sc_unit + e * sc_half;
+            const uint32_t a = at + h * sc_unit + e * sc_half;
             ks2[h][e] = lds_u8(a + ks_at) * 0x00100010u + kSubScaleBias * 0x00010001u;
             vs2[h][e] = lds_u8(a + vs_at1) * 0x00100000u + (lds_u8(a + vs_at0) * 16u + kSubScaleBias * 0x00010001u);
             top = hmax2_bf16(top, hmax2_bf16(ks2[h][e], vs2[h][e]));
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
 #pragma unroll
         for (int h = 0; h < G; ++h) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) lds_words(here + k_at + h * HC * X::BYTES + e * 8 * X::CB, kw[h][e]);
+          for (int e = 0; e < 2; ++e) lds_words(at + k_at + h * HC * X::BYTES + e * 8 * X::CB, kw[h][e]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) s[h][t][0] = s[h][t][1] = s[h][t][2] = s[h][t][3] = 0.f;
         }
@@ -305,9 +304,8 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            n[t][e] = fmaxf(s[0][t][e], s[0][t][2 + e]);
-            if (G == 2) n[t][e] = fmaxf(n[t][e], fmaxf(s[G - 1][t][e], s[G - 1][t][2 + e]));
-            up |= n[t][e] > m[t][e] + lazy;
+            n[t][e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
+            up |= fmaf(n[t][e], sl2, -kLazy) > z[t][e];
           }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -317,10 +315,8 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
               for (int y = 4; y < 32; y <<= 1) n[t][e] = fmaxf(n[t][e], __shfl_xor_sync(0xffffffffu, n[t][e], y));
-              n[t][e] = fmaxf(n[t][e], m[t][e]);
-              const float zn = n[t][e] == -kInf ? 0.f : n[t][e] * sl2;  // scores of -inf alone weigh 0
-              a[e] = m[t][e] == -kInf ? 1.f : ex2_approx(z[t][e] - zn);
-              m[t][e] = n[t][e];
+              const float zn = fmaxf(n[t][e] * sl2, z[t][e]);
+              a[e] = ex2_approx(z[t][e] - zn);
               z[t][e] = zn;
               l[t][e] *= a[e];
             }
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
           uint32_t vw[4][D / 64];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            lds_words(here + h * HC * X::BYTES + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
+            lds_words(at + h * HC * X::BYTES + ((e & 1) ? v_at1 : v_at0) + (e >> 1) * 8 * X::CB, vw[e]);
           const SubScale sc[2] = {sub_scale(vs2[h][0]), sub_scale(vs2[h][1])};
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
@@ -398,7 +394,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
           for (int i = 0; i < D / 16; i += 2)
             po[i / 2] = make_float4(o[i][t][e] * kSubUnscale, o[i][t][2 + e] * kSubUnscale, o[i + 1][t][e] * kSubUnscale,
                                     o[i + 1][t][2 + e] * kSubUnscale);
-          if (r == 0) w.part_ml[part + row] = make_float2(m[t][e] == -kInf ? -kInf : z[t][e], l[t][e]);
+          if (r == 0) w.part_ml[part + row] = make_float2(z[t][e] == kNone ? -kInf : z[t][e], l[t][e]);
         }
     }
   }
@@ -422,7 +418,7 @@ cudaError_t launch_t(const void* q, const TreeShape& sh, const CacheMap& map, co
   const uint32_t box[4] = {CB / 2, kUnit, HC, 1};
   if (!encode_tmap_4d(tk, pool.k_codes, dims, strides, box, CB) || !encode_tmap_4d(tv, pool.v_codes, dims, strides, box, CB))
     return cudaErrorInvalidValue;
-  const int stage = stage_bytes(D, kDecWarps / HC, pool.H_kv), qb = q_bytes(D, NT);
+  const int stage = stage_of(D, kWarpUnits * kDecWarps / HC, HC, pool.H_kv), qb = q_bytes(D, NT);
   const int fit = (Few<NT>::SMEM - 1024 - qb) / stage, stages = fit > kMaxStages ? kMaxStages : fit;
   auto kern = tree_few_kernel<D, HC, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<NT>::SMEM);
