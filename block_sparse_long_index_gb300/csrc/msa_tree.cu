@@ -20,8 +20,8 @@
 // Rows of a tile past the last one are computed on by the tensor cores alone; warps without a row rest.
 //
 // Measured, with the join: bf16 pages, 128 rows, 4 sequences of 262144 tokens: 636 us, HBM's rate (a tile takes 1955
-// cycles where the caches stay in L2, 2825 from HBM); 256 rows, 16 sequences of 1200 to 12000 tokens: 138 us, 0.47 of HBM
-// (107 us the context, whose two query tiles' softmax takes 3150 cycles a tile).  4-bit pages, 128 rows, 4 of 2^20 tokens:
+// cycles where the caches stay in L2, 2825 from HBM); 256 rows, 16 sequences of 1200 to 12000 tokens: 128 us, 0.51 of HBM
+// (101 us the context, whose two query tiles' softmax takes 3150 cycles a tile).  4-bit pages, 128 rows, 4 of 2^20 tokens:
 // 2534 us, 0.45 of the tensor cores' and 0.27 of HBM's rate: a tile is 6900 warp instructions, issue slots 58 % and ALU
 // 45 % busy (2950 cycles).  Tried there and no faster: expanding warps moved away from the schedulers of live rows, K's
 // stage handed over before V's, two tiles of codes in registers (spills, which cost a trip to L2 each beside 227 KB of
@@ -45,7 +45,7 @@ constexpr int kWarpMma = 16, kWarpLoad = 18, kWarpGuard = 19, kWarpExpand = 20;
 constexpr int kUnitRows = 16;                   // tokens of a tile that an expanding warp takes
 constexpr int kUnits = kKeysT / kUnitRows;      // warps that expand 4-bit codes
 __host__ __device__ constexpr int ctx_threads(bool kv4) { return 32 * (kv4 ? kWarpExpand + kUnits : kWarpExpand); }
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxRounds = 4;
 constexpr float kLazy = 8.0f;  // log2 units a row maximum may grow before O is rescaled
 
@@ -723,8 +723,9 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
         if (KV4) w0 *= kSubUnscale, w1 *= kSubUnscale;
         const bool live = row < rows[q];
         const Run& r = runs_s[warp];
-        const int64_t at = (((int64_t)r.seq + r.group) * (sh.H_kv * sh.RG) + r.unit) * sh.RU + (two ? q * kRowsT : 0) + row;
-        float4* po = reinterpret_cast<float4*>(w.part_o + at * D + part * PD);
+        const int64_t slot = (((int64_t)r.seq + r.group) * (sh.H_kv * sh.RG) + r.unit) * sh.RU;
+        const int lr = (two ? q * kRowsT : 0) + row;
+        float* po = w.part_o + slot * D + part_at(sh.RU, lr, part * PD);
 #pragma unroll 1
         for (int c = 0; c < PD / 16; ++c) {
           uint32_t o[16], p[16];
@@ -739,10 +740,10 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
           if (live)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              po[c * 4 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+              *reinterpret_cast<float4*>(po + part_at(sh.RU, 0, c * 16 + 4 * e)) = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
                                           __uint_as_float(o[4 * e + 3]));
         }
-        if (live && part == 0) w.part_ml[at] = make_float2(M, sum);
+        if (live && part == 0) w.part_ml[slot + lr] = make_float2(M, sum);
       }
       tc_fence_before();
       __syncwarp();
@@ -765,18 +766,21 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
 // for each 16 rows works out their softmax over the drafts that they see with mma.sync (m16n8k16; rows of T gs and at most 64
 // keys do not fill a tcgen05 tile).  Then, once the context kernel has ended, a warp for two rows joins that with the rows'
 // partials, four of each in flight.  Where there are few rows, up to 16 CTAs share those of a tile, and the warps of a CTA a
-// row.  Measured, 16 trees of 64 nodes, 32768 rows, with a cold L2: 37 us (46 with one row in hand and a piece of K or V in
-// flight; 70 with a warp a row for the drafts too, key by key in fp32).
+// row.  Measured, 16 trees of 64 nodes, 32768 rows, with a cold L2: 31 us, of which the launch's instructions are
+// half (46 with one row in hand, one piece of K or V in flight and CTAs of 256 threads; 70 with a warp a row for the drafts
+// too, key by key in fp32).
 // V's values that are not finite are taken out of shared memory, so that a weight of 0 leaves them out, and added for the rows
 // that see them.
 template <int D>
 struct JoinLayout {
   static constexpr int ROW = D * 2, KV = kMaxT * ROW;  // bytes of a head row, of the drafts' K or V
-  __host__ __device__ static constexpr int smem(int tiles) { return 2 * KV + tiles * 16 * (D * 4 + 8); }
+  // O of the drafts takes the place of K and V once they are done with
+  __host__ __device__ static constexpr int ml_at(int tiles) { return 2 * KV > tiles * 16 * D * 4 ? 2 * KV : tiles * 16 * D * 4; }
+  __host__ __device__ static constexpr int smem(int tiles) { return ml_at(tiles) + tiles * 16 * 8; }
 };
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh, const int32_t* __restrict__ parents,
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh, const int32_t* __restrict__ parents,
                                                                     const uint16_t* __restrict__ qp, const uint16_t* __restrict__ k_pool,
                                                                     const uint16_t* __restrict__ v_pool, Kv4Pool pool, CacheMap map,
                                                                     int n_cta, int m_tiles, float scale_log2, TreeScratch w,
@@ -784,15 +788,15 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   using J = JoinLayout<D>;
   constexpr int V = D / 32, CH = D / 8;  // channels of a lane when a row is joined, 16-byte pieces of a row
   extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ int64_t at[kMaxT];  // cache rows of the drafts
+  __shared__ int64_t at[kMaxT];  // head rows of the drafts
   __shared__ uint64_t sees[kMaxT];
   __shared__ int up[2][kMaxT];
   __shared__ __align__(16) float more_o[kJoinWarps][D];  // of rows that several warps share
   __shared__ float2 more_ml[kJoinWarps];
   __shared__ int bad_s;
   __shared__ unsigned long long wild_s;  // drafts whose V holds values that are not finite
-  float* o_s = reinterpret_cast<float*>(sm + 2 * J::KV);                  // [16 m_tiles][D]
-  float2* ml_s = reinterpret_cast<float2*>(sm + 2 * J::KV + m_tiles * 16 * D * 4);  // [16 m_tiles]
+  float* o_s = reinterpret_cast<float*>(sm);                             // [16 m_tiles][D]
+  float2* ml_s = reinterpret_cast<float2*>(sm + J::ml_at(m_tiles));  // [16 m_tiles]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / sh.H_kv, g = blockIdx.x % sh.H_kv;
   const int r_cta = blockIdx.y * 16 * m_tiles;  // the CTA's first row
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       const int64_t t = (int64_t)n + tid, lp = t / map.page;
       int32_t pp = __ldg(map.table + (int64_t)b * map.max_pages + lp);
       if (pp < 0 || (int64_t)pp >= map.n_pages) bad = true, pp = 0;
-      at[tid] = (int64_t)pp * map.page + (t - lp * map.page);
+      at[tid] = ((int64_t)pp * map.page + (t - lp * map.page)) * sh.H_kv + g;
     }
   }
   if (__syncthreads_or(bad) && g == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) bad_s = 1;
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       const int y = is_v ? x - Tp * CH : x, r = y / CH, ch = y % CH;
       raw[f] = make_uint4(0u, 0u, 0u, 0u);
       if (x < 2 * Tp * CH && r < T) {
-        const int64_t hr = at[r] * sh.H_kv + g;
+        const int64_t hr = at[r];
         if constexpr (!KV4) {
           raw[f] = *reinterpret_cast<const uint4*>((is_v ? v_pool : k_pool) + hr * D + ch * 8);
         } else {
@@ -848,14 +852,16 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       }
       if (is_v) {
         uint32_t v[4] = {c.x, c.y, c.z, c.w};
-        bool wild = false;
+        const uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu), __vmaxu2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
+        if (top >= 0x7F800000u || (top & 0xFFFFu) >= 0x7F80u) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if ((v[j] & 0x7F80u) == 0x7F80u) v[j] &= 0xFFFF0000u, wild = true;
-          if ((v[j] & 0x7F800000u) == 0x7F800000u) v[j] &= 0x0000FFFFu, wild = true;
+          for (int j = 0; j < 4; ++j) {
+            if ((v[j] & 0x7F80u) == 0x7F80u) v[j] &= 0xFFFF0000u;
+            if ((v[j] & 0x7F800000u) == 0x7F800000u) v[j] &= 0x0000FFFFu;
+          }
+          atomicOr(&wild_s, 1ull << r);
+          c = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        if (wild) atomicOr(&wild_s, 1ull << r);
-        c = make_uint4(v[0], v[1], v[2], v[3]);
       }
       *reinterpret_cast<uint4*>(sm + (is_v ? J::KV : 0) + r * J::ROW + ((ch ^ (is_v ? r & 7 : (r & 1) << 2)) << 4)) = c;
     }
@@ -882,17 +888,18 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
   const float kInf = __int_as_float(0x7f800000);
   const int rows = T * sh.gs;
   const int64_t first_row = (int64_t)b * sh.T * (sh.H_kv * sh.gs) + g * sh.gs;  // row r is first_row + (r / gs) H_q + r % gs
-  const int H_q = sh.H_kv * sh.gs;
+  const int H_q = sh.H_kv * sh.gs, lg = __ffs(sh.gs) - 1;  // (gs is a power of two)
   if (warp < m_tiles && r_cta + warp * 16 < rows) {
     // ---- 16 rows over the drafts: a lane has rows lane / 4 and 8 more, channels and keys by lane % 4
     const int r = lane >> 2, c = lane & 3;
     uint32_t qf[2][D / 8];  // channels 8 (4 t + c) .. + 7 of both rows: two steps of 16 each
-    uint64_t mask[2];
+    uint64_t mask[2], seen[2];  // drafts that a row sees, and from this lane's first key on
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = r_cta + warp * 16 + r + 8 * e;
-      mask[e] = rr < rows ? sees[rr / sh.gs] : 0ull;
-      const uint16_t* p = qp + (first_row + (int64_t)(rr / sh.gs) * H_q + rr % sh.gs) * D;
+      mask[e] = rr < rows ? sees[rr >> lg] : 0ull;
+      seen[e] = mask[e] >> (2 * c);
+      const uint16_t* p = qp + (first_row + (int64_t)(rr >> lg) * H_q + (rr & (sh.gs - 1))) * D;
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
         const uint4 y = rr < rows ? *reinterpret_cast<const uint4*>(p + (4 * t + c) * 8) : make_uint4(0u, 0u, 0u, 0u);
@@ -915,7 +922,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const bool on = mask[x >> 1] >> (8 * j + 2 * c + (x & 1)) & 1ull;
+          const bool on = seen[x >> 1] >> (8 * j + (x & 1)) & 1ull;
           s[j][x] = on ? s[j][x] * scale_log2 : -kInf;
           M[x >> 1] = fmaxf(M[x >> 1], s[j][x]);
         }
@@ -957,7 +964,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         for (uint64_t left = mask[e] & wild_s; left; left &= left - 1) {
-          const int64_t hr = at[__ffsll((long long)left) - 1] * sh.H_kv + g;
+          const int64_t hr = at[__ffsll((long long)left) - 1];
 #pragma unroll
           for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -970,6 +977,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
             }
         }
     }
+    __syncthreads();  // K and V are done with
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -979,6 +987,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       for (int j = 0; j < D / 8; ++j) *reinterpret_cast<float2*>(o_s + lr * D + 8 * j + 2 * c) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
       if (c == 0) ml_s[lr] = make_float2(M[e], l[e]);
     }
+  } else {
+    __syncthreads();
   }
   __syncthreads();
   griddep_wait();  // the partials
@@ -993,13 +1003,17 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
     c0 = (int)(f0 / quota) * sh.ways;
     c1 = (int)((f0 + (n - 1) / kKeysT) / quota) * sh.ways + sh.ways - 1;
   }
+  // the CTA's rows are of one unit (groups of rows are multiples of 64): its first one there, its partials
+  const int rg = r_cta / sh.RU;
+  const int64_t s0 = b * sh.ways * per + (int64_t)(g * sh.RG + rg) * sh.RU;
   // this CTA's slice of the rows; with fewer rows than warps, several warps a row, each with every `share`-th four partials
   const int slice = 16 * m_tiles / gridDim.z, share = slice < kJoinWarps ? kJoinWarps / slice : 1, sub = warp % share;
-  constexpr int NR = 2;  // rows that a warp has in hand
-  const int apart = kJoinWarps / share;
-  for (int i = warp / share; i < slice; i += NR * apart) {  // (once, where a row has several warps)
+  const int r_u = r_cta - rg * sh.RU + blockIdx.z * slice;
+  constexpr int NR = 2;  // rows that a warp has in hand, side by side (their partials are) where every warp has two
+  const bool beside = slice >= NR * kJoinWarps;
+  const int apart = beside ? 1 : kJoinWarps / share;
+  for (int i = beside ? NR * warp : warp / share; i < slice; i += NR * kJoinWarps / share) {  // (once, where a row has several warps)
     float acc[NR][V], M[NR], sum[NR];
-    int64_t s0[NR];
     bool live[NR];
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
@@ -1014,24 +1028,25 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[k][e] = o_s[lr * D + lane * V + e];
       }
-      const int rg = r / sh.RU, unit = g * sh.RG + rg;
-      s0[k] = b * sh.ways * per + (int64_t)unit * sh.RU + (r - rg * sh.RU);
     }
     if (!live[0] && share == 1) break;
     for (int c = c0 + 4 * sub; c <= c1; c += 4 * share) {  // four partials of each in flight
       float2 ml[NR][4];
       float x[NR][4][V];
+      const int left = c1 - c;
 #pragma unroll
-      for (int k = 0; k < NR; ++k)
+      for (int u = 0; u < 4; ++u) {
+        if (u > left) break;
+        const int64_t s = s0 + (c + u) * per;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int k = 0; k < NR; ++k) {
           ml[k][u] = make_float2(-kInf, 0.f);
 #pragma unroll
           for (int e = 0; e < V; ++e) x[k][u][e] = 0.f;
-          if (live[k] && c + u <= c1) {
-            const int64_t s = s0[k] + (c + u) * per;
-            ml[k][u] = w.part_ml[s];
-            const float* p = w.part_o + s * D + lane * V;
+          if (live[k]) {
+            const int r = r_u + i + k * apart;
+            ml[k][u] = w.part_ml[s + r];
+            const float* p = w.part_o + s * D + part_at(sh.RU, r, lane * V);
             if constexpr (V == 4) {
               const float4 y = *reinterpret_cast<const float4*>(p);
               x[k][u][0] = y.x, x[k][u][1] = y.y, x[k][u][2] = y.z, x[k][u][3] = y.w;
@@ -1041,9 +1056,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
             }
           }
         }
+      }
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
-        const float m = fmaxf(fmaxf(fmaxf(ml[k][0].x, ml[k][1].x), fmaxf(ml[k][2].x, ml[k][3].x)), M[k]);
+        float m = M[k];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u <= left) m = fmaxf(m, ml[k][u].x);
         const float old = M[k] == m ? 1.f : ex2_approx(M[k] - m);
         sum[k] *= old;
 #pragma unroll
@@ -1051,6 +1070,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
         M[k] = m;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+          if (u > left) break;
           const float wt = ml[k][u].x == m ? 1.f : ex2_approx(ml[k][u].x - m);
           sum[k] += ml[k][u].y * wt;
 #pragma unroll
@@ -1081,7 +1101,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(TreeShape sh
       const int r = r_cta + blockIdx.z * slice + i + k * apart;
       const bool any = sum[k] > 0.f || sum[k] != sum[k];  // scores of -inf alone weigh nothing: out 0, lse -inf
       const float inv = any ? 1.f / sum[k] : 0.f;
-      const int64_t row = first_row + (int64_t)(r / sh.gs) * H_q + r % sh.gs;
+      const int64_t row = first_row + (int64_t)(r >> lg) * H_q + (r & (sh.gs - 1));
       uint32_t y[V / 2];
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) y[e] = pack_bf16x2(acc[k][2 * e] * inv, acc[k][2 * e + 1] * inv);
@@ -1169,7 +1189,7 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   const int64_t tiles16 = (int64_t)p.B * p.H_kv * ((R + 15) / 16);
   const int sms = num_sms(), m_tiles = tiles16 >= (int64_t)8 * sms ? 4 : tiles16 >= (int64_t)4 * sms ? 2 : 1;
   int slices = 1;  // CTAs that share the joining of 16 rows, where there are few
-  while (m_tiles == 1 && slices < 16 && 2 * slices * tiles16 <= 2 * sms) slices *= 2;
+  while (m_tiles == 1 && slices < 16 && 2 * slices * tiles16 <= 4 * sms) slices *= 2;
   auto join = tree_join_kernel<D, KV4>;
   e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, JoinLayout<D>::smem(4));
   if (e != cudaSuccess) return e;

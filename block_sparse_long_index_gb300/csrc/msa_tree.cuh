@@ -36,9 +36,11 @@ struct TreeShape {
 struct TreeScratch {
   int64_t* starts;       // [B + 1] tiles before each sequence, then those of a run
   unsigned int* errors;  // [CTAs] flags each met
-  float* part_o;         // [slots][RU][D]; slot = ((sequence + group) ways + way) units + unit, which no two segments share
+  float* part_o;         // [slots][D / 8][RU][8] (a lane of the context kernel has a row, one of the joining one channels); slot = ((sequence + group) ways + way) units + unit, which no two segments share
   float2* part_ml;       // [slots][RU] maximum (log2 units) and sum
 };
+// Channel ch of row r in a slot's partial O.
+__device__ __forceinline__ int part_at(int RU, int r, int ch) { return ((ch >> 3) * RU + r) * 8 + (ch & 7); }
 
 // The context over 4-bit pages for few rows a K/V head (msa_tree_few.cu): most rows, most K/V heads; CTAs and partials.
 constexpr int kFewRows = 32, kFewHeads = 8;

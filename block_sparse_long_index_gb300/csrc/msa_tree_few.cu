@@ -389,10 +389,11 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
           for (int y = 4; y < 32; y <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], y);
           const int row = 8 * t + 2 * c + e;
           if (row >= R) continue;
-          float4* po = reinterpret_cast<float4*>(w.part_o + (part + row) * D + CT * r);
+          float* po = w.part_o + part * D + part_at(R, row, CT * r);
 #pragma unroll
           for (int i = 0; i < D / 16; i += 2)
-            po[i / 2] = make_float4(o[i][t][e] * kSubUnscale, o[i][t][2 + e] * kSubUnscale, o[i + 1][t][e] * kSubUnscale,
+            *reinterpret_cast<float4*>(po + part_at(R, 0, 2 * i)) =
+                make_float4(o[i][t][e] * kSubUnscale, o[i][t][2 + e] * kSubUnscale, o[i + 1][t][e] * kSubUnscale,
                                     o[i + 1][t][2 + e] * kSubUnscale);
           if (r == 0) w.part_ml[part + row] = make_float2(z[t][e] == kNone ? -kInf : z[t][e], l[t][e]);
         }
