@@ -16,8 +16,8 @@
 // order.  (64-bit floating point throughout would be bound by the few units for it; fp32 sums draw another token in one of
 // a thousand cases at 128000 tokens.)
 //
-// Measured: 64 trees of 24 nodes over 128000 tokens 53 us (0.18 of HBM, a few passes in a row of 4 us each); one tree of 6
-// over 50001 tokens 12 us.
+// Measured: 64 trees of 24 nodes over 128000 tokens 46 us (0.21 of HBM, a few passes in a row of 4 us each; 22 us where one
+// pass is all); one tree of 6 over 50001 tokens 12 us.
 #include <math.h>
 
 #include "msa_common.cuh"
@@ -270,6 +270,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
   double c = 0.0, W = 1.0;
   bool summed = false;  // whether the last pass's sums are those of the present residual
   long long total = 0;  // of the last pass; every thread's
+  const float u_last = tid == 0 ? a.u_last[b] : 0.f;
   if (tid == 0 && T > 0) path_s[n_path++] = 0;
   while (T > 0) {
     if (tid == 0) {
@@ -363,7 +364,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
     if (rank == 0 && tid == 0) a.next[b] = -1;
   } else {
     if (tid == 0) {
-      float ul = a.u_last[b];
+      float ul = u_last;
       ul = ul > 0.f ? fminf(ul, 0.99999994f) : 0.f;  // (a NaN counts as 0)
       target_s = (long long)((double)ul * (double)total);  // a whole sum exceeds u total where it exceeds its whole part
     }
@@ -389,48 +390,66 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
         if (lane >= o) incl += t;
       }
       const int w = __ffs(__ballot_sync(0xffffffffu, before + incl > target)) - 1;
-      if (warp == w) {
-        const Step step = step_s;
-        Residual r;
-        const int64_t at = ((int64_t)b * a.T + step.node) * a.V;
-        r.set(a, step, at, out_s);
-        const RowRun run = run_of(at, a.V, rank * kWarps + warp, kRuns);
-        int64_t last = -1, hit = -1;  // the last element with a share so far (an element's sum may round below its lane's); the one
-        long long sum = before + __shfl_sync(0xffffffffu, incl - mine, w);
-        for (int64_t v0 = run.v0; v0 < run.v1 && hit < 0; v0 += 32 * kFly) {
-          float4 pa[kFly], qa[kFly];
+      before += __shfl_sync(0xffffffffu, incl - mine, w);
+      // all warps take a part of that run each: the part, then its element.  (One warp through the whole run: 64 trees 53 us
+      // instead of 46.)
+      const Step step = step_s;
+      Residual r;
+      const int64_t at = ((int64_t)b * a.T + step.node) * a.V;
+      r.set(a, step, at, out_s);
+      const RowRun run = run_of(at, a.V, rank * kWarps + w, kRuns);
+      const int64_t each = ((run.v1 - run.v0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+      const int64_t first_v = min(run.v0 + warp * each, run.v1), end_v = min(first_v + each, run.v1);
+      auto load = [&](int64_t v, long long (&d)[4]) {
+        float4 pa, qa;
+        if (r.q) r.load<kTimes>(v, end_v, pa, qa);
+        else r.load<kPlain>(v, end_v, pa, qa);
+        r.each(v, pa, qa, d);
+        return (d[0] + d[1]) + (d[2] + d[3]);
+      };
+      long long d[4], sum = 0;
+#pragma unroll 4
+      for (int64_t v = first_v + lane; v < end_v; v += 32) sum += load(v, d);
 #pragma unroll
-          for (int u = 0; u < kFly; ++u) {
-            if (r.q) r.load<kTimes>(v0 + 32 * u + lane, run.v1, pa[u], qa[u]);
-            else r.load<kPlain>(v0 + 32 * u + lane, run.v1, pa[u], qa[u]);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) seg_s[buf ^ 1][warp] = sum;  // (the pass before the last one's are read)
+      __syncthreads();
+      const long long part = lane < kWarps ? seg_s[buf ^ 1][lane] : 0;
+      incl = part;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > target), some = __ballot_sync(0xffffffffu, part > 0);
+      // (the elements' sums may round below their lanes': then the last element with a share)
+      const int wp = past ? __ffs(past) - 1 : 31 - __clz(some | 1u);
+      if (warp == wp) {
+        sum = before + __shfl_sync(0xffffffffu, incl - part, wp);
+        int64_t last = -1, hit = -1;
+        for (int64_t v0 = first_v; v0 < end_v && hit < 0; v0 += 32) {
+          const int64_t v = v0 + lane;
+          const long long of_lane = load(v, d);
+          long long up = of_lane;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += t;
           }
+          long long x = sum + (up - of_lane);
+          int64_t first = -1, end = -1;
 #pragma unroll
-          for (int u = 0; u < kFly; ++u) {
-            const int64_t v = v0 + 32 * u + lane;
-            long long d[4];
-            r.each(v, pa[u], qa[u], d);
-            const long long of_lane = (d[0] + d[1]) + (d[2] + d[3]);
-            long long up = of_lane;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const long long t = __shfl_up_sync(0xffffffffu, up, o);
-              if (lane >= o) up += t;
+          for (int j = 0; j < 4; ++j) {
+            x += d[j];
+            if (d[j] > 0) {
+              end = v * 4 - r.skew + j;
+              if (first < 0 && x > target) first = end;
             }
-            long long s = sum + (up - of_lane);
-            int64_t first = -1, end = -1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              s += d[j];
-              if (d[j] > 0) {
-                end = v * 4 - r.skew + j;
-                if (first < 0 && s > target) first = end;
-              }
-            }
-            const unsigned found = __ballot_sync(0xffffffffu, first >= 0), share = __ballot_sync(0xffffffffu, end >= 0);
-            if (found && hit < 0) hit = __shfl_sync(0xffffffffu, first, __ffs(found) - 1);
-            if (share) last = __shfl_sync(0xffffffffu, end, 31 - __clz(share));
-            sum += __shfl_sync(0xffffffffu, up, 31);
           }
+          const unsigned found = __ballot_sync(0xffffffffu, first >= 0), share = __ballot_sync(0xffffffffu, end >= 0);
+          if (found) hit = __shfl_sync(0xffffffffu, first, __ffs(found) - 1);
+          if (share) last = __shfl_sync(0xffffffffu, end, 31 - __clz(share));
+          sum += __shfl_sync(0xffffffffu, up, 31);
         }
         if (lane == 0) a.next[b] = (int32_t)(hit >= 0 ? hit : last);
       }
