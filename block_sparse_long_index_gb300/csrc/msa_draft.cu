@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kCluster = 8;
 constexpr int kMaxNodes = 64;
-constexpr int kFly = 2;  // vectors of each row that a lane has in flight
+constexpr int kFly = 2;  // vectors of each row that a lane has in flight (3 and 4 are slower: 48 and 51 us for 46)
 constexpr double kUnit = 281474976710656.0;  // 2^48
 
 // A probability: what is not a positive finite number counts as 0.
