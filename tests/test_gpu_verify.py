@@ -427,3 +427,78 @@ def test_speculative_step_captured():
                         replayed[0].tensors() + [replayed[1].page_table, replayed[1].ctx_len, replayed[1].refs, replayed[2].out, replayed[3].path, replayed[4]]):
             assert torch.equal(a, b)
     assert int(eager[4].sum()) > 39 + 10
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("B,T,V,kind", [(24, 4, 9001, "random"), (45, 5, 7003, "random"), (41, 1, 20000, "chain")])
+def test_verify_many_trees_over_long_rows(B, T, V, kind, drawn):
+    a = trees(np.random.default_rng(B + V), B, T, V, kind, drawn)
+    run, *got = call(*a)
+    assert run.device_status() == 0
+    check(*a, *got)
+
+
+def many_accepts(n=150, T=30, page=16, seed=31):
+    """More entries than the plan's first form takes: random bases and branches, sequences of 0 to 200 tokens before them."""
+    r = np.random.default_rng(seed)
+    base = r.integers(0, 200, n)
+    base[:4] = [0, page, page - 1, 1]
+    lens = [int(b) + T + int(e) for b, e in zip(base, r.integers(0, 20, n))]
+    n_pages = sum(-(-x // page) for x in lens) + 5
+    pools = [torch.zeros((n_pages, page, 2, 8), dtype=torch.bfloat16, device="cuda")]
+    cache = cache_of(lens, page, n_pages, pools, seed=seed)
+    k = r.integers(0, T + 1, n)
+    k[:6] = [0, T, 1, T - 1, 0, T]
+    paths = [sorted(r.choice(T, size=x, replace=False).tolist()) for x in k]
+    entries = r.permutation(n)[:n - 7]
+    path = np.full((len(entries), T), -1, np.int32)
+    for i, s in enumerate(entries):
+        path[i, :k[s]] = paths[s]
+    return cache, pools, lens, base, paths, entries, path
+
+
+def test_accept_of_many_entries():
+    cache, pools, lens, base, paths, entries, path = many_accepts()
+    page = cache.page_size
+    before = [token_rows(cache, pools[0], s, n) for s, n in enumerate(lens)]
+    old = cache.page_table.clone()
+    cache.accept(i32(entries), i32(base[entries]), i32(path), i32([len(paths[s]) for s in entries]))
+    assert cache.device_status() == 0
+    live = set()
+    for s, n0 in enumerate(lens):
+        named = s in entries
+        n = int(base[s]) + len(paths[s]) if named else n0
+        held = -(-n // page)
+        assert int(cache.ctx_len[s]) == n
+        assert torch.equal(cache.page_table[s, :held], old[s, :held]) and bool((cache.page_table[s, held:] == -1).all())
+        live |= set(old[s, :held].tolist())
+        want = ref.accept(list(before[s]), int(base[s]), paths[s]) if named else list(before[s])
+        assert n == 0 or torch.equal(token_rows(cache, pools[0], s, n), torch.stack(want))
+    refs = cache.refs.cpu().numpy()
+    assert all(refs[i] == (1 if i in live else 0) for i in range(cache.n_pages))
+
+
+@pytest.mark.parametrize("what", ["a name twice", "a name outside", "a base past the end", "a path that falls", "a node past the end", "a shared page"])
+def test_accept_of_many_entries_changes_nothing_where_one_is_bad(what):
+    from block_sparse_long_index_gb300 import msa
+    cache, pools, lens, base, paths, entries, path = many_accepts(seed=32)
+    seqs, bases, n = entries.copy(), base[entries].copy(), np.array([len(paths[s]) for s in entries])
+    at = next(i for i in range(100, len(seqs)) if n[i] > 3)
+    if what == "a name twice":
+        seqs[at] = seqs[3]
+        bases[at], n[at] = 0, 0
+    elif what == "a name outside":
+        seqs[at] = len(lens)
+    elif what == "a base past the end":
+        bases[at], n[at] = lens[seqs[at]] + 1, 0
+    elif what == "a path that falls":
+        path[at, 2] = path[at, 1]
+    elif what == "a node past the end":
+        path[at, n[at] - 1] = lens[seqs[at]] - bases[at]
+    else:
+        cache.refs[cache.page_table[seqs[at], int(bases[at]) // 16].long()] = 2
+    held = (cache.page_table, cache.ctx_len, cache.refs, pools[0].view(torch.uint8))  # (the rows' bytes make NaNs, too)
+    state = [t.clone() for t in held]
+    cache.accept(i32(seqs), i32(bases), i32(path), i32(n))
+    assert cache.device_status() == msa.MSA_ERR_BAD_INDEX
+    assert all(torch.equal(a, b) for a, b in zip(state, held))
