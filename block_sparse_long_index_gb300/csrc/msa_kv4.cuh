@@ -106,35 +106,55 @@ __device__ __forceinline__ uint32_t codes8(const uint64_t (&x2)[4], float inv_s)
   return (lo - off) | (hi - off) << 16;
 }
 
-// A group's scale byte and a thread's word of 8 codes, from the 8 bf16 channels `x` of each of its LPG threads (`lanes`).
-template <int LPG>
-__device__ __forceinline__ void encode8(uint4 x, unsigned lanes, uint32_t& code, uint32_t& sb) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
+// A group's scale byte and a thread's words of 8 codes, from the W x 8 bf16 channels `x` of each of its LPG threads (`lanes`).
+template <int LPG, int W>
+__device__ __forceinline__ void encode(const uint4 (&x)[W], unsigned lanes, uint32_t (&code)[W], uint32_t& sb) {
+  uint32_t w[W][4], mx = 0u;  // largest |x| as bf16 bits: magnitudes order as integers, NaN and infinity on top
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
+  for (int i = 0; i < W; ++i) {
+    w[i][0] = x[i].x, w[i][1] = x[i].y, w[i][2] = x[i].z, w[i][3] = x[i].w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[i][j] & 0x7FFF7FFFu);
+  }
 #pragma unroll
   for (int o = 1; o < LPG; o <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(lanes, mx, o));
   mx = max(mx & 0xFFFFu, mx >> 16);
   sb = scale_of(mx);
   const float s = scale_f32(sb), inv = __fdividef(1.0f, s);
-  uint64_t x2[4];  // channels 2 j and 2 j + 1
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x2[j] = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
   if (mx >= 0x7F80u) {
     sb = kScaleNaN;
-    code = 0x88888888u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) code[i] = 0x88888888u;
     return;
   }
-  if (sb == kScaleMax) {  // the one scale whose group may reach past 7 s
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a, b;
-      f2_unpack(x2[j], a, b);
-      x2[j] = f2_pack(fminf(fmaxf(a, -7.f * s), 7.f * s), fminf(fmaxf(b, -7.f * s), 7.f * s));
+  for (int i = 0; i < W; ++i) {
+    uint64_t x2[4];  // channels 2 j and 2 j + 1
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x2[j] = f2_pack(bf16_lo(w[i][j]), bf16_hi(w[i][j]));
+    if (sb == kScaleMax) {  // the one scale whose group may reach past 7 s
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a, b;
+        f2_unpack(x2[j], a, b);
+        x2[j] = f2_pack(fminf(fmaxf(a, -7.f * s), 7.f * s), fminf(fmaxf(b, -7.f * s), 7.f * s));
+      }
     }
+    code[i] = codes8(x2, inv);
   }
-  code = codes8(x2, inv);
+}
+template <int LPG>
+__device__ __forceinline__ void encode8(uint4 x, unsigned lanes, uint32_t& code, uint32_t& sb) {
+  const uint4 one[1] = {x};
+  uint32_t c[1];
+  encode<LPG>(one, lanes, c, sb);
+  code = c[0];
+}
+template <int LPG>
+__device__ __forceinline__ void encode16(const uint4 (&x)[2], unsigned lanes, uint2& code, uint32_t& sb) {
+  uint32_t c[2];
+  encode<LPG>(x, lanes, c, sb);
+  code = make_uint2(c[0], c[1]);
 }
 
 }  // namespace kv4

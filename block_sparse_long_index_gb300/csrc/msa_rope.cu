@@ -162,6 +162,34 @@ __device__ __forceinline__ uint4 turn8_bf16(uint4 w, int p, int lanes, const Rop
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
+// The same for a piece of 16 channels, where the halves of the pairs are whole pieces or side by side.
+__device__ __forceinline__ void turn16_bf16(uint4 (&w)[2], int p, int lanes, const Rope& rope, const float* c, int span) {
+  if (rope.interleaved) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = turn8_bf16(w[h], 2 * p + h, lanes, rope, c, span);
+    return;
+  }
+  const int hp = rope.rot / 32;  // pieces of a half
+  const bool first = p < hp, in = p < 2 * hp;
+  const int q = !in ? p : first ? p + hp : p - hp, src = ((int)(threadIdx.x & 31u) & ~(lanes - 1)) | q;
+  const uint32_t sign = first ? 0x80008000u : 0u;
+  const float* cp = c + 16 * (first ? p : q);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4] = {w[h].x, w[h].y, w[h].z, w[h].w}, o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = __shfl_sync(0xffffffffu, v[j], src) ^ sign;
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const ulonglong2 cj = reinterpret_cast<const ulonglong2*>(cp + 8 * h)[j], sj = reinterpret_cast<const ulonglong2*>(cp + span + 8 * h)[j];
+        v[2 * j] = narrow2(add2(mul2(widen2(v[2 * j]), cj.x), mul2(widen2(o[2 * j]), sj.x)));
+        v[2 * j + 1] = narrow2(add2(mul2(widen2(v[2 * j + 1]), cj.y), mul2(widen2(o[2 * j + 1]), sj.y)));
+      }
+      w[h] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
@@ -291,12 +319,61 @@ __device__ __forceinline__ void append_kind(const AppendRows& a, const Rows& io,
   turn = (turn - batches % kWarps + kWarps) % kWarps;  // the next kind begins where this one ended
 }
 
+// K or V into a 4-bit pool with 16 channels a thread: what a group's threads each work out for themselves (its scale), and
+// a piece's place, is done half as often as with 8.  The halves of K's pairs have to be whole pieces: rot a multiple of 32,
+// or pairs side by side.
+__host__ __device__ constexpr bool wide_turn(int rot, bool interleaved) { return interleaved || rot % 32 == 0; }
+template <int D, Kind K>
+__device__ __forceinline__ void append_codes(const AppendRows& a, const Rows& io, int64_t i0, int n, const int64_t* rows,
+                                             const float* cs, int& turn) {
+  constexpr int LPR = D / 16, LPG = LPR / kGroups, FLY = kFly / 2;
+  const int lane = threadIdx.x & 31, pieces = io.H_kv * LPR, chunks = (pieces + 31) / 32, tasks = n * chunks;
+  const int batches = (tasks + FLY - 1) / FLY;
+  const uint16_t* const src = K == kK ? a.k : a.v;
+  const int64_t stride = K == kK ? a.k_stride : a.v_stride;
+  uint8_t* const codes = K == kV ? io.pool.v_codes : io.pool.k_codes;
+  uint8_t* const scales = K == kV ? io.pool.v_scales : io.pool.k_scales;
+  const unsigned group = ((1u << LPG) - 1u) << (lane & ~(LPG - 1));
+  for (int batch = turn; batch < batches; batch += kWarps) {
+    int c = batch * FLY / n, t = batch * FLY - c * n;  // the tokens of a chunk one after the other
+    uint4 w[FLY][2];
+    int tok[FLY], piece[FLY];  // piece -1 - e where this lane has none
+#pragma unroll
+    for (int u = 0; u < FLY; ++u) {
+      const int e = c * 32 + lane;
+      const bool on = c < chunks && e < pieces && rows[t] >= 0;
+      const uint16_t* p = src + (i0 + t) * stride + e * 16;
+      w[u][0] = on ? ld_once(p) : make_uint4(0u, 0u, 0u, 0u);
+      w[u][1] = on ? ld_once(p + 8) : make_uint4(0u, 0u, 0u, 0u);
+      tok[u] = t;
+      piece[u] = on ? e : -1 - e;
+      if (++t == n) t = 0, ++c;
+    }
+#pragma unroll
+    for (int u = 0; u < FLY; ++u) {
+      if (batch * FLY + u >= tasks) break;  // (uniform in the warp)
+      const bool on = piece[u] >= 0;
+      const int e = on ? piece[u] : -1 - piece[u];
+      if (K == kK) turn16_bf16(w[u], e & (LPR - 1), LPR, a.rope, cs + 2 * tok[u] * kSpan, kSpan);
+      uint2 code;
+      uint32_t sb;
+      encode16<LPG>(w[u], group, code, sb);
+      if (on) {
+        const int64_t row = rows[tok[u]];
+        reinterpret_cast<uint2*>(codes)[row * pieces + e] = code;
+        if (e % LPG == 0) scales[row * (io.H_kv * kGroups) + e / LPG] = (uint8_t)sb;
+      }
+    }
+  }
+  turn = (turn - batches % kWarps + kWarps) % kWarps;
+}
+
 // A CTA takes `toks` packed tokens: it looks up their places, works out their cos and sin, and its warps then go
 // through the tokens' chunks with four reads in flight.  K is rounded to bf16 once turned, then stored or quantized, so
 // that the cache holds what turning and storing in two calls would leave.  Bound: HBM, rows in and out once; few
 // tokens by the launch and the chain look-up, angles, rows.  Measured, 131072 tokens of 8 heads, d = 128, with index keys:
-// into bf16 pages 179 us (0.89 of the copy rate), into 4-bit pages 250 us, where the issue slots are 71 % busy with the
-// angles, the turns and the codes; 48 tokens with 32 query heads: 7 us.
+// into bf16 pages 179 us (0.89 of the copy rate), into 4-bit pages 207 us (0.49), where the issue slots are busy with the
+// angles, the turns and the codes (250 us with 8 channels a thread for K and V too); 48 tokens with 32 query heads: 7 us.
 template <int D, bool KV4>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64_t N, int toks, RowMap map, uint16_t* k_pool,
                                                              uint16_t* v_pool, Kv4Pool pool, DeviceStatus* st) {
@@ -315,8 +392,10 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(AppendRows a, int64
   const Rows io = {a.H_kv, k_pool, v_pool, pool};
   int turn = threadIdx.x >> 5;  // a batch of one kind after the other goes to the warps in turn
   if (a.q) append_kind<D, KV4, kQ>(a, io, a.H_q * LPR, i0, n, rows, cs[0], turn);
-  append_kind<D, KV4, kK>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
-  append_kind<D, KV4, kV>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
+  if (KV4 && wide_turn(a.rope.rot, a.rope.interleaved)) append_codes<D, kK>(a, io, i0, n, rows, cs[0], turn);
+  else append_kind<D, KV4, kK>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
+  if (KV4) append_codes<D, kV>(a, io, i0, n, rows, cs[0], turn);
+  else append_kind<D, KV4, kV>(a, io, a.H_kv * LPR, i0, n, rows, cs[0], turn);
   const float* cs_idx = cs[a.rope_idx_own ? 1 : 0];
   if (a.q_idx) append_kind<D, KV4, kQI>(a, io, a.H_kv * (a.d_I / 8), i0, n, rows, cs_idx, turn);
   if (a.k_idx) append_kind<D, KV4, kKI>(a, io, a.d_I / 8, i0, n, rows, cs_idx, turn);
