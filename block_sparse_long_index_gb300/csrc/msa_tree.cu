@@ -13,11 +13,12 @@
 // a fifth of its rate.  tree_context_kernel does a tile by tcgen05, S = Q K^T and O += P V
 // with 128 query rows, Q and K, V in shared memory, S / P and O in TMEM.  Two streams of it alternate, so that one's
 // softmax runs under the other's products:
-//   up to 128 rows, and over a 4-bit cache always (up to 32 rows there mostly take another form, msa_tree_few.cu): one query tile, whose even and odd key tiles are the streams (their O
+//   up to 128 rows, and over a 4-bit cache always: one query tile, whose even and odd key tiles are the streams (their O
 //   are merged at the run's end);
 //   more rows over bf16 pages: two query tiles over the same keys.  (4-bit pages are expanded again for each 128 rows: a
 //   tile's softmax takes as long, and the room of the second query tile holds the codes in flight.)
 // Rows of a tile past the last one are computed on by the tensor cores alone; warps without a row rest.
+// Over a 4-bit cache up to 32 rows of up to 8 K/V heads have a kernel of their own (msa_tree_few.cu).
 //
 // Measured, with the join: bf16 pages, 128 rows, 4 sequences of 262144 tokens: 636 us, HBM's rate (a tile takes 1955
 // cycles where the caches stay in L2, 2825 from HBM); 256 rows, 16 sequences of 1200 to 12000 tokens: 128 us, 0.51 of HBM
@@ -740,8 +741,9 @@ __global__ void __launch_bounds__(ctx_threads(KV4), 1) tree_context_kernel(
           if (live)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(po + part_at(sh.RU, 0, c * 16 + 4 * e)) = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                          __uint_as_float(o[4 * e + 3]));
+              *reinterpret_cast<float4*>(po + part_at(sh.RU, 0, c * 16 + 4 * e)) =
+                  make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                              __uint_as_float(o[4 * e + 3]));
         }
         if (live && part == 0) w.part_ml[slot + lr] = make_float2(M, sum);
       }
@@ -1001,7 +1003,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
   if (T > 0 && n > 0) {
     const int64_t quota = w.starts[sh.B], f0 = w.starts[b];
     c0 = (int)(f0 / quota) * sh.ways;
-    c1 = (int)((f0 + (n - 1) / kKeysT) / quota) * sh.ways + sh.ways - 1;
+    c1 = (int)((f0 + ((n - 1) >> sh.lg)) / quota) * sh.ways + sh.ways - 1;
   }
   // the CTA's rows are of one unit (groups of rows are multiples of 64): its first one there, its partials
   const int rg = r_cta / sh.RU;
@@ -1150,6 +1152,8 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
   sh.groups = p.groups;
   sh.rounds = p.rounds;
   sh.ways = p.ways;
+  sh.lg = p.few ? few_lg(p.B, sh.cap) : 7;
+  static_assert(kKeysT == 1 << 7, "a tile");
   if (p.few) {
     if ((e = launch_tree_few(q, sh, map, pool, D, sl2, w, st, s)) != cudaSuccess) return e;
   } else {

@@ -15,6 +15,7 @@ struct TreeShape {
   int RG, RU;          // row groups of a (sequence, K/V head), rows of one
   int groups, rounds;  // see tree_plan
   int ways;            // partials of a (segment, unit)
+  int lg;              // log2 of the tokens of an entry of the list that is split into runs (7: tiles)
   // Nodes and context of sequence b; bad lengths count as none of either.
   __device__ __forceinline__ bool lengths(int b, int& n, int& t) const {
     n = ctx[b];
@@ -30,13 +31,20 @@ struct TreeShape {
     lengths(b, n, t);
     return t ? (int)(((int64_t)n + kKeysT - 1) / kKeysT) : 0;
   }
+  __device__ __forceinline__ int spans(int b) const {
+    int n, t;
+    lengths(b, n, t);
+    return t ? (int)(((int64_t)n + (1 << lg) - 1) >> lg) : 0;
+  }
 };
 
 // Scratch of a call: what the context kernel leaves for the joining one.
 struct TreeScratch {
-  int64_t* starts;       // [B + 1] tiles before each sequence, then those of a run
+  int64_t* starts;       // [B + 1] entries of the list before each sequence, then those of a run
   unsigned int* errors;  // [CTAs] flags each met
-  float* part_o;         // [slots][D / 8][RU][8] (a lane of the context kernel has a row, one of the joining one channels); slot = ((sequence + group) ways + way) units + unit, which no two segments share
+  // [slots][D / 8][RU][8] (a lane of the context kernel has a row, one of the joining kernel channels); slot =
+  // ((sequence + group) ways + way) units + unit, which no two segments share
+  float* part_o;
   float2* part_ml;       // [slots][RU] maximum (log2 units) and sum
 };
 // Channel ch of row r in a slot's partial O.
@@ -46,6 +54,7 @@ __device__ __forceinline__ int part_at(int RU, int r, int ch) { return ((ch >> 3
 constexpr int kFewRows = 32, kFewHeads = 8;
 int few_ctas(int rows);
 int few_ways(int H_kv);
+int few_lg(int B, int64_t cap);
 cudaError_t launch_tree_few(const void* q, const TreeShape& sh, const CacheMap& map, const Kv4Pool& pool, int d, float scale_log2,
                             const TreeScratch& w, DeviceStatus* st, cudaStream_t s);
 

@@ -1,17 +1,18 @@
 // The context of drafted trees over a 4-bit cache where a K/V head has few rows (T gs up to 32), as partial softmaxes.
 //
-// As in the other form the sequences' 128-token tiles are one list, a CTA has an equal run of it.  As in the dense decode
-// over this cache its 8 warps take H heads x 8 / H pairs of 16-token units at a time (a step, from a ring that TMA fills),
-// and codes become mma.sync m16n8k16 operands in registers:
+// The sequences' 32-token spans are one list, a CTA has an equal run of it.  As in the dense decode over this cache its 8
+// warps take H heads x 8 / H pairs of 16-token units at a time (a step, from a ring that TMA fills), and codes become mma.sync
+// m16n8k16 operands in registers:
 //   S^T [16 tokens x 8 NT rows] = K q^T,  O^T [d x 8 NT rows] += V^T P^T,
 // an expanded K or V operand serving the NT groups of 8 rows.  q's operands lie in shared memory where NT > 1 leaves no
 // registers for them.  tcgen05's 128-row tile, for which codes have to be expanded into shared memory by warps that wait
 // for one another, takes as long for any number of rows up to 32 (2630 cycles a tile of 128 tokens of a head).
 //
 // Measured with the join, 8 heads, d = 128, tcgen05's form in brackets: 4 sequences of 2^20 tokens, 8 rows a head 817 us
-// (2400; 0.84 of HBM's rate, which bounds it), 16 rows 1094 us, 32 rows 1640 us (0.42 of HBM: 1806 cycles a tile and head, of
-// which the products need 1024; with registers for two warps a scheduler, what is left is latency); 16 sequences of
-// 15000 to 30000 tokens, 32 rows 169 us (226), 16 rows 116 us, 8 rows 93 us.
+// (2293; 0.84 of HBM's rate, which bounds it), 16 rows 1094 us (2288), 32 rows 1640 us (2297; 0.42 of HBM: 1806 cycles a tile
+// and head, of which the products need 1024; with registers for two warps a scheduler, what is left is latency); 16 sequences
+// of 15000 to 30000 tokens, 32, 16, 8 rows 169, 116, 93 us (226, 225, 225); 64 of 250 to 500 tokens, 16 and 4 rows 29, 21 us
+// (42, 40); one of 1500 tokens, 32, 16, 4 rows 22, 17, 14 us (20, 17, 17).
 #include <math.h>
 
 #include "msa_kv4_units.cuh"
@@ -49,32 +50,33 @@ __device__ __forceinline__ void sts_16(uint32_t at, uint4 y) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
 }
 
-// A CTA's run of the list of tiles (128 tokens), and segment by segment units [u0, u1) of one sequence.
-constexpr int kTileUnits = kKeysT / kUnit;
+// A CTA's run of the list of spans (32 tokens), and segment by segment units [u0, u1) of one sequence.
+constexpr int kLgUnit = 4;
 struct Run {
-  int f, f1, before;  // next tile, end, tiles before sequence `seq` (all tiles fit an int)
+  int f, f1, before;  // next span, end, spans before sequence `seq` (all spans fit an int)
   int seq, len, u0, u1;
   __device__ __forceinline__ bool next(const TreeShape& sh) {
     if (f >= f1) return false;
     int n, t;
-    while (f >= before + (n = sh.tiles(seq))) before += n, ++seq;  // (ends: the runs add up to all tiles)
+    while (f >= before + (n = sh.spans(seq))) before += n, ++seq;  // (ends: the runs add up to all spans)
     sh.lengths(seq, len, t);
     const int t0 = f - before, t1 = min(f1 - before, n);
-    u0 = t0 * kTileUnits;
-    u1 = min(t1 * kTileUnits, (len - 1) / kUnit + 1);  // (a sequence with tiles is not empty)
+    u0 = t0 << (sh.lg - kLgUnit);
+    u1 = min(t1 << (sh.lg - kLgUnit), (len - 1) / kUnit + 1);  // (a sequence with spans is not empty)
     f += t1 - t0;
     return true;
   }
 };
 
-// The run of the CTA, a multiple of `step` tiles.  Every thread takes part.  CTA 0 writes starts.
+// The run of the CTA, a multiple of a step's spans where it has as many: shorter ones leave warps idle, but spread a small
+// list over more CTAs.  Every thread takes part.  CTA 0 writes starts.
 __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* starts) {
   __shared__ int64_t sums[kDecWarps];
   __shared__ int seq_s, before_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sh.B + kDecThreads - 1) / kDecThreads, b0 = min(tid * per, sh.B), b1 = min(b0 + per, sh.B);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += sh.tiles(b);
+  for (int b = b0; b < b1; ++b) mine += sh.spans(b);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -90,12 +92,13 @@ __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* 
     if (w < warp) off += x;
     total += x;
   }
-  const int64_t quota = max(quota_of(total, gridDim.x, step), (int64_t)step);
+  int64_t quota = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
+  if (quota > step) quota = quota_of(total, gridDim.x, step);
   const int64_t first = off + incl - mine, at = blockIdx.x * quota;
-  if (at >= first && at < first + mine) {  // (nobody where the CTA has no tiles)
+  if (at >= first && at < first + mine) {  // (nobody where the CTA has no spans)
     int64_t x = first;
     int b = b0, n;
-    while (at >= x + (n = sh.tiles(b))) x += n, ++b;
+    while (at >= x + (n = sh.spans(b))) x += n, ++b;
     seq_s = b;
     before_s = (int)x;
   }
@@ -103,7 +106,7 @@ __device__ __forceinline__ Run find_run(const TreeShape& sh, int step, int64_t* 
     int64_t x = first;
     for (int b = b0; b < b1; ++b) {
       starts[b] = x;
-      x += sh.tiles(b);
+      x += sh.spans(b);
     }
     if (tid == 0) starts[sh.B] = quota;
   }
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kDecThreads, Few<NT>::CTAS) tree_few_kernel(
     }
   }
   volatile int* abort = &abort_flag;
-  Run run = find_run(sh, SU > kTileUnits ? SU / kTileUnits : 1, w.starts);
+  Run run = find_run(sh, max(SU >> (sh.lg - kLgUnit), 1), w.starts);
   const float kInf = __int_as_float(0x7f800000);
   constexpr int kV = SU * HC * X::BYTES, kScales = 2 * kV;  // offsets of V's codes and of the scales in a stage
   const int sc_unit = kUnit * H_kv * kGroups, sc_half = sc_unit / 2;
@@ -441,6 +444,8 @@ cudaError_t launch_h(const void* q, const TreeShape& sh, const CacheMap& map, co
 
 int few_ctas(int rows) { return num_sms() * (rows <= 8 ? Few<1>::CTAS : rows <= 16 ? Few<2>::CTAS : Few<4>::CTAS); }
 int few_ways(int H_kv) { return kDecWarps / heads_of(H_kv); }
+// Spans of 32 tokens where a batch's fit an int, else of 128 (whose number the caller has checked).
+int few_lg(int B, int64_t cap) { return (cap + 31) / 32 < ((int64_t)1 << 31) / B ? 5 : 7; }
 
 cudaError_t launch_tree_few(const void* q, const TreeShape& sh, const CacheMap& map, const Kv4Pool& pool, int d, float scale_log2,
                             const TreeScratch& w, DeviceStatus* st, cudaStream_t s) {

@@ -360,3 +360,16 @@ def test_many_sequences_in_4_bits():
         out, lse = c.run()
         assert c.dec.device_status() == 0
         c.check(out, lse, only=[0, 1, 2, 255, 256, 257, 511, 898, 899] + [int(i) for i in r.integers(0, 900, 12)])
+
+
+def test_room_for_more_spans_than_an_int_counts():
+    """A table whose width alone, times the sequences, asks for the coarser split of the 4-bit form's list."""
+    r = np.random.default_rng(25)
+    ctx = [int(x) for x in r.integers(0, 300, 1024)]
+    c = Case("kv4", ctx, 2, 2, 1, 64, 256, "chain", seed=25)
+    wide = torch.full((c.B, 1 << 18), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    out, lse = c.run()
+    assert c.dec.device_status() == 0
+    c.check(out, lse, only=[0, 1, 511, 512, 1022, 1023] + [int(i) for i in r.integers(0, 1024, 12)])
