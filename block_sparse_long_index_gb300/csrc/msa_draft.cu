@@ -11,16 +11,18 @@
 // 8 CTAs a sequence: each of its warps has one run of the vocabulary, a pass over a row leaves every run's sum in shared
 // memory, and the last pass's sums find the run, then the token, without another pass over the row.
 //
-// Which token is drawn hangs on comparisons of sums, so these are held to some 43 bits: each difference p - c q is an fp32
-// and its error, a lane's sum likewise, and all sums above a lane's are integers of 2^-48, which add up the same in any
-// order.  (64-bit floating point throughout would be bound by the few units for it; fp32 sums draw another token in one of
-// a thousand cases at 128000 tokens.)
+// Which token is drawn hangs on comparisons of sums, and a vocabulary may be long: each difference p - c q is worked out as
+// an fp32 and its error and counted in units of 2^-58 (exactly from p = 2^-35 on), and the counts are added as integers.
+// They add up the same in any order and however a row is split, so that a tree's outcome does not hang on the batch it is
+// in, and the sum of V tokens is off by V 2^-59 at most.  (64-bit floating point would be bound by the few units for it;
+// fp32 sums draw another token in one of a thousand cases at 128000 tokens.)
 //
 // Measured: 64 trees of 24 nodes over 128000 tokens 46 us (0.21 of HBM, a few passes in a row of 4 us each; 22 us where one
 // pass is all); one tree of 6 over 50001 tokens 12 us.
 #include <math.h>
 
 #include "msa_common.cuh"
+#include "msa_sm100.cuh"
 
 namespace msa {
 
@@ -29,14 +31,43 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kMaxNodes = 64;
 constexpr int kFly = 2;  // vectors of each row that a lane has in flight (3 and 4 are slower: 48 and 51 us for 46)
-constexpr double kUnit = 281474976710656.0;  // 2^48
+constexpr double kUnit = 288230376151711744.0;           // 2^58
+constexpr long long kMost = (1ll << 62) - 1;             // where sums stay: 16, far above a distribution's
 
 // A probability: what is not a positive finite number counts as 0.
 __device__ __forceinline__ float prob(float x) { return x > 0.f && x <= 3.402823466e38f ? x : 0.f; }
 
-// (x + err) 2^48 as an integer, for sums of lanes (2 at most: 8192 lanes' fit, and a distribution's lane holds no more).
-__device__ __forceinline__ long long fixed(float x, float err) {
-  return __float2ll_rn(fminf(x, 2.f) * (float)kUnit) + __float2ll_rn(fminf(err, 1.f) * (float)kUnit);
+// Sums of counts of what is no distribution stop at kMost, in any order (all counts are 0 or more).
+__device__ __forceinline__ long long add_up(long long a, long long b) { return min(a + b, kMost); }
+__device__ __forceinline__ long long warp_sum(long long d) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) d = add_up(d, __shfl_xor_sync(0xffffffffu, d, o));
+  return d;
+}
+// The sum of the warp's lanes up to this one.
+__device__ __forceinline__ long long warp_scan(long long d) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, d, o);
+    if (lane >= o) d = add_up(d, t);
+  }
+  return d;
+}
+
+// x + err, 0 <= x <= 2 and |err| <= 2^-22, in units of 2^-58.  Adding 1.5 2^(23 - k) rounds to a multiple of 2^-k that is
+// found in the sum's last bits; what is left goes on to the next k: 21, 44, 58.  err joins in at the second step, and what is
+// left of both is added in fp32 (to 2^-68).  Only the last step rounds.
+constexpr float kStep1 = 6.f, kStep2 = 7.152557373046875e-7f, kStep3 = 4.3655745685100555e-11f;  // 1.5 2^2, 2^-21, 2^-35
+constexpr uint32_t kBits1 = 0x40C00000u, kBits2 = 0x35400000u, kBits3 = 0x2E400000u;             // their bits
+constexpr int kShift1 = 58 - 21, kShift2 = 58 - 44;
+__device__ __forceinline__ long long counted(float x, float err) {
+  const float t = __fadd_rn(x, kStep1), r = __fsub_rn(x, __fsub_rn(t, kStep1));
+  const float u = __fadd_rn(r, kStep2), s = __fsub_rn(r, __fsub_rn(u, kStep2));
+  const float eu = __fadd_rn(err, kStep2), es = __fsub_rn(err, __fsub_rn(eu, kStep2));
+  const float w = __fadd_rn(__fadd_rn(s, es), kStep3);
+  return (int)(__float_as_uint(t) - kBits1) * (1ll << kShift1) +
+         (int)(__float_as_uint(u) + __float_as_uint(eu) - 2 * kBits2) * (1ll << kShift2) + (int)(__float_as_uint(w) - kBits3);
 }
 
 struct VerifyArgs {
@@ -155,14 +186,15 @@ struct Residual {
     V = args.V;
     skew = (int)(at & 3);
   }
-  // The vector's r, one by one and clean, as integers.
+  // The vector's r, one by one and clean, in units.  (Where p is a probability nothing is cut off.)
   __device__ __forceinline__ void each(int64_t v, const float4& a, const float4& b, long long (&d)[4]) const {
+    constexpr float kErr = 2.384185791015625e-7f;  // 2^-22
     const float pv[4] = {a.x, a.y, a.z, a.w}, qv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x, err;
       const bool on = q ? rest_of<kTimes>(prob(pv[j]), prob(qv[j]), ch, cl, x, err) : rest_of<kPlain>(prob(pv[j]), 0.f, 0.f, 0.f, x, err);
-      d[j] = on ? fixed(x, err) : 0;
+      d[j] = on ? max(counted(fminf(x, 2.f), fminf(fmaxf(err, -kErr), kErr)), 0ll) : 0;
     }
     for (int i = 0; i < n_out; ++i) {
       const int64_t at = (int64_t)out[i] + skew - v * 4;
@@ -173,52 +205,93 @@ struct Residual {
   }
 };
 
-// A lane's sum over the vectors v0 + lane, + 32, .. below v1.  The running sum begins at 2, above every probability, so that
-// the error of adding x to it is x - (sum - before); a value above 1 sends the lane through its vectors again, one by one.
+// The three steps' last bits of a lane's elements, added up (modulo 2^32; an element of 0 leaves the steps' own bits).
+struct Counts {
+  uint32_t a, b, c;
+};
+// A pair of elements, clean: counted() of both at once.
+template <Form F>
+__device__ __forceinline__ void count2(float p0, float p1, float q0, float q1, float ch, float cl, Counts& n) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  uint64_t x, err = 0ull;
+  if (F == kPlain) {
+    x = f2_pack(p0, p1);
+  } else if (F == kOnce) {
+    const uint64_t p = f2_pack(p0, p1), q = f2_pack(fminf(q0, p0), fminf(q1, p1));  // (p - p: 0, and no error)
+    x = f2_fma(q, minus, p);
+    err = f2_fma(q, minus, f2_fma(x, minus, p));
+  } else {
+    float x0, x1, e0, e1;
+    if (!rest_of<F>(p0, q0, ch, cl, x0, e0)) x0 = e0 = 0.f;
+    if (!rest_of<F>(p1, q1, ch, cl, x1, e1)) x1 = e1 = 0.f;
+    x = f2_pack(x0, x1);
+    err = f2_pack(e0, e1);
+  }
+  auto add_bits = [](uint32_t& sum, uint64_t v) { sum += (uint32_t)v + (uint32_t)(v >> 32); };
+  const uint64_t t = f2_add(x, f2_pack(kStep1, kStep1)), r = f2_fma(f2_add(t, f2_pack(-kStep1, -kStep1)), minus, x);
+  const uint64_t u = f2_add(r, f2_pack(kStep2, kStep2));
+  uint64_t s = f2_fma(f2_add(u, f2_pack(-kStep2, -kStep2)), minus, r);
+  add_bits(n.a, t);
+  add_bits(n.b, u);
+  if (F != kPlain) {
+    const uint64_t eu = f2_add(err, f2_pack(kStep2, kStep2));
+    s = f2_add(s, f2_fma(f2_add(eu, f2_pack(-kStep2, -kStep2)), minus, err));
+    add_bits(n.b, eu);
+  }
+  add_bits(n.c, f2_add(s, f2_pack(kStep3, kStep3)));
+}
+
+// A lane's sum over the vectors v0 + lane, + 32, .. below v1.  A value above 1 sends the lane through its vectors again, one
+// by one.
 template <Form F>
 __device__ __forceinline__ long long lane_sum(const Residual& r, int64_t v0, int64_t v1) {
+  constexpr uint32_t kEach = 4 * kFly, kTimesB = F == kPlain ? 1 : 2;
+  constexpr int kFlush = 32;  // the counts of as many rounds fit 32 bits: 256 elements of 2^21 and of 2^22 + 2^21
   const int lane = threadIdx.x & 31;
-  float hi = 2.f, lo = 0.f, most = 0.f;
-  for (int64_t v = v0 + lane; v < v1; v += 32 * kFly) {
-    float4 a[kFly], b[kFly];
+  float most = 0.f;
+  long long sum = 0;
+  for (int64_t v = v0 + lane; v < v1;) {
+    Counts n = {0u, 0u, 0u};
+    uint32_t rounds = 0;
+    for (; rounds < kFlush && v < v1; ++rounds, v += 32 * kFly) {
+      float4 a[kFly], b[kFly];
 #pragma unroll
-    for (int u = 0; u < kFly; ++u) r.load<F>(v + 32 * u, v1, a[u], b[u]);
+      for (int u = 0; u < kFly; ++u) r.load<F>(v + 32 * u, v1, a[u], b[u]);
 #pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      float pv[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
-      const float qv[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
-      if (F == kPlain)
-        for (int i = 0; i < r.n_out; ++i) {
-          const int64_t at = (int64_t)r.out[i] + r.skew - (v + 32 * u) * 4;
+      for (int u = 0; u < kFly; ++u) {
+        float p[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, q[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+        if (F == kPlain)
+          for (int i = 0; i < r.n_out; ++i) {
+            const int64_t at = (int64_t)r.out[i] + r.skew - (v + 32 * u) * 4;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (at == j) pv[j] = 0.f;
+            for (int j = 0; j < 4; ++j)
+              if (at == j) p[j] = 0.f;
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[j] = fmaxf(p[j], 0.f), q[j] = fmaxf(q[j], 0.f);  // (a NaN as 0)
+          most = fmaxf(most, F == kPlain ? p[j] : fmaxf(p[j], q[j]));
         }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x, err;
-        const float p = fmaxf(pv[j], 0.f), q = fmaxf(qv[j], 0.f);  // (a NaN as 0)
-        most = fmaxf(most, F == kPlain ? p : fmaxf(p, q));
-        if (rest_of<F>(p, q, r.ch, r.cl, x, err)) {
-          const float s = __fadd_rn(hi, x);
-          lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(x, __fsub_rn(s, hi)), err));
-          hi = s;
-        }
+        count2<F>(p[0], p[1], q[0], q[1], r.ch, r.cl, n);
+        count2<F>(p[2], p[3], q[2], q[3], r.ch, r.cl, n);
       }
     }
+    n.a -= rounds * (kEach * kBits1);
+    n.b -= rounds * (kEach * kTimesB * kBits2);
+    n.c -= rounds * (kEach * kBits3);
+    sum = add_up(sum, min((int)n.a, 1 << 24) * (1ll << kShift1) + (int)n.b * (1ll << kShift2) + (int)n.c);
   }
   if (!(most <= 1.f)) {  // no distribution, or an infinity
-    long long sum = 0;
+    sum = 0;
     for (int64_t v = v0 + lane; v < v1; v += 32) {
       float4 a, b;
       r.load<F>(v, v1, a, b);
       long long d[4];
       r.each(v, a, b, d);
-      sum = min(sum + (d[0] + d[1]) + (d[2] + d[3]), (long long)(2 * kUnit));
+      sum = add_up(sum, add_up(add_up(d[0], d[1]), add_up(d[2], d[3])));
     }
-    return sum;
   }
-  return fixed(hi - 2.f, lo);
+  return sum;
 }
 
 // What a CTA does next: one thread's decision, in 64 bits (all threads of a CTA would queue for the few units there are
@@ -335,14 +408,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
       long long d = step_s.form == kPlain ? lane_sum<kPlain>(r, run.v0, run.v1)
                     : step_s.form == kOnce ? lane_sum<kOnce>(r, run.v0, run.v1)
                                            : lane_sum<kTimes>(r, run.v0, run.v1);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      d = warp_sum(d);
       if (lane == 0) seg_s[passes & 1][warp] = d;
       __syncthreads();
       if (warp == 0) {
-        d = lane < kWarps ? seg_s[passes & 1][lane] : 0;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        d = warp_sum(lane < kWarps ? seg_s[passes & 1][lane] : 0);
         if (lane == 0) cta_s[passes & 1] = d;
       }
       cluster_sync();  // (and whoever read the buffer two passes ago is done)
@@ -350,7 +420,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
       __syncthreads();
       total = 0;
 #pragma unroll
-      for (int k = 0; k < kCluster; ++k) total += all_s[k];
+      for (int k = 0; k < kCluster; ++k) total = add_up(total, all_s[k]);
       ++passes;
     }
   }
@@ -377,20 +447,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
 #pragma unroll
     for (int i = 0; i < kCluster; ++i) {
       const long long x = all_s[i];
-      if (!done && before + x > target) k = i, done = true;
-      if (!done) before += x;
+      if (!done && add_up(before, x) > target) k = i, done = true;
+      if (!done) before = add_up(before, x);
     }
     if (done && k == rank) {  // (it is: the sums add up to the total)
       // the warps' runs likewise, a lane each
+      auto first_past = [&](long long of_lane, long long at) {  // of the lanes' sums, from `at` on; -1: none
+        return __ffs(__ballot_sync(0xffffffffu, add_up(at, warp_scan(of_lane)) > target)) - 1;
+      };
+      auto up_to = [&](long long of_lane, int n) { return warp_sum(lane < n ? of_lane : 0); };  // the first n lanes' sum
       const long long mine = lane < kWarps ? seg_s[buf][lane] : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      const int w = __ffs(__ballot_sync(0xffffffffu, before + incl > target)) - 1;
-      before += __shfl_sync(0xffffffffu, incl - mine, w);
+      const int w = first_past(mine, before);
+      before = add_up(before, up_to(mine, w));
       // all warps take a part of that run each: the part, then its element.  (One warp through the whole run: 64 trees 53 us
       // instead of 46.)
       const Step step = step_s;
@@ -405,53 +473,36 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
         if (r.q) r.load<kTimes>(v, end_v, pa, qa);
         else r.load<kPlain>(v, end_v, pa, qa);
         r.each(v, pa, qa, d);
-        return (d[0] + d[1]) + (d[2] + d[3]);
+        return add_up(add_up(d[0], d[1]), add_up(d[2], d[3]));
       };
       long long d[4], sum = 0;
 #pragma unroll 4
-      for (int64_t v = first_v + lane; v < end_v; v += 32) sum += load(v, d);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int64_t v = first_v + lane; v < end_v; v += 32) sum = add_up(sum, load(v, d));
+      sum = warp_sum(sum);
       if (lane == 0) seg_s[buf ^ 1][warp] = sum;  // (the pass before the last one's are read)
       __syncthreads();
       const long long part = lane < kWarps ? seg_s[buf ^ 1][lane] : 0;
-      incl = part;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + incl > target), some = __ballot_sync(0xffffffffu, part > 0);
-      // (the elements' sums may round below their lanes': then the last element with a share)
-      const int wp = past ? __ffs(past) - 1 : 31 - __clz(some | 1u);
+      const int wp = first_past(part, before);  // (there is one: the parts add up to the run)
       if (warp == wp) {
-        sum = before + __shfl_sync(0xffffffffu, incl - part, wp);
-        int64_t last = -1, hit = -1;
+        sum = add_up(before, up_to(part, wp));
+        int64_t hit = -1;
         for (int64_t v0 = first_v; v0 < end_v && hit < 0; v0 += 32) {
           const int64_t v = v0 + lane;
           const long long of_lane = load(v, d);
-          long long up = of_lane;
+          const int at_lane = first_past(of_lane, sum);
+          if (at_lane >= 0) {
+            long long x = add_up(sum, up_to(of_lane, at_lane));
+            int64_t e = -1;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, up, o);
-            if (lane >= o) up += t;
-          }
-          long long x = sum + (up - of_lane);
-          int64_t first = -1, end = -1;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x += d[j];
-            if (d[j] > 0) {
-              end = v * 4 - r.skew + j;
-              if (first < 0 && x > target) first = end;
+            for (int j = 0; j < 4; ++j) {
+              x = add_up(x, d[j]);
+              if (e < 0 && x > target) e = v * 4 - r.skew + j;
             }
+            hit = __shfl_sync(0xffffffffu, e, at_lane);
           }
-          const unsigned found = __ballot_sync(0xffffffffu, first >= 0), share = __ballot_sync(0xffffffffu, end >= 0);
-          if (found) hit = __shfl_sync(0xffffffffu, first, __ffs(found) - 1);
-          if (share) last = __shfl_sync(0xffffffffu, end, 31 - __clz(share));
-          sum += __shfl_sync(0xffffffffu, up, 31);
+          sum = add_up(sum, warp_sum(of_lane));
         }
-        if (lane == 0) a.next[b] = (int32_t)(hit >= 0 ? hit : last);
+        if (lane == 0) a.next[b] = (int32_t)hit;
       }
     }
   }

@@ -678,9 +678,13 @@ msa_status_t msa_append_paged_kv4(const msa_append_t* rows, int64_t N, const int
  *   path   [B, T] int32 out: the accepted nodes in order, node 0 first, then -1
  *   n_path [B] int32 out: their number (0 where tree_len is 0)
  *   next   [B] int32 out: the next token (-1 where tree_len is 0 or p holds nothing)
- * Sums are held to 2^-42 or so (each of at most 8192 parts to 2^-48).  A parent outside [-1, j) or a child's token outside
- * [0, V) takes the node out, a tree_len outside [0, T] counts as 0; both set the
- * device error word.  Supported: 1 <= V < 2^31, B <= 2^20.  workspace: msa_verify_workspace() bytes.
+ * Each r is counted in units of 2^-58 (exactly for c = 0 or 1 where p and q are 0 or
+ * at least 2^-35, otherwise to 2^-59 and 2^-46 p), and the counts are added as
+ * integers: a tree's outcome is the same in any batch.  (In a row that is no
+ * distribution a value counts 2 at most, a sum 16.)  A parent outside [-1, j) or a
+ * child's token outside [0, V) takes the node out, a tree_len outside [0, T] counts
+ * as 0; both set the device error word.  Supported: 1 <= V < 2^31, B <= 2^20.
+ * workspace: msa_verify_workspace() bytes.
  */
 size_t msa_tree_decode_workspace(int B, int T, int H_q, int H_kv, int d);
 msa_status_t msa_tree_decode_paged(const void* q, const msa_kv_pool_t* pool, const int32_t* page_table,
