@@ -1181,7 +1181,8 @@ cudaError_t launch_t(const void* q, const TreePlan& p, const void* k_pool, const
         return cudaErrorInvalidValue;
     }
     auto kern = tree_context_kernel<D, KV4>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(two, KV4));
+    // the most that any call needs: another thread's call must not lower it before this one's launch
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(!KV4, KV4));
     if (e != cudaSuccess) return e;
     kern<<<p.ctas, ctx_threads(KV4), L::smem(two, KV4), s>>>(*reinterpret_cast<const CUtensorMap*>(tq), *reinterpret_cast<const CUtensorMap*>(tk),
                                                        *reinterpret_cast<const CUtensorMap*>(tv), sh, map, pool, box_rows,
