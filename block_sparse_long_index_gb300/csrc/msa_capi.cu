@@ -25,6 +25,13 @@ int num_sms() {
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  // The driver's call fails in a thread without a context, and asking for the device does not give it one: setting it does.
+  thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
+    bound = true;
+  }
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;

@@ -1,4 +1,5 @@
 """Calls of two host threads at once, each with an object, tensors and a stream of its own."""
+import ctypes
 import threading
 
 import pytest
@@ -32,15 +33,57 @@ def at_once(*calls, times=2000):
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_trees_of_few_and_of_many_rows(d):
-    """One and two query tiles need different amounts of shared memory of one kernel."""
+    """One and two query tiles need different amounts of shared memory of one kernel.  (Calls of the C function itself: Python
+    threads run side by side within it alone.)"""
+    from block_sparse_long_index_gb300 import msa
     from test_gpu_tree import Case
     cases = [Case("bf16", [50, 3], T, 8, 2, d, 16, seed=T) for T in (2, 40)]
     want = [[t.clone() for t in c.run()] for c in cases]
     runs = []
     for c in cases:
-        ctx, par, s = i32(c.ctx), i32(c.parents), torch.cuda.Stream()
-        runs.append(lambda c=c, ctx=ctx, par=par, s=s: c.dec(c.q, c.table, ctx, par, None, c.scale, stream=s))
+        at = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        s, ctx, par, w = torch.cuda.Stream(), i32(c.ctx), i32(c.parents), c.dec.workspace
+        a = (at(c.q), ctypes.byref(c.pool.c), at(c.table), c.table.shape[1], at(ctx), None, at(par), c.B, c.T, c.H_q, c.scale, at(c.dec.out),
+             at(c.dec.lse), at(w), w.numel(), ctypes.c_void_p(s.cuda_stream))
+        keep = (ctx, par)
+
+        def run(f=msa.raw().msa_tree_decode_paged, a=a, s=s, keep=keep):
+            for _ in range(200):
+                if f(*a):
+                    raise RuntimeError("a launch failed")
+            s.synchronize()
+
+        runs.append(run)
     torch.cuda.synchronize()
-    at_once(*runs)
+    at_once(*runs, times=150)
     for c, w in zip(cases, want):
         assert torch.equal(c.dec.out, w[0]) and torch.equal(c.dec.lse, w[1])
+
+
+def serving_calls():
+    """A call of each kind whose first CUDA call may be the encoding of a tensor map."""
+    from block_sparse_long_index_gb300 import MsaDecodeKv4, MsaDensePrefill, MsaPrefill
+    from test_gpu_rope import rows
+    from test_gpu_tree import Case
+    out = {}
+    for kind, T in (("bf16", 3), ("kv4", 3), ("kv4", 40)):
+        c = Case(kind, [50, 3], T, 8, 2, 64, 16, seed=T)
+        c.run()
+        a = (c.q, c.table, i32(c.ctx), i32(c.parents), None, c.scale)
+        out["tree %s %d" % (kind, T)] = lambda c=c, a=a: c.dec(*a)
+        if kind == "kv4" and T == 3:
+            one, q = MsaDecodeKv4(c.pool, 2, c.table.shape[1], 8), rows(2, 8, 64, seed=1)
+            ctx = i32(c.ctx)
+            out["dense decode"] = lambda c=c, one=one, q=q, ctx=ctx: one.dense(q, c.table, ctx)
+    pre, x = MsaPrefill(300, 4, 2, 64, 32, 64, 3), [rows(300, *y, seed=2) for y in ((4, 64), (2, 64), (2, 64), (2, 32), (32,))]
+    out["prefill"] = lambda: pre(*x)
+    dense, cu = MsaDensePrefill(300, 4, 2, 64, 2), i32([0, 100, 300])
+    out["dense prefill"] = lambda: dense(*x[:3], cu)
+    return out
+
+
+@pytest.mark.parametrize("name", ["tree bf16 3", "tree kv4 3", "tree kv4 40", "dense decode", "prefill", "dense prefill"])
+def test_the_first_cuda_call_of_a_thread(name):
+    call = serving_calls()[name]
+    torch.cuda.synchronize()
+    at_once(call, times=1)
