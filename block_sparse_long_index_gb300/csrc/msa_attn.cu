@@ -446,7 +446,7 @@ cudaError_t launch_attn(const void* q, const void* k, const void* v, const int32
     if (e != cudaSuccess) return e;
     const CombineSmem lay = combine_smem(p.k, p.H_q, G);
     auto ck = p.d == 64 ? combine_kernel<64> : combine_kernel<128>;
-    e = cudaFuncSetAttribute(ck, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lay.total);
+    e = allow_shared((const void*)ck, lay.total);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>(T1 - T0, (int64_t)num_sms() * 2);
     ck<<<(unsigned)grid, kCombineThreads, lay.total, s>>>(block_idx, sc.part_o, sc.part_ml, p.N, p.H_q, G, p.gs, p.k,

@@ -24,6 +24,15 @@ int num_sms() {
   return cached;
 }
 
+cudaError_t allow_shared(const void* kern, size_t bytes) {
+  constexpr size_t kAlways = 32 * 1024, kAll = 227 * 1024;
+  if (bytes <= kAlways) return cudaSuccess;
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kern);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kAll - a.sharedSizeBytes));
+}
+
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   // The driver's call fails in a thread without a context, and asking for the device does not give it one: setting it does.
   thread_local bool bound = false;

@@ -701,7 +701,7 @@ cudaError_t launch_scan_c(const void* q_idx_t, const void* k_idx_cache, const in
                           cudaStream_t s) {
   const size_t smem = (size_t)p.max_cta_blocks * kGroupsPerMma * 4;
   auto kern = decode_scan_kernel<DI, BK, PAGED, F8, CAP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<dim3((unsigned)p.splits, (unsigned)p.B), kScanThreads, smem, s>>>(
       (const uint8_t*)q_idx_t, (const uint8_t*)k_idx_cache, ctx_len, p.ctx_max, map, p.H_kv, p.k, p.splits, sc.cand,
@@ -741,7 +741,7 @@ cudaError_t launch_attn_dep_t(const void* q_t, const void* k_cache, const void* 
   const size_t vb = (size_t)BK * D * 2, lb = group_lists_bytes(p);
   const int smem = (int)(vb > lb ? vb : lb);  // V rows of one block, or first the group's candidate lists
   auto kern = decode_attn_kernel<D, BK, PAGED, LPL, KV4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.k, (unsigned)p.H_kv, (unsigned)p.B);

@@ -15,6 +15,11 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int num_sms();  // cached cudaDevAttrMultiProcessorCount of the current device
 
+// Lets a launch of `kern` have `bytes` of dynamic shared memory, for kernels whose calls need different amounts.  The limit
+// belongs to the kernel, not to the call: it is set to all that a CTA can have, always the same, so that no other thread's
+// call lowers it before this one's launch.  Small launches need no limit raised.
+cudaError_t allow_shared(const void* kern, size_t bytes);
+
 // 2-D tiled TMA descriptor over a row-major matrix [rows, inner] of bf16
 // (elem_bytes 2) or bytes (elem_bytes 1, e.g. FP8 codes) with the given row
 // stride, box {box_inner, box_rows} and swizzle (0, 32, 64 or 128 bytes);

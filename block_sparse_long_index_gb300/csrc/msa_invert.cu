@@ -212,10 +212,10 @@ cudaError_t launch_invert(const int32_t* block_idx, int64_t N, int G, int Bk, in
   const int64_t nb = (N + Bk - 1) / Bk;
   const size_t hist_bytes = (size_t)nb * sizeof(int32_t);
   cudaError_t e;
-  e = cudaFuncSetAttribute(inv_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)hist_bytes);
+  e = allow_shared((const void*)inv_count_kernel, hist_bytes);
   if (e != cudaSuccess) return e;
   const size_t scatter_bytes = (size_t)(align_up_i(nb) + 2 * kScatterSub) * sizeof(int32_t);
-  e = cudaFuncSetAttribute(inv_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scatter_bytes);
+  e = allow_shared((const void*)inv_scatter_kernel, scatter_bytes);
   if (e != cudaSuccess) return e;
   dim3 grid_c((unsigned)sc.n_chunks, (unsigned)G);
   inv_count_kernel<<<grid_c, 256, hist_bytes, s>>>(block_idx, N, k, nb, sc.chunk, sc.n_chunks, sc.counts, st);

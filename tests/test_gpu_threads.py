@@ -87,3 +87,40 @@ def test_the_first_cuda_call_of_a_thread(name):
     call = serving_calls()[name]
     torch.cuda.synchronize()
     at_once(call, times=1)
+
+
+def test_decode_steps_of_small_and_of_large_tables():
+    """The scan keeps a maximum for each block that a table has room for."""
+    from block_sparse_long_index_gb300 import Kv4Pool, MsaDecodeKv4
+    from test_gpu_rope import rows
+    pool, idx = Kv4Pool.empty(4, 128, 2, 64), rows(4, 128, 64, seed=1)
+    x, y = rows(512, 2, 64, seed=2), rows(512, 2, 64, seed=3)
+    pool.store(x, y, i32([0, 512]), i32([0]), i32([[0, 1, 2, 3]]))
+    runs, want = [], []
+    for B, max_pages in ((2, 4), (310, 8192)):
+        run, s = MsaDecodeKv4(pool, B, max_pages, 4, d_I=64, Bk=64, k=4), torch.cuda.Stream()
+        table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+        table[:, :4] = i32([0, 1, 2, 3])
+        a = (rows(B, 4, 64, seed=4), rows(B, 2, 64, seed=5), idx, table, i32([400] * B))
+        want.append([t.clone() for t in run(*a)[:2]])
+        runs.append((run, a, s))
+    torch.cuda.synchronize()
+    at_once(*[lambda run=run, a=a, s=s: run(*a, stream=s) for run, a, s in runs], times=1000)
+    for (run, *_), w in zip(runs, want):
+        assert torch.equal(run.out, w[0]) and torch.equal(run.lse, w[1])
+
+
+def test_prefills_of_different_lengths():
+    """The inversion counts in shared memory what each block of keys is chosen by; the combine holds a position's partials."""
+    from block_sparse_long_index_gb300 import MsaPrefill
+    from test_gpu_rope import rows
+    runs, want = [], []
+    for N, H_q, k in ((300, 2, 3), (70000, 8, 16)):
+        run, s = MsaPrefill(N, H_q, 1, 64, 32, 64, k), torch.cuda.Stream()
+        a = [rows(N, *x, seed=6 + i) for i, x in enumerate(((H_q, 64), (1, 64), (1, 64), (1, 32), (32,)))]
+        want.append([t.clone() for t in run(*a)])
+        runs.append((run, a, s))
+    torch.cuda.synchronize()
+    at_once(*[lambda run=run, a=a, s=s: run(*a, stream=s) for run, a, s in runs], times=200)
+    for (run, *_), w in zip(runs, want):
+        assert torch.equal(run.block_idx, w[2])
