@@ -39,10 +39,11 @@ __device__ __forceinline__ float prob(float x) { return x > 0.f && x <= 3.402823
 
 // Sums of counts of what is no distribution stop at kMost, in any order (all counts are 0 or more).
 __device__ __forceinline__ long long add_up(long long a, long long b) { return min(a + b, kMost); }
-__device__ __forceinline__ long long warp_sum(long long d) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) d = add_up(d, __shfl_xor_sync(0xffffffffu, d, o));
-  return d;
+__device__ __forceinline__ long long warp_sum(long long d) {  // (by pieces of 22 bits, whose sums fit 32)
+  constexpr uint32_t kPiece = (1u << 22) - 1u, kTop = 1u << 18;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)d & kPiece), b = __reduce_add_sync(0xffffffffu, (uint32_t)(d >> 22) & kPiece);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(d >> 44));
+  return min(((long long)min(c, kTop) << 44) + ((long long)b << 22) + a, kMost);
 }
 // The sum of the warp's lanes up to this one.
 __device__ __forceinline__ long long warp_scan(long long d) {
@@ -452,13 +453,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
     }
     if (done && k == rank) {  // (it is: the sums add up to the total)
       // the warps' runs likewise, a lane each
-      auto first_past = [&](long long of_lane, long long at) {  // of the lanes' sums, from `at` on; -1: none
-        return __ffs(__ballot_sync(0xffffffffu, add_up(at, warp_scan(of_lane)) > target)) - 1;
+      // the first lane whose sum, with those of the lanes before it and `at`, exceeds the target (-1: none); `at` grows to
+      // what comes before that lane, or by all lanes
+      auto first_past = [&](long long of_lane, long long& at) {
+        const long long upto = add_up(at, warp_scan(of_lane));
+        const int n = __ffs(__ballot_sync(0xffffffffu, upto > target)) - 1;
+        const long long below = __shfl_sync(0xffffffffu, upto, n < 0 ? 31 : n > 0 ? n - 1 : 0);
+        if (n) at = below;
+        return n;
       };
-      auto up_to = [&](long long of_lane, int n) { return warp_sum(lane < n ? of_lane : 0); };  // the first n lanes' sum
-      const long long mine = lane < kWarps ? seg_s[buf][lane] : 0;
-      const int w = first_past(mine, before);
-      before = add_up(before, up_to(mine, w));
+      const int w = first_past(lane < kWarps ? seg_s[buf][lane] : 0, before);
       // all warps take a part of that run each: the part, then its element.  (One warp through the whole run: 64 trees 53 us
       // instead of 46.)
       const Step step = step_s;
@@ -482,16 +486,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
       if (lane == 0) seg_s[buf ^ 1][warp] = sum;  // (the pass before the last one's are read)
       __syncthreads();
       const long long part = lane < kWarps ? seg_s[buf ^ 1][lane] : 0;
-      const int wp = first_past(part, before);  // (there is one: the parts add up to the run)
-      if (warp == wp) {
-        sum = add_up(before, up_to(part, wp));
+      sum = before;
+      if (first_past(part, sum) == warp) {  // (there is one: the parts add up to the run)
         int64_t hit = -1;
         for (int64_t v0 = first_v; v0 < end_v && hit < 0; v0 += 32) {
           const int64_t v = v0 + lane;
           const long long of_lane = load(v, d);
           const int at_lane = first_past(of_lane, sum);
           if (at_lane >= 0) {
-            long long x = add_up(sum, up_to(of_lane, at_lane));
+            long long x = sum;  // (of lane at_lane; the others' results are not looked at)
             int64_t e = -1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -500,7 +503,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
             }
             hit = __shfl_sync(0xffffffffu, e, at_lane);
           }
-          sum = add_up(sum, warp_sum(of_lane));
         }
         if (lane == 0) a.next[b] = (int32_t)hit;
       }
