@@ -891,9 +891,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
   const int rows = T * sh.gs;
   const int64_t first_row = (int64_t)b * sh.T * (sh.H_kv * sh.gs) + g * sh.gs;  // row r is first_row + (r / gs) H_q + r % gs
   const int H_q = sh.H_kv * sh.gs, lg = __ffs(sh.gs) - 1;  // (gs is a power of two)
-  if (warp < m_tiles && r_cta + warp * 16 < rows) {
+  const bool drafts = warp < m_tiles && r_cta + warp * 16 < rows;  // (the warp's)
+  float own_o[D / 8][4], own_m[2], own_l[2];  // O, maxima and sums of a lane's part of its two rows
+  if (drafts) {
     // ---- 16 rows over the drafts: a lane has rows lane / 4 and 8 more, channels and keys by lane % 4
     const int r = lane >> 2, c = lane & 3;
+    own_m[0] = own_m[1] = -kInf;
+    own_l[0] = own_l[1] = 0.f;
     uint32_t qf[2][D / 8];  // channels 8 (4 t + c) .. + 7 of both rows: two steps of 16 each
     uint64_t mask[2], seen[2];  // drafts that a row sees, and from this lane's first key on
 #pragma unroll
@@ -908,7 +912,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
         qf[e][4 * t] = y.x, qf[e][4 * t + 1] = y.y, qf[e][4 * t + 2] = y.z, qf[e][4 * t + 3] = y.w;
       }
     }
-    float s[kMaxT / 8][4], M[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
+    float s[kMaxT / 8][4];
 #pragma unroll
     for (int j = 0; j < kMaxT / 8; ++j) {
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
@@ -926,20 +930,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
         for (int x = 0; x < 4; ++x) {
           const bool on = seen[x >> 1] >> (8 * j + (x & 1)) & 1ull;
           s[j][x] = on ? s[j][x] * scale_log2 : -kInf;
-          M[x >> 1] = fmaxf(M[x >> 1], s[j][x]);
+          own_m[x >> 1] = fmaxf(own_m[x >> 1], s[j][x]);
         }
       }
     }
     float mz[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      M[e] = fmaxf(M[e], __shfl_xor_sync(0xffffffffu, M[e], 1));
-      M[e] = fmaxf(M[e], __shfl_xor_sync(0xffffffffu, M[e], 2));
-      mz[e] = M[e] == -kInf ? 0.f : M[e];  // scores of -inf alone weigh 0
+      own_m[e] = fmaxf(own_m[e], __shfl_xor_sync(0xffffffffu, own_m[e], 1));
+      own_m[e] = fmaxf(own_m[e], __shfl_xor_sync(0xffffffffu, own_m[e], 2));
+      mz[e] = own_m[e] == -kInf ? 0.f : own_m[e];  // scores of -inf alone weigh 0
     }
-    float acc[D / 8][4];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    for (int j = 0; j < D / 8; ++j) own_o[j][0] = own_o[j][1] = own_o[j][2] = own_o[j][3] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < kMaxT / 16; ++kk) {
       if (16 * kk >= Tp) break;
@@ -949,7 +952,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float p0 = ex2_approx(s[2 * kk + y][2 * e] - mz[e]), p1 = ex2_approx(s[2 * kk + y][2 * e + 1] - mz[e]);
-          l[e] += p0 + p1;
+          own_l[e] += p0 + p1;
           pa[2 * y + e] = pack_bf16x2(p0, p1);
         }
       const int vr = 16 * kk + (lane & 15);
@@ -958,8 +961,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
         uint32_t v[4];
         ldmatrix_x4_trans(v[0], v[1], v[2], v[3], sm + J::KV + vr * J::ROW + (((2 * j + (lane >> 4)) ^ (vr & 7)) << 4));
         const uint32_t b0[2] = {v[0], v[1]}, b1[2] = {v[2], v[3]};
-        mma_bf16_16816(acc[2 * j], pa, b0);
-        mma_bf16_16816(acc[2 * j + 1], pa, b1);
+        mma_bf16_16816(own_o[2 * j], pa, b0);
+        mma_bf16_16816(own_o[2 * j + 1], pa, b1);
       }
     }
     if (wild_s) {
@@ -975,22 +978,26 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(TreeShape sh
               float v;
               if constexpr (KV4) v = pool.v_scales[hr * kGroups + ch / (D / kGroups)] == kScaleNaN ? __uint_as_float(0x7FFFFFFFu) : 0.f;
               else v = __uint_as_float((uint32_t)v_pool[hr * D + ch] << 16);
-              if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) acc[j][2 * e + x] += v;
+              if ((__float_as_uint(v) & 0x7F800000u) == 0x7F800000u) own_o[j][2 * e + x] += v;
             }
         }
     }
-    __syncthreads();  // K and V are done with
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      own_l[e] += __shfl_xor_sync(0xffffffffu, own_l[e], 1);
+      own_l[e] += __shfl_xor_sync(0xffffffffu, own_l[e], 2);
+    }
+  }
+  __syncthreads();  // K and V are done with
+  if (drafts) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       const int lr = warp * 16 + r + 8 * e;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) *reinterpret_cast<float2*>(o_s + lr * D + 8 * j + 2 * c) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
-      if (c == 0) ml_s[lr] = make_float2(M[e], l[e]);
+      for (int j = 0; j < D / 8; ++j) *reinterpret_cast<float2*>(o_s + lr * D + 8 * j + 2 * c) = make_float2(own_o[j][2 * e], own_o[j][2 * e + 1]);
+      if (c == 0) ml_s[lr] = make_float2(own_m[e], own_l[e]);
     }
-  } else {
-    __syncthreads();
   }
   __syncthreads();
   griddep_wait();  // the partials

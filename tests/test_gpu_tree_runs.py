@@ -102,3 +102,16 @@ def test_rounds(kind, T, H_q, H_kv, d, page):
     again = tuple(t.clone() for t in (out, lse))
     out, lse = c.run(tree_len=tl)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+@pytest.mark.parametrize("B,T,H_q,H_kv,d", [(3, 1, 2, 2, 64), (60, 3, 24, 6, 128), (80, 9, 32, 8, 64), (150, 17, 16, 8, 128), (70, 5, 64, 8, 64)])
+def test_joins_whose_warps_have_rows_or_none(kind, B, T, H_q, H_kv, d):
+    """One, two and four tiles of 16 rows a CTA of the joining kernel, the last ones in part or not at all filled."""
+    r = np.random.default_rng(43)
+    ctx = [int(x) for x in r.integers(0, 60, B)]
+    tl = [int(x) for x in r.integers(0, T + 1, B)]
+    c = Case(kind, ctx, T, H_q, H_kv, d, 16, "random", seed=43 + T)
+    out, lse = c.run(tree_len=tl)
+    assert c.dec.device_status() == 0
+    check(c, out, lse, tree_len=tl)
