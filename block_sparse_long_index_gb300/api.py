@@ -121,6 +121,14 @@ def _allocating_for(stream):
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
+def _settled(tensors):
+    """The tensors, whose clearing on the current stream is over: the first call on them may be on another stream."""
+    with torch.cuda.device(tensors[0].device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return tensors
+
+
 class MsaDensePrefill:
     """Dense causal attention over packed prompts of N rows in all, S sequences.
 
@@ -356,7 +364,7 @@ class KvPool(_Append):
 
     @classmethod
     def empty(cls, n_pages, page_size, H_kv, d, device="cuda"):
-        return cls(*[torch.zeros((n_pages, page_size, H_kv, d), dtype=torch.bfloat16, device=device) for _ in range(2)])
+        return cls(*_settled([torch.zeros((n_pages, page_size, H_kv, d), dtype=torch.bfloat16, device=device) for _ in range(2)]))
 
     def tensors(self):
         return [self.k, self.v]
@@ -386,8 +394,8 @@ class Kv4Pool(_Append):
 
     @classmethod
     def empty(cls, n_pages, page_size, H_kv, d, device="cuda"):
-        return cls(*[torch.zeros((n_pages, page_size, H_kv, last), dtype=torch.uint8, device=device)
-                     for last in (d // 2, 4, d // 2, 4)])
+        return cls(*_settled([torch.zeros((n_pages, page_size, H_kv, last), dtype=torch.uint8, device=device)
+                              for last in (d // 2, 4, d // 2, 4)]))
 
     def tensors(self):
         return [self.k_codes, self.k_scales, self.v_codes, self.v_scales]
@@ -494,8 +502,8 @@ class MsaTreeDecode:
         device = pool.tensors()[0].device
         self.pool, self.B, self.T, self.max_pages, self.H_q = pool, B, T, max_pages, H_q
         self.workspace = torch.empty(_c.msa_tree_decode_workspace(B, T, H_q, pool.H_kv, pool.d), dtype=torch.uint8, device=device)
-        self.out = torch.zeros((B, T, H_q, pool.d), dtype=torch.bfloat16, device=device)
-        self.lse = torch.zeros((B, T, H_q), dtype=torch.float32, device=device)
+        self.out, self.lse = _settled([torch.zeros((B, T, H_q, pool.d), dtype=torch.bfloat16, device=device),
+                                       torch.zeros((B, T, H_q), dtype=torch.float32, device=device)])
         self._call = _c.msa_tree_decode_paged_kv4 if isinstance(pool, Kv4Pool) else _c.msa_tree_decode_paged
 
     def __call__(self, q, page_table, ctx_len, parents, tree_len=None, scale=None, stream=None):
@@ -580,9 +588,9 @@ class PagedCache:
 
     @classmethod
     def empty(cls, n_seqs, max_pages, n_pages, page_size, pools=(), device="cuda"):
-        return cls(torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
-                   torch.zeros((n_seqs,), dtype=torch.int32, device=device),
-                   torch.zeros((n_pages,), dtype=torch.int32, device=device), page_size, pools)
+        return cls(*_settled([torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                              torch.zeros((n_seqs,), dtype=torch.int32, device=device),
+                              torch.zeros((n_pages,), dtype=torch.int32, device=device)]), page_size, pools)
 
     def reserve(self, seqs, new_len, stream=None):
         n, dev = seqs.numel(), _device(self.workspace)
