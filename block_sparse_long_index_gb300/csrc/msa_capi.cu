@@ -11,8 +11,8 @@
 namespace msa {
 
 int num_sms() {
-  static int cached_dev = -1;
-  static int cached = 0;
+  thread_local int cached_dev = -1;  // (of the thread: two words that another one may see half written otherwise)
+  thread_local int cached = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   if (dev != cached_dev) {
