@@ -17,8 +17,8 @@
 // in, and the sum of V tokens is off by V 2^-59 at most.  (64-bit floating point would be bound by the few units for it;
 // fp32 sums draw another token in one of a thousand cases at 128000 tokens.)
 //
-// Measured: 64 trees of 24 nodes over 128000 tokens 46 us (0.21 of HBM, a few passes in a row of 4 us each; 22 us where one
-// pass is all); one tree of 6 over 50001 tokens 12 us.
+// Measured: 64 trees of 24 nodes over 128000 tokens 53 us (0.19 of HBM; 47 us with the rows in L2, 17 us where one pass is all:
+// a few passes in a row, and the decision between two of them); one tree of 6 over 50001 tokens 12 to 13 us.
 #include <math.h>
 
 #include "msa_common.cuh"
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kCluster = 8;
 constexpr int kMaxNodes = 64;
-constexpr int kFly = 2;  // vectors of each row that a lane has in flight (3 and 4 are slower: 48 and 51 us for 46)
+constexpr int kFly = 2;  // vectors of each row that a lane has in flight (64 trees, rows in L2: 1 to 4 take 55, 47, 51, 53 us)
 constexpr double kUnit = 288230376151711744.0;           // 2^58
 constexpr long long kMost = (1ll << 62) - 1;             // where sums stay: 16, far above a distribution's
 
@@ -247,7 +247,7 @@ __device__ __forceinline__ void count2(float p0, float p1, float q0, float q1, f
 template <Form F>
 __device__ __forceinline__ long long lane_sum(const Residual& r, int64_t v0, int64_t v1) {
   constexpr uint32_t kEach = 4 * kFly, kTimesB = F == kPlain ? 1 : 2;
-  constexpr int kFlush = 32;  // the counts of as many rounds fit 32 bits: 256 elements of 2^21 and of 2^22 + 2^21
+  constexpr int kFlush = 256 / kEach;  // rounds whose counts fit 32 bits: 256 elements of 2^21 and of 2^22 + 2^21
   const int lane = threadIdx.x & 31;
   float most = 0.f;
   long long sum = 0;
@@ -463,8 +463,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(THREADS, 1024
         return n;
       };
       const int w = first_past(lane < kWarps ? seg_s[buf][lane] : 0, before);
-      // all warps take a part of that run each: the part, then its element.  (One warp through the whole run: 64 trees 53 us
-      // instead of 46.)
+      // all warps take a part of that run each: the part, then its element.  (One warp through the whole run: 7 us more for 64
+      // trees.)
       const Step step = step_s;
       Residual r;
       const int64_t at = ((int64_t)b * a.T + step.node) * a.V;

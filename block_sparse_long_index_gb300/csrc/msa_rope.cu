@@ -25,7 +25,8 @@ constexpr int kWarps = kRowThreads / 32;
 constexpr int kFly = 4;       // 16-byte reads a thread has in flight
 constexpr int kMaxToks = 16;  // tokens of a CTA
 
-// cos and sin of 2^-64 ph turns, each within 2^-25 of the nearest fp32.  The angle is reduced to +-1/8 turn around the
+// cos and sin of 2^-64 ph turns, each within 2^-24 of the exact value (half a step from 1/2 on, and what the last sum adds).  The
+// angle is reduced to +-1/8 turn around the
 // nearest quarter; there the Taylor polynomials, whose first missing terms are below 2^-37, are summed from the small
 // end with the roundings of the leading terms carried along (their products written as an fp32 and its error).
 __device__ __forceinline__ void cos_sin(uint64_t ph, float& c, float& s) {

@@ -18,6 +18,8 @@
 //   more rows over bf16 pages: two query tiles over the same keys.  (4-bit pages are expanded again for each 128 rows: a
 //   tile's softmax takes as long, and the room of the second query tile holds the codes in flight.)
 // Rows of a tile past the last one are computed on by the tensor cores alone; warps without a row rest.
+// P is rounded to bf16 for the product with V, whose operands have one type (V's is bf16, or exact in it); scores, sums and O
+// stay fp32.
 // Over a 4-bit cache up to 32 rows of up to 8 K/V heads have a kernel of their own (msa_tree_few.cu).
 //
 // Measured, with the join: bf16 pages, 128 rows, 4 sequences of 262144 tokens: 636 us, HBM's rate (a tile takes 1955

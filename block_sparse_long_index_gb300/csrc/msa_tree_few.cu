@@ -12,7 +12,9 @@
 // (2293; 0.84 of HBM's rate, which bounds it), 16 rows 1094 us (2288), 32 rows 1640 us (2297; 0.42 of HBM: 1806 cycles a tile
 // and head, of which the products need 1024; with registers for two warps a scheduler, what is left is latency); 16 sequences
 // of 15000 to 30000 tokens, 32, 16, 8 rows 169, 116, 93 us (226, 225, 225); 64 of 250 to 500 tokens, 16 and 4 rows 29, 21 us
-// (42, 40); one of 1500 tokens, 32, 16, 4 rows 22, 17, 14 us (20, 17, 17).
+// (42, 40); one of 1500 tokens, 32, 16, 4 rows 22, 17, 14 us (20, 17, 17).  The choice is by rows and heads alone: lengths are
+// on the device, and the table's width says little of them.  So 32 rows over a short context take 2 us more than they might;
+// rows beyond 32 have no registers here (a warp holds all of its head's).
 #include <math.h>
 
 #include "msa_kv4_units.cuh"

@@ -752,8 +752,9 @@ msa_status_t msa_verify_tree(const float* probs, const float* draft_probs, const
  * allowed).  pools: n_pools <= 8 host entries, each a device array of n_pages
  * pages of page_bytes (a multiple of 16) at a 16-byte aligned address; pass every
  * pool that the tables address.  (reserve and free touch no pool, and compact's
- * page_map tells where the pages of further pools go; fork has no such list, so
- * tables that are forked serve at most 8 pools.)  workspace:
+ * page_map tells where the pages of further pools go; fork and accept have no such
+ * list, so tables that are forked, or of which drafts are accepted, serve at most 8
+ * pools: layers beyond these have tables of their own.)  workspace:
  * msa_pages_workspace(pages, n) bytes, n as in the call (0 for compact).
  * Limits: n_pages, max_pages < 2^27; max_pages * page_size < 2^31.
  */
