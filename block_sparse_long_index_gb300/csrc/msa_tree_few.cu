@@ -7,6 +7,8 @@
 // an expanded K or V operand serving the NT groups of 8 rows.  q's operands lie in shared memory where NT > 1 leaves no
 // registers for them.  tcgen05's 128-row tile, for which codes have to be expanded into shared memory by warps that wait
 // for one another, takes as long for any number of rows up to 32 (2630 cycles a tile of 128 tokens of a head).
+// (With 32 rows and d = 128 the 255 registers leave 4 to 12 bytes in local memory: 2 loads and a store a warp by its counters,
+// outside the steps.)
 //
 // Measured with the join, 8 heads, d = 128, tcgen05's form in brackets: 4 sequences of 2^20 tokens, 8 rows a head 817 us
 // (2293; 0.84 of HBM's rate, which bounds it), 16 rows 1094 us (2288), 32 rows 1640 us (2297; 0.42 of HBM: 1806 cycles a tile
